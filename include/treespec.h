@@ -9,6 +9,13 @@
  *   ts_tree_accept_sample  the same verification at temperature T > 0 (rejection sampling)
  *   ts_tree_prune      cost-aware pruning of the tree before verification
  *
+ * Long contexts: tree attention over a choice of the prefix's pages
+ *   ts_kv_page_bounds          per-page bounds of the keys
+ *   ts_page_select             the pages each node attends to, by an exact upper-bound score
+ *   ts_tree_attention_sparse   tree attention over the chosen pages
+ * The page pool
+ *   ts_kv_reserve, ts_kv_fork, ts_kv_compact   hand out, share, copy, free and move pages
+ *
  * Conventions shared by every entry point
  *   - Every tensor argument is a DEVICE pointer owned by the caller.  The library never
  *     allocates device memory; scratch space is the caller's `workspace`, sized by the
@@ -53,7 +60,8 @@ typedef enum {
   TS_ERR_WORKSPACE = -3,     /* workspace smaller than the *_workspace() query */
   TS_ERR_CUDA = -4,          /* a CUDA launch or driver call failed */
   TS_ERR_TIMEOUT = -5,       /* device: a bounded wait gave up (written to *dev_status) */
-  TS_ERR_DEVICE_CHECK = -6   /* device: bad data found in an input (written to *dev_status) */
+  TS_ERR_DEVICE_CHECK = -6,  /* device: bad data found in an input (written to *dev_status) */
+  TS_ERR_NO_PAGES = -7       /* device: the page pool ran short (written to *dev_status) */
 } ts_status;
 
 typedef enum { TS_F32 = 0, TS_BF16 = 1 } ts_dtype;
@@ -62,6 +70,8 @@ typedef enum { TS_F32 = 0, TS_BF16 = 1 } ts_dtype;
 #define TS_MAX_NODES 256
 #define TS_MAX_TOPK 16
 #define TS_MAX_DEPTH 16
+/* ts_kv_reserve: B <= TS_MAX_POOL_ROWS. */
+#define TS_MAX_POOL_ROWS 4096
 /* ts_tree_accept_sample: V <= TS_SAMPLE_MAX_VOCAB. */
 #define TS_SAMPLE_MAX_VOCAB (1 << 20)
 
@@ -429,6 +439,174 @@ int ts_tree_prune(const int32_t* tokens, const int32_t* parents, const int32_t* 
                   int32_t* n_out, int32_t* tokens_out, int32_t* parents_out, int32_t* depth_out,
                   uint64_t* mask_out, double* values_out, int32_t* node_row_out, int32_t* kept_out,
                   float* expected_out, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * ts_kv_page_bounds — bounds of the keys of each complete page, the summary that
+ * ts_page_select scores.  The pages (web sources) have no counterpart; like the two calls after
+ * it, it exists for contexts too long to read whole in every verify pass.
+ *
+ * For every sequence b, logical page p with start_len[b]/bs <= p < prefix_len[b]/bs (the pages
+ * complete at prefix_len that were not at start_len), KV head h and channel c:
+ *   hi = max over the page's rows of k, lo = min (NaN ignored, 0 if there is nothing else;
+ *   magnitudes clamped to 255 * 2^40)
+ *   2^e = the smallest power of two, -40 <= e <= 40, with |hi|, |lo| <= 255 * 2^e over all
+ *         channels of the page and head
+ *   bounds[page][h][0][c] = ceil(hi / 2^e) * 2^e,   bounds[page][h][1][c] = floor(lo / 2^e) * 2^e
+ * Both are whole multiples of 2^e of at most 255, which bf16 holds exactly.  Bounds of other
+ * pages are left as they are.  A page's bounds stay valid until the page is written again.
+ *
+ * k_cache [num_blocks, Hkv, block_size, d] (dt), any d <= 256.  block_table [B, max_blocks],
+ * prefix_len [B] int32, start_len [B] int32 (NULL: 0).  bounds [num_blocks, Hkv, 2, d] bf16.
+ * One launch, no workspace.
+ * Device errors: a negative length, a prefix_len above max_blocks * block_size or a page id out
+ * of range -> TS_ERR_DEVICE_CHECK (that sequence or page is skipped).
+ * --------------------------------------------------------------------------------- */
+int ts_kv_page_bounds(const void* k_cache, ts_dtype dt, int num_blocks, int block_size, int Hkv, int d,
+                      const int32_t* block_table, int max_blocks, const int32_t* prefix_len,
+                      const int32_t* start_len, int B, void* bounds, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * ts_page_select — which complete prefix pages each tree node attends to.
+ *
+ * The query of (node i, head) is rounded to a grid of its own: 2^e as in ts_kv_page_bounds from
+ * its largest magnitude (NaN counts as 0, magnitudes clamped to 255 * 2^40), q~ = 2^e * rint(q / 2^e).
+ *   score(i, KV head h, page p) = max over the g heads of h of
+ *                                 sum_c max(q~_c * bounds[p][h][0][c], q~_c * bounds[p][h][1][c]),
+ * an upper bound of q~ . k over the page's keys.  Every product and partial sum is a whole
+ * multiple of one power of two below 2^24 times it, so fp32 holds the score exactly whatever the
+ * order of summation: the choice does not depend on tiling, batch or machine.
+ * Of the prefix_len[b] / block_size complete pages node i keeps the first `first`, the last
+ * `recent`, and then the best by score (ties -> lower index) until it has n_pages, or all if
+ * there are no more than n_pages.
+ *
+ * q [B, m, Hq, d] (dt).  bounds [num_blocks, Hkv, 2, d] bf16.  block_table [B, max_blocks],
+ * prefix_len [B].  max_prefix: host-side upper bound of prefix_len.
+ * 1 <= n_pages, first >= 0, recent >= 0, first + recent <= n_pages.
+ * Outputs, with C = max(1, max_prefix / block_size) and W = ceil(m / 64):
+ *   pages     [B, Hkv, C] int32: logical pages that any node keeps, ascending, then -1
+ *   count     [B, Hkv] int32: how many
+ *   node_mask [B, Hkv, C, W] uint64: bit i % 64 of word i / 64 is set iff node i keeps that
+ *             page (0 behind the last one)
+ * Supported: any d <= 256, m <= 256, Hq / Hkv <= 128, C <= 65536, B * Hkv <= 65535.
+ * workspace: ts_page_select_workspace(...) bytes.
+ * Device errors: prefix_len outside [0, max_prefix] (count 0, no pages) or a page id out of
+ * range (its score is 0) -> TS_ERR_DEVICE_CHECK; a wait over its time bound -> TS_ERR_TIMEOUT.
+ * --------------------------------------------------------------------------------- */
+size_t ts_page_select_workspace(int B, int m, int Hq, int Hkv, int d, int max_prefix, int block_size);
+int ts_page_select(const void* q, ts_dtype dt, const void* bounds, int num_blocks, int block_size,
+                   const int32_t* block_table, int max_blocks, const int32_t* prefix_len, int max_prefix,
+                   int B, int m, int Hq, int Hkv, int d, int n_pages, int first, int recent,
+                   int32_t* pages, int32_t* count, uint64_t* node_mask,
+                   void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * ts_tree_attention_sparse — ts_tree_attention over a choice of the prefix's pages.
+ *
+ * For sequence b, query head h on KV head kh and node i, with F = L_b / block_size complete
+ * pages:  keys = the positions of pages[b][kh][u], u < count[b][kh], whose node_mask bit i is set
+ *              U { F * block_size .. L_b - 1 }  (the page that is not complete yet)
+ *              U { L_b + t : mask bit t of row i is set }
+ * out and lse as ts_tree_attention; a node without any key gets out 0 and lse -inf.  With every
+ * complete page chosen for every node it computes what ts_tree_attention computes.
+ *
+ * pages [B, Hkv, C], count [B, Hkv], node_mask [B, Hkv, C, W] as ts_page_select writes them (any
+ * capacity C >= 1; each page at most once).  Other arguments as ts_tree_attention; the same types,
+ * head dims and page sizes are supported, and the same two paths serve them.
+ * Non-finite values in places that a node does not attend to do not reach its output.
+ * workspace: ts_tree_attention_sparse_workspace(...) bytes.
+ * Device errors: count outside [0, C], a chosen page outside [0, F), prefix_len negative or
+ * beyond max_blocks * block_size - m, or a page id out of range -> TS_ERR_DEVICE_CHECK; a wait
+ * over its time bound -> TS_ERR_TIMEOUT.
+ * --------------------------------------------------------------------------------- */
+size_t ts_tree_attention_sparse_workspace(ts_dtype dt, int B, int m, int Hq, int Hkv, int d, int C,
+                                          int block_size);
+int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_cache, ts_dtype dt,
+                             int num_blocks, int block_size, const int32_t* block_table, int max_blocks,
+                             const int32_t* prefix_len, const uint64_t* mask, const int32_t* pages,
+                             const int32_t* count, const uint64_t* node_mask, int C,
+                             int B, int m, int Hq, int Hkv, int d, float scale, void* out, float* lse,
+                             void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * The page pool.  refs [num_blocks] int32 counts, for each page, the block-table entries that
+ * name it plus whatever else the caller counts there; 0 = free.  Each call reads the state it is
+ * given (block_table, prefix_len, refs) and writes the new state to its outputs; where the text
+ * says so an output may be the very buffer of its input (partial overlap is not allowed).  All
+ * results are whole numbers that do not depend on the order of execution.
+ * ts_kv_commit lists what a verify step lets go of; pass that list to the next ts_kv_reserve.
+ * --------------------------------------------------------------------------------- */
+
+/*
+ * ts_kv_reserve — pages for the next n tokens of every sequence, ready to be written.
+ *
+ * First every freed[j] >= 0 loses one reference (the same page may be listed more than once).
+ * Then, for the sequences in order, with L = prefix_len[b], and for each logical page i in order
+ * with L / bs <= i < ceil((L + n) / bs):
+ *   - entry -1: a fresh page;
+ *   - i = L / bs, L % bs > 0 and the page has more than one reference: a fresh page takes its
+ *     place, the first L % bs rows of K and V are copied over for every KV head, and the old page
+ *     loses a reference (so the last sequence that holds a shared page keeps it);
+ *   - otherwise the entry stays.
+ * Fresh pages are the free ones (refs 0 after the release) in increasing id, one reference each.  If too
+ * few are left for all of a sequence's fresh pages, that sequence and the later ones that need any
+ * keep their entries, granted is -1 for them and *dev_status gets TS_ERR_NO_PAGES.
+ *
+ * k_cache, v_cache [num_blocks, Hkv, block_size, d] (dt), in/out.  block_table [B, max_blocks],
+ * prefix_len [B], refs [num_blocks].  freed [num_freed] int32 (-1 entries skipped; NULL with 0).
+ * block_table_out, refs_out: may be block_table, refs.  granted [B] int32: fresh pages taken, or -1.
+ * n >= 1, B <= TS_MAX_POOL_ROWS.  Two launches.  workspace: ts_kv_reserve_workspace(...) bytes.
+ * Errors: TS_ERR_INVALID also for d * element size not a multiple of 4.
+ * Device errors: a negative length, L + n > max_blocks * block_size or an entry out of range:
+ * TS_ERR_DEVICE_CHECK, the sequence stays as it is and granted is -1; a freed id out of range or
+ * of a page without references: TS_ERR_DEVICE_CHECK, skipped.
+ */
+size_t ts_kv_reserve_workspace(int num_blocks, int block_size, int B, int n);
+int ts_kv_reserve(void* k_cache, void* v_cache, ts_dtype dt, int num_blocks, int block_size, int Hkv, int d,
+                  const int32_t* block_table, int max_blocks, const int32_t* prefix_len, const int32_t* refs,
+                  int B, int n, const int32_t* freed, int num_freed, int32_t* block_table_out,
+                  int32_t* refs_out, int32_t* granted, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                  void* stream);
+
+/*
+ * ts_kv_fork — new sequences from old ones: fork, reorder and drop.
+ *
+ * Row r of the new state continues row src[r] of the old one (src[r] = -1: an empty row).  The new
+ * row names the ceil(L / bs) pages that hold the old row's L tokens, then -1; its length is L.  The
+ * new state replaces the old one: a page's count loses every entry of block_table that names it
+ * (those reserved beyond L among them) and gains every entry of block_table_out.  No K/V moves;
+ * the half-filled last page is shared until ts_kv_reserve copies it.
+ *
+ * block_table [B, max_blocks], prefix_len [B], refs [num_blocks], src [B_out].
+ * block_table_out [B_out, max_blocks] and prefix_len_out [B_out] must not be the inputs;
+ * refs_out may be refs.  B, B_out <= 65535.  Two launches, no workspace.
+ * Device errors: src outside [-1, B), a length outside [0, max_blocks * block_size] (the new row is
+ * empty), an entry out of range or missing among a kept row's pages (copied as -1), or a count that
+ * falls below zero -> TS_ERR_DEVICE_CHECK.
+ */
+int ts_kv_fork(const int32_t* block_table, int max_blocks, const int32_t* prefix_len, const int32_t* refs,
+               int num_blocks, int block_size, int B, const int32_t* src, int B_out, int32_t* block_table_out,
+               int32_t* prefix_len_out, int32_t* refs_out, int32_t* dev_status, void* stream);
+
+/*
+ * ts_kv_compact — move the pages in use to the lowest ids.
+ *
+ * With `live` pages in use (refs > 0), the i-th page in use with id >= live moves to the i-th free
+ * page with id < live: K and V rows, bounds (where given) and count.  remap[old id] is the id
+ * that a page in use has afterwards, -1 for a free one; block_table_out is block_table through
+ * remap.
+ *
+ * k_cache, v_cache [num_blocks, Hkv, block_size, d] (dt) and bounds [num_blocks, Hkv, 2, d] bf16 (NULL
+ * to leave out): in/out.  block_table [B, max_blocks], refs [num_blocks].
+ * block_table_out, refs_out: may be block_table, refs.  remap [num_blocks] int32, live [1] int32.
+ * Two launches.  workspace: ts_kv_compact_workspace(num_blocks) bytes.
+ * Errors: TS_ERR_INVALID also for d * element size not a multiple of 4.
+ * Device errors: a table entry out of range or naming a free page becomes -1 -> TS_ERR_DEVICE_CHECK.
+ */
+size_t ts_kv_compact_workspace(int num_blocks);
+int ts_kv_compact(void* k_cache, void* v_cache, ts_dtype dt, void* bounds, int num_blocks, int block_size,
+                  int Hkv, int d, const int32_t* block_table, int max_blocks, const int32_t* refs, int B,
+                  int32_t* block_table_out, int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace,
+                  size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------------------
  * ts_selftest_bounded_wait — failure-detection check of the bounded pipeline waits.

@@ -19,6 +19,10 @@ Plain, slow, obviously-correct numpy restatements of what the pages define:
   ("lesty.tech", section 4).
 * :mod:`oracle.tree_prune`   — cost-aware pruning of the tree before verification (same
   page, EAGLE-Harness section; "rainlin.net/posts/eagle", sections 7.1 and 六).
+* :mod:`oracle.page_select` — page bounds, the choice of pages by an upper-bound score, and tree
+  attention over the chosen pages (no counterpart on the pages).
+* :mod:`oracle.page_pool`    — the page pool: reserve, fork, compact ("lesty.tech", section 8 for the
+  reserved and released pages; the rest has no counterpart).
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and the CPU-baseline leg of
 ``bench.py`` may import this package.  The product (the CUDA library and its
@@ -36,3 +40,5 @@ from .lm_head import lm_head_logits, lm_head_argmax, fp32_error_bound  # noqa: F
 from .efficient_head import candidates, efficient_head  # noqa: F401
 from .accept_sample import accept_sample, softmax_t  # noqa: F401
 from .tree_prune import tree_prune  # noqa: F401
+from .page_select import page_bounds, page_select, page_scores, grid_query, tree_attention_sparse  # noqa: F401
+from . import page_pool  # noqa: F401

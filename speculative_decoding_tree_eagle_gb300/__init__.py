@@ -15,6 +15,13 @@ rejected pages), ``lm_head_argmax`` / ``tree_accept_hidden`` (target LM head wit
 its GEMM epilogue), ``efficient_head`` / ``tree_build_from_topk`` (the draft's two-stage head
 and the tree from its lists), ``tree_accept_sample`` (acceptance at temperature T > 0) and
 ``tree_prune`` (cost-aware pruning before verification).
+
+Long contexts: ``kv_page_bounds`` (per-page bounds of the keys), ``page_select`` (the pages each
+node attends to) and ``tree_attention_sparse`` (tree attention over them).  The page pool:
+``kv_reserve`` (room for the next tokens), ``kv_fork`` (fork, reorder and drop sequences) and
+``kv_compact`` (move the pages in use together).  These six run on the tensors' device, which need
+not be the current one, on that device's current stream, and take their workspace from torch's
+allocator call by call, so calls on several streams or in several captured graphs share none.
 """
 from __future__ import annotations
 
@@ -30,6 +37,7 @@ __all__ = [
     "TreeSpecError", "library", "library_path", "launch_count", "status_string",
     "tree_build", "tree_attention", "tree_accept", "kv_commit", "lm_head_argmax", "tree_accept_hidden",
     "efficient_head", "tree_build_from_topk", "tree_accept_sample", "tree_prune",
+    "kv_page_bounds", "page_select", "tree_attention_sparse", "kv_reserve", "kv_fork", "kv_compact",
     "new_status", "check_status",
     "tree_build_workspace", "tree_attention_workspace", "tree_accept_workspace", "tree_attention_plan",
 ]
@@ -108,6 +116,26 @@ def library():
         L.ts_selftest_bounded_wait.argtypes = [I, P, P, P]
         L.ts_kv_commit.restype = I
         L.ts_kv_commit.argtypes = [P, P, I, I, I, I, I, P, I, P, P, P, I, I, P, P, P, P]
+        L.ts_kv_page_bounds.restype = I
+        L.ts_kv_page_bounds.argtypes = [P, I, I, I, I, I, P, I, P, P, I, P, P, P]
+        L.ts_page_select_workspace.restype = S
+        L.ts_page_select_workspace.argtypes = [I, I, I, I, I, I, I]
+        L.ts_page_select.restype = I
+        L.ts_page_select.argtypes = [P, I, P, I, I, P, I, P, I, I, I, I, I, I, I, I, I, P, P, P, P, S, P, P]
+        L.ts_tree_attention_sparse_workspace.restype = S
+        L.ts_tree_attention_sparse_workspace.argtypes = [I, I, I, I, I, I, I, I]
+        L.ts_tree_attention_sparse.restype = I
+        L.ts_tree_attention_sparse.argtypes = [P, P, P, I, I, I, P, I, P, P, P, P, P, I, I, I, I, I, I, F, P, P, P, S, P, P]
+        L.ts_kv_reserve_workspace.restype = S
+        L.ts_kv_reserve_workspace.argtypes = [I, I, I, I]
+        L.ts_kv_reserve.restype = I
+        L.ts_kv_reserve.argtypes = [P, P, I, I, I, I, I, P, I, P, P, I, I, P, I, P, P, P, P, S, P, P]
+        L.ts_kv_fork.restype = I
+        L.ts_kv_fork.argtypes = [P, I, P, P, I, I, I, P, I, P, P, P, P, P]
+        L.ts_kv_compact_workspace.restype = S
+        L.ts_kv_compact_workspace.argtypes = [I]
+        L.ts_kv_compact.restype = I
+        L.ts_kv_compact.argtypes = [P, P, I, P, I, I, I, I, P, I, P, I, P, P, P, P, P, S, P, P]
         _lib = L
     return _lib
 
@@ -522,4 +550,271 @@ def tree_build_from_topk(row_tok: torch.Tensor, row_logp: torch.Tensor, root_tok
     _check(L.ts_tree_build_from_topk(_p(row_tok), _p(row_logp), _p(root_tokens), B, k, depth, m, _p(out["tokens"]),
                                      _p(out["parents"]), _p(out["depth"]), _p(out["mask"]), _p(out.get("values")),
                                      _p(out.get("node_row")), _p(status), _stream()))
+    return out
+
+
+def _same_device(**tensors) -> torch.device:
+    """The one CUDA device that all the given tensors (None skipped) are on."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+        dev = t.device
+    return dev
+
+
+def _shape(name: str, t: torch.Tensor, *want) -> None:
+    if tuple(t.shape) != tuple(want):
+        raise ValueError(f"{name} must have shape {list(want)}, got {list(t.shape)}")
+
+
+def _scratch(nbytes: int, device: torch.device, ws: Optional[torch.Tensor]) -> torch.Tensor:
+    """The caller's workspace, or one of this call's own."""
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _need_cuda("workspace", ws)
+    if ws.device != device:
+        raise ValueError(f"workspace is on {ws.device}, the other tensors on {device}")
+    if ws.numel() * ws.element_size() < nbytes:
+        raise ValueError("workspace too small")
+    return ws
+
+
+def _outputs(out: Optional[Dict[str, torch.Tensor]], device: torch.device, **want) -> Dict[str, torch.Tensor]:
+    """New output tensors, or the caller's after a check of their shapes and types."""
+    if out is None:
+        return {k: torch.empty(shape, dtype=dt, device=device) for k, (shape, dt) in want.items()}
+    for k, (shape, dt) in want.items():
+        _need_cuda(k, out[k], dt)
+        _shape(k, out[k], *shape)
+        if out[k].device != device:
+            raise ValueError(f"{k} is on {out[k].device}, the other tensors on {device}")
+    return out
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two contiguous tensors share memory without being the very same buffer."""
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    a1, b1 = a0 + a.numel() * a.element_size(), b0 + b.numel() * b.element_size()
+    return a0 < b1 and b0 < a1 and (a0, a1) != (b0, b1)
+
+
+def _need_cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
+    _need_cuda("k_cache", k_cache)
+    _need_cuda("v_cache", v_cache, k_cache.dtype)
+    if k_cache.dim() != 4:
+        raise ValueError("caches must be [num_blocks, Hkv, block_size, d]")
+    _shape("v_cache", v_cache, *k_cache.shape)
+
+
+def kv_page_bounds(k_cache: torch.Tensor, block_table: torch.Tensor, prefix_len: torch.Tensor, *,
+                   start_len: Optional[torch.Tensor] = None, bounds: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Bounds of the keys of the pages complete at prefix_len [B] that were not at start_len [B]
+    (default: at 0), into bounds [num_blocks,Hkv,2,d] bf16 (largest, smallest), which is returned.
+    Other pages' bounds stay; without ``bounds`` a tensor of zeros is made."""
+    L = library()
+    dev = _same_device(k_cache=k_cache, block_table=block_table, prefix_len=prefix_len, start_len=start_len, bounds=bounds,
+                       status=status)
+    _need_cuda("k_cache", k_cache)
+    _need_cuda("block_table", block_table, torch.int32)
+    _need_cuda("prefix_len", prefix_len, torch.int32)
+    NB, Hkv, bs, d = k_cache.shape
+    B, width = block_table.shape
+    _shape("prefix_len", prefix_len, B)
+    if start_len is not None:
+        _need_cuda("start_len", start_len, torch.int32)
+        _shape("start_len", start_len, B)
+    with torch.cuda.device(dev):
+        if bounds is None:
+            bounds = torch.zeros(NB, Hkv, 2, d, dtype=torch.bfloat16, device=dev)
+        else:
+            _need_cuda("bounds", bounds, torch.bfloat16)
+            _shape("bounds", bounds, NB, Hkv, 2, d)
+        _check(L.ts_kv_page_bounds(_p(k_cache), _dt(k_cache), NB, bs, Hkv, d, _p(block_table), width, _p(prefix_len),
+                                   _p(start_len), B, _p(bounds), _p(status), _stream()))
+    return bounds
+
+
+def page_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, prefix_len: torch.Tensor, n_pages: int, *,
+                block_size: int, max_prefix: int, first: int = 1, recent: int = 1,
+                out: Optional[Dict[str, torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
+                status: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
+    """The complete prefix pages each node of q [B,m,Hq,d] attends to: the first ``first``, the last
+    ``recent`` and the best by the bounds [num_blocks,Hkv,2,d] of its scores, n_pages in all, per KV head.
+    Returns pages [B,Hkv,C] (logical pages that any node keeps, ascending, -1 behind them), count
+    [B,Hkv] and node_mask [B,Hkv,C,ceil(m/64)] (bit i: node i keeps the page), C = max(1, max_prefix //
+    block_size): the selection that ``tree_attention_sparse`` takes."""
+    L = library()
+    dev = _same_device(q=q, bounds=bounds, block_table=block_table, prefix_len=prefix_len, status=status)
+    _need_cuda("q", q)
+    _need_cuda("bounds", bounds, torch.bfloat16)
+    _need_cuda("block_table", block_table, torch.int32)
+    _need_cuda("prefix_len", prefix_len, torch.int32)
+    B, m, Hq, d = q.shape
+    NB, Hkv, two, d2 = bounds.shape
+    if two != 2 or d2 != d:
+        raise ValueError("bounds do not match q")
+    _shape("prefix_len", prefix_len, B)
+    _shape("block_table", block_table, B, block_table.shape[1])
+    C = max(1, int(max_prefix) // int(block_size)) if block_size > 0 else 1
+    with torch.cuda.device(dev):
+        need = L.ts_page_select_workspace(B, m, Hq, Hkv, d, int(max_prefix), int(block_size))
+        if need == 0:
+            raise TreeSpecError("invalid page_select sizes")
+        out = _outputs(out, dev, pages=((B, Hkv, C), torch.int32), count=((B, Hkv), torch.int32),
+                       node_mask=((B, Hkv, C, (m + 63) // 64), torch.int64))
+        ws = _scratch(need, dev, workspace)
+        _check(L.ts_page_select(_p(q), _dt(q), _p(bounds), NB, int(block_size), _p(block_table), block_table.shape[1],
+                                _p(prefix_len), int(max_prefix), B, m, Hq, Hkv, d, int(n_pages), int(first), int(recent),
+                                _p(out["pages"]), _p(out["count"]), _p(out["node_mask"]), _p(ws),
+                                ws.numel() * ws.element_size(), _p(status), _stream()))
+    return out
+
+
+def tree_attention_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                          prefix_len: torch.Tensor, mask: torch.Tensor, selection: Dict[str, torch.Tensor], *,
+                          scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                          lse: Optional[torch.Tensor] = None, with_lse: bool = True,
+                          workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """Tree attention over chosen pages: each node of q [B,m,Hq,d] attends to the pages that
+    ``selection`` (pages, count and node_mask of ``page_select``) gives it, to the prefix rows of the page
+    that is not complete yet and to its ancestors (mask).  Returns (out, lse) like ``tree_attention``."""
+    L = library()
+    pages, count, node_mask = selection["pages"], selection["count"], selection["node_mask"]
+    dev = _same_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, prefix_len=prefix_len, mask=mask,
+                       pages=pages, count=count, node_mask=node_mask, out=out, lse=lse, status=status)
+    _need_cuda("q", q)
+    _need_cache(k_cache, v_cache)
+    if k_cache.dtype != q.dtype:
+        raise ValueError(f"k_cache must be {q.dtype}, got {k_cache.dtype}")
+    for name, t, dt in (("block_table", block_table, torch.int32), ("prefix_len", prefix_len, torch.int32),
+                        ("mask", mask, torch.int64), ("pages", pages, torch.int32), ("count", count, torch.int32),
+                        ("node_mask", node_mask, torch.int64)):
+        _need_cuda(name, t, dt)
+    B, m, Hq, d = q.shape
+    NB, Hkv, bs, d2 = k_cache.shape
+    if d2 != d:
+        raise ValueError("cache shapes do not match q")
+    W, C = (m + 63) // 64, pages.shape[-1]
+    _shape("block_table", block_table, B, block_table.shape[1])
+    _shape("prefix_len", prefix_len, B)
+    _shape("mask", mask, B, m, W)
+    _shape("pages", pages, B, Hkv, C)
+    _shape("count", count, B, Hkv)
+    _shape("node_mask", node_mask, B, Hkv, C, W)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty_like(q)
+        _need_cuda("out", out, q.dtype)
+        _shape("out", out, *q.shape)
+        if lse is None and with_lse:
+            lse = torch.empty(B, m, Hq, dtype=torch.float32, device=dev)
+        if lse is not None:
+            _need_cuda("lse", lse, torch.float32)
+            _shape("lse", lse, B, m, Hq)
+        need = L.ts_tree_attention_sparse_workspace(_dt(q), B, m, Hq, Hkv, d, C, bs)
+        ws = _scratch(need, dev, workspace) if need > 256 else None
+        _check(L.ts_tree_attention_sparse(_p(q), _p(k_cache), _p(v_cache), _dt(q), NB, bs, _p(block_table),
+                                          block_table.shape[1], _p(prefix_len), _p(mask), _p(pages), _p(count),
+                                          _p(node_mask), C, B, m, Hq, Hkv, d, float(scale), _p(out), _p(lse), _p(ws),
+                                          0 if ws is None else ws.numel() * ws.element_size(), _p(status), _stream()))
+    return out, lse
+
+
+def kv_reserve(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, prefix_len: torch.Tensor,
+               refs: torch.Tensor, n: int, *, freed: Optional[torch.Tensor] = None,
+               out: Optional[Dict[str, torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
+    """Pages for the next n tokens of every sequence: the pages in ``freed`` (any shape, -1 skipped; such as
+    kv_commit's freed_blocks) lose a reference each, missing pages are handed out, and a half-filled last page
+    that others hold too is replaced by a copy (its rows move in k_cache / v_cache).  Returns the new
+    block_table and refs and granted [B] (fresh pages per sequence, -1 where the pool ran short and the sequence
+    stays as it was).  ``out`` may hold the input tensors themselves, for an update in place."""
+    L = library()
+    dev = _same_device(k_cache=k_cache, v_cache=v_cache, block_table=block_table, prefix_len=prefix_len, refs=refs,
+                       freed=freed, status=status)
+    _need_cache(k_cache, v_cache)
+    for name, t in (("block_table", block_table), ("prefix_len", prefix_len), ("refs", refs)):
+        _need_cuda(name, t, torch.int32)
+    if freed is not None:
+        _need_cuda("freed", freed, torch.int32)
+    NB, Hkv, bs, d = k_cache.shape
+    B, width = block_table.shape
+    _shape("prefix_len", prefix_len, B)
+    _shape("refs", refs, NB)
+    with torch.cuda.device(dev):
+        need = L.ts_kv_reserve_workspace(NB, bs, B, int(n))
+        if need == 0:
+            raise TreeSpecError("invalid kv_reserve sizes")
+        out = _outputs(out, dev, block_table=((B, width), torch.int32), refs=((NB,), torch.int32),
+                       granted=((B,), torch.int32))
+        if _overlap(out["block_table"], block_table) or _overlap(out["refs"], refs):
+            raise ValueError("an output must be its input's buffer or lie apart from it")
+        ws = _scratch(need, dev, workspace)
+        nfreed = 0 if freed is None else freed.numel()
+        _check(L.ts_kv_reserve(_p(k_cache), _p(v_cache), _dt(k_cache), NB, bs, Hkv, d, _p(block_table), width,
+                               _p(prefix_len), _p(refs), B, int(n), _p(freed) if nfreed else None, nfreed,
+                               _p(out["block_table"]), _p(out["refs"]), _p(out["granted"]), _p(ws),
+                               ws.numel() * ws.element_size(), _p(status), _stream()))
+    return out
+
+
+def kv_fork(block_table: torch.Tensor, prefix_len: torch.Tensor, refs: torch.Tensor, src: torch.Tensor, block_size: int, *,
+            out: Optional[Dict[str, torch.Tensor]] = None, status: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
+    """New sequences from old ones: row r continues row src[r] (int32, any number of rows; -1: an empty row).
+    Returns the new block_table, prefix_len and refs, which replace the old ones: pages are shared, not
+    copied, and those of rows that nobody continues are let go.  ``out["refs"]`` may be ``refs`` itself."""
+    L = library()
+    dev = _same_device(block_table=block_table, prefix_len=prefix_len, refs=refs, src=src, status=status)
+    for name, t in (("block_table", block_table), ("prefix_len", prefix_len), ("refs", refs), ("src", src)):
+        _need_cuda(name, t, torch.int32)
+    B, width = block_table.shape
+    _shape("prefix_len", prefix_len, B)
+    if src.dim() != 1 or refs.dim() != 1:
+        raise ValueError("src and refs must have one dimension")
+    R, NB = src.shape[0], refs.shape[0]
+    with torch.cuda.device(dev):
+        out = _outputs(out, dev, block_table=((R, width), torch.int32), prefix_len=((R,), torch.int32),
+                       refs=((NB,), torch.int32))
+        for k, t in (("block_table", block_table), ("prefix_len", prefix_len), ("refs", refs)):
+            if _overlap(out[k], t) or (k != "refs" and out[k].data_ptr() == t.data_ptr()):
+                raise ValueError(f"out[{k!r}] must lie apart from {k}")
+        _check(L.ts_kv_fork(_p(block_table), width, _p(prefix_len), _p(refs), NB, int(block_size), B, _p(src), R,
+                            _p(out["block_table"]), _p(out["prefix_len"]), _p(out["refs"]), _p(status), _stream()))
+    return out
+
+
+def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, refs: torch.Tensor, *,
+               bounds: Optional[torch.Tensor] = None, out: Optional[Dict[str, torch.Tensor]] = None,
+               workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
+    """Move the pages in use (refs > 0) to the lowest ids, in place on k_cache / v_cache (and bounds).  Returns the
+    new block_table and refs, remap [num_blocks] (a page's new id, -1 for a free one) and live [1] (pages in
+    use).  ``out`` may hold block_table and refs themselves, for an update in place."""
+    L = library()
+    dev = _same_device(k_cache=k_cache, v_cache=v_cache, block_table=block_table, refs=refs, bounds=bounds, status=status)
+    _need_cache(k_cache, v_cache)
+    _need_cuda("block_table", block_table, torch.int32)
+    _need_cuda("refs", refs, torch.int32)
+    NB, Hkv, bs, d = k_cache.shape
+    B, width = block_table.shape
+    _shape("refs", refs, NB)
+    if bounds is not None:
+        _need_cuda("bounds", bounds, torch.bfloat16)
+        _shape("bounds", bounds, NB, Hkv, 2, d)
+    with torch.cuda.device(dev):
+        out = _outputs(out, dev, block_table=((B, width), torch.int32), refs=((NB,), torch.int32),
+                       remap=((NB,), torch.int32), live=((1,), torch.int32))
+        if _overlap(out["block_table"], block_table) or _overlap(out["refs"], refs):
+            raise ValueError("an output must be its input's buffer or lie apart from it")
+        ws = _scratch(L.ts_kv_compact_workspace(NB), dev, workspace)
+        _check(L.ts_kv_compact(_p(k_cache), _p(v_cache), _dt(k_cache), _p(bounds), NB, bs, Hkv, d, _p(block_table), width,
+                               _p(refs), B, _p(out["block_table"]), _p(out["refs"]), _p(out["remap"]), _p(out["live"]),
+                               _p(ws), ws.numel() * ws.element_size(), _p(status), _stream()))
     return out

@@ -64,6 +64,7 @@ const char* ts_status_string(int status) {
     case TS_ERR_CUDA: return "TS_ERR_CUDA: CUDA launch or driver call failed";
     case TS_ERR_TIMEOUT: return "TS_ERR_TIMEOUT: a bounded device wait timed out";
     case TS_ERR_DEVICE_CHECK: return "TS_ERR_DEVICE_CHECK: bad input data found on the device";
+    case TS_ERR_NO_PAGES: return "TS_ERR_NO_PAGES: the page pool has too few free pages";
     default: return "unknown ts_status";
   }
 }
@@ -357,6 +358,163 @@ int ts_tree_prune(const int32_t* tokens, const int32_t* parents, const int32_t* 
   return ts::tree_prune_launch(tokens, parents, depth, values, node_row, B, m, t_draft, t_fixed, t_node, n_out,
                                tokens_out, parents_out, depth_out, mask_out, values_out, node_row_out, kept_out,
                                expected_out, workspace, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+// What the calls on a paged cache share.
+static int check_cache(ts_dtype dt, int num_blocks, int block_size, int Hkv, int d, int max_blocks, int B) {
+  if (dt != TS_F32 && dt != TS_BF16) return TS_ERR_INVALID;
+  if (num_blocks <= 0 || block_size <= 0 || Hkv <= 0 || d <= 0 || max_blocks <= 0 || B <= 0) return TS_ERR_INVALID;
+  if (B > 65535) return TS_ERR_UNSUPPORTED;
+  return TS_OK;
+}
+
+int ts_kv_page_bounds(const void* k_cache, ts_dtype dt, int num_blocks, int block_size, int Hkv, int d,
+                      const int32_t* block_table, int max_blocks, const int32_t* prefix_len,
+                      const int32_t* start_len, int B, void* bounds, int32_t* dev_status, void* stream) {
+  const int rc = check_cache(dt, num_blocks, block_size, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  if (d > 256) return TS_ERR_UNSUPPORTED;
+  if (!k_cache || !block_table || !prefix_len || !bounds) return TS_ERR_INVALID;
+  const int sms = ts::device_sm_count();
+  if (sms <= 0) return TS_ERR_CUDA;
+  return ts::kv_page_bounds_launch(k_cache, dt, num_blocks, block_size, Hkv, d, block_table, max_blocks, prefix_len,
+                                   start_len, B, bounds, dev_status, static_cast<cudaStream_t>(stream), sms);
+}
+
+static int check_select(int B, int m, int Hq, int Hkv, int d, int max_prefix, int block_size) {
+  if (B <= 0 || m <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || max_prefix < 0 || block_size <= 0 || Hq % Hkv != 0)
+    return TS_ERR_INVALID;
+  if (m > TS_MAX_NODES || d > 256 || Hq / Hkv > 128 || max_prefix / block_size > 65536 ||
+      static_cast<long long>(B) * Hkv > 65535)
+    return TS_ERR_UNSUPPORTED;
+  return TS_OK;
+}
+
+size_t ts_page_select_workspace(int B, int m, int Hq, int Hkv, int d, int max_prefix, int block_size) {
+  if (check_select(B, m, Hq, Hkv, d, max_prefix, block_size) != TS_OK) return 0;
+  const int C = max_prefix / block_size;
+  return ts::page_select_workspace_bytes(B, m, Hkv, C > 0 ? C : 1);
+}
+
+int ts_page_select(const void* q, ts_dtype dt, const void* bounds, int num_blocks, int block_size,
+                   const int32_t* block_table, int max_blocks, const int32_t* prefix_len, int max_prefix,
+                   int B, int m, int Hq, int Hkv, int d, int n_pages, int first, int recent,
+                   int32_t* pages, int32_t* count, uint64_t* node_mask,
+                   void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  int rc = check_select(B, m, Hq, Hkv, d, max_prefix, block_size);
+  if (rc != TS_OK) return rc;
+  rc = check_cache(dt, num_blocks, block_size, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  if (n_pages < 1 || first < 0 || recent < 0 || static_cast<long long>(first) + recent > n_pages) return TS_ERR_INVALID;
+  if (static_cast<long long>(max_blocks) * block_size < max_prefix / block_size * static_cast<long long>(block_size))
+    return TS_ERR_INVALID;
+  if (!q || !bounds || !block_table || !prefix_len || !pages || !count || !node_mask || !workspace) return TS_ERR_INVALID;
+  if (!aligned16_ptr(bounds) || !aligned16_ptr(workspace)) return TS_ERR_INVALID;
+  if (ws_bytes < ts_page_select_workspace(B, m, Hq, Hkv, d, max_prefix, block_size)) return TS_ERR_WORKSPACE;
+  const int sms = ts::device_sm_count();
+  if (sms <= 0) return TS_ERR_CUDA;
+  ts::SelectCall c{q, dt, bounds, num_blocks, block_size, block_table, max_blocks, prefix_len, max_prefix, B, m, Hq, Hkv, d,
+                   n_pages, first, recent, pages, count, node_mask, workspace, dev_status};
+  return ts::page_select_launch(c, static_cast<cudaStream_t>(stream), sms);
+}
+
+static int check_sparse(ts_dtype dt, int B, int m, int Hq, int Hkv, int d, int C, int block_size) {
+  const int rc = ts::check_attention(dt, B, m, Hq, Hkv, d, 0);
+  if (rc != TS_OK) return rc;
+  if (C <= 0 || block_size <= 0) return TS_ERR_INVALID;
+  // keys a node can have at most, as a 32-bit position
+  if (static_cast<long long>(C) * block_size > (1LL << 30)) return TS_ERR_UNSUPPORTED;
+  return TS_OK;
+}
+
+size_t ts_tree_attention_sparse_workspace(ts_dtype dt, int B, int m, int Hq, int Hkv, int d, int C, int block_size) {
+  if (check_sparse(dt, B, m, Hq, Hkv, d, C, block_size) != TS_OK) return 0;
+  if (ts::attention_uses_tc(dt, d, block_size))
+    return ts::attention_sparse_tc_workspace_bytes(B, m, Hq, Hkv, C, block_size, ts::device_sm_count());
+  return 256;
+}
+
+int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_cache, ts_dtype dt,
+                             int num_blocks, int block_size, const int32_t* block_table, int max_blocks,
+                             const int32_t* prefix_len, const uint64_t* mask, const int32_t* pages,
+                             const int32_t* count, const uint64_t* node_mask, int C,
+                             int B, int m, int Hq, int Hkv, int d, float scale, void* out, float* lse,
+                             void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  int rc = check_sparse(dt, B, m, Hq, Hkv, d, C, block_size);
+  if (rc != TS_OK) return rc;
+  rc = check_cache(dt, num_blocks, block_size, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  if (!q || !k_cache || !v_cache || !block_table || !prefix_len || !mask || !pages || !count || !node_mask || !out)
+    return TS_ERR_INVALID;
+  if (!std::isfinite(scale)) return TS_ERR_INVALID;
+  ts::SparseCall a{q, k_cache, v_cache, dt, num_blocks, block_size, block_table, max_blocks, prefix_len, mask, pages, count,
+                   node_mask, C, B, m, Hq, Hkv, d, scale, out, lse, workspace, dev_status};
+  if (!ts::attention_uses_tc(dt, d, block_size)) return ts::attention_sparse_simt_launch(a, static_cast<cudaStream_t>(stream));
+  if (!aligned16_ptr(q) || !aligned16_ptr(k_cache) || !aligned16_ptr(v_cache) || !aligned16_ptr(out)) return TS_ERR_INVALID;
+  const int sms = ts::device_sm_count();
+  if (sms <= 0) return TS_ERR_CUDA;
+  const size_t need = ts::attention_sparse_tc_workspace_bytes(B, m, Hq, Hkv, C, block_size, sms);
+  if (need > 256 && (!workspace || ws_bytes < need)) return TS_ERR_WORKSPACE;
+  if (need > 256 && !aligned16_ptr(workspace)) return TS_ERR_INVALID;
+  return ts::attention_sparse_tc_launch(a, static_cast<cudaStream_t>(stream), sms);
+}
+
+size_t ts_kv_reserve_workspace(int num_blocks, int block_size, int B, int n) {
+  if (num_blocks <= 0 || block_size <= 0 || B <= 0 || n <= 0 || B > TS_MAX_POOL_ROWS) return 0;
+  return ts::kv_reserve_workspace_bytes(num_blocks, block_size, B, n);
+}
+
+int ts_kv_reserve(void* k_cache, void* v_cache, ts_dtype dt, int num_blocks, int block_size, int Hkv, int d,
+                  const int32_t* block_table, int max_blocks, const int32_t* prefix_len, const int32_t* refs,
+                  int B, int n, const int32_t* freed, int num_freed, int32_t* block_table_out,
+                  int32_t* refs_out, int32_t* granted, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                  void* stream) {
+  const int rc = check_cache(dt, num_blocks, block_size, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  if (num_blocks > (1 << 28)) return TS_ERR_UNSUPPORTED;
+  if (n <= 0 || num_freed < 0 || (num_freed > 0 && !freed)) return TS_ERR_INVALID;
+  if ((d * (dt == TS_BF16 ? 2LL : 4LL)) % 4 != 0) return TS_ERR_INVALID;
+  if (B > TS_MAX_POOL_ROWS) return TS_ERR_UNSUPPORTED;
+  if (!k_cache || !v_cache || !block_table || !prefix_len || !refs || !block_table_out || !refs_out || !granted || !workspace)
+    return TS_ERR_INVALID;
+  if (ws_bytes < ts::kv_reserve_workspace_bytes(num_blocks, block_size, B, n)) return TS_ERR_WORKSPACE;
+  ts::ReserveCall c{k_cache, v_cache, dt, num_blocks, block_size, Hkv, d, block_table, max_blocks, prefix_len, refs, B, n,
+                    freed, num_freed, block_table_out, refs_out, granted, workspace, dev_status};
+  return ts::kv_reserve_launch(c, static_cast<cudaStream_t>(stream));
+}
+
+int ts_kv_fork(const int32_t* block_table, int max_blocks, const int32_t* prefix_len, const int32_t* refs,
+               int num_blocks, int block_size, int B, const int32_t* src, int B_out, int32_t* block_table_out,
+               int32_t* prefix_len_out, int32_t* refs_out, int32_t* dev_status, void* stream) {
+  if (num_blocks <= 0 || block_size <= 0 || max_blocks <= 0 || B <= 0 || B_out <= 0) return TS_ERR_INVALID;
+  if (B > 65535 || B_out > 65535) return TS_ERR_UNSUPPORTED;
+  if (!block_table || !prefix_len || !refs || !src || !block_table_out || !prefix_len_out || !refs_out) return TS_ERR_INVALID;
+  if (block_table_out == block_table || prefix_len_out == prefix_len) return TS_ERR_INVALID;
+  const int sms = ts::device_sm_count();
+  if (sms <= 0) return TS_ERR_CUDA;
+  return ts::kv_fork_launch(block_table, max_blocks, prefix_len, refs, num_blocks, block_size, B, src, B_out, block_table_out,
+                            prefix_len_out, refs_out, dev_status, static_cast<cudaStream_t>(stream), sms);
+}
+
+size_t ts_kv_compact_workspace(int num_blocks) { return num_blocks > 0 ? ts::kv_compact_workspace_bytes(num_blocks) : 0; }
+
+int ts_kv_compact(void* k_cache, void* v_cache, ts_dtype dt, void* bounds, int num_blocks, int block_size,
+                  int Hkv, int d, const int32_t* block_table, int max_blocks, const int32_t* refs, int B,
+                  int32_t* block_table_out, int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace,
+                  size_t ws_bytes, int32_t* dev_status, void* stream) {
+  const int rc = check_cache(dt, num_blocks, block_size, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  if ((d * (dt == TS_BF16 ? 2LL : 4LL)) % 4 != 0) return TS_ERR_INVALID;
+  if (!k_cache || !v_cache || !block_table || !refs || !block_table_out || !refs_out || !remap || !live || !workspace)
+    return TS_ERR_INVALID;
+  if (num_blocks > (1 << 28)) return TS_ERR_UNSUPPORTED;
+  if (bounds && !aligned16_ptr(bounds)) return TS_ERR_INVALID;
+  if (ws_bytes < ts::kv_compact_workspace_bytes(num_blocks)) return TS_ERR_WORKSPACE;
+  const int sms = ts::device_sm_count();
+  if (sms <= 0) return TS_ERR_CUDA;
+  return ts::kv_compact_launch(k_cache, v_cache, dt, bounds, num_blocks, block_size, Hkv, d, block_table, max_blocks, refs, B,
+                               block_table_out, refs_out, remap, live, workspace, dev_status,
+                               static_cast<cudaStream_t>(stream), sms);
 }
 
 int ts_selftest_bounded_wait(int mode, int32_t* result, int32_t* dev_status, void* stream) {

@@ -104,4 +104,83 @@ int kv_commit_launch(void* k_cache, void* v_cache, ts_dtype dt, int num_blocks, 
                      int32_t* freed_blocks, int32_t* freed_count, int32_t* dev_status,
                      cudaStream_t stream);
 
+// Page bounds, the choice of pages and attention over it (page_bounds.cu, page_select.cu,
+// tree_attention_tc.cu / tree_attention_sparse.cu).
+int kv_page_bounds_launch(const void* k_cache, ts_dtype dt, int num_blocks, int block_size, int Hkv, int d,
+                          const int32_t* block_table, int max_blocks, const int32_t* prefix_len,
+                          const int32_t* start_len, int B, void* bounds, int32_t* dev_status, cudaStream_t stream,
+                          int num_sms);
+
+struct SelectCall {
+  const void* q;
+  ts_dtype dt;
+  const void* bounds;
+  int num_blocks, block_size;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* prefix_len;
+  int max_prefix, B, m, Hq, Hkv, d, n_pages, first, recent;
+  int32_t* pages;
+  int32_t* count;
+  uint64_t* node_mask;
+  void* workspace;
+  int32_t* dev_status;
+};
+size_t page_select_workspace_bytes(int B, int m, int Hkv, int C);
+int page_select_launch(const SelectCall& c, cudaStream_t stream, int num_sms);
+
+struct SparseCall {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  ts_dtype dt;
+  int num_blocks, block_size;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* prefix_len;
+  const uint64_t* mask;
+  const int32_t* pages;
+  const int32_t* count;
+  const uint64_t* node_mask;
+  int C, B, m, Hq, Hkv, d;
+  float scale;
+  void* out;
+  float* lse;
+  void* workspace;
+  int32_t* dev_status;
+};
+int attention_sparse_simt_launch(const SparseCall& a, cudaStream_t stream);
+size_t attention_sparse_tc_workspace_bytes(int B, int m, int Hq, int Hkv, int C, int block_size, int num_sms);
+int attention_sparse_tc_launch(const SparseCall& a, cudaStream_t stream, int num_sms);
+
+// The page pool (page_pool.cu).
+struct ReserveCall {
+  void* k_cache;
+  void* v_cache;
+  ts_dtype dt;
+  int num_blocks, block_size, Hkv, d;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* prefix_len;
+  const int32_t* refs;
+  int B, n;
+  const int32_t* freed;
+  int num_freed;
+  int32_t* block_table_out;
+  int32_t* refs_out;
+  int32_t* granted;
+  void* workspace;
+  int32_t* dev_status;
+};
+size_t kv_reserve_workspace_bytes(int num_blocks, int block_size, int B, int n);
+int kv_reserve_launch(const ReserveCall& c, cudaStream_t stream);
+int kv_fork_launch(const int32_t* block_table, int max_blocks, const int32_t* prefix_len, const int32_t* refs, int num_blocks,
+                   int block_size, int B, const int32_t* src, int B_out, int32_t* block_table_out, int32_t* prefix_len_out,
+                   int32_t* refs_out, int32_t* dev_status, cudaStream_t stream, int num_sms);
+size_t kv_compact_workspace_bytes(int num_blocks);
+int kv_compact_launch(void* k_cache, void* v_cache, ts_dtype dt, void* bounds, int num_blocks, int block_size, int Hkv, int d,
+                      const int32_t* block_table, int max_blocks, const int32_t* refs, int B, int32_t* block_table_out,
+                      int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace, int32_t* dev_status,
+                      cudaStream_t stream, int num_sms);
+
 }  // namespace ts

@@ -1,0 +1,562 @@
+// The page pool: ts_kv_reserve, ts_kv_fork, ts_kv_compact.
+//
+// State: a block table per sequence and refs, the number of table entries that name each page.
+// What a call decides (which pages are free, who gets which, what moves where) is bookkeeping over
+// refs and the tables: a few kilobytes to a few megabytes with a global order in it, so it is
+// bound by latency.  reserve and compact run it as ONE thread-block cluster of eight CTAs: each CTA
+// takes a contiguous share of the pages, and a step that needs everyone's result (how many free
+// pages lie before mine) is a hardware cluster barrier, not another launch.  The rows of K and V
+// that change place are then copied by a second, wide launch, bound by HBM.  fork has no global
+// order (counts change by whole numbers, which commute) and runs wide from the start.
+//
+// Free pages are always handed out in increasing id and requests are ranked by (sequence,
+// logical page), by prefix sums, so the outcome does not depend on the order of execution.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace ts {
+namespace {
+
+constexpr int kPoolCtas = 8;        // one cluster (the portable limit)
+constexpr int kPoolThreads = 1024;
+constexpr int kPoolWarps = kPoolThreads / 32;
+
+// Exclusive prefix sum of v over the CTA's threads; *total is the sum.  Two barriers.
+__device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  int w = s_warp[lane];  // kPoolWarps == 32: every warp sums the warps' totals for itself
+  int winc = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, winc, o);
+    if (lane >= o) winc += y;
+  }
+  const int before = __shfl_sync(0xffffffffu, winc - w, warp);
+  *total = __shfl_sync(0xffffffffu, winc, 31);
+  __syncthreads();
+  return before + inc - v;
+}
+
+// One value per CTA of the cluster: everyone gets the sum of the lower ranks' and the total.
+// Contains a cluster barrier (also for the global memory written before it).
+__device__ __forceinline__ int cluster_scan(int mine, int* s_all, int* total) {
+  const uint32_t rank = cluster_ctarank();
+  if (threadIdx.x < kPoolCtas)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_addr(smem_u32(s_all + rank), threadIdx.x)), "r"(mine)
+                 : "memory");
+  cluster_sync_all();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int c = 0; c < kPoolCtas; ++c) {
+    before += c < static_cast<int>(rank) ? s_all[c] : 0;
+    sum += s_all[c];
+  }
+  *total = sum;
+  return before;
+}
+
+// ------------------------------------------------------------------------------------ reserve
+struct ReserveArgs {
+  const int32_t* table;
+  const int32_t* prefix_len;
+  const int32_t* refs;
+  const int32_t* freed;
+  int32_t* table_out;
+  int32_t* refs_out;
+  int32_t* granted;
+  int32_t* tail;       // [B] page of the half-filled last page where others hold it too, else -1
+  int32_t* tail_refs;  // [B] its references before any copy
+  int32_t* want;       // [B] fresh pages the row asks for, -1 for a row with a bad state
+  int32_t* copy;       // [B, 2] page to copy from and to (from -1: none)
+  int32_t* free_list;  // the lowest free pages, as many as are asked for
+  int32_t* status;
+  long long n;
+  int num_blocks, bs, max_blocks, B, num_freed;
+};
+
+// The row's logical pages [first, last) for positions L .. L+n-1; false for a bad state.
+__device__ __forceinline__ bool row_span(const ReserveArgs& a, int b, int* L, int* first, int* last) {
+  *L = a.prefix_len[b];
+  if (*L < 0 || *L + a.n > static_cast<long long>(a.max_blocks) * a.bs) return false;
+  *first = *L / a.bs;
+  *last = static_cast<int>((*L + a.n + a.bs - 1) / a.bs);
+  return true;
+}
+
+__global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1) reserve_kernel(const ReserveArgs a) {
+  __shared__ int s_warp[32], s_all[kPoolCtas], s_first_short;
+  __shared__ int s_off[TS_MAX_POOL_ROWS];
+  pdl_wait();
+  if (threadIdx.x == 0) s_first_short = a.B;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gtid = rank * kPoolThreads + tid, gthreads = kPoolCtas * kPoolThreads;
+  const int gwarp = rank * kPoolWarps + warp, gwarps = kPoolCtas * kPoolWarps;
+  // the new state starts as the old one
+  if (a.refs_out != a.refs)
+    for (int i = gtid; i < a.num_blocks; i += gthreads) a.refs_out[i] = a.refs[i];
+  if (a.table_out != a.table) {
+    const long long cells = static_cast<long long>(a.B) * a.max_blocks;
+    for (long long i = gtid; i < cells; i += gthreads) a.table_out[i] = a.table[i];
+  }
+  if (a.num_freed > 0) {
+    cluster_sync_all();
+    for (int i = gtid; i < a.num_freed; i += gthreads) {
+      const int p = a.freed[i];
+      if (p < 0) continue;
+      if (p >= a.num_blocks) {
+        report(a.status, TS_ERR_DEVICE_CHECK);
+      } else if (atomicSub(a.refs_out + p, 1) <= 0) {  // undone: the sum is the same in every order
+        atomicAdd(a.refs_out + p, 1);
+        report(a.status, TS_ERR_DEVICE_CHECK);
+      }
+    }
+  }
+  cluster_sync_all();
+  // what each row lacks, and whether its last page is shared; a warp per row
+  for (int b = gwarp; b < a.B; b += gwarps) {
+    int L, first, last, need = 0, tail = -1;
+    bool ok = row_span(a, b, &L, &first, &last);
+    if (ok) {
+      const int32_t* row = a.table + static_cast<long long>(b) * a.max_blocks;
+      bool bad = false;
+      for (int i0 = first; i0 < last; i0 += 32) {
+        const int p = i0 + lane < last ? row[i0 + lane] : 0;
+        bad |= p < -1 || p >= a.num_blocks;
+        need += __popc(__ballot_sync(0xffffffffu, i0 + lane < last && p == -1));
+        if (i0 == first) tail = __shfl_sync(0xffffffffu, p, 0);
+      }
+      ok = !__any_sync(0xffffffffu, bad);
+      if (L % a.bs == 0 || !ok) tail = -1;
+    }
+    if (lane == 0) {
+      const int n = tail >= 0 ? __ldcg(a.refs_out + tail) : 0;
+      a.tail[b] = n > 1 ? tail : -1;
+      a.tail_refs[b] = n;
+      a.want[b] = ok ? need : -1;
+      if (!ok) report(a.status, TS_ERR_DEVICE_CHECK);
+    }
+  }
+  // free pages of this CTA's share
+  const int share = ((a.num_blocks + gthreads - 1) / gthreads) * kPoolThreads;
+  const int lo = static_cast<int>(min(static_cast<long long>(rank) * share, static_cast<long long>(a.num_blocks)));
+  const int hi = min(lo + share, a.num_blocks);
+  int nfree = 0;
+  for (int i = lo + tid; i < hi; i += kPoolThreads) nfree += __ldcg(a.refs_out + i) == 0;
+  int here;
+  block_scan(nfree, s_warp, &here);
+  int F;
+  const int free_before = cluster_scan(here, s_all, &F);
+  // of the rows that share a last page, each copies it as long as another reference is left
+  for (int b = gwarp; b < a.B; b += gwarps) {
+    const int t = __ldcg(a.tail + b);
+    if (t < 0) {
+      if (lane < 2) a.copy[2 * b + lane] = -1;
+      continue;
+    }
+    int before = 0;
+    for (int j = lane; j < b; j += 32) before += __ldcg(a.tail + j) == t;
+    before = __reduce_add_sync(0xffffffffu, before);
+    const bool copies = __ldcg(a.tail_refs + b) - before > 1;
+    if (lane == 0) {
+      a.copy[2 * b] = copies ? t : -1;
+      a.copy[2 * b + 1] = -1;
+      if (copies) a.want[b] = __ldcg(a.want + b) + 1;
+    }
+  }
+  cluster_sync_all();
+  // where each row's requests start in the order (every CTA for itself)
+  int R = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPoolThreads) {
+    const int w = b0 + tid < a.B ? max(0, __ldcg(a.want + b0 + tid)) : 0;
+    int sum;
+    const int at = block_scan(w, s_warp, &sum);
+    if (b0 + tid < a.B) s_off[b0 + tid] = R + at;
+    if (w > 0 && R + at + w > F) atomicMin(&s_first_short, b0 + tid);
+    R += sum;
+  }
+  // this CTA's free pages that somebody gets
+  int at = free_before;
+  for (int i0 = lo; i0 < hi && at < R; i0 += kPoolThreads) {
+    const int i = i0 + tid;
+    const int f = i < hi && __ldcg(a.refs_out + i) == 0;
+    int sum;
+    const int r = at + block_scan(f, s_warp, &sum);
+    if (f && r < R) a.free_list[r] = i;
+    at += sum;
+  }
+  cluster_sync_all();
+  const int first_short = s_first_short;
+  for (int b = gwarp; b < a.B; b += gwarps) {
+    const int w = __ldcg(a.want + b);
+    const int from = __ldcg(a.copy + 2 * b);
+    bool is_short = w > 0 && b >= first_short;
+    if (w == 0 && b > first_short) {
+      // it was to keep its last page because others before it would have left it: not all have
+      const int t = __ldcg(a.tail + b);
+      if (t >= 0) {
+        int left = 0;
+        for (int j = lane; j < first_short; j += 32) left += __ldcg(a.tail + j) == t;
+        is_short = __ldcg(a.tail_refs + b) - __reduce_add_sync(0xffffffffu, left) > 1;
+      }
+    }
+    if (w <= 0 || is_short) {
+      if (lane == 0) {
+        a.granted[b] = is_short ? -1 : w;
+        a.copy[2 * b] = -1;
+        if (is_short) report(a.status, TS_ERR_NO_PAGES);
+      }
+      continue;
+    }
+    int L, first, last;
+    row_span(a, b, &L, &first, &last);
+    int32_t* row = a.table_out + static_cast<long long>(b) * a.max_blocks;
+    int r = s_off[b];
+    for (int i0 = first; i0 < last; i0 += 32) {
+      const int i = i0 + lane;
+      const bool take = i < last && ((i == first && from >= 0) || __ldcg(row + i) == -1);
+      const unsigned m = __ballot_sync(0xffffffffu, take);
+      if (take) {
+        const int page = __ldcg(a.free_list + r + __popc(m & ((1u << lane) - 1u)));
+        row[i] = page;
+        a.refs_out[page] = 1;
+        if (i == first && from >= 0) {
+          a.copy[2 * b + 1] = page;
+          atomicSub(a.refs_out + from, 1);
+        }
+      }
+      r += __popc(m);
+    }
+    if (lane == 0) a.granted[b] = w;
+  }
+}
+
+// The first L % bs rows of the shared last pages, for every KV head: CTA (head, row b).
+template <typename Chunk>
+__global__ void __launch_bounds__(256) copy_tails_kernel(unsigned char* kc, unsigned char* vc, int Hkv, int bs, int row_bytes,
+                                                         const int32_t* __restrict__ copy,
+                                                         const int32_t* __restrict__ prefix_len) {
+  pdl_wait();
+  const int b = blockIdx.y, h = blockIdx.x;
+  const int from = copy[2 * b], to = copy[2 * b + 1];
+  if (from < 0 || to < 0) return;
+  const int chunks = prefix_len[b] % bs * (row_bytes / static_cast<int>(sizeof(Chunk)));
+  const long long page = static_cast<long long>(bs) * row_bytes;
+  const long long src = (static_cast<long long>(from) * Hkv + h) * page, dst = (static_cast<long long>(to) * Hkv + h) * page;
+  const Chunk* ks = reinterpret_cast<const Chunk*>(kc + src);
+  const Chunk* vs = reinterpret_cast<const Chunk*>(vc + src);
+  Chunk* kd = reinterpret_cast<Chunk*>(kc + dst);
+  Chunk* vd = reinterpret_cast<Chunk*>(vc + dst);
+  for (int i0 = threadIdx.x; i0 < chunks; i0 += 256 * 4) {
+    Chunk k[4], v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (i0 + 256 * u < chunks) {
+        k[u] = ks[i0 + 256 * u];
+        v[u] = vs[i0 + 256 * u];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (i0 + 256 * u < chunks) {
+        kd[i0 + 256 * u] = k[u];
+        vd[i0 + 256 * u] = v[u];
+      }
+    }
+  }
+}
+
+// --------------------------------------------------------------------------------------- fork
+// New rows, and refs_out = refs where they are different buffers.
+__global__ void __launch_bounds__(256) fork_rows_kernel(const int32_t* __restrict__ table, int max_blocks,
+                                                        const int32_t* __restrict__ prefix_len, const int32_t* refs,
+                                                        int num_blocks, int bs, int B, const int32_t* __restrict__ src,
+                                                        int B_out, int32_t* __restrict__ table_out,
+                                                        int32_t* __restrict__ prefix_out, int32_t* refs_out,
+                                                        int32_t* status) {
+  pdl_wait();
+  const int tid = threadIdx.x;
+  for (int r = blockIdx.x; r < B_out; r += gridDim.x) {
+    const int s = src[r];
+    bool bad = s < -1 || s >= B;
+    int L = 0;
+    if (!bad && s >= 0) {
+      L = prefix_len[s];
+      if (L < 0 || L > static_cast<long long>(max_blocks) * bs) {
+        bad = true;
+        L = 0;
+      }
+    }
+    const int kept = static_cast<int>((static_cast<long long>(L) + bs - 1) / bs);
+    int32_t* row = table_out + static_cast<long long>(r) * max_blocks;
+    for (int i = tid; i < max_blocks; i += 256) {
+      int p = -1;
+      if (i < kept) {
+        p = table[static_cast<long long>(s) * max_blocks + i];
+        if (p < 0 || p >= num_blocks) {
+          p = -1;
+          bad = true;
+        }
+      }
+      row[i] = p;
+    }
+    if (bad) report(status, TS_ERR_DEVICE_CHECK);
+    if (tid == 0) prefix_out[r] = L;
+  }
+  if (refs_out != refs)
+    for (int i = blockIdx.x * 256 + tid; i < num_blocks; i += gridDim.x * 256) refs_out[i] = refs[i];
+}
+
+// Counts: an entry of old row s among its kept pages is named once less and once more per new row
+// that continues s; an entry beyond them is only let go.  Rows continued exactly once cost no
+// atomic for their kept pages.
+__global__ void __launch_bounds__(256) fork_refs_kernel(const int32_t* __restrict__ table, int max_blocks,
+                                                        const int32_t* __restrict__ prefix_len, int num_blocks, int bs,
+                                                        int B, const int32_t* __restrict__ src, int B_out,
+                                                        int32_t* __restrict__ refs_out, int32_t* status) {
+  __shared__ int s_sum[8];
+  pdl_wait();
+  const int tid = threadIdx.x;
+  for (int s = blockIdx.x; s < B; s += gridDim.x) {
+    int times = 0;
+    for (int r = tid; r < B_out; r += 256) times += src[r] == s;
+    times = __reduce_add_sync(0xffffffffu, times);
+    __syncthreads();
+    if ((tid & 31) == 0) s_sum[tid >> 5] = times;
+    __syncthreads();
+    times = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) times += s_sum[w];
+    const int L = prefix_len[s];
+    const bool bad = L < 0 || L > static_cast<long long>(max_blocks) * bs;
+    const int kept = bad ? 0 : static_cast<int>((static_cast<long long>(L) + bs - 1) / bs);
+    for (int i = tid; i < max_blocks; i += 256) {
+      const int delta = (i < kept ? times : 0) - 1;
+      if (delta == 0) continue;
+      const int p = table[static_cast<long long>(s) * max_blocks + i];
+      if (p == -1) continue;
+      if (p < 0 || p >= num_blocks) {
+        report(status, TS_ERR_DEVICE_CHECK);
+      } else if (atomicAdd(refs_out + p, delta) + delta < 0) {
+        report(status, TS_ERR_DEVICE_CHECK);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------ compact
+struct CompactArgs {
+  const int32_t* refs;
+  int32_t* refs_out;
+  int32_t* remap;
+  int32_t* live;
+  int32_t* moves;  // [0] how many, then (from, to) pairs
+  int num_blocks;
+};
+
+__global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1) compact_kernel(const CompactArgs a) {
+  __shared__ int s_warp[32], s_all[3][kPoolCtas];
+  pdl_wait();
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int tid = threadIdx.x, gtid = rank * kPoolThreads + tid, gthreads = kPoolCtas * kPoolThreads;
+  const int share = ((a.num_blocks + gthreads - 1) / gthreads) * kPoolThreads;
+  const int lo = static_cast<int>(min(static_cast<long long>(rank) * share, static_cast<long long>(a.num_blocks)));
+  const int hi = min(lo + share, a.num_blocks);
+  cluster_sync_all();  // every CTA of the cluster runs before its shared memory is written to
+  int used = 0, sum;
+  for (int i = lo + tid; i < hi; i += kPoolThreads) used += a.refs[i] > 0;
+  block_scan(used, s_warp, &sum);
+  int live;
+  cluster_scan(sum, s_all[0], &live);
+  // free pages below `live` and pages in use from there on: as many of the one as of the other
+  int holes = 0, movers = 0, hsum, msum;
+  for (int i = lo + tid; i < hi; i += kPoolThreads) {
+    const bool u = a.refs[i] > 0;
+    holes += i < live && !u;
+    movers += i >= live && u;
+  }
+  block_scan(holes, s_warp, &hsum);
+  block_scan(movers, s_warp, &msum);
+  int htotal, mtotal;
+  int hat = cluster_scan(hsum, s_all[1], &htotal);
+  int mat = cluster_scan(msum, s_all[2], &mtotal);
+  for (int i0 = lo; i0 < hi; i0 += kPoolThreads) {
+    const int i = i0 + tid;
+    const int n = i < hi ? a.refs[i] : 0;
+    const bool u = n > 0, hole = i < hi && i < live && !u, mover = i >= live && u;
+    int s;
+    // a share may hold both kinds, holes before movers; one scan packs both counts
+    const int packed = block_scan(static_cast<int>(hole) + (static_cast<int>(mover) << 16), s_warp, &s);
+    if (hole) a.moves[2 + 2 * (hat + (packed & 0xffff))] = i;
+    if (mover) a.moves[1 + 2 * (mat + (packed >> 16))] = i;
+    if (i < hi && !mover) a.remap[i] = u ? i : -1;
+    if (a.refs_out != a.refs && i < hi && !mover && !hole) a.refs_out[i] = n;
+    hat += s & 0xffff;
+    mat += s >> 16;
+  }
+  if (gtid == 0) {
+    *a.live = live;
+    a.moves[0] = mtotal;
+  }
+  cluster_sync_all();
+  for (int k = gtid; k < mtotal; k += gthreads) {
+    const int from = __ldcg(a.moves + 1 + 2 * k), to = __ldcg(a.moves + 2 + 2 * k);
+    a.remap[from] = to;
+    a.refs_out[to] = a.refs[from];  // in place: `from` >= live > `to`, and each is touched once
+    a.refs_out[from] = 0;
+  }
+}
+
+// The moves' bytes and the tables: CTAs stride over (move, buffer) and over the table's cells.
+template <typename Chunk>
+__global__ void __launch_bounds__(256) move_pages_kernel(unsigned char* kc, unsigned char* vc, unsigned char* bounds,
+                                                         long long page_bytes, long long bounds_bytes,
+                                                         const int32_t* __restrict__ moves,
+                                                         const int32_t* __restrict__ remap, int num_blocks,
+                                                         const int32_t* table, int32_t* table_out, long long cells,
+                                                         int32_t* status) {
+  pdl_wait();
+  const int tid = threadIdx.x;
+  for (long long i = blockIdx.x * 256LL + tid; i < cells; i += gridDim.x * 256LL) {
+    const int p = table[i];
+    int q = -1;
+    if (p != -1) {
+      if (p >= 0 && p < num_blocks) q = remap[p];
+      if (q < 0) report(status, TS_ERR_DEVICE_CHECK);
+    }
+    table_out[i] = q;
+  }
+  const int n = moves[0], bufs = bounds != nullptr ? 3 : 2;
+  for (long long it = blockIdx.x; it < static_cast<long long>(n) * bufs; it += gridDim.x) {
+    const int k = static_cast<int>(it / bufs), which = static_cast<int>(it - static_cast<long long>(k) * bufs);
+    const long long from = moves[1 + 2 * k], to = moves[2 + 2 * k];
+    if (which == 2) {
+      const uint32_t* s = reinterpret_cast<const uint32_t*>(bounds + from * bounds_bytes);
+      uint32_t* d = reinterpret_cast<uint32_t*>(bounds + to * bounds_bytes);
+      for (long long i = tid; i < bounds_bytes / 4; i += 256) d[i] = s[i];
+      continue;
+    }
+    unsigned char* base = which == 0 ? kc : vc;
+    const Chunk* s = reinterpret_cast<const Chunk*>(base + from * page_bytes);
+    Chunk* d = reinterpret_cast<Chunk*>(base + to * page_bytes);
+    const int chunks = static_cast<int>(page_bytes / static_cast<long long>(sizeof(Chunk)));
+    for (int i0 = tid; i0 < chunks; i0 += 256 * 8) {
+      Chunk v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + 256 * u < chunks) v[u] = s[i0 + 256 * u];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + 256 * u < chunks) d[i0 + 256 * u] = v[u];
+    }
+  }
+}
+
+bool wide_rows(const void* k, const void* v, int row_bytes) {
+  return row_bytes % 16 == 0 && ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15u) == 0;
+}
+
+long long most_requests(int num_blocks, int block_size, int B, int n) {
+  const long long per_row = (static_cast<long long>(n) + block_size - 2) / block_size + 1;
+  return std::min<long long>(num_blocks, per_row * B);
+}
+
+}  // namespace
+
+size_t kv_reserve_workspace_bytes(int num_blocks, int block_size, int B, int n) {
+  return 4 * (static_cast<size_t>(5) * B + static_cast<size_t>(most_requests(num_blocks, block_size, B, n)));
+}
+
+int kv_reserve_launch(const ReserveCall& c, cudaStream_t stream) {
+  ReserveArgs a;
+  a.table = c.block_table;
+  a.prefix_len = c.prefix_len;
+  a.refs = c.refs;
+  a.freed = c.freed;
+  a.table_out = c.block_table_out;
+  a.refs_out = c.refs_out;
+  a.granted = c.granted;
+  a.tail = static_cast<int32_t*>(c.workspace);
+  a.tail_refs = a.tail + c.B;
+  a.want = a.tail_refs + c.B;
+  a.copy = a.want + c.B;
+  a.free_list = a.copy + 2 * static_cast<size_t>(c.B);
+  a.status = c.dev_status;
+  a.n = c.n;
+  a.num_blocks = c.num_blocks;
+  a.bs = c.block_size;
+  a.max_blocks = c.max_blocks;
+  a.B = c.B;
+  a.num_freed = c.num_freed;
+  cudaError_t e = launch_pdl(reserve_kernel, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
+  if (e != cudaSuccess) return TS_ERR_CUDA;
+  count_launches(1);
+  const int row_bytes = c.d * (c.dt == TS_BF16 ? 2 : 4);
+  unsigned char *k = static_cast<unsigned char*>(c.k_cache), *v = static_cast<unsigned char*>(c.v_cache);
+  const dim3 grid(c.Hkv, c.B);
+  e = wide_rows(k, v, row_bytes)
+          ? launch_pdl(copy_tails_kernel<uint4>, grid, dim3(256), 0, stream, k, v, c.Hkv, c.block_size, row_bytes, a.copy,
+                       c.prefix_len)
+          : launch_pdl(copy_tails_kernel<uint32_t>, grid, dim3(256), 0, stream, k, v, c.Hkv, c.block_size, row_bytes, a.copy,
+                       c.prefix_len);
+  if (e != cudaSuccess) return TS_ERR_CUDA;
+  count_launches(1);
+  return TS_OK;
+}
+
+int kv_fork_launch(const int32_t* block_table, int max_blocks, const int32_t* prefix_len, const int32_t* refs, int num_blocks,
+                   int block_size, int B, const int32_t* src, int B_out, int32_t* block_table_out, int32_t* prefix_len_out,
+                   int32_t* refs_out, int32_t* dev_status, cudaStream_t stream, int num_sms) {
+  const int copy_ctas = refs_out != refs ? (num_blocks + 1023) / 1024 : 1;
+  const int g1 = std::min(std::max(B_out, copy_ctas), 8 * num_sms);
+  cudaError_t e = launch_pdl(fork_rows_kernel, dim3(g1), dim3(256), 0, stream, block_table, max_blocks, prefix_len, refs,
+                             num_blocks, block_size, B, src, B_out, block_table_out, prefix_len_out, refs_out, dev_status);
+  if (e != cudaSuccess) return TS_ERR_CUDA;
+  count_launches(1);
+  e = launch_pdl(fork_refs_kernel, dim3(std::min(B, 8 * num_sms)), dim3(256), 0, stream, block_table, max_blocks, prefix_len,
+                 num_blocks, block_size, B, src, B_out, refs_out, dev_status);
+  if (e != cudaSuccess) return TS_ERR_CUDA;
+  count_launches(1);
+  return TS_OK;
+}
+
+size_t kv_compact_workspace_bytes(int num_blocks) { return 4 * (static_cast<size_t>(num_blocks) + 2); }
+
+int kv_compact_launch(void* k_cache, void* v_cache, ts_dtype dt, void* bounds, int num_blocks, int block_size, int Hkv, int d,
+                      const int32_t* block_table, int max_blocks, const int32_t* refs, int B, int32_t* block_table_out,
+                      int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace, int32_t* dev_status,
+                      cudaStream_t stream, int num_sms) {
+  CompactArgs a{refs, refs_out, remap, live, static_cast<int32_t*>(workspace), num_blocks};
+  cudaError_t e = launch_pdl(compact_kernel, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
+  if (e != cudaSuccess) return TS_ERR_CUDA;
+  count_launches(1);
+  const int row_bytes = d * (dt == TS_BF16 ? 2 : 4);
+  const long long page_bytes = static_cast<long long>(Hkv) * block_size * row_bytes;
+  const long long bounds_bytes = static_cast<long long>(Hkv) * 4 * d;
+  const long long cells = static_cast<long long>(B) * max_blocks;
+  unsigned char *k = static_cast<unsigned char*>(k_cache), *v = static_cast<unsigned char*>(v_cache);
+  unsigned char* bd = static_cast<unsigned char*>(bounds);
+  const dim3 grid(8 * num_sms);
+  e = wide_rows(k, v, row_bytes)
+          ? launch_pdl(move_pages_kernel<uint4>, grid, dim3(256), 0, stream, k, v, bd, page_bytes, bounds_bytes,
+                       a.moves, remap, num_blocks, block_table,
+                       block_table_out, cells, dev_status)
+          : launch_pdl(move_pages_kernel<uint32_t>, grid, dim3(256), 0, stream, k, v, bd, page_bytes, bounds_bytes,
+                       a.moves, remap, num_blocks, block_table,
+                       block_table_out, cells, dev_status);
+  if (e != cudaSuccess) return TS_ERR_CUDA;
+  count_launches(1);
+  return TS_OK;
+}
+
+}  // namespace ts

@@ -129,7 +129,105 @@ struct Params {
   int mc;  // row groups sharing each K/V tile through TMA multicast (a cluster along x), 1 = none
   int split_issue;  // 1: Q K^T and P V issued by two threads (warp 1, PV_WARP); 0: warp 1 issues both
   float scale_log2;
+  // sparse mode (tree_attn_tc_kernel<true>): the chosen pages of each (sequence, KV head)
+  const int32_t* pages;       // [B, Hkv, C]
+  const int32_t* count;       // [B, Hkv]
+  const uint64_t* node_mask;  // [B, Hkv, C, W]
+  int C;
 };
+
+// What one (sequence, KV head) reads.  The dense mode reads the sequence as it lies: L prefix keys,
+// then the tree.  The sparse mode reads a virtual sequence of whole pages: the nu chosen pages, then
+// the sequence's own pages from its first incomplete one (nf) on, so its "prefix" is the chosen pages
+// and the incomplete page's rows, and everything behind the address of a page is the same.
+struct Span {
+  int L, nkeys, nu, nf, T, tpc;
+  bool ok;
+};
+
+template <bool SP>
+__device__ __forceinline__ Span span_of(const Params& p, int b, int bk) {
+  Span s;
+  s.L = p.prefix_len[b];
+  s.nu = s.nf = 0;
+  if constexpr (SP) {
+    s.nu = p.count[bk];
+    s.ok = s.L >= 0 && s.nu >= 0 && s.nu <= p.C &&
+           static_cast<long long>(s.L) + p.m <= static_cast<long long>(p.max_blocks) * p.block_size;
+    if (!s.ok) return s;
+    s.nf = s.L / p.block_size;
+    s.L = s.nu * p.block_size + s.L - s.nf * p.block_size;
+  } else {
+    s.ok = s.L >= 0 && s.L <= p.max_prefix;
+  }
+  s.nkeys = s.L + p.m;
+  s.T = (s.nkeys + BN - 1) / BN;
+  // tiles per chunk: the dense plan's, from the longest allowed prefix; in the sparse mode, where the
+  // number of chosen pages is known here only, an even share of this unit's tiles of at least p.tpc
+  s.tpc = SP ? max(p.tpc, (s.T + p.nchunk - 1) / p.nchunk) : p.tpc;
+  return s;
+}
+
+// Logical page of virtual page v (sparse mode), -1 for a chosen page that the prefix does not complete.
+__device__ __forceinline__ int virtual_page(const Params& p, const Span& s, int bk, int v) {
+  if (v >= s.nu) return s.nf + v - s.nu;
+  const int lp = __ldg(p.pages + static_cast<long long>(bk) * p.C + v);
+  return lp >= 0 && lp < s.nf ? lp : -1;
+}
+
+// Exact output row of the sparse mode by one warp, one key at a time: used only for rows in which a
+// NaN came out of the tensor cores.  There a key that a row does not attend to has weight 0, and 0 times
+// a non-finite value of V is NaN; here such keys are not read at all.
+__device__ __noinline__ void repair_row(const Params& p, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int b, int kvh,
+                                        int node, int head) {
+  const int lane = threadIdx.x & 31, bk = b * p.Hkv + kvh;
+  const Span s = span_of<true>(p, b, bk);
+  const long long qo = ((static_cast<long long>(b) * p.m + node) * p.Hq + head) * HD + 4 * lane;
+  auto four = [](const __nv_bfloat16* x) {
+    const uint2 w = *reinterpret_cast<const uint2*>(x);
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+  };
+  const float4 q = four(p.q + qo);
+  const uint64_t* mrow = p.mask + (static_cast<long long>(b) * p.m + node) * p.W;
+  float M = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int key = 0; key < s.nkeys; ++key) {
+    const int v = key / p.block_size;
+    if (v < s.nu) {
+      const uint64_t w = p.node_mask[(static_cast<long long>(bk) * p.C + v) * p.W + (node >> 6)];
+      if (!((w >> (node & 63)) & 1ull)) {
+        key += p.block_size - 1;
+        continue;
+      }
+    } else if (key >= s.L) {
+      const int t = key - s.L;
+      if (!((mrow[t >> 6] >> (t & 63)) & 1ull)) continue;
+    }
+    const int lp = virtual_page(p, s, bk, v);
+    const int e = lp < 0 ? -1 : p.block_table[static_cast<long long>(b) * p.max_blocks + lp];
+    if (e < 0 || e >= p.num_blocks) continue;
+    const long long o = ((static_cast<long long>(e) * p.Hkv + kvh) * p.block_size + key % p.block_size) * HD + 4 * lane;
+    const float4 k = four(kc + o), x = four(vc + o);
+    float dot = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    dot *= p.scale_log2;
+    const float m2 = fmaxf(M, dot);
+    if (m2 == -INFINITY) continue;
+    const float c = exp2f(M - m2), w = exp2f(dot - m2);
+    l = l * c + w;
+    acc.x = acc.x * c + w * x.x;
+    acc.y = acc.y * c + w * x.y;
+    acc.z = acc.z * c + w * x.z;
+    acc.w = acc.w * c + w * x.w;
+    M = m2;
+  }
+  const float inv = l > 0.f ? 1.f / l : l;
+  *reinterpret_cast<uint2*>(p.out + qo) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[(static_cast<long long>(b) * p.m + node) * p.Hq + head] = (M + log2f(l)) * kLn2;
+}
 
 // Wait bounded by time only (used on the abort path, to let in-flight copies and MMAs land
 // before shared memory and TMEM are released).
@@ -166,9 +264,10 @@ __device__ __forceinline__ uint64_t visible64(int kb, int L, int m, uint64_t mw0
   return pre > 0 ? (((1ull << pre) - 1ull) | (tb << pre)) : tb;
 }
 
+template <bool SP>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                        const Params p) {
+                        const Params p, const __nv_bfloat16* kc, const __nv_bfloat16* vc) {
   using C = Cfg;
   constexpr int SK = C::SK;
   constexpr int SV = C::SV;
@@ -184,7 +283,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   // Launch order by decreasing prefix length (ties -> lower index): the CTAs of the longest
   // sequences are dispatched first and the short ones fill in behind them.
   int b = slot;
-  if (p.B > 1 && p.B <= kMaxSortedSeqs) {
+  if (!SP && p.B > 1 && p.B <= kMaxSortedSeqs) {
     int* s_len = reinterpret_cast<int*>(sptr + C::OFF_BLK);  // (the block-id area, not used yet)
     int* s_pick = s_len + kMaxSortedSeqs;
     if (threadIdx.x < p.B) s_len[threadIdx.x] = p.prefix_len[threadIdx.x];
@@ -203,22 +302,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     __syncthreads();
   }
   const int bk = b * p.Hkv + kvh;
-  const int L = p.prefix_len[b];
-  // (the whole cluster shares b, so every CTA of a cluster returns here together)
-  if (L < 0 || L > p.max_prefix) {
+  const Span span = span_of<SP>(p, b, bk);
+  // (the whole cluster shares b and the KV head, so every CTA of a cluster returns here together)
+  if (!span.ok) {
     if (threadIdx.x == 0 && rg == 0 && chunk == 0) report(p.status, TS_ERR_DEVICE_CHECK);
     return;
   }
-  const int nkeys = L + p.m;
-  const int T = (nkeys + BN - 1) / BN;
+  const int L = span.L, nkeys = span.nkeys, T = span.T, tpc = span.tpc;
   // chunk c covers tiles [c*tpc, (c+1)*tpc) of this sequence (tpc from the longest allowed
   // prefix), so a shorter sequence uses fewer chunks and its CTAs past the end leave at once;
   // the last chunk, which holds the masked tree tile, is never the longest
-  const int t0 = chunk * p.tpc;
-  const int nt = max(0, min(T, t0 + p.tpc) - t0);
+  const int t0 = chunk * tpc;
+  const int nt = max(0, min(T, t0 + tpc) - t0);
   if (nt == 0 && p.mode != kCluster) return;  // (an idle CTA of a cluster still merges)
   // a sequence whose tiles all fall into one chunk is written directly also in the global mode
-  const bool direct = p.mode == kDirect || (p.mode == kGlobal && T <= p.tpc);
+  const bool direct = p.mode == kDirect || (p.mode == kGlobal && T <= tpc);
   const int R0 = rg * BM;
   const int rows_here = min(p.rows - R0, BM);
   const int nact = (rows_here + 31) / 32;  // softmax warps that hold rows of this group
@@ -275,6 +373,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  // sparse mode written directly: rows to compute again (the cluster merge's area, not used then)
+  volatile int* nan_row = reinterpret_cast<volatile int*>(sptr + C::OFF_ML);
+  if (SP && threadIdx.x < BM) nan_row[threadIdx.x] = 0;
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
     tmem_relinquish();
@@ -294,8 +395,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int e = e0 + 32 * u;
         const int key = t0 * BN + e * rpb;
         ids[u] = -1;
-        if (e < nbox && key < nkeys)
-          ids[u] = __ldg(p.block_table + static_cast<long long>(b) * p.max_blocks + key / p.block_size);
+        if (e < nbox && key < nkeys) {
+          const int lp = SP ? virtual_page(p, span, bk, key / p.block_size) : key / p.block_size;
+          if (!SP || lp >= 0) ids[u] = __ldg(p.block_table + static_cast<long long>(b) * p.max_blocks + lp);
+        }
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -572,8 +675,31 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         *other = xch[(par * 2 + (hh ^ 1)) * BM + r];
         return true;
       };
+      // sparse mode: bit u = whether this row's node keeps the page of keys 16u .. 16u+15 of this
+      // thread's half of the tile (1 from the incomplete page on), fetched a tile ahead
+      const int bs_log2 = 31 - __clz(p.block_size);  // (a power of two on this path)
+      const uint64_t* nm = SP ? p.node_mask + static_cast<long long>(bk) * p.C * p.W + (node >> 6) : nullptr;
+      auto kept16 = [&](int t) -> uint32_t {
+        const int v0 = ((t0 + t) * BN + 64 * hh) >> bs_log2;
+        uint64_t w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {  // pages of 16 tokens differ for every u, larger ones repeat
+          const int v = v0 + ((16 * u) >> bs_log2);
+          w[u] = v < span.nu ? __ldg(reinterpret_cast<const unsigned long long*>(nm + static_cast<long long>(v) * p.W)) : ~0ull;
+        }
+        uint32_t bits = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) bits |= static_cast<uint32_t>((w[u] >> (node & 63)) & 1ull) << u;
+        return bits;
+      };
+      uint32_t kept = 0, kept_next = 0;
+      if constexpr (SP) kept_next = kept16(0);
       for (int t = 0; t < nt; ++t) {
         const int sb = t & 1;
+        if constexpr (SP) {
+          kept = kept_next;
+          if (t + 1 < nt) kept_next = kept16(t + 1);
+        }
         const uint32_t tS = tmem + lane_off + C::COL_S + 128u * sb + 64u * hh;
         const uint32_t tP = tmem + lane_off + C::COL_P + 64u * sb + 32u * hh;
         ok = mbar_wait_warp(s_full(sb), (t >> 1) & 1, abort_flag, p.status);
@@ -586,6 +712,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           tmem_ld64(tS, u);
 #pragma unroll
           for (int c = 0; c < 64; ++c) s[c] = __uint_as_float(u[c]);
+        }
+        if constexpr (SP) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const bool k = (kept >> u) & 1u;
+#pragma unroll
+            for (int c = 16 * u; c < 16 * u + 16; ++c) s[c] = k ? s[c] : -INFINITY;
+          }
         }
         if (key0 + BN > L) {
           // one visibility bit per column (prefix columns, then this row's ancestors)
@@ -684,12 +818,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int head = kvh * p.g + (valid ? grow % p.g : 0);
         if (direct) {
           const float inv = (valid && l_sum > 0.f) ? 1.f / l_sum : 0.f;
+          bool nan = false;
           __nv_bfloat16* dst = p.out + ((static_cast<long long>(b) * p.m + node) * p.Hq + head) * HD + 64 * hh;
 #pragma unroll 1
           for (int cc = 0; cc < 2; ++cc) {
             uint32_t o[32];
             tmem_ld32(tO + 32u * cc, o);
             if (valid) {
+#pragma unroll
+              for (int j = 0; SP && j < 32; ++j) nan |= isnan(__uint_as_float(o[j]));
 #pragma unroll
               for (int v4 = 0; v4 < 4; ++v4) {
                 uint4 w;
@@ -703,6 +840,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
           if (valid && hh == 0 && p.lse != nullptr)
             p.lse[(static_cast<long long>(b) * p.m + node) * p.Hq + head] = (m_ref + log2f(l_sum)) * kLn2;
+          if (SP && nan) nan_row[r] = 1;
         } else if (p.mode == kGlobal) {
           const long long prow = (static_cast<long long>(bk) * p.rows + grow) * p.nchunk + chunk;
           float* dst = p.part_o + prow * HD + 64 * hh;
@@ -810,31 +948,37 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
+  if constexpr (SP) {
+    for (int r = warp; direct && r < rows_here; r += C::THREADS / 32)
+      if (nan_row[r]) repair_row(p, kc, vc, b, kvh, (R0 + r) / p.g, kvh * p.g + (R0 + r) % p.g);
+  }
 }
 
 // Split-K merge for the global mode: one warp per (sequence, KV head, row); rows of
 // sequences that fit in one chunk were written directly by the attention kernel.
+template <bool SP>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ part_o,
                                                       const float2* __restrict__ part_ml,
-                                                      const int32_t* __restrict__ prefix_len,
-                                                      Params p, int total_rows) {
+                                                      Params p, int total_rows, const __nv_bfloat16* kc,
+                                                      const __nv_bfloat16* vc) {
   pdl_wait();
   const int wid = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (wid >= total_rows) return;
   const int bk = wid / p.rows, grow = wid % p.rows;
   const int b = bk / p.Hkv, kvh = bk % p.Hkv;
-  const int L = prefix_len[b];
-  if (L < 0 || L > p.max_prefix) return;
-  const int T = (L + p.m + BN - 1) / BN;
+  const Span span = span_of<SP>(p, b, bk);
+  if (!span.ok) return;
+  const int T = span.T, tpc = span.tpc;
   const int nc = p.nchunk;
-  if (T <= p.tpc) return;  // one chunk: written directly by the attention kernel
+  if (T <= tpc) return;  // one chunk: written directly by the attention kernel
   const long long prow = static_cast<long long>(wid) * nc;
   // chunk c holds tiles [c*tpc, (c+1)*tpc); chunks past the end wrote nothing.  The used
   // chunks are merged four at a time, all their loads issued before any is used, into a
   // running (max, sum, O) in the log2 domain.
-  const int used = min(nc, (T + p.tpc - 1) / p.tpc);
+  const int used = min(nc, (T + tpc - 1) / tpc);
   float M = -INFINITY, Ls = 0.f;
+  bool nan_sum = false;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c0 = 0; c0 < used; c0 += 4) {
     float2 ml[4];
@@ -847,6 +991,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
+      if (SP) nan_sum |= isnan(ml[u].y);
       if (!(ml[u].y > 0.f)) continue;
       if (ml[u].x > M) {
         const float r = exp2f(M - ml[u].x);  // 0 while M is -inf
@@ -871,6 +1016,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   uint2 w;
   w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  if constexpr (SP) {
+    if (__any_sync(0xffffffffu, nan_sum || isnan(acc.x) || isnan(acc.y) || isnan(acc.z) || isnan(acc.w))) {
+      repair_row(p, kc, vc, b, kvh, node, head);
+      return;
+    }
+  }
   *reinterpret_cast<uint2*>(p.out + oo) = w;
   if (lane == 0 && p.lse != nullptr)
     p.lse[(static_cast<long long>(b) * p.m + node) * p.Hq + head] = (M + log2f(Ls)) * kLn2;
@@ -880,7 +1031,9 @@ static cudaError_t set_smem_attr() {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [] {
-    err = cudaFuncSetAttribute(tree_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    err = cudaFuncSetAttribute(tree_attn_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    if (err == cudaSuccess)
+      err = cudaFuncSetAttribute(tree_attn_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
   });
   return err;
 }
@@ -907,7 +1060,7 @@ static int active_clusters(int cx, int cy) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, tree_attn_tc_kernel, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, tree_attn_tc_kernel<false>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -1142,8 +1295,9 @@ static int cuda_fail(cudaError_t e, const char* where) {
   return TS_ERR_CUDA;
 }
 
+template <bool SP>
 static int launch_kernel(const CUtensorMap& mk, const CUtensorMap& mv, const Params& prm, const Plan& pl, int B,
-                         int Hkv, cudaStream_t stream) {
+                         int Hkv, const void* kc, const void* vc, cudaStream_t stream) {
   const cudaError_t ea = set_smem_attr();
   if (ea != cudaSuccess) return cuda_fail(ea, "shared-memory attribute");
   cudaLaunchConfig_t cfg = {};
@@ -1163,8 +1317,78 @@ static int launch_kernel(const CUtensorMap& mk, const CUtensorMap& mv, const Par
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
-  const cudaError_t el = cudaLaunchKernelEx(&cfg, tree_attn_tc_kernel, mk, mv, prm);
-  return el == cudaSuccess ? TS_OK : cuda_fail(el, "launch");
+  const cudaError_t el = cudaLaunchKernelEx(&cfg, tree_attn_tc_kernel<SP>, mk, mv, prm,
+                                            static_cast<const __nv_bfloat16*>(kc), static_cast<const __nv_bfloat16*>(vc));
+  if (el != cudaSuccess) return cuda_fail(el, "launch");
+  int launches = 1;
+  if (pl.mode == kGlobal) {
+    const int total_rows = B * Hkv * prm.rows;
+    const cudaError_t ec = launch_pdl(combine_kernel<SP>, dim3((total_rows + 7) / 8), dim3(256), 0, stream, prm.part_o,
+                                      prm.part_ml, prm, total_rows, static_cast<const __nv_bfloat16*>(kc),
+                                      static_cast<const __nv_bfloat16*>(vc));
+    if (ec != cudaSuccess) return cuda_fail(ec, "combine launch");
+    ++launches;
+  }
+  count_launches(launches);
+  const cudaError_t eg = cudaGetLastError();
+  return eg == cudaSuccess ? TS_OK : cuda_fail(eg, "after launch");
+}
+
+// Plan of the sparse mode.  How many pages the union of the nodes' choices holds is known on the
+// device only, so the split is one wave of CTAs and each unit shares its own tiles out evenly
+// (Span::tpc); a chunk takes at least kSparseMinTiles of them.
+constexpr int kSparseMinTiles = 4;
+
+static Plan sparse_plan(int B, int m, int Hq, int Hkv, int C, int block_size, int num_sms) {
+  Plan pl;
+  if (num_sms < 1) num_sms = 1;
+  const int rows = m * (Hq / Hkv);
+  pl.rowgroups = (rows + BM - 1) / BM;
+  pl.mc = multicast_width(pl.rowgroups);
+  pl.tpc = kSparseMinTiles;
+  const long long T = (static_cast<long long>(C) * block_size + block_size - 1 + m + BN - 1) / BN;
+  const long long units = static_cast<long long>(B) * Hkv * pl.rowgroups;
+  const long long slots = pl.mc > 1 ? static_cast<long long>(active_clusters(pl.mc, 1)) * pl.mc : num_sms;
+  // the staged block ids (smallest pages) bound a chunk's tiles
+  const long long least = (T * (BN / 16) + kMaxChunkBoxes - 1) / kMaxChunkBoxes;
+  const long long most = (T + kSparseMinTiles - 1) / kSparseMinTiles;
+  long long nc = slots / units;
+  if (nc > most) nc = most;
+  if (nc < least) nc = least;
+  if (nc < 1) nc = 1;
+  // Optional override for tests and tuning: TREESPEC_ATTN_SPLIT=direct | global:N, where feasible
+  if (const char* ov = std::getenv("TREESPEC_ATTN_SPLIT")) {
+    int n = 0;
+    if (std::strcmp(ov, "direct") == 0 && least <= 1) nc = 1;
+    else if (std::sscanf(ov, "global:%d", &n) == 1 && n >= least && n <= T) nc = n, pl.tpc = 1;
+  }
+  pl.nc = static_cast<int>(nc);
+  pl.mode = nc > 1 ? kGlobal : kDirect;
+  return pl;
+}
+
+// Partial sums of the global mode: fp32 O rows, then (max, sum).
+static size_t partial_rows(int B, int Hkv, int rows, int nc) { return static_cast<size_t>(B) * Hkv * rows * nc; }
+
+static void fill_params(Params* prm, const Plan& pl, void* workspace, float scale) {
+  prm->g = prm->Hq / prm->Hkv;
+  prm->rows = prm->m * prm->g;
+  prm->W = (prm->m + 63) / 64;
+  prm->tpc = pl.tpc;
+  prm->nchunk = pl.nc;
+  prm->mode = pl.mode;
+  prm->mc = pl.mc;
+  // two MMA-issuing threads pay off where the tensor cores set the pace (several row groups);
+  // with one row group the single issuer is 2% faster
+  prm->split_issue = pl.rowgroups >= 2 ? 1 : 0;
+  if (const char* ov = std::getenv("TREESPEC_ATTN_ISSUE")) {
+    if (std::strcmp(ov, "1") == 0) prm->split_issue = 0;
+    else if (std::strcmp(ov, "2") == 0) prm->split_issue = 1;
+  }
+  prm->scale_log2 = scale * 1.4426950408889634f;
+  const size_t prow = partial_rows(prm->B, prm->Hkv, prm->rows, pl.nc);
+  prm->part_o = pl.mode == kGlobal ? static_cast<float*>(workspace) : nullptr;
+  prm->part_ml = pl.mode == kGlobal ? reinterpret_cast<float2*>(static_cast<char*>(workspace) + prow * HD * 4) : nullptr;
 }
 
 }  // namespace tc
@@ -1208,43 +1432,52 @@ int attention_tc_launch(const AttnArgs& a, int num_sms) {
   prm.m = a.m;
   prm.Hq = a.Hq;
   prm.Hkv = a.Hkv;
-  prm.g = a.Hq / a.Hkv;
-  prm.rows = a.m * prm.g;
-  prm.W = (a.m + 63) / 64;
   prm.max_blocks = a.max_blocks;
   prm.num_blocks = a.num_blocks;
   prm.block_size = a.block_size;
   prm.max_prefix = a.max_prefix;
-  prm.tpc = pl.tpc;
-  prm.nchunk = pl.nc;
-  prm.mode = pl.mode;
-  prm.mc = pl.mc;
-  // two MMA-issuing threads pay off where the tensor cores set the pace (several row groups);
-  // with one row group the single issuer is 2% faster
-  prm.split_issue = pl.rowgroups >= 2 ? 1 : 0;
-  if (const char* ov = std::getenv("TREESPEC_ATTN_ISSUE")) {
-    if (std::strcmp(ov, "1") == 0) prm.split_issue = 0;
-    else if (std::strcmp(ov, "2") == 0) prm.split_issue = 1;
-  }
-  prm.scale_log2 = a.scale * 1.4426950408889634f;
-  const size_t prow = static_cast<size_t>(a.B) * a.Hkv * prm.rows * pl.nc;
-  prm.part_o = pl.mode == tc::kGlobal ? static_cast<float*>(a.workspace) : nullptr;
-  prm.part_ml = pl.mode == tc::kGlobal
-                    ? reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + prow * tc::HD * 4)
-                    : nullptr;
-  const int rc = tc::launch_kernel(mk, mv, prm, pl, a.B, a.Hkv, a.stream);
-  if (rc != TS_OK) return rc;
-  int launches = 1;
-  if (pl.mode == tc::kGlobal) {
-    const int total_rows = a.B * a.Hkv * prm.rows;
-    const cudaError_t ec = launch_pdl(tc::combine_kernel, dim3((total_rows + 7) / 8), dim3(256), 0, a.stream,
-                                      prm.part_o, prm.part_ml, a.prefix_len, prm, total_rows);
-    if (ec != cudaSuccess) return tc::cuda_fail(ec, "combine launch");
-    ++launches;
-  }
-  count_launches(launches);
-  const cudaError_t eg = cudaGetLastError();
-  return eg == cudaSuccess ? TS_OK : tc::cuda_fail(eg, "after launch");
+  tc::fill_params(&prm, pl, a.workspace, a.scale);
+  prm.pages = nullptr;
+  prm.count = nullptr;
+  prm.node_mask = nullptr;
+  prm.C = 0;
+  return tc::launch_kernel<false>(mk, mv, prm, pl, a.B, a.Hkv, a.k_cache, a.v_cache, a.stream);
+}
+
+size_t attention_sparse_tc_workspace_bytes(int B, int m, int Hq, int Hkv, int C, int block_size, int num_sms) {
+  const tc::Plan pl = tc::sparse_plan(B, m, Hq, Hkv, C, block_size, num_sms);
+  if (pl.mode != tc::kGlobal) return 256;
+  return tc::partial_rows(B, Hkv, m * (Hq / Hkv), pl.nc) * (tc::HD * 4 + 8) + 512;
+}
+
+int attention_sparse_tc_launch(const SparseCall& a, cudaStream_t stream, int num_sms) {
+  const tc::Plan pl = tc::sparse_plan(a.B, a.m, a.Hq, a.Hkv, a.C, a.block_size, num_sms);
+  CUtensorMap mk, mv;
+  if (!tc::cached_kv_map(&mk, a.k_cache, a.num_blocks, a.Hkv, a.block_size, tc::kHalfBox) ||
+      !tc::cached_kv_map(&mv, a.v_cache, a.num_blocks, a.Hkv, a.block_size, tc::kPageBox))
+    return tc::cuda_fail(cudaErrorInvalidValue, "tensor map encode");
+  tc::Params prm;
+  prm.q = static_cast<const __nv_bfloat16*>(a.q);
+  prm.block_table = a.block_table;
+  prm.prefix_len = a.prefix_len;
+  prm.mask = a.mask;
+  prm.out = static_cast<__nv_bfloat16*>(a.out);
+  prm.lse = a.lse;
+  prm.status = a.dev_status;
+  prm.B = a.B;
+  prm.m = a.m;
+  prm.Hq = a.Hq;
+  prm.Hkv = a.Hkv;
+  prm.max_blocks = a.max_blocks;
+  prm.num_blocks = a.num_blocks;
+  prm.block_size = a.block_size;
+  prm.max_prefix = 0;
+  tc::fill_params(&prm, pl, a.workspace, a.scale);
+  prm.pages = a.pages;
+  prm.count = a.count;
+  prm.node_mask = a.node_mask;
+  prm.C = a.C;
+  return tc::launch_kernel<true>(mk, mv, prm, pl, a.B, a.Hkv, a.k_cache, a.v_cache, stream);
 }
 
 }  // namespace ts
