@@ -510,8 +510,8 @@ int ts_page_select(const void* q, ts_dtype dt, const void* bounds, int num_block
  * complete page chosen for every node it computes what ts_tree_attention computes.
  *
  * pages [B, Hkv, C], count [B, Hkv], node_mask [B, Hkv, C, W] as ts_page_select writes them (any
- * capacity C >= 1; each page at most once).  Other arguments as ts_tree_attention; the same types,
- * head dims and page sizes are supported, and the same two paths serve them.
+ * capacity C >= 1; each page at most once).  Other arguments as ts_tree_attention, scale > 0; the same
+ * types, head dims and page sizes are supported, and the same two paths serve them.
  * Non-finite values in places that a node does not attend to do not reach its output.
  * workspace: ts_tree_attention_sparse_workspace(...) bytes.
  * Device errors: count outside [0, C], a chosen page outside [0, F), prefix_len negative or

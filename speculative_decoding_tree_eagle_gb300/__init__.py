@@ -553,62 +553,60 @@ def tree_build_from_topk(row_tok: torch.Tensor, row_logp: torch.Tensor, root_tok
     return out
 
 
-def _same_device(**tensors) -> torch.device:
-    """The one CUDA device that all the given tensors (None skipped) are on."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-        dev = t.device
-    return dev
+# The six calls below check each tensor once (device, type, shape, layout) and run on the tensors' own device.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(i).cuda_stream without building a Stream object
+_I32, _I64, _BF16, _F32 = torch.int32, torch.int64, torch.bfloat16, torch.float32
 
 
-def _shape(name: str, t: torch.Tensor, *want) -> None:
-    if tuple(t.shape) != tuple(want):
-        raise ValueError(f"{name} must have shape {list(want)}, got {list(t.shape)}")
+def _refuse(name: str, t: torch.Tensor, index: int, dtype, shape) -> None:
+    _need_cuda(name, t, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{index}")
 
 
-def _scratch(nbytes: int, device: torch.device, ws: Optional[torch.Tensor]) -> torch.Tensor:
-    """The caller's workspace, or one of this call's own."""
+def _arg(name: str, t: torch.Tensor, index: int, dtype, shape) -> int:
+    """The address of a contiguous tensor of this type and shape on device ``index``."""
+    if t.get_device() != index or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(name, t, index, dtype, shape)
+    return t.data_ptr()
+
+
+def _status_arg(status: Optional[torch.Tensor], index: int) -> Optional[int]:
+    return None if status is None else _arg("status", status, index, _I32, (1,))
+
+
+def _index_of(name: str, t: torch.Tensor, dims: int) -> int:
+    """Device index of the tensor that decides where the call runs."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {list(t.shape)}")
+    return index
+
+
+def _scratch(nbytes: int, like: torch.Tensor, ws: Optional[torch.Tensor]):
+    """(address, bytes) of the caller's workspace, or of one of this call's own, and what keeps it."""
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = like.new_empty(nbytes, dtype=torch.uint8)
+        return ws.data_ptr(), nbytes, ws
     _need_cuda("workspace", ws)
-    if ws.device != device:
-        raise ValueError(f"workspace is on {ws.device}, the other tensors on {device}")
-    if ws.numel() * ws.element_size() < nbytes:
+    if ws.device != like.device:
+        raise ValueError(f"workspace is on {ws.device}, the other tensors on {like.device}")
+    size = ws.numel() * ws.element_size()
+    if size < nbytes:
         raise ValueError("workspace too small")
-    return ws
+    return ws.data_ptr(), size, ws
 
 
-def _outputs(out: Optional[Dict[str, torch.Tensor]], device: torch.device, **want) -> Dict[str, torch.Tensor]:
-    """New output tensors, or the caller's after a check of their shapes and types."""
-    if out is None:
-        return {k: torch.empty(shape, dtype=dt, device=device) for k, (shape, dt) in want.items()}
-    for k, (shape, dt) in want.items():
-        _need_cuda(k, out[k], dt)
-        _shape(k, out[k], *shape)
-        if out[k].device != device:
-            raise ValueError(f"{k} is on {out[k].device}, the other tensors on {device}")
-    return out
-
-
-def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
-    """Whether two contiguous tensors share memory without being the very same buffer."""
-    a0, b0 = a.data_ptr(), b.data_ptr()
-    a1, b1 = a0 + a.numel() * a.element_size(), b0 + b.numel() * b.element_size()
-    return a0 < b1 and b0 < a1 and (a0, a1) != (b0, b1)
-
-
-def _need_cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
-    _need_cuda("k_cache", k_cache)
-    _need_cuda("v_cache", v_cache, k_cache.dtype)
-    if k_cache.dim() != 4:
-        raise ValueError("caches must be [num_blocks, Hkv, block_size, d]")
-    _shape("v_cache", v_cache, *k_cache.shape)
+def _apart(out: torch.Tensor, t: torch.Tensor, may_be_same: bool) -> None:
+    """Refuse an output that shares memory with its input, unless it is the very same buffer and may be."""
+    a0, b0 = out.data_ptr(), t.data_ptr()
+    a1, b1 = a0 + out.numel() * out.element_size(), b0 + t.numel() * t.element_size()
+    if a0 < b1 and b0 < a1 and not (may_be_same and a0 == b0 and a1 == b1):
+        raise ValueError("an output must lie apart from the inputs" + (" or be its input's buffer" if may_be_same else ""))
 
 
 def kv_page_bounds(k_cache: torch.Tensor, block_table: torch.Tensor, prefix_len: torch.Tensor, *,
@@ -618,25 +616,20 @@ def kv_page_bounds(k_cache: torch.Tensor, block_table: torch.Tensor, prefix_len:
     (default: at 0), into bounds [num_blocks,Hkv,2,d] bf16 (largest, smallest), which is returned.
     Other pages' bounds stay; without ``bounds`` a tensor of zeros is made."""
     L = library()
-    dev = _same_device(k_cache=k_cache, block_table=block_table, prefix_len=prefix_len, start_len=start_len, bounds=bounds,
-                       status=status)
-    _need_cuda("k_cache", k_cache)
-    _need_cuda("block_table", block_table, torch.int32)
-    _need_cuda("prefix_len", prefix_len, torch.int32)
-    NB, Hkv, bs, d = k_cache.shape
+    ix = _index_of("k_cache", k_cache, 4)
+    if ix != torch.cuda.current_device():
+        with torch.cuda.device(ix):
+            return kv_page_bounds(k_cache, block_table, prefix_len, start_len=start_len, bounds=bounds, status=status)
+    dt = _dt(k_cache)
+    NB, Hkv, bs, d = shape = k_cache.shape
     B, width = block_table.shape
-    _shape("prefix_len", prefix_len, B)
-    if start_len is not None:
-        _need_cuda("start_len", start_len, torch.int32)
-        _shape("start_len", start_len, B)
-    with torch.cuda.device(dev):
-        if bounds is None:
-            bounds = torch.zeros(NB, Hkv, 2, d, dtype=torch.bfloat16, device=dev)
-        else:
-            _need_cuda("bounds", bounds, torch.bfloat16)
-            _shape("bounds", bounds, NB, Hkv, 2, d)
-        _check(L.ts_kv_page_bounds(_p(k_cache), _dt(k_cache), NB, bs, Hkv, d, _p(block_table), width, _p(prefix_len),
-                                   _p(start_len), B, _p(bounds), _p(status), _stream()))
+    if bounds is None:
+        bounds = k_cache.new_zeros(NB, Hkv, 2, d, dtype=_BF16)
+    _check(L.ts_kv_page_bounds(_arg("k_cache", k_cache, ix, k_cache.dtype, shape), dt, NB, bs, Hkv, d,
+                               _arg("block_table", block_table, ix, _I32, (B, width)), width,
+                               _arg("prefix_len", prefix_len, ix, _I32, (B,)),
+                               None if start_len is None else _arg("start_len", start_len, ix, _I32, (B,)), B,
+                               _arg("bounds", bounds, ix, _BF16, (NB, Hkv, 2, d)), _status_arg(status, ix), _raw_stream(ix)))
     return bounds
 
 
@@ -650,29 +643,31 @@ def page_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor
     [B,Hkv] and node_mask [B,Hkv,C,ceil(m/64)] (bit i: node i keeps the page), C = max(1, max_prefix //
     block_size): the selection that ``tree_attention_sparse`` takes."""
     L = library()
-    dev = _same_device(q=q, bounds=bounds, block_table=block_table, prefix_len=prefix_len, status=status)
-    _need_cuda("q", q)
-    _need_cuda("bounds", bounds, torch.bfloat16)
-    _need_cuda("block_table", block_table, torch.int32)
-    _need_cuda("prefix_len", prefix_len, torch.int32)
-    B, m, Hq, d = q.shape
-    NB, Hkv, two, d2 = bounds.shape
-    if two != 2 or d2 != d:
-        raise ValueError("bounds do not match q")
-    _shape("prefix_len", prefix_len, B)
-    _shape("block_table", block_table, B, block_table.shape[1])
-    C = max(1, int(max_prefix) // int(block_size)) if block_size > 0 else 1
-    with torch.cuda.device(dev):
-        need = L.ts_page_select_workspace(B, m, Hq, Hkv, d, int(max_prefix), int(block_size))
-        if need == 0:
-            raise TreeSpecError("invalid page_select sizes")
-        out = _outputs(out, dev, pages=((B, Hkv, C), torch.int32), count=((B, Hkv), torch.int32),
-                       node_mask=((B, Hkv, C, (m + 63) // 64), torch.int64))
-        ws = _scratch(need, dev, workspace)
-        _check(L.ts_page_select(_p(q), _dt(q), _p(bounds), NB, int(block_size), _p(block_table), block_table.shape[1],
-                                _p(prefix_len), int(max_prefix), B, m, Hq, Hkv, d, int(n_pages), int(first), int(recent),
-                                _p(out["pages"]), _p(out["count"]), _p(out["node_mask"]), _p(ws),
-                                ws.numel() * ws.element_size(), _p(status), _stream()))
+    ix = _index_of("q", q, 4)
+    if ix != torch.cuda.current_device():
+        with torch.cuda.device(ix):
+            return page_select(q, bounds, block_table, prefix_len, n_pages, block_size=block_size, max_prefix=max_prefix,
+                               first=first, recent=recent, out=out, workspace=workspace, status=status)
+    dt = _dt(q)
+    B, m, Hq, d = shape = q.shape
+    NB, Hkv = bounds.shape[:2]
+    width = block_table.shape[1]
+    W = (m + 63) // 64
+    need = L.ts_page_select_workspace(B, m, Hq, Hkv, d, max_prefix, block_size)
+    if need == 0:
+        raise TreeSpecError("invalid page_select sizes")
+    C = max(1, max_prefix // block_size)
+    if out is None:
+        out = dict(pages=prefix_len.new_empty((B, Hkv, C)), count=prefix_len.new_empty((B, Hkv)),
+                   node_mask=prefix_len.new_empty((B, Hkv, C, W), dtype=_I64))
+    ws, ws_bytes, keep = _scratch(need, q, workspace)
+    _check(L.ts_page_select(_arg("q", q, ix, q.dtype, shape), dt, _arg("bounds", bounds, ix, _BF16, (NB, Hkv, 2, d)), NB,
+                            block_size, _arg("block_table", block_table, ix, _I32, (B, width)), width,
+                            _arg("prefix_len", prefix_len, ix, _I32, (B,)), max_prefix, B, m, Hq, Hkv, d, n_pages, first,
+                            recent, _arg("pages", out["pages"], ix, _I32, (B, Hkv, C)),
+                            _arg("count", out["count"], ix, _I32, (B, Hkv)),
+                            _arg("node_mask", out["node_mask"], ix, _I64, (B, Hkv, C, W)), ws, ws_bytes,
+                            _status_arg(status, ix), _raw_stream(ix)))
     return out
 
 
@@ -685,46 +680,34 @@ def tree_attention_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     ``selection`` (pages, count and node_mask of ``page_select``) gives it, to the prefix rows of the page
     that is not complete yet and to its ancestors (mask).  Returns (out, lse) like ``tree_attention``."""
     L = library()
-    pages, count, node_mask = selection["pages"], selection["count"], selection["node_mask"]
-    dev = _same_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, prefix_len=prefix_len, mask=mask,
-                       pages=pages, count=count, node_mask=node_mask, out=out, lse=lse, status=status)
-    _need_cuda("q", q)
-    _need_cache(k_cache, v_cache)
-    if k_cache.dtype != q.dtype:
-        raise ValueError(f"k_cache must be {q.dtype}, got {k_cache.dtype}")
-    for name, t, dt in (("block_table", block_table, torch.int32), ("prefix_len", prefix_len, torch.int32),
-                        ("mask", mask, torch.int64), ("pages", pages, torch.int32), ("count", count, torch.int32),
-                        ("node_mask", node_mask, torch.int64)):
-        _need_cuda(name, t, dt)
-    B, m, Hq, d = q.shape
-    NB, Hkv, bs, d2 = k_cache.shape
+    ix = _index_of("q", q, 4)
+    if ix != torch.cuda.current_device():
+        with torch.cuda.device(ix):
+            return tree_attention_sparse(q, k_cache, v_cache, block_table, prefix_len, mask, selection, scale=scale, out=out,
+                                         lse=lse, with_lse=with_lse, workspace=workspace, status=status)
+    dtype, dt = q.dtype, _dt(q)
+    B, m, Hq, d = shape = q.shape
+    NB, Hkv, bs, d2 = cache = k_cache.shape
     if d2 != d:
         raise ValueError("cache shapes do not match q")
-    W, C = (m + 63) // 64, pages.shape[-1]
-    _shape("block_table", block_table, B, block_table.shape[1])
-    _shape("prefix_len", prefix_len, B)
-    _shape("mask", mask, B, m, W)
-    _shape("pages", pages, B, Hkv, C)
-    _shape("count", count, B, Hkv)
-    _shape("node_mask", node_mask, B, Hkv, C, W)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty_like(q)
-        _need_cuda("out", out, q.dtype)
-        _shape("out", out, *q.shape)
-        if lse is None and with_lse:
-            lse = torch.empty(B, m, Hq, dtype=torch.float32, device=dev)
-        if lse is not None:
-            _need_cuda("lse", lse, torch.float32)
-            _shape("lse", lse, B, m, Hq)
-        need = L.ts_tree_attention_sparse_workspace(_dt(q), B, m, Hq, Hkv, d, C, bs)
-        ws = _scratch(need, dev, workspace) if need > 256 else None
-        _check(L.ts_tree_attention_sparse(_p(q), _p(k_cache), _p(v_cache), _dt(q), NB, bs, _p(block_table),
-                                          block_table.shape[1], _p(prefix_len), _p(mask), _p(pages), _p(count),
-                                          _p(node_mask), C, B, m, Hq, Hkv, d, float(scale), _p(out), _p(lse), _p(ws),
-                                          0 if ws is None else ws.numel() * ws.element_size(), _p(status), _stream()))
+    pages = selection["pages"]
+    W, C, width = (m + 63) // 64, pages.shape[-1], block_table.shape[1]
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and with_lse:
+        lse = q.new_empty((B, m, Hq), dtype=_F32)
+    need = L.ts_tree_attention_sparse_workspace(dt, B, m, Hq, Hkv, d, C, bs)
+    ws, ws_bytes, keep = _scratch(need, q, workspace) if need > 256 else (None, 0, None)
+    _check(L.ts_tree_attention_sparse(_arg("q", q, ix, dtype, shape), _arg("k_cache", k_cache, ix, dtype, cache),
+                                      _arg("v_cache", v_cache, ix, dtype, cache), dt, NB, bs,
+                                      _arg("block_table", block_table, ix, _I32, (B, width)), width,
+                                      _arg("prefix_len", prefix_len, ix, _I32, (B,)),
+                                      _arg("mask", mask, ix, _I64, (B, m, W)), _arg("pages", pages, ix, _I32, (B, Hkv, C)),
+                                      _arg("count", selection["count"], ix, _I32, (B, Hkv)),
+                                      _arg("node_mask", selection["node_mask"], ix, _I64, (B, Hkv, C, W)), C, B, m, Hq, Hkv,
+                                      d, 1.0 / math.sqrt(d) if scale is None else scale, _arg("out", out, ix, dtype, shape),
+                                      None if lse is None else _arg("lse", lse, ix, _F32, (B, m, Hq)), ws, ws_bytes,
+                                      _status_arg(status, ix), _raw_stream(ix)))
     return out, lse
 
 
@@ -738,31 +721,32 @@ def kv_reserve(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
     block_table and refs and granted [B] (fresh pages per sequence, -1 where the pool ran short and the sequence
     stays as it was).  ``out`` may hold the input tensors themselves, for an update in place."""
     L = library()
-    dev = _same_device(k_cache=k_cache, v_cache=v_cache, block_table=block_table, prefix_len=prefix_len, refs=refs,
-                       freed=freed, status=status)
-    _need_cache(k_cache, v_cache)
-    for name, t in (("block_table", block_table), ("prefix_len", prefix_len), ("refs", refs)):
-        _need_cuda(name, t, torch.int32)
-    if freed is not None:
-        _need_cuda("freed", freed, torch.int32)
-    NB, Hkv, bs, d = k_cache.shape
-    B, width = block_table.shape
-    _shape("prefix_len", prefix_len, B)
-    _shape("refs", refs, NB)
-    with torch.cuda.device(dev):
-        need = L.ts_kv_reserve_workspace(NB, bs, B, int(n))
-        if need == 0:
-            raise TreeSpecError("invalid kv_reserve sizes")
-        out = _outputs(out, dev, block_table=((B, width), torch.int32), refs=((NB,), torch.int32),
-                       granted=((B,), torch.int32))
-        if _overlap(out["block_table"], block_table) or _overlap(out["refs"], refs):
-            raise ValueError("an output must be its input's buffer or lie apart from it")
-        ws = _scratch(need, dev, workspace)
-        nfreed = 0 if freed is None else freed.numel()
-        _check(L.ts_kv_reserve(_p(k_cache), _p(v_cache), _dt(k_cache), NB, bs, Hkv, d, _p(block_table), width,
-                               _p(prefix_len), _p(refs), B, int(n), _p(freed) if nfreed else None, nfreed,
-                               _p(out["block_table"]), _p(out["refs"]), _p(out["granted"]), _p(ws),
-                               ws.numel() * ws.element_size(), _p(status), _stream()))
+    ix = _index_of("k_cache", k_cache, 4)
+    if ix != torch.cuda.current_device():
+        with torch.cuda.device(ix):
+            return kv_reserve(k_cache, v_cache, block_table, prefix_len, refs, n, freed=freed, out=out, workspace=workspace,
+                              status=status)
+    dtype, dt = k_cache.dtype, _dt(k_cache)
+    NB, Hkv, bs, d = cache = k_cache.shape
+    B, width = table = block_table.shape
+    need = L.ts_kv_reserve_workspace(NB, bs, B, n)
+    if need == 0:
+        raise TreeSpecError("invalid kv_reserve sizes")
+    args = [_arg("k_cache", k_cache, ix, dtype, cache), _arg("v_cache", v_cache, ix, dtype, cache), dt, NB, bs, Hkv, d,
+            _arg("block_table", block_table, ix, _I32, table), width, _arg("prefix_len", prefix_len, ix, _I32, (B,)),
+            _arg("refs", refs, ix, _I32, (NB,)), B, n]
+    nfreed = 0 if freed is None else freed.numel()
+    freed_at = _arg("freed", freed, ix, _I32, freed.shape) if nfreed else None
+    if out is None:
+        out = dict(block_table=torch.empty_like(block_table), refs=torch.empty_like(refs),
+                   granted=torch.empty_like(prefix_len))
+    else:
+        _apart(out["block_table"], block_table, True)
+        _apart(out["refs"], refs, True)
+    ws, ws_bytes, keep = _scratch(need, refs, workspace)
+    _check(L.ts_kv_reserve(*args, freed_at, nfreed, _arg("block_table", out["block_table"], ix, _I32, table),
+                           _arg("refs", out["refs"], ix, _I32, (NB,)), _arg("granted", out["granted"], ix, _I32, (B,)), ws,
+                           ws_bytes, _status_arg(status, ix), _raw_stream(ix)))
     return out
 
 
@@ -772,22 +756,24 @@ def kv_fork(block_table: torch.Tensor, prefix_len: torch.Tensor, refs: torch.Ten
     Returns the new block_table, prefix_len and refs, which replace the old ones: pages are shared, not
     copied, and those of rows that nobody continues are let go.  ``out["refs"]`` may be ``refs`` itself."""
     L = library()
-    dev = _same_device(block_table=block_table, prefix_len=prefix_len, refs=refs, src=src, status=status)
-    for name, t in (("block_table", block_table), ("prefix_len", prefix_len), ("refs", refs), ("src", src)):
-        _need_cuda(name, t, torch.int32)
-    B, width = block_table.shape
-    _shape("prefix_len", prefix_len, B)
-    if src.dim() != 1 or refs.dim() != 1:
-        raise ValueError("src and refs must have one dimension")
+    ix = _index_of("block_table", block_table, 2)
+    if ix != torch.cuda.current_device():
+        with torch.cuda.device(ix):
+            return kv_fork(block_table, prefix_len, refs, src, block_size, out=out, status=status)
+    B, width = table = block_table.shape
     R, NB = src.shape[0], refs.shape[0]
-    with torch.cuda.device(dev):
-        out = _outputs(out, dev, block_table=((R, width), torch.int32), prefix_len=((R,), torch.int32),
-                       refs=((NB,), torch.int32))
-        for k, t in (("block_table", block_table), ("prefix_len", prefix_len), ("refs", refs)):
-            if _overlap(out[k], t) or (k != "refs" and out[k].data_ptr() == t.data_ptr()):
-                raise ValueError(f"out[{k!r}] must lie apart from {k}")
-        _check(L.ts_kv_fork(_p(block_table), width, _p(prefix_len), _p(refs), NB, int(block_size), B, _p(src), R,
-                            _p(out["block_table"]), _p(out["prefix_len"]), _p(out["refs"]), _p(status), _stream()))
+    args = [_arg("block_table", block_table, ix, _I32, table), width, _arg("prefix_len", prefix_len, ix, _I32, (B,)),
+            _arg("refs", refs, ix, _I32, (NB,)), NB, block_size, B, _arg("src", src, ix, _I32, (R,)), R]
+    if out is None:
+        out = dict(block_table=block_table.new_empty((R, width)), prefix_len=torch.empty_like(src), refs=torch.empty_like(refs))
+    else:
+        _apart(out["block_table"], block_table, False)
+        _apart(out["prefix_len"], prefix_len, False)
+        _apart(out["prefix_len"], src, False)
+        _apart(out["refs"], refs, True)
+    _check(L.ts_kv_fork(*args, _arg("block_table", out["block_table"], ix, _I32, (R, width)),
+                        _arg("prefix_len", out["prefix_len"], ix, _I32, (R,)), _arg("refs", out["refs"], ix, _I32, (NB,)),
+                        _status_arg(status, ix), _raw_stream(ix)))
     return out
 
 
@@ -798,23 +784,26 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
     new block_table and refs, remap [num_blocks] (a page's new id, -1 for a free one) and live [1] (pages in
     use).  ``out`` may hold block_table and refs themselves, for an update in place."""
     L = library()
-    dev = _same_device(k_cache=k_cache, v_cache=v_cache, block_table=block_table, refs=refs, bounds=bounds, status=status)
-    _need_cache(k_cache, v_cache)
-    _need_cuda("block_table", block_table, torch.int32)
-    _need_cuda("refs", refs, torch.int32)
-    NB, Hkv, bs, d = k_cache.shape
-    B, width = block_table.shape
-    _shape("refs", refs, NB)
-    if bounds is not None:
-        _need_cuda("bounds", bounds, torch.bfloat16)
-        _shape("bounds", bounds, NB, Hkv, 2, d)
-    with torch.cuda.device(dev):
-        out = _outputs(out, dev, block_table=((B, width), torch.int32), refs=((NB,), torch.int32),
-                       remap=((NB,), torch.int32), live=((1,), torch.int32))
-        if _overlap(out["block_table"], block_table) or _overlap(out["refs"], refs):
-            raise ValueError("an output must be its input's buffer or lie apart from it")
-        ws = _scratch(L.ts_kv_compact_workspace(NB), dev, workspace)
-        _check(L.ts_kv_compact(_p(k_cache), _p(v_cache), _dt(k_cache), _p(bounds), NB, bs, Hkv, d, _p(block_table), width,
-                               _p(refs), B, _p(out["block_table"]), _p(out["refs"]), _p(out["remap"]), _p(out["live"]),
-                               _p(ws), ws.numel() * ws.element_size(), _p(status), _stream()))
+    ix = _index_of("k_cache", k_cache, 4)
+    if ix != torch.cuda.current_device():
+        with torch.cuda.device(ix):
+            return kv_compact(k_cache, v_cache, block_table, refs, bounds=bounds, out=out, workspace=workspace, status=status)
+    dtype, dt = k_cache.dtype, _dt(k_cache)
+    NB, Hkv, bs, d = cache = k_cache.shape
+    B, width = table = block_table.shape
+    args = [_arg("k_cache", k_cache, ix, dtype, cache), _arg("v_cache", v_cache, ix, dtype, cache), dt,
+            None if bounds is None else _arg("bounds", bounds, ix, _BF16, (NB, Hkv, 2, d)), NB, bs, Hkv, d,
+            _arg("block_table", block_table, ix, _I32, table), width, _arg("refs", refs, ix, _I32, (NB,)), B]
+    if out is None:
+        out = dict(block_table=torch.empty_like(block_table), refs=torch.empty_like(refs), remap=torch.empty_like(refs),
+                   live=refs.new_empty((1,)))
+    else:
+        _apart(out["block_table"], block_table, True)
+        _apart(out["refs"], refs, True)
+        _apart(out["remap"], refs, False)
+        _apart(out["remap"], out["refs"], False)
+    ws, ws_bytes, keep = _scratch(L.ts_kv_compact_workspace(NB), refs, workspace)
+    _check(L.ts_kv_compact(*args, _arg("block_table", out["block_table"], ix, _I32, table),
+                           _arg("refs", out["refs"], ix, _I32, (NB,)), _arg("remap", out["remap"], ix, _I32, (NB,)),
+                           _arg("live", out["live"], ix, _I32, (1,)), ws, ws_bytes, _status_arg(status, ix), _raw_stream(ix)))
     return out

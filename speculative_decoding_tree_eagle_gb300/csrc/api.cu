@@ -446,7 +446,7 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
   if (rc != TS_OK) return rc;
   if (!q || !k_cache || !v_cache || !block_table || !prefix_len || !mask || !pages || !count || !node_mask || !out)
     return TS_ERR_INVALID;
-  if (!std::isfinite(scale)) return TS_ERR_INVALID;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return TS_ERR_INVALID;
   ts::SparseCall a{q, k_cache, v_cache, dt, num_blocks, block_size, block_table, max_blocks, prefix_len, mask, pages, count,
                    node_mask, C, B, m, Hq, Hkv, d, scale, out, lse, workspace, dev_status};
   if (!ts::attention_uses_tc(dt, d, block_size)) return ts::attention_sparse_simt_launch(a, static_cast<cudaStream_t>(stream));
@@ -489,7 +489,7 @@ int ts_kv_fork(const int32_t* block_table, int max_blocks, const int32_t* prefix
   if (num_blocks <= 0 || block_size <= 0 || max_blocks <= 0 || B <= 0 || B_out <= 0) return TS_ERR_INVALID;
   if (B > 65535 || B_out > 65535) return TS_ERR_UNSUPPORTED;
   if (!block_table || !prefix_len || !refs || !src || !block_table_out || !prefix_len_out || !refs_out) return TS_ERR_INVALID;
-  if (block_table_out == block_table || prefix_len_out == prefix_len) return TS_ERR_INVALID;
+  if (block_table_out == block_table || prefix_len_out == prefix_len || prefix_len_out == src) return TS_ERR_INVALID;
   const int sms = ts::device_sm_count();
   if (sms <= 0) return TS_ERR_CUDA;
   return ts::kv_fork_launch(block_table, max_blocks, prefix_len, refs, num_blocks, block_size, B, src, B_out, block_table_out,

@@ -10,12 +10,13 @@
 //   score_kernel   tcgen05: 128 rows (whole nodes, all g heads of each) x 128 pages x 2 d per tile;
 //                  the epilogue takes the maximum over the heads and writes one 32-bit key per
 //                  (node, page) whose unsigned order is the score's.
-//   choose_kernel  a CTA per (sequence, KV head, node): the n-th largest key by bisection over the
-//                  key's bits with the keys in registers, ties by index; sets the node's bit in
-//                  each kept page's word (an OR, the same in every order).
+//   choose_*       a warp (or, for long rows, a CTA) per (sequence, KV head, node): the n-th largest
+//                  key by bisection with the keys in registers, ties by index; sets the node's bit
+//                  in each kept page's word (an OR, the same in every order).
 //   pack_kernel    a CTA per (sequence, KV head): the pages with any bit, ascending.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -24,11 +25,13 @@
 namespace ts {
 namespace {
 
-constexpr int kScoreThreads = 256;
+constexpr int kCopyThreads = 256, kKeyThreads = 512;  // score kernel: warps 0..7 and 8..23
+constexpr int kIssueWarp = (kCopyThreads + kKeyThreads) / 32;
+constexpr int kScoreThreads = 32 * (kIssueWarp + 1);
 constexpr int kRows = 128;
-constexpr int kChooseThreads = 256;
+constexpr int kChooseThreads = 256;      // a CTA per row
+constexpr int kChooseWarpThreads = 64;   // a warp per row: small CTAs fill the SMs whatever the rows' registers
 constexpr int kPackThreads = 1024;
-constexpr uint32_t kForced = 0xFFFFFFFFu;  // above every score's key
 
 // Unsigned order = order of the scores (finite; -0 becomes +0).
 __device__ __forceinline__ uint32_t key_of(float s) {
@@ -41,7 +44,7 @@ struct SelectArgs {
   const __nv_bfloat16* bounds;
   const int32_t* table;
   const int32_t* prefix_len;
-  uint32_t* keys;             // [B, Hkv, m, C]
+  uint32_t* keys;             // [B, Hkv, m, stride]
   unsigned long long* dense;  // [B, Hkv, C, W]
   int32_t* pages;
   int32_t* count;
@@ -50,6 +53,9 @@ struct SelectArgs {
   int num_blocks, bs, max_blocks, max_prefix, B, m, Hq, Hkv, g, d, C, W;
   int n, first, recent;
   int nodes_per_tile;
+  int stride;  // keys per row: C rounded up to whole tiles of 128
+  int lg;      // log2 g where shuffles fold the heads, else -1
+  bool q_vec;
 };
 
 // Complete pages of the sequence, -1 for a length out of range.
@@ -59,219 +65,550 @@ __device__ __forceinline__ int complete_pages(const SelectArgs& a, int b) {
   return L / a.bs;
 }
 
-__device__ __forceinline__ float load_q(const float* p) { return *p; }
-__device__ __forceinline__ float load_q(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes to shared memory without passing registers; bytes = 0 writes zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Shared memory of the score kernel: A and B as 128-byte-swizzled K-major chunks of 64 channels
-// (first the chunks of hi / q+, then those of lo / q-), the epilogue's rows, a little state.
-struct ScoreSmem {
-  uint32_t off_b, off_e, off_id, off_bar, bytes;
-  __host__ __device__ ScoreSmem(int chunks, int NT) {
-    off_b = chunks * kRows * 128;
-    off_e = off_b + chunks * NT * 128;
-    off_id = off_e + 2 * kRows * 33 * 4;
-    off_bar = off_id + 128 * 4;
-    bytes = off_bar + 64 + 1024;
+// Keys of 32 pages out of a warp's accumulator rows, 2^LG heads per node: each step halves the columns that a
+// lane is responsible for, so a node's lanes end with the maxima of 32 / 2^LG columns each.  Pages that do
+// not compete (they are kept anyway) and those past the last get key 0 (rows of keys are padded to whole
+// tiles).
+struct Compete {
+  int head, n;  // pages head .. head + n - 1
+  __device__ __forceinline__ uint32_t operator()(float s, int p) const {
+    return static_cast<unsigned>(p - head) < static_cast<unsigned>(n) ? key_of(s) : 0u;
   }
 };
 
-template <typename T, int NT>
+template <int LG>
+__device__ __forceinline__ void fold_out(float (&s)[32], uint32_t* keys, int stride, int r, int rows, const Compete& key,
+                                         int p) {
+  constexpr int LEFT = 32 >> LG;
+  const int lane = threadIdx.x & 31;
+  int col = 0;
+#pragma unroll
+  for (int x = 0; x < LG; ++x) {
+    const int H = 16 >> x;
+    const bool upper = (lane >> x) & 1;
+#pragma unroll
+    for (int c = 0; c < H; ++c) {
+      const float send = upper ? s[c] : s[c + H], mine = upper ? s[c + H] : s[c];
+      s[c] = fmaxf(mine, __shfl_xor_sync(0xffffffffu, send, 1 << x));
+    }
+    col += upper ? H : 0;
+  }
+  if (r >= rows) return;
+  uint32_t* o = keys + static_cast<long long>(r >> LG) * stride + p + col;
+  p += col;
+  if constexpr (LEFT >= 4) {
+#pragma unroll
+    for (int c = 0; c < LEFT; c += 4)
+      *reinterpret_cast<uint4*>(o + c) =
+          make_uint4(key(s[c], p + c), key(s[c + 1], p + c + 1), key(s[c + 2], p + c + 2), key(s[c + 3], p + c + 3));
+  } else {
+#pragma unroll
+    for (int c = 0; c < LEFT; ++c) o[c] = key(s[c], p + c);
+  }
+}
+
+// A load that stays where it is written (ahead of its use).
+__device__ __forceinline__ int load_now(const int32_t* p) {
+  int v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// One arrival per warp, after what all its lanes did (an arrival per lane would be 32 operations on one
+// word, one after the other).
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// Head groups that are a power of two of at most 32 rows are folded by shuffles.
+__host__ __device__ inline bool fold_by_shuffles(int g) { return g <= 32 && (g & (g - 1)) == 0; }
+
+// Shared memory of the score kernel: A (the chunks of 64 channels of q+, then of q-), the B stages (a tile's
+// pages by the chunks of one half, hi or lo), both 128-byte-swizzled and K-major; rows of scores for
+// head groups that shuffles cannot fold; barriers.
+template <int NCH, int NT>
+struct ScoreCfg {
+  static constexpr int ST = NCH == 4 ? 2 : 4;  // stages
+  static constexpr uint32_t STAGE = NCH * NT * 128;
+  static constexpr uint32_t OFF_B = 2 * NCH * kRows * 128;
+  static constexpr uint32_t OFF_E = OFF_B + ST * STAGE;
+  static constexpr uint32_t E_BYTES = 2 * kRows * 33 * 4;
+  // full[ST] empty[ST] acc_full[2] acc_free[2] a_ready done, abort flag, TMEM address
+  static constexpr uint32_t STATE = (2 * ST + 6) * 8 + 16;
+  __host__ __device__ static constexpr uint32_t off_state(bool fold) { return OFF_E + (fold ? 0 : E_BYTES); }
+  __host__ __device__ static constexpr uint32_t bytes(bool fold) { return off_state(fold) + STATE + 1024; }
+};
+
+// NCH chunks of 64 channels per half, NT pages per tile.  Warp roles: 0..7 copy the pages' bounds
+// (cp.async, straight into the swizzled stages), 8..23 first put the queries on their grids and store
+// A, then turn accumulators into keys, 24 issues the products.  Two accumulators, so a tile's products run while
+// the keys of the tile before are written.
+template <typename T, int NCH, int NT>
 __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectArgs a) {
+  using C = ScoreCfg<NCH, NT>;
+  constexpr int ST = C::ST;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   unsigned char* sptr = smem_raw + (sbase - raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bh = blockIdx.z, b = bh / a.Hkv, h = bh % a.Hkv;
-  const int nch = (a.d + 63) / 64;  // chunks per half
-  const ScoreSmem S(2 * nch, NT);
-  pdl_wait();
-  const int nf = complete_pages(a, b);
-  if (nf <= 0) return;
-  const int n0 = blockIdx.y * a.nodes_per_tile;
-  const int nodes = min(a.nodes_per_tile, a.m - n0);
-  const int rows = nodes * a.g;
-  if (blockIdx.y == 0) {  // the words that choose_kernel ORs into
-    const long long words = static_cast<long long>(nf) * a.W;
-    for (long long i = blockIdx.x * kScoreThreads + tid; i < words; i += gridDim.x * kScoreThreads)
-      a.dense[static_cast<long long>(bh) * a.C * a.W + i] = 0ull;
-  }
-  const int ntiles = (nf + NT - 1) / NT;
-  if (static_cast<int>(blockIdx.x) >= ntiles) return;
-
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sptr + S.off_bar + 8);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sptr + S.off_bar + 16);
-  const uint32_t bar = sbase + S.off_bar;
-  int* s_id = reinterpret_cast<int*>(sptr + S.off_id);
-  float* s_e = reinterpret_cast<float*>(sptr + S.off_e);
+  const bool fold = a.lg >= 0;
+  const uint32_t state = C::off_state(fold);
+  auto bar = [&](int i) -> uint32_t { return sbase + state + 8u * i; };
+  auto full = [&](int s) { return bar(s); };
+  auto empty = [&](int s) { return bar(ST + s); };
+  auto acc_full = [&](int x) { return bar(2 * ST + x); };
+  auto acc_free = [&](int x) { return bar(2 * ST + 2 + x); };
+  const uint32_t a_ready = bar(2 * ST + 4), done = bar(2 * ST + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sptr + state + (2 * ST + 6) * 8);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sptr + state + (2 * ST + 6) * 8 + 8);
   if (tid == 0) {
-    mbar_init(bar, 1);
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(full(s), kCopyThreads);
+      mbar_init(empty(s), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(acc_full(x), 1);
+      mbar_init(acc_free(x), kKeyThreads / 32);
+    }
+    mbar_init(a_ready, kKeyThreads / 32);
+    mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0) {
-    tmem_alloc(smem_u32(tmem_holder), NT);
+  if (warp == kIssueWarp) {
+    tmem_alloc(smem_u32(tmem_holder), 2 * NT);
     tmem_relinquish();
   }
-  if (a.d % 64 != 0) {  // channels past d stay zero on both sides
-    for (uint32_t i = tid * 16; i < S.off_e; i += kScoreThreads * 16)
-      *reinterpret_cast<uint4*>(sptr + i) = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
-  }
-  // A: a warp per row puts the query on its grid
-  for (int r = warp; r < rows; r += kScoreThreads / 32) {
-    const T* qrow = static_cast<const T*>(a.q) +
-                    ((static_cast<long long>(b) * a.m + n0 + r / a.g) * a.Hq + h * a.g + r % a.g) * a.d;
-    float v[8], amax = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = lane + 32 * j;
-      v[j] = c < a.d ? grid_clamp(load_q(qrow + c)) : 0.f;
-      amax = fmaxf(amax, fabsf(v[j]));
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    const int e = grid_exponent(amax);
-    const float up = pow2(-e), grid = pow2(e);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = lane + 32 * j;
-      if (c >= a.d) break;
-      const float x = rintf(v[j] * up) * grid;  // at most eight bits: exact in bf16
-      const int col = c & 63;
-      unsigned char* o = sptr + (c >> 6) * (kRows * 128) + r * 128 + (((col >> 3) ^ (r & 7)) << 4) + (col & 7) * 2;
-      *reinterpret_cast<__nv_bfloat16*>(o) = __float2bfloat16_rn(fmaxf(x, 0.f));
-      *reinterpret_cast<__nv_bfloat16*>(o + nch * kRows * 128) = __float2bfloat16_rn(fminf(x, 0.f));
-    }
-  }
+  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const bool vec = a.d % 8 == 0;
-  bool ok = true;
-  uint32_t phase = 0;
-  for (int t = blockIdx.x; t < ntiles; t += gridDim.x, phase ^= 1u) {
-    const int here = min(NT, nf - t * NT);
-    for (int j = tid; j < here; j += kScoreThreads) {
-      int id = a.table[static_cast<long long>(b) * a.max_blocks + t * NT + j];
-      if (id < 0 || id >= a.num_blocks) {
-        report(a.status, TS_ERR_DEVICE_CHECK);
-        id = -1;
-      }
-      s_id[j] = id;
-    }
-    __syncthreads();
-    if (vec) {
-      const int half = a.d / 8, U = 2 * half;  // 16-byte pieces of a page's [hi | lo]
-      for (int i = tid; i < here * U; i += kScoreThreads) {
-        const int j = i / U, u = i - j * U, hf = u >= half ? 1 : 0, w = u - hf * half;
-        const uint32_t off = S.off_b + (hf * nch + (w >> 3)) * (NT * 128) + j * 128 + (((w & 7) ^ (j & 7)) << 4);
-        const int id = s_id[j];
-        if (id >= 0) {
-          cp_async16(sbase + off, a.bounds + (static_cast<long long>(id) * a.Hkv + h) * 2 * a.d + u * 8);
+
+  const int nf = complete_pages(a, b);
+  const int n0 = blockIdx.y * a.nodes_per_tile;
+  const int nodes = min(a.nodes_per_tile, a.m - n0);
+  const int rows = nodes * a.g;
+  const int ntiles = nf > 0 ? (nf + NT - 1) / NT : 0;
+  const int t0 = blockIdx.x, step = gridDim.x;
+  const int nt = t0 < ntiles ? (ntiles - t0 + step - 1) / step : 0;  // this CTA's tiles: t0, t0 + step, ...
+
+  if (warp < kCopyThreads / 32) {
+    // --------------------------------- bounds -> stages ---------------------------------
+    // 8 NCH lanes take the 16-byte pieces of one page's half (zeros for channels past d and pages without an
+    // id).  A thread's piece and its place in the swizzle are the same for all its pages, as these lie a
+    // multiple of eight rows apart.
+    constexpr int PP = 8 * NCH, STEP = kCopyThreads / PP, N = NT / STEP;
+    const int piece = tid % PP, j0 = tid / PP;
+    const uint32_t dst0 = sbase + C::OFF_B + (piece >> 3) * (NT * 128) + j0 * 128 + (((piece & 7) ^ (j0 & 7)) << 4);
+    const bool in_d = 8 * piece < a.d, vec = a.d % 8 == 0;
+    // (a piece past d copies nothing; its address is that of the first)
+    const __nv_bfloat16* head = a.bounds + static_cast<long long>(h) * 2 * a.d + (in_d ? 8 * piece : 0);
+    const long long page_elems = static_cast<long long>(a.Hkv) * 2 * a.d;
+    const int32_t* table = a.table + static_cast<long long>(b) * a.max_blocks;
+    // Physical pages: lane l of a warp holds that of the warp's page l % PW in step l / PW, loaded a tile ahead.
+    // (The load is unconditional, from a clamped place: a conditional one is waited for where the branches
+    // join, which exposed its 2000 cycles in every tile.)
+    constexpr int PW = 32 / PP;
+    const int my_page = warp * PW + lane % PW + STEP * (lane / PW);
+    auto fetch = [&](int i) -> int { return load_now(table + min((t0 + i * step) * NT + my_page, nf - 1)); };
+    int next = nt > 0 ? fetch(0) : 0;
+    bool ok = true;
+    for (int i = 0; i < nt && ok; ++i) {
+      const bool inside = lane < PW * N && (t0 + i * step) * NT + my_page < nf;
+      if (inside && (next < 0 || next >= a.num_blocks)) report(a.status, TS_ERR_DEVICE_CHECK);
+      const int held = inside && next < a.num_blocks ? next : -1;
+      next = fetch(i + 1);
+      int id[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) id[k] = __shfl_sync(0xffffffffu, held, k * PW + lane / PP);
+      for (int hf = 0; hf < 2; ++hf) {
+        const int j = 2 * i + hf, s = j % ST;
+        ok = mbar_wait_warp(empty(s), ((j / ST) & 1) ^ 1u, abort_flag, a.status);
+        if (!ok) break;
+        const uint32_t dst = dst0 + s * C::STAGE;
+        if (vec) {
+#pragma unroll
+          for (int k = 0; k < N; ++k)
+            cp_async16(dst + k * (STEP * 128), head + max(id[k], 0) * page_elems + hf * a.d, in_d && id[k] >= 0 ? 16 : 0);
         } else {
-          *reinterpret_cast<uint4*>(sptr + off) = make_uint4(0u, 0u, 0u, 0u);
+          for (int k = 0; k < N; ++k) {  // (kept out of the loop above: its code would be fetched in every tile)
+            const int page = __shfl_sync(0xffffffffu, held, k * PW + lane / PP);
+            const __nv_bfloat16* src = head + max(page, 0) * page_elems + hf * a.d;
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<__nv_bfloat16*>(sptr + (dst - sbase) + k * (STEP * 128) + 2 * e) =
+                  page >= 0 && 8 * piece + e < a.d ? src[e] : __float2bfloat16_rn(0.f);
+          }
+        }
+        // The stage's barrier counts this thread when its copies have landed.  (Signalling from here, after a wait
+        // for older copies, would make every product wait for the issue of later ones: 26 us where this takes
+        // XX on the long-context choice below.)
+        if (vec) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full(s)) : "memory");
+        else mbar_arrive(full(s));
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == kIssueWarp) {
+    // ------------------------------------- products -------------------------------------
+    if (lane == 0 && nt > 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(kRows, NT, 0, 0);
+      const uint64_t adesc = sdesc_sw128(sbase, 16, 1024), bdesc = sdesc_sw128(sbase + C::OFF_B, 16, 1024);
+      bool ok = mbar_wait(a_ready, 0, abort_flag, a.status);
+      for (int i = 0; i < nt && ok; ++i) {
+        if (i >= 2) ok = mbar_wait(acc_free(i & 1), ((i >> 1) & 1) ^ 1u, abort_flag, a.status);
+        for (int hf = 0; hf < 2 && ok; ++hf) {
+          const int j = 2 * i + hf, s = j % ST;
+          ok = mbar_wait(full(s), (j / ST) & 1, abort_flag, a.status);
+          if (!ok) break;
+          fence_proxy_async_smem();  // the copies' writes, seen through the barrier, before the tensor cores' reads
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4 * NCH; ++kk) {  // descriptors count in 16 bytes
+            const uint32_t ao = ((hf * NCH + (kk >> 2)) * (kRows * 128) + (kk & 3) * 32) >> 4;
+            const uint32_t bo = (s * C::STAGE + (kk >> 2) * (NT * 128) + (kk & 3) * 32) >> 4;
+            mma_ss(tmem + (i & 1) * NT, adesc + ao, bdesc + bo, idesc, (hf > 0 || kk > 0) ? 1u : 0u);
+          }
+          tc_commit(empty(s));
+          if (hf == 1) tc_commit(acc_full(i & 1));
         }
       }
-      cp_async_wait_all();
-    } else {
-      for (int i = tid; i < here * 2 * a.d; i += kScoreThreads) {
-        const int j = i / (2 * a.d), u = i - j * 2 * a.d, hf = u >= a.d ? 1 : 0, c = u - hf * a.d;
-        const uint32_t off = S.off_b + (hf * nch + (c >> 6)) * (NT * 128) + j * 128 + ((((c & 63) >> 3) ^ (j & 7)) << 4) + (c & 7) * 2;
-        const int id = s_id[j];
-        *reinterpret_cast<__nv_bfloat16*>(sptr + off) =
-            id >= 0 ? a.bounds[(static_cast<long long>(id) * a.Hkv + h) * 2 * a.d + u] : __float2bfloat16_rn(0.f);
+      if (!ok) {  // the products in flight land, or the limit passes, before TMEM is given back
+        tc_commit(done);
+        const uint64_t start = global_timer_ns();
+        while (!mbar_try(done, 0) && global_timer_ns() - start < kWaitLimitNs) {
+        }
       }
     }
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-      tc_fence_after();
-      constexpr uint32_t idesc = idesc_bf16_f32(kRows, NT, 0, 0);
-      for (int kk = 0; kk < 8 * nch; ++kk) {
-        const uint32_t c = kk >> 2, ko = (kk & 3) * 32;
-        mma_ss(tmem, sdesc_sw128(sbase + c * (kRows * 128) + ko, 16, 1024),
-               sdesc_sw128(sbase + S.off_b + c * (NT * 128) + ko, 16, 1024), idesc, kk > 0 ? 1u : 0u);
-      }
-      tc_commit(bar);
+    __syncwarp();
+  } else {
+    // ------------------------------------- queries --------------------------------------
+    const int kt = tid - kCopyThreads, kw = warp - kCopyThreads / 32;  // thread and warp among these
+    if (blockIdx.y == 0) {  // the words that the choosers OR into
+      const long long words = static_cast<long long>(nf) * a.W;
+      for (long long i = blockIdx.x * kKeyThreads + kt; i < words; i += gridDim.x * kKeyThreads)
+        a.dense[static_cast<long long>(bh) * a.C * a.W + i] = 0ull;
     }
-    ok = mbar_wait_warp(bar, phase, abort_flag, a.status);
-    ok = __syncthreads_and(ok);
-    if (!ok) break;
-    tc_fence_after();
-    const int q4 = warp & 3, hf = warp >> 2;
+    if (nt > 0) {
+      // eight channels (a piece) per lane, LPR lanes per row.  All of a thread's pieces are first copied to where
+      // its q- (and, for fp32, q+) will lie, so their latencies overlap, and then replaced one by one.
+      constexpr int LPR = 8 * NCH, RPW = 32 / LPR, RSTEP = kKeyThreads / 32 * RPW;
+      const int c = lane % LPR, r0 = kw * RPW + lane / LPR;
+      const T* q0 = static_cast<const T*>(a.q) + ((static_cast<long long>(b) * a.m + n0) * a.Hq + h * a.g) * a.d + 8 * c;
+      auto q_of = [&](int r) {
+        const int node = fold ? r >> a.lg : r / a.g;
+        return q0 + (static_cast<long long>(node) * (a.Hq - a.g) + r) * a.d;
+      };
+      auto place = [&](int r) -> uint32_t { return (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+      constexpr uint32_t NEG = NCH * kRows * 128;
+      if (a.q_vec) {
+        for (int r = r0; r < rows; r += RSTEP) {
+          const T* q = q_of(r);
+          const int bytes = 8 * c < a.d ? 16 : 0;
+          const void* src = bytes != 0 ? q : a.q;
+          cp_async16(sbase + place(r) + NEG, src, bytes);
+          if (sizeof(T) == 4) cp_async16(sbase + place(r), static_cast<const char*>(src) + bytes, bytes);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      }
 #pragma unroll 1
-    for (int cg = 0; cg < NT / 32; cg += 2) {
-      if (q4 * 32 < rows) {
-        uint32_t u[32];
-        tmem_ld32(tmem + (static_cast<uint32_t>(q4 * 32) << 16) + 32u * (cg + hf), u);
-        float* row = s_e + (hf * kRows + q4 * 32 + lane) * 33;
+      for (int rr = kw * RPW; rr < rows; rr += RSTEP) {  // (the whole warp stays for the shuffles)
+        const int r = rr + lane / LPR;
+        float v[8];
+        if (r >= rows) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) row[c] = __uint_as_float(u[c]);
+          for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        } else if (a.q_vec) {
+          const uint4 w = *reinterpret_cast<const uint4*>(sptr + place(r) + NEG);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          if (sizeof(T) == 2) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(u[e]), v[2 * e + 1] = bf16_hi(u[e]);
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(sptr + place(r));
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(u[e]), v[4 + e] = __uint_as_float(y[e]);
+          }
+        } else {
+          const T* q = q_of(r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = 8 * c + e < a.d ? static_cast<float>(q[e]) : 0.f;
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[e] = grid_clamp(v[e]);
+          amax = fmaxf(amax, fabsf(v[e]));
+        }
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        const int e = grid_exponent(amax);
+        const float up = pow2(-e), grid = pow2(e);
+        uint32_t pos[4], neg[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // at most eight bits each: exact in bf16
+          const float x = rintf(v[2 * i] * up) * grid, y = rintf(v[2 * i + 1] * up) * grid;
+          pos[i] = pack_bf16x2(fmaxf(x, 0.f), fmaxf(y, 0.f));
+          neg[i] = pack_bf16x2(fminf(x, 0.f), fminf(y, 0.f));
+        }
+        if (r < rows) {
+          *reinterpret_cast<uint4*>(sptr + place(r)) = make_uint4(pos[0], pos[1], pos[2], pos[3]);
+          *reinterpret_cast<uint4*>(sptr + place(r) + NEG) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+        }
       }
-      __syncthreads();
-      for (int i = tid; i < 64 * nodes; i += kScoreThreads) {
-        const int c = i & 31, hb = (i >> 5) & 1, node = i >> 6;
-        const int p = t * NT + (cg + hb) * 32 + c;
-        if (p >= nf) continue;
-        const float* v = s_e + (hb * kRows + node * a.g) * 33 + c;
-        float best = v[0];
-        for (int j = 1; j < a.g; ++j) best = fmaxf(best, v[j * 33]);
-        a.keys[(static_cast<long long>(bh) * a.m + n0 + node) * a.C + p] = key_of(best);
-      }
-      __syncthreads();
+      fence_proxy_async_smem();
+      warp_arrive(a_ready);
     }
-    tc_fence_before();
-    __syncthreads();
+    // --------------------------------------- keys ---------------------------------------
+    const int q4 = kw & 3, part = kw >> 2;  // rows 32 q4 .. +31, 32 columns
+    const bool mine = 32 * part < NT && q4 * 32 < rows;
+    const int forced = min(a.first, max(nf, 0));
+    const Compete key{forced, max(0, nf - a.recent - forced)};
+    uint32_t* keys = a.keys + (static_cast<long long>(bh) * a.m + n0) * a.stride;
+    float* s_e = reinterpret_cast<float*>(sptr + C::OFF_E);
+    bool ok = true;
+    for (int i = 0; i < nt; ++i) {
+      // (after a wait that gave up the warps still meet at the barriers below)
+      if (ok) ok = mbar_wait_warp(acc_full(i & 1), (i >> 1) & 1, abort_flag, a.status);
+      if (!ok && fold) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + (i & 1) * NT + (static_cast<uint32_t>(q4 * 32) << 16);
+      const int p0 = (t0 + i * step) * NT;
+      float s[32];
+      if (ok && mine) {
+        uint32_t u[32];
+        tmem_ld32(acc + 32 * part, u);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(u[c]);
+      }
+      tc_fence_before();
+      warp_arrive(acc_free(i & 1));  // the accumulator is in registers
+      if (fold) {
+        if (mine) {
+          const int r = q4 * 32 + lane, p = p0 + 32 * part;
+          switch (a.lg) {
+            case 0: fold_out<0>(s, keys, a.stride, r, rows, key, p); break;
+            case 1: fold_out<1>(s, keys, a.stride, r, rows, key, p); break;
+            case 2: fold_out<2>(s, keys, a.stride, r, rows, key, p); break;
+            case 3: fold_out<3>(s, keys, a.stride, r, rows, key, p); break;
+            case 4: fold_out<4>(s, keys, a.stride, r, rows, key, p); break;
+            default: fold_out<5>(s, keys, a.stride, r, rows, key, p); break;
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int cg = 0; cg < NT / 64; ++cg) {  // two parts at a time go through shared memory
+          if (ok && mine && (part >> 1) == cg) {
+            float* row = s_e + ((part & 1) * kRows + q4 * 32 + lane) * 33;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) row[c] = s[c];
+          }
+          asm volatile("bar.sync 1, %0;" ::"n"(kKeyThreads) : "memory");
+          for (int x = kt; ok && x < 64 * nodes; x += kKeyThreads) {
+            const int c = x & 31, hb = (x >> 5) & 1, node = x >> 6;
+            const float* v = s_e + (hb * kRows + node * a.g) * 33 + c;
+            float best = v[0];
+            for (int y = 1; y < a.g; ++y) best = fmaxf(best, v[y * 33]);
+            const int p = p0 + 32 * (2 * cg + hb) + c;
+            keys[static_cast<long long>(node) * a.stride + p] = key(best, p);
+          }
+          asm volatile("bar.sync 1, %0;" ::"n"(kKeyThreads) : "memory");
+        }
+      }
+    }
   }
-  if (warp == 0) {
-    if (!ok) {  // the products in flight land, or the limit passes, before TMEM is given back
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try(bar, phase) && global_timer_ns() - t0 < kWaitLimitNs) {
-      }
-      __syncwarp();
-    }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssueWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, NT);
+    tmem_dealloc(tmem, 2 * NT);
   }
 }
 
-// KPT keys per thread in registers; rows longer than that are read again in every round (KPT 0).
+// What a chooser needs of its row: forced pages have no key of their own.
+struct Row {
+  const uint32_t* keys;
+  unsigned long long* dense;  // word of this node for page 0, W apart
+  unsigned long long bit;
+  int nf, head, tail, need;   // pages [head, tail) compete for `need` places
+};
+
+__device__ __forceinline__ Row row_of(const SelectArgs& a, long long row) {
+  Row r;
+  const int bh = static_cast<int>(row / a.m), node = static_cast<int>(row % a.m);
+  r.nf = complete_pages(a, bh / a.Hkv);
+  r.keys = a.keys + row * a.stride;
+  r.dense = a.dense + static_cast<long long>(bh) * a.C * a.W + (node >> 6);
+  r.bit = 1ull << (node & 63);
+  r.head = min(a.first, max(r.nf, 0));
+  r.tail = max(r.nf - a.recent, r.head);
+  r.need = a.n - r.head - (r.nf - r.tail);
+  return r;
+}
+
+// The next bound to try between two keys: the middle of their scores for the first rounds (scores spread
+// evenly halve the candidates each time), then the middle of the keys, which ends after 32 more.
+__device__ __forceinline__ float score_of(uint32_t key) {
+  return __uint_as_float((key >> 31) != 0u ? key ^ 0x80000000u : ~key);
+}
+__device__ __forceinline__ uint32_t middle(uint32_t lo, uint32_t hi, int round) {  // lo < hi; in (lo, hi]
+  if (round >= 20) return lo + (hi - lo + 1u) / 2u;
+  const uint32_t mid = key_of(0.5f * score_of(lo) + 0.5f * score_of(hi));
+  return max(lo + 1u, min(hi, mid));
+}
+
+// A warp per node, the row's keys in registers (4 consecutive pages per lane and step, KPT in all):
+// bisection between the smallest and the largest key until exactly `need` keys reach the bound (about
+// a dozen rounds of KPT comparisons, no barrier).  Bound by issue slots.  ONE (m = 1): what the node
+// keeps is the union, so the warp writes the outputs itself.
+template <int KPT, bool ONE>
+__global__ void __launch_bounds__(kChooseWarpThreads) choose_warp_kernel(const SelectArgs a, long long rows) {
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  const long long row = blockIdx.x * static_cast<long long>(kChooseWarpThreads / 32) + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const Row r = row_of(a, row);
+  if (ONE && r.nf < 0 && lane == 0) report(a.status, TS_ERR_DEVICE_CHECK);
+  if (!ONE && r.nf <= 0) return;
+  auto page = [&](int j) { return (j / 4 * 32 + lane) * 4 + (j & 3); };
+  const bool all = r.tail - r.head <= r.need;
+  unsigned long long mine = 0ull;  // bit j: page(j) is kept
+#pragma unroll 1
+  for (int s = 0; s < KPT / 4; ++s) {  // those kept without a comparison
+    const int p0 = page(4 * s);
+    auto below = [&](int x) { return (1u << max(0, min(4, x - p0))) - 1u; };
+    const unsigned four = below(r.nf) & ~(all ? 0u : below(r.tail) & ~below(r.head));
+    mine |= static_cast<unsigned long long>(four) << (4 * s);
+  }
+  if (!all && r.need > 0) {
+    uint32_t k[KPT], lo = 0xFFFFFFFFu, hi = 0u;
+#pragma unroll
+    for (int j = 0; j < KPT; j += 4) {
+      const int p = page(j);
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (p < r.nf) w = __ldg(reinterpret_cast<const uint4*>(r.keys + p));  // (0 for pages that do not compete)
+      k[j] = w.x, k[j + 1] = w.y, k[j + 2] = w.z, k[j + 3] = w.w;
+    }
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      lo = min(lo, k[j] - 1u);  // (a key of 0 becomes the largest)
+      hi = max(hi, k[j]);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo) + 1u;
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    // invariant: at least `need` keys reach lo (cnt of them), fewer than `need` reach hi + 1 (above of them)
+    int cnt = r.tail - r.head, above = 0;
+    for (int round = 0; lo < hi && cnt != r.need; ++round) {
+      const uint32_t mid = middle(lo, hi, round);
+      int c[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < KPT; ++j) c[j & 3] += k[j] >= mid;
+      const int n = __reduce_add_sync(0xffffffffu, (c[0] + c[1]) + (c[2] + c[3]));
+      if (n >= r.need) {
+        lo = mid;
+        cnt = n;
+      } else {
+        hi = mid - 1u;
+        above = n;
+      }
+    }
+    unsigned long long reach = 0ull;
+#pragma unroll
+    for (int j = 0; j < KPT; ++j)
+      if (k[j] >= lo) reach |= 1ull << j;
+    if (cnt != r.need) {  // ties at lo == hi: of the keys equal to it only the first
+      unsigned long long eq = 0ull;
+#pragma unroll
+      for (int j = 0; j < KPT; ++j)
+        if (k[j] == lo) eq |= 1ull << j;
+      reach &= ~eq;
+      int left = r.need - above;
+#pragma unroll 1
+      for (int s = 0; s < KPT / 4 && left > 0; ++s) {
+        const unsigned four = static_cast<unsigned>(eq >> (4 * s)) & 0xFu;
+        int before = __popc(four);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += y;
+        }
+        const int sum = __shfl_sync(0xffffffffu, before, 31);
+        before -= __popc(four);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (((four >> e) & 1u) != 0u && before + __popc(four & ((1u << e) - 1u)) < left) reach |= 1ull << (4 * s + e);
+        left -= sum;
+      }
+    }
+    mine |= reach;
+  }
+  if constexpr (!ONE) {
+    while (mine != 0ull) {
+      const int j = __ffsll(static_cast<long long>(mine)) - 1;
+      mine &= mine - 1ull;
+      atomicOr(r.dense + static_cast<long long>(page(j)) * a.W, r.bit);
+    }
+  } else {
+    int32_t* pages = a.pages + row * a.C;
+    unsigned long long* words = a.node_mask + row * a.C;
+    int at = 0;
+#pragma unroll 1
+    for (int s = 0; s < KPT / 4 && 128 * s < r.nf; ++s) {
+      unsigned four = static_cast<unsigned>(mine >> (4 * s)) & 0xFu;
+      int before = __popc(four);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+      }
+      const int sum = __shfl_sync(0xffffffffu, before, 31);
+      int o = at + before - __popc(four);
+      for (; four != 0u; four &= four - 1u, ++o) {
+        pages[o] = page(4 * s + __ffs(four) - 1);
+        words[o] = 1ull;
+      }
+      at += sum;
+    }
+    for (int p = at + lane; p < a.C; p += 32) {
+      pages[p] = -1;
+      words[p] = 0ull;
+    }
+    if (lane == 0) a.count[row] = at;
+  }
+}
+
+// A CTA per node for longer rows: the same bisection, KPT keys per thread in registers, or read
+// again in every round (KPT 0).
 template <int KPT>
 __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const SelectArgs a) {
   __shared__ int s_part[2][kChooseThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
-  const long long row = blockIdx.x;
-  const int bh = static_cast<int>(row / a.m), node = static_cast<int>(row % a.m);
-  const int nf = complete_pages(a, bh / a.Hkv);
-  if (nf <= 0) return;
-  const uint32_t* keys = a.keys + row * a.C;
-  const int head = min(a.first, nf), tail = nf - a.recent;
-  auto key_at = [&](int p) -> uint32_t { return p < head || p >= tail ? kForced : __ldg(keys + p); };
+  const Row r = row_of(a, blockIdx.x);
+  if (r.nf <= 0) return;
+  auto keep = [&](int p) { atomicOr(r.dense + static_cast<long long>(p) * a.W, r.bit); };
+  const bool all = r.tail - r.head <= r.need;
+  for (int p = tid; p < r.nf; p += kChooseThreads)
+    if (p < r.head || p >= r.tail || all) keep(p);
+  if (all || r.need <= 0) return;
   uint32_t k[KPT > 0 ? KPT : 1];
   if constexpr (KPT > 0) {
 #pragma unroll
     for (int j = 0; j < KPT; ++j) {
-      const int p = tid + kChooseThreads * j;
-      k[j] = p < nf ? key_at(p) : 0u;  // below every key
+      const int p = r.head + tid + kChooseThreads * j;
+      k[j] = p < r.tail ? __ldg(r.keys + p) : 0u;  // below every key
     }
   }
   int round = 0;
-  auto at_least = [&](uint32_t x) -> int {  // pages with key >= x (x > 0), in every thread
-    int c = 0;
-    if constexpr (KPT > 0) {
-#pragma unroll
-      for (int j = 0; j < KPT; ++j) c += k[j] >= x;
-    } else {
-      for (int p = tid; p < nf; p += kChooseThreads) c += key_at(p) >= x;
-    }
+  auto sum_up = [&](int c) -> int {
     c = __reduce_add_sync(0xffffffffu, c);
     if (lane == 0) s_part[round & 1][warp] = c;
     __syncthreads();
@@ -281,42 +618,39 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const SelectArgs
     ++round;
     return sum;
   };
-  unsigned long long* dense = a.dense + static_cast<long long>(bh) * a.C * a.W + (node >> 6);
-  const unsigned long long bit = 1ull << (node & 63);
-  auto keep = [&](int p) { atomicOr(dense + static_cast<long long>(p) * a.W, bit); };
-  // the largest x with at least n keys >= x: the n-th largest key
-  uint32_t x = 1u;
-  int cnt = nf;
-  if (nf > a.n) {
-    x = 0u;
-    for (int i = 31; i >= 0; --i) {
-      const uint32_t y = x | (1u << i);
-      const int c = at_least(y);
-      if (c >= a.n) {
-        x = y;
-        cnt = c;
-        if (c == a.n) break;
-      }
-    }
-  }
-  if (cnt <= a.n) {  // no more keys than wanted reach x
+  auto at_least = [&](uint32_t x) -> int {  // keys >= x (x > 0), in every thread
+    int c = 0;
     if constexpr (KPT > 0) {
 #pragma unroll
-      for (int j = 0; j < KPT; ++j)
-        if (k[j] >= x) keep(tid + kChooseThreads * j);
+      for (int j = 0; j < KPT; ++j) c += k[j] >= x;
     } else {
-      for (int p = tid; p < nf; p += kChooseThreads)
-        if (key_at(p) >= x) keep(p);
+      for (int p = r.head + tid; p < r.tail; p += kChooseThreads) c += __ldg(r.keys + p) >= x;
     }
-    return;
+    return sum_up(c);
+  };
+  uint32_t lo = key_of(-3.4e38f), hi = key_of(3.4e38f);  // (scores are far below)
+  int cnt = r.tail - r.head;
+  for (int step = 0; lo < hi && cnt != r.need; ++step) {
+    const uint32_t mid = middle(lo, hi, step + 20);
+    const int c = at_least(mid);
+    if (c >= r.need) {
+      lo = mid;
+      cnt = c;
+    } else {
+      hi = mid - 1u;
+    }
   }
-  // ties at x: all above it, and the first of those equal to it
-  int left = a.n - at_least(x + 1u);
-  for (int p0 = 0; p0 < nf; p0 += kChooseThreads) {
+  // all above lo, and of those equal to it the first `left` (all of them when cnt == need)
+  int left = cnt == r.need ? cnt : r.need - at_least(lo + 1u);
+  for (int p0 = r.head; p0 < r.tail; p0 += kChooseThreads) {
     const int p = p0 + tid;
-    const uint32_t key = p < nf ? key_at(p) : 0u;
-    if (key > x) keep(p);
-    const unsigned eq = __ballot_sync(0xffffffffu, key == x && p < nf);
+    const uint32_t key = p < r.tail ? __ldg(r.keys + p) : 0u;
+    if (cnt == r.need) {
+      if (key >= lo) keep(p);
+      continue;
+    }
+    if (key > lo) keep(p);
+    const unsigned eq = __ballot_sync(0xffffffffu, key == lo);
     if (lane == 0) s_part[round & 1][warp] = __popc(eq);
     __syncthreads();
     int before = 0, sum = 0;
@@ -376,25 +710,35 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const SelectArgs a) 
   if (tid == 0) a.count[bh] = at;
 }
 
-template <typename T, int NT>
+template <typename T, int NCH, int NT>
 cudaError_t launch_score(const SelectArgs& a, cudaStream_t stream, int num_sms) {
-  const ScoreSmem S(2 * ((a.d + 63) / 64), NT);
+  using C = ScoreCfg<NCH, NT>;
+  static_assert(C::bytes(false) <= 232448, "shared memory budget");
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(score_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    attr = cudaFuncSetAttribute(score_kernel<T, NCH, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes(false));
   });
   if (attr != cudaSuccess) return attr;
   const int groups = (a.m + a.nodes_per_tile - 1) / a.nodes_per_tile;
   const int tiles = (a.C + NT - 1) / NT;
   const long long units = static_cast<long long>(a.B) * a.Hkv * groups;
-  const int gx = static_cast<int>(std::min<long long>(tiles, std::max<long long>(1, (num_sms + units - 1) / units)));
-  return launch_pdl(score_kernel<T, NT>, dim3(gx, groups, a.B * a.Hkv), dim3(kScoreThreads), S.bytes, stream, a);
+  // one wave: a second one would pay the set-up and the queries' rounding again
+  const int gx = static_cast<int>(std::min<long long>(tiles, std::max<long long>(1, num_sms / units)));
+  return launch_pdl(score_kernel<T, NCH, NT>, dim3(gx, groups, a.B * a.Hkv), dim3(kScoreThreads), C::bytes(a.lg >= 0), stream,
+                    a);
 }
 
-size_t keys_bytes(int B, int m, int Hkv, int C) {
-  return (static_cast<size_t>(B) * Hkv * m * C * 4 + 15) / 16 * 16;
+template <typename T>
+cudaError_t launch_score(const SelectArgs& a, cudaStream_t stream, int num_sms) {
+  // 128 pages a tile while the operands leave room for four stages of half a tile, else 64 pages and two stages
+  if (a.d <= 64) return launch_score<T, 1, 128>(a, stream, num_sms);
+  return a.d <= 128 ? launch_score<T, 2, 128>(a, stream, num_sms) : launch_score<T, 4, 64>(a, stream, num_sms);
 }
+
+int key_stride(int C) { return (C + 127) / 128 * 128; }
+
+size_t keys_bytes(int B, int m, int Hkv, int C) { return static_cast<size_t>(B) * Hkv * m * key_stride(C) * 4; }
 
 }  // namespace
 
@@ -428,23 +772,33 @@ int page_select_launch(const SelectCall& c, cudaStream_t stream, int num_sms) {
   a.first = c.first;
   a.recent = c.recent;
   a.nodes_per_tile = kRows / a.g;
+  a.stride = key_stride(a.C);
+  a.lg = fold_by_shuffles(a.g) ? 31 - __builtin_clz(static_cast<unsigned>(a.g)) : -1;
+  a.q_vec = c.d % 8 == 0 && (reinterpret_cast<uintptr_t>(c.q) & 15u) == 0;
   a.keys = static_cast<uint32_t*>(c.workspace);
   a.dense = reinterpret_cast<unsigned long long*>(static_cast<char*>(c.workspace) + keys_bytes(c.B, c.m, c.Hkv, a.C));
-  cudaError_t e;
-  // 128 pages a tile while both operands fit shared memory, 64 for head dims above 128
-  if (c.dt == TS_BF16)
-    e = c.d <= 128 ? launch_score<__nv_bfloat16, 128>(a, stream, num_sms) : launch_score<__nv_bfloat16, 64>(a, stream, num_sms);
-  else
-    e = c.d <= 128 ? launch_score<float, 128>(a, stream, num_sms) : launch_score<float, 64>(a, stream, num_sms);
+  cudaError_t e = c.dt == TS_BF16 ? launch_score<__nv_bfloat16>(a, stream, num_sms) : launch_score<float>(a, stream, num_sms);
   if (e != cudaSuccess) return TS_ERR_CUDA;
   count_launches(1);
-  const dim3 grid(static_cast<unsigned>(static_cast<long long>(c.B) * c.Hkv * c.m));
-  if (a.C <= 8 * kChooseThreads)
-    e = launch_pdl(choose_kernel<8>, grid, dim3(kChooseThreads), 0, stream, a);
-  else if (a.C <= 32 * kChooseThreads)
-    e = launch_pdl(choose_kernel<32>, grid, dim3(kChooseThreads), 0, stream, a);
-  else
-    e = launch_pdl(choose_kernel<0>, grid, dim3(kChooseThreads), 0, stream, a);
+  const long long rows = static_cast<long long>(c.B) * c.Hkv * c.m;
+  const int wpc = kChooseWarpThreads / 32;
+  const dim3 warps(static_cast<unsigned>((rows + wpc - 1) / wpc)), wblock(kChooseWarpThreads);
+  const dim3 ctas(static_cast<unsigned>(rows)), block(kChooseThreads);
+  if (a.C <= 2048) {
+    const bool one = c.m == 1;
+    auto* choose = a.C <= 512 ? (one ? choose_warp_kernel<16, true> : choose_warp_kernel<16, false>)
+                   : a.C <= 1024 ? (one ? choose_warp_kernel<32, true> : choose_warp_kernel<32, false>)
+                                 : (one ? choose_warp_kernel<64, true> : choose_warp_kernel<64, false>);
+    e = launch_pdl(choose, warps, wblock, 0, stream, a, rows);
+    if (one) {
+      count_launches(1);
+      return e == cudaSuccess ? TS_OK : TS_ERR_CUDA;
+    }
+  } else if (a.C <= 32 * kChooseThreads) {
+    e = launch_pdl(choose_kernel<32>, ctas, block, 0, stream, a);
+  } else {
+    e = launch_pdl(choose_kernel<0>, ctas, block, 0, stream, a);
+  }
   if (e != cudaSuccess) return TS_ERR_CUDA;
   count_launches(1);
   e = launch_pdl(pack_kernel, dim3(c.B * c.Hkv), dim3(kPackThreads), 0, stream, a);

@@ -110,6 +110,8 @@ struct Cfg {
   static constexpr uint32_t OFF_ML = OFF_MISC + 16;            // (max, sum) per row, cluster merge
   static constexpr uint32_t OFF_BLK = OFF_ML + BM * 8;
   static constexpr uint32_t SMEM_BYTES = OFF_BLK + 4 * kMaxChunkBoxes + 1024;  // + alignment slack
+  // sparse mode: a chunk's block ids and page bits (see sparse_smem) follow from OFF_BLK
+  static constexpr uint32_t MAX_SMEM = 232448;
   static_assert(COL_P + 64 * 2 <= TMEM_COLS, "TMEM budget");
   static_assert(SK * KTILE >= BM * 512, "O rows must fit in the K ring for the merge");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -134,6 +136,9 @@ struct Params {
   const int32_t* count;       // [B, Hkv]
   const uint64_t* node_mask;  // [B, Hkv, C, W]
   int C;
+  int share;       // chunks a unit is to be cut into where it has the tiles for it
+  int cap_tiles;   // tiles whose ids and bits a CTA can stage
+  int bit_words;   // 32-bit words of page bits per node
 };
 
 // What one (sequence, KV head) reads.  The dense mode reads the sequence as it lies: L prefix keys,
@@ -163,8 +168,9 @@ __device__ __forceinline__ Span span_of(const Params& p, int b, int bk) {
   s.nkeys = s.L + p.m;
   s.T = (s.nkeys + BN - 1) / BN;
   // tiles per chunk: the dense plan's, from the longest allowed prefix; in the sparse mode, where the
-  // number of chosen pages is known here only, an even share of this unit's tiles of at least p.tpc
-  s.tpc = SP ? max(p.tpc, (s.T + p.nchunk - 1) / p.nchunk) : p.tpc;
+  // number of chosen pages is known here only, an even share of this unit's tiles of at least p.tpc and
+  // at most what a CTA can stage (p.nchunk of those hold the longest unit)
+  s.tpc = SP ? min(p.cap_tiles, max(p.tpc, (s.T + p.share - 1) / p.share)) : p.tpc;
   return s;
 }
 
@@ -277,8 +283,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   unsigned char* sptr = smem_raw + (sbase - raw);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rg = blockIdx.x, chunk = blockIdx.y;
-  const int slot = blockIdx.z / p.Hkv, kvh = blockIdx.z % p.Hkv;
+  // (sparse mode: chunks slowest, as the later ones are often empty)
+  const int rg = blockIdx.x, chunk = SP ? blockIdx.z : blockIdx.y;
+  const int unit = SP ? blockIdx.y : blockIdx.z;
+  const int slot = unit / p.Hkv, kvh = unit % p.Hkv;
   pdl_wait();
   // Launch order by decreasing prefix length (ties -> lower index): the CTAs of the longest
   // sequences are dispatched first and the short ones fill in behind them.
@@ -411,6 +419,26 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           else report(p.status, TS_ERR_DEVICE_CHECK);
         }
         s_blk[e] = phys;
+      }
+    }
+  }
+  // Sparse mode: the page-major node words are turned into node-major bits, 32 groups of 16 keys at a
+  // time: lane = group, one ballot per node.  1 from the incomplete page on (the general visibility
+  // test takes over there).
+  uint32_t* s_bits = reinterpret_cast<uint32_t*>(s_blk + (SP ? p.cap_tiles * bpt : 0));
+  if constexpr (SP) {
+    const int bs_log2 = 31 - __clz(p.block_size);  // (a power of two on this path)
+    const int node0 = R0 / p.g, nodes = (R0 + rows_here - 1) / p.g - node0 + 1;
+    const int words = (nt * (BN / 16) + 31) / 32;
+    for (int w = warp; w < words; w += C::THREADS / 32) {
+      const int v = (t0 * BN + (32 * w + lane) * 16) >> bs_log2;
+      const uint64_t* nm = p.node_mask + (static_cast<long long>(bk) * p.C + v) * p.W;
+      uint64_t x = ~0ull;
+      for (int j = 0; j < nodes; ++j) {
+        const int node = node0 + j;
+        if (v < span.nu && (j == 0 || (node & 63) == 0)) x = __ldg(reinterpret_cast<const unsigned long long*>(nm + (node >> 6)));
+        const uint32_t bits = __ballot_sync(0xffffffffu, (x >> (node & 63)) & 1ull);
+        if (lane == (j & 31)) s_bits[j * p.bit_words + w] = bits;
       }
     }
   }
@@ -675,31 +703,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         *other = xch[(par * 2 + (hh ^ 1)) * BM + r];
         return true;
       };
-      // sparse mode: bit u = whether this row's node keeps the page of keys 16u .. 16u+15 of this
-      // thread's half of the tile (1 from the incomplete page on), fetched a tile ahead
-      const int bs_log2 = 31 - __clz(p.block_size);  // (a power of two on this path)
-      const uint64_t* nm = SP ? p.node_mask + static_cast<long long>(bk) * p.C * p.W + (node >> 6) : nullptr;
-      auto kept16 = [&](int t) -> uint32_t {
-        const int v0 = ((t0 + t) * BN + 64 * hh) >> bs_log2;
-        uint64_t w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {  // pages of 16 tokens differ for every u, larger ones repeat
-          const int v = v0 + ((16 * u) >> bs_log2);
-          w[u] = v < span.nu ? __ldg(reinterpret_cast<const unsigned long long*>(nm + static_cast<long long>(v) * p.W)) : ~0ull;
-        }
-        uint32_t bits = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) bits |= static_cast<uint32_t>((w[u] >> (node & 63)) & 1ull) << u;
-        return bits;
-      };
-      uint32_t kept = 0, kept_next = 0;
-      if constexpr (SP) kept_next = kept16(0);
+      // sparse mode: bit u of kept = whether this row's node keeps the page of keys 16u .. 16u+15 of
+      // this thread's half of the tile
+      const uint32_t* my_bits = s_bits + (valid ? node - R0 / p.g : 0) * p.bit_words;
+      uint32_t kept = 0xFu;
       for (int t = 0; t < nt; ++t) {
         const int sb = t & 1;
-        if constexpr (SP) {
-          kept = kept_next;
-          if (t + 1 < nt) kept_next = kept16(t + 1);
-        }
+        if constexpr (SP) kept = (my_bits[t >> 2] >> ((t & 3) * 8 + 4 * hh)) & 0xFu;
         const uint32_t tS = tmem + lane_off + C::COL_S + 128u * sb + 64u * hh;
         const uint32_t tP = tmem + lane_off + C::COL_P + 64u * sb + 32u * hh;
         ok = mbar_wait_warp(s_full(sb), (t >> 1) & 1, abort_flag, p.status);
@@ -713,14 +723,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < 64; ++c) s[c] = __uint_as_float(u[c]);
         }
-        if constexpr (SP) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const bool k = (kept >> u) & 1u;
-#pragma unroll
-            for (int c = 16 * u; c < 16 * u + 16; ++c) s[c] = k ? s[c] : -INFINITY;
-          }
-        }
         if (key0 + BN > L) {
           // one visibility bit per column (prefix columns, then this row's ancestors)
           const uint64_t vis = visible64(key0 + 64 * hh, L, p.m, mw0, mw1, mw2, mw3);
@@ -729,11 +731,26 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
         float mx;
         {  // eight independent running maxima, then a tree; then the partner's half
+          // (sparse mode: two for each 16 keys, which count only if their page is kept)
           float m8[8];
+          if constexpr (SP) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) m8[c] = s[c];
+            for (int u = 0; u < 4; ++u) {
+              float a0 = s[16 * u], a1 = s[16 * u + 1];
 #pragma unroll
-          for (int c = 8; c < 64; ++c) m8[c & 7] = fmaxf(m8[c & 7], s[c]);
+              for (int c = 2; c < 16; c += 2) {
+                a0 = fmaxf(a0, s[16 * u + c]);
+                a1 = fmaxf(a1, s[16 * u + c + 1]);
+              }
+              m8[2 * u] = ((kept >> u) & 1u) ? a0 : -INFINITY;
+              m8[2 * u + 1] = ((kept >> u) & 1u) ? a1 : -INFINITY;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) m8[c] = s[c];
+#pragma unroll
+            for (int c = 8; c < 64; ++c) m8[c & 7] = fmaxf(m8[c & 7], s[c]);
+          }
           mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
           float mo;
           ok = exchange(t, mx, &mo);
@@ -754,12 +771,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
         // padding rows take an infinite reference, so every exponential of theirs is 0
         const float mu = !valid ? INFINITY : (m_ref == -INFINITY) ? 0.f : m_ref;
+        // so do keys of pages that are not kept (a non-finite score there gives NaN, and the row is then
+        // computed again without those keys: repair_row)
+        float mu4[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mu4[u] = !SP || ((kept >> u) & 1u) ? mu : INFINITY;
         {
           float rs4[4] = {0.f, 0.f, 0.f, 0.f};
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const float x0 = fmaf(s[2 * c], sl2, -mu), x1 = fmaf(s[2 * c + 1], sl2, -mu);
+            const float x0 = fmaf(s[2 * c], sl2, -mu4[c >> 3]), x1 = fmaf(s[2 * c + 1], sl2, -mu4[c >> 3]);
             const float p0 = ex2_approx(x0);
             const float p1 = ex2_approx(x1);
             rs4[c & 3] += p0 + p1;
@@ -1033,7 +1055,8 @@ static cudaError_t set_smem_attr() {
   std::call_once(once, [] {
     err = cudaFuncSetAttribute(tree_attn_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
     if (err == cudaSuccess)
-      err = cudaFuncSetAttribute(tree_attn_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+      err = cudaFuncSetAttribute(tree_attn_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Cfg::MAX_SMEM);
   });
   return err;
 }
@@ -1070,6 +1093,8 @@ static int active_clusters(int cx, int cy) {
 
 struct Plan {
   int rowgroups, mc, nc, tpc, mode;
+  int share = 0, cap_tiles = 0, bit_words = 0;  // sparse mode
+  uint32_t smem = 0;
 };
 
 // Row groups that share each K/V tile through TMA multicast: all of them up to four, else the
@@ -1301,9 +1326,9 @@ static int launch_kernel(const CUtensorMap& mk, const CUtensorMap& mv, const Par
   const cudaError_t ea = set_smem_attr();
   if (ea != cudaSuccess) return cuda_fail(ea, "shared-memory attribute");
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pl.rowgroups, pl.nc, B * Hkv);
+  cfg.gridDim = SP ? dim3(pl.rowgroups, B * Hkv, pl.nc) : dim3(pl.rowgroups, pl.nc, B * Hkv);
   cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+  cfg.dynamicSmemBytes = SP ? pl.smem : Cfg::SMEM_BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1349,21 +1374,29 @@ static Plan sparse_plan(int B, int m, int Hq, int Hkv, int C, int block_size, in
   const long long T = (static_cast<long long>(C) * block_size + block_size - 1 + m + BN - 1) / BN;
   const long long units = static_cast<long long>(B) * Hkv * pl.rowgroups;
   const long long slots = pl.mc > 1 ? static_cast<long long>(active_clusters(pl.mc, 1)) * pl.mc : num_sms;
-  // the staged block ids (smallest pages) bound a chunk's tiles
-  const long long least = (T * (BN / 16) + kMaxChunkBoxes - 1) / kMaxChunkBoxes;
+  // A CTA stages, per 128-key tile, the ids of its boxes (4 bytes each) and for every node of its row
+  // group a bit per 16 keys (1 byte): at 8 heads per KV head and 16-token pages some 600 tiles fit.
+  const int nodes = rows < BM ? m : (BM - 1) / (Hq / Hkv) + 2;
+  const int per_tile = 4 * (BN / (block_size < 64 ? block_size : 64)) + nodes;
+  const int room = static_cast<int>(Cfg::MAX_SMEM - 1024 - Cfg::OFF_BLK);
+  pl.cap_tiles = (room - 4 * nodes) / per_tile;
+  if (pl.cap_tiles > T) pl.cap_tiles = static_cast<int>(T);
+  pl.bit_words = (pl.cap_tiles + 3) / 4;
+  pl.smem = Cfg::OFF_BLK + 4 * pl.cap_tiles * (BN / (block_size < 64 ? block_size : 64)) + 4 * nodes * pl.bit_words + 1024;
   const long long most = (T + kSparseMinTiles - 1) / kSparseMinTiles;
-  long long nc = slots / units;
-  if (nc > most) nc = most;
-  if (nc < least) nc = least;
-  if (nc < 1) nc = 1;
-  // Optional override for tests and tuning: TREESPEC_ATTN_SPLIT=direct | global:N, where feasible
+  long long share = slots / units;
+  if (share > most) share = most;
+  if (share < 1) share = 1;
+  // Optional override for tests and tuning: TREESPEC_ATTN_SPLIT=direct | global:N
   if (const char* ov = std::getenv("TREESPEC_ATTN_SPLIT")) {
     int n = 0;
-    if (std::strcmp(ov, "direct") == 0 && least <= 1) nc = 1;
-    else if (std::sscanf(ov, "global:%d", &n) == 1 && n >= least && n <= T) nc = n, pl.tpc = 1;
+    if (std::strcmp(ov, "direct") == 0) share = 1;
+    else if (std::sscanf(ov, "global:%d", &n) == 1 && n >= 1 && n <= T) share = n, pl.tpc = 1;
   }
-  pl.nc = static_cast<int>(nc);
-  pl.mode = nc > 1 ? kGlobal : kDirect;
+  pl.share = static_cast<int>(share);
+  const long long least = (T + pl.cap_tiles - 1) / pl.cap_tiles;
+  pl.nc = static_cast<int>(share > least ? share : least);
+  pl.mode = pl.nc > 1 ? kGlobal : kDirect;
   return pl;
 }
 
@@ -1378,6 +1411,9 @@ static void fill_params(Params* prm, const Plan& pl, void* workspace, float scal
   prm->nchunk = pl.nc;
   prm->mode = pl.mode;
   prm->mc = pl.mc;
+  prm->share = pl.share;
+  prm->cap_tiles = pl.cap_tiles;
+  prm->bit_words = pl.bit_words;
   // two MMA-issuing threads pay off where the tensor cores set the pace (several row groups);
   // with one row group the single issuer is 2% faster
   prm->split_issue = pl.rowgroups >= 2 ? 1 : 0;

@@ -57,7 +57,7 @@ def _sparse(lib, dt=1, nb=4, bs=16, width=8, C=4, B=1, m=4, Hq=4, Hkv=2, d=128, 
 
 def test_tree_attention_sparse_validation(lib):
     for kw in (dict(dt=5), dict(nb=0), dict(bs=0), dict(width=0), dict(C=0), dict(B=0), dict(m=0), dict(Hq=5), dict(d=0),
-               dict(scale=float("inf")), dict(ptr=None), dict(ptr=8)):
+               dict(scale=float("inf")), dict(scale=0.0), dict(scale=-0.1), dict(ptr=None), dict(ptr=8)):
         assert _sparse(lib, **kw) == INVALID, kw
     for kw in (dict(m=257), dict(d=257), dict(B=65536), dict(C=2 ** 27)):
         assert _sparse(lib, **kw) == UNSUPPORTED, kw
@@ -87,7 +87,7 @@ def _fork(lib, nb=4, bs=16, width=8, B=2, R=3, src=(16, 32, 48, 64, 80, 96, 112)
 
 def test_kv_fork_validation(lib):
     for kw in (dict(nb=0), dict(bs=0), dict(width=0), dict(B=0), dict(R=0), dict(src=(16, 32, 48, None, 80, 96, 112)),
-               dict(src=(16, 32, 48, 64, 16, 96, 112)), dict(src=(16, 32, 48, 64, 80, 32, 112))):
+               dict(src=(16, 32, 48, 64, 16, 96, 112)), dict(src=(16, 32, 48, 64, 80, 32, 112)), dict(src=(16, 32, 48, 64, 80, 64, 112))):
         assert _fork(lib, **kw) == INVALID, kw
     assert _fork(lib, B=65536) == UNSUPPORTED and _fork(lib, R=65536) == UNSUPPORTED
 
