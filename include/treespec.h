@@ -577,8 +577,8 @@ int ts_kv_reserve(void* k_cache, void* v_cache, ts_dtype dt, int num_blocks, int
  * the half-filled last page is shared until ts_kv_reserve copies it.
  *
  * block_table [B, max_blocks], prefix_len [B], refs [num_blocks], src [B_out].
- * block_table_out [B_out, max_blocks] and prefix_len_out [B_out] must not be the inputs;
- * refs_out may be refs.  B, B_out <= 65535.  Two launches, no workspace.
+ * block_table_out [B_out, max_blocks] and prefix_len_out [B_out] must not be inputs;
+ * refs_out may be refs.  B, B_out <= 65535.  One or two launches, no workspace.
  * Device errors: src outside [-1, B), a length outside [0, max_blocks * block_size] (the new row is
  * empty), an entry out of range or missing among a kept row's pages (copied as -1), or a count that
  * falls below zero -> TS_ERR_DEVICE_CHECK.

@@ -590,7 +590,7 @@ def _index_of(name: str, t: torch.Tensor, dims: int) -> int:
 def _scratch(nbytes: int, like: torch.Tensor, ws: Optional[torch.Tensor]):
     """(address, bytes) of the caller's workspace, or of one of this call's own, and what keeps it."""
     if ws is None:
-        ws = like.new_empty(nbytes, dtype=torch.uint8)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
         return ws.data_ptr(), nbytes, ws
     _need_cuda("workspace", ws)
     if ws.device != like.device:
@@ -624,7 +624,7 @@ def kv_page_bounds(k_cache: torch.Tensor, block_table: torch.Tensor, prefix_len:
     NB, Hkv, bs, d = shape = k_cache.shape
     B, width = block_table.shape
     if bounds is None:
-        bounds = k_cache.new_zeros(NB, Hkv, 2, d, dtype=_BF16)
+        bounds = torch.zeros((NB, Hkv, 2, d), dtype=_BF16, device=k_cache.device)
     _check(L.ts_kv_page_bounds(_arg("k_cache", k_cache, ix, k_cache.dtype, shape), dt, NB, bs, Hkv, d,
                                _arg("block_table", block_table, ix, _I32, (B, width)), width,
                                _arg("prefix_len", prefix_len, ix, _I32, (B,)),
@@ -658,8 +658,9 @@ def page_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor
         raise TreeSpecError("invalid page_select sizes")
     C = max(1, max_prefix // block_size)
     if out is None:
-        out = dict(pages=prefix_len.new_empty((B, Hkv, C)), count=prefix_len.new_empty((B, Hkv)),
-                   node_mask=prefix_len.new_empty((B, Hkv, C, W), dtype=_I64))
+        dev = q.device
+        out = dict(pages=torch.empty((B, Hkv, C), dtype=_I32, device=dev), count=torch.empty((B, Hkv), dtype=_I32, device=dev),
+                   node_mask=torch.empty((B, Hkv, C, W), dtype=_I64, device=dev))
     ws, ws_bytes, keep = _scratch(need, q, workspace)
     _check(L.ts_page_select(_arg("q", q, ix, q.dtype, shape), dt, _arg("bounds", bounds, ix, _BF16, (NB, Hkv, 2, d)), NB,
                             block_size, _arg("block_table", block_table, ix, _I32, (B, width)), width,
@@ -695,7 +696,7 @@ def tree_attention_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     if out is None:
         out = torch.empty_like(q)
     if lse is None and with_lse:
-        lse = q.new_empty((B, m, Hq), dtype=_F32)
+        lse = torch.empty((B, m, Hq), dtype=_F32, device=q.device)
     need = L.ts_tree_attention_sparse_workspace(dt, B, m, Hq, Hkv, d, C, bs)
     ws, ws_bytes, keep = _scratch(need, q, workspace) if need > 256 else (None, 0, None)
     _check(L.ts_tree_attention_sparse(_arg("q", q, ix, dtype, shape), _arg("k_cache", k_cache, ix, dtype, cache),
@@ -765,7 +766,8 @@ def kv_fork(block_table: torch.Tensor, prefix_len: torch.Tensor, refs: torch.Ten
     args = [_arg("block_table", block_table, ix, _I32, table), width, _arg("prefix_len", prefix_len, ix, _I32, (B,)),
             _arg("refs", refs, ix, _I32, (NB,)), NB, block_size, B, _arg("src", src, ix, _I32, (R,)), R]
     if out is None:
-        out = dict(block_table=block_table.new_empty((R, width)), prefix_len=torch.empty_like(src), refs=torch.empty_like(refs))
+        out = dict(block_table=torch.empty((R, width), dtype=_I32, device=refs.device), prefix_len=torch.empty_like(src),
+                   refs=torch.empty_like(refs))
     else:
         _apart(out["block_table"], block_table, False)
         _apart(out["prefix_len"], prefix_len, False)
@@ -796,7 +798,7 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
             _arg("block_table", block_table, ix, _I32, table), width, _arg("refs", refs, ix, _I32, (NB,)), B]
     if out is None:
         out = dict(block_table=torch.empty_like(block_table), refs=torch.empty_like(refs), remap=torch.empty_like(refs),
-                   live=refs.new_empty((1,)))
+                   live=torch.empty((1,), dtype=_I32, device=refs.device))
     else:
         _apart(out["block_table"], block_table, True)
         _apart(out["refs"], refs, True)

@@ -8,6 +8,7 @@
 // registers, and join across rows by shuffles.  No shared memory and no barrier, so a page's
 // loads are all in flight at once and warps do not wait for each other.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -18,37 +19,81 @@ namespace {
 
 constexpr int kBoundsThreads = 256;
 
-// Running extremes of VEC channels per lane.  fmaxf / fminf return the operand that is a number,
-// so NaN never enters; a channel of nothing but NaN keeps (-inf, +inf) and is set to 0.
+// Running extremes of VEC channels per lane.  The maximum and minimum instructions return the operand that is
+// a number, so NaN never enters; a channel of nothing but NaN keeps (-inf, +inf) and is set to 0.  bf16 chunks
+// are kept in pairs (two channels per instruction, half the shuffles).  fetch() and row() are apart so that the
+// loads of several rows can be issued before the first is used.
 template <typename T, int VEC>
 struct Extremes {
+  using Raw = typename std::conditional<VEC == 1, T, uint4>::type;
   float hi[VEC], lo[VEC];
   __device__ void clear() {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      hi[j] = -INFINITY;
-      lo[j] = INFINITY;
-    }
+    for (int j = 0; j < VEC; ++j) hi[j] = -INFINITY, lo[j] = INFINITY;
   }
+  static __device__ Raw fetch(const T* p) { return __ldg(reinterpret_cast<const Raw*>(p)); }
   __device__ void take(int j, float x) {
     hi[j] = fmaxf(hi[j], x);
     lo[j] = fminf(lo[j], x);
   }
-  __device__ void row(const T* p) {
+  __device__ void row(const Raw& w) {
     if constexpr (VEC == 1) {
-      take(0, static_cast<float>(*p));
+      take(0, static_cast<float>(w));
     } else {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      take(0, __uint_as_float(w.x));
+      take(1, __uint_as_float(w.y));
+      take(2, __uint_as_float(w.z));
+      take(3, __uint_as_float(w.w));
+    }
+  }
+  __device__ void from_lane(int src, bool there) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (VEC == 8) {
-          take(2 * j, bf16_lo(u[j]));
-          take(2 * j + 1, bf16_hi(u[j]));
-        } else {
-          take(j, __uint_as_float(u[j]));
-        }
+    for (int j = 0; j < VEC; ++j) {
+      const float oh = __shfl_sync(0xffffffffu, hi[j], src), ol = __shfl_sync(0xffffffffu, lo[j], src);
+      if (there) {
+        hi[j] = fmaxf(hi[j], oh);
+        lo[j] = fminf(lo[j], ol);
       }
+    }
+  }
+  __device__ void values(float (&h)[VEC], float (&l)[VEC]) const {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) h[j] = hi[j], l[j] = lo[j];
+  }
+};
+
+template <>
+struct Extremes<__nv_bfloat16, 8> {
+  using Raw = uint4;
+  __nv_bfloat162 hi[4], lo[4];
+  __device__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) hi[j] = __float2bfloat162_rn(-INFINITY), lo[j] = __float2bfloat162_rn(INFINITY);
+  }
+  static __device__ Raw fetch(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ void row(const Raw& w) {
+    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      hi[j] = __hmax2(hi[j], x[j]);
+      lo[j] = __hmin2(lo[j], x[j]);
+    }
+  }
+  __device__ void from_lane(int src, bool there) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 oh = __shfl_sync(0xffffffffu, hi[j], src), ol = __shfl_sync(0xffffffffu, lo[j], src);
+      if (there) {
+        hi[j] = __hmax2(hi[j], oh);
+        lo[j] = __hmin2(lo[j], ol);
+      }
+    }
+  }
+  __device__ void values(float (&h)[8], float (&l)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[2 * j] = __low2float(hi[j]), h[2 * j + 1] = __high2float(hi[j]);
+      l[2 * j] = __low2float(lo[j]), l[2 * j + 1] = __high2float(lo[j]);
     }
   }
 };
@@ -61,6 +106,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(
     int max_blocks, const int32_t* __restrict__ prefix_len, const int32_t* __restrict__ start_len,
     __nv_bfloat16* __restrict__ bounds, int32_t* status) {
   pdl_wait();
+  const bool wide_out = (reinterpret_cast<uintptr_t>(bounds) & 15u) == 0;
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int warps = gridDim.x * (kBoundsThreads / 32);
   const int L = prefix_len[b], S = start_len != nullptr ? start_len[b] : 0;
@@ -73,15 +119,28 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(
   const int cpr = d / VEC;                          // chunks per row
   const int rpp = NJ > 1 || cpr >= 32 ? 1 : 32 / cpr;  // rows per pass
   const int r0 = NJ > 1 ? 0 : lane / cpr, c0 = NJ > 1 ? lane : lane % cpr;
-  const long long items = static_cast<long long>(np) * Hkv;
-  for (long long it = blockIdx.x * (kBoundsThreads / 32) + (threadIdx.x >> 5); it < items; it += warps) {
-    const int p = p0 + static_cast<int>(it / Hkv), h = static_cast<int>(it % Hkv);
-    const int page = table[static_cast<long long>(b) * max_blocks + p];
+  // a warp takes heads h, h + dh, ... of pages p, p + dp, ...: the items it, it + warps, ... in page-major
+  // order, without a division each; the next item's page id is loaded an item ahead
+  const int it0 = blockIdx.x * (kBoundsThreads / 32) + (threadIdx.x >> 5);
+  const int dp = warps / Hkv, dh = warps % Hkv;
+  int p = p0 + it0 / Hkv, h = it0 % Hkv;
+  const int end = p0 + np;
+  const int32_t* row = table + static_cast<long long>(b) * max_blocks;
+  int next = p < end ? __ldg(row + p) : 0;
+  while (p < end) {
+    const int page = next, head = h;
+    p += dp;
+    h += dh;
+    if (h >= Hkv) {
+      h -= Hkv;
+      ++p;
+    }
+    next = __ldg(row + min(p, end - 1));
     if (page < 0 || page >= num_blocks) {
       if (lane == 0) report(status, TS_ERR_DEVICE_CHECK);
       continue;
     }
-    const long long ph = static_cast<long long>(page) * Hkv + h;
+    const long long ph = static_cast<long long>(page) * Hkv + head;
     const T* base = kc + ph * bs * d;
     Extremes<T, VEC> x[NJ];
 #pragma unroll
@@ -89,36 +148,34 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(
       x[j].clear();
       const int c = c0 + 32 * j;
       if (r0 < rpp && c < cpr) {
-#pragma unroll 8
-        for (int r = r0; r < bs; r += rpp) x[j].row(base + static_cast<long long>(r) * d + c * VEC);
+        const T* at = base + c * VEC + static_cast<long long>(r0) * d;
+        const long long step = static_cast<long long>(rpp) * d;
+        int r = r0;
+        for (; r + 7 * rpp < bs; r += 8 * rpp, at += 8 * step) {  // eight loads in flight
+          typename Extremes<T, VEC>::Raw w[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) w[u] = Extremes<T, VEC>::fetch(at + u * step);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) x[j].row(w[u]);
+        }
+        for (; r < bs; r += rpp, at += step) x[j].row(Extremes<T, VEC>::fetch(at));
       }
     }
     if constexpr (NJ == 1) {
-      for (int o = 1; o < rpp; ++o) {  // lanes of the first row gather the other rows' extremes
-        const int from = lane + o * cpr;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float oh = __shfl_sync(0xffffffffu, x[0].hi[j], from & 31);
-          const float ol = __shfl_sync(0xffffffffu, x[0].lo[j], from & 31);
-          if (from < 32) {
-            x[0].hi[j] = fmaxf(x[0].hi[j], oh);
-            x[0].lo[j] = fminf(x[0].lo[j], ol);
-          }
-        }
-      }
+      for (int o = 1; o < rpp; ++o)  // lanes of the first row gather the other rows' extremes
+        x[0].from_lane((lane + o * cpr) & 31, lane + o * cpr < 32);
     }
-    float amax = 0.f;
+    float amax = 0.f, xh[NJ][VEC], xl[NJ][VEC];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int c = c0 + 32 * j;
-      if (r0 == 0 && c < cpr) {
+      x[j].values(xh[j], xl[j]);
+      const bool mine = r0 == 0 && c0 + 32 * j < cpr;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const bool none = x[j].hi[i] < x[j].lo[i];
-          x[j].hi[i] = none ? 0.f : grid_clamp(x[j].hi[i]);
-          x[j].lo[i] = none ? 0.f : grid_clamp(x[j].lo[i]);
-          amax = fmaxf(amax, fmaxf(fabsf(x[j].hi[i]), fabsf(x[j].lo[i])));
-        }
+      for (int i = 0; i < VEC; ++i) {
+        const bool none = xh[j][i] < xl[j][i];
+        xh[j][i] = none ? 0.f : grid_clamp(xh[j][i]);
+        xl[j][i] = none ? 0.f : grid_clamp(xl[j][i]);
+        if (mine) amax = fmaxf(amax, fmaxf(fabsf(xh[j][i]), fabsf(xl[j][i])));
       }
     }
 #pragma unroll
@@ -129,17 +186,22 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(
     for (int j = 0; j < NJ; ++j) {
       const int c = c0 + 32 * j;
       if (r0 == 0 && c < cpr) {
-        __nv_bfloat16 hi[VEC], lo[VEC];
+        alignas(16) __nv_bfloat16 hi[VEC], lo[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          hi[i] = __float2bfloat16_rn(ceilf(x[j].hi[i] * up) * grid);   // exact: at most 8 bits
-          lo[i] = __float2bfloat16_rn(floorf(x[j].lo[i] * up) * grid);
+          hi[i] = __float2bfloat16_rn(ceilf(xh[j][i] * up) * grid);   // exact: at most 8 bits
+          lo[i] = __float2bfloat16_rn(floorf(xl[j][i] * up) * grid);
         }
         __nv_bfloat16* o = bounds + ph * 2 * d + c * VEC;
+        if (VEC == 8 && wide_out) {
+          *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(hi);
+          *reinterpret_cast<uint4*>(o + d) = *reinterpret_cast<const uint4*>(lo);
+        } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          o[i] = hi[i];
-          o[d + i] = lo[i];
+          for (int i = 0; i < VEC; ++i) {
+            o[i] = hi[i];
+            o[d + i] = lo[i];
+          }
         }
       }
     }
@@ -150,9 +212,10 @@ template <typename T, int VEC, int NJ>
 cudaError_t go(const void* kc, int num_blocks, int bs, int Hkv, int d, const int32_t* table, int max_blocks,
                const int32_t* prefix_len, const int32_t* start_len, int B, void* bounds, int32_t* status,
                cudaStream_t stream, int num_sms) {
-  // about eight CTAs per SM over the batch: enough loads in flight to fill HBM
+  // six CTAs per SM over the batch, as many as fit at once (4 x 32768 tokens: 54.5 us; five 56.3, eight, of which
+  // two wait for a second round, 60.3, 64 with an item a warp 61.5)
   const long long most = (static_cast<long long>(max_blocks) * Hkv + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32);
-  const long long want = std::max(1LL, (8LL * num_sms + B - 1) / B);
+  const long long want = std::max(1LL, (6LL * num_sms + B - 1) / B);
   return launch_pdl(page_bounds_kernel<T, VEC, NJ>, dim3(static_cast<unsigned>(std::min(most, want)), B),
                     dim3(kBoundsThreads), 0, stream, static_cast<const T*>(kc), num_blocks, bs, Hkv, d, table, max_blocks,
                     prefix_len, start_len, static_cast<__nv_bfloat16*>(bounds), status);

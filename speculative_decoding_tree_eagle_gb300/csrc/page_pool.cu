@@ -277,16 +277,25 @@ __global__ void __launch_bounds__(256) copy_tails_kernel(unsigned char* kc, unsi
 }
 
 // --------------------------------------------------------------------------------------- fork
-// New rows, and refs_out = refs where they are different buffers.
-__global__ void __launch_bounds__(256) fork_rows_kernel(const int32_t* __restrict__ table, int max_blocks,
-                                                        const int32_t* __restrict__ prefix_len, const int32_t* refs,
-                                                        int num_blocks, int bs, int B, const int32_t* __restrict__ src,
-                                                        int B_out, int32_t* __restrict__ table_out,
-                                                        int32_t* __restrict__ prefix_out, int32_t* refs_out,
-                                                        int32_t* status) {
-  pdl_wait();
-  const int tid = threadIdx.x;
-  for (int r = blockIdx.x; r < B_out; r += gridDim.x) {
+struct ForkArgs {
+  const int32_t* table;
+  const int32_t* prefix_len;
+  const int32_t* refs;
+  const int32_t* src;
+  int32_t* table_out;
+  int32_t* prefix_out;
+  int32_t* refs_out;
+  int32_t* status;
+  int max_blocks, num_blocks, bs, B, B_out;
+};
+constexpr int kForkThreads = 256;
+
+// New rows, and refs_out = refs where they are different buffers: the share of CTA `cta` of `ctas`.
+__device__ __forceinline__ void fork_rows(const ForkArgs& a, int cta, int ctas) {
+  const int tid = threadIdx.x, max_blocks = a.max_blocks, num_blocks = a.num_blocks, bs = a.bs, B = a.B, B_out = a.B_out;
+  const int32_t *table = a.table, *prefix_len = a.prefix_len, *src = a.src;
+  int32_t *table_out = a.table_out, *prefix_out = a.prefix_out, *status = a.status;
+  for (int r = cta; r < B_out; r += ctas) {
     const int s = src[r];
     bool bad = s < -1 || s >= B;
     int L = 0;
@@ -313,21 +322,19 @@ __global__ void __launch_bounds__(256) fork_rows_kernel(const int32_t* __restric
     if (bad) report(status, TS_ERR_DEVICE_CHECK);
     if (tid == 0) prefix_out[r] = L;
   }
-  if (refs_out != refs)
-    for (int i = blockIdx.x * 256 + tid; i < num_blocks; i += gridDim.x * 256) refs_out[i] = refs[i];
+  if (a.refs_out != a.refs)
+    for (int i = cta * kForkThreads + tid; i < num_blocks; i += ctas * kForkThreads) a.refs_out[i] = a.refs[i];
 }
 
 // Counts: an entry of old row s among its kept pages is named once less and once more per new row
 // that continues s; an entry beyond them is only let go.  Rows continued exactly once cost no
 // atomic for their kept pages.
-__global__ void __launch_bounds__(256) fork_refs_kernel(const int32_t* __restrict__ table, int max_blocks,
-                                                        const int32_t* __restrict__ prefix_len, int num_blocks, int bs,
-                                                        int B, const int32_t* __restrict__ src, int B_out,
-                                                        int32_t* __restrict__ refs_out, int32_t* status) {
+__device__ __forceinline__ void fork_refs(const ForkArgs& a, int cta, int ctas) {
   __shared__ int s_sum[8];
-  pdl_wait();
-  const int tid = threadIdx.x;
-  for (int s = blockIdx.x; s < B; s += gridDim.x) {
+  const int tid = threadIdx.x, max_blocks = a.max_blocks, num_blocks = a.num_blocks, bs = a.bs, B = a.B, B_out = a.B_out;
+  const int32_t *table = a.table, *prefix_len = a.prefix_len, *src = a.src;
+  int32_t *refs_out = a.refs_out, *status = a.status;
+  for (int s = cta; s < B; s += ctas) {
     int times = 0;
     for (int r = tid; r < B_out; r += 256) times += src[r] == s;
     times = __reduce_add_sync(0xffffffffu, times);
@@ -354,6 +361,22 @@ __global__ void __launch_bounds__(256) fork_refs_kernel(const int32_t* __restric
   }
 }
 
+__global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(const ForkArgs a) {
+  pdl_wait();
+  fork_rows(a, blockIdx.x, gridDim.x);
+}
+__global__ void __launch_bounds__(kForkThreads) fork_refs_kernel(const ForkArgs a) {
+  pdl_wait();
+  fork_refs(a, blockIdx.x, gridDim.x);
+}
+// Both in one launch by one cluster, the barrier between them the cluster's.
+__global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kForkThreads) fork_small_kernel(const ForkArgs a) {
+  pdl_wait();
+  fork_rows(a, blockIdx.x, kPoolCtas);
+  cluster_sync_all();
+  fork_refs(a, blockIdx.x, kPoolCtas);
+}
+
 // ------------------------------------------------------------------------------------ compact
 struct CompactArgs {
   const int32_t* refs;
@@ -364,43 +387,73 @@ struct CompactArgs {
   int num_blocks;
 };
 
+// A CTA's share of the pages is cut into runs of 4096, four neighbouring pages per thread; the first run's counts
+// stay in registers (pools of up to 32768 pages have no other), longer shares read theirs again.
 __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1) compact_kernel(const CompactArgs a) {
   __shared__ int s_warp[32], s_all[3][kPoolCtas];
-  pdl_wait();
+  constexpr int RUN = 4 * kPoolThreads;
   const int rank = static_cast<int>(cluster_ctarank());
   const int tid = threadIdx.x, gtid = rank * kPoolThreads + tid, gthreads = kPoolCtas * kPoolThreads;
-  const int share = ((a.num_blocks + gthreads - 1) / gthreads) * kPoolThreads;
+  cluster_sync_all();  // every CTA of the cluster runs before its shared memory is written to
+  pdl_wait();
+  const int share = (a.num_blocks + kPoolCtas * RUN - 1) / (kPoolCtas * RUN) * RUN;
   const int lo = static_cast<int>(min(static_cast<long long>(rank) * share, static_cast<long long>(a.num_blocks)));
   const int hi = min(lo + share, a.num_blocks);
-  cluster_sync_all();  // every CTA of the cluster runs before its shared memory is written to
+  int n0[4];
+  auto load = [&](int i0, int (&n)[4]) {  // references of this thread's four pages of the run from i0 (0 past the share)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) n[u] = i0 + 4 * tid + u < hi ? a.refs[i0 + 4 * tid + u] : 0;
+  };
+  load(lo, n0);
   int used = 0, sum;
-  for (int i = lo + tid; i < hi; i += kPoolThreads) used += a.refs[i] > 0;
+  for (int i0 = lo; i0 < hi; i0 += RUN) {
+    int n[4] = {n0[0], n0[1], n0[2], n0[3]};
+    if (i0 > lo) load(i0, n);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) used += n[u] > 0;
+  }
   block_scan(used, s_warp, &sum);
   int live;
   cluster_scan(sum, s_all[0], &live);
   // free pages below `live` and pages in use from there on: as many of the one as of the other
   int holes = 0, movers = 0, hsum, msum;
-  for (int i = lo + tid; i < hi; i += kPoolThreads) {
-    const bool u = a.refs[i] > 0;
-    holes += i < live && !u;
-    movers += i >= live && u;
+  for (int i0 = lo; i0 < hi; i0 += RUN) {
+    int n[4] = {n0[0], n0[1], n0[2], n0[3]};
+    if (i0 > lo) load(i0, n);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + 4 * tid + u;
+      holes += i < hi && i < live && n[u] <= 0;
+      movers += i >= live && n[u] > 0;
+    }
   }
   block_scan(holes, s_warp, &hsum);
   block_scan(movers, s_warp, &msum);
   int htotal, mtotal;
   int hat = cluster_scan(hsum, s_all[1], &htotal);
   int mat = cluster_scan(msum, s_all[2], &mtotal);
-  for (int i0 = lo; i0 < hi; i0 += kPoolThreads) {
-    const int i = i0 + tid;
-    const int n = i < hi ? a.refs[i] : 0;
-    const bool u = n > 0, hole = i < hi && i < live && !u, mover = i >= live && u;
+  for (int i0 = lo; i0 < hi; i0 += RUN) {
+    int n[4] = {n0[0], n0[1], n0[2], n0[3]};
+    if (i0 > lo) load(i0, n);
+    int kinds = 0;  // holes in the low half, movers in the high one
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + 4 * tid + u;
+      kinds += (i < hi && i < live && n[u] <= 0) + (static_cast<int>(i >= live && n[u] > 0) << 16);
+    }
     int s;
-    // a share may hold both kinds, holes before movers; one scan packs both counts
-    const int packed = block_scan(static_cast<int>(hole) + (static_cast<int>(mover) << 16), s_warp, &s);
-    if (hole) a.moves[2 + 2 * (hat + (packed & 0xffff))] = i;
-    if (mover) a.moves[1 + 2 * (mat + (packed >> 16))] = i;
-    if (i < hi && !mover) a.remap[i] = u ? i : -1;
-    if (a.refs_out != a.refs && i < hi && !mover && !hole) a.refs_out[i] = n;
+    const int at = block_scan(kinds, s_warp, &s);
+    int h = hat + (at & 0xffff), m = mat + (at >> 16);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + 4 * tid + u;
+      if (i >= hi) break;
+      const bool use = n[u] > 0, hole = i < live && !use, mover = i >= live && use;
+      if (hole) a.moves[2 + 2 * h++] = i;
+      if (mover) a.moves[1 + 2 * m++] = i;
+      if (!mover) a.remap[i] = use ? i : -1;
+      if (a.refs_out != a.refs && !mover && !hole) a.refs_out[i] = n[u];
+    }
     hat += s & 0xffff;
     mat += s >> 16;
   }
@@ -517,14 +570,22 @@ int kv_reserve_launch(const ReserveCall& c, cudaStream_t stream) {
 int kv_fork_launch(const int32_t* block_table, int max_blocks, const int32_t* prefix_len, const int32_t* refs, int num_blocks,
                    int block_size, int B, const int32_t* src, int B_out, int32_t* block_table_out, int32_t* prefix_len_out,
                    int32_t* refs_out, int32_t* dev_status, cudaStream_t stream, int num_sms) {
+  const ForkArgs a{block_table, prefix_len, refs, src, block_table_out, prefix_len_out, refs_out, dev_status,
+                   max_blocks, num_blocks, block_size, B, B_out};
+  // Up to some ten thousand words, one cluster does both steps in less than a second launch costs (one sequence to
+  // eight of 128 pages: XX us against 6.3); larger states are spread over the GPU.
+  const long long words = (static_cast<long long>(B) + B_out) * max_blocks + num_blocks;
+  if (words <= 32768) {
+    const cudaError_t e = launch_pdl(fork_small_kernel, dim3(kPoolCtas), dim3(kForkThreads), 0, stream, a);
+    count_launches(1);
+    return e == cudaSuccess ? TS_OK : TS_ERR_CUDA;
+  }
   const int copy_ctas = refs_out != refs ? (num_blocks + 1023) / 1024 : 1;
   const int g1 = std::min(std::max(B_out, copy_ctas), 8 * num_sms);
-  cudaError_t e = launch_pdl(fork_rows_kernel, dim3(g1), dim3(256), 0, stream, block_table, max_blocks, prefix_len, refs,
-                             num_blocks, block_size, B, src, B_out, block_table_out, prefix_len_out, refs_out, dev_status);
+  cudaError_t e = launch_pdl(fork_rows_kernel, dim3(g1), dim3(kForkThreads), 0, stream, a);
   if (e != cudaSuccess) return TS_ERR_CUDA;
   count_launches(1);
-  e = launch_pdl(fork_refs_kernel, dim3(std::min(B, 8 * num_sms)), dim3(256), 0, stream, block_table, max_blocks, prefix_len,
-                 num_blocks, block_size, B, src, B_out, refs_out, dev_status);
+  e = launch_pdl(fork_refs_kernel, dim3(std::min(B, 8 * num_sms)), dim3(kForkThreads), 0, stream, a);
   if (e != cudaSuccess) return TS_ERR_CUDA;
   count_launches(1);
   return TS_OK;
@@ -546,7 +607,10 @@ int kv_compact_launch(void* k_cache, void* v_cache, ts_dtype dt, void* bounds, i
   const long long cells = static_cast<long long>(B) * max_blocks;
   unsigned char *k = static_cast<unsigned char*>(k_cache), *v = static_cast<unsigned char*>(v_cache);
   unsigned char* bd = static_cast<unsigned char*>(bounds);
-  const dim3 grid(8 * num_sms);
+  // A CTA per buffer of a move up to 64 per SM (16384 of 24576 pages' K and V moved by a third: 148 us against 160
+  // with eight per SM), at most what this pool can have.
+  const long long most = std::max((cells + 255) / 256, (static_cast<long long>(num_blocks) / 2 + 1) * (bounds ? 3 : 2));
+  const dim3 grid(static_cast<unsigned>(std::min<long long>(64LL * num_sms, most)));
   e = wide_rows(k, v, row_bytes)
           ? launch_pdl(move_pages_kernel<uint4>, grid, dim3(256), 0, stream, k, v, bd, page_bytes, bounds_bytes,
                        a.moves, remap, num_blocks, block_table,

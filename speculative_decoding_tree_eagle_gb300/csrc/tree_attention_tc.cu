@@ -12,8 +12,8 @@
 // the second read comes from L2.  One CTA per SM.
 //
 // Warp roles (12 warps + extra producers):
-//   warps 0,3 (+ extra)  K producers; warp 0 first stages the chunk's physical block ids in
-//                        shared memory.  One thread per producer warp issues TMA loads: per
+//   warps 0,3 (+ extra)  K producers (all warps first stage the chunk's physical block ids in
+//                        shared memory).  One thread per producer warp issues TMA loads: per
 //                        128-key tile one box of min(block_size,64) rows x 64 bf16 (128-byte
 //                        swizzle) per page and head-dim half, an even share of the tile's boxes
 //                        per producer; positions past the sequence load an out-of-range block
@@ -27,8 +27,8 @@
 //                        runs.
 //   warps 4..11          softmax, two threads per row (TMEM lane): warps 4..7 take keys 0..63
 //                        of every tile, warps 8..11 keys 64..127.  First each stages its row's
-//                        head-dim half of Q in shared memory (the MMA thread waits for all of
-//                        them on an mbarrier).  Per tile each loads its 64 scores,
+//                        head-dim half of Q, loaded during the CTA's set-up, in shared memory (the
+//                        MMA thread waits for all of them on an mbarrier).  Per tile each loads its 64 scores,
 //                        applies the tree mask on the tiles that reach the tree, exchanges its
 //                        row maximum with its partner through shared memory, and runs the
 //                        online softmax in the log2 domain with lazy rescaling of its half of O
@@ -388,55 +388,61 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
     tmem_relinquish();
   }
-  // Physical block of every TMA box row group of this chunk -> shared memory (warp 0,
-  // coalesced, 4 independent loads in flight per lane); out-of-range ids are reported and
-  // replaced by the out-of-bounds block, positions past the sequence get it too.
+  // This softmax thread's half row of Q, on its way while the CTA sets itself up (stored to shared memory
+  // below, once the barriers exist).
+  const int sm_q4 = warp & 3, sm_hh = (warp - 4) >> 2, sm_row = sm_q4 * 32 + lane;
+  const bool sm_valid = warp >= 4 && warp < C::EXTRA_WARP && sm_row < rows_here;
+  uint4 qv[8];
+  {
+    const int grow = R0 + (sm_valid ? sm_row : 0);
+    const long long qoff =
+        ((static_cast<long long>(b) * p.m + grow / p.g) * p.Hq + kvh * p.g + grow % p.g) * HD + 64 * (sm_valid ? sm_hh : 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      qv[j] = sm_valid && nt > 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + qoff) + j) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  // Sparse mode: the page-major node words of this warp's first 32 groups of 16 keys (see below), requested
+  // ahead of the ids' two dependent loads.
+  const int bs_log2 = 31 - __clz(p.block_size);  // (a power of two on this path)
+  const int node0 = R0 / p.g;
+  auto node_word = [&](int w, int word) -> uint64_t {
+    const int v = (t0 * BN + (32 * w + lane) * 16) >> bs_log2;
+    const uint64_t* at = p.node_mask + (static_cast<long long>(bk) * p.C + max(0, min(v, span.nu - 1))) * p.W + word;
+    const uint64_t x = __ldg(reinterpret_cast<const unsigned long long*>(at));
+    return v < span.nu ? x : ~0ull;
+  };
+  uint64_t first_word = 0ull;
+  if constexpr (SP) first_word = node_word(warp, node0 >> 6);
+  // Physical block of every TMA box row group of this chunk -> shared memory, a box per thread (in the
+  // sparse mode two dependent loads each: by one warp, four at a time, they took 9000 cycles of a 33-tile
+  // CTA's 95000); out-of-range ids are reported and replaced by the out-of-bounds block, positions past the
+  // sequence get it too.
   const int rpb = min(p.block_size, 64);  // rows per box
   const int bpt = BN / rpb;               // box rows per tile
   int* s_blk = reinterpret_cast<int*>(sptr + C::OFF_BLK);
-  if (warp == 0) {
-    const int nbox = nt * bpt;
-    for (int e0 = lane; e0 < nbox; e0 += 4 * 32) {
-      int ids[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int e = e0 + 32 * u;
-        const int key = t0 * BN + e * rpb;
-        ids[u] = -1;
-        if (e < nbox && key < nkeys) {
-          const int lp = SP ? virtual_page(p, span, bk, key / p.block_size) : key / p.block_size;
-          if (!SP || lp >= 0) ids[u] = __ldg(p.block_table + static_cast<long long>(b) * p.max_blocks + lp);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int e = e0 + 32 * u;
-        if (e >= nbox) break;
-        const int key = t0 * BN + e * rpb;
-        int phys = p.num_blocks;
-        if (key < nkeys) {
-          if (ids[u] >= 0 && ids[u] < p.num_blocks) phys = ids[u];
-          else report(p.status, TS_ERR_DEVICE_CHECK);
-        }
-        s_blk[e] = phys;
-      }
+  for (int e = threadIdx.x; e < nt * bpt; e += C::THREADS) {
+    const int key = t0 * BN + e * rpb;
+    int phys = p.num_blocks;
+    if (key < nkeys) {
+      const int lp = SP ? virtual_page(p, span, bk, key / p.block_size) : key / p.block_size;
+      const int id = !SP || lp >= 0 ? __ldg(p.block_table + static_cast<long long>(b) * p.max_blocks + lp) : -1;
+      if (id >= 0 && id < p.num_blocks) phys = id;
+      else report(p.status, TS_ERR_DEVICE_CHECK);
     }
+    s_blk[e] = phys;
   }
   // Sparse mode: the page-major node words are turned into node-major bits, 32 groups of 16 keys at a
   // time: lane = group, one ballot per node.  1 from the incomplete page on (the general visibility
   // test takes over there).
   uint32_t* s_bits = reinterpret_cast<uint32_t*>(s_blk + (SP ? p.cap_tiles * bpt : 0));
   if constexpr (SP) {
-    const int bs_log2 = 31 - __clz(p.block_size);  // (a power of two on this path)
-    const int node0 = R0 / p.g, nodes = (R0 + rows_here - 1) / p.g - node0 + 1;
+    const int nodes = (R0 + rows_here - 1) / p.g - node0 + 1;
     const int words = (nt * (BN / 16) + 31) / 32;
     for (int w = warp; w < words; w += C::THREADS / 32) {
-      const int v = (t0 * BN + (32 * w + lane) * 16) >> bs_log2;
-      const uint64_t* nm = p.node_mask + (static_cast<long long>(bk) * p.C + v) * p.W;
-      uint64_t x = ~0ull;
+      uint64_t x = w == warp ? first_word : node_word(w, node0 >> 6);
       for (int j = 0; j < nodes; ++j) {
         const int node = node0 + j;
-        if (v < span.nu && (j == 0 || (node & 63) == 0)) x = __ldg(reinterpret_cast<const unsigned long long*>(nm + (node >> 6)));
+        if (j > 0 && (node & 63) == 0) x = node_word(w, node >> 6);
         const uint32_t bits = __ballot_sync(0xffffffffu, (x >> (node & 63)) & 1ull);
         if (lane == (j & 31)) s_bits[j * p.bit_words + w] = bits;
       }
@@ -676,21 +682,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       }
       const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
       const uint32_t tO = tmem + lane_off + 64u * hh;
-      {  // this row's head-dim half hh of Q -> shared memory in the 128-byte-swizzled K-major
-         // layout (16-byte chunk j of row r at chunk j ^ (r % 8)); zeros for padding rows.  The
-         // softmax threads stage Q after the CTA's set-up, while the producers start loading.
-        const long long qoff =
-            ((static_cast<long long>(b) * p.m + node) * p.Hq + kvh * p.g + (valid ? grow % p.g : 0)) * HD + 64 * hh;
-        uint4 qv[8];
+      // this row's head-dim half hh of Q -> shared memory in the 128-byte-swizzled K-major layout (16-byte
+      // chunk j of row r at chunk j ^ (r % 8)); zeros for padding rows
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          qv[j] = valid ? __ldg(reinterpret_cast<const uint4*>(p.q + qoff) + j) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(sptr + C::OFF_Q + hh * QHALF + r * 128 + ((j ^ (r & 7)) << 4)) = qv[j];
-        fence_proxy_async_smem();
-        mbar_arrive(q_ready);
-      }
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(sptr + C::OFF_Q + hh * QHALF + r * 128 + ((j ^ (r & 7)) << 4)) = qv[j];
+      fence_proxy_async_smem();
+      mbar_arrive(q_ready);
       const float sl2 = p.scale_log2;
       float* xch = reinterpret_cast<float*>(sptr + C::OFF_XCH);
       // the partner thread's value for exchange round `round` (both threads of a row take part
@@ -940,8 +938,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       }
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       float Ls = 0.f;
+      bool nan_sum = false;
 #pragma unroll
       for (int c = 0; c < kMaxCluster; ++c) {
+        if (SP) nan_sum |= isnan(mls[c].y);
         if (!(mls[c].y > 0.f)) continue;
         const float w = ex2_approx(mls[c].x - M);
         Ls += w * mls[c].y;
@@ -954,6 +954,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
       const int node = grow / p.g, head = kvh * p.g + grow % p.g;
       const long long oo = ((static_cast<long long>(b) * p.m + node) * p.Hq + head) * HD + lane * 4;
+      if constexpr (SP) {
+        if (__any_sync(0xffffffffu, nan_sum || isnan(acc.x) || isnan(acc.y) || isnan(acc.z) || isnan(acc.w))) {
+          repair_row(p, kc, vc, b, kvh, node, head);
+          continue;
+        }
+      }
       uint2 w2;
       w2.x = pack_bf16x2(acc.x * inv, acc.y * inv);
       w2.y = pack_bf16x2(acc.z * inv, acc.w * inv);
@@ -1337,9 +1343,10 @@ static int launch_kernel(const CUtensorMap& mk, const CUtensorMap& mv, const Par
   cfg.numAttrs = 1;
   if (pl.mode == kCluster || pl.mc > 1) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
+    const int chunks = pl.mode == kCluster ? pl.nc : 1;
     attr[1].val.clusterDim.x = pl.mc;
-    attr[1].val.clusterDim.y = pl.mode == kCluster ? pl.nc : 1;
-    attr[1].val.clusterDim.z = 1;
+    attr[1].val.clusterDim.y = SP ? 1 : chunks;
+    attr[1].val.clusterDim.z = SP ? chunks : 1;
     cfg.numAttrs = 2;
   }
   const cudaError_t el = cudaLaunchKernelEx(&cfg, tree_attn_tc_kernel<SP>, mk, mv, prm,
@@ -1383,18 +1390,34 @@ static Plan sparse_plan(int B, int m, int Hq, int Hkv, int C, int block_size, in
   if (pl.cap_tiles > T) pl.cap_tiles = static_cast<int>(T);
   pl.bit_words = (pl.cap_tiles + 3) / 4;
   pl.smem = Cfg::OFF_BLK + 4 * pl.cap_tiles * (BN / (block_size < 64 ? block_size : 64)) + 4 * nodes * pl.bit_words + 1024;
-  const long long most = (T + kSparseMinTiles - 1) / kSparseMinTiles;
   long long share = slots / units;
-  if (share > most) share = most;
+  if (share > T) share = T;
   if (share < 1) share = 1;
-  // Optional override for tests and tuning: TREESPEC_ATTN_SPLIT=direct | global:N
+  // Optional override for tests and tuning: TREESPEC_ATTN_SPLIT=direct | cluster:N | global:N, as far as feasible
+  bool forced_global = false, forced_cluster = false;
   if (const char* ov = std::getenv("TREESPEC_ATTN_SPLIT")) {
     int n = 0;
     if (std::strcmp(ov, "direct") == 0) share = 1;
-    else if (std::sscanf(ov, "global:%d", &n) == 1 && n >= 1 && n <= T) share = n, pl.tpc = 1;
+    else if (std::sscanf(ov, "cluster:%d", &n) == 1 && n >= 1 && n <= T) share = n, forced_cluster = true;
+    else if (std::sscanf(ov, "global:%d", &n) == 1 && n >= 1 && n <= T) share = n, pl.tpc = 1, forced_global = true;
+  }
+  const long long least = (T + pl.cap_tiles - 1) / pl.cap_tiles;
+  // Few units: their chunks are the CTAs of one cluster and merge through its shared memory, which needs neither
+  // partials nor a second launch, as long as all clusters run at once (one node over 64 pages, 8 KV heads: one
+  // sequence 17.5 us with 8 chunks each, 19.6 through the workspace; two sequences 19.6 us with 4, 27.8 with 8,
+  // which take a second wave, 21.6 through the workspace).  Where even eight chunks a unit leave two thirds of the
+  // GPU idle, long unions gain more from the whole GPU.
+  int cs = 1;
+  while (cs * 2 <= share && pl.mc * cs * 2 <= kMaxCluster) cs *= 2;
+  if (!forced_cluster)
+    while (cs > 1 && active_clusters(pl.mc, cs) < units / pl.mc) cs /= 2;
+  if (!forced_global && cs > 1 && (forced_cluster || share < 3 * cs) && least <= cs && active_clusters(pl.mc, cs) > 0) {
+    pl.share = pl.nc = cs;
+    pl.tpc = 1;
+    pl.mode = kCluster;
+    return pl;
   }
   pl.share = static_cast<int>(share);
-  const long long least = (T + pl.cap_tiles - 1) / pl.cap_tiles;
   pl.nc = static_cast<int>(share > least ? share : least);
   pl.mode = pl.nc > 1 ? kGlobal : kDirect;
   return pl;

@@ -120,7 +120,7 @@ def test_matches_the_oracle(c):
     _check(*x[:4], c["L"], *x[4:], out, lse)
 
 
-@pytest.mark.parametrize("split", ["direct", "global:2", "global:3", "global:7"])
+@pytest.mark.parametrize("split", ["direct", "cluster:2", "cluster:4", "cluster:8", "global:2", "global:3", "global:7"])
 def test_every_split(split, monkeypatch):
     lib()
     monkeypatch.setenv("TREESPEC_ATTN_SPLIT", split)
@@ -158,7 +158,7 @@ def test_flat_and_sharp_scores(spread):
         assert (np.abs(out.double().cpu().numpy() - ref) <= 2.0 ** -8 * (s + np.abs(ref)) + 2.0 ** -7 * s).all()
 
 
-@pytest.mark.parametrize("split", ["direct", "global:3"])
+@pytest.mark.parametrize("split", ["direct", "cluster:4", "global:3"])
 @pytest.mark.parametrize("c", [CASES[2], dict(CASES[10], L=[100, 48, 41])], ids=_id)
 def test_non_finite_values_in_places_not_attended_to(c, split, monkeypatch):
     """NaN and infinities in pages that a node does not keep, in other branches of the tree, and behind the
