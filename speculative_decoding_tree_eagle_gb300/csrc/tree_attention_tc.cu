@@ -401,8 +401,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     for (int j = 0; j < 8; ++j)
       qv[j] = sm_valid && nt > 0 ? __ldg(reinterpret_cast<const uint4*>(p.q + qoff) + j) : make_uint4(0u, 0u, 0u, 0u);
   }
-  // Sparse mode: the page-major node words of this warp's first 32 groups of 16 keys (see below), requested
-  // ahead of the ids' two dependent loads.
+  // Sparse mode: the page-major node words of this softmax warp's first 32 groups of 16 keys (see below),
+  // requested ahead of the ids' two dependent loads.
   const int bs_log2 = 31 - __clz(p.block_size);  // (a power of two on this path)
   const int node0 = R0 / p.g;
   auto node_word = [&](int w, int word) -> uint64_t {
@@ -411,8 +411,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const uint64_t x = __ldg(reinterpret_cast<const unsigned long long*>(at));
     return v < span.nu ? x : ~0ull;
   };
+  const int sm_index = sm_hh * nact + sm_q4;  // this warp among the 2 nact softmax warps that hold rows
   uint64_t first_word = 0ull;
-  if constexpr (SP) first_word = node_word(warp, node0 >> 6);
+  if constexpr (SP) {
+    if (warp >= 4 && warp < C::EXTRA_WARP) first_word = node_word(sm_index, node0 >> 6);
+  }
   // Physical block of every TMA box row group of this chunk -> shared memory, a box per thread (in the
   // sparse mode two dependent loads each: by one warp, four at a time, they took 9000 cycles of a 33-tile
   // CTA's 95000); out-of-range ids are reported and replaced by the out-of-bounds block, positions past the
@@ -431,23 +434,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     }
     s_blk[e] = phys;
   }
-  // Sparse mode: the page-major node words are turned into node-major bits, 32 groups of 16 keys at a
-  // time: lane = group, one ballot per node.  1 from the incomplete page on (the general visibility
-  // test takes over there).
   uint32_t* s_bits = reinterpret_cast<uint32_t*>(s_blk + (SP ? p.cap_tiles * bpt : 0));
-  if constexpr (SP) {
-    const int nodes = (R0 + rows_here - 1) / p.g - node0 + 1;
-    const int words = (nt * (BN / 16) + 31) / 32;
-    for (int w = warp; w < words; w += C::THREADS / 32) {
-      uint64_t x = w == warp ? first_word : node_word(w, node0 >> 6);
-      for (int j = 0; j < nodes; ++j) {
-        const int node = node0 + j;
-        if (j > 0 && (node & 63) == 0) x = node_word(w, node >> 6);
-        const uint32_t bits = __ballot_sync(0xffffffffu, (x >> (node & 63)) & 1ull);
-        if (lane == (j & 31)) s_bits[j * p.bit_words + w] = bits;
-      }
-    }
-  }
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -701,6 +688,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         *other = xch[(par * 2 + (hh ^ 1)) * BM + r];
         return true;
       };
+      // Sparse mode: the page-major node words are turned into node-major bits, 32 groups of 16 keys at a
+      // time: lane = group, one ballot per node.  1 from the incomplete page on (the general visibility
+      // test takes over there).  The softmax warps do it while the first K tile is on its way.
+      if constexpr (SP) {
+        const int nodes = (R0 + rows_here - 1) / p.g - node0 + 1;
+        const int words = (nt * (BN / 16) + 31) / 32;
+        for (int w = sm_index; w < words; w += 2 * nact) {
+          uint64_t x = w == sm_index ? first_word : node_word(w, node0 >> 6);
+          for (int j = 0; j < nodes; ++j) {
+            const int n = node0 + j;
+            if (j > 0 && (n & 63) == 0) x = node_word(w, n >> 6);
+            const uint32_t bits = __ballot_sync(0xffffffffu, (x >> (n & 63)) & 1ull);
+            if (lane == (j & 31)) s_bits[j * p.bit_words + w] = bits;
+          }
+        }
+        asm volatile("bar.sync 1, %0;" ::"r"(64 * nact) : "memory");
+      }
       // sparse mode: bit u of kept = whether this row's node keeps the page of keys 16u .. 16u+15 of
       // this thread's half of the tile
       const uint32_t* my_bits = s_bits + (valid ? node - R0 / p.g : 0) * p.bit_words;
