@@ -29,7 +29,7 @@ import ctypes
 import math
 import os
 import threading
-from typing import Dict, Optional
+from typing import Dict, List, Optional
 
 import torch
 
@@ -573,6 +573,13 @@ def _arg(name: str, t: torch.Tensor, index: int, dtype, shape) -> int:
     return t.data_ptr()
 
 
+def _out_args(out: Dict[str, torch.Tensor], index: int, made: bool, **want) -> List[int]:
+    """The addresses of the outputs; those of the caller's making are checked."""
+    if made:
+        return [out[name].data_ptr() for name in want]
+    return [_arg(name, out[name], index, dtype, shape) for name, (dtype, shape) in want.items()]
+
+
 def _status_arg(status: Optional[torch.Tensor], index: int) -> Optional[int]:
     return None if status is None else _arg("status", status, index, _I32, (1,))
 
@@ -657,7 +664,8 @@ def page_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor
     if need == 0:
         raise TreeSpecError("invalid page_select sizes")
     C = max(1, max_prefix // block_size)
-    if out is None:
+    made = out is None
+    if made:
         dev = q.device
         out = dict(pages=torch.empty((B, Hkv, C), dtype=_I32, device=dev), count=torch.empty((B, Hkv), dtype=_I32, device=dev),
                    node_mask=torch.empty((B, Hkv, C, W), dtype=_I64, device=dev))
@@ -665,9 +673,9 @@ def page_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor
     _check(L.ts_page_select(_arg("q", q, ix, q.dtype, shape), dt, _arg("bounds", bounds, ix, _BF16, (NB, Hkv, 2, d)), NB,
                             block_size, _arg("block_table", block_table, ix, _I32, (B, width)), width,
                             _arg("prefix_len", prefix_len, ix, _I32, (B,)), max_prefix, B, m, Hq, Hkv, d, n_pages, first,
-                            recent, _arg("pages", out["pages"], ix, _I32, (B, Hkv, C)),
-                            _arg("count", out["count"], ix, _I32, (B, Hkv)),
-                            _arg("node_mask", out["node_mask"], ix, _I64, (B, Hkv, C, W)), ws, ws_bytes,
+                            recent,
+                            *_out_args(out, ix, made, pages=(_I32, (B, Hkv, C)), count=(_I32, (B, Hkv)),
+                                       node_mask=(_I64, (B, Hkv, C, W))), ws, ws_bytes,
                             _status_arg(status, ix), _raw_stream(ix)))
     return out
 
@@ -693,10 +701,15 @@ def tree_attention_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
         raise ValueError("cache shapes do not match q")
     pages = selection["pages"]
     W, C, width = (m + 63) // 64, pages.shape[-1], block_table.shape[1]
+    # (given ones are checked, new ones are not)
+    out_at = None if out is None else _arg("out", out, ix, dtype, shape)
+    lse_at = None if lse is None else _arg("lse", lse, ix, _F32, (B, m, Hq))
     if out is None:
         out = torch.empty_like(q)
+        out_at = out.data_ptr()
     if lse is None and with_lse:
         lse = torch.empty((B, m, Hq), dtype=_F32, device=q.device)
+        lse_at = lse.data_ptr()
     need = L.ts_tree_attention_sparse_workspace(dt, B, m, Hq, Hkv, d, C, bs)
     ws, ws_bytes, keep = _scratch(need, q, workspace) if need > 256 else (None, 0, None)
     _check(L.ts_tree_attention_sparse(_arg("q", q, ix, dtype, shape), _arg("k_cache", k_cache, ix, dtype, cache),
@@ -706,8 +719,7 @@ def tree_attention_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
                                       _arg("mask", mask, ix, _I64, (B, m, W)), _arg("pages", pages, ix, _I32, (B, Hkv, C)),
                                       _arg("count", selection["count"], ix, _I32, (B, Hkv)),
                                       _arg("node_mask", selection["node_mask"], ix, _I64, (B, Hkv, C, W)), C, B, m, Hq, Hkv,
-                                      d, 1.0 / math.sqrt(d) if scale is None else scale, _arg("out", out, ix, dtype, shape),
-                                      None if lse is None else _arg("lse", lse, ix, _F32, (B, m, Hq)), ws, ws_bytes,
+                                      d, 1.0 / math.sqrt(d) if scale is None else scale, out_at, lse_at, ws, ws_bytes,
                                       _status_arg(status, ix), _raw_stream(ix)))
     return out, lse
 
@@ -738,15 +750,16 @@ def kv_reserve(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
             _arg("refs", refs, ix, _I32, (NB,)), B, n]
     nfreed = 0 if freed is None else freed.numel()
     freed_at = _arg("freed", freed, ix, _I32, freed.shape) if nfreed else None
-    if out is None:
+    made = out is None
+    if made:
         out = dict(block_table=torch.empty_like(block_table), refs=torch.empty_like(refs),
                    granted=torch.empty_like(prefix_len))
     else:
         _apart(out["block_table"], block_table, True)
         _apart(out["refs"], refs, True)
     ws, ws_bytes, keep = _scratch(need, refs, workspace)
-    _check(L.ts_kv_reserve(*args, freed_at, nfreed, _arg("block_table", out["block_table"], ix, _I32, table),
-                           _arg("refs", out["refs"], ix, _I32, (NB,)), _arg("granted", out["granted"], ix, _I32, (B,)), ws,
+    _check(L.ts_kv_reserve(*args, freed_at, nfreed,
+                           *_out_args(out, ix, made, block_table=(_I32, table), refs=(_I32, (NB,)), granted=(_I32, (B,))), ws,
                            ws_bytes, _status_arg(status, ix), _raw_stream(ix)))
     return out
 
@@ -765,7 +778,8 @@ def kv_fork(block_table: torch.Tensor, prefix_len: torch.Tensor, refs: torch.Ten
     R, NB = src.shape[0], refs.shape[0]
     args = [_arg("block_table", block_table, ix, _I32, table), width, _arg("prefix_len", prefix_len, ix, _I32, (B,)),
             _arg("refs", refs, ix, _I32, (NB,)), NB, block_size, B, _arg("src", src, ix, _I32, (R,)), R]
-    if out is None:
+    made = out is None
+    if made:
         out = dict(block_table=torch.empty((R, width), dtype=_I32, device=refs.device), prefix_len=torch.empty_like(src),
                    refs=torch.empty_like(refs))
     else:
@@ -773,9 +787,8 @@ def kv_fork(block_table: torch.Tensor, prefix_len: torch.Tensor, refs: torch.Ten
         _apart(out["prefix_len"], prefix_len, False)
         _apart(out["prefix_len"], src, False)
         _apart(out["refs"], refs, True)
-    _check(L.ts_kv_fork(*args, _arg("block_table", out["block_table"], ix, _I32, (R, width)),
-                        _arg("prefix_len", out["prefix_len"], ix, _I32, (R,)), _arg("refs", out["refs"], ix, _I32, (NB,)),
-                        _status_arg(status, ix), _raw_stream(ix)))
+    _check(L.ts_kv_fork(*args, *_out_args(out, ix, made, block_table=(_I32, (R, width)), prefix_len=(_I32, (R,)),
+                                          refs=(_I32, (NB,))), _status_arg(status, ix), _raw_stream(ix)))
     return out
 
 
@@ -796,7 +809,8 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
     args = [_arg("k_cache", k_cache, ix, dtype, cache), _arg("v_cache", v_cache, ix, dtype, cache), dt,
             None if bounds is None else _arg("bounds", bounds, ix, _BF16, (NB, Hkv, 2, d)), NB, bs, Hkv, d,
             _arg("block_table", block_table, ix, _I32, table), width, _arg("refs", refs, ix, _I32, (NB,)), B]
-    if out is None:
+    made = out is None
+    if made:
         out = dict(block_table=torch.empty_like(block_table), refs=torch.empty_like(refs), remap=torch.empty_like(refs),
                    live=torch.empty((1,), dtype=_I32, device=refs.device))
     else:
@@ -805,7 +819,6 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
         _apart(out["remap"], refs, False)
         _apart(out["remap"], out["refs"], False)
     ws, ws_bytes, keep = _scratch(L.ts_kv_compact_workspace(NB), refs, workspace)
-    _check(L.ts_kv_compact(*args, _arg("block_table", out["block_table"], ix, _I32, table),
-                           _arg("refs", out["refs"], ix, _I32, (NB,)), _arg("remap", out["remap"], ix, _I32, (NB,)),
-                           _arg("live", out["live"], ix, _I32, (1,)), ws, ws_bytes, _status_arg(status, ix), _raw_stream(ix)))
+    _check(L.ts_kv_compact(*args, *_out_args(out, ix, made, block_table=(_I32, table), refs=(_I32, (NB,)),
+                                             remap=(_I32, (NB,)), live=(_I32, (1,))), ws, ws_bytes, _status_arg(status, ix), _raw_stream(ix)))
     return out

@@ -23,6 +23,10 @@ constexpr int kPoolCtas = 8;        // one cluster (the portable limit)
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWarps = kPoolThreads / 32;
 
+__device__ __forceinline__ void st_dsmem_u32(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // Exclusive prefix sum of v over the CTA's threads; *total is the sum.  Two barriers.
 __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -51,9 +55,7 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
 // Contains a cluster barrier (also for the global memory written before it).
 __device__ __forceinline__ int cluster_scan(int mine, int* s_all, int* total) {
   const uint32_t rank = cluster_ctarank();
-  if (threadIdx.x < kPoolCtas)
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_addr(smem_u32(s_all + rank), threadIdx.x)), "r"(mine)
-                 : "memory");
+  if (threadIdx.x < kPoolCtas) st_dsmem_u32(dsmem_addr(smem_u32(s_all + rank), threadIdx.x), mine);
   cluster_sync_all();
   int before = 0, sum = 0;
 #pragma unroll
@@ -74,9 +76,6 @@ struct ReserveArgs {
   int32_t* table_out;
   int32_t* refs_out;
   int32_t* granted;
-  int32_t* tail;       // [B] page of the half-filled last page where others hold it too, else -1
-  int32_t* tail_refs;  // [B] its references before any copy
-  int32_t* want;       // [B] fresh pages the row asks for, -1 for a row with a bad state
   int32_t* copy;       // [B, 2] page to copy from and to (from -1: none)
   int32_t* free_list;  // the lowest free pages, as many as are asked for
   int32_t* status;
@@ -93,15 +92,24 @@ __device__ __forceinline__ bool row_span(const ReserveArgs& a, int b, int* L, in
   return true;
 }
 
+// Steps, with a cluster barrier between each two: copy the state; release; count what each row lacks and the free
+// pages of each CTA's share; (where last pages are shared) decide who copies; number the requests and list the
+// lowest free pages; hand them out.  What all CTAs need to know of a row (its shared last page, how many pages
+// it wants) is written straight into every CTA's shared memory; what only its own warp needs stays in registers
+// (lane k of a warp holds that of its k-th row).  A step costs its dependent loads, some 1300 cycles each.
 __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1) reserve_kernel(const ReserveArgs a) {
-  __shared__ int s_warp[32], s_all[kPoolCtas], s_first_short;
-  __shared__ int s_off[TS_MAX_POOL_ROWS];
-  pdl_wait();
-  if (threadIdx.x == 0) s_first_short = a.B;
+  __shared__ int s_warp[32], s_all[2][kPoolCtas], s_first_short, s_shared;
+  __shared__ int s_want[TS_MAX_POOL_ROWS], s_tail[TS_MAX_POOL_ROWS];
+  constexpr int RUN = 4 * kPoolThreads;  // pages of a share looked at at a time, four neighbours per thread
   const int rank = static_cast<int>(cluster_ctarank());
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gtid = rank * kPoolThreads + tid, gthreads = kPoolCtas * kPoolThreads;
   const int gwarp = rank * kPoolWarps + warp, gwarps = kPoolCtas * kPoolWarps;
+  if (tid == 0) {
+    s_first_short = a.B;
+    s_shared = 0;
+  }
+  pdl_wait();
   // the new state starts as the old one
   if (a.refs_out != a.refs)
     for (int i = gtid; i < a.num_blocks; i += gthreads) a.refs_out[i] = a.refs[i];
@@ -109,8 +117,9 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     const long long cells = static_cast<long long>(a.B) * a.max_blocks;
     for (long long i = gtid; i < cells; i += gthreads) a.table_out[i] = a.table[i];
   }
+  cluster_sync_all();  // (also: every CTA runs before its shared memory is written to)
+  const int32_t* refs = a.refs;
   if (a.num_freed > 0) {
-    cluster_sync_all();
     for (int i = gtid; i < a.num_freed; i += gthreads) {
       const int p = a.freed[i];
       if (p < 0) continue;
@@ -121,11 +130,26 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
         report(a.status, TS_ERR_DEVICE_CHECK);
       }
     }
+    refs = a.refs_out;
+    cluster_sync_all();
   }
-  cluster_sync_all();
+  // free pages of this CTA's share (a bit per page; the first run's stay in a register)
+  const int share = (a.num_blocks + kPoolCtas * RUN - 1) / (kPoolCtas * RUN) * RUN;
+  const int lo = static_cast<int>(min(static_cast<long long>(rank) * share, static_cast<long long>(a.num_blocks)));
+  const int hi = min(lo + share, a.num_blocks);
+  auto free_bits = [&](int i0) -> unsigned {
+    unsigned bits = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + 4 * tid + u < hi && __ldcg(refs + i0 + 4 * tid + u) == 0) bits |= 1u << u;
+    return bits;
+  };
+  const unsigned first_run = free_bits(lo);
   // what each row lacks, and whether its last page is shared; a warp per row
-  for (int b = gwarp; b < a.B; b += gwarps) {
-    int L, first, last, need = 0, tail = -1;
+  int my_want = 0, my_refs = 0;
+  bool my_copy = false;
+  for (int b = gwarp, k = 0; b < a.B; b += gwarps, ++k) {
+    int L, first, last, need = 0, tail = -1, tail_refs = 0;
     bool ok = row_span(a, b, &L, &first, &last);
     if (ok) {
       const int32_t* row = a.table + static_cast<long long>(b) * a.max_blocks;
@@ -138,82 +162,96 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
       }
       ok = !__any_sync(0xffffffffu, bad);
       if (L % a.bs == 0 || !ok) tail = -1;
+      if (tail >= 0) tail_refs = __ldcg(refs + tail);
+      if (tail_refs <= 1) tail = -1;
     }
-    if (lane == 0) {
-      const int n = tail >= 0 ? __ldcg(a.refs_out + tail) : 0;
-      a.tail[b] = n > 1 ? tail : -1;
-      a.tail_refs[b] = n;
-      a.want[b] = ok ? need : -1;
-      if (!ok) report(a.status, TS_ERR_DEVICE_CHECK);
+    if (!ok && lane == 0) report(a.status, TS_ERR_DEVICE_CHECK);
+    if (lane < kPoolCtas) {
+      st_dsmem_u32(dsmem_addr(smem_u32(s_want + b), lane), ok ? need : -1);
+      st_dsmem_u32(dsmem_addr(smem_u32(s_tail + b), lane), tail);
+    }
+    if (tail >= 0 && lane == 0) atomicAdd(&s_shared, 1);
+    if (lane == k) {
+      my_want = ok ? need : -1;
+      my_refs = tail_refs;
     }
   }
-  // free pages of this CTA's share
-  const int share = ((a.num_blocks + gthreads - 1) / gthreads) * kPoolThreads;
-  const int lo = static_cast<int>(min(static_cast<long long>(rank) * share, static_cast<long long>(a.num_blocks)));
-  const int hi = min(lo + share, a.num_blocks);
-  int nfree = 0;
-  for (int i = lo + tid; i < hi; i += kPoolThreads) nfree += __ldcg(a.refs_out + i) == 0;
-  int here;
+  int nfree = 0, here;
+  for (int i0 = lo; i0 < hi; i0 += RUN) nfree += __popc(i0 == lo ? first_run : free_bits(i0));
   block_scan(nfree, s_warp, &here);
-  int F;
-  const int free_before = cluster_scan(here, s_all, &F);
-  // of the rows that share a last page, each copies it as long as another reference is left
-  for (int b = gwarp; b < a.B; b += gwarps) {
-    const int t = __ldcg(a.tail + b);
-    if (t < 0) {
-      if (lane < 2) a.copy[2 * b + lane] = -1;
-      continue;
-    }
-    int before = 0;
-    for (int j = lane; j < b; j += 32) before += __ldcg(a.tail + j) == t;
-    before = __reduce_add_sync(0xffffffffu, before);
-    const bool copies = __ldcg(a.tail_refs + b) - before > 1;
-    if (lane == 0) {
-      a.copy[2 * b] = copies ? t : -1;
-      a.copy[2 * b + 1] = -1;
-      if (copies) a.want[b] = __ldcg(a.want + b) + 1;
-    }
+  if (tid < kPoolCtas) {
+    st_dsmem_u32(dsmem_addr(smem_u32(&s_all[0][rank]), tid), here);
+    st_dsmem_u32(dsmem_addr(smem_u32(&s_all[1][rank]), tid), s_shared);
   }
   cluster_sync_all();
-  // where each row's requests start in the order (every CTA for itself)
+  int F = 0, free_before = 0, any_shared = 0;
+#pragma unroll
+  for (int c = 0; c < kPoolCtas; ++c) {
+    free_before += c < rank ? s_all[0][c] : 0;
+    F += s_all[0][c];
+    any_shared += s_all[1][c];
+  }
+  // of the rows that share a last page, each copies it as long as another reference is left
+  for (int b = gwarp, k = 0; b < a.B; b += gwarps, ++k) {
+    const int t = s_tail[b];
+    bool copies = false;
+    if (t >= 0) {
+      int before = 0;
+      for (int j = lane; j < b; j += 32) before += s_tail[j] == t;
+      before = __reduce_add_sync(0xffffffffu, before);
+      copies = __shfl_sync(0xffffffffu, my_refs, k) - before > 1;
+      if (lane == k) {
+        my_copy = copies;
+        my_want += copies;
+      }
+      const int w = __shfl_sync(0xffffffffu, my_want, k);
+      if (copies && lane < kPoolCtas) st_dsmem_u32(dsmem_addr(smem_u32(s_want + b), lane), w);
+    }
+    if (lane < 2) a.copy[2 * b + lane] = lane == 0 && copies ? t : -1;
+  }
+  if (any_shared > 0) cluster_sync_all();
+  else __syncthreads();
+  // where each row's requests start in the order (every CTA for itself), in place of how many they are
   int R = 0;
   for (int b0 = 0; b0 < a.B; b0 += kPoolThreads) {
-    const int w = b0 + tid < a.B ? max(0, __ldcg(a.want + b0 + tid)) : 0;
+    const int w = b0 + tid < a.B ? max(0, s_want[b0 + tid]) : 0;
     int sum;
     const int at = block_scan(w, s_warp, &sum);
-    if (b0 + tid < a.B) s_off[b0 + tid] = R + at;
+    if (b0 + tid < a.B) s_want[b0 + tid] = R + at;
     if (w > 0 && R + at + w > F) atomicMin(&s_first_short, b0 + tid);
     R += sum;
   }
   // this CTA's free pages that somebody gets
   int at = free_before;
-  for (int i0 = lo; i0 < hi && at < R; i0 += kPoolThreads) {
-    const int i = i0 + tid;
-    const int f = i < hi && __ldcg(a.refs_out + i) == 0;
+  for (int i0 = lo; i0 < hi && at < R; i0 += RUN) {
+    const unsigned bits = i0 == lo ? first_run : free_bits(i0);
     int sum;
-    const int r = at + block_scan(f, s_warp, &sum);
-    if (f && r < R) a.free_list[r] = i;
+    int r = at + block_scan(__popc(bits), s_warp, &sum);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if ((bits >> u) & 1u) {
+        if (r < R) a.free_list[r] = i0 + 4 * tid + u;
+        ++r;
+      }
+    }
     at += sum;
   }
   cluster_sync_all();
   const int first_short = s_first_short;
-  for (int b = gwarp; b < a.B; b += gwarps) {
-    const int w = __ldcg(a.want + b);
-    const int from = __ldcg(a.copy + 2 * b);
+  for (int b = gwarp, k = 0; b < a.B; b += gwarps, ++k) {
+    const int w = __shfl_sync(0xffffffffu, my_want, k);
+    const bool copies = __shfl_sync(0xffffffffu, my_copy ? 1 : 0, k) != 0;
     bool is_short = w > 0 && b >= first_short;
-    if (w == 0 && b > first_short) {
+    if (w == 0 && b > first_short && s_tail[b] >= 0) {
       // it was to keep its last page because others before it would have left it: not all have
-      const int t = __ldcg(a.tail + b);
-      if (t >= 0) {
-        int left = 0;
-        for (int j = lane; j < first_short; j += 32) left += __ldcg(a.tail + j) == t;
-        is_short = __ldcg(a.tail_refs + b) - __reduce_add_sync(0xffffffffu, left) > 1;
-      }
+      int left = 0;
+      for (int j = lane; j < first_short; j += 32) left += s_tail[j] == s_tail[b];
+      is_short = __shfl_sync(0xffffffffu, my_refs, k) - __reduce_add_sync(0xffffffffu, left) > 1;
     }
     if (w <= 0 || is_short) {
       if (lane == 0) {
         a.granted[b] = is_short ? -1 : w;
-        a.copy[2 * b] = -1;
+        if (copies) a.copy[2 * b] = -1;
         if (is_short) report(a.status, TS_ERR_NO_PAGES);
       }
       continue;
@@ -221,18 +259,18 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     int L, first, last;
     row_span(a, b, &L, &first, &last);
     int32_t* row = a.table_out + static_cast<long long>(b) * a.max_blocks;
-    int r = s_off[b];
+    int r = s_want[b];
     for (int i0 = first; i0 < last; i0 += 32) {
       const int i = i0 + lane;
-      const bool take = i < last && ((i == first && from >= 0) || __ldcg(row + i) == -1);
+      const bool take = i < last && ((i == first && copies) || __ldcg(row + i) == -1);
       const unsigned m = __ballot_sync(0xffffffffu, take);
       if (take) {
         const int page = __ldcg(a.free_list + r + __popc(m & ((1u << lane) - 1u)));
         row[i] = page;
         a.refs_out[page] = 1;
-        if (i == first && from >= 0) {
+        if (i == first && copies) {
           a.copy[2 * b + 1] = page;
-          atomicSub(a.refs_out + from, 1);
+          atomicSub(a.refs_out + s_tail[b], 1);
         }
       }
       r += __popc(m);
@@ -527,7 +565,7 @@ long long most_requests(int num_blocks, int block_size, int B, int n) {
 }  // namespace
 
 size_t kv_reserve_workspace_bytes(int num_blocks, int block_size, int B, int n) {
-  return 4 * (static_cast<size_t>(5) * B + static_cast<size_t>(most_requests(num_blocks, block_size, B, n)));
+  return 4 * (static_cast<size_t>(2) * B + static_cast<size_t>(most_requests(num_blocks, block_size, B, n)));
 }
 
 int kv_reserve_launch(const ReserveCall& c, cudaStream_t stream) {
@@ -539,10 +577,7 @@ int kv_reserve_launch(const ReserveCall& c, cudaStream_t stream) {
   a.table_out = c.block_table_out;
   a.refs_out = c.refs_out;
   a.granted = c.granted;
-  a.tail = static_cast<int32_t*>(c.workspace);
-  a.tail_refs = a.tail + c.B;
-  a.want = a.tail_refs + c.B;
-  a.copy = a.want + c.B;
+  a.copy = static_cast<int32_t*>(c.workspace);
   a.free_list = a.copy + 2 * static_cast<size_t>(c.B);
   a.status = c.dev_status;
   a.n = c.n;
