@@ -36,7 +36,7 @@
  *     host threads.  It caches launch set-up per process, under locks: kernel attributes,
  *     cluster occupancy and encoded K/V tensor maps (filled by the first calls, which
  *     should come before any stream capture) and the no-allocation scratch address.  The
- *     attribute and occupancy caches assume one GPU model per process; the tested use is
+ *     occupancy cache assumes one GPU model per process; the tested use is
  *     one process per GPU.  Calls that share a workspace must be ordered on one stream.
  *
  * Notation: B sequences, m tree nodes per sequence INCLUDING the root (node 0), k draft
@@ -533,7 +533,8 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
  * given (block_table, prefix_len, refs) and writes the new state to its outputs; where the text
  * says so an output may be the very buffer of its input (partial overlap is not allowed).  All
  * results are whole numbers that do not depend on the order of execution.
- * ts_kv_commit lists what a verify step lets go of; pass that list to the next ts_kv_reserve.
+ * ts_kv_commit lists what a verify step lets go of; pass that list to the next ts_kv_reserve (until then those
+ * pages count as in use).
  * --------------------------------------------------------------------------------- */
 
 /*

@@ -449,12 +449,13 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
   if (!std::isfinite(scale) || !(scale > 0.f)) return TS_ERR_INVALID;
   ts::SparseCall a{q, k_cache, v_cache, dt, num_blocks, block_size, block_table, max_blocks, prefix_len, mask, pages, count,
                    node_mask, C, B, m, Hq, Hkv, d, scale, out, lse, workspace, dev_status};
+  const int sms = ts::device_sm_count();
   if (!ts::attention_uses_tc(dt, d, block_size)) {
     if (Hq > 65535) return TS_ERR_UNSUPPORTED;
-    return ts::attention_sparse_simt_launch(a, static_cast<cudaStream_t>(stream));
+    if (sms <= 0) return TS_ERR_CUDA;
+    return ts::attention_sparse_simt_launch(a, static_cast<cudaStream_t>(stream), sms);
   }
   if (!aligned16_ptr(q) || !aligned16_ptr(k_cache) || !aligned16_ptr(v_cache) || !aligned16_ptr(out)) return TS_ERR_INVALID;
-  const int sms = ts::device_sm_count();
   if (sms <= 0) return TS_ERR_CUDA;
   const size_t need = ts::attention_sparse_tc_workspace_bytes(B, m, Hq, Hkv, C, block_size, sms);
   if (need > 256 && (!workspace || ws_bytes < need)) return TS_ERR_WORKSPACE;

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -11,6 +12,20 @@
 namespace ts {
 
 int device_sm_count();
+
+// Runs `set` (a kernel's attribute, which CUDA keeps per device) the first time the current device is seen;
+// `done` holds a bit per device.  Several threads may run it at once, which does no harm.
+template <typename F>
+inline cudaError_t once_per_device(std::atomic<uint64_t>& done, F set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if ((done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  e = set();
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 size_t tree_build_workspace_bytes(int B, int V, int k, int depth, int num_sms);
 int tree_build_launch(const float* draft_logp, const int32_t* root_tokens, int B, int V, int k,
@@ -149,7 +164,7 @@ struct SparseCall {
   void* workspace;
   int32_t* dev_status;
 };
-int attention_sparse_simt_launch(const SparseCall& a, cudaStream_t stream);
+int attention_sparse_simt_launch(const SparseCall& a, cudaStream_t stream, int num_sms);
 size_t attention_sparse_tc_workspace_bytes(int B, int m, int Hq, int Hkv, int C, int block_size, int num_sms);
 int attention_sparse_tc_launch(const SparseCall& a, cudaStream_t stream, int num_sms);
 

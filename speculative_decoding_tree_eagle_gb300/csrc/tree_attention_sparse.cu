@@ -1,7 +1,7 @@
 // ts_tree_attention_sparse, CUDA-core path: fp32 inputs (any head dim <= 256) and bf16 shapes the
 // tensor-core path does not take.  fp32 arithmetic and accumulation, accurate expf.
 //
-// One CTA per (node, sequence, KV head, group of up to four of its query heads): a node reads only the
+// One CTA (or cluster) per (node, sequence, KV head, group of up to four of its query heads): a node reads only the
 // pages it keeps, and every K/V row it reads serves its group's heads.  The kept pages are listed in
 // shared memory first (up to 1024 at a time), so that no warp waits for a page it will skip; then the
 // eight warps take four keys at a time, lanes across the head dim.  The 4 x 4 dot products are folded
@@ -20,6 +20,11 @@ constexpr int kWarps = 8;
 constexpr int kListed = 1024;  // kept pages listed at a time
 constexpr int KEYS = 4;
 
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ float ld_v(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float ld_v(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void st_v(float* p, float v) { *p = v; }
@@ -34,15 +39,48 @@ __device__ __forceinline__ constexpr int lane_of(int i) {
   return r;
 }
 
-// G query heads (1, 2 or 4) at once, DPL head-dim elements per lane.
-template <typename T, int G, int DPL>
-__global__ void __launch_bounds__(kWarps * 32) sparse_simt_kernel(const SparseCall a, int W) {
+// N neighbouring elements with the widest loads (p aligned to N of them).
+template <int N>
+__device__ __forceinline__ void ld_n(const float* p, float (&v)[N]) {
+  if constexpr (N == 2) {
+    const float2 x = __ldg(reinterpret_cast<const float2*>(p));
+    v[0] = x.x, v[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(p + i));
+      v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void ld_n(const __nv_bfloat16* p, float (&v)[N]) {
+  uint32_t w[N / 2];
+  if constexpr (N == 2) {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  } else if constexpr (N == 4) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = x.x, w[1] = x.y;
+  } else {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+}
+
+// G query heads (1, 2 or 4) at once, DPL head-dim elements per lane: neighbours, in one load (WIDE: d = 32 DPL
+// and aligned tensors), or 32 apart.
+template <typename T, int G, int DPL, bool WIDE>
+__global__ void __launch_bounds__(kWarps * 32) sparse_simt_kernel(const SparseCall a, int W, int cs) {
   __shared__ long long s_row[kListed];  // first K/V row of each listed page
   __shared__ int s_warp[kWarps];
   __shared__ float s_m[kWarps][G], s_l[kWarps][G], s_acc[kWarps][G][32 * DPL];
+  __shared__ float s_part_m[G], s_part_l[G];  // this CTA's share (its output over s_acc[0])
   pdl_wait();
   const int g = a.Hq / a.Hkv, groups = (g + G - 1) / G;
-  const int node = blockIdx.x, b = blockIdx.y, kh = blockIdx.z / groups, h0 = blockIdx.z % groups * G;
+  const int rank = blockIdx.x % cs, share = kWarps * cs;  // cs CTAs (a cluster) share a node's keys
+  const int node = blockIdx.x / cs, b = blockIdx.y, kh = blockIdx.z / groups, h0 = blockIdx.z % groups * G;
   const int bk = b * a.Hkv + kh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int L = a.prefix_len[b], bs = a.block_size, d = a.d, m = a.m;
@@ -56,17 +94,25 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_simt_kernel(const SparseCa
   const T* vc = static_cast<const T*>(a.v_cache);
   const int32_t* table = a.block_table + static_cast<long long>(b) * a.max_blocks;
   const long long q0 = ((static_cast<long long>(b) * m + node) * a.Hq + kh * g + h0) * d;
+  auto channel = [&](int j) { return WIDE ? lane * DPL + j : lane + 32 * j; };
+  auto row_of = [&](const T* p, bool there, float (&v)[DPL]) {  // this lane's part of a row, zeros if there is none
+    if constexpr (WIDE) {
+      if (there) {
+        ld_n<DPL>(p + lane * DPL, v);
+        return;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < DPL; ++j) v[j] = !WIDE && there && channel(j) < d ? ld_v(p + channel(j)) : 0.f;
+  };
   float q[G][DPL], acc[G][DPL], run_m[G], run_l[G];
 #pragma unroll
   for (int h = 0; h < G; ++h) {
     run_m[h] = -INFINITY;
     run_l[h] = 0.f;
+    row_of(static_cast<const T*>(a.q) + q0 + h * d, h0 + h < g, q[h]);
 #pragma unroll
-    for (int j = 0; j < DPL; ++j) {
-      const int c = lane + 32 * j;
-      q[h][j] = c < d && h0 + h < g ? ld_v(static_cast<const T*>(a.q) + q0 + h * d + c) : 0.f;
-      acc[h][j] = 0.f;
-    }
+    for (int j = 0; j < DPL; ++j) acc[h][j] = 0.f;
   }
   // First row of logical page p, -1 where there is none.
   auto page_row = [&](int p) -> long long {
@@ -86,12 +132,8 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_simt_kernel(const SparseCa
     for (int x = 0; x < KEYS; ++x) {
       float kk[DPL];
       const long long at = max(row[x], 0LL) * d;
-#pragma unroll
-      for (int j = 0; j < DPL; ++j) {
-        const int c = lane + 32 * j;
-        kk[j] = row[x] >= 0 && c < d ? ld_v(kc + at + c) : 0.f;
-        vv[x][j] = row[x] >= 0 && c < d ? ld_v(vc + at + c) : 0.f;
-      }
+      row_of(kc + at, row[x] >= 0, kk);
+      row_of(vc + at, row[x] >= 0, vv[x]);
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         float s = 0.f;
@@ -181,7 +223,7 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_simt_kernel(const SparseCa
       u0 += kWarps * 32;
       __syncthreads();
     }
-    for (int it = warp; it < listed * per_page; it += kWarps) {  // (at most C * bs / 4, below 2^28)
+    for (int it = rank * kWarps + warp; it < listed * per_page; it += share) {  // (at most C * bs / 4, below 2^28)
       const long long base = s_row[it / per_page];
       const int r0 = it % per_page * KEYS;
       long long row[KEYS];
@@ -193,20 +235,22 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_simt_kernel(const SparseCa
   }
   // the incomplete page's prefix rows and the node's ancestors
   const uint64_t* mrow = a.mask + (static_cast<long long>(b) * m + node) * W;
-  for (int pos0 = nf * bs + warp * KEYS; pos0 < L + m; pos0 += kWarps * KEYS) {
+  const long long end = static_cast<long long>(L) + m;
+  for (long long pos0 = static_cast<long long>(nf) * bs + (rank * kWarps + warp) * KEYS; pos0 < end; pos0 += share * KEYS) {
     long long row[KEYS];
     bool any = false;
 #pragma unroll
     for (int x = 0; x < KEYS; ++x) {
-      const int pos = pos0 + x, t = pos - L;
-      const bool seen = pos < L || (pos < L + m && ((mrow[t >> 6] >> (t & 63)) & 1ull));
-      const long long first = seen ? page_row(pos / bs) : -1;
+      const long long pos = pos0 + x;
+      const int t = static_cast<int>(pos - L);
+      const bool seen = pos < L || (pos < end && ((mrow[t >> 6] >> (t & 63)) & 1ull));
+      const long long first = seen ? page_row(static_cast<int>(pos / bs)) : -1;
       row[x] = first >= 0 ? first + pos % bs : -1;
       any |= row[x] >= 0;
     }
     if (any) four(row);
   }
-  // join the warps
+  // join the warps, then the CTAs of the cluster
 #pragma unroll
   for (int h = 0; h < G; ++h) {
     if (lane == 0) {
@@ -214,9 +258,12 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_simt_kernel(const SparseCa
       s_l[warp][h] = run_l[h];
     }
 #pragma unroll
-    for (int j = 0; j < DPL; ++j) s_acc[warp][h][lane + 32 * j] = acc[h][j];
+    for (int j = 0; j < DPL; ++j) s_acc[warp][h][channel(j)] = acc[h][j];
   }
   __syncthreads();
+  // weight of a part (m, l) against the common maximum M; a NaN sum is kept, an empty part is not read
+  auto weight = [](float m1, float l1, float M) { return m1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : expf(m1 - M); };
+#pragma unroll 1
   for (int h = 0; h < G && h0 + h < g; ++h) {
     float M = -INFINITY;
 #pragma unroll
@@ -224,42 +271,79 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_simt_kernel(const SparseCa
     float l = 0.f, e[kWarps];
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      e[w] = s_m[w][h] == -INFINITY ? (s_l[w][h] == 0.f ? 0.f : 1.f) : expf(s_m[w][h] - M);  // (a NaN sum is kept)
+      e[w] = weight(s_m[w][h], s_l[w][h], M);
       l += e[w] * s_l[w][h];
     }
-    const float inv = l > 0.f ? 1.f / l : l;  // no key: 0; NaN stays
-    for (int c = tid; c < d; c += kWarps * 32) {
-      float o = 0.f;
+    const int c = tid;  // (d <= 256 = the CTA's threads)
+    float o = 0.f;
+    if (c < d) {
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
         if (e[w] != 0.f) o += e[w] * s_acc[w][h][c];
-      st_v(static_cast<T*>(a.out) + q0 + h * d + c, o * inv);
     }
+    if (cs > 1) {
+      if (c < d) s_acc[0][h][c] = o;  // (read and written by this thread only)
+      if (tid == 0) {
+        s_part_m[h] = M;
+        s_part_l[h] = l;
+      }
+      continue;
+    }
+    const float inv = l > 0.f ? 1.f / l : l;  // no key: 0; NaN stays
+    if (c < d) st_v(static_cast<T*>(a.out) + q0 + h * d + c, o * inv);
     if (a.lse != nullptr && tid == 0) a.lse[(static_cast<long long>(b) * m + node) * a.Hq + kh * g + h0 + h] = M + logf(l);
   }
+  if (cs == 1) return;
+  cluster_sync_all();
+#pragma unroll 1
+  for (int h = rank; h < G && h0 + h < g; h += cs) {  // the CTAs take the heads in turn
+    float M = -INFINITY, l = 0.f, o = 0.f;
+    for (int r = 0; r < cs; ++r) M = fmaxf(M, ld_dsmem_f32(dsmem_addr(smem_u32(s_part_m + h), r)));
+    for (int r = 0; r < cs; ++r) {
+      const float l1 = ld_dsmem_f32(dsmem_addr(smem_u32(s_part_l + h), r));
+      const float e = weight(ld_dsmem_f32(dsmem_addr(smem_u32(s_part_m + h), r)), l1, M);
+      l += e * l1;
+      if (e != 0.f && tid < d) o += e * ld_dsmem_f32(dsmem_addr(smem_u32(&s_acc[0][h][tid]), r));
+    }
+    const float inv = l > 0.f ? 1.f / l : l;
+    if (tid < d) st_v(static_cast<T*>(a.out) + q0 + h * d + tid, o * inv);
+    if (a.lse != nullptr && tid == 0) a.lse[(static_cast<long long>(b) * m + node) * a.Hq + kh * g + h0 + h] = M + logf(l);
+  }
+  cluster_sync_all();  // no CTA leaves while another may still read its shared memory
 }
 
 template <typename T, int G, int DPL>
-cudaError_t go(const SparseCall& a, cudaStream_t stream) {
+cudaError_t go(const SparseCall& a, cudaStream_t stream, int num_sms) {
   const int groups = (a.Hq / a.Hkv + G - 1) / G;
-  return launch_pdl(sparse_simt_kernel<T, G, DPL>, dim3(a.m, a.B, a.Hkv * groups), dim3(kWarps * 32), 0, stream, a, (a.m + 63) / 64);
+  // Few nodes: a cluster of up to eight CTAs per node, as long as they fill the GPU at most twice over (one node of 8
+  // heads on 2 over 64 pages, fp32: 14.9 us against 39).
+  const long long ctas = static_cast<long long>(a.m) * a.B * a.Hkv * groups;
+  int cs = 1;
+  while (cs < 8 && ctas * cs * 2 <= 2LL * num_sms) cs *= 2;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k_cache) |
+                       reinterpret_cast<uintptr_t>(a.v_cache);
+  const bool wide = a.d == 32 * DPL && at % 16 == 0;
+  return launch_pdl_cluster(wide ? sparse_simt_kernel<T, G, DPL, true> : sparse_simt_kernel<T, G, DPL, false>,
+                            dim3(a.m * cs, a.B, a.Hkv * groups), dim3(kWarps * 32), cs, stream, a, (a.m + 63) / 64, cs);
 }
 
 template <typename T, int DPL>
-cudaError_t go_heads(const SparseCall& a, cudaStream_t stream) {
+cudaError_t go_heads(const SparseCall& a, cudaStream_t stream, int num_sms) {
   const int g = a.Hq / a.Hkv;
-  return g >= 3 ? go<T, 4, DPL>(a, stream) : g == 2 ? go<T, 2, DPL>(a, stream) : go<T, 1, DPL>(a, stream);
+  return g >= 3 ? go<T, 4, DPL>(a, stream, num_sms)
+         : g == 2 ? go<T, 2, DPL>(a, stream, num_sms)
+                  : go<T, 1, DPL>(a, stream, num_sms);
 }
 
 template <typename T>
-cudaError_t go_dim(const SparseCall& a, cudaStream_t stream) {
-  return a.d <= 64 ? go_heads<T, 2>(a, stream) : a.d <= 128 ? go_heads<T, 4>(a, stream) : go_heads<T, 8>(a, stream);
+cudaError_t go_dim(const SparseCall& a, cudaStream_t stream, int num_sms) {
+  return a.d <= 64 ? go_heads<T, 2>(a, stream, num_sms) : a.d <= 128 ? go_heads<T, 4>(a, stream, num_sms) : go_heads<T, 8>(a, stream, num_sms);
 }
 
 }  // namespace
 
-int attention_sparse_simt_launch(const SparseCall& a, cudaStream_t stream) {
-  const cudaError_t e = a.dt == TS_F32 ? go_dim<float>(a, stream) : go_dim<__nv_bfloat16>(a, stream);
+int attention_sparse_simt_launch(const SparseCall& a, cudaStream_t stream, int num_sms) {
+  const cudaError_t e = a.dt == TS_F32 ? go_dim<float>(a, stream, num_sms) : go_dim<__nv_bfloat16>(a, stream, num_sms);
   count_launches(1);
   return e == cudaSuccess ? TS_OK : TS_ERR_CUDA;
 }
