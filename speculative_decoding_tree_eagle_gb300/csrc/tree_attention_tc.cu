@@ -748,12 +748,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if constexpr (SP) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              float a0 = s[16 * u], a1 = s[16 * u + 1];
+              float a0 = max3(s[16 * u], s[16 * u + 1], s[16 * u + 2]), a1 = max3(s[16 * u + 3], s[16 * u + 4], s[16 * u + 5]);
 #pragma unroll
-              for (int c = 2; c < 16; c += 2) {
-                a0 = fmaxf(a0, s[16 * u + c]);
-                a1 = fmaxf(a1, s[16 * u + c + 1]);
+              for (int c = 6; c < 14; c += 4) {
+                a0 = max3(a0, s[16 * u + c], s[16 * u + c + 1]);
+                a1 = max3(a1, s[16 * u + c + 2], s[16 * u + c + 3]);
               }
+              a0 = max3(a0, s[16 * u + 14], s[16 * u + 15]);
               m8[2 * u] = ((kept >> u) & 1u) ? a0 : -INFINITY;
               m8[2 * u + 1] = ((kept >> u) & 1u) ? a1 : -INFINITY;
             }
@@ -761,9 +762,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < 8; ++c) m8[c] = s[c];
 #pragma unroll
-            for (int c = 8; c < 64; ++c) m8[c & 7] = fmaxf(m8[c & 7], s[c]);
+            for (int c = 8; c < 56; c += 16)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) m8[e] = max3(m8[e], s[c + e], s[c + 8 + e]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], s[56 + e]);
           }
-          mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+          mx = fmaxf(max3(max3(m8[0], m8[1], m8[2]), m8[3], m8[4]), max3(m8[5], m8[6], m8[7]));
           float mo;
           ok = exchange(t, mx, &mo);
           if (!ok) break;
@@ -790,14 +795,29 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         for (int u = 0; u < 4; ++u) mu4[u] = !SP || ((kept >> u) & 1u) ? mu : INFINITY;
         {
           float rs4[4] = {0.f, 0.f, 0.f, 0.f};
+          uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};  // sparse mode: sums of the even and of the odd columns
           uint32_t pk[32];
+          const uint64_t sl2x2 = pack_f32x2(sl2, sl2);
+          uint64_t mu2[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mu2[u] = pack_f32x2(-mu4[u], -mu4[u]);
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const float x0 = fmaf(s[2 * c], sl2, -mu4[c >> 3]), x1 = fmaf(s[2 * c + 1], sl2, -mu4[c >> 3]);
+            float x0, x1;
+            unpack_f32x2(fma_f32x2(pack_f32x2(s[2 * c], s[2 * c + 1]), sl2x2, mu2[c >> 3]), x0, x1);
             const float p0 = ex2_approx(x0);
             const float p1 = ex2_approx(x1);
-            rs4[c & 3] += p0 + p1;
+            if constexpr (SP) rs2[c & 3] = add_f32x2(rs2[c & 3], pack_f32x2(p0, p1));
+            else rs4[c & 3] += p0 + p1;
             pk[c] = pack_bf16x2(p0, p1);
+          }
+          if constexpr (SP) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              float a0, a1;
+              unpack_f32x2(rs2[u], a0, a1);
+              rs4[u] = a0 + a1;
+            }
           }
           if (p.split_issue && t >= 2) {  // P V of tile t-2 has read this P buffer
             ok = mbar_wait_warp(p_free(sb), ((t >> 1) - 1) & 1, abort_flag, p.status);
