@@ -52,9 +52,9 @@
 // own pages from the first incomplete one on (struct Span), and the softmax gives the keys of a page that
 // a row's node did not choose an infinite reference, so their weights are 0.  Its floor is the union's K/V,
 // read once; it computes every row against the whole union, so it is bound like the dense kernel, by the
-// softmax pipeline of a CTA (some 1900 cycles per 128 x 128 tile, 14000 of set-up and 6500 of epilogue
+// softmax pipeline of a CTA (some 1750 cycles per 128 x 128 tile, 14000 of set-up and 6500 of epilogue
 // per CTA).  16 sequences x 60 nodes, 64 heads on 8, 128 of 2048 16-token pages per node (unions of 256):
-// 171 us, 0.27 GB of K/V at 1.6 TB/s, 0.77 PFLOP/s over the unions; dense attention takes 167 us over 4096
+// 162 us, 0.27 GB of K/V at 1.7 TB/s, 0.81 PFLOP/s over the unions; dense attention takes 167 us over 4096
 // tokens, as many keys, and 1006 us over the 32768 that were chosen from.
 #include <cuda.h>
 #include <cudaTypedefs.h>
