@@ -488,7 +488,7 @@ int ts_kv_page_bounds(const void* k_cache, ts_dtype dt, int num_blocks, int bloc
  *   node_mask [B, Hkv, C, W] uint64: bit i % 64 of word i / 64 is set iff node i keeps that
  *             page (0 behind the last one)
  * Supported: any d <= 256, m <= 256, Hq / Hkv <= 128, C <= 65536, B * Hkv <= 65535.
- * workspace: ts_page_select_workspace(...) bytes.
+ * workspace: ts_page_select_workspace(...) bytes; it and bounds 16-byte aligned.
  * Device errors: prefix_len outside [0, max_prefix] (count 0, no pages) or a page id out of
  * range (its score is 0) -> TS_ERR_DEVICE_CHECK; a wait over its time bound -> TS_ERR_TIMEOUT.
  * --------------------------------------------------------------------------------- */
@@ -513,7 +513,7 @@ int ts_page_select(const void* q, ts_dtype dt, const void* bounds, int num_block
  * capacity C >= 1; each page at most once).  Other arguments as ts_tree_attention, scale > 0; the same
  * types, head dims and page sizes are supported, and the same two paths serve them.
  * Non-finite values in places that a node does not attend to do not reach its output.
- * workspace: ts_tree_attention_sparse_workspace(...) bytes.
+ * workspace: ts_tree_attention_sparse_workspace(...) bytes, 16-byte aligned (not read where that is 256 or less).
  * Device errors: count outside [0, C], a chosen page outside [0, F), prefix_len negative or
  * beyond max_blocks * block_size - m, or a page id out of range -> TS_ERR_DEVICE_CHECK; a wait
  * over its time bound -> TS_ERR_TIMEOUT.
@@ -555,8 +555,9 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
  * k_cache, v_cache [num_blocks, Hkv, block_size, d] (dt), in/out.  block_table [B, max_blocks],
  * prefix_len [B], refs [num_blocks].  freed [num_freed] int32 (-1 entries skipped; NULL with 0).
  * block_table_out, refs_out: may be block_table, refs.  granted [B] int32: fresh pages taken, or -1.
- * n >= 1, B <= TS_MAX_POOL_ROWS.  Two launches.  workspace: ts_kv_reserve_workspace(...) bytes.
- * Errors: TS_ERR_INVALID also for d * element size not a multiple of 4.
+ * n >= 1, B <= TS_MAX_POOL_ROWS, B * max_blocks < 2^31.  Two launches.
+ * workspace: ts_kv_reserve_workspace(...) bytes, 16-byte aligned.
+ * Errors: TS_ERR_INVALID also for d * element size or a cache's address not a multiple of 4.
  * Device errors: a negative length, L + n > max_blocks * block_size or an entry out of range:
  * TS_ERR_DEVICE_CHECK, the sequence stays as it is and granted is -1; a freed id out of range or
  * of a page without references: TS_ERR_DEVICE_CHECK, skipped.
@@ -599,8 +600,8 @@ int ts_kv_fork(const int32_t* block_table, int max_blocks, const int32_t* prefix
  * k_cache, v_cache [num_blocks, Hkv, block_size, d] (dt) and bounds [num_blocks, Hkv, 2, d] bf16 (NULL
  * to leave out): in/out.  block_table [B, max_blocks], refs [num_blocks].
  * block_table_out, refs_out: may be block_table, refs.  remap [num_blocks] int32, live [1] int32.
- * Two launches.  workspace: ts_kv_compact_workspace(num_blocks) bytes.
- * Errors: TS_ERR_INVALID also for d * element size not a multiple of 4.
+ * Two launches.  workspace: ts_kv_compact_workspace(num_blocks) bytes, 16-byte aligned; bounds likewise aligned.
+ * Errors: TS_ERR_INVALID also for d * element size or a cache's address not a multiple of 4.
  * Device errors: a table entry out of range or naming a free page becomes -1 -> TS_ERR_DEVICE_CHECK.
  */
 size_t ts_kv_compact_workspace(int num_blocks);

@@ -51,6 +51,7 @@ static int check_accept(ts_dtype dt, int B, int m, int V) {
 
 }  // namespace ts
 
+static bool aligned4_ptr(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 static bool aligned16_ptr(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 extern "C" {
@@ -479,8 +480,10 @@ int ts_kv_reserve(void* k_cache, void* v_cache, ts_dtype dt, int num_blocks, int
   if (n <= 0 || num_freed < 0 || (num_freed > 0 && !freed)) return TS_ERR_INVALID;
   if ((d * (dt == TS_BF16 ? 2LL : 4LL)) % 4 != 0) return TS_ERR_INVALID;
   if (B > TS_MAX_POOL_ROWS) return TS_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * max_blocks > INT32_MAX) return TS_ERR_UNSUPPORTED;  // requests are counted in 32 bits
   if (!k_cache || !v_cache || !block_table || !prefix_len || !refs || !block_table_out || !refs_out || !granted || !workspace)
     return TS_ERR_INVALID;
+  if (!aligned4_ptr(k_cache) || !aligned4_ptr(v_cache) || !aligned16_ptr(workspace)) return TS_ERR_INVALID;
   if (ws_bytes < ts::kv_reserve_workspace_bytes(num_blocks, block_size, B, n)) return TS_ERR_WORKSPACE;
   ts::ReserveCall c{k_cache, v_cache, dt, num_blocks, block_size, Hkv, d, block_table, max_blocks, prefix_len, refs, B, n,
                     freed, num_freed, block_table_out, refs_out, granted, workspace, dev_status};
@@ -511,6 +514,7 @@ int ts_kv_compact(void* k_cache, void* v_cache, ts_dtype dt, void* bounds, int n
   if ((d * (dt == TS_BF16 ? 2LL : 4LL)) % 4 != 0) return TS_ERR_INVALID;
   if (!k_cache || !v_cache || !block_table || !refs || !block_table_out || !refs_out || !remap || !live || !workspace)
     return TS_ERR_INVALID;
+  if (!aligned4_ptr(k_cache) || !aligned4_ptr(v_cache) || !aligned16_ptr(workspace)) return TS_ERR_INVALID;
   if (num_blocks > (1 << 28)) return TS_ERR_UNSUPPORTED;
   if (bounds && !aligned16_ptr(bounds)) return TS_ERR_INVALID;
   if (ws_bytes < ts::kv_compact_workspace_bytes(num_blocks)) return TS_ERR_WORKSPACE;

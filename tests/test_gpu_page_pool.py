@@ -248,3 +248,33 @@ def test_overlapping_outputs_are_refused():
         ts.kv_compact(k, k.clone(), both[:2], refs, out=dict(out, remap=_g([0] * 4), live=_g([0])))
     with pytest.raises(ValueError):
         ts.kv_fork(both[:2], L, refs, _g([0, 1]), 2, out=dict(block_table=both[:2], prefix_len=_g([0, 0]), refs=_g([0] * 4)))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_caches_off_the_allocations_alignment(dtype):
+    """fp32 caches at any element move in 4-byte pieces; bf16 ones two bytes off are refused."""
+    lib()
+    rng = np.random.default_rng(4)
+    table, L, refs = _state(rng, 6, 2, 60, 6, 8, 30, pinned=0.1)
+    k, v = _caches(rng, 60, 2, 8, 4, dtype)
+
+    def off(t):
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=dev())
+        flat[1:].copy_(t.reshape(-1).to(dev()))
+        return flat[1:].view(t.shape)
+
+    gk, gv = off(k), off(v)
+    if dtype == torch.bfloat16:
+        with pytest.raises(ts.TreeSpecError):
+            ts.kv_reserve(gk, gv, _g(table), _g(L), _g(refs), 4)
+        with pytest.raises(ts.TreeSpecError):
+            ts.kv_compact(gk, gv, _g(table), _g(refs))
+        return
+    got = ts.kv_reserve(gk, gv, _g(table), _g(L), _g(refs), 4)
+    rk, rv, rt, rr, rg, errors = pool.reserve(_bits(k), _bits(v), table, L, refs, 4)
+    assert not errors
+    np.testing.assert_array_equal(_bits(gk), rk)
+    ts.kv_compact(gk, gv, got["block_table"], got["refs"])
+    *_, (rk, rv) = pool.compact(rt, rr, rk, rv)
+    np.testing.assert_array_equal(_bits(gk), rk)
+    np.testing.assert_array_equal(_bits(gv), rv)

@@ -247,3 +247,32 @@ def test_refusals():
         _run_select(c, table, bounds, q, workspace=torch.empty(16, dtype=torch.uint8, device=dev()))
     with pytest.raises(ValueError):
         _run_select(c, table, bounds, q, out=dict(pages=torch.empty(3, 2, 4, dtype=torch.int32, device=dev())))
+
+
+def _offset(t):
+    """The same contiguous tensor one element off the allocation's alignment."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=dev())
+    flat[1:].copy_(t.reshape(-1).to(dev()))
+    return flat[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_tensors_off_the_allocations_alignment(dtype):
+    lib()
+    rng = np.random.default_rng(9)
+    table, nb = _table(rng, [5, 3])
+    k = _keys(rng, nb, 2, 16, 128, dtype)
+    want = oracle.page_bounds(k, table, [80, 41], [0, 0], np.zeros((nb, 2, 2, 128)))
+    L = torch.tensor([80, 41], dtype=torch.int32, device=dev())
+    out = _offset(torch.zeros(nb, 2, 2, 128, dtype=torch.bfloat16))
+    got = ts.kv_page_bounds(_offset(k), torch.from_numpy(table).to(dev()), L, bounds=out)
+    np.testing.assert_array_equal(got.double().cpu().numpy(), want)
+    c = dict(SELECT[0], dtype=dtype)
+    table, bounds, q = _select_case(c)
+    got = ts.page_select(_offset(q), bounds.to(dev()), torch.from_numpy(table).to(dev()),
+                         torch.tensor(c["L"], dtype=torch.int32, device=dev()), c["n"], block_size=16, max_prefix=300, first=1,
+                         recent=2)
+    _check_select(c, table, bounds, q, got)
+    with pytest.raises(ts.TreeSpecError):   # bounds are copied 16 bytes at a time
+        ts.page_select(q.to(dev()), _offset(bounds), torch.from_numpy(table).to(dev()),
+                       torch.tensor(c["L"], dtype=torch.int32, device=dev()), c["n"], block_size=16, max_prefix=300)

@@ -264,3 +264,23 @@ def test_refusals():
             run(**kw)
     with pytest.raises(ValueError):
         run(table=table.astype(np.int64))
+
+
+def test_fp32_tensors_off_the_allocations_alignment():
+    lib()
+    c = dict(L=[100, 48], m=6, Hq=6, Hkv=2, d=128, bs=16, dtype=F32, n=3)
+    x = _case(12, **c)
+
+    def off(t):
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=dev())
+        flat[1:].copy_(t.reshape(-1).to(dev()))
+        return flat[1:].view(t.shape)
+
+    from oracle.page_select import pack
+    pages, count, words = pack(x[5], 1)
+    t = lambda a: torch.from_numpy(a).to(dev())
+    sel = dict(pages=t(pages), count=t(count), node_mask=t(words.view(np.int64)))
+    mw = np.stack([oracle.mask_to_words(y) for y in x[4]])
+    out, lse = ts.tree_attention_sparse(off(x[0]), off(x[1]), off(x[2]), t(x[3]),
+                                        torch.tensor(c["L"], dtype=torch.int32, device=dev()), t(mw.view(np.int64)), sel)
+    _check(*x[:4], c["L"], *x[4:], out, lse)

@@ -72,9 +72,9 @@ def _reserve(lib, dt=1, nb=4, bs=16, hkv=2, d=128, width=8, B=2, n=8, freed=None
 
 def test_kv_reserve_validation(lib):
     for kw in (dict(dt=5), dict(nb=0), dict(bs=0), dict(hkv=0), dict(d=0), dict(d=3), dict(width=0), dict(B=0), dict(n=0),
-               dict(nfreed=-1), dict(nfreed=1), dict(ptr=None), dict(ws=None)):
+               dict(nfreed=-1), dict(nfreed=1), dict(ptr=None), dict(ws=None), dict(ptr=18), dict(ws=8)):
         assert _reserve(lib, **kw) == INVALID, kw
-    for kw in (dict(B=4097), dict(nb=(1 << 28) + 1)):
+    for kw in (dict(B=4097), dict(nb=(1 << 28) + 1), dict(B=4096, width=1 << 20)):
         assert _reserve(lib, **kw) == UNSUPPORTED, kw
     assert _reserve(lib, wsb=16) == WORKSPACE
     assert lib.ts_kv_reserve_workspace(4, 16, 4097, 8) == 0
@@ -99,7 +99,7 @@ def _compact(lib, dt=1, nb=4, bs=16, hkv=2, d=128, width=8, B=2, bounds=None, pt
 
 def test_kv_compact_validation(lib):
     for kw in (dict(dt=5), dict(nb=0), dict(bs=0), dict(hkv=0), dict(d=0), dict(d=3), dict(width=0), dict(B=0), dict(ptr=None),
-               dict(ws=None), dict(bounds=8)):
+               dict(ws=None), dict(bounds=8), dict(ptr=18), dict(ws=8)):
         assert _compact(lib, **kw) == INVALID, kw
     assert _compact(lib, nb=(1 << 28) + 1) == UNSUPPORTED
     assert _compact(lib, wsb=8) == WORKSPACE
