@@ -488,7 +488,7 @@ int ts_kv_page_bounds(const void* k_cache, ts_dtype dt, int num_blocks, int bloc
  *   node_mask [B, Hkv, C, W] uint64: bit i % 64 of word i / 64 is set iff node i keeps that
  *             page (0 behind the last one)
  * Supported: any d <= 256, m <= 256, Hq / Hkv <= 128, C <= 65536, B * Hkv <= 65535.
- * workspace: ts_page_select_workspace(...) bytes; it and bounds 16-byte aligned.
+ * workspace: ts_page_select_workspace(...) bytes (not read where that is 256 or less); it and bounds 16-byte aligned.
  * Device errors: prefix_len outside [0, max_prefix] (count 0, no pages) or a page id out of
  * range (its score is 0) -> TS_ERR_DEVICE_CHECK; a wait over its time bound -> TS_ERR_TIMEOUT.
  * --------------------------------------------------------------------------------- */

@@ -669,7 +669,7 @@ def page_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor
         dev = q.device
         out = dict(pages=torch.empty((B, Hkv, C), dtype=_I32, device=dev), count=torch.empty((B, Hkv), dtype=_I32, device=dev),
                    node_mask=torch.empty((B, Hkv, C, W), dtype=_I64, device=dev))
-    ws, ws_bytes, keep = _scratch(need, q, workspace)
+    ws, ws_bytes, keep = _scratch(need, q, workspace) if need > 256 else (None, 0, None)
     _check(L.ts_page_select(_arg("q", q, ix, q.dtype, shape), dt, _arg("bounds", bounds, ix, _BF16, (NB, Hkv, 2, d)), NB,
                             block_size, _arg("block_table", block_table, ix, _I32, (B, width)), width,
                             _arg("prefix_len", prefix_len, ix, _I32, (B,)), max_prefix, B, m, Hq, Hkv, d, n_pages, first,

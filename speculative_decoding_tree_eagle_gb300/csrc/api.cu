@@ -394,7 +394,7 @@ static int check_select(int B, int m, int Hq, int Hkv, int d, int max_prefix, in
 size_t ts_page_select_workspace(int B, int m, int Hq, int Hkv, int d, int max_prefix, int block_size) {
   if (check_select(B, m, Hq, Hkv, d, max_prefix, block_size) != TS_OK) return 0;
   const int C = max_prefix / block_size;
-  return ts::page_select_workspace_bytes(B, m, Hkv, C > 0 ? C : 1);
+  return ts::page_select_workspace_bytes(B, m, Hq, Hkv, d, C > 0 ? C : 1);
 }
 
 int ts_page_select(const void* q, ts_dtype dt, const void* bounds, int num_blocks, int block_size,
@@ -409,9 +409,11 @@ int ts_page_select(const void* q, ts_dtype dt, const void* bounds, int num_block
   if (n_pages < 1 || first < 0 || recent < 0 || static_cast<long long>(first) + recent > n_pages) return TS_ERR_INVALID;
   if (static_cast<long long>(max_blocks) * block_size < max_prefix / block_size * static_cast<long long>(block_size))
     return TS_ERR_INVALID;
-  if (!q || !bounds || !block_table || !prefix_len || !pages || !count || !node_mask || !workspace) return TS_ERR_INVALID;
-  if (!aligned16_ptr(bounds) || !aligned16_ptr(workspace)) return TS_ERR_INVALID;
-  if (ws_bytes < ts_page_select_workspace(B, m, Hq, Hkv, d, max_prefix, block_size)) return TS_ERR_WORKSPACE;
+  if (!q || !bounds || !block_table || !prefix_len || !pages || !count || !node_mask) return TS_ERR_INVALID;
+  if (!aligned16_ptr(bounds)) return TS_ERR_INVALID;
+  const size_t need = ts_page_select_workspace(B, m, Hq, Hkv, d, max_prefix, block_size);
+  if (need > 256 && (!workspace || !aligned16_ptr(workspace))) return TS_ERR_INVALID;
+  if (need > 256 && ws_bytes < need) return TS_ERR_WORKSPACE;
   const int sms = ts::device_sm_count();
   if (sms <= 0) return TS_ERR_CUDA;
   ts::SelectCall c{q, dt, bounds, num_blocks, block_size, block_table, max_blocks, prefix_len, max_prefix, B, m, Hq, Hkv, d,

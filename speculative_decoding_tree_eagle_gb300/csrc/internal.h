@@ -141,7 +141,7 @@ struct SelectCall {
   void* workspace;
   int32_t* dev_status;
 };
-size_t page_select_workspace_bytes(int B, int m, int Hkv, int C);
+size_t page_select_workspace_bytes(int B, int m, int Hq, int Hkv, int d, int C);
 int page_select_launch(const SelectCall& c, cudaStream_t stream, int num_sms);
 
 struct SparseCall {

@@ -6,7 +6,7 @@
 // page.  Both sides are eight-bit whole numbers on power-of-two grids (page_grid.cuh), so bf16
 // holds them and the tensor cores' fp32 sums are exact.
 //
-// Three launches:
+// Three launches (one, one_node_kernel, for single nodes of few sequences):
 //   score_kernel   tcgen05: 128 rows (whole nodes, all g heads of each) x 128 pages x 2 d per tile;
 //                  the epilogue takes the maximum over the heads and writes one 32-bit key per
 //                  (node, page) whose unsigned order is the score's (0 for pages kept anyway).
@@ -19,8 +19,7 @@
 // (33.6 MB of bounds, 8.6 GFLOP): score 19.5 us, choose 17 us, pack 5.5 us.  The score kernel's SMs spend half
 // their issue slots and the tensor pipe 24%: copies, queries' rounding (5 us of set-up per CTA) and
 // keys take turns on two row groups that read the same bounds.  The choosers are integer comparisons, 13
-// warps per SM.  For one sequence and one node (8.4 MB) score and choose take 8 and 10.5 us, dependent loads and
-// instruction fetch.
+// warps per SM.
 #include <algorithm>
 #include <type_traits>
 
@@ -671,6 +670,373 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const SelectArgs
   }
 }
 
+// One node per sequence: a cluster of eight CTAs per (sequence, KV head) scores all its pages on the CUDA
+// cores, each key goes straight into the shared memory of the cluster's first CTA, and that one chooses and
+// writes the outputs.  One launch and nothing in the workspace.
+//
+// LPP lanes hold a page's channels, eight each, with the queries' values in registers, G heads (a smaller group
+// repeats its last head, which changes no maximum).  Up to four heads are kept as q+ and q- (two FMA per head and
+// channel); eight as q, the bound picked by its sign (three instructions), to stay within the registers.
+//
+// What bounds it: latency and code that runs once.  8 KV heads of 4 heads, 2048 pages, d = 128 (8.4 MB): 19000
+// cycles of the first CTA, 4000 of them for the queries (each warp rounding all heads by itself: 6000), 6500 for the
+// scores (64 of 152 SMs), 4000 for the bound (bisection: 7400, of 600 each round) and 2500 for the outputs.
+constexpr int kOneCtas = 8, kOneThreads = 512, kOneWarps = kOneThreads / 32;
+constexpr int kOnePages = 8192;                     // keys the first CTA holds
+static_assert(kOnePages / kOneThreads * kOneWarps <= kOneThreads, "a count per warp and step, one per thread");
+constexpr int kOneBins = kOneThreads;
+constexpr int kOneAhead = 2;                        // pages whose bounds a lane has on their way
+
+template <typename T, int LPP, int G>
+__global__ void __cluster_dims__(kOneCtas, 1, 1) __launch_bounds__(kOneThreads, 1) one_node_kernel(const SelectArgs a) {
+  __shared__ uint32_t s_key[kOnePages];
+  __shared__ int s_cnt[kOneThreads];
+  __shared__ int s_part[2][kOneWarps];
+  __shared__ float4 s_q4[G <= 4 ? 2 * G : G][2 * LPP];
+  __shared__ int s_bin[kOneBins];
+  __shared__ uint32_t s_near[32], s_high[2][kOneWarps];
+  __shared__ int s_found[4];
+  auto s_q = reinterpret_cast<float (*)[8 * LPP]>(s_q4);
+  constexpr int PPW = 32 / LPP;  // pages per warp and step
+  constexpr int STEP = kOneCtas * kOneWarps * PPW;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_ctarank()), bh = blockIdx.x / kOneCtas, b = bh / a.Hkv, h = bh % a.Hkv;
+  pdl_wait();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const int32_t* table = a.table + static_cast<long long>(b) * a.max_blocks;
+  const int last = min(a.C, a.max_blocks) - 1;  // the table is read ahead of the length, from a clamped place
+  const int p0 = (rank * kOneWarps + warp) * PPW + lane / LPP;
+  int ids[kOneAhead];
+#pragma unroll
+  for (int u = 0; u < kOneAhead; ++u) ids[u] = load_now(table + min(p0 + u * STEP, last));
+  const int nf = complete_pages(a, b);
+  const int c = lane % LPP;
+  const bool in_d = 8 * c < a.d;
+  const __nv_bfloat16* bounds = a.bounds + static_cast<long long>(h) * 2 * a.d + (in_d ? 8 * c : 0);
+  const long long page_elems = static_cast<long long>(a.Hkv) * 2 * a.d;
+  uint4 hi[kOneAhead], lo[kOneAhead];
+  auto load = [&](int s0) {  // the bounds of pages s0 + p0 + u * STEP, whose ids are held; then the ids after them
+#pragma unroll
+    for (int u = 0; u < kOneAhead; ++u) {
+      hi[u] = lo[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (s0 + p0 + u * STEP < nf) {
+        if (ids[u] >= 0 && ids[u] < a.num_blocks) {
+          const __nv_bfloat16* at = bounds + ids[u] * page_elems;
+          if (in_d) {
+            hi[u] = __ldg(reinterpret_cast<const uint4*>(at));
+            lo[u] = __ldg(reinterpret_cast<const uint4*>(at + a.d));
+          }
+        } else {
+          report(a.status, TS_ERR_DEVICE_CHECK);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kOneAhead; ++u) ids[u] = load_now(table + min(s0 + p0 + (kOneAhead + u) * STEP, last));
+  };
+  load(0);
+
+  // Queries on their grids: a warp per head, for all warps.
+  constexpr bool SPLIT = G <= 4;
+  if (warp < G) {
+    constexpr int E = LPP / 4;  // channels per lane
+    const int d0 = lane * E;
+    const T* q = static_cast<const T*>(a.q) + (static_cast<long long>(b) * a.Hq + h * a.g + min(warp, a.g - 1)) * a.d;
+    float v[E], amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      v[e] = d0 + e < a.d ? grid_clamp(static_cast<float>(q[d0 + e])) : 0.f;
+      amax = fmaxf(amax, fabsf(v[e]));
+    }
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // (not negative)
+    const int e2 = grid_exponent(amax);
+    const float up = pow2(-e2), grid = pow2(e2);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float x = rintf(v[e] * up) * grid;
+      s_q[warp][d0 + e] = SPLIT ? fmaxf(x, 0.f) : x;
+      if constexpr (SPLIT) s_q[G + warp][d0 + e] = fminf(x, 0.f);
+    }
+  }
+  s_bin[tid] = 0;
+  if (tid < 4) s_found[tid] = 0;
+  __syncthreads();
+  uint64_t qp[G][4], qn[SPLIT ? G : 1][4];  // two channels each
+#pragma unroll
+  for (int x = 0; x < G; ++x) {
+    auto fetch = [&](int row, uint64_t (&to)[4]) {
+      const ulonglong2* from = reinterpret_cast<const ulonglong2*>(s_q[row] + 8 * c);
+      const ulonglong2 f = from[0], g = from[1];
+      to[0] = f.x, to[1] = f.y, to[2] = g.x, to[3] = g.y;
+    };
+    fetch(x, qp[x]);
+    if constexpr (SPLIT) fetch(G + x, qn[x]);
+  }
+
+  // ------------------------------------------- keys --------------------------------------------
+  const int head = min(a.first, max(nf, 0)), tail = max(nf - a.recent, head), need = a.n - head - (nf - tail);
+  const bool all = tail - head <= need;
+  const Compete key{head, tail - head};
+  const uint32_t to = dsmem_addr(smem_u32(s_key), 0);
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA runs: its shared memory can be written
+  for (int s0 = 0; s0 < nf; s0 += kOneAhead * STEP) {
+    if (s0 > 0) load(s0);
+#pragma unroll
+    for (int u = 0; u < kOneAhead; ++u) {
+      uint64_t acc2[G];
+#pragma unroll
+      for (int x = 0; x < G; ++x) acc2[x] = 0ull;
+      const uint32_t wh[4] = {hi[u].x, hi[u].y, hi[u].z, hi[u].w}, wl[4] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float h0 = bf16_lo(wh[e]), h1 = bf16_hi(wh[e]), l0 = bf16_lo(wl[e]), l1 = bf16_hi(wl[e]);
+#pragma unroll
+        for (int x = 0; x < G; ++x) {
+          if constexpr (SPLIT) {
+            acc2[x] = fma_f32x2(qn[x][e], pack_f32x2(l0, l1), fma_f32x2(qp[x][e], pack_f32x2(h0, h1), acc2[x]));
+          } else {
+            float q0, q1;
+            unpack_f32x2(qp[x][e], q0, q1);
+            acc2[x] = fma_f32x2(qp[x][e], pack_f32x2(q0 >= 0.f ? h0 : l0, q1 >= 0.f ? h1 : l1), acc2[x]);
+          }
+        }
+      }
+      float acc[G];
+#pragma unroll
+      for (int x = 0; x < G; ++x) {
+        float a0, a1;
+        unpack_f32x2(acc2[x], a0, a1);
+        acc[x] = a0 + a1;
+      }
+      // sums over the page's lanes: the first steps also divide the heads among the lanes
+      int off = LPP / 2;
+#pragma unroll
+      for (int n = G; n > 1; n >>= 1, off >>= 1) {
+        const bool upper = (lane & off) != 0;
+#pragma unroll
+        for (int x = 0; x < n / 2; ++x) {
+          const float send = upper ? acc[x] : acc[x + n / 2], mine = upper ? acc[x + n / 2] : acc[x];
+          acc[x] = mine + __shfl_xor_sync(0xffffffffu, send, off);
+        }
+      }
+      float sum = acc[0];
+#pragma unroll
+      for (int o = LPP / (2 * G); o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+      for (int o = LPP / 2; o >= LPP / G; o >>= 1) sum = fmaxf(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+      const int p = s0 + p0 + u * STEP;
+      if (c == 0 && p < nf) asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + 4u * p), "r"(key(sum, p)) : "memory");
+    }
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  int32_t* pages = a.pages + static_cast<long long>(bh) * a.C;
+  unsigned long long* words = a.node_mask + static_cast<long long>(bh) * a.C;
+  const int kept = nf <= 0 ? 0 : all ? nf : a.n;
+  for (int p = kept + rank * kOneThreads + tid; p < a.C; p += kOneCtas * kOneThreads) {
+    pages[p] = -1;
+    words[p] = 0ull;
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (rank != 0) return;
+
+  // ------------------------------------------ choice -------------------------------------------
+  if (tid == 0) {
+    a.count[bh] = kept;
+    if (nf < 0) report(a.status, TS_ERR_DEVICE_CHECK);
+  }
+  if (nf <= 0) return;
+  // (The loops from here on are not unrolled and read the keys from shared memory: this code runs once, by one CTA,
+  // and what it costs is fetching it.)
+  const int nk = (nf + kOneThreads - 1) / kOneThreads;  // pages tid + 512 j, j < nk
+  auto key_at = [&](int j) -> uint32_t {
+    const int p = tid + kOneThreads * j;
+    return p < nf ? s_key[p] : 0u;
+  };
+  int round = 0;
+  auto sum_up = [&](int v) -> int {  // of all threads, in every thread
+    v = __reduce_add_sync(0xffffffffu, v);
+    if (lane == 0) s_part[round & 1][warp] = v;
+    __syncthreads();
+    const int t = lane < kOneWarps ? s_part[round & 1][lane] : 0;
+    ++round;
+    return __reduce_add_sync(0xffffffffu, t);
+  };
+  auto sum_before = [&](int v) -> int {  // of the threads before this one
+    int at = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += y;
+    }
+    if (lane == 31) s_part[round & 1][warp] = at;
+    __syncthreads();
+    const int t = lane < warp ? s_part[round & 1][lane % kOneWarps] : 0;
+    ++round;
+    return at - v + __reduce_add_sync(0xffffffffu, t);
+  };
+  // Positions of flagged pages (flags bit j: page tid + 512 j) among all flagged ones, in page order.
+  auto count_all = [&](uint32_t flags) {
+    __syncthreads();
+    s_cnt[tid] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int j = 0; j < nk; ++j) {
+      const unsigned m = __ballot_sync(0xffffffffu, (flags >> j) & 1u);
+      if (lane == 0) s_cnt[j * kOneWarps + warp] = __popc(m);
+    }
+    __syncthreads();
+    const int at = sum_before(s_cnt[tid]);
+    s_cnt[tid] = at;
+    __syncthreads();
+  };
+  auto position = [&](int j, uint32_t flags) -> int {  // (every lane of the warp)
+    const unsigned m = __ballot_sync(0xffffffffu, (flags >> j) & 1u);
+    return s_cnt[j * kOneWarps + warp] + __popc(m & ((1u << lane) - 1u));
+  };
+  uint32_t lo_key = 1u, hi_key = 0xFFFFFFFFu, keep = 0u;
+  int cnt = tail - head, above = 0;
+  const bool choose = !all && need > 0;
+  if (choose) {
+    uint32_t low = 0xFFFFFFFFu, high = 0u;
+    auto of_all = [&]() {  // smallest low and largest high
+      low = __reduce_min_sync(0xffffffffu, low);
+      high = __reduce_max_sync(0xffffffffu, high);
+      if (lane == 0) s_part[round & 1][warp] = static_cast<int>(low), s_high[round & 1][warp] = high;
+      __syncthreads();
+      lo_key = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(s_part[round & 1][lane % kOneWarps]));
+      hi_key = __reduce_max_sync(0xffffffffu, s_high[round & 1][lane % kOneWarps]);
+      ++round;
+    };
+#pragma unroll 1
+    for (int j = 0; j < nk; ++j) {
+      const uint32_t k = key_at(j);
+      low = min(low, k - 1u);  // (a key of 0 becomes the largest)
+      high = max(high, k);
+    }
+    of_all();
+    ++lo_key;
+    // invariant: at least `need` keys reach lo_key (cnt of them), fewer than `need` reach hi_key + 1 (above of them)
+    if (lo_key < hi_key && cnt != need) {
+      // The counts of 512 equal ranges of scores find the range that holds the need-th key (rounding keeps the
+      // order), and where at most 32 keys lie in it, those are compared with one another.
+      const float s0 = score_of(lo_key), scale = (kOneBins - 1) / (score_of(hi_key) - s0);
+      auto bin = [&](uint32_t x) { return max(0, min(kOneBins - 1, static_cast<int>((score_of(x) - s0) * scale))); };
+#pragma unroll 1
+      for (int j = 0; j < nk; ++j) {
+        const uint32_t k = key_at(j);
+        if (k != 0u) atomicAdd(s_bin + bin(k), 1);
+      }
+      __syncthreads();
+      const int v = s_bin[kOneBins - 1 - tid];  // the highest range first
+      const int at = sum_before(v);
+      if (at < need && at + v >= need) s_found[0] = kOneBins - 1 - tid, s_found[1] = at, s_found[2] = v, s_found[3] = 0;
+      __syncthreads();
+      const int range = s_found[0], n = s_found[2];
+      above = s_found[1];
+      cnt = above + n;
+      low = 0xFFFFFFFFu, high = 0u;
+#pragma unroll 1
+      for (int j = 0; j < nk; ++j) {
+        const uint32_t k = key_at(j);
+        if (k == 0u || bin(k) != range) continue;
+        low = min(low, k);
+        high = max(high, k);
+        if (n <= 32) s_near[min(atomicAdd(s_found + 3, 1), 31)] = k;
+      }
+      __syncwarp();
+      if (n <= 32) {
+        __syncthreads();
+        // (every warp by itself: the key that fewer than `need` keys exceed and at least `need` reach)
+        const uint32_t x = lane < n ? s_near[lane] : 0u;
+        int more = 0, reach = 0;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          const uint32_t y = s_near[i];
+          more += y > x;
+          reach += y >= x;
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, lane < n && above + more < need && above + reach >= need);
+        const int who = __ffs(m) - 1;
+        lo_key = hi_key = __shfl_sync(0xffffffffu, x, who);
+        cnt = above + __shfl_sync(0xffffffffu, reach, who);
+        above += __shfl_sync(0xffffffffu, more, who);
+      } else {
+        of_all();
+      }
+    }
+#pragma unroll 1
+    for (int step = 0; lo_key < hi_key && cnt != need; ++step) {
+      const uint32_t mid = middle(lo_key, hi_key, step);
+      int v = 0;
+#pragma unroll 1
+      for (int j = 0; j < nk; ++j) v += key_at(j) >= mid;
+      v = sum_up(v);
+      if (v >= need) {
+        lo_key = mid;
+        cnt = v;
+      } else {
+        hi_key = mid - 1u;
+        above = v;
+      }
+    }
+  }
+  uint32_t equal = 0u;  // bit j: page tid + 512 j
+#pragma unroll 1
+  for (int j = 0; j < nk; ++j) {
+    const int p = tid + kOneThreads * j;
+    const uint32_t k = key_at(j);
+    const bool tie = choose && cnt != need && k == lo_key;  // at lo_key == hi_key: only the first of them
+    const bool in = all || p < head || p >= tail || (choose && k >= lo_key);
+    if (p < nf && in && !tie) keep |= 1u << j;
+    if (tie) equal |= 1u << j;
+  }
+  if (choose && cnt != need) {
+    count_all(equal);
+#pragma unroll 1
+    for (int j = 0; j < nk; ++j)
+      if (position(j, equal) < need - above && ((equal >> j) & 1u)) keep |= 1u << j;
+  }
+  count_all(keep);
+#pragma unroll 1
+  for (int j = 0; j < nk; ++j) {
+    const int o = position(j, keep);
+    if ((keep >> j) & 1u) {
+      pages[o] = tid + kOneThreads * j;
+      words[o] = 1ull;
+    }
+  }
+}
+
+template <typename T, int LPP>
+cudaError_t launch_one(const SelectArgs& a, cudaStream_t stream) {
+  const dim3 grid(kOneCtas * a.B * a.Hkv), block(kOneThreads);
+  if (a.g == 1) return launch_pdl(one_node_kernel<T, LPP, 1>, grid, block, 0, stream, a);
+  if (a.g == 2) return launch_pdl(one_node_kernel<T, LPP, 2>, grid, block, 0, stream, a);
+  if (a.g <= 4) return launch_pdl(one_node_kernel<T, LPP, 4>, grid, block, 0, stream, a);
+  return launch_pdl(one_node_kernel<T, LPP, 8>, grid, block, 0, stream, a);
+}
+
+template <typename T>
+cudaError_t launch_one(const SelectArgs& a, cudaStream_t stream) {
+  if (a.d <= 64) return launch_one<T, 8>(a, stream);
+  return a.d <= 128 ? launch_one<T, 16>(a, stream) : launch_one<T, 32>(a, stream);
+}
+
+// Whether one_node_kernel takes the call: while its clusters run at once and a cluster's work is small.  Against the
+// score and choice kernels, d = 128, in us on the device (from Python 20 and 25):
+//   8 clusters of 4 heads: 64 pages 8.5 and 12.4, 2048 pages 12.5 and 18.6; 16 clusters: 12.4 and 12.4, 18.6 and 18.7;
+//   32 clusters: 14.7 and 12.4, 24.8 and 20.7; 8 clusters of 8 heads, 2048 pages: 18.5 and 16.7;
+//   one of 8 heads, 8192 pages: 48 and 27.
+bool one_node(int B, int m, int Hq, int Hkv, int d, int C) {
+  constexpr long long kClusters = 16, kWork = 1 << 20;  // kWork: pages x heads x channels, as the kernel rounds them up
+  const int g = Hq / Hkv, heads = g <= 2 ? g : g <= 4 ? 4 : 8, channels = d <= 64 ? 64 : d <= 128 ? 128 : 256;
+  return m == 1 && d % 8 == 0 && g <= 8 && C <= kOnePages && static_cast<long long>(B) * Hkv <= kClusters &&
+         static_cast<long long>(C) * heads * channels <= kWork;
+}
+
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const SelectArgs a) {
   __shared__ int s_warp[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -747,7 +1113,8 @@ size_t keys_bytes(int B, int m, int Hkv, int C) { return static_cast<size_t>(B) 
 
 }  // namespace
 
-size_t page_select_workspace_bytes(int B, int m, int Hkv, int C) {
+size_t page_select_workspace_bytes(int B, int m, int Hq, int Hkv, int d, int C) {
+  if (one_node(B, m, Hq, Hkv, d, C)) return 256;
   return keys_bytes(B, m, Hkv, C) + static_cast<size_t>(B) * Hkv * C * ((m + 63) / 64) * 8;
 }
 
@@ -782,6 +1149,11 @@ int page_select_launch(const SelectCall& c, cudaStream_t stream, int num_sms) {
   a.q_vec = c.d % 8 == 0 && (reinterpret_cast<uintptr_t>(c.q) & 15u) == 0;
   a.keys = static_cast<uint32_t*>(c.workspace);
   a.dense = reinterpret_cast<unsigned long long*>(static_cast<char*>(c.workspace) + keys_bytes(c.B, c.m, c.Hkv, a.C));
+  if (one_node(c.B, c.m, c.Hq, c.Hkv, c.d, a.C)) {
+    count_launches(1);
+    return (c.dt == TS_BF16 ? launch_one<__nv_bfloat16>(a, stream) : launch_one<float>(a, stream)) == cudaSuccess ? TS_OK
+                                                                                                              : TS_ERR_CUDA;
+  }
   cudaError_t e = c.dt == TS_BF16 ? launch_score<__nv_bfloat16>(a, stream, num_sms) : launch_score<float>(a, stream, num_sms);
   if (e != cudaSuccess) return TS_ERR_CUDA;
   count_launches(1);

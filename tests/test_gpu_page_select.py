@@ -100,6 +100,23 @@ SELECT = [dict(L=[300, 16, 7], m=5, Hq=8, Hkv=2, d=128, bs=16, n=4, first=1, rec
           dict(L=[9000], m=1, Hq=2, Hkv=1, d=8, bs=1, n=1000, first=5, recent=5, dtype=torch.bfloat16)]
 
 
+# one node per sequence: head groups of 1 to 9 (8 is the last that a cluster takes), head dims of 8 to 256 and one not a
+# multiple of 8, rows of up to 8192 pages and one more, empty and short sequences, all pages wanted, 16
+# clusters and 25
+ONE = [dict(L=[2100, 0, 5], m=1, Hq=4, Hkv=4, d=128, bs=1, n=40, first=1, recent=1, dtype=torch.bfloat16),
+       dict(L=[8192, 8191], m=1, Hq=4, Hkv=2, d=8, bs=1, n=1000, first=5, recent=5, dtype=torch.bfloat16),
+       dict(L=[8193], m=1, Hq=4, Hkv=2, d=8, bs=1, n=1000, first=5, recent=5, dtype=torch.bfloat16),
+       dict(L=[513, 1024, 1], m=1, Hq=6, Hkv=2, d=64, bs=1, n=100, first=0, recent=0, dtype=torch.bfloat16),
+       dict(L=[700, 300], m=1, Hq=8, Hkv=2, d=72, bs=2, n=1, first=0, recent=0, dtype=torch.float32),
+       dict(L=[900], m=1, Hq=5, Hkv=1, d=256, bs=3, n=299, first=1, recent=1, dtype=torch.bfloat16),
+       dict(L=[900], m=1, Hq=16, Hkv=2, d=200, bs=3, n=300, first=1, recent=1, dtype=torch.float32),
+       dict(L=[640, 77], m=1, Hq=14, Hkv=2, d=128, bs=16, n=30, first=2, recent=3, dtype=torch.bfloat16),
+       dict(L=[640], m=1, Hq=9, Hkv=1, d=128, bs=16, n=12, first=2, recent=3, dtype=torch.bfloat16),
+       dict(L=[640], m=1, Hq=4, Hkv=2, d=36, bs=4, n=12, first=12, recent=0, dtype=torch.float32),
+       dict(L=[40, 33, 16, 15] * 4, m=1, Hq=2, Hkv=1, d=16, bs=4, n=4, first=0, recent=4, dtype=torch.bfloat16),
+       dict(L=[40, 33, 16, 15, 3] * 5, m=1, Hq=8, Hkv=1, d=16, bs=4, n=4, first=2, recent=1, dtype=torch.bfloat16)]
+
+
 def _select_case(c, seed=0, ties=False):
     rng = np.random.default_rng(seed + c["d"])
     B = len(c["L"])
@@ -139,6 +156,62 @@ def test_choice_matches_the_oracle(c, ties):
     got = _run_select(c, table, bounds, q, status)
     ts.check_status(status)
     _check_select(c, table, bounds, q, got)
+
+
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("c", ONE, ids=lambda c: f"L{c['L'][0]}_{c['Hq']}x{c['Hkv']}_d{c['d']}_{str(c['dtype'])[6:]}")
+def test_choice_of_one_node_matches_the_oracle(c, ties):
+    lib()
+    table, bounds, q = _select_case(c, ties=ties)
+    status = ts.new_status(dev())
+    got = _run_select(c, table, bounds, q, status)
+    ts.check_status(status)
+    _check_select(c, table, bounds, q, got)
+    _check_select(c, table, bounds, q, _run_select(c, table, bounds, _offset(q), status))  # queries off 16 bytes
+
+
+@pytest.mark.parametrize("g", [4, 8])
+@pytest.mark.parametrize("d", [128, 256])
+def test_scores_of_one_node_are_exact_at_their_largest(d, g):
+    """As test_scores_are_exact_at_their_largest, one query per sequence and sign, the group's last head the best."""
+    lib()
+    c = dict(L=[200, 200], m=1, Hq=g, Hkv=1, d=d, bs=1, n=60, first=0, recent=0)
+    rng = np.random.default_rng(4)
+    bounds = np.full((200, 1, 2, d), 255.0)
+    less = rng.permutation(200)
+    for p in range(200):
+        np.subtract.at(bounds[p, 0, 0], rng.integers(0, d, size=less[p]), 1.0)
+    bounds[:, :, 1] = -255.0
+    q = torch.zeros((2, 1, g, d), dtype=torch.bfloat16)
+    q[0, 0, g - 1], q[1, 0, g - 1] = 255.0, -255.0
+    table = np.stack([np.arange(200), rng.permutation(200)]).astype(np.int32)
+    b = torch.from_numpy(bounds).to(torch.bfloat16)
+    status = ts.new_status(dev())
+    got = _run_select(c, table, b, q, status)
+    ts.check_status(status)
+    _check_select(c, table, b, q, got)
+
+
+@pytest.mark.parametrize("L,entry", [(640, 40), (640, -1), (-1, 0), (641, 0)])
+def test_bad_state_of_one_node_is_reported(L, entry):
+    """A table entry out of range (its page scores 0) or a length that is not in 0 .. max_prefix (no pages)."""
+    lib()
+    c = dict(L=[L], m=1, Hq=4, Hkv=2, d=64, bs=16, n=5, first=1, recent=1)
+    rng = np.random.default_rng(5)
+    table = np.arange(40, dtype=np.int32)[None].copy()
+    bounds = torch.from_numpy(rng.integers(1, 200, size=(40, 2, 2, 64)).astype(np.float64)).to(torch.bfloat16)
+    bounds[:, :, 1] = -bounds[:, :, 0]
+    q = torch.from_numpy(rng.standard_normal((1, 1, 4, 64))).to(torch.bfloat16)
+    table[0, 7] = entry if entry else table[0, 7]
+    status = ts.new_status(dev())
+    got = _run_select(c, table, bounds, q, status, max_prefix=640)
+    assert int(status.item()) == -6
+    if L != 640:
+        assert (got["count"] == 0).all() and (got["pages"] == -1).all() and (got["node_mask"] == 0).all()
+    else:
+        table[0, 7], rest = 0, torch.cat([bounds, torch.zeros_like(bounds[:1])])
+        table[0, 7] = 40  # a page of zeros
+        _check_select(c, table, rest, q, got)
 
 
 @pytest.mark.parametrize("d", [128, 256])
