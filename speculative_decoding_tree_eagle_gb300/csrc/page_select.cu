@@ -8,18 +8,18 @@
 //
 // Three launches (one, one_node_kernel, for single nodes of few sequences):
 //   score_kernel   tcgen05: 128 rows (whole nodes, all g heads of each) x 128 pages x 2 d per tile;
-//                  the epilogue takes the maximum over the heads and writes one 32-bit key per
-//                  (node, page) whose unsigned order is the score's (0 for pages kept anyway).
+//                  the epilogue takes the maximum over the heads and writes one fp32 score per
+//                  (node, page), NaN for pages kept anyway.
 //   choose_*       a warp (or, for long rows, a CTA) per (sequence, KV head, node): the n-th largest
-//                  key by bisection with the keys in registers, ties by index; sets the node's bit
+//                  score by bisection with the scores in registers, ties by index; sets the node's bit
 //                  in each kept page's word (an OR, the same in every order).
 //   pack_kernel    a CTA per (sequence, KV head): the pages with any bit, ascending.
 //
 // What bounds it (GB300, ncu): 4 sequences x 8 KV heads, 64 nodes of 4 heads, 2048 pages, d = 128, 128 kept
-// (33.6 MB of bounds, 8.6 GFLOP): score 19.5 us, choose 17 us, pack 5.5 us.  The score kernel's SMs spend half
-// their issue slots and the tensor pipe 24%: copies, queries' rounding (5 us of set-up per CTA) and
-// keys take turns on two row groups that read the same bounds.  The choosers are integer comparisons, 13
-// warps per SM.
+// (33.6 MB of bounds, 8.6 GFLOP): score 19.5 us, choose 14.5 us, pack 5.5 us, 32.6 us one after the
+// other.  The score kernel's SMs spend half their issue slots and the tensor pipe 24%: copies, queries' rounding (5 us
+// of set-up per CTA) and scores take turns on two row groups that read the same bounds.  The choosers are comparisons,
+// 13 warps per SM.
 #include <algorithm>
 #include <type_traits>
 
@@ -49,7 +49,7 @@ struct SelectArgs {
   const __nv_bfloat16* bounds;
   const int32_t* table;
   const int32_t* prefix_len;
-  uint32_t* keys;             // [B, Hkv, m, stride]
+  float* scores;              // [B, Hkv, m, stride], NaN for pages that do not compete
   unsigned long long* dense;  // [B, Hkv, C, W]
   int32_t* pages;
   int32_t* count;
@@ -58,7 +58,7 @@ struct SelectArgs {
   int num_blocks, bs, max_blocks, max_prefix, B, m, Hq, Hkv, g, d, C, W;
   int n, first, recent;
   int nodes_per_tile;
-  int stride;  // keys per row: C rounded up to whole tiles of 128
+  int stride;  // scores per row: C rounded up to whole tiles of 128
   int lg;      // log2 g where shuffles fold the heads, else -1
   bool q_vec;
 };
@@ -75,20 +75,24 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Keys of 32 pages out of a warp's accumulator rows, 2^LG heads per node: each step halves the columns that a
-// lane is responsible for, so a node's lanes end with the maxima of 32 / 2^LG columns each.  Pages that do
-// not compete (they are kept anyway) and those past the last get key 0 (rows of keys are padded to whole
-// tiles).
+constexpr float kLeast = -3.4e38f;  // far below every score
+
+// Pages that compete for places: those kept anyway and those past the last do not, and get NaN for a score, which
+// minima, maxima and comparisons pass over (rows of scores are padded to whole tiles).
 struct Compete {
   int head, n;  // pages head .. head + n - 1
-  __device__ __forceinline__ uint32_t operator()(float s, int p) const {
-    return static_cast<unsigned>(p - head) < static_cast<unsigned>(n) ? key_of(s) : 0u;
+  __device__ __forceinline__ float operator()(float s, int p) const {
+    // (a NaN among the bounds, which ts_kv_page_bounds never writes, makes a page the last choice)
+    return static_cast<unsigned>(p - head) < static_cast<unsigned>(n) ? fmaxf(s, kLeast) : __uint_as_float(0x7FFFFFFFu);
   }
 };
 
+// Scores of 32 pages out of a warp's accumulator rows, 2^LG heads per node: each step halves the columns that a
+// lane is responsible for, so a node's lanes end with the maxima of 32 / 2^LG columns each.
+
 template <int LG>
-__device__ __forceinline__ void fold_out(float (&s)[32], uint32_t* keys, int stride, int r, int rows, const Compete& key,
-                                         int p) {
+__device__ __forceinline__ void fold_out(float (&s)[32], float* scores, int stride, int r, int rows,
+                                         const Compete& compete, int p) {
   constexpr int LEFT = 32 >> LG;
   const int lane = threadIdx.x & 31;
   int col = 0;
@@ -104,16 +108,16 @@ __device__ __forceinline__ void fold_out(float (&s)[32], uint32_t* keys, int str
     col += upper ? H : 0;
   }
   if (r >= rows) return;
-  uint32_t* o = keys + static_cast<long long>(r >> LG) * stride + p + col;
+  float* o = scores + static_cast<long long>(r >> LG) * stride + p + col;
   p += col;
   if constexpr (LEFT >= 4) {
 #pragma unroll
     for (int c = 0; c < LEFT; c += 4)
-      *reinterpret_cast<uint4*>(o + c) =
-          make_uint4(key(s[c], p + c), key(s[c + 1], p + c + 1), key(s[c + 2], p + c + 2), key(s[c + 3], p + c + 3));
+      *reinterpret_cast<float4*>(o + c) = make_float4(compete(s[c], p + c), compete(s[c + 1], p + c + 1),
+                                                      compete(s[c + 2], p + c + 2), compete(s[c + 3], p + c + 3));
   } else {
 #pragma unroll
-    for (int c = 0; c < LEFT; ++c) o[c] = key(s[c], p + c);
+    for (int c = 0; c < LEFT; ++c) o[c] = compete(s[c], p + c);
   }
 }
 
@@ -372,12 +376,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectArg
       fence_proxy_async_smem();
       warp_arrive(a_ready);
     }
-    // --------------------------------------- keys ---------------------------------------
+    // -------------------------------------- scores --------------------------------------
     const int q4 = kw & 3, part = kw >> 2;  // rows 32 q4 .. +31, 32 columns
     const bool mine = 32 * part < NT && q4 * 32 < rows;
     const int forced = min(a.first, max(nf, 0));
-    const Compete key{forced, max(0, nf - a.recent - forced)};
-    uint32_t* keys = a.keys + (static_cast<long long>(bh) * a.m + n0) * a.stride;
+    const Compete compete{forced, max(0, nf - a.recent - forced)};
+    float* scores = a.scores + (static_cast<long long>(bh) * a.m + n0) * a.stride;
     float* s_e = reinterpret_cast<float*>(sptr + C::OFF_E);
     bool ok = true;
     for (int i = 0; i < nt; ++i) {
@@ -400,12 +404,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectArg
         if (mine) {
           const int r = q4 * 32 + lane, p = p0 + 32 * part;
           switch (a.lg) {
-            case 0: fold_out<0>(s, keys, a.stride, r, rows, key, p); break;
-            case 1: fold_out<1>(s, keys, a.stride, r, rows, key, p); break;
-            case 2: fold_out<2>(s, keys, a.stride, r, rows, key, p); break;
-            case 3: fold_out<3>(s, keys, a.stride, r, rows, key, p); break;
-            case 4: fold_out<4>(s, keys, a.stride, r, rows, key, p); break;
-            default: fold_out<5>(s, keys, a.stride, r, rows, key, p); break;
+            case 0: fold_out<0>(s, scores, a.stride, r, rows, compete, p); break;
+            case 1: fold_out<1>(s, scores, a.stride, r, rows, compete, p); break;
+            case 2: fold_out<2>(s, scores, a.stride, r, rows, compete, p); break;
+            case 3: fold_out<3>(s, scores, a.stride, r, rows, compete, p); break;
+            case 4: fold_out<4>(s, scores, a.stride, r, rows, compete, p); break;
+            default: fold_out<5>(s, scores, a.stride, r, rows, compete, p); break;
           }
         }
       } else {
@@ -423,7 +427,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectArg
             float best = v[0];
             for (int y = 1; y < a.g; ++y) best = fmaxf(best, v[y * 33]);
             const int p = p0 + 32 * (2 * cg + hb) + c;
-            keys[static_cast<long long>(node) * a.stride + p] = key(best, p);
+            scores[static_cast<long long>(node) * a.stride + p] = compete(best, p);
           }
           asm volatile("bar.sync 1, %0;" ::"n"(kKeyThreads) : "memory");
         }
@@ -438,9 +442,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_kernel(const SelectArg
   }
 }
 
-// What a chooser needs of its row: forced pages have no key of their own.
+// What a chooser needs of its row.
 struct Row {
-  const uint32_t* keys;
+  const float* scores;
   unsigned long long* dense;  // word of this node for page 0, W apart
   unsigned long long bit;
   int nf, head, tail, need;   // pages [head, tail) compete for `need` places
@@ -450,7 +454,7 @@ __device__ __forceinline__ Row row_of(const SelectArgs& a, long long row) {
   Row r;
   const int bh = static_cast<int>(row / a.m), node = static_cast<int>(row % a.m);
   r.nf = complete_pages(a, bh / a.Hkv);
-  r.keys = a.keys + row * a.stride;
+  r.scores = a.scores + row * a.stride;
   r.dense = a.dense + static_cast<long long>(bh) * a.C * a.W + (node >> 6);
   r.bit = 1ull << (node & 63);
   r.head = min(a.first, max(r.nf, 0));
@@ -470,10 +474,21 @@ __device__ __forceinline__ uint32_t middle(uint32_t lo, uint32_t hi, int round) 
   return max(lo + 1u, min(hi, mid));
 }
 
-// A warp per node, the row's keys in registers (4 consecutive pages per lane and step, KPT in all):
-// bisection between the smallest and the largest key until exactly `need` keys reach the bound (about
-// a dozen rounds of KPT comparisons, no barrier).  Bound by issue slots.  ONE (m = 1): what the node
-// keeps is the union, so the warp writes the outputs itself.
+// n + 1 if x >= bound, else n: a comparison and a predicated addition.
+__device__ __forceinline__ void count_from(float& n, float x, float bound) {
+  asm("{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %1, %2;\n\t@p add.f32 %0, %0, 0f3F800000;\n\t}" : "+f"(n) : "f"(x), "f"(bound));
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {  // (a NaN operand is ignored)
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// A warp per node, the row's scores in registers (4 consecutive pages per lane and step, KPT in all):
+// bisection between the smallest and the largest score until exactly `need` scores reach the bound (about
+// a dozen rounds of KPT comparisons, no barrier).  The bounds tried are keys, the scores stay floats: a comparison
+// and a predicated addition, two instructions on different pipes (integer keys: 17 us where this takes 14.5).  Bound
+// by issue slots.  ONE (m = 1): what the node keeps is the union, so the warp writes the outputs itself.
 template <int KPT, bool ONE>
 __global__ void __launch_bounds__(kChooseWarpThreads) choose_warp_kernel(const SelectArgs a, long long rows) {
   const int lane = threadIdx.x & 31;
@@ -485,38 +500,37 @@ __global__ void __launch_bounds__(kChooseWarpThreads) choose_warp_kernel(const S
   if (!ONE && r.nf <= 0) return;
   auto page = [&](int j) { return (j / 4 * 32 + lane) * 4 + (j & 3); };
   const bool all = r.tail - r.head <= r.need;
-  unsigned long long mine = 0ull;  // bit j: page(j) is kept
-#pragma unroll 1
-  for (int s = 0; s < KPT / 4; ++s) {  // those kept without a comparison
-    const int p0 = page(4 * s);
-    auto below = [&](int x) { return (1u << max(0, min(4, x - p0))) - 1u; };
-    const unsigned four = below(r.nf) & ~(all ? 0u : below(r.tail) & ~below(r.head));
-    mine |= static_cast<unsigned long long>(four) << (4 * s);
-  }
-  if (!all && r.need > 0) {
-    uint32_t k[KPT], lo = 0xFFFFFFFFu, hi = 0u;
+  // bit j: page(j) is kept; at first all complete pages
+  const int steps = max(r.nf, 0) / 128, part = max(0, min(4, r.nf - 128 * steps - 4 * lane));
+  unsigned long long mine = steps >= KPT / 4 ? ~0ull >> (64 - KPT)
+                                             : ((1ull << part) - 1ull) << (4 * steps) | ((1ull << (4 * steps)) - 1ull);
+  if (!all) {
+    const float nan = __uint_as_float(0x7FFFFFFFu);
+    float k[KPT], low = nan, high = nan;
 #pragma unroll
     for (int j = 0; j < KPT; j += 4) {
       const int p = page(j);
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (p < r.nf) w = __ldg(reinterpret_cast<const uint4*>(r.keys + p));  // (0 for pages that do not compete)
+      float4 w = make_float4(nan, nan, nan, nan);
+      if (p < r.nf) w = __ldg(reinterpret_cast<const float4*>(r.scores + p));
       k[j] = w.x, k[j + 1] = w.y, k[j + 2] = w.z, k[j + 3] = w.w;
     }
 #pragma unroll
-    for (int j = 0; j < KPT; ++j) {
-      lo = min(lo, k[j] - 1u);  // (a key of 0 becomes the largest)
-      hi = max(hi, k[j]);
+    for (int j = 0; j < KPT; j += 2) {
+      low = min3(low, k[j], k[j + 1]);
+      high = max3(high, k[j], k[j + 1]);
     }
-    lo = __reduce_min_sync(0xffffffffu, lo) + 1u;
-    hi = __reduce_max_sync(0xffffffffu, hi);
+    // (a lane may have none)
+    uint32_t lo = __reduce_min_sync(0xffffffffu, isnan(low) ? 0xFFFFFFFFu : key_of(low));
+    uint32_t hi = __reduce_max_sync(0xffffffffu, isnan(high) ? 0u : key_of(high));
     // invariant: at least `need` keys reach lo (cnt of them), fewer than `need` reach hi + 1 (above of them)
     int cnt = r.tail - r.head, above = 0;
-    for (int round = 0; lo < hi && cnt != r.need; ++round) {
+    for (int round = 0; lo < hi && cnt != r.need && r.need > 0; ++round) {
       const uint32_t mid = middle(lo, hi, round);
-      int c[4] = {0, 0, 0, 0};
+      const float bound = score_of(mid);
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < KPT; ++j) c[j & 3] += k[j] >= mid;
-      const int n = __reduce_add_sync(0xffffffffu, (c[0] + c[1]) + (c[2] + c[3]));
+      for (int j = 0; j < KPT; ++j) count_from(c[j & 3], k[j], bound);
+      const int n = __reduce_add_sync(0xffffffffu, static_cast<int>((c[0] + c[1]) + (c[2] + c[3])));
       if (n >= r.need) {
         lo = mid;
         cnt = n;
@@ -525,15 +539,17 @@ __global__ void __launch_bounds__(kChooseWarpThreads) choose_warp_kernel(const S
         above = n;
       }
     }
+    // those kept without a comparison have NaN and are not below the bound either
+    const float bound = r.need > 0 ? score_of(lo) : INFINITY;
     unsigned long long reach = 0ull;
 #pragma unroll
     for (int j = 0; j < KPT; ++j)
-      if (k[j] >= lo) reach |= 1ull << j;
-    if (cnt != r.need) {  // ties at lo == hi: of the keys equal to it only the first
+      if (!(k[j] < bound)) reach |= 1ull << j;
+    if (r.need > 0 && cnt != r.need) {  // ties at lo == hi: of the keys equal to it only the first
       unsigned long long eq = 0ull;
 #pragma unroll
       for (int j = 0; j < KPT; ++j)
-        if (k[j] == lo) eq |= 1ull << j;
+        if (k[j] == bound) eq |= 1ull << j;
       reach &= ~eq;
       int left = r.need - above;
 #pragma unroll 1
@@ -553,7 +569,7 @@ __global__ void __launch_bounds__(kChooseWarpThreads) choose_warp_kernel(const S
         left -= sum;
       }
     }
-    mine |= reach;
+    mine &= reach;
   }
   if constexpr (!ONE) {
     while (mine != 0ull) {
@@ -609,7 +625,7 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const SelectArgs
 #pragma unroll
     for (int j = 0; j < KPT; ++j) {
       const int p = r.head + tid + kChooseThreads * j;
-      k[j] = p < r.tail ? __ldg(r.keys + p) : 0u;  // below every key
+      k[j] = p < r.tail ? key_of(__ldg(r.scores + p)) : 0u;  // below every key
     }
   }
   int round = 0;
@@ -629,11 +645,11 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const SelectArgs
 #pragma unroll
       for (int j = 0; j < KPT; ++j) c += k[j] >= x;
     } else {
-      for (int p = r.head + tid; p < r.tail; p += kChooseThreads) c += __ldg(r.keys + p) >= x;
+      for (int p = r.head + tid; p < r.tail; p += kChooseThreads) c += key_of(__ldg(r.scores + p)) >= x;
     }
     return sum_up(c);
   };
-  uint32_t lo = key_of(-3.4e38f), hi = key_of(3.4e38f);  // (scores are far below)
+  uint32_t lo = key_of(kLeast), hi = key_of(-kLeast);
   int cnt = r.tail - r.head;
   for (int step = 0; lo < hi && cnt != r.need; ++step) {
     const uint32_t mid = middle(lo, hi, step + 20);
@@ -649,7 +665,7 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(const SelectArgs
   int left = cnt == r.need ? cnt : r.need - at_least(lo + 1u);
   for (int p0 = r.head; p0 < r.tail; p0 += kChooseThreads) {
     const int p = p0 + tid;
-    const uint32_t key = p < r.tail ? __ldg(r.keys + p) : 0u;
+    const uint32_t key = p < r.tail ? key_of(__ldg(r.scores + p)) : 0u;
     if (cnt == r.need) {
       if (key >= lo) keep(p);
       continue;
@@ -776,7 +792,6 @@ __global__ void __cluster_dims__(kOneCtas, 1, 1) __launch_bounds__(kOneThreads, 
   // ------------------------------------------- keys --------------------------------------------
   const int head = min(a.first, max(nf, 0)), tail = max(nf - a.recent, head), need = a.n - head - (nf - tail);
   const bool all = tail - head <= need;
-  const Compete key{head, tail - head};
   const uint32_t to = dsmem_addr(smem_u32(s_key), 0);
   __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA runs: its shared memory can be written
@@ -826,7 +841,7 @@ __global__ void __cluster_dims__(kOneCtas, 1, 1) __launch_bounds__(kOneThreads, 
 #pragma unroll
       for (int o = LPP / 2; o >= LPP / G; o >>= 1) sum = fmaxf(sum, __shfl_xor_sync(0xffffffffu, sum, o));
       const int p = s0 + p0 + u * STEP;
-      if (c == 0 && p < nf) asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + 4u * p), "r"(key(sum, p)) : "memory");
+      if (c == 0 && p < nf) asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + 4u * p), "r"(p >= head && p < tail ? key_of(fmaxf(sum, kLeast)) : 0u) : "memory");
     }
   }
   __syncwarp();
@@ -1107,15 +1122,15 @@ cudaError_t launch_score(const SelectArgs& a, cudaStream_t stream, int num_sms) 
   return a.d <= 128 ? launch_score<T, 2, 128>(a, stream, num_sms) : launch_score<T, 4, 64>(a, stream, num_sms);
 }
 
-int key_stride(int C) { return (C + 127) / 128 * 128; }
+int score_stride(int C) { return (C + 127) / 128 * 128; }
 
-size_t keys_bytes(int B, int m, int Hkv, int C) { return static_cast<size_t>(B) * Hkv * m * key_stride(C) * 4; }
+size_t scores_bytes(int B, int m, int Hkv, int C) { return static_cast<size_t>(B) * Hkv * m * score_stride(C) * 4; }
 
 }  // namespace
 
 size_t page_select_workspace_bytes(int B, int m, int Hq, int Hkv, int d, int C) {
   if (one_node(B, m, Hq, Hkv, d, C)) return 256;
-  return keys_bytes(B, m, Hkv, C) + static_cast<size_t>(B) * Hkv * C * ((m + 63) / 64) * 8;
+  return scores_bytes(B, m, Hkv, C) + static_cast<size_t>(B) * Hkv * C * ((m + 63) / 64) * 8;
 }
 
 int page_select_launch(const SelectCall& c, cudaStream_t stream, int num_sms) {
@@ -1144,11 +1159,11 @@ int page_select_launch(const SelectCall& c, cudaStream_t stream, int num_sms) {
   a.first = c.first;
   a.recent = c.recent;
   a.nodes_per_tile = kRows / a.g;
-  a.stride = key_stride(a.C);
+  a.stride = score_stride(a.C);
   a.lg = fold_by_shuffles(a.g) ? 31 - __builtin_clz(static_cast<unsigned>(a.g)) : -1;
   a.q_vec = c.d % 8 == 0 && (reinterpret_cast<uintptr_t>(c.q) & 15u) == 0;
-  a.keys = static_cast<uint32_t*>(c.workspace);
-  a.dense = reinterpret_cast<unsigned long long*>(static_cast<char*>(c.workspace) + keys_bytes(c.B, c.m, c.Hkv, a.C));
+  a.scores = static_cast<float*>(c.workspace);
+  a.dense = reinterpret_cast<unsigned long long*>(static_cast<char*>(c.workspace) + scores_bytes(c.B, c.m, c.Hkv, a.C));
   if (one_node(c.B, c.m, c.Hq, c.Hkv, c.d, a.C)) {
     count_launches(1);
     return (c.dt == TS_BF16 ? launch_one<__nv_bfloat16>(a, stream) : launch_one<float>(a, stream)) == cudaSuccess ? TS_OK
