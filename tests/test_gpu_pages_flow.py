@@ -181,10 +181,11 @@ def _same(a, b):
                for x, y in zip(a, b))
 
 
-def test_captured_and_replayed_with_new_inputs():
+@pytest.mark.parametrize("m", [5, 1])
+def test_captured_and_replayed_with_new_inputs(m):
     """The whole step in a graph: replays on other inputs give what eager calls give on them."""
     lib()
-    states = [_step_state(s) for s in (1, 2, 3)]
+    states = [_step_state(s, m=m) for s in (1, 2, 3)]
     want = [[x.clone() for x in _step(_copy(s))] for s in states]
     held = _copy(states[0])
     side = torch.cuda.Stream()
@@ -208,9 +209,10 @@ def _copy(s):
     return {n: t.clone() if torch.is_tensor(t) else t for n, t in s.items()}
 
 
-def test_two_graphs_and_two_streams_share_nothing():
+@pytest.mark.parametrize("m", [5, 1])
+def test_two_graphs_and_two_streams_share_nothing(m):
     lib()
-    states = [_step_state(s, L=L) for s, L in ((4, (200, 37, 129)), (5, (16, 255, 90)))]
+    states = [_step_state(s, m=m, L=L) for s, L in ((4, (200, 37, 129)), (5, (16, 255, 90)))]
     want = [[x.clone() for x in _step(_copy(s))] for s in states]
     torch.cuda.synchronize()
     graphs, got, held = [], [], [_copy(s) for s in states]
