@@ -389,11 +389,6 @@ def _plain_reserve(st):
     rank = need.flatten().cumsum(0).view_as(need) - 1
     free = (refs == 0).nonzero().flatten()
     short = (need & (rank >= free.numel())).any(1)
-    # who was to keep a page because the holders before it would take copies, but those found no room
-    row = torch.arange(B, device="cuda")
-    stop = torch.where(short, row, B).amin()
-    left = ((tail[:, None] == tail[None, :]) & (tail >= 0) & (row < stop)).sum(1)
-    short |= (tail >= 0) & (row > stop) & (refs[tail.clamp(min=0)] - left > 1)
     take = need & ~short[:, None]
     fresh = free[rank[take]]
     rows, cols = take.nonzero(as_tuple=True)
