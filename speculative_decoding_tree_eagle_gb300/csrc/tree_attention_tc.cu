@@ -228,8 +228,8 @@ __device__ __noinline__ void repair_row(const Params& p, const __nv_bfloat16* kc
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
     dot *= p.scale_log2;
-    const float m2 = fmaxf(M, dot);
-    if (m2 == -INFINITY) continue;
+    const float m2 = fmaxf(M, dot);  // (a NaN is not the larger one, but makes w, and with it l and acc, NaN for good)
+    if (M == -INFINITY && dot == -INFINITY) continue;
     const float c = exp2f(M - m2), w = exp2f(dot - m2);
     l = l * c + w;
     acc.x = acc.x * c + w * x.x;

@@ -284,3 +284,47 @@ def test_fp32_tensors_off_the_allocations_alignment():
     out, lse = ts.tree_attention_sparse(off(x[0]), off(x[1]), off(x[2]), t(x[3]),
                                         torch.tensor(c["L"], dtype=torch.int32, device=dev()), t(mw.view(np.int64)), sel)
     _check(*x[:4], c["L"], *x[4:], out, lse)
+
+
+def _tolerance(q, k, L, ref, spread):
+    """The tolerance of the outputs (see the top) for finite q and k."""
+    if q.dtype == torch.bfloat16 and q.shape[-1] == 128:
+        return 2.0 ** -8 * (spread + np.abs(ref)) + 2.0 ** -12 * spread
+    X = float(q.double().norm(dim=-1).max() * k.double().norm(dim=-1).max()) / math.sqrt(q.shape[-1])
+    tol = (2 * (max(L) + q.shape[1]) + 40 * X + 16) * 2.0 ** -24 * spread
+    return tol + 2.0 ** -8 * np.abs(ref) if q.dtype == torch.bfloat16 else tol
+
+
+def _check_attended_nan(c, where):
+    """A NaN among the scores of the keys that a row attends to makes its output and sum NaN, wherever it stands; the
+    other rows are as without it."""
+    q, k, v, table, mask, kept = _case(13, **c)
+    q2, k2 = q.clone(), k.clone()
+    B, m, Hq, d = q.shape
+    g = Hq // k.shape[1]
+    hit = np.zeros((B, m, Hq), dtype=bool)
+    if where == "query":                                   # every score of one row
+        q2[0, m // 2, 1, 3] = float("nan")
+        hit[0, m // 2, 1] = True
+    else:                                                  # one page that nodes of the first sequence keep
+        pages = np.nonzero(kept[0, 0].any(0))[0]
+        page = pages[0] if where == "first_key" else pages[len(pages) // 2]
+        rows = slice(0, 1) if where == "first_key" else slice(None)
+        k2[table[0, page], 0, rows] = float("nan")
+        hit[0, :, :g] = kept[0, 0, :, page, None]
+    out, lse = _run(q2, k2, v, table, c["L"], mask, kept)
+    ref, rl, spread = oracle.tree_attention_sparse(q, k, v, table, c["L"], mask, kept, 1 / math.sqrt(d))
+    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert hit.any()
+    assert np.isnan(got[hit]).all() and np.isnan(gl[hit]).all()
+    assert (np.abs(got - ref) <= _tolerance(q, k, c["L"], ref, spread))[~hit].all()
+    assert np.isfinite(gl[~hit]).all()
+
+
+@pytest.mark.parametrize("where", ["query", "page", "first_key"])
+@pytest.mark.parametrize("split", ["direct", "cluster:4", "global:3"])
+@pytest.mark.parametrize("c", [CASES[0], CASES[2], CASES[7], dict(CASES[7], m=1)], ids=_id)
+def test_nan_scores_on_the_tensor_cores(c, split, where, monkeypatch):
+    lib()
+    monkeypatch.setenv("TREESPEC_ATTN_SPLIT", split)
+    _check_attended_nan(c, where)
