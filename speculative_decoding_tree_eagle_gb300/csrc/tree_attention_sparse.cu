@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_simt_kernel(const SparseCa
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     top = fmaxf(top, my_m);
     const bool none = top == -INFINITY;
-    const float p = none || my_row < 0 ? 0.f : expf(s - top);
+    // (the maxima pass over a NaN score, so one is told from no key by the score itself: it makes the sum NaN)
+    const float p = s == -INFINITY ? 0.f : expf(s - top);
     const float corr = none ? 1.f : expf(my_m - top);
     float sum = p + __shfl_xor_sync(0xffffffffu, p, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);

@@ -328,3 +328,11 @@ def test_nan_scores_on_the_tensor_cores(c, split, where, monkeypatch):
     lib()
     monkeypatch.setenv("TREESPEC_ATTN_SPLIT", split)
     _check_attended_nan(c, where)
+
+
+@pytest.mark.parametrize("where", ["query", "page", "first_key"])
+@pytest.mark.parametrize("c", [CASES[9], CASES[10], CASES[11], CASES[12], CASES[13], dict(CASES[13], Hq=2)], ids=_id)
+def test_nan_scores_on_the_cuda_cores(c, where):
+    """Few nodes are spread over clusters of up to eight CTAs, whose warps may then have no other key than NaN ones."""
+    lib()
+    _check_attended_nan(c, where)
