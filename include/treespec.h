@@ -514,9 +514,10 @@ int ts_page_select(const void* q, ts_dtype dt, const void* bounds, int num_block
  * types, head dims and page sizes are supported, and the same two paths serve them.
  * Non-finite values in places that a node does not attend to do not reach its output.
  * workspace: ts_tree_attention_sparse_workspace(...) bytes, 16-byte aligned (not read where that is 256 or less).
- * Device errors: count outside [0, C], a chosen page outside [0, F), prefix_len negative or
- * beyond max_blocks * block_size - m, or a page id out of range -> TS_ERR_DEVICE_CHECK; a wait
- * over its time bound -> TS_ERR_TIMEOUT.
+ * Device errors, TS_ERR_DEVICE_CHECK: a count outside [0, C] or a prefix_len negative or beyond
+ * max_blocks * block_size - m (the rows of that KV head or sequence are not written), a chosen page
+ * outside [0, F) or a page id out of range (its keys are left out); a wait over its time bound ->
+ * TS_ERR_TIMEOUT.
  * --------------------------------------------------------------------------------- */
 size_t ts_tree_attention_sparse_workspace(ts_dtype dt, int B, int m, int Hq, int Hkv, int d, int C,
                                           int block_size);

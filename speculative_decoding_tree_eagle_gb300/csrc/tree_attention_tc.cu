@@ -700,16 +700,19 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       };
       // Sparse mode: the page-major node words are turned into node-major bits, 32 groups of 16 keys at a
       // time: lane = group, one ballot per node.  1 from the incomplete page on (the general visibility
-      // test takes over there).  The softmax warps do it while the first K tile is on its way.
+      // test takes over there), 0 for a page without an id.  The softmax warps do it while the first K tile is on
+      // its way.
       if constexpr (SP) {
         const int nodes = (R0 + rows_here - 1) / p.g - node0 + 1;
         const int words = (nt * (BN / 16) + 31) / 32;
         for (int w = sm_index; w < words; w += 2 * nact) {
           uint64_t x = w == sm_index ? first_word : node_word(w, node0 >> 6);
+          const int box = (32 * w + lane) * 16 / rpb;  // (reported above; its keys read as zeros and get no weight)
+          const bool there = box < nt * bpt && s_blk[box] < p.num_blocks;
           for (int j = 0; j < nodes; ++j) {
             const int n = node0 + j;
             if (j > 0 && (n & 63) == 0) x = node_word(w, n >> 6);
-            const uint32_t bits = __ballot_sync(0xffffffffu, (x >> (n & 63)) & 1ull);
+            const uint32_t bits = __ballot_sync(0xffffffffu, there && ((x >> (n & 63)) & 1ull));
             if (lane == (j & 31)) s_bits[j * p.bit_words + w] = bits;
           }
         }

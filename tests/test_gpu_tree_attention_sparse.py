@@ -336,3 +336,50 @@ def test_nan_scores_on_the_cuda_cores(c, where):
     """Few nodes are spread over clusters of up to eight CTAs, whose warps may then have no other key than NaN ones."""
     lib()
     _check_attended_nan(c, where)
+
+
+@pytest.mark.parametrize("split", ["direct", "cluster:4", "global:3"])
+@pytest.mark.parametrize("case", ["page", "page_low", "entry", "tail", "tree"])
+@pytest.mark.parametrize("dtype,bs", [(BF, 16), (BF, 32), (BF, 128), (F32, 16)])
+def test_keys_of_a_page_without_an_id_are_left_out(dtype, bs, case, split, monkeypatch):
+    """A chosen page that the prefix does not complete, or a table entry out of range, is reported, and the rows of
+    the same sequence attend to their other keys."""
+    lib()
+    monkeypatch.setenv("TREESPEC_ATTN_SPLIT", split)
+    L, m = [6 * bs + 5, 4 * bs], 5 if case != "tree" else bs + 3
+    q, k, v, table, mask, kept = _case(14, L=L, m=m, Hq=4, Hkv=2, d=128, bs=bs, dtype=dtype, n=3)
+    from oracle.page_select import pack
+    pages, count, words = pack(kept, (m + 63) // 64)
+    B, Hkv, nb = 2, 2, k.shape[0]
+    # the same state as pages of one token: kept1 over the prefix, the mask over the tree
+    longest = max(L)
+    flat = [x.permute(0, 2, 1, 3).reshape(nb * bs, Hkv, 1, 128) for x in (k, v)]
+    ids = (np.maximum(table, 0)[:, :, None] * bs + np.arange(bs)).reshape(B, -1)
+    kept1 = np.zeros((B, Hkv, m, longest), dtype=bool)
+    for b in range(B):
+        nf = L[b] // bs
+        kept1[b, :, :, :nf * bs] = np.repeat(kept[b, :, :, :nf], bs, 2)
+        kept1[b, :, :, nf * bs:L[b]] = True
+    mask1 = mask.copy()
+    page = int(pages[0, 0, 1])
+    if case in ("page", "page_low"):
+        pages[0, 0, 1] = 6 if case == "page" else -1
+        kept1[0, 0, :, page * bs:(page + 1) * bs] = False
+    else:
+        at = page if case == "entry" else 6 if case == "tail" else 7
+        table[0, at] = nb if case != "tree" else -1
+        kept1[0, :, :, at * bs:(at + 1) * bs] = False
+        lost = np.arange(at * bs, (at + 1) * bs) - L[0]
+        mask1[0][:, lost[(lost >= 0) & (lost < m)]] = False
+    mw = np.stack([oracle.mask_to_words(x) for x in mask])
+    t = lambda x: torch.from_numpy(x).to(dev())
+    status = ts.new_status(dev())
+    out, lse = ts.tree_attention_sparse(q.to(dev()), k.to(dev()), v.to(dev()), t(table),
+                                        torch.tensor(L, dtype=torch.int32, device=dev()), t(mw.view(np.int64)),
+                                        dict(pages=t(pages), count=t(count), node_mask=t(words.view(np.int64))), status=status)
+    assert int(status.item()) == -6
+    ref, rl, spread = oracle.tree_attention_sparse(q, *flat, ids, L, mask1, kept1, 1 / math.sqrt(128))
+    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert (np.abs(got - ref) <= _tolerance(q, k, L, ref, spread)).all()
+    X = float(q.double().norm(dim=-1).max() * k.double().norm(dim=-1).max()) / math.sqrt(128)
+    assert (np.abs(gl - rl) <= (128 * X + 4 * (np.abs(rl) + longest + m)) * 2.0 ** -24).all()
