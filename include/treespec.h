@@ -532,8 +532,9 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
  * The page pool.  refs [num_blocks] int32 counts, for each page, the block-table entries that
  * name it plus whatever else the caller counts there; 0 = free.  Each call reads the state it is
  * given (block_table, prefix_len, refs) and writes the new state to its outputs; where the text
- * says so an output may be the very buffer of its input (partial overlap is not allowed).  All
- * results are whole numbers that do not depend on the order of execution.
+ * says so an output may be the very buffer of its input.  Any other overlap of an output (or the
+ * workspace) with an input or another output returns TS_ERR_INVALID.  All results are whole numbers
+ * that do not depend on the order of execution.
  * ts_kv_commit lists what a verify step lets go of; pass that list to the next ts_kv_reserve (until then those
  * pages count as in use).
  * --------------------------------------------------------------------------------- */

@@ -29,7 +29,7 @@ import ctypes
 import math
 import os
 import threading
-from typing import Dict, List, Optional
+from typing import Dict, List, Optional, Tuple
 
 import torch
 
@@ -608,12 +608,19 @@ def _scratch(nbytes: int, like: torch.Tensor, ws: Optional[torch.Tensor]):
     return ws.data_ptr(), size, ws
 
 
-def _apart(out: torch.Tensor, t: torch.Tensor, may_be_same: bool) -> None:
-    """Refuse an output that shares memory with its input, unless it is the very same buffer and may be."""
-    a0, b0 = out.data_ptr(), t.data_ptr()
-    a1, b1 = a0 + out.numel() * out.element_size(), b0 + t.numel() * t.element_size()
-    if a0 < b1 and b0 < a1 and not (may_be_same and a0 == b0 and a1 == b1):
-        raise ValueError("an output must lie apart from the inputs" + (" or be its input's buffer" if may_be_same else ""))
+def _apart(out: Dict[str, torch.Tensor], may_be_same: Tuple[str, ...], **inputs: Optional[torch.Tensor]) -> None:
+    """Refuse outputs that share memory with an input or with one another; those named in ``may_be_same`` may be the
+    very buffer of the input of their name."""
+    def memory(t):
+        at = t.data_ptr()
+        return at, at + t.numel() * t.element_size()
+
+    outs = [(f"out[{name!r}]", name, *memory(t)) for name, t in out.items()]
+    ins = [(name, name, *memory(t)) for name, t in inputs.items() if t is not None]
+    for i, (label, name, a0, a1) in enumerate(outs):
+        for other, theirs, b0, b1 in ins + outs[i + 1:]:
+            if a0 < b1 and b0 < a1 and not (theirs == name and name in may_be_same and a0 == b0 and a1 == b1):
+                raise ValueError(f"{label} shares memory with {other}")
 
 
 def kv_page_bounds(k_cache: torch.Tensor, block_table: torch.Tensor, prefix_len: torch.Tensor, *,
@@ -732,7 +739,8 @@ def kv_reserve(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
     kv_commit's freed_blocks) lose a reference each, missing pages are handed out, and a half-filled last page
     that others hold too is replaced by a copy (its rows move in k_cache / v_cache).  Returns the new
     block_table and refs and granted [B] (fresh pages per sequence, -1 where the pool ran short and the sequence
-    stays as it was).  ``out`` may hold the input tensors themselves, for an update in place."""
+    stays as it was).  In ``out``, block_table and refs may be the input tensors themselves, for an update in place;
+    otherwise the outputs lie apart from the inputs and from one another."""
     L = library()
     ix = _index_of("k_cache", k_cache, 4)
     if ix != torch.cuda.current_device():
@@ -755,8 +763,8 @@ def kv_reserve(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
         out = dict(block_table=torch.empty_like(block_table), refs=torch.empty_like(refs),
                    granted=torch.empty_like(prefix_len))
     else:
-        _apart(out["block_table"], block_table, True)
-        _apart(out["refs"], refs, True)
+        _apart(out, ("block_table", "refs"), block_table=block_table, refs=refs, prefix_len=prefix_len, freed=freed,
+               k_cache=k_cache, v_cache=v_cache)
     ws, ws_bytes, keep = _scratch(need, refs, workspace)
     _check(L.ts_kv_reserve(*args, freed_at, nfreed,
                            *_out_args(out, ix, made, block_table=(_I32, table), refs=(_I32, (NB,)), granted=(_I32, (B,))), ws,
@@ -768,7 +776,8 @@ def kv_fork(block_table: torch.Tensor, prefix_len: torch.Tensor, refs: torch.Ten
             out: Optional[Dict[str, torch.Tensor]] = None, status: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
     """New sequences from old ones: row r continues row src[r] (int32, any number of rows; -1: an empty row).
     Returns the new block_table, prefix_len and refs, which replace the old ones: pages are shared, not
-    copied, and those of rows that nobody continues are let go.  ``out["refs"]`` may be ``refs`` itself."""
+    copied, and those of rows that nobody continues are let go.  ``out["refs"]`` may be ``refs`` itself; otherwise the
+    outputs lie apart from the inputs and from one another."""
     L = library()
     ix = _index_of("block_table", block_table, 2)
     if ix != torch.cuda.current_device():
@@ -783,10 +792,7 @@ def kv_fork(block_table: torch.Tensor, prefix_len: torch.Tensor, refs: torch.Ten
         out = dict(block_table=torch.empty((R, width), dtype=_I32, device=refs.device), prefix_len=torch.empty_like(src),
                    refs=torch.empty_like(refs))
     else:
-        _apart(out["block_table"], block_table, False)
-        _apart(out["prefix_len"], prefix_len, False)
-        _apart(out["prefix_len"], src, False)
-        _apart(out["refs"], refs, True)
+        _apart(out, ("refs",), block_table=block_table, prefix_len=prefix_len, refs=refs, src=src)
     _check(L.ts_kv_fork(*args, *_out_args(out, ix, made, block_table=(_I32, (R, width)), prefix_len=(_I32, (R,)),
                                           refs=(_I32, (NB,))), _status_arg(status, ix), _raw_stream(ix)))
     return out
@@ -797,7 +803,8 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
                workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
     """Move the pages in use (refs > 0) to the lowest ids, in place on k_cache / v_cache (and bounds).  Returns the
     new block_table and refs, remap [num_blocks] (a page's new id, -1 for a free one) and live [1] (pages in
-    use).  ``out`` may hold block_table and refs themselves, for an update in place."""
+    use).  In ``out``, block_table and refs may be the input tensors themselves, for an update in place;
+    otherwise the outputs lie apart from the inputs and from one another."""
     L = library()
     ix = _index_of("k_cache", k_cache, 4)
     if ix != torch.cuda.current_device():
@@ -814,10 +821,7 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
         out = dict(block_table=torch.empty_like(block_table), refs=torch.empty_like(refs), remap=torch.empty_like(refs),
                    live=torch.empty((1,), dtype=_I32, device=refs.device))
     else:
-        _apart(out["block_table"], block_table, True)
-        _apart(out["refs"], refs, True)
-        _apart(out["remap"], refs, False)
-        _apart(out["remap"], out["refs"], False)
+        _apart(out, ("block_table", "refs"), block_table=block_table, refs=refs, k_cache=k_cache, v_cache=v_cache, bounds=bounds)
     ws, ws_bytes, keep = _scratch(L.ts_kv_compact_workspace(NB), refs, workspace)
     _check(L.ts_kv_compact(*args, *_out_args(out, ix, made, block_table=(_I32, table), refs=(_I32, (NB,)),
                                              remap=(_I32, (NB,)), live=(_I32, (1,))), ws, ws_bytes, _status_arg(status, ix), _raw_stream(ix)))

@@ -3,6 +3,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "common.cuh"
 #include "internal.h"
@@ -50,6 +51,30 @@ static int check_accept(ts_dtype dt, int B, int m, int V) {
 }
 
 }  // namespace ts
+
+// A tensor's memory, as the checks for overlap see it (size 0 where a tensor is left out).
+struct Memory {
+  uintptr_t at;
+  size_t size;
+  Memory(const void* p, size_t elems, size_t elem_size) : at(reinterpret_cast<uintptr_t>(p)), size(p ? elems * elem_size : 0) {}
+};
+static bool overlap(const Memory& a, const Memory& b) {
+  return a.size > 0 && b.size > 0 && a.at < b.at + b.size && b.at < a.at + a.size;
+}
+// Whether every output lies apart from the inputs and from the other outputs; an output that may be its input's buffer
+// and is leaves that input out.
+static bool outputs_apart(std::initializer_list<Memory> outs, std::initializer_list<Memory> ins) {
+  for (const Memory* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Memory& i : ins)
+      if (overlap(*o, i)) return false;
+    for (const Memory* other = o + 1; other != outs.end(); ++other)
+      if (overlap(*o, *other)) return false;
+  }
+  return true;
+}
+static size_t times(int a, int b, int c = 1, int d = 1) {
+  return static_cast<size_t>(a) * static_cast<size_t>(b) * static_cast<size_t>(c) * static_cast<size_t>(d);
+}
 
 static bool aligned4_ptr(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 static bool aligned16_ptr(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -486,7 +511,17 @@ int ts_kv_reserve(void* k_cache, void* v_cache, ts_dtype dt, int num_blocks, int
   if (!k_cache || !v_cache || !block_table || !prefix_len || !refs || !block_table_out || !refs_out || !granted || !workspace)
     return TS_ERR_INVALID;
   if (!aligned4_ptr(k_cache) || !aligned4_ptr(v_cache) || !aligned16_ptr(workspace)) return TS_ERR_INVALID;
-  if (ws_bytes < ts::kv_reserve_workspace_bytes(num_blocks, block_size, B, n)) return TS_ERR_WORKSPACE;
+  const size_t need = ts::kv_reserve_workspace_bytes(num_blocks, block_size, B, n);
+  if (ws_bytes < need) return TS_ERR_WORKSPACE;
+  const size_t cache = times(num_blocks, Hkv, block_size, d), size = dt == TS_BF16 ? 2 : 4, cells = times(B, max_blocks);
+  if (!outputs_apart({{block_table_out, cells, 4}, {refs_out, times(num_blocks, 1), 4}, {granted, times(B, 1), 4}, {workspace, need, 1}},
+                     {{block_table_out == block_table ? nullptr : block_table, cells, 4},
+                      {refs_out == refs ? nullptr : refs, times(num_blocks, 1), 4},
+                      {prefix_len, times(B, 1), 4},
+                      {freed, times(num_freed, 1), 4},
+                      {k_cache, cache, size},
+                      {v_cache, cache, size}}))
+    return TS_ERR_INVALID;
   ts::ReserveCall c{k_cache, v_cache, dt, num_blocks, block_size, Hkv, d, block_table, max_blocks, prefix_len, refs, B, n,
                     freed, num_freed, block_table_out, refs_out, granted, workspace, dev_status};
   return ts::kv_reserve_launch(c, static_cast<cudaStream_t>(stream));
@@ -498,7 +533,13 @@ int ts_kv_fork(const int32_t* block_table, int max_blocks, const int32_t* prefix
   if (num_blocks <= 0 || block_size <= 0 || max_blocks <= 0 || B <= 0 || B_out <= 0) return TS_ERR_INVALID;
   if (B > 65535 || B_out > 65535) return TS_ERR_UNSUPPORTED;
   if (!block_table || !prefix_len || !refs || !src || !block_table_out || !prefix_len_out || !refs_out) return TS_ERR_INVALID;
-  if (block_table_out == block_table || prefix_len_out == prefix_len || prefix_len_out == src) return TS_ERR_INVALID;
+  const size_t rows = B_out, pages = num_blocks;
+  if (!outputs_apart({{block_table_out, times(B_out, max_blocks), 4}, {prefix_len_out, rows, 4}, {refs_out, pages, 4}},
+                     {{block_table, times(B, max_blocks), 4},
+                      {prefix_len, times(B, 1), 4},
+                      {refs_out == refs ? nullptr : refs, pages, 4},
+                      {src, rows, 4}}))
+    return TS_ERR_INVALID;
   const int sms = ts::device_sm_count();
   if (sms <= 0) return TS_ERR_CUDA;
   return ts::kv_fork_launch(block_table, max_blocks, prefix_len, refs, num_blocks, block_size, B, src, B_out, block_table_out,
@@ -519,7 +560,17 @@ int ts_kv_compact(void* k_cache, void* v_cache, ts_dtype dt, void* bounds, int n
   if (!aligned4_ptr(k_cache) || !aligned4_ptr(v_cache) || !aligned16_ptr(workspace)) return TS_ERR_INVALID;
   if (num_blocks > (1 << 28)) return TS_ERR_UNSUPPORTED;
   if (bounds && !aligned16_ptr(bounds)) return TS_ERR_INVALID;
-  if (ws_bytes < ts::kv_compact_workspace_bytes(num_blocks)) return TS_ERR_WORKSPACE;
+  const size_t need = ts::kv_compact_workspace_bytes(num_blocks);
+  if (ws_bytes < need) return TS_ERR_WORKSPACE;
+  const size_t cache = times(num_blocks, Hkv, block_size, d), size = dt == TS_BF16 ? 2 : 4, cells = times(B, max_blocks);
+  const size_t pages = num_blocks;
+  if (!outputs_apart({{block_table_out, cells, 4}, {refs_out, pages, 4}, {remap, pages, 4}, {live, 1, 4}, {workspace, need, 1}},
+                     {{block_table_out == block_table ? nullptr : block_table, cells, 4},
+                      {refs_out == refs ? nullptr : refs, pages, 4},
+                      {k_cache, cache, size},
+                      {v_cache, cache, size},
+                      {bounds, times(num_blocks, Hkv, 2, d), 2}}))
+    return TS_ERR_INVALID;
   const int sms = ts::device_sm_count();
   if (sms <= 0) return TS_ERR_CUDA;
   return ts::kv_compact_launch(k_cache, v_cache, dt, bounds, num_blocks, block_size, Hkv, d, block_table, max_blocks, refs, B,

@@ -278,3 +278,24 @@ def test_caches_off_the_allocations_alignment(dtype):
     *_, (rk, rv) = pool.compact(rt, rr, rk, rv)
     np.testing.assert_array_equal(_bits(gk), rk)
     np.testing.assert_array_equal(_bits(gv), rv)
+
+
+@pytest.mark.parametrize("op,name,other", [
+    ("reserve", "granted", "L"), ("reserve", "granted", "freed"), ("reserve", "granted", "refs"), ("reserve", "refs", "refs_out"),
+    ("fork", "refs", "src"), ("fork", "prefix_len", "L"), ("fork", "prefix_len", "refs"), ("compact", "remap", "refs"),
+    ("compact", "live", "table"), ("compact", "live", "remap")])
+def test_outputs_that_are_other_inputs_or_outputs_are_refused(op, name, other):
+    lib()
+    k = torch.zeros(4, 1, 2, 2, device=dev())
+    t = dict(table=_g(np.full((4, 2), -1)), L=_g([0] * 4), refs=_g([0] * 4), freed=_g([-1] * 4), src=_g([0] * 4))
+    outs = dict(reserve=dict(block_table=_g(np.zeros((4, 2))), refs=_g([0] * 4), granted=_g([0] * 4)),
+                fork=dict(block_table=_g(np.zeros((4, 2))), refs=_g([0] * 4), prefix_len=_g([0] * 4)),
+                compact=dict(block_table=_g(np.zeros((4, 2))), refs=_g([0] * 4), remap=_g([0] * 4), live=_g([0])))
+    call = dict(reserve=lambda out: ts.kv_reserve(k, k.clone(), t["table"], t["L"], t["refs"], 1, freed=t["freed"], out=out),
+                fork=lambda out: ts.kv_fork(t["table"], t["L"], t["refs"], t["src"], 2, out=out),
+                compact=lambda out: ts.kv_compact(k, k.clone(), t["table"], t["refs"], out=out))[op]
+    call(outs[op])
+    out = dict(outs[op])
+    out[name] = (out["granted"] if other == "refs_out" else t.get(other, out.get(other))).view(-1)[:out[name].numel()].view(out[name].shape)
+    with pytest.raises(ValueError):
+        call(out)

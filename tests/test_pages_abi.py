@@ -122,3 +122,45 @@ def test_binding_refuses_cpu_tensors(lib):
     for call in calls:
         with pytest.raises(ValueError):
             call()
+
+
+# Addresses a MiB apart; the calls below are refused, so nothing is ever read there.
+_AT = {n: (i + 1) << 20 for i, n in enumerate(("k", "v", "bounds", "table", "lens", "refs", "src", "freed", "table_out", "lens_out",
+                                               "refs_out", "granted", "remap", "live", "ws"))}
+
+
+def _pool_call(lib, op, **at):
+    p = {**_AT, **at}
+    if op == "reserve":   # 300 rows of 8 pages
+        return lib.ts_kv_reserve(p["k"], p["v"], 1, 500, 16, 2, 8, p["table"], 8, p["lens"], p["refs"], 300, 8, p["freed"], 70,
+                                 p["table_out"], p["refs_out"], p["granted"], p["ws"], 1 << 20, None, None)
+    if op == "fork":      # 300 rows become 200
+        return lib.ts_kv_fork(p["table"], 8, p["lens"], p["refs"], 500, 16, 300, p["src"], 200, p["table_out"], p["lens_out"],
+                              p["refs_out"], None, None)
+    return lib.ts_kv_compact(p["k"], p["v"], 1, p["bounds"], 500, 16, 2, 8, p["table"], 8, p["refs"], 300, p["table_out"],
+                             p["refs_out"], p["remap"], p["live"], p["ws"], 1 << 20, None, None)
+
+
+@pytest.mark.parametrize("op,out,others", [
+    ("reserve", "granted", ("lens", "refs", "table", "freed", "k", "v", "refs_out", "table_out", "ws")),
+    ("reserve", "refs_out", ("lens", "table", "freed", "table_out", "k")),
+    ("reserve", "table_out", ("lens", "refs", "freed", "v")),
+    ("fork", "table_out", ("table", "lens", "refs", "src", "lens_out", "refs_out")),
+    ("fork", "lens_out", ("table", "lens", "refs", "src", "refs_out")),
+    ("fork", "refs_out", ("table", "lens", "src")),
+    ("compact", "remap", ("table", "refs", "k", "v", "bounds", "table_out", "refs_out", "live", "ws")),
+    ("compact", "live", ("table", "refs", "bounds", "table_out", "refs_out", "ws")),
+    ("compact", "refs_out", ("table", "table_out", "k")),
+    ("compact", "table_out", ("refs", "v"))])
+def test_pool_outputs_that_overlap_are_refused(lib, op, out, others):
+    for other in others:
+        assert _pool_call(lib, op, **{out: _AT[other]}) == INVALID, other           # the very buffer
+        if other != "live":
+            assert _pool_call(lib, op, **{out: _AT[other] + 64}) == INVALID, other  # a part of it
+
+
+def test_pool_updates_in_place_are_of_the_whole_buffer(lib):
+    for op in ("reserve", "compact"):
+        assert _pool_call(lib, op, table_out=_AT["table"] + 32) == INVALID
+        assert _pool_call(lib, op, refs_out=_AT["refs"] - 4) == INVALID
+    assert _pool_call(lib, "fork", refs_out=_AT["refs"] + 4) == INVALID
