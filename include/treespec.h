@@ -26,6 +26,9 @@
  *     pointers return TS_ERR_INVALID, sizes outside the supported range return
  *     TS_ERR_UNSUPPORTED, a too-small workspace returns TS_ERR_WORKSPACE.  Nothing is
  *     launched in those cases.  A failed launch returns TS_ERR_CUDA.
+ *   - ts_kv_page_bounds, ts_page_select, ts_tree_attention_sparse and the page pool refuse outputs
+ *     (and workspaces) that share memory with an input or another output, but for those of the
+ *     pool that may be their input's buffer: TS_ERR_INVALID.
  *   - Problems the host cannot see (a block id out of range, a parent index that does
  *     not precede its child, a prefix length above `max_prefix`, a bounded wait that
  *     timed out) are reported on the device: the first such error code is stored into

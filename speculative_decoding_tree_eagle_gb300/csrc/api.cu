@@ -1,5 +1,6 @@
 // C ABI of libtreespec.so (declared in include/treespec.h): host-side argument validation,
 // workspace sizing and dispatch to the kernels.  Nothing here allocates device memory.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -401,6 +402,13 @@ int ts_kv_page_bounds(const void* k_cache, ts_dtype dt, int num_blocks, int bloc
   if (rc != TS_OK) return rc;
   if (d > 256) return TS_ERR_UNSUPPORTED;
   if (!k_cache || !block_table || !prefix_len || !bounds) return TS_ERR_INVALID;
+  const size_t size = dt == TS_BF16 ? 2 : 4;
+  if (!outputs_apart({{bounds, times(num_blocks, Hkv, 2, d), 2}},
+                     {{k_cache, times(num_blocks, Hkv, block_size, d), size},
+                      {block_table, times(B, max_blocks), 4},
+                      {prefix_len, times(B, 1), 4},
+                      {start_len, times(B, 1), 4}}))
+    return TS_ERR_INVALID;
   const int sms = ts::device_sm_count();
   if (sms <= 0) return TS_ERR_CUDA;
   return ts::kv_page_bounds_launch(k_cache, dt, num_blocks, block_size, Hkv, d, block_table, max_blocks, prefix_len,
@@ -439,6 +447,16 @@ int ts_page_select(const void* q, ts_dtype dt, const void* bounds, int num_block
   const size_t need = ts_page_select_workspace(B, m, Hq, Hkv, d, max_prefix, block_size);
   if (need > 256 && (!workspace || !aligned16_ptr(workspace))) return TS_ERR_INVALID;
   if (need > 256 && ws_bytes < need) return TS_ERR_WORKSPACE;
+  const size_t places = times(B, Hkv, std::max(1, max_prefix / block_size)), size = dt == TS_BF16 ? 2 : 4;
+  if (!outputs_apart({{pages, places, 4},
+                      {count, times(B, Hkv), 4},
+                      {node_mask, places * ((m + 63) / 64), 8},
+                      {need > 256 ? workspace : nullptr, need, 1}},
+                     {{q, times(B, m, Hq, d), size},
+                      {bounds, times(num_blocks, Hkv, 2, d), 2},
+                      {block_table, times(B, max_blocks), 4},
+                      {prefix_len, times(B, 1), 4}}))
+    return TS_ERR_INVALID;
   const int sms = ts::device_sm_count();
   if (sms <= 0) return TS_ERR_CUDA;
   ts::SelectCall c{q, dt, bounds, num_blocks, block_size, block_table, max_blocks, prefix_len, max_prefix, B, m, Hq, Hkv, d,
@@ -475,6 +493,21 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
   if (!q || !k_cache || !v_cache || !block_table || !prefix_len || !mask || !pages || !count || !node_mask || !out)
     return TS_ERR_INVALID;
   if (!std::isfinite(scale) || !(scale > 0.f)) return TS_ERR_INVALID;
+  const size_t rows = times(B, m, Hq), size = dt == TS_BF16 ? 2 : 4, cache = times(num_blocks, Hkv, block_size, d);
+  const size_t words = (m + 63) / 64, places = times(B, Hkv, C);
+  auto apart = [&](size_t used) {  // with the bytes of the workspace that are used
+    return outputs_apart({{out, rows * d, size}, {lse, rows, 4}, {workspace, used, 1}},
+                         {{q, rows * d, size},  // (rows computed again read it after others have been written)
+                          {k_cache, cache, size},
+                          {v_cache, cache, size},
+                          {block_table, times(B, max_blocks), 4},
+                          {prefix_len, times(B, 1), 4},
+                          {mask, times(B, m) * words, 8},
+                          {pages, places, 4},
+                          {count, times(B, Hkv), 4},
+                          {node_mask, places * words, 8}});
+  };
+  if (!apart(0)) return TS_ERR_INVALID;
   ts::SparseCall a{q, k_cache, v_cache, dt, num_blocks, block_size, block_table, max_blocks, prefix_len, mask, pages, count,
                    node_mask, C, B, m, Hq, Hkv, d, scale, out, lse, workspace, dev_status};
   const int sms = ts::device_sm_count();
@@ -487,7 +520,7 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
   if (sms <= 0) return TS_ERR_CUDA;
   const size_t need = ts::attention_sparse_tc_workspace_bytes(B, m, Hq, Hkv, C, block_size, sms);
   if (need > 256 && (!workspace || ws_bytes < need)) return TS_ERR_WORKSPACE;
-  if (need > 256 && !aligned16_ptr(workspace)) return TS_ERR_INVALID;
+  if (need > 256 && (!aligned16_ptr(workspace) || !apart(need))) return TS_ERR_INVALID;
   return ts::attention_sparse_tc_launch(a, static_cast<cudaStream_t>(stream), sms);
 }
 

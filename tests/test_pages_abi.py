@@ -164,3 +164,32 @@ def test_pool_updates_in_place_are_of_the_whole_buffer(lib):
         assert _pool_call(lib, op, table_out=_AT["table"] + 32) == INVALID
         assert _pool_call(lib, op, refs_out=_AT["refs"] - 4) == INVALID
     assert _pool_call(lib, "fork", refs_out=_AT["refs"] + 4) == INVALID
+
+
+def _choice_call(lib, op, **at):
+    p = {**{n: (i + 1) << 24 for i, n in enumerate(("q", "k", "v", "bounds", "table", "lens", "start", "mask", "pages", "count", "bits",
+                                                    "out", "lse", "ws"))}, **at}
+    if op == "bounds":
+        return lib.ts_kv_page_bounds(p["k"], 1, 500, 16, 2, 128, p["table"], 40, p["lens"], p["start"], 6, p["bounds"], None, None)
+    if op == "select":
+        return lib.ts_page_select(p["q"], 1, p["bounds"], 500, 16, p["table"], 40, p["lens"], 600, 6, 9, 4, 2, 128, 4, 1, 1,
+                                  p["pages"], p["count"], p["bits"], p["ws"], 1 << 22, None, None)
+    return lib.ts_tree_attention_sparse(p["q"], p["k"], p["v"], 1, 500, 16, p["table"], 40, p["lens"], p["mask"], p["pages"],
+                                        p["count"], p["bits"], 37, 6, 9, 4, 2, 128, 0.1, p["out"], p["lse"], p["ws"], 1 << 22,
+                                        None, None)
+
+
+@pytest.mark.parametrize("op,out,others", [
+    ("bounds", "bounds", ("k", "table", "lens", "start")),
+    ("select", "pages", ("q", "bounds", "table", "lens", "count", "bits", "ws")),
+    ("select", "count", ("q", "bounds", "table", "lens", "bits", "ws")),
+    ("select", "bits", ("q", "bounds", "table", "lens", "ws")),
+    ("attend", "out", ("q", "k", "v", "table", "lens", "mask", "pages", "count", "bits", "lse")),
+    ("attend", "lse", ("q", "k", "v", "table", "lens", "mask", "pages", "count", "bits"))])
+def test_outputs_that_overlap_are_refused(lib, op, out, others):
+    """(also where the other is given the output's address: 16 bytes into it)"""
+    base = {n: (i + 1) << 24 for i, n in enumerate(("q", "k", "v", "bounds", "table", "lens", "start", "mask", "pages", "count", "bits",
+                                                    "out", "lse", "ws"))}
+    for other in others:
+        assert _choice_call(lib, op, **{out: base[other]}) == INVALID, other
+        assert _choice_call(lib, op, **{other: base[out] + 16}) == INVALID, other
