@@ -383,3 +383,19 @@ def test_keys_of_a_page_without_an_id_are_left_out(dtype, bs, case, split, monke
     assert (np.abs(got - ref) <= _tolerance(q, k, L, ref, spread)).all()
     X = float(q.double().norm(dim=-1).max() * k.double().norm(dim=-1).max()) / math.sqrt(128)
     assert (np.abs(gl - rl) <= (128 * X + 4 * (np.abs(rl) + longest + m)) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("split,B", [("", 80), ("direct", 2), ("cluster:2", 2), ("global:5", 2)])
+def test_unions_longer_than_a_cta_stages(split, B, monkeypatch):
+    """130 nodes of one head: a CTA stages the ids and bits of some 190 tiles, the capacity and the first sequence's
+    union are of 205.  With 80 sequences the GPU is full without splitting, so only this limit splits."""
+    lib()
+    if split:
+        monkeypatch.setenv("TREESPEC_ATTN_SPLIT", split)
+    c = dict(L=[26000] + [40, 0, 3000, 16][:B - 1] + [25] * max(0, B - 5), m=130, Hq=1, Hkv=1, d=128, bs=16, dtype=BF, n=60)
+    x = _case(15, **c)
+    assert x[5][0, 0].any(0).sum() > 1550
+    status = ts.new_status(dev())
+    out, lse = _run(x[0], x[1], x[2], x[3], c["L"], x[4], x[5], status=status)
+    ts.check_status(status)
+    _check(*x[:4], c["L"], *x[4:], out, lse)
