@@ -191,12 +191,13 @@ __device__ __forceinline__ int virtual_page(const Params& p, const Span& s, int 
   return lp >= 0 && lp < s.nf ? lp : -1;
 }
 
-// Exact output row of the sparse mode by one warp, one key at a time: used only for rows in which a
+// Exact output row of the sparse mode by one warp, four keys at a time: used only for rows in which a
 // NaN came out of the tensor cores.  There a key that a row does not attend to has weight 0, and 0 times
-// a non-finite value of V is NaN; here such keys are not read at all.
+// a non-finite value of V is NaN; here such keys are not read at all.  A NaN score makes the whole row NaN, so
+// nothing more is read after one.
 __device__ __noinline__ void repair_row(const Params& p, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int b, int kvh,
                                         int node, int head) {
-  const int lane = threadIdx.x & 31, bk = b * p.Hkv + kvh;
+  const int lane = threadIdx.x & 31, bk = b * p.Hkv + kvh, bs = p.block_size;
   const Span s = span_of<true>(p, b, bk);
   const long long qo = ((static_cast<long long>(b) * p.m + node) * p.Hq + head) * HD + 4 * lane;
   auto four = [](const __nv_bfloat16* x) {
@@ -205,38 +206,62 @@ __device__ __noinline__ void repair_row(const Params& p, const __nv_bfloat16* kc
   };
   const float4 q = four(p.q + qo);
   const uint64_t* mrow = p.mask + (static_cast<long long>(b) * p.m + node) * p.W;
+  const int vpages = (s.nkeys + bs - 1) / bs;
   float M = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int key = 0; key < s.nkeys; ++key) {
-    const int v = key / p.block_size;
-    if (v < s.nu) {
-      const uint64_t w = p.node_mask[(static_cast<long long>(bk) * p.C + v) * p.W + (node >> 6)];
-      if (!((w >> (node & 63)) & 1ull)) {
-        key += p.block_size - 1;
-        continue;
-      }
-    } else if (key >= s.L) {
-      const int t = key - s.L;
-      if (!((mrow[t >> 6] >> (t & 63)) & 1ull)) continue;
+  for (int v0 = 0; v0 < vpages && !isnan(l); v0 += 32) {
+    // lane j: the block of virtual page v0 + j, -1 where this row attends to none
+    const int v = v0 + lane;
+    int block = -1;
+    if (v < vpages &&
+        (v >= s.nu || ((p.node_mask[(static_cast<long long>(bk) * p.C + v) * p.W + (node >> 6)] >> (node & 63)) & 1ull))) {
+      const int lp = virtual_page(p, s, bk, v);
+      if (lp >= 0) block = p.block_table[static_cast<long long>(b) * p.max_blocks + lp];
+      if (block >= p.num_blocks) block = -1;
     }
-    const int lp = virtual_page(p, s, bk, v);
-    const int e = lp < 0 ? -1 : p.block_table[static_cast<long long>(b) * p.max_blocks + lp];
-    if (e < 0 || e >= p.num_blocks) continue;
-    const long long o = ((static_cast<long long>(e) * p.Hkv + kvh) * p.block_size + key % p.block_size) * HD + 4 * lane;
-    const float4 k = four(kc + o), x = four(vc + o);
-    float dot = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+    for (unsigned left = __ballot_sync(0xffffffffu, block >= 0); left != 0u && !isnan(l); left &= left - 1u) {
+      const int j = __ffs(left) - 1;
+      const long long first = (static_cast<long long>(__shfl_sync(0xffffffffu, block, j)) * p.Hkv + kvh) * bs;
+      for (int r = 0; r < bs && !isnan(l); r += 4) {  // (pages hold a multiple of 16 keys)
+        float4 k[4], x[4];
+        float dot[4];
+        bool seen[4];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-    dot *= p.scale_log2;
-    const float m2 = fmaxf(M, dot);  // (a NaN is not the larger one, but makes w, and with it l and acc, NaN for good)
-    if (M == -INFINITY && dot == -INFINITY) continue;
-    const float c = exp2f(M - m2), w = exp2f(dot - m2);
-    l = l * c + w;
-    acc.x = acc.x * c + w * x.x;
-    acc.y = acc.y * c + w * x.y;
-    acc.z = acc.z * c + w * x.z;
-    acc.w = acc.w * c + w * x.w;
-    M = m2;
+        for (int u = 0; u < 4; ++u) {
+          const int t = (v0 + j) * bs + r + u - s.L;  // tree node, negative in the prefix
+          seen[u] = t < 0 || (t < p.m && ((mrow[t >> 6] >> (t & 63)) & 1ull));
+          k[u] = x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (seen[u]) {
+            const long long o = (first + r + u) * HD + 4 * lane;
+            k[u] = four(kc + o);
+            x[u] = four(vc + o);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) dot[u] = q.x * k[u].x + q.y * k[u].y + q.z * k[u].z + q.w * k[u].w;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], off);
+        float m2 = M;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          dot[u] = seen[u] ? dot[u] * p.scale_log2 : -INFINITY;
+          m2 = fmaxf(m2, dot[u]);  // (passes over a NaN, which makes its weight NaN)
+        }
+        const float c = M == m2 ? 1.f : exp2f(M - m2);
+        l *= c;
+        acc.x *= c, acc.y *= c, acc.z *= c, acc.w *= c;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (!seen[u]) continue;
+          const float w = dot[u] == -INFINITY ? 0.f : exp2f(dot[u] - m2);
+          l += w;
+          acc.x += w * x[u].x, acc.y += w * x[u].y, acc.z += w * x[u].z, acc.w += w * x[u].w;
+        }
+        M = m2;
+      }
+    }
   }
   const float inv = l > 0.f ? 1.f / l : l;
   *reinterpret_cast<uint2*>(p.out + qo) =

@@ -399,3 +399,32 @@ def test_unions_longer_than_a_cta_stages(split, B, monkeypatch):
     out, lse = _run(x[0], x[1], x[2], x[3], c["L"], x[4], x[5], status=status)
     ts.check_status(status)
     _check(*x[:4], c["L"], *x[4:], out, lse)
+
+
+@pytest.mark.parametrize("split", ["direct", "cluster:2", "global:3"])
+@pytest.mark.parametrize("c", [CASES[2], CASES[3], CASES[4], CASES[5], dict(CASES[7], m=1), CASES[10]], ids=_id)
+def test_a_nan_value_reaches_its_channel_of_the_rows_that_attend_to_it(c, split, monkeypatch):
+    """NaN in one channel of V, at a key of a page and at a tree node: that channel of the rows that attend to it, and
+    nothing else."""
+    lib()
+    monkeypatch.setenv("TREESPEC_ATTN_SPLIT", split)
+    q, k, v, table, mask, kept = _case(16, **c)
+    L, (B, m, Hq, d), bs = c["L"], q.shape, c["bs"]
+    g = Hq // k.shape[1]
+    page, node, b1 = int(np.nonzero(kept[0, 0].any(0))[0][-1]), m // 2, len(L) - 1
+    v2 = v.clone()
+    v2[table[0, page], 0, bs - 2, 9] = float("nan")
+    pos = L[b1] + node
+    v2[table[b1, pos // bs], -1, pos % bs, 70] = float("nan")
+    hit = np.zeros((B, m, Hq, d), dtype=bool)
+    hit[0, :, :g, 9] = kept[0, 0, :, page, None]
+    hit[b1, :, -g:, 70] |= mask[b1, :, node, None]
+    status = ts.new_status(dev())
+    out, lse = _run(q, k, v2, table, L, mask, kept, status=status)
+    ts.check_status(status)
+    ref, rl, spread = oracle.tree_attention_sparse(q, k, v, table, L, mask, kept, 1 / math.sqrt(d))
+    got = out.double().cpu().numpy()
+    assert np.isnan(got[hit]).all()
+    assert (np.abs(got - ref) <= _tolerance(q, k, L, ref, spread))[~hit].all()
+    X = float(q.double().norm(dim=-1).max() * k.double().norm(dim=-1).max()) / math.sqrt(d)
+    assert (np.abs(lse.double().cpu().numpy() - rl) <= (128 * X + 4 * (np.abs(rl) + max(L) + m)) * 2.0 ** -24).all()
