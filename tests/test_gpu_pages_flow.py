@@ -267,3 +267,40 @@ def test_tensors_of_another_place_or_layout_are_refused():
             call()
     with pytest.raises(ts.TreeSpecError):
         ts.kv_reserve(s["k"], s["v"], s["table"], s["L"], s["refs"], 0)
+
+
+@pytest.mark.parametrize("m", [5, 1])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_caches_whose_offsets_pass_32_bits(dtype, m):
+    """A step over the last 80 of 2^19 + 80 pages of 4096 values gives what it gives over 80 pages alone."""
+    lib()
+    s = _step_state(8, m=m)
+    s["k"], s["v"] = s["k"].to(dtype), s["v"].to(dtype)
+    s["q"] = s["q"].to(dtype)
+    low = 2 ** 19
+    far = dict(s)
+    for name in ("k", "v"):
+        far[name] = torch.empty(low + 80, *s[name].shape[1:], dtype=dtype, device=dev())
+        far[name][:low // 2].fill_(float("nan"))   # (the rest of the low half is never touched: whatever is there)
+        far[name][low:] = s[name]
+    assert far["k"].numel() > 2 ** 31
+    far["table"] = torch.where(s["table"] >= 0, s["table"] + low, -1)
+    far["refs"] = torch.cat([torch.ones(low, dtype=torch.int32, device=dev()), s["refs"]])   # the low pages are others'
+
+    def step(t):
+        f = ts.kv_fork(t["table"], t["L"], t["refs"], t["src"], t["bs"])
+        r = ts.kv_reserve(t["k"], t["v"], f["block_table"], f["prefix_len"], f["refs"], t["m"])
+        b = ts.kv_page_bounds(t["k"], r["block_table"], f["prefix_len"])
+        sel = ts.page_select(t["q"], b, r["block_table"], f["prefix_len"], 3, block_size=t["bs"], max_prefix=t["maxp"])
+        out, lse = ts.tree_attention_sparse(t["q"], t["k"], t["v"], r["block_table"], f["prefix_len"], t["words"], sel)
+        c = ts.kv_compact(t["k"], t["v"], r["block_table"], r["refs"], bounds=b)
+        return ([f["block_table"], r["block_table"], c["block_table"]], [f["refs"], r["refs"], c["refs"], c["remap"], t["k"], t["v"], b],
+                [f["prefix_len"], r["granted"], *sel.values(), out, lse], c["live"])
+
+    tables, pages, others, live = step(_copy(s))
+    far_tables, far_pages, far_others, far_live = step(far)
+    for x, y in zip(tables, far_tables):
+        assert torch.equal(torch.where(x >= 0, x + low, -1), y)
+    pages[3] = torch.where(pages[3] >= 0, pages[3] + low, -1)
+    assert _same(pages, [x[low:] for x in far_pages]) and _same(others, far_others)
+    assert int(far_live.item()) == int(live.item()) + low and (pages[3] >= low).any() and (s["refs"] == 0).any()
