@@ -11,7 +11,7 @@
  *
  * Long contexts: tree attention over a choice of the prefix's pages
  *   ts_kv_page_bounds          per-page bounds of the keys
- *   ts_page_select             the pages each node attends to, by an exact upper-bound score
+ *   ts_page_select             the pages each node attends to, by a bound of its rounded query's scores
  *   ts_tree_attention_sparse   tree attention over the chosen pages
  * The page pool
  *   ts_kv_reserve, ts_kv_fork, ts_kv_compact   hand out, share, copy, free and move pages
@@ -475,9 +475,11 @@ int ts_kv_page_bounds(const void* k_cache, ts_dtype dt, int num_blocks, int bloc
  * its largest magnitude (NaN counts as 0, magnitudes clamped to 255 * 2^40), q~ = 2^e * rint(q / 2^e).
  *   score(i, KV head h, page p) = max over the g heads of h of
  *                                 sum_c max(q~_c * bounds[p][h][0][c], q~_c * bounds[p][h][1][c]),
- * an upper bound of q~ . k over the page's keys.  Every product and partial sum is a whole
- * multiple of one power of two below 2^24 times it, so fp32 holds the score exactly whatever the
- * order of summation: the choice does not depend on tiling, batch or machine.
+ * an upper bound of q~ . k over the page's keys (not of q . k, which exceeds it by at most 2^(e-1)
+ * sum_c max(|bounds[p][h][0][c]|, |bounds[p][h][1][c]|): a channel below 1/510 of the largest may
+ * round to 0).  Every product and partial sum is a whole multiple of one power of two below 2^24
+ * times it, so fp32 holds the score exactly whatever the order of summation: the choice does not
+ * depend on tiling, batch or machine.
  * Of the prefix_len[b] / block_size complete pages node i keeps the first `first`, the last
  * `recent`, and then the best by score (ties -> lower index) until it has n_pages, or all if
  * there are no more than n_pages.
@@ -539,7 +541,7 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
  * workspace) with an input or another output returns TS_ERR_INVALID.  All results are whole numbers
  * that do not depend on the order of execution.
  * ts_kv_commit lists what a verify step lets go of; pass that list to the next ts_kv_reserve (until then those
- * pages count as in use).
+ * pages count as in use, and a ts_kv_compact in between moves them: take such ids through its remap).
  * --------------------------------------------------------------------------------- */
 
 /*
@@ -560,7 +562,8 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
  * k_cache, v_cache [num_blocks, Hkv, block_size, d] (dt), in/out.  block_table [B, max_blocks],
  * prefix_len [B], refs [num_blocks].  freed [num_freed] int32 (-1 entries skipped; NULL with 0).
  * block_table_out, refs_out: may be block_table, refs.  granted [B] int32: fresh pages taken, or -1.
- * n >= 1, B <= TS_MAX_POOL_ROWS, B * max_blocks < 2^31.  Two launches.
+ * n >= 1, B <= TS_MAX_POOL_ROWS, B * max_blocks < 2^31 (more rows, which ts_kv_fork makes: a call for each
+ * slice of rows, refs handed on, freed with the first).  Two launches.
  * workspace: ts_kv_reserve_workspace(...) bytes, 16-byte aligned.
  * Errors: TS_ERR_INVALID also for d * element size or a cache's address not a multiple of 4.
  * Device errors: a negative length, L + n > max_blocks * block_size or an entry out of range:
@@ -588,7 +591,8 @@ int ts_kv_reserve(void* k_cache, void* v_cache, ts_dtype dt, int num_blocks, int
  * refs_out may be refs.  B, B_out <= 65535.  One or two launches, no workspace.
  * Device errors: src outside [-1, B), a length outside [0, max_blocks * block_size] (the new row is
  * empty), an entry out of range or missing among a kept row's pages (copied as -1), or a count that
- * falls below zero -> TS_ERR_DEVICE_CHECK.
+ * ends below zero -> TS_ERR_DEVICE_CHECK.  (So may a page be reported that has fewer references than entries
+ * that name it and whose count is below zero in between only.)
  */
 int ts_kv_fork(const int32_t* block_table, int max_blocks, const int32_t* prefix_len, const int32_t* refs,
                int num_blocks, int block_size, int B, const int32_t* src, int B_out, int32_t* block_table_out,

@@ -1,10 +1,14 @@
-// ts_page_select: the pages each tree node attends to, by an upper bound of its scores.
+// ts_page_select: the pages each tree node attends to, by an upper bound of the rounded query's scores.
 //
-// For a query value q and a page's bounds lo <= k <= hi of a channel, max(q hi, q lo) is
+// For a query value q and a page's bounds lo <= k <= hi of a channel, max(q hi, q lo) >= q k is
 // q+ hi + q- lo with q+ = max(q, 0), q- = min(q, 0), so the bounds of all nodes and pages are one
 // matrix product per (sequence, KV head):  [q+ | q-] (m g rows, 2 d long) times [hi | lo] of every
 // page.  Both sides are eight-bit whole numbers on power-of-two grids (page_grid.cuh), so bf16
-// holds them and the tensor cores' fp32 sums are exact.
+// holds them and the tensor cores' fp32 sums are exact.  The bounds are rounded outwards, the query to the nearest:
+// the score bounds q~ k, and the query's own q k exceeds it by at most 2^(e-1) sum_c max(|hi_c|, |lo_c|), 2^e
+// being the query's step (1/255 to 1/127 of its largest channel).  The rounding buys a choice that is the same in every
+// order of summation; of 64 pages out of 512 it changes 0.2 to 1.1% (queries with four channels up to 300 times
+// the others), and the softmax mass of the chosen pages by less than 0.0002.
 //
 // Three launches (one, one_node_kernel, for single nodes of few sequences):
 //   score_kernel   tcgen05: 128 rows (whole nodes, all g heads of each) x 128 pages x 2 d per tile;
@@ -15,9 +19,9 @@
 //                  in each kept page's word (an OR, the same in every order).
 //   pack_kernel    a CTA per (sequence, KV head): the pages with any bit, ascending.
 //
-// What bounds it (GB300, ncu): 4 sequences x 8 KV heads, 64 nodes of 4 heads, 2048 pages, d = 128, 128 kept
-// (33.6 MB of bounds, 8.6 GFLOP): score 19.5 us, choose 14.5 us, pack 5.5 us, 32.6 us one after the
-// other.  The score kernel's SMs spend half their issue slots and the tensor pipe 24%: copies, queries' rounding (5 us
+// What bounds it (GB300): 4 sequences x 8 KV heads, 64 nodes of 4 heads, 2048 pages, d = 128, 128 kept
+// (33.6 MB of bounds, 8.6 GFLOP): 33 us back to back.  Replayed alone from a graph, which adds some 4 us to each:
+// score 19.5 us, choose 14.5 us, pack 5.5 us.  The score kernel's SMs spend half their issue slots and the tensor pipe 24%: copies, queries' rounding (5 us
 // of set-up per CTA) and scores take turns on two row groups that read the same bounds.  The choosers are comparisons,
 // 13 warps per SM.
 #include <algorithm>

@@ -5,6 +5,7 @@ import itertools
 import numpy as np
 
 import oracle
+from oracle.page_select import grid_exponent
 
 
 def _table(rng, B, width):
@@ -88,3 +89,33 @@ def test_a_node_without_keys():
     out, lse, _ = oracle.tree_attention_sparse(np.ones((1, 2, 1, 2)), k, k, np.array([[0]]), [0],
                                                np.array([[[True, False], [False, False]]]), np.zeros((1, 1, 2, 1), bool), 1.0)
     assert (out[0, 1] == 0).all() and lse[0, 1, 0] == -np.inf and (out[0, 0] == 1).all()
+
+
+def test_the_query_itself_exceeds_the_score_by_half_a_step_at_most():
+    """The query is rounded to the nearest multiple of its step 2^e, so a channel is off by half of one at most: the
+    score of the query as it is differs by at most 2^(e-1) sum_c max(|hi_c|, |lo_c|), and a page is chosen in place of
+    another only where such scores are that close.  Queries with a few large channels among them."""
+    rng = np.random.default_rng(3)
+    nf, d, n = 24, 32, 8
+    above = 0
+    for big in (1.0, 30.0, 300.0):
+        k = rng.standard_normal((nf, 1, 2, d)) * np.exp(rng.standard_normal((nf, 1, 1, d)))
+        b = oracle.page_bounds(k, np.arange(nf).reshape(1, nf), [2 * nf], [0], np.zeros((nf, 1, 2, d)))[:, 0]
+        for _ in range(20):
+            q = rng.standard_normal(d)
+            q[:2] *= big
+            s = oracle.page_scores(q.reshape(1, 1, d), b[:, None], np.arange(nf), nf)[0, 0]
+            own = np.maximum(q * b[:, 0], q * b[:, 1]).sum(-1)
+            step = 2.0 ** grid_exponent(np.abs(q).max())
+            room = step / 2 * np.abs(b).max(1).sum(-1) * (1 + 1e-12)
+            assert (np.abs(s - own) <= room).all()
+            dots = (k[:, 0] @ q).max(1)
+            assert (dots <= s + room).all()
+            above += int((np.abs(s - own) > 0).any())
+            order = np.lexsort((np.arange(nf), -s))
+            best = np.lexsort((np.arange(nf), -own))[:n]
+            for p in order[:n]:
+                for other in best:
+                    if other not in order[:n]:
+                        assert own[other] - own[p] <= room[other] + room[p]
+    assert above > 50
