@@ -2,7 +2,8 @@
 // outwards to the page's power-of-two grid (page_grid.cuh) and kept in bf16.
 //
 // The K rows of the pages are read once (block_size * d values per page and head) and 2 d bf16 are
-// written, 1/16 of the bytes for 16-token bf16 pages: bound by HBM.  A warp owns one (page, head),
+// written, 1/8 of the bytes for 16-token bf16 pages: bound by HBM (4 x 32768 tokens, 8 KV heads, d = 128: bf16 50.9
+// us, 89% of the copy rate; fp32 87, some 98%).  A warp owns one (page, head),
 // whose block_size * d values are contiguous: its lanes take 16-byte chunks of consecutive rows (two
 // rows of d = 128 bf16 per load instruction), keep running extremes of their channels in
 // registers, and join across rows by shuffles.  No shared memory and no barrier, so a page's

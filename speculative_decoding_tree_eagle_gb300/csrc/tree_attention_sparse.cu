@@ -7,10 +7,11 @@
 // eight warps take four keys at a time, lanes across the head dim.  The 4 x 4 dot products are folded
 // by a reduce-scatter (16 shuffles instead of 80), so a lane ends with one (key, head) score, takes one
 // exponential, and hands its weight back by a shuffle.  Each warp keeps its own running maximum, sum and
-// output; they are joined through shared memory at the end.  Bound by load latency, shuffles and issue slots:
-// fp32, 14 heads on 2, d = 128, 16 sequences x 32 nodes over 64 of 256 16-token pages take 353 us (floor 11; 365
-// with loads of single elements), one node of 8 heads on 2 15 us as a cluster of eight CTAs (39 as one; a warp per
-// node and head that skipped pages as it met them took 8610 and 1119 us).
+// output; they are joined through shared memory at the end.  Bound by issue slots (72% of them busy, ncu), which
+// nodes that keep the same page spend once each: fp32, 14 heads on 2, d = 128, 16 sequences x 32 nodes over 64 of 256
+// 16-token pages take 355 us (floor 11; 365 with loads of single elements; bf16 at d = 64 248, floor 3), one node of 8
+// heads on 2 15 us as a cluster of eight CTAs (39 as one; a warp per node and head that skipped pages as it met them
+// took 8610 and 1119 us).
 #include <cmath>
 
 #include "common.cuh"

@@ -50,12 +50,14 @@
 // ts_tree_attention_sparse is the same kernel in its sparse mode (template parameter SP): the tiles are
 // taken from the pages that the nodes of one (sequence, KV head) chose together, then from the sequence's
 // own pages from the first incomplete one on (struct Span), and the softmax gives the keys of a page that
-// a row's node did not choose an infinite reference, so their weights are 0.  Its floor is the union's K/V,
-// read once; it computes every row against the whole union, so it is bound like the dense kernel, by the
-// softmax pipeline of a CTA (some 1750 cycles per 128 x 128 tile, 14000 of set-up and 6500 of epilogue
-// per CTA).  16 sequences x 60 nodes, 64 heads on 8, 128 of 2048 16-token pages per node (unions of 256):
-// 162 us, 0.27 GB of K/V at 1.7 TB/s, 0.81 PFLOP/s over the unions; dense attention takes 167 us over 4096
-// tokens, as many keys, and 1006 us over the 32768 that were chosen from.
+// a row's node did not choose an infinite reference, so their weights are 0.  As in the dense mode the weights
+// are rounded to bf16 for the P V product (one type for both operands, half a step of 2^-8 each), their sum is not:
+// outputs are 0.0023 from fp64 where one rounding at the end alone would be 0.0017 (relative, over a batch).
+// Its floor is the union's K/V, read once; it computes every row against the whole union.  16 sequences x 60 nodes, 64
+// heads on 8, 128 of 2048 16-token pages per node (unions of 256): 162 us, 0.27 GB of K/V at 1.7 TB/s, 0.81
+// PFLOP/s over the unions.  A CTA takes some 78000 cycles: 33 tiles of 128 x 128 at 1750 (their two products alone
+// 1300 at the measured tensor rate), 14000 of set-up and 6500 of epilogue; and 512 CTAs on 152 SMs pay 3.4 waves as 4.
+// Dense attention takes 167 us over 4096 tokens, as many keys, and 1006 us over the 32768 that were chosen from.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -120,7 +122,7 @@ struct Cfg {
   static constexpr uint32_t OFF_ML = OFF_MISC + 16;            // (max, sum) per row, cluster merge
   static constexpr uint32_t OFF_BLK = OFF_ML + BM * 8;
   static constexpr uint32_t SMEM_BYTES = OFF_BLK + 4 * kMaxChunkBoxes + 1024;  // + alignment slack
-  // sparse mode: a chunk's block ids and page bits (see sparse_smem) follow from OFF_BLK
+  // sparse mode: a chunk's block ids and page bits (as many as sparse_plan leaves room for) follow from OFF_BLK
   static constexpr uint32_t MAX_SMEM = 232448;
   static_assert(COL_P + 64 * 2 <= TMEM_COLS, "TMEM budget");
   static_assert(SK * KTILE >= BM * 512, "O rows must fit in the K ring for the merge");
