@@ -556,6 +556,7 @@ def tree_build_from_topk(row_tok: torch.Tensor, row_logp: torch.Tensor, root_tok
 # The six calls below check each tensor once (device, type, shape, layout) and run on the tensors' own device.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(i).cuda_stream without building a Stream object
+_INVALID = -1
 _I32, _I64, _BF16, _F32 = torch.int32, torch.int64, torch.bfloat16, torch.float32
 
 
@@ -609,8 +610,8 @@ def _scratch(nbytes: int, like: torch.Tensor, ws: Optional[torch.Tensor]):
 
 
 def _apart(out: Dict[str, torch.Tensor], may_be_same: Tuple[str, ...], **inputs: Optional[torch.Tensor]) -> None:
-    """Refuse outputs that share memory with an input or with one another; those named in ``may_be_same`` may be the
-    very buffer of the input of their name."""
+    """Name the outputs that share memory with an input or with one another; those in ``may_be_same`` may be the very
+    buffer of the input of their name.  (The library refuses such calls; this says why.)"""
     def memory(t):
         at = t.data_ptr()
         return at, at + t.numel() * t.element_size()
@@ -762,13 +763,14 @@ def kv_reserve(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
     if made:
         out = dict(block_table=torch.empty_like(block_table), refs=torch.empty_like(refs),
                    granted=torch.empty_like(prefix_len))
-    else:
+    ws, ws_bytes, keep = _scratch(need, refs, workspace)
+    rc = L.ts_kv_reserve(*args, freed_at, nfreed,
+                         *_out_args(out, ix, made, block_table=(_I32, table), refs=(_I32, (NB,)), granted=(_I32, (B,))), ws,
+                         ws_bytes, _status_arg(status, ix), _raw_stream(ix))
+    if rc == _INVALID and not made:
         _apart(out, ("block_table", "refs"), block_table=block_table, refs=refs, prefix_len=prefix_len, freed=freed,
                k_cache=k_cache, v_cache=v_cache)
-    ws, ws_bytes, keep = _scratch(need, refs, workspace)
-    _check(L.ts_kv_reserve(*args, freed_at, nfreed,
-                           *_out_args(out, ix, made, block_table=(_I32, table), refs=(_I32, (NB,)), granted=(_I32, (B,))), ws,
-                           ws_bytes, _status_arg(status, ix), _raw_stream(ix)))
+    _check(rc)
     return out
 
 
@@ -791,10 +793,11 @@ def kv_fork(block_table: torch.Tensor, prefix_len: torch.Tensor, refs: torch.Ten
     if made:
         out = dict(block_table=torch.empty((R, width), dtype=_I32, device=refs.device), prefix_len=torch.empty_like(src),
                    refs=torch.empty_like(refs))
-    else:
+    rc = L.ts_kv_fork(*args, *_out_args(out, ix, made, block_table=(_I32, (R, width)), prefix_len=(_I32, (R,)),
+                                        refs=(_I32, (NB,))), _status_arg(status, ix), _raw_stream(ix))
+    if rc == _INVALID and not made:
         _apart(out, ("refs",), block_table=block_table, prefix_len=prefix_len, refs=refs, src=src)
-    _check(L.ts_kv_fork(*args, *_out_args(out, ix, made, block_table=(_I32, (R, width)), prefix_len=(_I32, (R,)),
-                                          refs=(_I32, (NB,))), _status_arg(status, ix), _raw_stream(ix)))
+    _check(rc)
     return out
 
 
@@ -820,9 +823,10 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
     if made:
         out = dict(block_table=torch.empty_like(block_table), refs=torch.empty_like(refs), remap=torch.empty_like(refs),
                    live=torch.empty((1,), dtype=_I32, device=refs.device))
-    else:
-        _apart(out, ("block_table", "refs"), block_table=block_table, refs=refs, k_cache=k_cache, v_cache=v_cache, bounds=bounds)
     ws, ws_bytes, keep = _scratch(L.ts_kv_compact_workspace(NB), refs, workspace)
-    _check(L.ts_kv_compact(*args, *_out_args(out, ix, made, block_table=(_I32, table), refs=(_I32, (NB,)),
-                                             remap=(_I32, (NB,)), live=(_I32, (1,))), ws, ws_bytes, _status_arg(status, ix), _raw_stream(ix)))
+    rc = L.ts_kv_compact(*args, *_out_args(out, ix, made, block_table=(_I32, table), refs=(_I32, (NB,)),
+                                           remap=(_I32, (NB,)), live=(_I32, (1,))), ws, ws_bytes, _status_arg(status, ix), _raw_stream(ix))
+    if rc == _INVALID and not made:
+        _apart(out, ("block_table", "refs"), block_table=block_table, refs=refs, k_cache=k_cache, v_cache=v_cache, bounds=bounds)
+    _check(rc)
     return out
