@@ -13,6 +13,9 @@
  *   ts_kv_page_bounds          per-page bounds of the keys
  *   ts_page_select             the pages each node attends to, by a bound of its rounded query's scores
  *   ts_tree_attention_sparse   tree attention over the chosen pages
+ * A cache in 8 bits: e4m3 codes beside a scale for each block of tokens and head
+ *   ts_kv_write_fp8, ts_kv_read_fp8, ts_kv_commit_fp8   write, read back, keep the accepted path
+ *   ts_tree_attention_fp8      tree attention over it
  * The page pool
  *   ts_kv_reserve, ts_kv_fork, ts_kv_compact   hand out, share, copy, free and move pages
  *
@@ -26,7 +29,7 @@
  *     pointers return TS_ERR_INVALID, sizes outside the supported range return
  *     TS_ERR_UNSUPPORTED, a too-small workspace returns TS_ERR_WORKSPACE.  Nothing is
  *     launched in those cases.  A failed launch returns TS_ERR_CUDA.
- *   - ts_kv_page_bounds, ts_page_select, ts_tree_attention_sparse and the page pool refuse outputs
+ *   - ts_kv_page_bounds, ts_page_select, ts_tree_attention_sparse, the calls on 8-bit caches and the page pool refuse outputs
  *     (and workspaces) that share memory with an input or another output, but for those of the
  *     pool that may be their input's buffer: TS_ERR_INVALID.
  *   - Problems the host cannot see (a block id out of range, a parent index that does
@@ -532,6 +535,92 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
                              const int32_t* count, const uint64_t* node_mask, int C,
                              int B, int m, int Hq, int Hkv, int d, float scale, void* out, float* lse,
                              void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * The cache in 8 bits.  The pages (web sources) have no counterpart: a verify pass over a long prefix is bound by the
+ * bytes of K and V, and these calls halve them.
+ *
+ * k_cache, v_cache [num_blocks, Hkv, block_size, d] hold e4m3 codes (one byte; the finite-only "fn" kind, largest value
+ * 448, 0x7f and 0xff NaN), k_scale, v_scale [num_blocks, Hkv, block_size / scale_block] fp32: scale_block consecutive rows of a
+ * page share one scale per KV head (scale_block divides block_size; 1 gives every token its own).  value = code * scale.
+ * Scales are read clamped to [2^-40, 2^40] (NaN, zero and negative count as 2^-40).
+ *
+ * Quantising a block (one scale; K and V apart) over the values of its rows:
+ *   2^e  = the smallest power of two, -40 <= e <= 40, with |value| <= 448 * 2^e for all of them (NaN passed over)
+ *   code = e4m3(value * 2^-e), to nearest even, saturated to +-448 (infinities too); NaN stays NaN.   scale = 2^e
+ * A code times its scale is exact in bf16.  Rows that are quantised again under another scale keep their values but for what
+ * falls among e4m3's subnormals.
+ * --------------------------------------------------------------------------------- */
+
+/*
+ * ts_kv_write_fp8 — rows of K and V into the cache.
+ *
+ * For every sequence b the rows 0 .. length[b] - 1 of k[b], v[b] become positions start_len[b] .. of the sequence.  Every block
+ * of scale_block positions that gets a new row is quantised over its kept rows (positions below start_len[b], value = code *
+ * scale) and its new ones.  The sequence ends behind the write: rows further back in its last block keep their bytes and lose
+ * their meaning.  Blocks that get no row are not touched.
+ *
+ * k, v        [B, n, Hkv, d] (dt), any layout with contiguous head rows: k_strides, v_strides [3] (host) are the elements between
+ *             sequences, rows and heads (>= 0), so k and v may be slices of a fused projection's output.
+ * block_table [B, max_blocks], start_len [B], length [B] int32 (NULL: n each), 0 <= length <= n.
+ * A page that is written must belong to one sequence alone (ts_kv_reserve sees to that).  Any d <= 256.  One launch.
+ * Device errors, TS_ERR_DEVICE_CHECK: a negative start, a length outside [0, n] or positions beyond max_blocks * block_size (the
+ * sequence is skipped); a page id out of range (its rows are skipped).
+ */
+int ts_kv_write_fp8(const void* k, const void* v, ts_dtype dt, const int64_t* k_strides, const int64_t* v_strides, void* k_cache,
+                    void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size, int scale_block, int Hkv,
+                    int d, const int32_t* block_table, int max_blocks, const int32_t* start_len, const int32_t* length, int B,
+                    int n, int32_t* dev_status, void* stream);
+
+/*
+ * ts_kv_read_fp8 — values of the cache.
+ *
+ * k, v [B, n, Hkv, d] (dt): row t holds the value (code * scale, rounded to dt) of position start_len[b] + t where that is below
+ * prefix_len[b], 0 otherwise.  start_len NULL: 0.  Any d <= 256.  One launch.
+ * Device errors, TS_ERR_DEVICE_CHECK: a negative length or start, or a prefix beyond max_blocks * block_size (the rows are 0); a
+ * page id out of range (its rows are 0).
+ */
+int ts_kv_read_fp8(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, int num_blocks,
+                   int block_size, int scale_block, int Hkv, int d, const int32_t* block_table, int max_blocks,
+                   const int32_t* prefix_len, const int32_t* start_len, int B, int n, void* k, void* v, ts_dtype dt,
+                   int32_t* dev_status, void* stream);
+
+/*
+ * ts_kv_commit_fp8 — ts_kv_commit on an 8-bit cache.
+ *
+ * The values of the accepted rows (positions prefix_len[b] + accept_path[b][j]) become positions prefix_len[b] + j, quantised as
+ * ts_kv_write_fp8 would quantise them (kept rows below prefix_len[b], new ones behind): rejected rows no longer weigh on a block's
+ * scale.  Table, lengths and released pages as ts_kv_commit, but the old state is read and the new one written:
+ * block_table_out and prefix_len_out may be block_table and prefix_len themselves, for an update in place, or others, for the
+ * next layer's cache to be committed from the same old state.
+ *
+ * freed_blocks [B, max_blocks], freed_count [B].  m <= TS_MAX_NODES, any d <= 256.  Two launches, no workspace.
+ * Device errors: as ts_kv_commit (the sequence's cache is left untouched, its table row and length are copied).
+ */
+int ts_kv_commit_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size,
+                     int scale_block, int Hkv, int d, const int32_t* block_table, int max_blocks, const int32_t* prefix_len,
+                     const int32_t* accept_path, const int32_t* accept_len, int B, int m, int32_t* block_table_out,
+                     int32_t* prefix_len_out, int32_t* freed_blocks, int32_t* freed_count, int32_t* dev_status, void* stream);
+
+/*
+ * ts_tree_attention_fp8 — ts_tree_attention over an 8-bit cache.
+ *
+ * Arguments, layouts and results as ts_tree_attention with k = code * scale, v = code * scale; a node without any key (a mask row
+ * without its own bit and an empty prefix) gets out 0 and lse -inf.  scale finite, > 0.  What lies in places that a node does not
+ * attend to (NaN codes among them) does not reach its output; a NaN or an infinity in a query makes that row NaN.
+ * Supported: fp32 and bf16, any d <= 256 and any block_size on the CUDA cores (fp32 arithmetic throughout); bf16 with d == 128
+ * and block_size in {16, 32, 64, 128} on the tensor cores (queries split exactly into two 8-bit parts, weights rounded to fp16 for
+ * the product with V, sums in fp32).  max_prefix <= 2^30.
+ * workspace: ts_tree_attention_fp8_workspace(...) bytes, 16-byte aligned (not read where that is 256 or less).
+ * Device errors, TS_ERR_DEVICE_CHECK: a prefix_len outside [0, max_prefix] or beyond max_blocks * block_size - m (the rows of that
+ * sequence are not written), a page id out of range (its keys are left out); a wait over its time bound -> TS_ERR_TIMEOUT.
+ */
+size_t ts_tree_attention_fp8_workspace(ts_dtype dt, int B, int m, int Hq, int Hkv, int d, int max_prefix, int block_size);
+int ts_tree_attention_fp8(const void* q, ts_dtype dt, const void* k_cache, const void* v_cache, const float* k_scale,
+                          const float* v_scale, int num_blocks, int block_size, int scale_block, const int32_t* block_table,
+                          int max_blocks, const int32_t* prefix_len, int max_prefix, const uint64_t* mask, int B, int m,
+                          int Hq, int Hkv, int d, float scale, void* out, float* lse, void* workspace, size_t ws_bytes,
+                          int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------------------
  * The page pool.  refs [num_blocks] int32 counts, for each page, the block-table entries that

@@ -23,6 +23,7 @@ Plain, slow, obviously-correct numpy restatements of what the pages define:
   attention over the chosen pages (no counterpart on the pages).
 * :mod:`oracle.page_pool`    — the page pool: reserve, fork, compact ("lesty.tech", section 8 for the
   reserved and released pages; the rest has no counterpart).
+* :mod:`oracle.kv_fp8`       — a cache in 8 bits: write, read, commit and tree attention (no counterpart).
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and the CPU-baseline leg of
 ``bench.py`` may import this package.  The product (the CUDA library and its
@@ -42,3 +43,4 @@ from .accept_sample import accept_sample, softmax_t  # noqa: F401
 from .tree_prune import tree_prune  # noqa: F401
 from .page_select import page_bounds, page_select, page_scores, grid_query, tree_attention_sparse  # noqa: F401
 from . import page_pool  # noqa: F401
+from . import kv_fp8  # noqa: F401

@@ -17,9 +17,11 @@ and the tree from its lists), ``tree_accept_sample`` (acceptance at temperature 
 ``tree_prune`` (cost-aware pruning before verification).
 
 Long contexts: ``kv_page_bounds`` (per-page bounds of the keys), ``page_select`` (the pages each
-node attends to) and ``tree_attention_sparse`` (tree attention over them).  The page pool:
+node attends to) and ``tree_attention_sparse`` (tree attention over them).  A cache in 8 bits, e4m3
+codes beside a scale for each block of tokens and head: ``kv_write_fp8``, ``kv_read_fp8``,
+``kv_commit_fp8`` and ``tree_attention_fp8``.  The page pool:
 ``kv_reserve`` (room for the next tokens), ``kv_fork`` (fork, reorder and drop sequences) and
-``kv_compact`` (move the pages in use together).  These six run on the tensors' device, which need
+``kv_compact`` (move the pages in use together).  These ten run on the tensors' device, which need
 not be the current one, on that device's current stream, and take their workspace from torch's
 allocator call by call, so calls on several streams or in several captured graphs share none.
 """
@@ -38,6 +40,7 @@ __all__ = [
     "tree_build", "tree_attention", "tree_accept", "kv_commit", "lm_head_argmax", "tree_accept_hidden",
     "efficient_head", "tree_build_from_topk", "tree_accept_sample", "tree_prune",
     "kv_page_bounds", "page_select", "tree_attention_sparse", "kv_reserve", "kv_fork", "kv_compact",
+    "kv_write_fp8", "kv_read_fp8", "kv_commit_fp8", "tree_attention_fp8",
     "new_status", "check_status",
     "tree_build_workspace", "tree_attention_workspace", "tree_accept_workspace", "tree_attention_plan",
 ]
@@ -136,6 +139,16 @@ def library():
         L.ts_kv_compact_workspace.argtypes = [I]
         L.ts_kv_compact.restype = I
         L.ts_kv_compact.argtypes = [P, P, I, P, I, I, I, I, P, I, P, I, P, P, P, P, P, S, P, P]
+        L.ts_kv_write_fp8.restype = I
+        L.ts_kv_write_fp8.argtypes = [P, P, I, P, P, P, P, P, P, I, I, I, I, I, P, I, P, P, I, I, P, P]
+        L.ts_kv_read_fp8.restype = I
+        L.ts_kv_read_fp8.argtypes = [P, P, P, P, I, I, I, I, I, P, I, P, P, I, I, P, P, I, P, P]
+        L.ts_kv_commit_fp8.restype = I
+        L.ts_kv_commit_fp8.argtypes = [P, P, P, P, I, I, I, I, I, P, I, P, P, P, I, I, P, P, P, P, P, P]
+        L.ts_tree_attention_fp8_workspace.restype = S
+        L.ts_tree_attention_fp8_workspace.argtypes = [I, I, I, I, I, I, I, I]
+        L.ts_tree_attention_fp8.restype = I
+        L.ts_tree_attention_fp8.argtypes = [P, I, P, P, P, P, I, I, I, P, I, P, I, P, I, I, I, I, I, F, P, P, P, S, P, P]
         _lib = L
     return _lib
 
@@ -553,11 +566,12 @@ def tree_build_from_topk(row_tok: torch.Tensor, row_logp: torch.Tensor, root_tok
     return out
 
 
-# The six calls below check each tensor once (device, type, shape, layout) and run on the tensors' own device.
+# The calls below check each tensor once (device, type, shape, layout) and run on the tensors' own device.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(i).cuda_stream without building a Stream object
 _INVALID = -1
 _I32, _I64, _BF16, _F32 = torch.int32, torch.int64, torch.bfloat16, torch.float32
+_E4M3 = torch.float8_e4m3fn
 
 
 def _refuse(name: str, t: torch.Tensor, index: int, dtype, shape) -> None:
@@ -830,3 +844,155 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
         _apart(out, ("block_table", "refs"), block_table=block_table, refs=refs, k_cache=k_cache, v_cache=v_cache, bounds=bounds)
     _check(rc)
     return out
+
+
+def _fp8_cache(k_cache, v_cache, k_scale, v_scale, ix):
+    """Addresses and sizes of an 8-bit cache: codes [num_blocks,Hkv,bs,d] e4m3, scales [num_blocks,Hkv,bs/sb] fp32."""
+    NB, Hkv, bs, d = cache = k_cache.shape
+    if k_scale.dim() != 3 or k_scale.shape[2] < 1 or bs % k_scale.shape[2]:
+        raise ValueError(f"k_scale must have shape [{NB}, {Hkv}, a divisor of {bs}], got {list(k_scale.shape)}")
+    scales = (NB, Hkv, k_scale.shape[2])
+    at = [_arg("k_cache", k_cache, ix, _E4M3, cache), _arg("v_cache", v_cache, ix, _E4M3, cache),
+          _arg("k_scale", k_scale, ix, _F32, scales), _arg("v_scale", v_scale, ix, _F32, scales)]
+    return at, (NB, bs, bs // scales[2], Hkv, d)
+
+
+def _rows_arg(name: str, t: torch.Tensor, ix: int, dtype, shape):
+    """The address and strides (sequences, rows, heads) of a tensor whose head rows are contiguous."""
+    if t.get_device() != ix or t.dtype is not dtype or t.shape != shape:
+        _refuse(name, t.contiguous(), ix, dtype, shape)
+    if t.stride(3) != 1 and shape[3] != 1:
+        raise ValueError(f"{name} must have contiguous head rows, got strides {list(t.stride())}")
+    return t.data_ptr(), (ctypes.c_int64 * 3)(*t.stride()[:3])
+
+
+def kv_write_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor, block_table: torch.Tensor, start_len: torch.Tensor, *,
+                 length: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> None:
+    """Quantise rows of k, v [B,n,Hkv,d] (bf16 or fp32; strides are free but for contiguous head rows) into the cache, in
+    place: codes k_cache, v_cache [num_blocks,Hkv,bs,d] float8_e4m3fn and scales k_scale, v_scale [num_blocks,Hkv,bs/sb]
+    fp32, one for every sb tokens of a page and head.  Row t of sequence b becomes position start_len[b] + t, t < length[b]
+    (default: n).  A block's scale is the smallest power of two (2^-40 to 2^40) that brings its rows, those below start_len
+    and the new ones, to at most 448; the sequence ends behind the write."""
+    L = library()
+    ix = _index_of("k_cache", k_cache, 4)
+    if ix != torch.cuda.current_device():
+        with torch.cuda.device(ix):
+            return kv_write_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start_len, length=length, status=status)
+    cache, sizes = _fp8_cache(k_cache, v_cache, k_scale, v_scale, ix)
+    B, width = block_table.shape
+    if k.dim() != 4:
+        raise ValueError(f"k must have 4 dimensions, got {list(k.shape)}")
+    dt, shape = _dt(k), (B, k.shape[1], *k_cache.shape[1::2])
+    k_at, k_strides = _rows_arg("k", k, ix, k.dtype, shape)
+    v_at, v_strides = _rows_arg("v", v, ix, k.dtype, shape)
+    _check(L.ts_kv_write_fp8(k_at, v_at, dt, k_strides, v_strides, *cache, *sizes,
+                             _arg("block_table", block_table, ix, _I32, (B, width)), width,
+                             _arg("start_len", start_len, ix, _I32, (B,)),
+                             None if length is None else _arg("length", length, ix, _I32, (B,)), B, shape[1],
+                             _status_arg(status, ix), _raw_stream(ix)))
+
+
+def kv_read_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                block_table: torch.Tensor, prefix_len: torch.Tensor, n: int, *, start_len: Optional[torch.Tensor] = None,
+                dtype: torch.dtype = torch.bfloat16, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The values k, v [B,n,Hkv,d] (bf16, in which they are exact, or fp32) of positions start_len[b] .. start_len[b] + n - 1
+    (default: from 0); rows at and behind prefix_len[b] are 0."""
+    L = library()
+    ix = _index_of("k_cache", k_cache, 4)
+    if ix != torch.cuda.current_device():
+        with torch.cuda.device(ix):
+            return kv_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, n, start_len=start_len, dtype=dtype,
+                               out=out, status=status)
+    cache, sizes = _fp8_cache(k_cache, v_cache, k_scale, v_scale, ix)
+    B, width = block_table.shape
+    shape = (B, n, *k_cache.shape[1::2])
+    if out is None:
+        k, v = (torch.empty(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
+    else:
+        k, v = out
+        dtype = k.dtype
+    dt = _dt(k)
+    _check(L.ts_kv_read_fp8(*cache, *sizes, _arg("block_table", block_table, ix, _I32, (B, width)), width,
+                            _arg("prefix_len", prefix_len, ix, _I32, (B,)),
+                            None if start_len is None else _arg("start_len", start_len, ix, _I32, (B,)), B, n,
+                            _arg("k", k, ix, dtype, shape), _arg("v", v, ix, dtype, shape), dt, _status_arg(status, ix),
+                            _raw_stream(ix)))
+    return k, v
+
+
+def kv_commit_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                  block_table: torch.Tensor, prefix_len: torch.Tensor, accept_path: torch.Tensor, accept_len: torch.Tensor, *,
+                  out: Optional[Dict[str, torch.Tensor]] = None,
+                  status: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
+    """kv_commit on an 8-bit cache: the accepted path's rows move in the caches (in place, quantised again with the block they
+    move to).  Returns the new block_table and prefix_len, freed_blocks [B,max_blocks] (-1 padded) and freed_count [B].
+    In ``out``, block_table and prefix_len may be the input tensors themselves; otherwise the outputs lie apart from the
+    inputs and from one another."""
+    L = library()
+    ix = _index_of("k_cache", k_cache, 4)
+    if ix != torch.cuda.current_device():
+        with torch.cuda.device(ix):
+            return kv_commit_fp8(k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, accept_path, accept_len, out=out,
+                                 status=status)
+    cache, sizes = _fp8_cache(k_cache, v_cache, k_scale, v_scale, ix)
+    B, width = table = block_table.shape
+    m = accept_path.shape[1]
+    args = [*cache, *sizes, _arg("block_table", block_table, ix, _I32, table), width,
+            _arg("prefix_len", prefix_len, ix, _I32, (B,)), _arg("accept_path", accept_path, ix, _I32, (B, m)),
+            _arg("accept_len", accept_len, ix, _I32, (B,)), B, m]
+    made = out is None
+    if made:
+        out = dict(block_table=torch.empty_like(block_table), prefix_len=torch.empty_like(prefix_len),
+                   freed_blocks=torch.empty_like(block_table), freed_count=torch.empty_like(prefix_len))
+    rc = L.ts_kv_commit_fp8(*args, *_out_args(out, ix, made, block_table=(_I32, table), prefix_len=(_I32, (B,)),
+                                              freed_blocks=(_I32, table), freed_count=(_I32, (B,))), _status_arg(status, ix),
+                            _raw_stream(ix))
+    if rc == _INVALID and not made:
+        _apart(out, ("block_table", "prefix_len"), block_table=block_table, prefix_len=prefix_len, accept_path=accept_path,
+               accept_len=accept_len, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    _check(rc)
+    return out
+
+
+def tree_attention_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                       v_scale: torch.Tensor, block_table: torch.Tensor, prefix_len: torch.Tensor, mask: torch.Tensor, *,
+                       max_prefix: int, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                       lse: Optional[torch.Tensor] = None, with_lse: bool = True, workspace: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None):
+    """Tree attention over an 8-bit cache (codes float8_e4m3fn and scales fp32, as kv_write_fp8 fills them).  q
+    [B,m,Hq,d] bf16 or fp32; the rest as ``tree_attention``.  Returns (out, lse)."""
+    L = library()
+    ix = _index_of("q", q, 4)
+    if ix != torch.cuda.current_device():
+        with torch.cuda.device(ix):
+            return tree_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, mask, max_prefix=max_prefix,
+                                      scale=scale, out=out, lse=lse, with_lse=with_lse, workspace=workspace, status=status)
+    dtype, dt = q.dtype, _dt(q)
+    B, m, Hq, d = shape = q.shape
+    _index_of("k_cache", k_cache, 4)
+    cache, (NB, bs, sb, Hkv, d2) = _fp8_cache(k_cache, v_cache, k_scale, v_scale, ix)
+    if d2 != d:
+        raise ValueError("cache shapes do not match q")
+    width = block_table.shape[1]
+    # (given ones are checked, new ones are not)
+    out_at = None if out is None else _arg("out", out, ix, dtype, shape)
+    lse_at = None if lse is None else _arg("lse", lse, ix, _F32, (B, m, Hq))
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out_at = out.data_ptr()
+    if lse is None and with_lse:
+        lse = torch.empty((B, m, Hq), dtype=_F32, device=q.device)
+        lse_at = lse.data_ptr()
+    need = L.ts_tree_attention_fp8_workspace(dt, B, m, Hq, Hkv, d, max_prefix, bs)
+    if need == 0:
+        raise TreeSpecError("invalid tree_attention_fp8 sizes")
+    ws, ws_bytes, keep = _scratch(need, q, workspace) if need > 256 else (None, 0, None)
+    _check(L.ts_tree_attention_fp8(_arg("q", q, ix, dtype, shape), dt, *cache, NB, bs, sb,
+                                   _arg("block_table", block_table, ix, _I32, (B, width)), width,
+                                   _arg("prefix_len", prefix_len, ix, _I32, (B,)), max_prefix,
+                                   _arg("mask", mask, ix, _I64, (B, m, (m + 63) // 64)), B, m, Hq, Hkv, d,
+                                   1.0 / math.sqrt(d) if scale is None else scale, out_at, lse_at, ws, ws_bytes,
+                                   _status_arg(status, ix), _raw_stream(ix)))
+    return out, lse

@@ -524,6 +524,168 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
   return ts::attention_sparse_tc_launch(a, static_cast<cudaStream_t>(stream), sms);
 }
 
+// What the calls on 8-bit caches share.
+static int check_fp8(int num_blocks, int block_size, int scale_block, int Hkv, int d, int max_blocks, int B) {
+  const int rc = check_cache(TS_F32, num_blocks, block_size, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  if (scale_block <= 0 || block_size % scale_block != 0) return TS_ERR_INVALID;
+  if (d > 256 || Hkv > 65535 / 2) return TS_ERR_UNSUPPORTED;
+  return TS_OK;
+}
+// Elements from a strided tensor's first to its last, and one.
+static size_t extent(const int64_t* strides, int B, int n, int Hkv, int d) {
+  return static_cast<size_t>((B - 1) * strides[0] + (n - 1) * strides[1] + (Hkv - 1) * strides[2] + d);
+}
+
+int ts_kv_write_fp8(const void* k, const void* v, ts_dtype dt, const int64_t* k_strides, const int64_t* v_strides, void* k_cache,
+                    void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size, int scale_block, int Hkv,
+                    int d, const int32_t* block_table, int max_blocks, const int32_t* start_len, const int32_t* length, int B,
+                    int n, int32_t* dev_status, void* stream) {
+  const int rc = check_fp8(num_blocks, block_size, scale_block, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  if ((dt != TS_F32 && dt != TS_BF16) || n <= 0) return TS_ERR_INVALID;
+  if (!k || !v || !k_strides || !v_strides || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !start_len)
+    return TS_ERR_INVALID;
+  const size_t size = dt == TS_BF16 ? 2 : 4;
+  ts::Fp8WriteCall c{k, v, dt, {}, {}, k_cache, v_cache, k_scale, v_scale, num_blocks, block_size, scale_block, Hkv, d,
+                     block_table, max_blocks, start_len, length, B, n, dev_status};
+  for (int i = 0; i < 3; ++i) {
+    if (k_strides[i] < 0 || v_strides[i] < 0 || k_strides[i] > (1LL << 40) || v_strides[i] > (1LL << 40)) return TS_ERR_INVALID;
+    c.k_stride[i] = k_strides[i];
+    c.v_stride[i] = v_strides[i];
+  }
+  if (reinterpret_cast<uintptr_t>(k) % size != 0 || reinterpret_cast<uintptr_t>(v) % size != 0 || !aligned4_ptr(k_scale) ||
+      !aligned4_ptr(v_scale))
+    return TS_ERR_INVALID;
+  const size_t cache = times(num_blocks, Hkv, block_size, d), scales = times(num_blocks, Hkv, block_size / scale_block);
+  if (!outputs_apart({{k_cache, cache, 1}, {v_cache, cache, 1}, {k_scale, scales, 4}, {v_scale, scales, 4}},
+                     {{k, extent(k_strides, B, n, Hkv, d), size},
+                      {v, extent(v_strides, B, n, Hkv, d), size},
+                      {block_table, times(B, max_blocks), 4},
+                      {start_len, times(B, 1), 4},
+                      {length, times(B, 1), 4}}))
+    return TS_ERR_INVALID;
+  return ts::kv_write_fp8_launch(c, static_cast<cudaStream_t>(stream));
+}
+
+int ts_kv_read_fp8(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, int num_blocks,
+                   int block_size, int scale_block, int Hkv, int d, const int32_t* block_table, int max_blocks,
+                   const int32_t* prefix_len, const int32_t* start_len, int B, int n, void* k, void* v, ts_dtype dt,
+                   int32_t* dev_status, void* stream) {
+  const int rc = check_fp8(num_blocks, block_size, scale_block, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  if ((dt != TS_F32 && dt != TS_BF16) || n <= 0) return TS_ERR_INVALID;
+  if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !prefix_len) return TS_ERR_INVALID;
+  const size_t size = dt == TS_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(k) % size != 0 || reinterpret_cast<uintptr_t>(v) % size != 0 || !aligned4_ptr(k_scale) ||
+      !aligned4_ptr(v_scale))
+    return TS_ERR_INVALID;
+  const size_t cache = times(num_blocks, Hkv, block_size, d), scales = times(num_blocks, Hkv, block_size / scale_block);
+  const size_t rows = times(B, n, Hkv, d);
+  if (!outputs_apart({{k, rows, size}, {v, rows, size}},
+                     {{k_cache, cache, 1},
+                      {v_cache, cache, 1},
+                      {k_scale, scales, 4},
+                      {v_scale, scales, 4},
+                      {block_table, times(B, max_blocks), 4},
+                      {prefix_len, times(B, 1), 4},
+                      {start_len, times(B, 1), 4}}))
+    return TS_ERR_INVALID;
+  const int sms = ts::device_sm_count();
+  if (sms <= 0) return TS_ERR_CUDA;
+  ts::Fp8ReadCall c{k_cache, v_cache, k_scale, v_scale, num_blocks, block_size, scale_block, Hkv, d, block_table, max_blocks,
+                    prefix_len, start_len, B, n, k, v, dt, dev_status};
+  return ts::kv_read_fp8_launch(c, static_cast<cudaStream_t>(stream), sms);
+}
+
+int ts_kv_commit_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size,
+                     int scale_block, int Hkv, int d, const int32_t* block_table, int max_blocks, const int32_t* prefix_len,
+                     const int32_t* accept_path, const int32_t* accept_len, int B, int m, int32_t* block_table_out,
+                     int32_t* prefix_len_out, int32_t* freed_blocks, int32_t* freed_count, int32_t* dev_status, void* stream) {
+  const int rc = check_fp8(num_blocks, block_size, scale_block, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  if (m <= 0) return TS_ERR_INVALID;
+  if (m > TS_MAX_NODES) return TS_ERR_UNSUPPORTED;
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !prefix_len || !accept_path || !accept_len ||
+      !block_table_out || !prefix_len_out || !freed_blocks || !freed_count)
+    return TS_ERR_INVALID;
+  if (!aligned4_ptr(k_scale) || !aligned4_ptr(v_scale)) return TS_ERR_INVALID;
+  const size_t cache = times(num_blocks, Hkv, block_size, d), scales = times(num_blocks, Hkv, block_size / scale_block);
+  const size_t cells = times(B, max_blocks), rows = B;
+  if (!outputs_apart({{k_cache, cache, 1},
+                      {v_cache, cache, 1},
+                      {k_scale, scales, 4},
+                      {v_scale, scales, 4},
+                      {block_table_out, cells, 4},
+                      {prefix_len_out, rows, 4},
+                      {freed_blocks, cells, 4},
+                      {freed_count, rows, 4}},
+                     {{block_table_out == block_table ? nullptr : block_table, cells, 4},
+                      {prefix_len_out == prefix_len ? nullptr : prefix_len, rows, 4},
+                      {accept_path, times(B, m), 4},
+                      {accept_len, rows, 4}}))
+    return TS_ERR_INVALID;
+  ts::Fp8CommitCall c{k_cache, v_cache, k_scale, v_scale, num_blocks, block_size, scale_block, Hkv, d, block_table, max_blocks,
+                      prefix_len, accept_path, accept_len, B, m, block_table_out, prefix_len_out, freed_blocks, freed_count,
+                      dev_status};
+  return ts::kv_commit_fp8_launch(c, static_cast<cudaStream_t>(stream));
+}
+
+static int check_attention_fp8(ts_dtype dt, int B, int m, int Hq, int Hkv, int d, int max_prefix, int block_size) {
+  const int rc = ts::check_attention(dt, B, m, Hq, Hkv, d, max_prefix);
+  if (rc != TS_OK) return rc;
+  if (block_size <= 0) return TS_ERR_INVALID;
+  if (max_prefix > (1 << 30)) return TS_ERR_UNSUPPORTED;  // positions and their tiles are counted in 32 bits
+  return TS_OK;
+}
+
+size_t ts_tree_attention_fp8_workspace(ts_dtype dt, int B, int m, int Hq, int Hkv, int d, int max_prefix, int block_size) {
+  if (check_attention_fp8(dt, B, m, Hq, Hkv, d, max_prefix, block_size) != TS_OK) return 0;
+  const int sms = ts::device_sm_count();
+  return ts::attention_fp8_uses_tc(dt, d, block_size) ? ts::attention_fp8_tc_workspace_bytes(B, m, Hq, Hkv, max_prefix, sms)
+                                                      : ts::attention_fp8_simt_workspace_bytes(B, m, Hq, Hkv, d, max_prefix, sms);
+}
+
+int ts_tree_attention_fp8(const void* q, ts_dtype dt, const void* k_cache, const void* v_cache, const float* k_scale,
+                          const float* v_scale, int num_blocks, int block_size, int scale_block, const int32_t* block_table,
+                          int max_blocks, const int32_t* prefix_len, int max_prefix, const uint64_t* mask, int B, int m,
+                          int Hq, int Hkv, int d, float scale, void* out, float* lse, void* workspace, size_t ws_bytes,
+                          int32_t* dev_status, void* stream) {
+  int rc = check_attention_fp8(dt, B, m, Hq, Hkv, d, max_prefix, block_size);
+  if (rc != TS_OK) return rc;
+  rc = check_fp8(num_blocks, block_size, scale_block, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !prefix_len || !mask || !out) return TS_ERR_INVALID;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return TS_ERR_INVALID;
+  const size_t size = dt == TS_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(q) % size != 0 || reinterpret_cast<uintptr_t>(out) % size != 0 || !aligned4_ptr(k_scale) ||
+      !aligned4_ptr(v_scale))
+    return TS_ERR_INVALID;
+  const bool tc = ts::attention_fp8_uses_tc(dt, d, block_size);
+  if (tc && (!aligned16_ptr(q) || !aligned16_ptr(k_cache) || !aligned16_ptr(v_cache) || !aligned16_ptr(out))) return TS_ERR_INVALID;
+  const size_t need = ts_tree_attention_fp8_workspace(dt, B, m, Hq, Hkv, d, max_prefix, block_size);
+  if (need > 256 && (!workspace || ws_bytes < need)) return TS_ERR_WORKSPACE;
+  if (need > 256 && !aligned16_ptr(workspace)) return TS_ERR_INVALID;
+  const size_t rows = times(B, m, Hq), cache = times(num_blocks, Hkv, block_size, d);
+  const size_t scales = times(num_blocks, Hkv, block_size / scale_block);
+  if (!outputs_apart({{out, rows * d, size}, {lse, rows, 4}, {workspace, need > 256 ? need : 0, 1}},
+                     {{q, rows * d, size},
+                      {k_cache, cache, 1},
+                      {v_cache, cache, 1},
+                      {k_scale, scales, 4},
+                      {v_scale, scales, 4},
+                      {block_table, times(B, max_blocks), 4},
+                      {prefix_len, times(B, 1), 4},
+                      {mask, times(B, m, (m + 63) / 64), 8}}))
+    return TS_ERR_INVALID;
+  const int sms = ts::device_sm_count();
+  if (sms <= 0) return TS_ERR_CUDA;
+  ts::Fp8AttnCall a{q, dt, k_cache, v_cache, k_scale, v_scale, num_blocks, block_size, scale_block, block_table, max_blocks,
+                    prefix_len, max_prefix, mask, B, m, Hq, Hkv, d, scale, out, lse, workspace, dev_status};
+  return tc ? ts::attention_fp8_tc_launch(a, static_cast<cudaStream_t>(stream), sms)
+            : ts::attention_fp8_simt_launch(a, static_cast<cudaStream_t>(stream), sms);
+}
+
 size_t ts_kv_reserve_workspace(int num_blocks, int block_size, int B, int n) {
   if (num_blocks <= 0 || block_size <= 0 || B <= 0 || n <= 0 || B > TS_MAX_POOL_ROWS) return 0;
   return ts::kv_reserve_workspace_bytes(num_blocks, block_size, B, n);

@@ -168,6 +168,90 @@ int attention_sparse_simt_launch(const SparseCall& a, cudaStream_t stream, int n
 size_t attention_sparse_tc_workspace_bytes(int B, int m, int Hq, int Hkv, int C, int block_size, int num_sms);
 int attention_sparse_tc_launch(const SparseCall& a, cudaStream_t stream, int num_sms);
 
+// The paged cache in 8 bits (kv_fp8.cu) and tree attention over it (tree_attention_fp8_tc.cu, tree_attention_fp8.cu).
+struct Fp8WriteCall {
+  const void* k;
+  const void* v;
+  ts_dtype dt;
+  long long k_stride[3], v_stride[3];  // elements between sequences, rows and heads
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int num_blocks, block_size, scale_block, Hkv, d;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* start_len;
+  const int32_t* length;
+  int B, n;
+  int32_t* dev_status;
+};
+int kv_write_fp8_launch(const Fp8WriteCall& c, cudaStream_t stream);
+
+struct Fp8ReadCall {
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  int num_blocks, block_size, scale_block, Hkv, d;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* prefix_len;
+  const int32_t* start_len;
+  int B, n;
+  void* k;
+  void* v;
+  ts_dtype dt;
+  int32_t* dev_status;
+};
+int kv_read_fp8_launch(const Fp8ReadCall& c, cudaStream_t stream, int num_sms);
+
+struct Fp8CommitCall {
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int num_blocks, block_size, scale_block, Hkv, d;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* prefix_len;
+  const int32_t* accept_path;
+  const int32_t* accept_len;
+  int B, m;
+  int32_t* block_table_out;
+  int32_t* prefix_len_out;
+  int32_t* freed_blocks;
+  int32_t* freed_count;
+  int32_t* dev_status;
+};
+int kv_commit_fp8_launch(const Fp8CommitCall& c, cudaStream_t stream);
+
+struct Fp8AttnCall {
+  const void* q;
+  ts_dtype dt;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  int num_blocks, block_size, scale_block;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* prefix_len;
+  int max_prefix;
+  const uint64_t* mask;
+  int B, m, Hq, Hkv, d;
+  float scale;
+  void* out;
+  float* lse;
+  void* workspace;
+  int32_t* dev_status;
+};
+bool attention_fp8_uses_tc(ts_dtype dt, int d, int block_size);
+size_t attention_fp8_simt_workspace_bytes(int B, int m, int Hq, int Hkv, int d, int max_prefix, int num_sms);
+int attention_fp8_simt_launch(const Fp8AttnCall& a, cudaStream_t stream, int num_sms);
+size_t attention_fp8_tc_workspace_bytes(int B, int m, int Hq, int Hkv, int max_prefix, int num_sms);
+int attention_fp8_tc_launch(const Fp8AttnCall& a, cudaStream_t stream, int num_sms);
+
 // The page pool (page_pool.cu).
 struct ReserveCall {
   void* k_cache;
