@@ -28,8 +28,8 @@
 // to the workspace and join_kernel merges them.  With several row groups CTAs of neighbouring index walk the same tiles
 // for different rows, so all but one read them from L2.
 //
-// Warps: 0 TMA producer (one lane per page), 1 MMA issuer and TMEM owner, 2 scales, 3 idle, 4..7 Q and V converters,
-// from 8 on softmax: four warps (one per 32 TMEM lanes) for every CPT columns.
+// Warps: 0 TMA copies of K, 1 K Q^T and owner of the tensor memory, 2 scales, 3 copies of V, 4..7 Q and V converters, 8 and 9 second
+// ones of 0 and 3, 10 idle, 11 V^T P^T, from 12 on softmax: four warps (one per 32 TMEM lanes) for every CPT columns.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -57,7 +57,11 @@ struct Cfg {
   static constexpr int CPT = R == 16 ? 16 : R == 32 ? 16 : 32;  // columns per softmax thread
   static constexpr int NG = R / CPT;                             // column groups of four warps
   static constexpr int SOFT = 4 * NG;
-  static constexpr int FIRST_SOFT = 8;
+  // A TMA copy keeps its issuing warp busy for some 140 cycles and a tile of 16-token pages is 16 of them: up to 64 rows, where
+  // a tile has to be done in the time that its bytes take, K and V have two issuing warps each.
+  static constexpr int EXTRA = 4;
+  static constexpr int ISSUERS = R == 128 ? 1 : 2;
+  static constexpr int FIRST_SOFT = 8 + EXTRA;
   static constexpr int THREADS = 32 * (FIRST_SOFT + SOFT);
   static constexpr int SK = R == 128 ? 3 : R == 16 ? 5 : 4;
   static constexpr int SV = R >= 64 ? 2 : 4;
@@ -97,7 +101,7 @@ struct Params {
   float* part_o;    // [RG * Gr, 2, R, 128]
   float2* part_ml;  // [RG * Gr, 2, R]
   int32_t* status;
-  int B, m, Hq, Hkv, g, rows, W, bs, sb, nsb, max_blocks, num_blocks, max_prefix;
+  int B, m, Hq, Hkv, g, rows, W, bs, nsb, bs_log2, sb_log2, max_blocks, num_blocks, max_prefix;
   int RG, Gr;       // row groups, CTAs per row group
   float scale_log2;
 };
@@ -170,8 +174,8 @@ __device__ __forceinline__ Walk walk_from(const Params& p, long long x, long lon
   return w;
 }
 
-// The CTA of a row group whose range [c N / Gr, (c + 1) N / Gr) holds tile x.
-__device__ __forceinline__ int cta_of(long long x, long long N, int Gr) {
+// The CTA of a row group whose range [c N / Gr, (c + 1) N / Gr) holds tile x (Gr <= N).
+__device__ __forceinline__ int cta_of(long long x, long long N, long long Gr) {
   return static_cast<int>(((x + 1) * Gr + N - 1) / N) - 1;
 }
 
@@ -181,12 +185,34 @@ __device__ __forceinline__ int block_at(const Params& p, int b, int lp, int page
   return id >= 0 && id < p.num_blocks ? id : -1;
 }
 
-// D (+)= A * B of 8-bit types.
+// D (+)= A * B by one lane of a converged warp: 8-bit types, and fp16.
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "{\n\t.reg .pred p, one;\n\telect.sync _|one, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, one;\n\telect.sync _|one, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The barrier gets an arrival when the MMAs that the elected lane has issued are done.
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\t"
+      "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+// One box of a tensor map by the elected lane.
+__device__ __forceinline__ void tma_elected(uint32_t dst, const void* tmap, uint32_t bar, int c2, int c3) {
+  asm volatile(
+      "{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\t"
+      "@one cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
 }
 // Instruction descriptors (fields as in idesc_bf16_f32; format 0 is e4m3 in kind f8f6f4 and fp16 in kind f16, 1 is e5m2).
@@ -211,8 +237,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
   return w;
 }
-// N consecutive columns of this thread's lane, and wait for them.
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+// 16 consecutive columns of this thread's lane, and wait for them.
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -222,7 +247,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -249,6 +273,29 @@ __device__ __forceinline__ int ordered(float x) {
   return i ^ ((i >> 31) & 0x7FFFFFFF);
 }
 __device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
+
+// Bounded wait of a whole warp.  Every branch on its way is a vote, so what follows is uniform to the compiler too: descriptors and
+// addresses of MMAs and copies then stay in uniform registers instead of being moved there for each instruction, which
+// took some 100 cycles an MMA and 140 a copy where one lane issued them.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    if ((it & 63u) == 0u) {
+      const bool late = global_timer_ns() - t0 > kWaitLimitNs;
+      if (__any_sync(0xffffffffu, *abort_flag != 0 || late)) {
+        if (late && (threadIdx.x & 31) == 0 && *abort_flag == 0) {
+          *abort_flag = 1;
+          report(status, TS_ERR_TIMEOUT);
+        }
+        __syncwarp();
+        if (__any_sync(0xffffffffu, late)) *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
 
 // On the way out after a failed wait: lets copies and MMAs in flight land.
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
@@ -288,6 +335,7 @@ template <int R>
 __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const __grid_constant__ Params p) {
   using C = Cfg<R>;
+  constexpr int HALF = 16;  // columns that a softmax thread works on at a time
   constexpr int CPT = C::CPT, SK = C::SK, SV = C::SV, NP = C::NP, NV = C::NV;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -305,8 +353,8 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   };
   const uint32_t full_k = take(SK), empty_k = take(SK), full_v = take(SV), empty_v = take(SV), v16_full = take(NV),
                  v16_empty = take(NV), s_full = take(2), s_empty = take(2), p_full = take(NP), p_empty = take(NP),
-                 sc_full = take(kScaleSlots), sc_empty = take(kScaleSlots), o_done = take(1), q_full = take(1),
-                 q_empty = take(1), o_free = take(1), last = take(1);
+                 sc_full = take(kScaleSlots), sc_empty = take(kScaleSlots), q_full = take(1),
+                 q_empty = take(1), o_free = take(1), last = take(2);
   unsigned char* misc = sptr + C::OFF_MISC;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
@@ -314,16 +362,16 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   Walk* s_walk = reinterpret_cast<Walk*>(misc + 16);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < SK; ++i) mbar_init(full_k + 8 * i, 1), mbar_init(empty_k + 8 * i, 1);
-    for (int i = 0; i < SV; ++i) mbar_init(full_v + 8 * i, 1), mbar_init(empty_v + 8 * i, 4);
+    for (int i = 0; i < SK; ++i) mbar_init(full_k + 8 * i, C::ISSUERS), mbar_init(empty_k + 8 * i, 1);
+    for (int i = 0; i < SV; ++i) mbar_init(full_v + 8 * i, C::ISSUERS), mbar_init(empty_v + 8 * i, 4);
     for (int i = 0; i < NV; ++i) mbar_init(v16_full + 8 * i, 4), mbar_init(v16_empty + 8 * i, 1);
     for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(s_empty + 8 * i, C::SOFT);
     for (int i = 0; i < NP; ++i) mbar_init(p_full + 8 * i, C::SOFT), mbar_init(p_empty + 8 * i, 1);
     for (int i = 0; i < kScaleSlots; ++i) mbar_init(sc_full + 8 * i, 1), mbar_init(sc_empty + 8 * i, C::SOFT);
-    mbar_init(o_done, 1);
     mbar_init(q_full, 4);
     mbar_init(q_empty, 1 + C::SOFT);
     mbar_init(last, 1);
+    mbar_init(last + 8, 1);
     mbar_init(o_free, C::SOFT);
     *abort_flag = 0;
     nan_seg[0] = nan_seg[1] = 0;
@@ -336,7 +384,8 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   pdl_wait();
   if (warp == 0) {
     const long long N = total_tiles(p, lane);
-    const Walk w = walk_from(p, cta * N / p.Gr, (cta + 1) * N / p.Gr, lane);
+    const long long Gr = min(static_cast<long long>(p.Gr), N);  // (no CTA between two parts of a unit is without tiles)
+    const Walk w = cta < Gr ? walk_from(p, cta * N / Gr, (cta + 1) * N / Gr, lane) : Walk{0, 0, 0, 0, 0};
     if (lane == 0) *s_walk = w;
     if (blockIdx.x == 0)
       for (int b = lane; b < p.B; b += 32)
@@ -348,133 +397,170 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   const uint32_t tmem = *s_tmem;
   Walk walk = *s_walk;
   Segment sg;
-  const int ppt = BK / p.bs;  // pages per tile
+  const int ppt = BK >> p.bs_log2;  // pages per tile
   bool ok = true;
 
-  if (warp == 0) {
-    // ------------------------------ K and V codes by TMA: lane i issues page i of a tile ------------------------------
-    int it = 0;
+  // warps 8..11: second issuers of K and V, the second scale warp, and P V
+  const int part = warp >= 8 && warp < 11 ? 1 : 0;
+  const int role = warp < 4 ? warp : warp < 8 ? 5 : warp == 11 ? 4 : warp >= C::FIRST_SOFT ? 6 : C::ISSUERS == 1 || warp == 10 ? -1 : warp == 8 ? 0 : 3;
+  if (role == 0 || role == 3) {
+    // ------------------------------ codes by TMA (role 0: K, 3: V): lane i issues page ISSUERS i + part of a tile ------------------------------
+    const bool is_k = role == 0;
+    const int stages = is_k ? SK : SV;
+    const uint32_t full = is_k ? full_k : full_v, empty = is_k ? empty_k : empty_v;
+    const uint32_t ring = sbase + (is_k ? C::OFF_K : C::OFF_V);
+    const CUtensorMap* map = is_k ? &tmk : &tmv;
+    const int my = C::ISSUERS * lane + part;
+    const int mine = (ppt + C::ISSUERS - 1 - part) / C::ISSUERS;  // pages of a tile that this warp issues
+    const bool issues = my < ppt;
+    int it = 0, stage = 0, phase = 0;
     while (ok && walk.next(p, sg)) {
-      const int pages = (sg.L + p.m + p.bs - 1) / p.bs;
-      int id = lane < ppt ? block_at(p, sg.b, sg.t0 * ppt + lane, pages) : 0;
+      const int pages = (sg.L + p.m + p.bs - 1) >> p.bs_log2;
+      int id = issues ? block_at(p, sg.b, sg.t0 * ppt + my, pages) : 0;
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
         const int cur = id;
-        if (lane < ppt && t + 1 < sg.t1) id = block_at(p, sg.b, (t + 1) * ppt + lane, pages);
+        if (issues && t + 1 < sg.t1) id = block_at(p, sg.b, (t + 1) * ppt + my, pages);
         if (cur == -1) report(p.status, TS_ERR_DEVICE_CHECK);
         const int blk = cur < 0 ? p.num_blocks : cur;  // (out of range: the copy fills zeros)
-        const int sk = it % SK, sv = it % SV;
-        ok = mbar_wait_warp(empty_k + 8 * sk, ((it / SK) & 1) ^ 1, abort_flag, p.status);
+        ok = wait_warp(empty + 8 * stage, phase ^ 1, abort_flag, p.status);
         if (!ok) break;
-        if (lane == 0) mbar_expect_tx(full_k + 8 * sk, TILE8);
+        if (lane == 0) mbar_expect_tx(full + 8 * stage, mine * p.bs * HD);
         __syncwarp();
-        if (lane < ppt) tma_load_4d(sbase + C::OFF_K + sk * TILE8 + lane * p.bs * HD, &tmk, full_k + 8 * sk, 0, 0, sg.h, blk);
-        ok = mbar_wait_warp(empty_v + 8 * sv, ((it / SV) & 1) ^ 1, abort_flag, p.status);
-        if (!ok) {
-          drain(full_k + 8 * sk, (it / SK) & 1);
-          break;
-        }
-        if (lane == 0) mbar_expect_tx(full_v + 8 * sv, TILE8);
-        __syncwarp();
-        if (lane < ppt) tma_load_4d(sbase + C::OFF_V + sv * TILE8 + lane * p.bs * HD, &tmv, full_v + 8 * sv, 0, 0, sg.h, blk);
+        for (int i = 0; i < mine; ++i)
+          tma_elected(ring + stage * TILE8 + (C::ISSUERS * i + part) * p.bs * HD, map, full + 8 * stage, sg.h,
+                      __shfl_sync(0xffffffffu, blk, i));
+        if (++stage == stages) stage = 0, phase ^= 1;
       }
     }
     // after an abort nobody waits for what is still on its way: the newest copy of every stage
-    if (!ok) {
-      for (int i = max(0, it - SK); i < it; ++i) drain(full_k + 8 * (i % SK), (i / SK) & 1);
-      for (int i = max(0, it - SV); i < it; ++i) drain(full_v + 8 * (i % SV), (i / SV) & 1);
-    }
-  } else if (warp == 1) {
-    // ------------------------------ MMA issuer ------------------------------
-    if (lane == 0) {
-      constexpr uint32_t iq1 = idesc_of(R, 0, 0, 0), iq2 = idesc_of(R, 1, 0, 0), ip = idesc_of(R, 0, 1, 1);
-      auto qk = [&](int it) {
+    if (!ok)
+      for (int i = max(0, it - stages); i < it; ++i) drain(full + 8 * (i % stages), (i / stages) & 1);
+  } else if (role == 1) {
+    // ------------------------------ S^T = K Q^T (the warp issues as one) ------------------------------
+    constexpr uint32_t iq1 = idesc_of(R, 0, 0, 0), iq2 = idesc_of(R, 1, 0, 0);
+    const uint64_t kdesc = sdesc(sbase + C::OFF_K, 16, 1024, 128), qdesc = sdesc(sbase + C::OFF_Q, 16, 1024, 128);
+    int it = 0, seg = 0;
+    while (ok && walk.next(p, sg)) {
+      ok = wait_warp(q_full, seg & 1, abort_flag, p.status);
+      if (!ok) break;
+      for (int t = sg.t0; t < sg.t1; ++t, ++it) {
         const int sk = it % SK, s = it & 1;
-        if (!mbar_wait(full_k + 8 * sk, (it / SK) & 1, abort_flag, p.status)) return false;
-        if (!mbar_wait(s_empty + 8 * s, ((it >> 1) & 1) ^ 1, abort_flag, p.status)) return false;
+        ok = wait_warp(full_k + 8 * sk, (it / SK) & 1, abort_flag, p.status);
+        if (!ok) break;
+        ok = wait_warp(s_empty + 8 * s, ((it >> 1) & 1) ^ 1, abort_flag, p.status);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + R + R * s;
+        // (descriptors count 16-byte units: a step of 32 bytes adds 2)
+        const uint64_t kd = kdesc + static_cast<uint64_t>(sk * (TILE8 >> 4));
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int kk = 0; kk < HD / 32; ++kk) mma_f8(d, kd + 2u * kk, qdesc + 2u * kk, iq1, kk > 0 ? 1u : 0u);
 #pragma unroll
-          for (int kk = 0; kk < HD / 32; ++kk)
-            mma_f8(d, sdesc(sbase + C::OFF_K + sk * TILE8 + 32 * kk, 16, 1024, 128),
-                   sdesc(sbase + C::OFF_Q + part * C::QPART + 32 * kk, 16, 1024, 128), part == 0 ? iq1 : iq2,
-                   part + kk > 0 ? 1u : 0u);
-        tc_commit(s_full + 8 * s);
-        tc_commit(empty_k + 8 * sk);
-        return true;
-      };
-      int it = 0, seg = 0;
-      while (ok && walk.next(p, sg)) {
-        ok = mbar_wait(q_full, seg & 1, abort_flag, p.status);
-        if (!ok) break;
-        const int n = sg.t1 - sg.t0;
-        ok = qk(it);
-        if (ok && n == 1) tc_commit(q_empty);
-        // (the accumulator is free once the last segment's has been read)
-        if (ok) ok = mbar_wait(o_free, (seg & 1) ^ 1, abort_flag, p.status);
-        for (int i = 0; ok && i < n; ++i, ++it) {
-          if (i + 1 < n) {
-            ok = qk(it + 1);
-            if (!ok) break;
-            if (i + 2 == n) tc_commit(q_empty);
-          }
-          const int v = it % NV, pb = it % NP;
-          ok = mbar_wait(v16_full + 8 * v, (it / NV) & 1, abort_flag, p.status) &&
-               mbar_wait(p_full + 8 * pb, (it / NP) & 1, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            mma_ss(tmem, sdesc(sbase + C::OFF_V16 + v * TILE16 + 2048 * kk, BK * 128, 1024, 128),
-                   sdesc(sbase + C::OFF_P + pb * C::PBUF + 16 * C::PROW * kk, BK * 128, 8 * C::PROW, C::PROW), ip,
-                   i + kk > 0 ? 1u : 0u);
-          tc_commit(v16_empty + 8 * v);
-          tc_commit(p_empty + 8 * pb);
-          tc_commit(o_done);
-        }
-        ++seg;
+        for (int kk = 0; kk < HD / 32; ++kk) mma_f8(d, kd + 2u * kk, qdesc + (C::QPART >> 4) + 2u * kk, iq2, 1u);
+        commit_elected(s_full + 8 * s);
+        commit_elected(empty_k + 8 * sk);
       }
-      if (!ok) {
-        // MMAs in flight end before the accumulators are given back
-        tc_commit(last);
-        drain(last, 0);
-      }
+      if (!ok) break;
+      commit_elected(q_empty);
+      ++seg;
     }
-    __syncwarp();
-  } else if (warp == 2) {
+    if (!ok) {
+      // MMAs in flight end before the accumulators are given back
+      commit_elected(last);
+      drain(last, 0);
+    }
+  } else if (role == 4) {
+    // ------------------------------ O^T += V^T P^T ------------------------------
+    constexpr uint32_t ip = idesc_of(R, 0, 1, 1);
+    const uint64_t vdesc = sdesc(sbase + C::OFF_V16, BK * 128, 1024, 128);
+    const uint64_t pdesc = sdesc(sbase + C::OFF_P, BK * 128, 8 * C::PROW, C::PROW);
+    int it = 0, seg = 0;
+    while (ok && walk.next(p, sg)) {
+      // (the accumulator is free once the last segment's has been read)
+      ok = wait_warp(o_free, (seg & 1) ^ 1, abort_flag, p.status);
+      if (!ok) break;
+      for (int t = sg.t0; t < sg.t1; ++t, ++it) {
+        const int v = it % NV, pb = it % NP;
+        ok = wait_warp(v16_full + 8 * v, (it / NV) & 1, abort_flag, p.status);
+        if (!ok) break;
+        ok = wait_warp(p_full + 8 * pb, (it / NP) & 1, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = vdesc + static_cast<uint64_t>(v * (TILE16 >> 4)), pd = pdesc + static_cast<uint64_t>(pb * (C::PBUF >> 4));
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          mma_f16(tmem, vd + (2048u >> 4) * kk, pd + C::PROW * kk, ip, kk > 0 || t > sg.t0 ? 1u : 0u);
+        commit_elected(v16_empty + 8 * v);
+        commit_elected(p_empty + 8 * pb);
+      }
+      ++seg;
+    }
+    if (!ok) {
+      commit_elected(last + 8);
+      drain(last + 8, 0);
+    }
+  } else if (role == 2) {
     // ------------------------------ scales ------------------------------
+    // Four tiles' scales are under way in registers, and the ids of the next four: one tile ahead the two dependent loads set the
+    // pace (4800 cycles a tile unprefetched, 1700 one ahead, where a tile's bytes take 1400).
+    constexpr int AHEAD = 4;
     int it = 0;
     while (ok && walk.next(p, sg)) {
-      const int pages = (sg.L + p.m + p.bs - 1) / p.bs;
-      for (int t = sg.t0; t < sg.t1; ++t, ++it) {
-        const int slot = it % kScaleSlots;
-        float2 v[4];
+      const int pages = (sg.L + p.m + p.bs - 1) >> p.bs_log2, n = sg.t1 - sg.t0;
+      int id[AHEAD][4];
+      float ks[AHEAD][4], vs[AHEAD][4];
+      bool id_was[AHEAD][4];
+      auto ids = [&](int u, int i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) id[u][j] = i < n ? block_at(p, sg.b, ((sg.t0 + i) * BK + 32 * j + lane) >> p.bs_log2, pages) : -2;
+      };
+      auto load = [&](int u, int i) {  // with the ids of tile i; a page without an id: its keys get no weight
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int pos = t * BK + 32 * j + lane;
-          const int id = block_at(p, sg.b, pos / p.bs, pages);
-          v[j] = make_float2(0.f, -INFINITY);  // (a page without an id: its keys get no weight)
-          if (id >= 0) {
-            const long long o = (static_cast<long long>(id) * p.Hkv + sg.h) * p.nsb + pos % p.bs / p.sb;
-            v[j] = make_float2(scale_in_range(__ldg(p.ks + o)) * p.scale_log2, __log2f(scale_in_range(__ldg(p.vs + o))));
+          ks[u][j] = 0.f, vs[u][j] = 0.f;
+          id_was[u][j] = id[u][j] >= 0;
+          if (id_was[u][j]) {
+            const int row = ((sg.t0 + i) * BK + 32 * j + lane) & (p.bs - 1);
+            const long long o = (static_cast<long long>(id[u][j]) * p.Hkv + sg.h) * p.nsb + (row >> p.sb_log2);
+            ks[u][j] = __ldg(p.ks + o);
+            vs[u][j] = __ldg(p.vs + o);
           }
         }
-        ok = mbar_wait_warp(sc_empty + 8 * slot, ((it / kScaleSlots) & 1) ^ 1, abort_flag, p.status);
-        if (!ok) break;
-        float2* to = reinterpret_cast<float2*>(sptr + C::OFF_SC) + slot * BK;
+      };
 #pragma unroll
-        for (int j = 0; j < 4; ++j) to[32 * j + lane] = v[j];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sc_full + 8 * slot);
+      for (int u = 0; u < AHEAD; ++u) ids(u, u);
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) load(u, u);
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) ids(u, AHEAD + u);
+      for (int i = 0; ok && i < n; i += AHEAD) {
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          if (!ok || i + u >= n) break;
+          const int slot = (it + u) % kScaleSlots;
+          ok = wait_warp(sc_empty + 8 * slot, (((it + u) / kScaleSlots) & 1) ^ 1, abort_flag, p.status);
+          if (!ok) break;
+          float2* to = reinterpret_cast<float2*>(sptr + C::OFF_SC) + slot * BK;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            to[32 * j + lane] = make_float2(scale_in_range(ks[u][j]) * p.scale_log2,
+                                            id_was[u][j] ? __log2f(scale_in_range(vs[u][j])) : -INFINITY);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sc_full + 8 * slot);
+        }
+        it += min(AHEAD, n - i);
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) load(u, i + AHEAD + u);
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) ids(u, i + 2 * AHEAD + u);
       }
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (role == 5) {
     // ------------------------------ Q and V into the tensor cores' types ------------------------------
     const int w = warp - 4;
     int it = 0, seg = 0;
     while (ok && walk.next(p, sg)) {
-      ok = mbar_wait_warp(q_empty, (seg & 1) ^ 1, abort_flag, p.status);
+      ok = wait_warp(q_empty, (seg & 1) ^ 1, abort_flag, p.status);
       if (!ok) break;
       // eight lanes per row, 16 values each
       for (int r0 = w * 4; r0 < R; r0 += 16) {
@@ -524,8 +610,8 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       if (lane == 0) mbar_arrive(q_full);
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
         const int sv = it % SV, v = it % NV;
-        ok = mbar_wait_warp(full_v + 8 * sv, (it / SV) & 1, abort_flag, p.status) &&
-             mbar_wait_warp(v16_empty + 8 * v, ((it / NV) & 1) ^ 1, abort_flag, p.status);
+        ok = wait_warp(full_v + 8 * sv, (it / SV) & 1, abort_flag, p.status) &&
+             wait_warp(v16_empty + 8 * v, ((it / NV) & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
         const unsigned char* from = sptr + C::OFF_V + sv * TILE8;
         unsigned char* to = sptr + C::OFF_V16 + v * TILE16;
@@ -534,31 +620,37 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
         // reads (chunk c at c ^ (k % 8)) and writes (chunks 2c, 2c + 1 of the half's 128-byte row, the same way) then touch
         // all banks once.
         const int pair = lane >> 3, k8 = (lane & 4) ? pair ^ 5 : pair, c4 = lane & 3;
+        // (all loads first: with a branch and a store between them each waited for its own, 2400 cycles a tile)
+        uint4 x[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int k = (w * 4 + (u >> 1)) * 8 + k8, c = c4 + 4 * (u & 1);
-          uint4 x = *reinterpret_cast<const uint4*>(from + k * 128 + ((c ^ k8) << 4));
-          if (tail) {
-            const int pos = t * BK + k;
+        for (int u = 0; u < 8; ++u)
+          x[u] = *reinterpret_cast<const uint4*>(from + ((w * 4 + (u >> 1)) * 8 + k8) * 128 + (((c4 + 4 * (u & 1)) ^ k8) << 4));
+        if (tail) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int pos = t * BK + (w * 4 + (u >> 1)) * 8 + k8;
             if (pos >= sg.L + p.m) {
-              x = make_uint4(0, 0, 0, 0);
+              x[u] = make_uint4(0, 0, 0, 0);
             } else if (pos >= sg.L) {
               // a NaN of a tree row reaches the rows that attend to it in the epilogue: here it would reach all
-              const uint32_t n0 = __vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu), n1 = __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
-                             n2 = __vcmpeq4(x.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu), n3 = __vcmpeq4(x.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+              const uint32_t n0 = __vcmpeq4(x[u].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu), n1 = __vcmpeq4(x[u].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
+                             n2 = __vcmpeq4(x[u].z & 0x7F7F7F7Fu, 0x7F7F7F7Fu), n3 = __vcmpeq4(x[u].w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
               if ((n0 | n1 | n2 | n3) != 0u) {
                 nan_seg[seg & 1] = seg + 1;
-                x = make_uint4(x.x & ~n0, x.y & ~n1, x.z & ~n2, x.w & ~n3);
+                x[u] = make_uint4(x[u].x & ~n0, x[u].y & ~n1, x[u].z & ~n2, x[u].w & ~n3);
               }
             }
           }
-          const uint4 a = make_uint4(decode_e4m3x2_f16(x.x), decode_e4m3x2_f16(x.x >> 16), decode_e4m3x2_f16(x.y),
-                                     decode_e4m3x2_f16(x.y >> 16));
-          const uint4 b2 = make_uint4(decode_e4m3x2_f16(x.z), decode_e4m3x2_f16(x.z >> 16), decode_e4m3x2_f16(x.w),
-                                      decode_e4m3x2_f16(x.w >> 16));
-          unsigned char* row = to + (u & 1) * (BK * 128) + k * 128;
-          *reinterpret_cast<uint4*>(row + (((2 * c4) ^ k8) << 4)) = a;
-          *reinterpret_cast<uint4*>(row + (((2 * c4 + 1) ^ k8) << 4)) = b2;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          unsigned char* row = to + (u & 1) * (BK * 128) + ((w * 4 + (u >> 1)) * 8 + k8) * 128;
+          *reinterpret_cast<uint4*>(row + (((2 * c4) ^ k8) << 4)) =
+              make_uint4(decode_e4m3x2_f16(x[u].x), decode_e4m3x2_f16(x[u].x >> 16), decode_e4m3x2_f16(x[u].y),
+                         decode_e4m3x2_f16(x[u].y >> 16));
+          *reinterpret_cast<uint4*>(row + (((2 * c4 + 1) ^ k8) << 4)) =
+              make_uint4(decode_e4m3x2_f16(x[u].z), decode_e4m3x2_f16(x[u].z >> 16), decode_e4m3x2_f16(x[u].w),
+                         decode_e4m3x2_f16(x[u].w >> 16));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -569,7 +661,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       }
       ++seg;
     }
-  } else if (warp >= C::FIRST_SOFT) {
+  } else if (role == 6) {
     // ------------------------------ softmax ------------------------------
     const int quarter = warp & 3, group = (warp - C::FIRST_SOFT) >> 2, col0 = group * CPT;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
@@ -577,10 +669,13 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
     float* rmf = reinterpret_cast<float*>(rm);
     float* red = reinterpret_cast<float*>(sptr + C::OFF_RED) + col0;      // [quarter * R + c]
     float* fac = reinterpret_cast<float*>(sptr + C::OFF_FAC) + col0;
+    // P V of tile i is done: its P buffer is free again.  (A barrier of one phase per tile would not do: with two P buffers
+    // the softmax may be two tiles ahead of P V, and a wait by parity would take the older phase for the newer.)
+    auto o_holds = [&](int i) { return wait_warp(p_empty + 8 * (i % NP), (i / NP) & 1, abort_flag, p.status); };
     auto m_at = [&](int c) -> float& { return rmf[(c >> 1) * 4 + 2 + (c & 1)]; };
     int it = 0, seg = 0;
     while (walk.next(p, sg)) {
-      if (ok) ok = mbar_wait_warp(q_full, seg & 1, abort_flag, p.status);
+      if (ok) ok = wait_warp(q_full, seg & 1, abort_flag, p.status);
       if (group_any(group, !ok)) {
         ok = false;
         break;
@@ -594,36 +689,48 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       uint64_t l2[CPT / 2];
 #pragma unroll
       for (int c = 0; c < CPT / 2; ++c) l2[c] = 0ull;
+      // {r0, r1, -M0, -M1}: with 16 columns they stay in registers
+      float4 held[HALF / 2];
+      auto hold = [&]() {
+        if (CPT == HALF) {
+#pragma unroll
+          for (int c = 0; c < HALF / 2; ++c) held[c] = rm[c];
+        }
+      };
+      hold();
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
         const int s = it & 1, slot = it % kScaleSlots;
         const uint32_t tS = tmem + lanes + R + R * s + col0;
         if (ok)
-          ok = mbar_wait_warp(sc_full + 8 * slot, (it / kScaleSlots) & 1, abort_flag, p.status) &&
-               mbar_wait_warp(s_full + 8 * s, (it >> 1) & 1, abort_flag, p.status);
+          ok = wait_warp(sc_full + 8 * slot, (it / kScaleSlots) & 1, abort_flag, p.status) &&
+               wait_warp(s_full + 8 * s, (it >> 1) & 1, abort_flag, p.status);
         float2 sc = make_float2(0.f, 0.f);
-        uint32_t x[CPT];
+        uint32_t x[HALF];
         float zmax = -INFINITY;
         const bool tail = (t + 1) * BK > sg.L;
         uint32_t vis = 0u;  // bit c: row c attends to this key (tail tiles)
-        auto scores = [&]() {  // x <- z = y - M
-          tmem_ld(tS, x);
+        auto scores = [&](int half) {  // x <- z = y - M of 16 columns
+          tmem_ld(tS + HALF * half, x);
           const uint64_t a2 = pack_f32x2(sc.x, sc.x), v2 = pack_f32x2(sc.y, sc.y);
-          zmax = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < CPT; c += 2) {
-            const float4 k = rm[c / 2];
+          for (int c = 0; c < HALF; c += 2) {
+            const float4 k = CPT == HALF ? held[c / 2] : rm[(HALF * half + c) / 2];
             const uint64_t z2 = fma_f32x2(pack_f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
                                           mul_f32x2(a2, pack_f32x2(k.x, k.y)), add_f32x2(v2, pack_f32x2(k.z, k.w)));
             float z0, z1;
             unpack_f32x2(z2, z0, z1);
-            if (tail) {
-              if (!((vis >> c) & 1u)) z0 = -INFINITY;
-              if (!((vis >> (c + 1)) & 1u)) z1 = -INFINITY;
-            }
-            zmax = max3(zmax, z0, z1);
             x[c] = __float_as_uint(z0);
             x[c + 1] = __float_as_uint(z1);
           }
+          if (tail) {
+#pragma unroll
+            for (int c = 0; c < HALF; ++c)
+              if (!((vis >> (HALF * half + c)) & 1u)) x[c] = 0xFF800000u;
+          }
+        };
+        auto highest = [&]() {
+#pragma unroll
+          for (int c = 0; c < HALF; c += 2) zmax = max3(zmax, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
         };
         if (ok) {
           tc_fence_after();
@@ -633,15 +740,23 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
             const int n = t * BK + 32 * quarter + lane - sg.L;
             vis = sc.y == -INFINITY ? 0u : ~0u;
             if (n >= p.m) vis = 0u;
-            else if (n >= 0) {
-              for (int c = 0; c < CPT; ++c) {
-                const int row = min(R0 + col0 + c, p.rows - 1);
-                const uint64_t word = __ldg(p.mask + (static_cast<long long>(sg.b) * p.m + row / p.g) * p.W + (n >> 6));
-                if (!((word >> (n & 63)) & 1ull)) vis &= ~(1u << c);
-              }
+            const int word = min(max(n, 0), p.m - 1) >> 6;
+            uint32_t seen = 0u;
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) {
+              const int row = min(R0 + col0 + c, p.rows - 1);
+              const uint64_t w = __ldg(p.mask + (static_cast<long long>(sg.b) * p.m + row / p.g) * p.W + word);
+              seen |= static_cast<uint32_t>((w >> (n & 63)) & 1ull) << c;
             }
+            if (n >= 0) vis &= seen;
           }
-          scores();
+          // The first pass finds whether the reference has to rise, the second makes the weights; between them 32 columns'
+          // scores stay in tensor memory (kept in registers beside the sums they spilled: 7500 cycles a tile of 128 rows).
+#pragma unroll
+          for (int half = 0; half < CPT / HALF; ++half) {
+            scores(half);
+            highest();
+          }
         }
         if (group_any(group, !ok || zmax > kRise)) {
           // Rare: a reference has to rise (every unit's first tile does this).
@@ -649,15 +764,19 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
             ok = false;
             break;
           }
-          tmem_ld(tS, x);
           int top = 0x80000000;
 #pragma unroll
-          for (int c = 0; c < CPT; ++c) {
-            const float r = rmf[(c >> 1) * 4 + (c & 1)];
-            float y = fmaf(__uint_as_float(x[c]), sc.x * r, sc.y);
-            if (y != y || (tail && !((vis >> c) & 1u))) y = -INFINITY;  // (a NaN goes into the weights, not into the reference)
-            const int most = __reduce_max_sync(0xffffffffu, ordered(y));
-            if (lane == c) top = most;
+          for (int half = 0; half < CPT / HALF; ++half) {
+            tmem_ld(tS + HALF * half, x);
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) {
+              const int c = HALF * half + i;
+              const float r = rmf[(c >> 1) * 4 + (c & 1)];
+              float y = fmaf(__uint_as_float(x[i]), sc.x * r, sc.y);
+              if (y != y || (tail && !((vis >> c) & 1u))) y = -INFINITY;  // (a NaN goes into the weights, not into the reference)
+              const int most = __reduce_max_sync(0xffffffffu, ordered(y));
+              if (lane == c) top = most;
+            }
           }
           if (lane < CPT) red[quarter * R + lane] = from_ordered(top);
           group_sync(group);
@@ -672,53 +791,62 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < CPT / 2; ++c) l2[c] = mul_f32x2(l2[c], pack_f32x2(fac[2 * c], fac[2 * c + 1]));
           if (t > sg.t0) {
-            ok = mbar_wait_warp(o_done, (it - 1) & 1, abort_flag, p.status);
+            ok = o_holds(it - 1);
             if (ok) {
               tc_fence_after();
-              uint32_t o[CPT];
-              tmem_ld(tmem + lanes + col0, o);
 #pragma unroll
-              for (int c = 0; c < CPT; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * fac[c]);
-              tmem_st(tmem + lanes + col0, o);
+              for (int half = 0; half < CPT / HALF; ++half) {
+                tmem_ld(tmem + lanes + col0 + HALF * half, x);
+#pragma unroll
+                for (int c = 0; c < HALF; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * fac[HALF * half + c]);
+                tmem_st(tmem + lanes + col0 + HALF * half, x);
+              }
               tmem_st_wait();
             }
           }
-          scores();
-        }
-        if (!ok) continue;  // (leaves at the next vote)
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(s_empty + 8 * s);
-          mbar_arrive(sc_empty + 8 * slot);
-        }
-        const float iv = sc.y == -INFINITY ? 0.f : ex2_approx(-sc.y);
-        const uint64_t iv2 = pack_f32x2(iv, iv);
-        uint32_t h[CPT / 2];
-#pragma unroll
-        for (int c = 0; c < CPT; c += 2) {
-          const float p0 = ex2_approx(__uint_as_float(x[c])), p1 = ex2_approx(__uint_as_float(x[c + 1]));
-          l2[c / 2] = fma_f32x2(pack_f32x2(p0, p1), iv2, l2[c / 2]);
-          h[c / 2] = pack_f16x2(p0, p1);
+          hold();
+          if (CPT == HALF) scores(0);
         }
         const int pb = it % NP;
-        ok = mbar_wait_warp(p_empty + 8 * pb, ((it / NP) & 1) ^ 1, abort_flag, p.status);
-        if (!ok) continue;
+        if (ok) ok = wait_warp(p_empty + 8 * pb, ((it / NP) & 1) ^ 1, abort_flag, p.status);
+        if (!ok) continue;  // (leaves at the next vote)
+        const float iv = sc.y == -INFINITY ? 0.f : ex2_approx(-sc.y);
+        const uint64_t iv2 = pack_f32x2(iv, iv);
         // P^T [key][row]: rows of PROW bytes, 16-byte chunks swizzled with the key
         const int k = 32 * quarter + lane;
         unsigned char* prow = sptr + C::OFF_P + pb * C::PBUF + (col0 / 64) * (BK * 128) + k * C::PROW;
         const int chunk0 = (col0 % 64) / 8;
         const int swz = C::PROW == 128 ? (k & 7) : C::PROW == 64 ? ((k >> 1) & 3) : ((k >> 2) & 1);
 #pragma unroll
-        for (int j = 0; j < CPT / 8; ++j)
-          *reinterpret_cast<uint4*>(prow + (((chunk0 + j) ^ swz) << 4)) =
-              make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+        for (int half = 0; half < CPT / HALF; ++half) {
+          if (CPT > HALF) scores(half);
+          if (half + 1 == CPT / HALF) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(s_empty + 8 * s);
+              mbar_arrive(sc_empty + 8 * slot);
+            }
+          }
+          uint32_t h[HALF / 2];
+#pragma unroll
+          for (int c = 0; c < HALF; c += 2) {
+            const float p0 = ex2_approx(__uint_as_float(x[c])), p1 = ex2_approx(__uint_as_float(x[c + 1]));
+            uint64_t& l = l2[HALF / 2 * half + c / 2];
+            l = fma_f32x2(pack_f32x2(p0, p1), iv2, l);
+            h[c / 2] = pack_f16x2(p0, p1);
+          }
+#pragma unroll
+          for (int j = 0; j < HALF / 8; ++j)
+            *reinterpret_cast<uint4*>(prow + (((chunk0 + HALF / 8 * half + j) ^ swz) << 4)) =
+                make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + 8 * pb);
       }
-      if (ok) ok = mbar_wait_warp(o_done, (it - 1) & 1, abort_flag, p.status);
+      if (ok) ok = o_holds(it - 1);
       if (group_any(group, !ok)) {
         ok = false;
         break;
@@ -737,27 +865,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
         l = (red[lane] + red[R + lane]) + (red[2 * R + lane] + red[3 * R + lane]);
         M = -m_at(lane);
       }
-      uint32_t o[CPT];
-      tmem_ld(tmem + lanes + col0, o);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
       const int ch = 32 * quarter + lane;
-      if (nan_seg[seg & 1] == seg + 1) {
-        // a NaN in a tree row's V: the rows that attend to it get it
-        for (int n = max(0, sg.t0 * BK - sg.L); n < min(p.m, sg.t1 * BK - sg.L); ++n) {
-          const int pos = sg.L + n, id = p.table[static_cast<long long>(sg.b) * p.max_blocks + pos / p.bs];
-          if (id < 0 || id >= p.num_blocks) continue;
-          const uint32_t code = p.vc[((static_cast<long long>(id) * p.Hkv + sg.h) * p.bs + pos % p.bs) * HD + ch];
-          if ((code & 0x7Fu) != 0x7Fu) continue;
-#pragma unroll
-          for (int c = 0; c < CPT; ++c) {
-            const int row = min(R0 + col0 + c, p.rows - 1);
-            const uint64_t word = __ldg(p.mask + (static_cast<long long>(sg.b) * p.m + row / p.g) * p.W + (n >> 6));
-            if ((word >> (n & 63)) & 1ull) o[c] = 0x7FC00000u;
-          }
-        }
-      }
       const long long slot = (static_cast<long long>(rg) * p.Gr + cta) * 2 + (sg.t0 == 0 ? 1 : 0);
       if (lane < CPT && quarter == 0 && col0 + lane < rows_here) {
         const int row = R0 + col0 + lane, node = row / p.g, head = sg.h * p.g + row % p.g;
@@ -767,15 +875,41 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-      for (int c = 0; c < CPT; ++c) {
-        const float f = __shfl_sync(0xffffffffu, inv, c);
-        if (col0 + c < rows_here) {
-          if (whole) {
-            const int row = R0 + col0 + c, node = row / p.g, head = sg.h * p.g + row % p.g;
-            p.out[((static_cast<long long>(sg.b) * p.m + node) * p.Hq + head) * HD + ch] =
-                __float2bfloat16_rn(__uint_as_float(o[c]) * f);
-          } else {
-            p.part_o[(slot * R + col0 + c) * HD + ch] = __uint_as_float(o[c]);
+      for (int half = 0; half < CPT / HALF; ++half) {
+        uint32_t o[HALF];
+        tmem_ld(tmem + lanes + col0 + HALF * half, o);
+        if (half + 1 == CPT / HALF) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free);
+        }
+        const int first = col0 + HALF * half;
+        if (nan_seg[seg & 1] == seg + 1) {
+          // a NaN in a tree row's V: the rows that attend to it get it
+          for (int n = max(0, sg.t0 * BK - sg.L); n < min(p.m, sg.t1 * BK - sg.L); ++n) {
+            const int pos = sg.L + n, id = p.table[static_cast<long long>(sg.b) * p.max_blocks + (pos >> p.bs_log2)];
+            if (id < 0 || id >= p.num_blocks) continue;
+            const uint32_t code = p.vc[((static_cast<long long>(id) * p.Hkv + sg.h) * p.bs + (pos & (p.bs - 1))) * HD + ch];
+            if ((code & 0x7Fu) != 0x7Fu) continue;
+#pragma unroll
+            for (int c = 0; c < HALF; ++c) {
+              const int row = min(R0 + first + c, p.rows - 1);
+              const uint64_t word = __ldg(p.mask + (static_cast<long long>(sg.b) * p.m + row / p.g) * p.W + (n >> 6));
+              if ((word >> (n & 63)) & 1ull) o[c] = 0x7FC00000u;
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < HALF; ++c) {
+          const float f = __shfl_sync(0xffffffffu, inv, HALF * half + c);
+          if (first + c < rows_here) {
+            if (whole) {
+              const int row = R0 + first + c, node = row / p.g, head = sg.h * p.g + row % p.g;
+              p.out[((static_cast<long long>(sg.b) * p.m + node) * p.Hq + head) * HD + ch] =
+                  __float2bfloat16_rn(__uint_as_float(o[c]) * f);
+            } else {
+              p.part_o[(slot * R + first + c) * HD + ch] = __uint_as_float(o[c]);
+            }
           }
         }
       }
@@ -810,7 +944,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
   }
   N *= p.Hkv;
   const long long first = before * p.Hkv + static_cast<long long>(h) * T;
-  const int c0 = cta_of(first, N, p.Gr), c1 = cta_of(first + T - 1, N, p.Gr);
+  const long long Gr = min(static_cast<long long>(p.Gr), N);
+  const int c0 = cta_of(first, N, Gr), c1 = cta_of(first + T - 1, N, Gr);
   if (c0 == c1) return;  // (one CTA had the whole unit)
   const int rg = row / R, r = row - rg * R;
   auto slot = [&](int c) { return (((static_cast<long long>(rg) * p.Gr + c) * 2 + (c == c0 ? 1 : 0)) * R + r); };
@@ -840,6 +975,11 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
 struct Plan {
   int R, RG, Gr;
 };
+int log2_of(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
 // R: the smallest tile width that holds all rows, 128 at most.  CTAs: one per SM, of kMinTiles tiles at least.
 constexpr int kMinTiles = 2;
 Plan plan_of(int B, int m, int Hq, int Hkv, int max_prefix, int num_sms) {
@@ -919,7 +1059,9 @@ int attention_fp8_tc_launch(const Fp8AttnCall& a, cudaStream_t stream, int num_s
   p.part_o = static_cast<float*>(a.workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(pl.RG) * pl.Gr * 2 * pl.R * HD);
   p.B = a.B, p.m = a.m, p.Hq = a.Hq, p.Hkv = a.Hkv, p.g = a.Hq / a.Hkv, p.rows = a.m * p.g, p.W = (a.m + 63) / 64;
-  p.bs = a.block_size, p.sb = a.scale_block, p.nsb = a.block_size / a.scale_block;
+  p.bs = a.block_size, p.nsb = a.block_size / a.scale_block;
+  // (a page of a power of two tokens is cut into powers of two: shifts, as a division takes one warp hundreds of cycles)
+  p.bs_log2 = log2_of(a.block_size), p.sb_log2 = log2_of(a.scale_block);
   p.max_blocks = a.max_blocks, p.num_blocks = a.num_blocks, p.max_prefix = a.max_prefix;
   p.RG = pl.RG, p.Gr = pl.Gr;
   p.scale_log2 = a.scale * kLog2e;

@@ -23,8 +23,12 @@ def _query(rng, shape, dtype):
 
 def _attend(c, q, mask, scale=None, max_prefix=None, **kw):
     status = ts.new_status()
+    B, m, Hq, d = q.shape
+    top = int(c.lens.max()) if max_prefix is None else max_prefix
+    need = ts.library().ts_tree_attention_fp8_workspace(int(q.dtype == torch.bfloat16), B, m, Hq, c.codes[0].shape[1], d, top, c.bs)
+    kw.setdefault("workspace", torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda"))      # (any contents, NaN here)
     r = ts.tree_attention_fp8(q.cuda(), *c.device(), ints(c.table), ints(c.lens), words(mask),
-                              max_prefix=int(c.lens.max()) if max_prefix is None else max_prefix, scale=scale, status=status, **kw)
+                              max_prefix=top, scale=scale, status=status, **kw)
     ts.check_status(status)
     return r
 
