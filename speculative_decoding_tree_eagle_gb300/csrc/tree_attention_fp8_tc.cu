@@ -46,45 +46,48 @@ constexpr int HD = 128;
 constexpr int BK = 128;                      // keys per tile
 constexpr uint32_t TILE8 = BK * HD;          // codes of one tile of K or V
 constexpr uint32_t TILE16 = 2 * TILE8;       // V in fp16
-constexpr int kScaleSlots = 4;
+constexpr int kScaleSlots = 8;
+constexpr uint32_t kNoPage = 0x7FDEAD01u;    // in the place of a scale: its key's page has no id
 constexpr float kFloor = -1e30f;             // reference of a row that has met no key
 constexpr float kBelow = 7.f, kRise = 15.f;  // the reference lies kBelow under the largest y; raised when exceeded by kRise
 constexpr float kLn2f = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634074f;
 
+// R: queries' rows per CTA.  Up to 32 they are the columns of the products (keys, then channels, in the 128 rows), above they are
+// its rows ("wide": R = 128).
 template <int R>
 struct Cfg {
-  static constexpr int CPT = R == 16 ? 16 : R == 32 ? 16 : 32;  // columns per softmax thread
-  static constexpr int NG = R / CPT;                             // column groups of four warps
-  static constexpr int SOFT = 4 * NG;
-  // A TMA copy keeps its issuing warp busy for some 140 cycles and a tile of 16-token pages is 16 of them: up to 64 rows, where
-  // a tile has to be done in the time that its bytes take, K and V have two issuing warps each.
-  static constexpr int EXTRA = 4;
-  static constexpr int ISSUERS = R == 128 ? 1 : 2;
-  static constexpr int FIRST_SOFT = 8 + EXTRA;
+  static constexpr bool WIDE = R == 128;
+  static constexpr int CPT = WIDE ? 64 : 16;                     // scores per softmax thread and tile
+  static constexpr int GROUPS = WIDE ? 4 : R / CPT;              // what shares references: a quadrant's two warps, or four warps
+  static constexpr int SOFT = WIDE ? 8 : 4 * GROUPS;
+  static constexpr int FIRST_SOFT = 12;
   static constexpr int THREADS = 32 * (FIRST_SOFT + SOFT);
-  static constexpr int SK = R == 128 ? 3 : R == 16 ? 5 : 4;
-  static constexpr int SV = R >= 64 ? 2 : 4;
-  static constexpr int NP = R == 128 ? 1 : 2;                    // P buffers
+  static constexpr int SK = WIDE ? 4 : 5;
+  static constexpr int SV = 3;
+  static constexpr int NP = 2;                                   // P buffers (wide: in tensor memory)
   static constexpr int NV = 2;                                   // fp16 V buffers
-  static constexpr uint32_t PROW = R >= 64 ? 128 : 2 * R;        // bytes of a P row inside a swizzle atom
+  static constexpr uint32_t PROW = 2 * R;                        // bytes of a P^T row, the width of its swizzle
   static constexpr uint32_t QPART = R * HD;                      // one of Q's two parts
-  static constexpr uint32_t PBUF = BK * R * 2;
+  static constexpr uint32_t PBUF = WIDE ? 0 : BK * R * 2;
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_K = OFF_Q + 2 * QPART;
   static constexpr uint32_t OFF_V = OFF_K + SK * TILE8;
   static constexpr uint32_t OFF_V16 = OFF_V + SV * TILE8;
   static constexpr uint32_t OFF_P = OFF_V16 + NV * TILE16;
-  static constexpr uint32_t OFF_SC = OFF_P + NP * PBUF;          // {ks * scale * log2 e, log2 vs} per key
-  static constexpr uint32_t OFF_RM = OFF_SC + kScaleSlots * BK * 8;  // per pair of rows {r0, r1, -M0, -M1}
-  static constexpr uint32_t OFF_R2 = OFF_RM + R * 8;             // row scales of the next segment
-  static constexpr uint32_t OFF_RED = OFF_R2 + R * 4;            // [4 quarters][R]
-  static constexpr uint32_t OFF_FAC = OFF_RED + 4 * R * 4;       // [R]
+  static constexpr uint32_t OFF_RAW = OFF_P + NP * PBUF;         // {ks, vs} per key, kScaleSlots tiles
+  static constexpr uint32_t OFF_SC = OFF_RAW + kScaleSlots * BK * 8;  // wide: {ks * scale * log2 e}, {log2 vs}, {1 / vs} of two tiles
+  static constexpr uint32_t OFF_RM = OFF_SC + (WIDE ? 2 * 3 * BK * 4 : 0);  // per pair of rows {r0, r1, -M0, -M1}
+  static constexpr uint32_t OFF_R2 = OFF_RM + (WIDE ? 0 : R * 8);  // row scales of the next segment
+  static constexpr uint32_t OFF_RED = OFF_R2 + R * 4;            // exchanged maxima and sums
+  static constexpr uint32_t OFF_FAC = OFF_RED + 4 * R * 4;
   static constexpr uint32_t OFF_BAR = OFF_FAC + R * 4;
-  static constexpr int NBAR = 2 * SK + 2 * SV + 2 * NV + 4 + 2 * NP + 2 * kScaleSlots + 5;
+  static constexpr int NBAR = 2 * SK + 2 * SV + 2 * NV + 4 + 2 * NP + 2 * kScaleSlots + 4 + 5;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t SMEM = OFF_MISC + 64 + 1024;
-  static constexpr uint32_t TMEM_COLS = R == 16 ? 64 : 4 * R;    // O, S_0, S_1 (a power of two)
+  static constexpr uint32_t TMEM_COLS = R == 16 ? 64 : R == 32 ? 128 : 512;
+  static constexpr uint32_t COL_S = R;                           // O, then S_0, S_1, wide: P_0, P_1
+  static constexpr uint32_t COL_P = 3 * R;
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -200,6 +203,14 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// A from tensor memory.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, one;\n\telect.sync _|one, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // The barrier gets an arrival when the MMAs that the elected lane has issued are done.
 __device__ __forceinline__ void commit_elected(uint32_t bar) {
   asm volatile(
@@ -216,10 +227,31 @@ __device__ __forceinline__ void tma_elected(uint32_t dst, const void* tmap, uint
       : "memory");
 }
 // Instruction descriptors (fields as in idesc_bf16_f32; format 0 is e4m3 in kind f8f6f4 and fp16 in kind f16, 1 is e5m2).
-__host__ __device__ constexpr uint32_t idesc_of(int N, int b_format, int a_mn, int b_mn) {
-  return (1u << 4) | (static_cast<uint32_t>(b_format) << 10) | (static_cast<uint32_t>(a_mn) << 15) |
-         (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(BK >> 4) << 24);
+__host__ __device__ constexpr uint32_t idesc_of(int N, int a_format, int b_format, int a_mn, int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(a_format) << 7) | (static_cast<uint32_t>(b_format) << 10) |
+         (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(BK >> 4) << 24);
 }
+// Four bytes global -> shared, asynchronously, and a lane's arrival once its copies so far have landed.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_copied(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// A key's scales in the exponent's units: y = s a + lv, and 1 / vs.
+struct KeyScale {
+  float a, lv, iv;
+};
+__device__ __forceinline__ KeyScale key_scale(float2 raw, float scale_log2) {
+  KeyScale k;
+  k.a = scale_in_range(raw.x) * scale_log2;
+  k.lv = __log2f(scale_in_range(raw.y));
+  k.iv = ex2_approx(-k.lv);
+  if (__float_as_uint(raw.x) == kNoPage) k = KeyScale{0.f, -INFINITY, 0.f};
+  return k;
+}
+
 // Shared-memory descriptor with a swizzle of `row` bytes (128, 64 or 32): layout codes 2, 4, 6.
 __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t row) {
   const uint64_t layout = row == 128 ? 2 : row == 64 ? 4 : 6;
@@ -255,15 +287,17 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
       : "memory");
 }
 
-// Named barriers of the softmax's column groups: 128 threads each.
-__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
-__device__ __forceinline__ bool group_any(int group, bool v) {
+// Named barriers of the softmax's groups.
+__device__ __forceinline__ void group_sync(int group, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool group_any(int group, int threads, bool v) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(1 + group), "r"(static_cast<uint32_t>(v))
+      : "r"(1 + group), "r"(threads), "r"(static_cast<uint32_t>(v))
       : "memory");
   return r != 0u;
 }
@@ -280,21 +314,13 @@ __device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i ^
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
   if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
   const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 1;; ++it) {
+#pragma unroll 1
+  do {
     if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-    if ((it & 63u) == 0u) {
-      const bool late = global_timer_ns() - t0 > kWaitLimitNs;
-      if (__any_sync(0xffffffffu, *abort_flag != 0 || late)) {
-        if (late && (threadIdx.x & 31) == 0 && *abort_flag == 0) {
-          *abort_flag = 1;
-          report(status, TS_ERR_TIMEOUT);
-        }
-        __syncwarp();
-        if (__any_sync(0xffffffffu, late)) *abort_flag = 1;
-        return false;
-      }
-    }
-  }
+  } while (__all_sync(0xffffffffu, *abort_flag == 0 && global_timer_ns() - t0 <= kWaitLimitNs));
+  if (*abort_flag == 0) report(status, TS_ERR_TIMEOUT);
+  *abort_flag = 1;
+  return false;
 }
 
 // On the way out after a failed wait: lets copies and MMAs in flight land.
@@ -331,19 +357,465 @@ __device__ __forceinline__ float column_sums(float (&v)[N], int lane) {
   return v[0];
 }
 
+// What the softmax warps need of their CTA.
+struct Bars {
+  uint32_t s_full, s_empty, p_full, p_empty, sc_full, sc_empty, q_full, q_empty, o_free;
+};
+template <int R>
+struct Cta {
+  const Params& p;
+  Bars bar;
+  unsigned char* sptr;
+  uint32_t tmem;
+  volatile int* abort_flag;
+  volatile int* nan_seg;
+  int rg, cta, R0, rows_here;
+  __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity) const { return wait_warp(b, parity, abort_flag, p.status); }
+  // P V of tile i is done: its P buffer is free again.  (A barrier of one phase per tile would not do: the softmax may be two tiles
+  // ahead of P V, and a wait by parity would take the older phase for the newer.)
+  __device__ __forceinline__ bool o_holds(int i) const { return wait(bar.p_empty + 8 * (i & 1), (i >> 1) & 1); }
+  __device__ __forceinline__ long long slot(const Segment& s) const {
+    return (static_cast<long long>(rg) * p.Gr + cta) * 2 + (s.t0 == 0 ? 1 : 0);
+  }
+  // index of a row's query, output and log-sum-exp
+  __device__ __forceinline__ long long row_at(const Segment& s, int r) const {
+    const int row = R0 + r, node = row / p.g;
+    return (static_cast<long long>(s.b) * p.m + node) * p.Hq + s.h * p.g + row - node * p.g;
+  }
+  __device__ __forceinline__ const uint64_t* mask_of(const Segment& s, int r) const {
+    return p.mask + (static_cast<long long>(s.b) * p.m + min(R0 + r, p.rows - 1) / p.g) * p.W;
+  }
+  // V code row of tree node n (nullptr: its page has no id)
+  __device__ __forceinline__ const uint8_t* v_row(const Segment& s, int n) const {
+    const int pos = s.L + n, id = p.table[static_cast<long long>(s.b) * p.max_blocks + (pos >> p.bs_log2)];
+    if (id < 0 || id >= p.num_blocks) return nullptr;
+    return p.vc + ((static_cast<long long>(id) * p.Hkv + s.h) * p.bs + (pos & (p.bs - 1))) * HD;
+  }
+};
+__device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2f; }
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
+// Columns are rows: a thread has one key (its TMEM lane) and 16 of the R rows; four warps share the rows' references.
+template <int R>
+__device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int warp, int lane) {
+  using C = Cfg<R>;
+  constexpr int N = C::CPT;
+  const Params& p = c.p;
+  const int quarter = warp & 3, group = (warp - C::FIRST_SOFT) >> 2, col0 = group * N, key = 32 * quarter + lane;
+  const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16, tO = c.tmem + lanes + col0;
+  float* rm = reinterpret_cast<float*>(c.sptr + C::OFF_RM) + 2 * col0;  // {r0, r1, M0, M1} per pair of rows
+  float* red = reinterpret_cast<float*>(c.sptr + C::OFF_RED) + col0;    // [quarter * R + row]
+  float* shift = reinterpret_cast<float*>(c.sptr + C::OFF_FAC) + col0;
+  auto m_at = [&](int r) -> float& { return rm[(r >> 1) * 4 + 2 + (r & 1)]; };
+  // P^T [key][row]: rows of PROW bytes, 16-byte chunks swizzled with the key
+  const int swz = C::PROW == 64 ? ((key >> 1) & 3) : ((key >> 2) & 1);
+  unsigned char* prow = c.sptr + C::OFF_P + key * C::PROW;
+  Segment sg;
+  bool ok = true;
+  int it = 0, seg = 0, slot = 0, slot_phase = 0;
+  while (walk.next(p, sg)) {
+    if (ok) ok = c.wait(c.bar.q_full, seg & 1);
+    if (group_any(group, 128, !ok)) break;
+    if (quarter == 0 && lane < N) {
+      rm[(lane >> 1) * 4 + (lane & 1)] = reinterpret_cast<const float*>(c.sptr + C::OFF_R2)[col0 + lane];
+      m_at(lane) = col0 + lane < c.rows_here ? kFloor : -kFloor;  // (padding: weights 0)
+    }
+    group_sync(group, 128);
+    if (lane == 0) mbar_arrive(c.bar.q_empty);  // (the row scales are taken; the MMA warp says when Q is)
+    uint64_t l2[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) l2[i] = 0ull;
+    // The rows' constants stay in registers: {r0, r1} and {-M0, -M1}, 0 for the reference of a row that has met no key.
+    uint64_t r2[N / 2], m2[N / 2];
+    bool unmet = true;
+    auto hold = [&]() {
+      unmet = false;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const float4 k = reinterpret_cast<const float4*>(rm)[i];
+        r2[i] = pack_f32x2(k.x, k.y);
+        m2[i] = pack_f32x2(k.z == kFloor ? 0.f : -k.z, k.w == kFloor ? 0.f : -k.w);
+        unmet = unmet || k.z == kFloor || k.w == kFloor;
+      }
+    };
+    hold();
+    for (int t = sg.t0; t < sg.t1; ++t, ++it) {
+      const int s = it & 1;
+      if (ok) ok = c.wait(c.bar.sc_full + 8 * slot, slot_phase) && c.wait(c.bar.s_full + 8 * s, (it >> 1) & 1);
+      KeyScale k = {0.f, 0.f, 0.f};
+      uint32_t x[N];
+      float top = -INFINITY;
+      if (ok) {
+        tc_fence_after();
+        k = key_scale(reinterpret_cast<const float2*>(c.sptr + C::OFF_RAW)[slot * BK + key], p.scale_log2);
+        tmem_ld(c.tmem + lanes + C::COL_S + R * s + col0, x);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(c.bar.s_empty + 8 * s);
+          mbar_arrive(c.bar.sc_empty + 8 * slot);
+        }
+        const uint64_t a2 = pack_f32x2(k.a, k.a), v2 = pack_f32x2(k.lv, k.lv);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const uint64_t z2 = fma_f32x2(pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), mul_f32x2(a2, r2[i / 2]),
+                                        add_f32x2(v2, m2[i / 2]));
+          float z0, z1;
+          unpack_f32x2(z2, z0, z1);
+          x[i] = __float_as_uint(z0);
+          x[i + 1] = __float_as_uint(z1);
+        }
+        if ((t + 1) * BK > sg.L) {
+          // rows that do not attend to this thread's key
+          const int n = t * BK + key - sg.L, word = min(max(n, 0), p.m - 1) >> 6;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const uint64_t w = __ldg(c.mask_of(sg, col0 + i) + word);
+            if (k.iv == 0.f || n >= p.m || (n >= 0 && !((w >> (n & 63)) & 1ull))) x[i] = 0xFF800000u;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < N; i += 2) top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      }
+      if (++slot == kScaleSlots) slot = 0, slot_phase ^= 1;
+      if (group_any(group, 128, !ok || unmet || top > kRise)) {
+        // Rare: a reference has to rise (every unit's first tile does this).
+        if (group_any(group, 128, !ok)) {
+          ok = false;
+          break;
+        }
+        int high = 0x80000000;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float z = __uint_as_float(x[i]);
+          const int most = __reduce_max_sync(0xffffffffu, ordered(z != z ? -INFINITY : z));  // (a NaN goes into the weights alone)
+          if (lane == i) high = most;
+        }
+        if (lane < N) red[quarter * R + lane] = from_ordered(high);
+        group_sync(group, 128);
+        if (quarter == 0 && lane < N) {
+          const float old = m_at(lane), base = old == kFloor ? 0.f : old;
+          const float most = fmaxf(fmaxf(red[lane], red[R + lane]), fmaxf(red[2 * R + lane], red[3 * R + lane]));
+          float M = base + most - kBelow;
+          if (most == -INFINITY || (old != kFloor && !(M > old))) M = old;
+          m_at(lane) = M;
+          shift[lane] = base - (M == kFloor ? 0.f : M);  // to be added to z
+        }
+        group_sync(group, 128);
+        hold();
+        float f[N];  // factor of what was summed (nothing yet where the shift is upwards)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          x[i] = __float_as_uint(__uint_as_float(x[i]) + shift[i]);
+          f[i] = ex2_approx(fminf(shift[i], 0.f));
+        }
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) l2[i] = mul_f32x2(l2[i], pack_f32x2(f[2 * i], f[2 * i + 1]));
+        if (t > sg.t0) {
+          ok = c.o_holds(it - 1);
+          if (ok) {
+            tc_fence_after();
+            uint32_t o[N];
+            tmem_ld(tO, o);
+#pragma unroll
+            for (int i = 0; i < N; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i]);
+            tmem_st(tO, o);
+            tmem_st_wait();
+          }
+        }
+      }
+      if (ok) ok = c.wait(c.bar.p_empty + 8 * s, ((it >> 1) & 1) ^ 1);
+      if (!ok) continue;  // (leaves at the next vote)
+      const uint64_t iv2 = pack_f32x2(k.iv, k.iv);
+      uint32_t h[N / 2];
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float p0 = ex2_approx(__uint_as_float(x[i])), p1 = ex2_approx(__uint_as_float(x[i + 1]));
+        l2[i / 2] = fma_f32x2(pack_f32x2(p0, p1), iv2, l2[i / 2]);
+        h[i / 2] = pack_f16x2(p0, p1);
+      }
+#pragma unroll
+      for (int j = 0; j < N / 8; ++j)
+        *reinterpret_cast<uint4*>(prow + s * C::PBUF + (((col0 / 8 + j) ^ swz) << 4)) =
+            make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c.bar.p_full + 8 * s);
+    }
+    if (ok) ok = c.o_holds(it - 1);
+    if (group_any(group, 128, !ok)) break;
+    // ------------------------------ the segment's result ------------------------------
+    tc_fence_after();
+    float lv[N];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) unpack_f32x2(l2[i], lv[2 * i], lv[2 * i + 1]);
+    const float mine = column_sums(lv, lane);  // lane i: column i's sum over this warp's keys
+    if (lane < N) red[quarter * R + lane] = mine;
+    group_sync(group, 128);
+    const bool whole = sg.t0 == 0 && sg.t1 == sg.T;
+    const long long slot_at = c.slot(sg) * R + col0;
+    float l = 0.f;
+    if (lane < N) {
+      l = (red[lane] + red[R + lane]) + (red[2 * R + lane] + red[3 * R + lane]);
+      if (quarter == 0 && col0 + lane < c.rows_here) {
+        if (!whole) p.part_ml[slot_at + lane] = make_float2(m_at(lane), l);
+        else if (p.lse != nullptr) p.lse[c.row_at(sg, col0 + lane)] = lse_of(m_at(lane), l);
+      }
+    }
+    const float inv = inverse(l);
+    uint32_t o[N];
+    tmem_ld(tO, o);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar.o_free);
+    if (c.nan_seg[seg & 1] == seg + 1) {
+      // a NaN in a tree row's V: the rows that attend to it get it (this thread has channel `key`)
+#pragma unroll 1
+      for (int n = max(0, sg.t0 * BK - sg.L); n < min(p.m, sg.t1 * BK - sg.L); ++n) {
+        const uint8_t* v = c.v_row(sg, n);
+        if (v == nullptr || (v[key] & 0x7Fu) != 0x7Fu) continue;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if ((c.mask_of(sg, col0 + i)[n >> 6] >> (n & 63)) & 1ull) o[i] = 0x7FC00000u;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float f = __shfl_sync(0xffffffffu, inv, i);
+      if (col0 + i < c.rows_here) {
+        if (whole) p.out[c.row_at(sg, col0 + i) * HD + key] = __float2bfloat16_rn(__uint_as_float(o[i]) * f);
+        else p.part_o[(slot_at + i) * HD + key] = __uint_as_float(o[i]);
+      }
+    }
+    group_sync(group, 128);  // (red and the references are written again)
+    ++seg;
+  }
+}
+
+// Keys kb .. kb + 63 that a row attends to: the prefix, then the bits of its mask words for the tree, nothing behind it.
+__device__ __forceinline__ uint64_t visible64(int kb, int L, int m, const uint64_t* words, int W) {
+  const int pre = L - kb;
+  if (pre >= 64) return ~0ull;
+  const int n0 = max(0, -pre);  // first tree node among the keys
+  uint64_t bits = 0ull;
+  if (n0 < m) {
+    const int q = n0 >> 6, sh = n0 & 63;
+    bits = words[q] >> sh;
+    if (sh != 0 && q + 1 < W) bits |= words[q + 1] << (64 - sh);
+    if (m - n0 < 64) bits &= (1ull << (m - n0)) - 1ull;
+  }
+  return pre > 0 ? ((1ull << pre) - 1ull) | (bits << pre) : bits;
+}
+
+// Rows are rows: a thread has one row (its TMEM lane) and 64 of the tile's keys, the thread of the warp four further on the others;
+// both keep the row's reference.  P goes to tensor memory.
+template <int R>
+__device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int warp, int lane) {
+  using C = Cfg<R>;
+  constexpr int N = C::CPT;
+  const Params& p = c.p;
+  const int quad = warp & 3, half = (warp - C::FIRST_SOFT) >> 2, row = 32 * quad + lane;
+  if (32 * quad >= c.rows_here) return;
+  const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16, tO = c.tmem + lanes + 64 * half;
+  float* red = reinterpret_cast<float*>(c.sptr + C::OFF_RED);  // [half][row]
+  const bool valid = row < c.rows_here;
+  Segment sg;
+  bool ok = true;
+  int it = 0, seg = 0;
+  while (walk.next(p, sg)) {
+    if (ok) ok = c.wait(c.bar.q_full, seg & 1);
+    if (group_any(quad, 64, !ok)) break;
+    const float r = reinterpret_cast<const float*>(c.sptr + C::OFF_R2)[row];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar.q_empty);  // (the row scale is taken; the MMA warp says when Q is)
+    const uint64_t* words = c.mask_of(sg, row);
+    float M = valid ? kFloor : -kFloor;  // (padding: weights 0)
+    uint64_t l2 = 0ull;
+    for (int t = sg.t0; t < sg.t1; ++t, ++it) {
+      const int s = it & 1;
+      if (ok) ok = c.wait(c.bar.sc_full + 8 * s, (it >> 1) & 1) && c.wait(c.bar.s_full + 8 * s, (it >> 1) & 1);
+      const float* sc = reinterpret_cast<const float*>(c.sptr + C::OFF_SC) + s * 3 * BK + 64 * half;  // a, lv, iv of this half's keys
+      uint32_t x[N];
+      float top = -INFINITY;
+      if (ok) {
+        tc_fence_after();
+        tmem_ld64(c.tmem + lanes + C::COL_S + BK * s + 64 * half, x);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.bar.s_empty + 8 * s);
+        const float ref = M == kFloor ? 0.f : -M;
+        const uint64_t r2 = pack_f32x2(r, r), m2 = pack_f32x2(ref, ref);
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(sc + i), v = *reinterpret_cast<const float4*>(sc + BK + i);
+          const uint64_t z01 = fma_f32x2(pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                         mul_f32x2(pack_f32x2(a.x, a.y), r2), add_f32x2(pack_f32x2(v.x, v.y), m2));
+          const uint64_t z23 = fma_f32x2(pack_f32x2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
+                                         mul_f32x2(pack_f32x2(a.z, a.w), r2), add_f32x2(pack_f32x2(v.z, v.w), m2));
+          float z[4];
+          unpack_f32x2(z01, z[0], z[1]);
+          unpack_f32x2(z23, z[2], z[3]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[i + j] = __float_as_uint(z[j]);
+        }
+        if ((t + 1) * BK > sg.L) {
+          const uint64_t vis = visible64(t * BK + 64 * half, sg.L, p.m, words, p.W);
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (!((vis >> i) & 1ull) || sc[2 * BK + i] == 0.f) x[i] = 0xFF800000u;
+        }
+#pragma unroll
+        for (int i = 0; i < N; i += 2) top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      }
+      if (group_any(quad, 64, !ok || top > kRise || (M == kFloor && top > -INFINITY))) {
+        // Rare: a reference has to rise (every unit's first tile does this).
+        if (group_any(quad, 64, !ok)) {
+          ok = false;
+          break;
+        }
+        red[half * R + row] = top;
+        group_sync(quad, 64);
+        const float base = M == kFloor ? 0.f : M, most = fmaxf(top, red[(half ^ 1) * R + row]);
+        float M2 = base + most - kBelow;
+        if (most == -INFINITY || (M != kFloor && !(M2 > M))) M2 = M;
+        const float shift = base - (M2 == kFloor ? 0.f : M2), f = ex2_approx(fminf(shift, 0.f));
+        M = M2;
+        l2 = mul_f32x2(l2, pack_f32x2(f, f));
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) + shift);
+        if (t > sg.t0) {
+          ok = c.o_holds(it - 1);
+          if (ok) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < N; i += 16) {
+              uint32_t o[16];
+              tmem_ld(tO + i, o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st(tO + i, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        group_sync(quad, 64);  // (red is written again)
+      }
+      if (ok) ok = c.wait(c.bar.p_empty + 8 * s, ((it >> 1) & 1) ^ 1);
+      if (!ok) continue;  // (leaves at the next vote)
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < N; i += 32) {
+        uint32_t h[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(sc + 2 * BK + i + j);
+          const float p0 = ex2_approx(__uint_as_float(x[i + j])), p1 = ex2_approx(__uint_as_float(x[i + j + 1]));
+          const float p2 = ex2_approx(__uint_as_float(x[i + j + 2])), p3 = ex2_approx(__uint_as_float(x[i + j + 3]));
+          l2 = fma_f32x2(pack_f32x2(p0, p1), pack_f32x2(v.x, v.y), l2);
+          l2 = fma_f32x2(pack_f32x2(p2, p3), pack_f32x2(v.z, v.w), l2);
+          h[j / 2] = pack_f16x2(p0, p1);
+          h[j / 2 + 1] = pack_f16x2(p2, p3);
+        }
+        tmem_st(c.tmem + lanes + C::COL_P + 64 * s + 32 * half + i / 2, h);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(c.bar.sc_empty + 8 * s);
+        mbar_arrive(c.bar.p_full + 8 * s);
+      }
+    }
+    if (ok) ok = c.o_holds(it - 1);
+    if (group_any(quad, 64, !ok)) break;
+    // ------------------------------ the segment's result ------------------------------
+    tc_fence_after();
+    float l, other;
+    unpack_f32x2(l2, l, other);
+    l += other;
+    red[half * R + row] = l;
+    group_sync(quad, 64);
+    l = red[row] + red[R + row];  // (both threads in the same order)
+    const bool whole = sg.t0 == 0 && sg.t1 == sg.T, poison = c.nan_seg[seg & 1] == seg + 1;
+    const long long to = whole ? c.row_at(sg, row) : c.slot(sg) * R + row;
+    if (valid && half == 0) {
+      if (!whole) p.part_ml[to] = make_float2(M, l);
+      else if (p.lse != nullptr) p.lse[to] = lse_of(M, l);
+    }
+    const float inv = whole ? inverse(l) : 1.f;
+#pragma unroll 1
+    for (int i = 0; i < N; i += 16) {
+      uint32_t o[16];
+      tmem_ld(tO + i, o);
+      const int ch = 64 * half + i;
+      if (poison) {
+        // a NaN in a tree row's V: the rows that attend to it get it
+        for (int n = max(0, sg.t0 * BK - sg.L); n < min(p.m, sg.t1 * BK - sg.L); ++n) {
+          const uint8_t* v = c.v_row(sg, n);
+          if (v == nullptr || !((words[n >> 6] >> (n & 63)) & 1ull)) continue;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if ((v[ch + j] & 0x7Fu) == 0x7Fu) o[j] = 0x7FC00000u;
+        }
+      }
+      if (!valid) continue;
+      float f[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(o[j]) * inv;
+      if (whole) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + to * HD + ch);
+        dst[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+        dst[1] = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]), pack_bf16x2(f[12], f[13]), pack_bf16x2(f[14], f[15]));
+      } else {
+        float4* dst = reinterpret_cast<float4*>(p.part_o + to * HD + ch);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dst[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar.o_free);
+    group_sync(quad, 64);  // (red is written again)
+    ++seg;
+  }
+}
+
+__device__ const uint32_t g_no_page[1] = {kNoPage};
+
+// Block ids of a segment's pages by one warp: a lane holds one of 32, the next 32 are on their way.
+struct Pages {
+  int now, next, base, end, first;  // base: index (in the segment) of `now`'s first
+  __device__ __forceinline__ void begin(const Params& p, const Segment& s, int ppt, int lane) {
+    first = s.t0 * ppt;
+    end = (s.L + p.m + p.bs - 1) >> p.bs_log2;
+    base = 0;
+    now = block_at(p, s.b, first + lane, end);
+    next = block_at(p, s.b, first + 32 + lane, end);
+  }
+  // Makes `now` hold pages i .. (tile by tile; a tile's pages never straddle: both are powers of two).
+  __device__ __forceinline__ void seek(const Params& p, const Segment& s, int i, int lane) {
+    if (i < base + 32) return;
+    base += 32;
+    now = next;
+    next = block_at(p, s.b, first + base + 32 + lane, end);
+  }
+};
+
 template <int R>
 __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const __grid_constant__ Params p) {
   using C = Cfg<R>;
-  constexpr int HALF = 16;  // columns that a softmax thread works on at a time
-  constexpr int CPT = C::CPT, SK = C::SK, SV = C::SV, NP = C::NP, NV = C::NV;
+  constexpr int SK = C::SK, SV = C::SV, NP = C::NP, NV = C::NV;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   unsigned char* sptr = smem_raw + (sbase - raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rg = blockIdx.x % p.RG, cta = blockIdx.x / p.RG;
   const int R0 = rg * R, rows_here = min(R, p.rows - R0);
+  // wide: quadrants of 32 rows that hold any; the softmax warps of the others have nothing to do
+  const int soft = C::WIDE ? 2 * ((rows_here + 31) / 32) : C::SOFT;
 
   uint32_t at = sbase + C::OFF_BAR;
   auto take = [&](int n) {
@@ -353,8 +825,8 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   };
   const uint32_t full_k = take(SK), empty_k = take(SK), full_v = take(SV), empty_v = take(SV), v16_full = take(NV),
                  v16_empty = take(NV), s_full = take(2), s_empty = take(2), p_full = take(NP), p_empty = take(NP),
-                 sc_full = take(kScaleSlots), sc_empty = take(kScaleSlots), q_full = take(1),
-                 q_empty = take(1), o_free = take(1), last = take(2);
+                 raw_full = take(kScaleSlots), raw_empty = take(kScaleSlots), sc_full = take(2), sc_empty = take(2),
+                 q_full = take(1), q_empty = take(1), o_free = take(1), last = take(2);
   unsigned char* misc = sptr + C::OFF_MISC;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
@@ -362,17 +834,18 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   Walk* s_walk = reinterpret_cast<Walk*>(misc + 16);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < SK; ++i) mbar_init(full_k + 8 * i, C::ISSUERS), mbar_init(empty_k + 8 * i, 1);
-    for (int i = 0; i < SV; ++i) mbar_init(full_v + 8 * i, C::ISSUERS), mbar_init(empty_v + 8 * i, 4);
+    for (int i = 0; i < SK; ++i) mbar_init(full_k + 8 * i, 1), mbar_init(empty_k + 8 * i, 1);
+    for (int i = 0; i < SV; ++i) mbar_init(full_v + 8 * i, 1), mbar_init(empty_v + 8 * i, 4);
     for (int i = 0; i < NV; ++i) mbar_init(v16_full + 8 * i, 4), mbar_init(v16_empty + 8 * i, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(s_empty + 8 * i, C::SOFT);
-    for (int i = 0; i < NP; ++i) mbar_init(p_full + 8 * i, C::SOFT), mbar_init(p_empty + 8 * i, 1);
-    for (int i = 0; i < kScaleSlots; ++i) mbar_init(sc_full + 8 * i, 1), mbar_init(sc_empty + 8 * i, C::SOFT);
+    for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(s_empty + 8 * i, soft);
+    for (int i = 0; i < NP; ++i) mbar_init(p_full + 8 * i, soft), mbar_init(p_empty + 8 * i, 1);
+    for (int i = 0; i < kScaleSlots; ++i) mbar_init(raw_full + 8 * i, 32), mbar_init(raw_empty + 8 * i, C::WIDE ? 4 : soft);
+    for (int i = 0; i < 2; ++i) mbar_init(sc_full + 8 * i, 4), mbar_init(sc_empty + 8 * i, soft);
     mbar_init(q_full, 4);
-    mbar_init(q_empty, 1 + C::SOFT);
+    mbar_init(q_empty, 1 + soft);
+    mbar_init(o_free, soft);
     mbar_init(last, 1);
     mbar_init(last + 8, 1);
-    mbar_init(o_free, C::SOFT);
     *abort_flag = 0;
     nan_seg[0] = nan_seg[1] = 0;
     fence_mbar_init();
@@ -394,71 +867,69 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
   Walk walk = *s_walk;
   Segment sg;
   const int ppt = BK >> p.bs_log2;  // pages per tile
   bool ok = true;
 
-  // warps 8..11: second issuers of K and V, the second scale warp, and P V
-  const int part = warp >= 8 && warp < 11 ? 1 : 0;
-  const int role = warp < 4 ? warp : warp < 8 ? 5 : warp == 11 ? 4 : warp >= C::FIRST_SOFT ? 6 : C::ISSUERS == 1 || warp == 10 ? -1 : warp == 8 ? 0 : 3;
-  if (role == 0 || role == 3) {
-    // ------------------------------ codes by TMA (role 0: K, 3: V): lane i issues page ISSUERS i + part of a tile ------------------------------
-    const bool is_k = role == 0;
+  if (warp == 0 || warp == 3) {
+    // ------------------------------ codes by TMA: warp 0 K, warp 3 V ------------------------------
+    const bool is_k = warp == 0;
     const int stages = is_k ? SK : SV;
     const uint32_t full = is_k ? full_k : full_v, empty = is_k ? empty_k : empty_v;
-    const uint32_t ring = sbase + (is_k ? C::OFF_K : C::OFF_V);
+    const uint32_t ring = sbase + (is_k ? C::OFF_K : C::OFF_V), box = p.bs * HD;
     const CUtensorMap* map = is_k ? &tmk : &tmv;
-    const int my = C::ISSUERS * lane + part;
-    const int mine = (ppt + C::ISSUERS - 1 - part) / C::ISSUERS;  // pages of a tile that this warp issues
-    const bool issues = my < ppt;
-    int it = 0, stage = 0, phase = 0;
+    int it = 0, stage = 0, phase = 1;
+    Pages pg;
     while (ok && walk.next(p, sg)) {
-      const int pages = (sg.L + p.m + p.bs - 1) >> p.bs_log2;
-      int id = issues ? block_at(p, sg.b, sg.t0 * ppt + my, pages) : 0;
-      for (int t = sg.t0; t < sg.t1; ++t, ++it) {
-        const int cur = id;
-        if (issues && t + 1 < sg.t1) id = block_at(p, sg.b, (t + 1) * ppt + my, pages);
-        if (cur == -1) report(p.status, TS_ERR_DEVICE_CHECK);
-        const int blk = cur < 0 ? p.num_blocks : cur;  // (out of range: the copy fills zeros)
-        ok = wait_warp(empty + 8 * stage, phase ^ 1, abort_flag, p.status);
+      pg.begin(p, sg, ppt, lane);
+      for (int i = 0; i < (sg.t1 - sg.t0) * ppt; i += ppt, ++it) {
+        pg.seek(p, sg, i, lane);
+        if (is_k && pg.now == -1) report(p.status, TS_ERR_DEVICE_CHECK);
+        ok = wait_warp(empty + 8 * stage, phase, abort_flag, p.status);
         if (!ok) break;
-        if (lane == 0) mbar_expect_tx(full + 8 * stage, mine * p.bs * HD);
+        if (lane == 0) mbar_expect_tx(full + 8 * stage, TILE8);
         __syncwarp();
-        for (int i = 0; i < mine; ++i)
-          tma_elected(ring + stage * TILE8 + (C::ISSUERS * i + part) * p.bs * HD, map, full + 8 * stage, sg.h,
-                      __shfl_sync(0xffffffffu, blk, i));
+        const uint32_t to = ring + stage * TILE8;
+#pragma unroll 2
+        for (int j = 0; j < ppt; ++j) {
+          const int id = __shfl_sync(0xffffffffu, pg.now, i - pg.base + j);
+          tma_elected(to + j * box, map, full + 8 * stage, sg.h, id < 0 ? p.num_blocks : id);  // (out of range: zeros)
+        }
         if (++stage == stages) stage = 0, phase ^= 1;
       }
     }
     // after an abort nobody waits for what is still on its way: the newest copy of every stage
     if (!ok)
       for (int i = max(0, it - stages); i < it; ++i) drain(full + 8 * (i % stages), (i / stages) & 1);
-  } else if (role == 1) {
-    // ------------------------------ S^T = K Q^T (the warp issues as one) ------------------------------
-    constexpr uint32_t iq1 = idesc_of(R, 0, 0, 0), iq2 = idesc_of(R, 1, 0, 0);
+  } else if (warp == 1) {
+    // ------------------------------ scores: K Q^T, wide Q K^T (the warp issues as one) ------------------------------
+    constexpr int N = C::WIDE ? BK : R;
+    constexpr uint32_t iq1 = idesc_of(N, 0, 0, 0, 0), iq2 = C::WIDE ? idesc_of(N, 1, 0, 0, 0) : idesc_of(N, 0, 1, 0, 0);
     const uint64_t kdesc = sdesc(sbase + C::OFF_K, 16, 1024, 128), qdesc = sdesc(sbase + C::OFF_Q, 16, 1024, 128);
-    int it = 0, seg = 0;
+    int it = 0, seg = 0, sk = 0, phase = 0;
     while (ok && walk.next(p, sg)) {
       ok = wait_warp(q_full, seg & 1, abort_flag, p.status);
       if (!ok) break;
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
-        const int sk = it % SK, s = it & 1;
-        ok = wait_warp(full_k + 8 * sk, (it / SK) & 1, abort_flag, p.status);
-        if (!ok) break;
-        ok = wait_warp(s_empty + 8 * s, ((it >> 1) & 1) ^ 1, abort_flag, p.status);
+        const int s = it & 1;
+        ok = wait_warp(full_k + 8 * sk, phase, abort_flag, p.status) &&
+             wait_warp(s_empty + 8 * s, ((it >> 1) & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + R + R * s;
+        const uint32_t d = tmem + C::COL_S + N * s;
         // (descriptors count 16-byte units: a step of 32 bytes adds 2)
         const uint64_t kd = kdesc + static_cast<uint64_t>(sk * (TILE8 >> 4));
 #pragma unroll
-        for (int kk = 0; kk < HD / 32; ++kk) mma_f8(d, kd + 2u * kk, qdesc + 2u * kk, iq1, kk > 0 ? 1u : 0u);
-#pragma unroll
-        for (int kk = 0; kk < HD / 32; ++kk) mma_f8(d, kd + 2u * kk, qdesc + (C::QPART >> 4) + 2u * kk, iq2, 1u);
+        for (int kk = 0; kk < 2 * HD / 32; ++kk) {
+          const uint64_t a = kd + 2u * (kk & 3), b = qdesc + (C::QPART >> 4) * (kk >> 2) + 2u * (kk & 3);
+          if (C::WIDE) mma_f8(d, b, a, kk < 4 ? iq1 : iq2, kk > 0 ? 1u : 0u);
+          else mma_f8(d, a, b, kk < 4 ? iq1 : iq2, kk > 0 ? 1u : 0u);
+        }
         commit_elected(s_full + 8 * s);
         commit_elected(empty_k + 8 * sk);
+        if (++sk == SK) sk = 0, phase ^= 1;
       }
       if (!ok) break;
       commit_elected(q_empty);
@@ -469,9 +940,9 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       commit_elected(last);
       drain(last, 0);
     }
-  } else if (role == 4) {
-    // ------------------------------ O^T += V^T P^T ------------------------------
-    constexpr uint32_t ip = idesc_of(R, 0, 1, 1);
+  } else if (warp == 8) {
+    // ------------------------------ outputs: V^T P^T, wide P V ------------------------------
+    constexpr uint32_t ip = C::WIDE ? idesc_of(HD, 0, 0, 0, 1) : idesc_of(R, 0, 0, 1, 1);
     const uint64_t vdesc = sdesc(sbase + C::OFF_V16, BK * 128, 1024, 128);
     const uint64_t pdesc = sdesc(sbase + C::OFF_P, BK * 128, 8 * C::PROW, C::PROW);
     int it = 0, seg = 0;
@@ -480,18 +951,19 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       ok = wait_warp(o_free, (seg & 1) ^ 1, abort_flag, p.status);
       if (!ok) break;
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
-        const int v = it % NV, pb = it % NP;
-        ok = wait_warp(v16_full + 8 * v, (it / NV) & 1, abort_flag, p.status);
-        if (!ok) break;
-        ok = wait_warp(p_full + 8 * pb, (it / NP) & 1, abort_flag, p.status);
+        const int b = it & 1, phase = (it >> 1) & 1;
+        ok = wait_warp(v16_full + 8 * b, phase, abort_flag, p.status) && wait_warp(p_full + 8 * b, phase, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t vd = vdesc + static_cast<uint64_t>(v * (TILE16 >> 4)), pd = pdesc + static_cast<uint64_t>(pb * (C::PBUF >> 4));
+        const uint64_t vd = vdesc + static_cast<uint64_t>(b * (TILE16 >> 4)), pd = pdesc + static_cast<uint64_t>(b * (C::PBUF >> 4));
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk)
-          mma_f16(tmem, vd + (2048u >> 4) * kk, pd + C::PROW * kk, ip, kk > 0 || t > sg.t0 ? 1u : 0u);
-        commit_elected(v16_empty + 8 * v);
-        commit_elected(p_empty + 8 * pb);
+        for (int kk = 0; kk < BK / 16; ++kk) {
+          const uint32_t more = kk > 0 || t > sg.t0 ? 1u : 0u;
+          if (C::WIDE) mma_f16_ts(tmem, tmem + C::COL_P + 64 * b + 8 * kk, vd + (2048u >> 4) * kk, ip, more);
+          else mma_f16(tmem, vd + (2048u >> 4) * kk, pd + C::PROW * kk, ip, more);
+        }
+        commit_elected(v16_empty + 8 * b);
+        commit_elected(p_empty + 8 * b);
       }
       ++seg;
     }
@@ -499,70 +971,40 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       commit_elected(last + 8);
       drain(last + 8, 0);
     }
-  } else if (role == 2) {
-    // ------------------------------ scales ------------------------------
-    // Four tiles' scales are under way in registers, and the ids of the next four: one tile ahead the two dependent loads set the
-    // pace (4800 cycles a tile unprefetched, 1700 one ahead, where a tile's bytes take 1400).
-    constexpr int AHEAD = 4;
-    int it = 0;
+  } else if (warp == 2) {
+    // ------------------------------ scales: copied as they are, eight tiles ahead ------------------------------
+    int slot = 0, phase = 1;
+    Pages pg;
     while (ok && walk.next(p, sg)) {
-      const int pages = (sg.L + p.m + p.bs - 1) >> p.bs_log2, n = sg.t1 - sg.t0;
-      int id[AHEAD][4];
-      float ks[AHEAD][4], vs[AHEAD][4];
-      bool id_was[AHEAD][4];
-      auto ids = [&](int u, int i) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) id[u][j] = i < n ? block_at(p, sg.b, ((sg.t0 + i) * BK + 32 * j + lane) >> p.bs_log2, pages) : -2;
-      };
-      auto load = [&](int u, int i) {  // with the ids of tile i; a page without an id: its keys get no weight
+      pg.begin(p, sg, ppt, lane);
+      for (int i = 0; i < (sg.t1 - sg.t0) * ppt; i += ppt) {
+        pg.seek(p, sg, i, lane);
+        ok = wait_warp(raw_empty + 8 * slot, phase, abort_flag, p.status);
+        if (!ok) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          ks[u][j] = 0.f, vs[u][j] = 0.f;
-          id_was[u][j] = id[u][j] >= 0;
-          if (id_was[u][j]) {
-            const int row = ((sg.t0 + i) * BK + 32 * j + lane) & (p.bs - 1);
-            const long long o = (static_cast<long long>(id[u][j]) * p.Hkv + sg.h) * p.nsb + (row >> p.sb_log2);
-            ks[u][j] = __ldg(p.ks + o);
-            vs[u][j] = __ldg(p.vs + o);
-          }
+          const int key = 32 * j + lane;
+          const int id = __shfl_sync(0xffffffffu, pg.now, i - pg.base + (key >> p.bs_log2));
+          const long long o = (static_cast<long long>(id) * p.Hkv + sg.h) * p.nsb + ((key & (p.bs - 1)) >> p.sb_log2);
+          const float* none = reinterpret_cast<const float*>(g_no_page);
+          const uint32_t to = sbase + C::OFF_RAW + (slot * BK + key) * 8;
+          copy4(to, id >= 0 ? p.ks + o : none);
+          copy4(to + 4, id >= 0 ? p.vs + o : none);
         }
-      };
-#pragma unroll
-      for (int u = 0; u < AHEAD; ++u) ids(u, u);
-#pragma unroll
-      for (int u = 0; u < AHEAD; ++u) load(u, u);
-#pragma unroll
-      for (int u = 0; u < AHEAD; ++u) ids(u, AHEAD + u);
-      for (int i = 0; ok && i < n; i += AHEAD) {
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-          if (!ok || i + u >= n) break;
-          const int slot = (it + u) % kScaleSlots;
-          ok = wait_warp(sc_empty + 8 * slot, (((it + u) / kScaleSlots) & 1) ^ 1, abort_flag, p.status);
-          if (!ok) break;
-          float2* to = reinterpret_cast<float2*>(sptr + C::OFF_SC) + slot * BK;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            to[32 * j + lane] = make_float2(scale_in_range(ks[u][j]) * p.scale_log2,
-                                            id_was[u][j] ? __log2f(scale_in_range(vs[u][j])) : -INFINITY);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sc_full + 8 * slot);
-        }
-        it += min(AHEAD, n - i);
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) load(u, i + AHEAD + u);
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) ids(u, i + 2 * AHEAD + u);
+        arrive_copied(raw_full + 8 * slot);
+        if (++slot == kScaleSlots) slot = 0, phase ^= 1;
       }
     }
-  } else if (role == 5) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp >= 4 && warp < 8) {
     // ------------------------------ Q and V into the tensor cores' types ------------------------------
     const int w = warp - 4;
-    int it = 0, seg = 0;
+    int it = 0, seg = 0, sv = 0, phase = 0;
     while (ok && walk.next(p, sg)) {
       ok = wait_warp(q_empty, (seg & 1) ^ 1, abort_flag, p.status);
       if (!ok) break;
       // eight lanes per row, 16 values each
+#pragma unroll 1
       for (int r0 = w * 4; r0 < R; r0 += 16) {
         const int r = r0 + (lane >> 3), c = lane & 7;
         uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
@@ -573,14 +1015,9 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
           x[1] = __ldg(src + 1);
         }
         const uint32_t in[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-        float v[16];
         uint32_t big = 0;  // largest magnitude, as bits (an infinity or a NaN makes the row NaN)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[2 * j] = bf16_lo(in[j]);
-          v[2 * j + 1] = bf16_hi(in[j]);
-          big = max(big, max(__float_as_uint(v[2 * j]) & 0x7FFFFFFFu, __float_as_uint(v[2 * j + 1]) & 0x7FFFFFFFu));
-        }
+        for (int j = 0; j < 8; ++j) big = max(big, max((in[j] << 16) & 0x7FFF0000u, in[j] & 0x7FFF0000u));
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
         // 2^e: the largest magnitude times 2^-e lies in [128, 256) (2^-e in two factors, as it may pass 2^127)
@@ -592,7 +1029,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
           uint32_t a = 0, b2 = 0;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float y0 = v[4 * j + 2 * u] * f0 * f1, y1 = v[4 * j + 2 * u + 1] * f0 * f1;
+            const float y0 = bf16_lo(in[2 * j + u]) * f0 * f1, y1 = bf16_hi(in[2 * j + u]) * f0 * f1;
             const uint32_t two = encode_e4m3x2(y0, y1);
             const float2 back = decode_e4m3x2(two);
             a |= two << (16 * u);
@@ -609,26 +1046,42 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
-        const int sv = it % SV, v = it % NV;
-        ok = wait_warp(full_v + 8 * sv, (it / SV) & 1, abort_flag, p.status) &&
-             wait_warp(v16_empty + 8 * v, ((it / NV) & 1) ^ 1, abort_flag, p.status);
+        const int v = it & 1;
+        if constexpr (C::WIDE) {
+          // the tile's scales as the softmax wants them: a key per thread
+          const int slot = it % kScaleSlots, key = 32 * w + lane;
+          ok = wait_warp(raw_full + 8 * slot, (it / kScaleSlots) & 1, abort_flag, p.status) &&
+               wait_warp(sc_empty + 8 * v, ((it >> 1) & 1) ^ 1, abort_flag, p.status);
+          if (!ok) break;
+          const KeyScale k = key_scale(reinterpret_cast<const float2*>(sptr + C::OFF_RAW)[slot * BK + key], p.scale_log2);
+          float* to = reinterpret_cast<float*>(sptr + C::OFF_SC) + v * 3 * BK;
+          to[key] = k.a;
+          to[BK + key] = k.lv;
+          to[2 * BK + key] = k.iv;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(raw_empty + 8 * slot);
+            mbar_arrive(sc_full + 8 * v);
+          }
+        }
+        ok = wait_warp(full_v + 8 * sv, phase, abort_flag, p.status) &&
+             wait_warp(v16_empty + 8 * v, ((it >> 1) & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
         const unsigned char* from = sptr + C::OFF_V + sv * TILE8;
         unsigned char* to = sptr + C::OFF_V16 + v * TILE16;
-        const bool tail = (t + 1) * BK > sg.L;
         // Keys in groups of eight; of a group, lanes of one eighth of the warp take keys k and k ^ 5 and four 16-byte chunks:
         // reads (chunk c at c ^ (k % 8)) and writes (chunks 2c, 2c + 1 of the half's 128-byte row, the same way) then touch
         // all banks once.
-        const int pair = lane >> 3, k8 = (lane & 4) ? pair ^ 5 : pair, c4 = lane & 3;
+        const int pair = lane >> 3, k8 = (lane & 4) ? pair ^ 5 : pair, c4 = lane & 3, k0 = 32 * w + k8;
         // (all loads first: with a branch and a store between them each waited for its own, 2400 cycles a tile)
         uint4 x[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          x[u] = *reinterpret_cast<const uint4*>(from + ((w * 4 + (u >> 1)) * 8 + k8) * 128 + (((c4 + 4 * (u & 1)) ^ k8) << 4));
-        if (tail) {
+          x[u] = *reinterpret_cast<const uint4*>(from + (k0 + 8 * (u >> 1)) * 128 + (((c4 + 4 * (u & 1)) ^ k8) << 4));
+        if ((t + 1) * BK > sg.L) {
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const int pos = t * BK + (w * 4 + (u >> 1)) * 8 + k8;
+            const int pos = t * BK + k0 + 8 * (u >> 1);
             if (pos >= sg.L + p.m) {
               x[u] = make_uint4(0, 0, 0, 0);
             } else if (pos >= sg.L) {
@@ -644,7 +1097,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          unsigned char* row = to + (u & 1) * (BK * 128) + ((w * 4 + (u >> 1)) * 8 + k8) * 128;
+          unsigned char* row = to + (u & 1) * (BK * 128) + (k0 + 8 * (u >> 1)) * 128;
           *reinterpret_cast<uint4*>(row + (((2 * c4) ^ k8) << 4)) =
               make_uint4(decode_e4m3x2_f16(x[u].x), decode_e4m3x2_f16(x[u].x >> 16), decode_e4m3x2_f16(x[u].y),
                          decode_e4m3x2_f16(x[u].y >> 16));
@@ -658,264 +1111,15 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
           mbar_arrive(empty_v + 8 * sv);
           mbar_arrive(v16_full + 8 * v);
         }
+        if (++sv == SV) sv = 0, phase ^= 1;
       }
       ++seg;
     }
-  } else if (role == 6) {
-    // ------------------------------ softmax ------------------------------
-    const int quarter = warp & 3, group = (warp - C::FIRST_SOFT) >> 2, col0 = group * CPT;
-    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-    float4* rm = reinterpret_cast<float4*>(sptr + C::OFF_RM) + col0 / 2;  // {r0, r1, -M0, -M1} of this group's pairs
-    float* rmf = reinterpret_cast<float*>(rm);
-    float* red = reinterpret_cast<float*>(sptr + C::OFF_RED) + col0;      // [quarter * R + c]
-    float* fac = reinterpret_cast<float*>(sptr + C::OFF_FAC) + col0;
-    // P V of tile i is done: its P buffer is free again.  (A barrier of one phase per tile would not do: with two P buffers
-    // the softmax may be two tiles ahead of P V, and a wait by parity would take the older phase for the newer.)
-    auto o_holds = [&](int i) { return wait_warp(p_empty + 8 * (i % NP), (i / NP) & 1, abort_flag, p.status); };
-    auto m_at = [&](int c) -> float& { return rmf[(c >> 1) * 4 + 2 + (c & 1)]; };
-    int it = 0, seg = 0;
-    while (walk.next(p, sg)) {
-      if (ok) ok = wait_warp(q_full, seg & 1, abort_flag, p.status);
-      if (group_any(group, !ok)) {
-        ok = false;
-        break;
-      }
-      if (quarter == 0 && lane < CPT) {
-        rmf[(lane >> 1) * 4 + (lane & 1)] = reinterpret_cast<const float*>(sptr + C::OFF_R2)[col0 + lane];
-        m_at(lane) = col0 + lane < rows_here ? -kFloor : kFloor;  // (padding: weights 0)
-      }
-      group_sync(group);
-      if (lane == 0) mbar_arrive(q_empty);  // (the row scales are taken; the MMA thread says when Q is)
-      uint64_t l2[CPT / 2];
-#pragma unroll
-      for (int c = 0; c < CPT / 2; ++c) l2[c] = 0ull;
-      // {r0, r1, -M0, -M1}: with 16 columns they stay in registers
-      float4 held[HALF / 2];
-      auto hold = [&]() {
-        if (CPT == HALF) {
-#pragma unroll
-          for (int c = 0; c < HALF / 2; ++c) held[c] = rm[c];
-        }
-      };
-      hold();
-      for (int t = sg.t0; t < sg.t1; ++t, ++it) {
-        const int s = it & 1, slot = it % kScaleSlots;
-        const uint32_t tS = tmem + lanes + R + R * s + col0;
-        if (ok)
-          ok = wait_warp(sc_full + 8 * slot, (it / kScaleSlots) & 1, abort_flag, p.status) &&
-               wait_warp(s_full + 8 * s, (it >> 1) & 1, abort_flag, p.status);
-        float2 sc = make_float2(0.f, 0.f);
-        uint32_t x[HALF];
-        float zmax = -INFINITY;
-        const bool tail = (t + 1) * BK > sg.L;
-        uint32_t vis = 0u;  // bit c: row c attends to this key (tail tiles)
-        auto scores = [&](int half) {  // x <- z = y - M of 16 columns
-          tmem_ld(tS + HALF * half, x);
-          const uint64_t a2 = pack_f32x2(sc.x, sc.x), v2 = pack_f32x2(sc.y, sc.y);
-#pragma unroll
-          for (int c = 0; c < HALF; c += 2) {
-            const float4 k = CPT == HALF ? held[c / 2] : rm[(HALF * half + c) / 2];
-            const uint64_t z2 = fma_f32x2(pack_f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
-                                          mul_f32x2(a2, pack_f32x2(k.x, k.y)), add_f32x2(v2, pack_f32x2(k.z, k.w)));
-            float z0, z1;
-            unpack_f32x2(z2, z0, z1);
-            x[c] = __float_as_uint(z0);
-            x[c + 1] = __float_as_uint(z1);
-          }
-          if (tail) {
-#pragma unroll
-            for (int c = 0; c < HALF; ++c)
-              if (!((vis >> (HALF * half + c)) & 1u)) x[c] = 0xFF800000u;
-          }
-        };
-        auto highest = [&]() {
-#pragma unroll
-          for (int c = 0; c < HALF; c += 2) zmax = max3(zmax, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-        };
-        if (ok) {
-          tc_fence_after();
-          sc = reinterpret_cast<const float2*>(sptr + C::OFF_SC)[slot * BK + 32 * quarter + lane];
-          if (tail) {
-            // which of this thread's rows attend to its key
-            const int n = t * BK + 32 * quarter + lane - sg.L;
-            vis = sc.y == -INFINITY ? 0u : ~0u;
-            if (n >= p.m) vis = 0u;
-            const int word = min(max(n, 0), p.m - 1) >> 6;
-            uint32_t seen = 0u;
-#pragma unroll
-            for (int c = 0; c < CPT; ++c) {
-              const int row = min(R0 + col0 + c, p.rows - 1);
-              const uint64_t w = __ldg(p.mask + (static_cast<long long>(sg.b) * p.m + row / p.g) * p.W + word);
-              seen |= static_cast<uint32_t>((w >> (n & 63)) & 1ull) << c;
-            }
-            if (n >= 0) vis &= seen;
-          }
-          // The first pass finds whether the reference has to rise, the second makes the weights; between them 32 columns'
-          // scores stay in tensor memory (kept in registers beside the sums they spilled: 7500 cycles a tile of 128 rows).
-#pragma unroll
-          for (int half = 0; half < CPT / HALF; ++half) {
-            scores(half);
-            highest();
-          }
-        }
-        if (group_any(group, !ok || zmax > kRise)) {
-          // Rare: a reference has to rise (every unit's first tile does this).
-          if (group_any(group, !ok)) {
-            ok = false;
-            break;
-          }
-          int top = 0x80000000;
-#pragma unroll
-          for (int half = 0; half < CPT / HALF; ++half) {
-            tmem_ld(tS + HALF * half, x);
-#pragma unroll
-            for (int i = 0; i < HALF; ++i) {
-              const int c = HALF * half + i;
-              const float r = rmf[(c >> 1) * 4 + (c & 1)];
-              float y = fmaf(__uint_as_float(x[i]), sc.x * r, sc.y);
-              if (y != y || (tail && !((vis >> c) & 1u))) y = -INFINITY;  // (a NaN goes into the weights, not into the reference)
-              const int most = __reduce_max_sync(0xffffffffu, ordered(y));
-              if (lane == c) top = most;
-            }
-          }
-          if (lane < CPT) red[quarter * R + lane] = from_ordered(top);
-          group_sync(group);
-          if (quarter == 0 && lane < CPT) {
-            const float old = -m_at(lane);
-            const float most = fmaxf(fmaxf(red[lane], red[R + lane]), fmaxf(red[2 * R + lane], red[3 * R + lane])) - kBelow;
-            const float M = most > old ? most : old;
-            fac[lane] = M == old ? 1.f : ex2_approx(old - M);
-            m_at(lane) = -M;
-          }
-          group_sync(group);
-#pragma unroll
-          for (int c = 0; c < CPT / 2; ++c) l2[c] = mul_f32x2(l2[c], pack_f32x2(fac[2 * c], fac[2 * c + 1]));
-          if (t > sg.t0) {
-            ok = o_holds(it - 1);
-            if (ok) {
-              tc_fence_after();
-#pragma unroll
-              for (int half = 0; half < CPT / HALF; ++half) {
-                tmem_ld(tmem + lanes + col0 + HALF * half, x);
-#pragma unroll
-                for (int c = 0; c < HALF; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * fac[HALF * half + c]);
-                tmem_st(tmem + lanes + col0 + HALF * half, x);
-              }
-              tmem_st_wait();
-            }
-          }
-          hold();
-          if (CPT == HALF) scores(0);
-        }
-        const int pb = it % NP;
-        if (ok) ok = wait_warp(p_empty + 8 * pb, ((it / NP) & 1) ^ 1, abort_flag, p.status);
-        if (!ok) continue;  // (leaves at the next vote)
-        const float iv = sc.y == -INFINITY ? 0.f : ex2_approx(-sc.y);
-        const uint64_t iv2 = pack_f32x2(iv, iv);
-        // P^T [key][row]: rows of PROW bytes, 16-byte chunks swizzled with the key
-        const int k = 32 * quarter + lane;
-        unsigned char* prow = sptr + C::OFF_P + pb * C::PBUF + (col0 / 64) * (BK * 128) + k * C::PROW;
-        const int chunk0 = (col0 % 64) / 8;
-        const int swz = C::PROW == 128 ? (k & 7) : C::PROW == 64 ? ((k >> 1) & 3) : ((k >> 2) & 1);
-#pragma unroll
-        for (int half = 0; half < CPT / HALF; ++half) {
-          if (CPT > HALF) scores(half);
-          if (half + 1 == CPT / HALF) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(s_empty + 8 * s);
-              mbar_arrive(sc_empty + 8 * slot);
-            }
-          }
-          uint32_t h[HALF / 2];
-#pragma unroll
-          for (int c = 0; c < HALF; c += 2) {
-            const float p0 = ex2_approx(__uint_as_float(x[c])), p1 = ex2_approx(__uint_as_float(x[c + 1]));
-            uint64_t& l = l2[HALF / 2 * half + c / 2];
-            l = fma_f32x2(pack_f32x2(p0, p1), iv2, l);
-            h[c / 2] = pack_f16x2(p0, p1);
-          }
-#pragma unroll
-          for (int j = 0; j < HALF / 8; ++j)
-            *reinterpret_cast<uint4*>(prow + (((chunk0 + HALF / 8 * half + j) ^ swz) << 4)) =
-                make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * pb);
-      }
-      if (ok) ok = o_holds(it - 1);
-      if (group_any(group, !ok)) {
-        ok = false;
-        break;
-      }
-      // ------------------------------ the segment's result ------------------------------
-      tc_fence_after();
-      float lv[CPT];
-#pragma unroll
-      for (int c = 0; c < CPT / 2; ++c) unpack_f32x2(l2[c], lv[2 * c], lv[2 * c + 1]);
-      const float mine = column_sums(lv, lane);  // lane c: column c's sum over this warp's keys
-      if (lane < CPT) red[quarter * R + lane] = mine;
-      group_sync(group);
-      const bool whole = sg.t0 == 0 && sg.t1 == sg.T;
-      float l = 0.f, M = 0.f;
-      if (lane < CPT) {
-        l = (red[lane] + red[R + lane]) + (red[2 * R + lane] + red[3 * R + lane]);
-        M = -m_at(lane);
-      }
-      const int ch = 32 * quarter + lane;
-      const long long slot = (static_cast<long long>(rg) * p.Gr + cta) * 2 + (sg.t0 == 0 ? 1 : 0);
-      if (lane < CPT && quarter == 0 && col0 + lane < rows_here) {
-        const int row = R0 + col0 + lane, node = row / p.g, head = sg.h * p.g + row % p.g;
-        if (!whole) p.part_ml[slot * R + col0 + lane] = make_float2(M, l);
-        else if (p.lse != nullptr)
-          p.lse[(static_cast<long long>(sg.b) * p.m + node) * p.Hq + head] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2f;
-      }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-      for (int half = 0; half < CPT / HALF; ++half) {
-        uint32_t o[HALF];
-        tmem_ld(tmem + lanes + col0 + HALF * half, o);
-        if (half + 1 == CPT / HALF) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(o_free);
-        }
-        const int first = col0 + HALF * half;
-        if (nan_seg[seg & 1] == seg + 1) {
-          // a NaN in a tree row's V: the rows that attend to it get it
-          for (int n = max(0, sg.t0 * BK - sg.L); n < min(p.m, sg.t1 * BK - sg.L); ++n) {
-            const int pos = sg.L + n, id = p.table[static_cast<long long>(sg.b) * p.max_blocks + (pos >> p.bs_log2)];
-            if (id < 0 || id >= p.num_blocks) continue;
-            const uint32_t code = p.vc[((static_cast<long long>(id) * p.Hkv + sg.h) * p.bs + (pos & (p.bs - 1))) * HD + ch];
-            if ((code & 0x7Fu) != 0x7Fu) continue;
-#pragma unroll
-            for (int c = 0; c < HALF; ++c) {
-              const int row = min(R0 + first + c, p.rows - 1);
-              const uint64_t word = __ldg(p.mask + (static_cast<long long>(sg.b) * p.m + row / p.g) * p.W + (n >> 6));
-              if ((word >> (n & 63)) & 1ull) o[c] = 0x7FC00000u;
-            }
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < HALF; ++c) {
-          const float f = __shfl_sync(0xffffffffu, inv, HALF * half + c);
-          if (first + c < rows_here) {
-            if (whole) {
-              const int row = R0 + first + c, node = row / p.g, head = sg.h * p.g + row % p.g;
-              p.out[((static_cast<long long>(sg.b) * p.m + node) * p.Hq + head) * HD + ch] =
-                  __float2bfloat16_rn(__uint_as_float(o[c]) * f);
-            } else {
-              p.part_o[(slot * R + first + c) * HD + ch] = __uint_as_float(o[c]);
-            }
-          }
-        }
-      }
-      group_sync(group);  // (red and the references are written again)
-      ++seg;
-    }
+  } else if (warp >= C::FIRST_SOFT) {
+    const Bars bars{s_full, s_empty, p_full, p_empty, C::WIDE ? sc_full : raw_full, C::WIDE ? sc_empty : raw_empty, q_full, q_empty, o_free};
+    const Cta<R> c{p, bars, sptr, tmem, abort_flag, nan_seg, rg, cta, R0, rows_here};
+    if constexpr (C::WIDE) softmax_wide(c, walk, warp, lane);
+    else softmax_narrow(c, walk, warp, lane);
   }
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
@@ -985,7 +1189,7 @@ constexpr int kMinTiles = 2;
 Plan plan_of(int B, int m, int Hq, int Hkv, int max_prefix, int num_sms) {
   const int rows = m * (Hq / Hkv);
   Plan pl;
-  pl.R = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  pl.R = rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
   pl.RG = (rows + pl.R - 1) / pl.R;
   const long long tiles = (static_cast<long long>(max_prefix) + m + BK - 1) / BK * B * Hkv;
   const long long want = std::max(1LL, tiles / kMinTiles);
@@ -1071,7 +1275,6 @@ int attention_fp8_tc_launch(const Fp8AttnCall& a, cudaStream_t stream, int num_s
   switch (pl.R) {
     case 16: return launch<16>(p, mk, mv, stream);
     case 32: return launch<32>(p, mk, mv, stream);
-    case 64: return launch<64>(p, mk, mv, stream);
     default: return launch<128>(p, mk, mv, stream);
   }
 }
