@@ -28,8 +28,9 @@
 // to the workspace and join_kernel merges them.  With several row groups CTAs of neighbouring index walk the same tiles
 // for different rows, so all but one read them from L2.
 //
-// Warps: 0 TMA copies of K, 1 K Q^T and owner of the tensor memory, 2 scales, 3 copies of V, 4..7 Q and V converters, 8 and 9 second
-// ones of 0 and 3, 10 idle, 11 V^T P^T, from 12 on softmax: four warps (one per 32 TMEM lanes) for every CPT columns.
+// Warps: 0 TMA copies of K and copies of the scales, 1 K Q^T and owner of the tensor memory, 2 V^T P^T, 3 TMA copies of V, 4..7 Q and V
+// converters, from 8 on the softmax.  The roles share one instruction cache: code that every tile runs is kept short, and
+// code that runs once per unit is rolled up (unrolled, half of the fetches missed and every warp waited for them).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -46,7 +47,7 @@ constexpr int HD = 128;
 constexpr int BK = 128;                      // keys per tile
 constexpr uint32_t TILE8 = BK * HD;          // codes of one tile of K or V
 constexpr uint32_t TILE16 = 2 * TILE8;       // V in fp16
-constexpr int kScaleSlots = 8;
+constexpr int kScaleSlots = 6;
 constexpr uint32_t kNoPage = 0x7FDEAD01u;    // in the place of a scale: its key's page has no id
 constexpr float kFloor = -1e30f;             // reference of a row that has met no key
 constexpr float kBelow = 7.f, kRise = 15.f;  // the reference lies kBelow under the largest y; raised when exceeded by kRise
@@ -61,7 +62,7 @@ struct Cfg {
   static constexpr int CPT = WIDE ? 64 : 16;                     // scores per softmax thread and tile
   static constexpr int GROUPS = WIDE ? 4 : R / CPT;              // what shares references: a quadrant's two warps, or four warps
   static constexpr int SOFT = WIDE ? 8 : 4 * GROUPS;
-  static constexpr int FIRST_SOFT = 12;
+  static constexpr int FIRST_SOFT = 8;
   static constexpr int THREADS = 32 * (FIRST_SOFT + SOFT);
   static constexpr int SK = WIDE ? 4 : 5;
   static constexpr int SV = 3;
@@ -81,7 +82,8 @@ struct Cfg {
   static constexpr uint32_t OFF_R2 = OFF_RM + (WIDE ? 0 : R * 8);  // row scales of the next segment
   static constexpr uint32_t OFF_RED = OFF_R2 + R * 4;            // exchanged maxima and sums
   static constexpr uint32_t OFF_FAC = OFF_RED + 4 * R * 4;
-  static constexpr uint32_t OFF_BAR = OFF_FAC + R * 4;
+  static constexpr uint32_t OFF_VIS = OFF_FAC + R * 4;           // columns: mask words of the rows
+  static constexpr uint32_t OFF_BAR = OFF_VIS + (WIDE ? 0 : R * 32);
   static constexpr int NBAR = 2 * SK + 2 * SV + 2 * NV + 4 + 2 * NP + 2 * kScaleSlots + 4 + 5;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t SMEM = OFF_MISC + 64 + 1024;
@@ -121,8 +123,7 @@ struct Segment {
 };
 // The segments of the tile range [x, x1), from sequence b on; `off` tiles into its unit h.
 struct Walk {
-  long long x, x1;
-  int b, h, off;
+  int x, x1, b, h, off;
   __device__ __forceinline__ bool next(const Params& p, Segment& s) {
     if (x >= x1) return false;
     int T = tiles_of(p, b);
@@ -132,7 +133,7 @@ struct Walk {
     }
     s.b = b, s.h = h, s.T = T, s.L = p.prefix_len[b];
     s.t0 = off;
-    s.t1 = static_cast<int>(min(static_cast<long long>(T), off + (x1 - x)));
+    s.t1 = min(T, off + (x1 - x));
     x += s.t1 - s.t0;
     off = s.t1;
     if (off == T) {
@@ -143,43 +144,46 @@ struct Walk {
   }
 };
 
-// All tiles of a row group, and where tile x lies (by one warp).
-__device__ __forceinline__ long long total_tiles(const Params& p, int lane) {
-  long long n = 0;
-  for (int b = lane; b < p.B; b += 32) n += tiles_of(p, b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n * p.Hkv;
-}
-__device__ __forceinline__ Walk walk_from(const Params& p, long long x, long long x1, int lane) {
-  Walk w{x, x1, 0, 0, 0};
-  long long before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
+// How N tiles are dealt out to CTAs: the first `more` of them get one more than `each`.  (No CTA between two parts of a unit is without
+// tiles.)
+struct Share {
+  int each, more;
+  __device__ __forceinline__ Share(int N, int Gr) : each(N / Gr), more(N - N / Gr * Gr) {}
+  __device__ __forceinline__ int start(int c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int cta_of(int x) const {
+    const int wide = more * (each + 1);
+    return x < wide ? x / (each + 1) : more + (x - wide) / each;
+  }
+};
+
+// The run of tiles of CTA `cta`: all tiles of a row group in the order of sequences and heads, dealt out (by one warp).
+__device__ __forceinline__ Walk walk_of(const Params& p, int cta, int lane) {
+  int N = 0;
+  for (int b = lane; b < p.B; b += 32) N += tiles_of(p, b);
+  N = static_cast<int>(__reduce_add_sync(0xffffffffu, N)) * p.Hkv;
+  const Share share(N, p.Gr);
+  Walk w{share.start(cta), share.start(cta + 1), 0, 0, 0};
+  int before = 0;
+  for (int b0 = 0; b0 < p.B && w.x < w.x1; b0 += 32) {
     const int T = b0 + lane < p.B ? tiles_of(p, b0 + lane) : 0;
-    long long sum = static_cast<long long>(T) * p.Hkv;
+    int sum = T * p.Hkv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += y;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + sum > x);
+    const unsigned hit = __ballot_sync(0xffffffffu, before + sum > w.x);
     if (hit != 0u) {
-      const int l = __ffs(hit) - 1;
-      const int Tl = __shfl_sync(0xffffffffu, T, l);
-      const long long at = x - (before + __shfl_sync(0xffffffffu, sum, l) - static_cast<long long>(Tl) * p.Hkv);
+      const int l = __ffs(hit) - 1, Tl = __shfl_sync(0xffffffffu, T, l);
+      const int at = w.x - (before + __shfl_sync(0xffffffffu, sum, l) - Tl * p.Hkv);
       w.b = b0 + l;
-      w.h = static_cast<int>(at / Tl);
-      w.off = static_cast<int>(at - static_cast<long long>(w.h) * Tl);
-      return w;
+      w.h = at / Tl;
+      w.off = at - w.h * Tl;
+      break;
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
   }
   return w;
-}
-
-// The CTA of a row group whose range [c N / Gr, (c + 1) N / Gr) holds tile x (Gr <= N).
-__device__ __forceinline__ int cta_of(long long x, long long N, long long Gr) {
-  return static_cast<int>(((x + 1) * Gr + N - 1) / N) - 1;
 }
 
 __device__ __forceinline__ int block_at(const Params& p, int b, int lp, int pages) {
@@ -285,6 +289,16 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       TS_W8(0), TS_W8(8)
       : "memory");
+}
+
+// One column.
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr) : "memory");
+  return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
 }
 
 // Named barriers of the softmax's groups.
@@ -405,7 +419,8 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
   const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16, tO = c.tmem + lanes + col0;
   float* rm = reinterpret_cast<float*>(c.sptr + C::OFF_RM) + 2 * col0;  // {r0, r1, M0, M1} per pair of rows
   float* red = reinterpret_cast<float*>(c.sptr + C::OFF_RED) + col0;    // [quarter * R + row]
-  float* shift = reinterpret_cast<float*>(c.sptr + C::OFF_FAC) + col0;
+  float* factor = reinterpret_cast<float*>(c.sptr + C::OFF_FAC) + col0;
+  uint64_t* vis = reinterpret_cast<uint64_t*>(c.sptr + C::OFF_VIS) + 4 * col0;  // mask words of this group's rows
   auto m_at = [&](int r) -> float& { return rm[(r >> 1) * 4 + 2 + (r & 1)]; };
   // P^T [key][row]: rows of PROW bytes, 16-byte chunks swizzled with the key
   const int swz = C::PROW == 64 ? ((key >> 1) & 3) : ((key >> 2) & 1);
@@ -419,6 +434,10 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
     if (quarter == 0 && lane < N) {
       rm[(lane >> 1) * 4 + (lane & 1)] = reinterpret_cast<const float*>(c.sptr + C::OFF_R2)[col0 + lane];
       m_at(lane) = col0 + lane < c.rows_here ? kFloor : -kFloor;  // (padding: weights 0)
+      if (sg.t1 * BK > sg.L) {
+        const uint64_t* words = c.mask_of(sg, col0 + lane);
+        for (int i = 0; i < p.W; ++i) vis[4 * lane + i] = words[i];
+      }
     }
     group_sync(group, 128);
     if (lane == 0) mbar_arrive(c.bar.q_empty);  // (the row scales are taken; the MMA warp says when Q is)
@@ -439,91 +458,97 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
       }
     };
     hold();
+    bool left = false;
     for (int t = sg.t0; t < sg.t1; ++t, ++it) {
       const int s = it & 1;
+      const bool tail = (t + 1) * BK > sg.L;
+      const uint32_t tS = c.tmem + lanes + C::COL_S + R * s + col0;
       if (ok) ok = c.wait(c.bar.sc_full + 8 * slot, slot_phase) && c.wait(c.bar.s_full + 8 * s, (it >> 1) & 1);
       KeyScale k = {0.f, 0.f, 0.f};
       uint32_t x[N];
-      float top = -INFINITY;
+      uint32_t seen = ~0u;  // rows that attend to this thread's key
       if (ok) {
         tc_fence_after();
         k = key_scale(reinterpret_cast<const float2*>(c.sptr + C::OFF_RAW)[slot * BK + key], p.scale_log2);
-        tmem_ld(c.tmem + lanes + C::COL_S + R * s + col0, x);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(c.bar.s_empty + 8 * s);
-          mbar_arrive(c.bar.sc_empty + 8 * slot);
-        }
-        const uint64_t a2 = pack_f32x2(k.a, k.a), v2 = pack_f32x2(k.lv, k.lv);
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-          const uint64_t z2 = fma_f32x2(pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), mul_f32x2(a2, r2[i / 2]),
-                                        add_f32x2(v2, m2[i / 2]));
-          float z0, z1;
-          unpack_f32x2(z2, z0, z1);
-          x[i] = __float_as_uint(z0);
-          x[i + 1] = __float_as_uint(z1);
-        }
-        if ((t + 1) * BK > sg.L) {
-          // rows that do not attend to this thread's key
-          const int n = t * BK + key - sg.L, word = min(max(n, 0), p.m - 1) >> 6;
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const uint64_t w = __ldg(c.mask_of(sg, col0 + i) + word);
-            if (k.iv == 0.f || n >= p.m || (n >= 0 && !((w >> (n & 63)) & 1ull))) x[i] = 0xFF800000u;
+        if (tail) {
+          const int n = t * BK + key - sg.L;
+          if (k.iv == 0.f || n >= p.m) {
+            seen = 0u;
+          } else if (n >= 0) {
+            seen = 0u;
+#pragma unroll 4
+            for (int i = 0; i < N; ++i) seen |= static_cast<uint32_t>((vis[i * 4 + (n >> 6)] >> (n & 63)) & 1ull) << i;
           }
         }
-#pragma unroll
-        for (int i = 0; i < N; i += 2) top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
       }
-      if (++slot == kScaleSlots) slot = 0, slot_phase ^= 1;
-      if (group_any(group, 128, !ok || unmet || top > kRise)) {
-        // Rare: a reference has to rise (every unit's first tile does this).
+      const uint64_t a2 = pack_f32x2(k.a, k.a), v2 = pack_f32x2(k.lv, k.lv);
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        float top = -INFINITY;
+        if (ok) {
+          tmem_ld(tS, x);
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {
+            const uint64_t z2 = fma_f32x2(pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), mul_f32x2(a2, r2[i / 2]),
+                                          add_f32x2(v2, m2[i / 2]));
+            float z0, z1;
+            unpack_f32x2(z2, z0, z1);
+            x[i] = __float_as_uint(z0);
+            x[i + 1] = __float_as_uint(z1);
+          }
+          if (tail) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (!((seen >> i) & 1u)) x[i] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int i = 0; i < N; i += 2) top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+        }
+        if (again || !group_any(group, 128, !ok || unmet || top > kRise)) break;
+        // Rare (every unit's first tile does this): the references rise to the tile's largest, and the scores are taken again.
         if (group_any(group, 128, !ok)) {
-          ok = false;
+          left = true;
           break;
         }
         int high = 0x80000000;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < N; ++i) {
-          const float z = __uint_as_float(x[i]);
-          const int most = __reduce_max_sync(0xffffffffu, ordered(z != z ? -INFINITY : z));  // (a NaN goes into the weights alone)
+          float y = fmaf(tmem_ld1(tS + i), k.a * rm[(i >> 1) * 4 + (i & 1)], k.lv);
+          if (y != y || !((seen >> i) & 1u)) y = -INFINITY;  // (a NaN goes into the weights, not into the reference)
+          const int most = __reduce_max_sync(0xffffffffu, ordered(y));
           if (lane == i) high = most;
         }
         if (lane < N) red[quarter * R + lane] = from_ordered(high);
         group_sync(group, 128);
         if (quarter == 0 && lane < N) {
-          const float old = m_at(lane), base = old == kFloor ? 0.f : old;
-          const float most = fmaxf(fmaxf(red[lane], red[R + lane]), fmaxf(red[2 * R + lane], red[3 * R + lane]));
-          float M = base + most - kBelow;
-          if (most == -INFINITY || (old != kFloor && !(M > old))) M = old;
-          m_at(lane) = M;
-          shift[lane] = base - (M == kFloor ? 0.f : M);  // to be added to z
+          const float old = m_at(lane);
+          const float M = fmaxf(fmaxf(red[lane], red[R + lane]), fmaxf(red[2 * R + lane], red[3 * R + lane])) - kBelow;
+          const bool rises = M > old;  // (kFloor before the first key, and nothing where there is none yet)
+          factor[lane] = rises && old != kFloor ? ex2_approx(old - M) : 1.f;
+          if (rises) m_at(lane) = M;
         }
         group_sync(group, 128);
         hold();
-        float f[N];  // factor of what was summed (nothing yet where the shift is upwards)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          x[i] = __float_as_uint(__uint_as_float(x[i]) + shift[i]);
-          f[i] = ex2_approx(fminf(shift[i], 0.f));
-        }
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) l2[i] = mul_f32x2(l2[i], pack_f32x2(f[2 * i], f[2 * i + 1]));
+        for (int i = 0; i < N / 2; ++i) l2[i] = mul_f32x2(l2[i], *reinterpret_cast<const uint64_t*>(factor + 2 * i));
         if (t > sg.t0) {
           ok = c.o_holds(it - 1);
           if (ok) {
             tc_fence_after();
-            uint32_t o[N];
-            tmem_ld(tO, o);
-#pragma unroll
-            for (int i = 0; i < N; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i]);
-            tmem_st(tO, o);
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) tmem_st1(tO + i, tmem_ld1(tO + i) * factor[i]);
             tmem_st_wait();
           }
         }
       }
+      if (left) break;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(c.bar.s_empty + 8 * s);
+        mbar_arrive(c.bar.sc_empty + 8 * slot);
+      }
+      if (++slot == kScaleSlots) slot = 0, slot_phase ^= 1;
       if (ok) ok = c.wait(c.bar.p_empty + 8 * s, ((it >> 1) & 1) ^ 1);
       if (!ok) continue;  // (leaves at the next vote)
       const uint64_t iv2 = pack_f32x2(k.iv, k.iv);
@@ -543,6 +568,7 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
       __syncwarp();
       if (lane == 0) mbar_arrive(c.bar.p_full + 8 * s);
     }
+    if (left) ok = false;
     if (ok) ok = c.o_holds(it - 1);
     if (group_any(group, 128, !ok)) break;
     // ------------------------------ the segment's result ------------------------------
@@ -563,31 +589,25 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
         else if (p.lse != nullptr) p.lse[c.row_at(sg, col0 + lane)] = lse_of(m_at(lane), l);
       }
     }
-    const float inv = inverse(l);
-    uint32_t o[N];
-    tmem_ld(tO, o);
+    const float inv = whole ? inverse(l) : 1.f;
+    const bool poison = c.nan_seg[seg & 1] == seg + 1;
+#pragma unroll 1
+    for (int i = 0; i < min(N, c.rows_here - col0); ++i) {
+      float o = tmem_ld1(tO + i) * __shfl_sync(0xffffffffu, inv, i);
+      if (poison) {
+        // a NaN in a tree row's V: the rows that attend to it get it (this thread has channel `key`)
+        for (int n = max(0, sg.t0 * BK - sg.L); n < min(p.m, sg.t1 * BK - sg.L); ++n) {
+          const uint8_t* v = c.v_row(sg, n);
+          if (v != nullptr && (v[key] & 0x7Fu) == 0x7Fu && ((vis[4 * i + (n >> 6)] >> (n & 63)) & 1ull)) o = __int_as_float(0x7FC00000);
+        }
+      }
+      if (whole) p.out[c.row_at(sg, col0 + i) * HD + key] = __float2bfloat16_rn(o);
+      else p.part_o[(slot_at + i) * HD + key] = o;
+      __syncwarp();
+    }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(c.bar.o_free);
-    if (c.nan_seg[seg & 1] == seg + 1) {
-      // a NaN in a tree row's V: the rows that attend to it get it (this thread has channel `key`)
-#pragma unroll 1
-      for (int n = max(0, sg.t0 * BK - sg.L); n < min(p.m, sg.t1 * BK - sg.L); ++n) {
-        const uint8_t* v = c.v_row(sg, n);
-        if (v == nullptr || (v[key] & 0x7Fu) != 0x7Fu) continue;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if ((c.mask_of(sg, col0 + i)[n >> 6] >> (n & 63)) & 1ull) o[i] = 0x7FC00000u;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float f = __shfl_sync(0xffffffffu, inv, i);
-      if (col0 + i < c.rows_here) {
-        if (whole) p.out[c.row_at(sg, col0 + i) * HD + key] = __float2bfloat16_rn(__uint_as_float(o[i]) * f);
-        else p.part_o[(slot_at + i) * HD + key] = __uint_as_float(o[i]);
-      }
-    }
     group_sync(group, 128);  // (red and the references are written again)
     ++seg;
   }
@@ -632,58 +652,57 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
     const uint64_t* words = c.mask_of(sg, row);
     float M = valid ? kFloor : -kFloor;  // (padding: weights 0)
     uint64_t l2 = 0ull;
+    bool left = false;
     for (int t = sg.t0; t < sg.t1; ++t, ++it) {
       const int s = it & 1;
       if (ok) ok = c.wait(c.bar.sc_full + 8 * s, (it >> 1) & 1) && c.wait(c.bar.s_full + 8 * s, (it >> 1) & 1);
       const float* sc = reinterpret_cast<const float*>(c.sptr + C::OFF_SC) + s * 3 * BK + 64 * half;  // a, lv, iv of this half's keys
       uint32_t x[N];
-      float top = -INFINITY;
-      if (ok) {
-        tc_fence_after();
-        tmem_ld64(c.tmem + lanes + C::COL_S + BK * s + 64 * half, x);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(c.bar.s_empty + 8 * s);
-        const float ref = M == kFloor ? 0.f : -M;
-        const uint64_t r2 = pack_f32x2(r, r), m2 = pack_f32x2(ref, ref);
+      const bool tail = (t + 1) * BK > sg.L;
+      if (ok) tc_fence_after();
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        float top = -INFINITY;
+        if (ok) {
+          tmem_ld64(c.tmem + lanes + C::COL_S + BK * s + 64 * half, x);
+          const float ref = M == kFloor ? 0.f : -M;
+          const uint64_t r2 = pack_f32x2(r, r), m2 = pack_f32x2(ref, ref);
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-          const float4 a = *reinterpret_cast<const float4*>(sc + i), v = *reinterpret_cast<const float4*>(sc + BK + i);
-          const uint64_t z01 = fma_f32x2(pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                                         mul_f32x2(pack_f32x2(a.x, a.y), r2), add_f32x2(pack_f32x2(v.x, v.y), m2));
-          const uint64_t z23 = fma_f32x2(pack_f32x2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
-                                         mul_f32x2(pack_f32x2(a.z, a.w), r2), add_f32x2(pack_f32x2(v.z, v.w), m2));
-          float z[4];
-          unpack_f32x2(z01, z[0], z[1]);
-          unpack_f32x2(z23, z[2], z[3]);
+          for (int i = 0; i < N; i += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(sc + i), v = *reinterpret_cast<const float4*>(sc + BK + i);
+            const uint64_t z01 = fma_f32x2(pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                           mul_f32x2(pack_f32x2(a.x, a.y), r2), add_f32x2(pack_f32x2(v.x, v.y), m2));
+            const uint64_t z23 = fma_f32x2(pack_f32x2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
+                                           mul_f32x2(pack_f32x2(a.z, a.w), r2), add_f32x2(pack_f32x2(v.z, v.w), m2));
+            float z[4];
+            unpack_f32x2(z01, z[0], z[1]);
+            unpack_f32x2(z23, z[2], z[3]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[i + j] = __float_as_uint(z[j]);
+            for (int j = 0; j < 4; ++j) x[i + j] = __float_as_uint(z[j]);
+          }
+          if (tail) {
+            const uint64_t vis = visible64(t * BK + 64 * half, sg.L, p.m, words, p.W);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (!((vis >> i) & 1ull) || sc[2 * BK + i] == 0.f) x[i] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int i = 0; i < N; i += 2) top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
         }
-        if ((t + 1) * BK > sg.L) {
-          const uint64_t vis = visible64(t * BK + 64 * half, sg.L, p.m, words, p.W);
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (!((vis >> i) & 1ull) || sc[2 * BK + i] == 0.f) x[i] = 0xFF800000u;
-        }
-#pragma unroll
-        for (int i = 0; i < N; i += 2) top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-      }
-      if (group_any(quad, 64, !ok || top > kRise || (M == kFloor && top > -INFINITY))) {
-        // Rare: a reference has to rise (every unit's first tile does this).
+        if (again || !group_any(quad, 64, !ok || top > kRise || (M == kFloor && top > -INFINITY))) break;
+        // Rare (every unit's first tile does this): the reference rises to the tile's largest, and the scores are taken again.
         if (group_any(quad, 64, !ok)) {
-          ok = false;
+          left = true;
           break;
         }
         red[half * R + row] = top;
         group_sync(quad, 64);
-        const float base = M == kFloor ? 0.f : M, most = fmaxf(top, red[(half ^ 1) * R + row]);
-        float M2 = base + most - kBelow;
-        if (most == -INFINITY || (M != kFloor && !(M2 > M))) M2 = M;
-        const float shift = base - (M2 == kFloor ? 0.f : M2), f = ex2_approx(fminf(shift, 0.f));
-        M = M2;
+        const float high = (M == kFloor ? 0.f : M) + fmaxf(top, red[(half ^ 1) * R + row]) - kBelow;
+        group_sync(quad, 64);  // (red is written again)
+        const bool rises = high > M;
+        const float f = rises && M != kFloor ? ex2_approx(M - high) : 1.f;
+        if (rises) M = high;
         l2 = mul_f32x2(l2, pack_f32x2(f, f));
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) + shift);
         if (t > sg.t0) {
           ok = c.o_holds(it - 1);
           if (ok) {
@@ -699,8 +718,11 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
             tmem_st_wait();
           }
         }
-        group_sync(quad, 64);  // (red is written again)
       }
+      if (left) break;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c.bar.s_empty + 8 * s);
       if (ok) ok = c.wait(c.bar.p_empty + 8 * s, ((it >> 1) & 1) ^ 1);
       if (!ok) continue;  // (leaves at the next vote)
       tc_fence_after();
@@ -727,6 +749,7 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
         mbar_arrive(c.bar.p_full + 8 * s);
       }
     }
+    if (left) ok = false;
     if (ok) ok = c.o_holds(it - 1);
     if (group_any(quad, 64, !ok)) break;
     // ------------------------------ the segment's result ------------------------------
@@ -759,19 +782,19 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
             if ((v[ch + j] & 0x7Fu) == 0x7Fu) o[j] = 0x7FC00000u;
         }
       }
-      if (!valid) continue;
       float f[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(o[j]) * inv;
-      if (whole) {
+      if (whole && valid) {
         uint4* dst = reinterpret_cast<uint4*>(p.out + to * HD + ch);
         dst[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
         dst[1] = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]), pack_bf16x2(f[12], f[13]), pack_bf16x2(f[14], f[15]));
-      } else {
+      } else if (valid) {
         float4* dst = reinterpret_cast<float4*>(p.part_o + to * HD + ch);
 #pragma unroll
         for (int j = 0; j < 4; ++j) dst[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
       }
+      __syncwarp();
     }
     tc_fence_before();
     __syncwarp();
@@ -856,9 +879,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   }
   pdl_wait();
   if (warp == 0) {
-    const long long N = total_tiles(p, lane);
-    const long long Gr = min(static_cast<long long>(p.Gr), N);  // (no CTA between two parts of a unit is without tiles)
-    const Walk w = cta < Gr ? walk_from(p, cta * N / Gr, (cta + 1) * N / Gr, lane) : Walk{0, 0, 0, 0, 0};
+    const Walk w = walk_of(p, cta, lane);
     if (lane == 0) *s_walk = w;
     if (blockIdx.x == 0)
       for (int b = lane; b < p.B; b += 32)
@@ -874,25 +895,42 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   bool ok = true;
 
   if (warp == 0 || warp == 3) {
-    // ------------------------------ codes by TMA: warp 0 K, warp 3 V ------------------------------
+    // ------------------------------ codes by TMA: warp 0 K, warp 3 V; warp 0 also copies the scales, as they are ------------------------------
     const bool is_k = warp == 0;
     const int stages = is_k ? SK : SV;
     const uint32_t full = is_k ? full_k : full_v, empty = is_k ? empty_k : empty_v;
     const uint32_t ring = sbase + (is_k ? C::OFF_K : C::OFF_V), box = p.bs * HD;
     const CUtensorMap* map = is_k ? &tmk : &tmv;
-    int it = 0, stage = 0, phase = 1;
+    int it = 0, stage = 0, phase = 1, slot = 0, slot_phase = 1;
     Pages pg;
     while (ok && walk.next(p, sg)) {
       pg.begin(p, sg, ppt, lane);
+#pragma unroll 1
       for (int i = 0; i < (sg.t1 - sg.t0) * ppt; i += ppt, ++it) {
         pg.seek(p, sg, i, lane);
-        if (is_k && pg.now == -1) report(p.status, TS_ERR_DEVICE_CHECK);
+        if (is_k) {
+          if (pg.now == -1) report(p.status, TS_ERR_DEVICE_CHECK);
+          ok = wait_warp(raw_empty + 8 * slot, slot_phase, abort_flag, p.status);
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = 32 * j + lane;
+            const int id = __shfl_sync(0xffffffffu, pg.now, i - pg.base + (key >> p.bs_log2));
+            const long long o = (static_cast<long long>(id) * p.Hkv + sg.h) * p.nsb + ((key & (p.bs - 1)) >> p.sb_log2);
+            const float* none = reinterpret_cast<const float*>(g_no_page);
+            const uint32_t to = sbase + C::OFF_RAW + (slot * BK + key) * 8;
+            copy4(to, id >= 0 ? p.ks + o : none);
+            copy4(to + 4, id >= 0 ? p.vs + o : none);
+          }
+          arrive_copied(raw_full + 8 * slot);
+          if (++slot == kScaleSlots) slot = 0, slot_phase ^= 1;
+        }
         ok = wait_warp(empty + 8 * stage, phase, abort_flag, p.status);
         if (!ok) break;
         if (lane == 0) mbar_expect_tx(full + 8 * stage, TILE8);
         __syncwarp();
         const uint32_t to = ring + stage * TILE8;
-#pragma unroll 2
+#pragma unroll 1
         for (int j = 0; j < ppt; ++j) {
           const int id = __shfl_sync(0xffffffffu, pg.now, i - pg.base + j);
           tma_elected(to + j * box, map, full + 8 * stage, sg.h, id < 0 ? p.num_blocks : id);  // (out of range: zeros)
@@ -903,6 +941,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
     // after an abort nobody waits for what is still on its way: the newest copy of every stage
     if (!ok)
       for (int i = max(0, it - stages); i < it; ++i) drain(full + 8 * (i % stages), (i / stages) & 1);
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1) {
     // ------------------------------ scores: K Q^T, wide Q K^T (the warp issues as one) ------------------------------
     constexpr int N = C::WIDE ? BK : R;
@@ -940,7 +979,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       commit_elected(last);
       drain(last, 0);
     }
-  } else if (warp == 8) {
+  } else if (warp == 2) {
     // ------------------------------ outputs: V^T P^T, wide P V ------------------------------
     constexpr uint32_t ip = C::WIDE ? idesc_of(HD, 0, 0, 0, 1) : idesc_of(R, 0, 0, 1, 1);
     const uint64_t vdesc = sdesc(sbase + C::OFF_V16, BK * 128, 1024, 128);
@@ -971,31 +1010,6 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       commit_elected(last + 8);
       drain(last + 8, 0);
     }
-  } else if (warp == 2) {
-    // ------------------------------ scales: copied as they are, eight tiles ahead ------------------------------
-    int slot = 0, phase = 1;
-    Pages pg;
-    while (ok && walk.next(p, sg)) {
-      pg.begin(p, sg, ppt, lane);
-      for (int i = 0; i < (sg.t1 - sg.t0) * ppt; i += ppt) {
-        pg.seek(p, sg, i, lane);
-        ok = wait_warp(raw_empty + 8 * slot, phase, abort_flag, p.status);
-        if (!ok) break;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int key = 32 * j + lane;
-          const int id = __shfl_sync(0xffffffffu, pg.now, i - pg.base + (key >> p.bs_log2));
-          const long long o = (static_cast<long long>(id) * p.Hkv + sg.h) * p.nsb + ((key & (p.bs - 1)) >> p.sb_log2);
-          const float* none = reinterpret_cast<const float*>(g_no_page);
-          const uint32_t to = sbase + C::OFF_RAW + (slot * BK + key) * 8;
-          copy4(to, id >= 0 ? p.ks + o : none);
-          copy4(to + 4, id >= 0 ? p.vs + o : none);
-        }
-        arrive_copied(raw_full + 8 * slot);
-        if (++slot == kScaleSlots) slot = 0, phase ^= 1;
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------ Q and V into the tensor cores' types ------------------------------
     const int w = warp - 4;
@@ -1135,21 +1149,17 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
   const int row = static_cast<int>(item % p.rows), bh = static_cast<int>(item / p.rows), b = bh / p.Hkv, h = bh % p.Hkv;
   const int T = tiles_of(p, b);
   if (T == 0) return;
-  long long before = 0, N = 0;  // tiles of the sequences before b, of all
+  int before = 0, N = 0;  // tiles of the sequences before b, of all
   for (int i = lane; i < p.B; i += 32) {
     const int x = tiles_of(p, i);
     N += x;
     if (i < b) before += x;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    N += __shfl_xor_sync(0xffffffffu, N, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  N *= p.Hkv;
-  const long long first = before * p.Hkv + static_cast<long long>(h) * T;
-  const long long Gr = min(static_cast<long long>(p.Gr), N);
-  const int c0 = cta_of(first, N, Gr), c1 = cta_of(first + T - 1, N, Gr);
+  N = static_cast<int>(__reduce_add_sync(0xffffffffu, N)) * p.Hkv;
+  before = static_cast<int>(__reduce_add_sync(0xffffffffu, before));
+  const Share share(N, p.Gr);
+  const int first = before * p.Hkv + h * T;
+  const int c0 = share.cta_of(first), c1 = share.cta_of(first + T - 1);
   if (c0 == c1) return;  // (one CTA had the whole unit)
   const int rg = row / R, r = row - rg * R;
   auto slot = [&](int c) { return (((static_cast<long long>(rg) * p.Gr + c) * 2 + (c == c0 ? 1 : 0)) * R + r); };
@@ -1254,6 +1264,8 @@ size_t attention_fp8_tc_workspace_bytes(int B, int m, int Hq, int Hkv, int max_p
 
 int attention_fp8_tc_launch(const Fp8AttnCall& a, cudaStream_t stream, int num_sms) {
   using namespace fp8tc;
+  // (tiles are counted in 32 bits)
+  if ((static_cast<long long>(a.max_prefix) + a.m + BK - 1) / BK * a.B * a.Hkv > INT32_MAX) return TS_ERR_UNSUPPORTED;
   const Plan pl = plan_of(a.B, a.m, a.Hq, a.Hkv, a.max_prefix, num_sms);
   Params p;
   p.q = static_cast<const __nv_bfloat16*>(a.q);
