@@ -47,7 +47,7 @@ constexpr int HD = 128;
 constexpr int BK = 128;                      // keys per tile
 constexpr uint32_t TILE8 = BK * HD;          // codes of one tile of K or V
 constexpr uint32_t TILE16 = 2 * TILE8;       // V in fp16
-constexpr int kScaleSlots = 6;
+constexpr int kScaleSlots = 8;
 constexpr uint32_t kNoPage = 0x7FDEAD01u;    // in the place of a scale: its key's page has no id
 constexpr float kFloor = -1e30f;             // reference of a row that has met no key
 constexpr float kBelow = 7.f, kRise = 15.f;  // the reference lies kBelow under the largest y; raised when exceeded by kRise
@@ -59,12 +59,12 @@ constexpr float kLog2e = 1.4426950408889634074f;
 template <int R>
 struct Cfg {
   static constexpr bool WIDE = R == 128;
-  static constexpr int CPT = WIDE ? 64 : 16;                     // scores per softmax thread and tile
+  static constexpr int CPT = WIDE ? 64 : 8;                      // scores per softmax thread and tile
   static constexpr int GROUPS = WIDE ? 4 : R / CPT;              // what shares references: a quadrant's two warps, or four warps
   static constexpr int SOFT = WIDE ? 8 : 4 * GROUPS;
   static constexpr int FIRST_SOFT = 8;
   static constexpr int THREADS = 32 * (FIRST_SOFT + SOFT);
-  static constexpr int SK = WIDE ? 4 : 5;
+  static constexpr int SK = R == 16 ? 5 : 4;
   static constexpr int SV = 3;
   static constexpr int NP = 2;                                   // P buffers (wide: in tensor memory)
   static constexpr int NV = 2;                                   // fp16 V buffers
@@ -77,14 +77,15 @@ struct Cfg {
   static constexpr uint32_t OFF_V16 = OFF_V + SV * TILE8;
   static constexpr uint32_t OFF_P = OFF_V16 + NV * TILE16;
   static constexpr uint32_t OFF_RAW = OFF_P + NP * PBUF;         // {ks, vs} per key, kScaleSlots tiles
-  static constexpr uint32_t OFF_SC = OFF_RAW + kScaleSlots * BK * 8;  // wide: {ks * scale * log2 e}, {log2 vs}, {1 / vs} of two tiles
-  static constexpr uint32_t OFF_RM = OFF_SC + (WIDE ? 2 * 3 * BK * 4 : 0);  // per pair of rows {r0, r1, -M0, -M1}
+  // {ks * scale * log2 e, log2 vs, 1 / vs} of two tiles: wide as three arrays, else four floats a key
+  static constexpr uint32_t OFF_SC = OFF_RAW + kScaleSlots * BK * 8;
+  static constexpr uint32_t OFF_RM = OFF_SC + 2 * BK * 16;       // per pair of rows {r0, r1, M0, M1}
   static constexpr uint32_t OFF_R2 = OFF_RM + (WIDE ? 0 : R * 8);  // row scales of the next segment
   static constexpr uint32_t OFF_RED = OFF_R2 + R * 4;            // exchanged maxima and sums
   static constexpr uint32_t OFF_FAC = OFF_RED + 4 * R * 4;
   static constexpr uint32_t OFF_VIS = OFF_FAC + R * 4;           // columns: mask words of the rows
   static constexpr uint32_t OFF_BAR = OFF_VIS + (WIDE ? 0 : R * 32);
-  static constexpr int NBAR = 2 * SK + 2 * SV + 2 * NV + 4 + 2 * NP + 2 * kScaleSlots + 4 + 5;
+  static constexpr int NBAR = 2 * SK + 2 * SV + 2 * NV + 2 + 2 * NP + 2 * kScaleSlots + 2 + 5;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t SMEM = OFF_MISC + 64 + 1024;
   static constexpr uint32_t TMEM_COLS = R == 16 ? 64 : R == 32 ? 128 : 512;
@@ -273,7 +274,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
   return w;
 }
-// 16 consecutive columns of this thread's lane, and wait for them.
+// 16 (or 8) consecutive columns of this thread's lane, and wait for them.
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -291,6 +292,12 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+               : TS_R8(0)
+               : "r"(taddr)
+               : "memory");
+}
 // One column.
 __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
   uint32_t r;
@@ -373,7 +380,7 @@ __device__ __forceinline__ float column_sums(float (&v)[N], int lane) {
 
 // What the softmax warps need of their CTA.
 struct Bars {
-  uint32_t s_full, s_empty, p_full, p_empty, sc_full, sc_empty, q_full, q_empty, o_free;
+  uint32_t s_full, p_full, p_empty, sc_full, q_full, q_empty, o_free;
 };
 template <int R>
 struct Cta {
@@ -385,6 +392,12 @@ struct Cta {
   volatile int* nan_seg;
   int rg, cta, R0, rows_here;
   __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity) const { return wait_warp(b, parity, abort_flag, p.status); }
+  // The scores and the scales of buffer s are there.
+  __device__ __forceinline__ bool scores_in(int s, uint32_t parity) const {
+    const uint32_t a = bar.sc_full + 8 * s, b = bar.s_full + 8 * s;
+    if (__all_sync(0xffffffffu, mbar_try(a, parity) && mbar_try(b, parity))) return true;
+    return wait(a, parity) && wait(b, parity);
+  }
   // P V of tile i is done: its P buffer is free again.  (A barrier of one phase per tile would not do: the softmax may be two tiles
   // ahead of P V, and a wait by parity would take the older phase for the newer.)
   __device__ __forceinline__ bool o_holds(int i) const { return wait(bar.p_empty + 8 * (i & 1), (i >> 1) & 1); }
@@ -427,7 +440,7 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
   unsigned char* prow = c.sptr + C::OFF_P + key * C::PROW;
   Segment sg;
   bool ok = true;
-  int it = 0, seg = 0, slot = 0, slot_phase = 0;
+  int it = 0, seg = 0;
   while (walk.next(p, sg)) {
     if (ok) ok = c.wait(c.bar.q_full, seg & 1);
     if (group_any(group, 128, !ok)) break;
@@ -463,16 +476,16 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
       const int s = it & 1;
       const bool tail = (t + 1) * BK > sg.L;
       const uint32_t tS = c.tmem + lanes + C::COL_S + R * s + col0;
-      if (ok) ok = c.wait(c.bar.sc_full + 8 * slot, slot_phase) && c.wait(c.bar.s_full + 8 * s, (it >> 1) & 1);
-      KeyScale k = {0.f, 0.f, 0.f};
+      if (ok) ok = c.scores_in(s, (it >> 1) & 1);
+      float4 k = make_float4(0.f, 0.f, 0.f, 0.f);  // a, lv, 1 / vs
       uint32_t x[N];
       uint32_t seen = ~0u;  // rows that attend to this thread's key
       if (ok) {
         tc_fence_after();
-        k = key_scale(reinterpret_cast<const float2*>(c.sptr + C::OFF_RAW)[slot * BK + key], p.scale_log2);
+        k = reinterpret_cast<const float4*>(c.sptr + C::OFF_SC)[s * BK + key];
         if (tail) {
           const int n = t * BK + key - sg.L;
-          if (k.iv == 0.f || n >= p.m) {
+          if (k.z == 0.f || n >= p.m) {
             seen = 0u;
           } else if (n >= 0) {
             seen = 0u;
@@ -481,10 +494,10 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
           }
         }
       }
-      const uint64_t a2 = pack_f32x2(k.a, k.a), v2 = pack_f32x2(k.lv, k.lv);
+      const uint64_t a2 = pack_f32x2(k.x, k.x), v2 = pack_f32x2(k.y, k.y);
 #pragma unroll 1
       for (bool again = false;; again = true) {
-        float top = -INFINITY;
+        float top = -INFINITY, top2 = -INFINITY;
         if (ok) {
           tmem_ld(tS, x);
 #pragma unroll
@@ -502,7 +515,11 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
               if (!((seen >> i) & 1u)) x[i] = 0xFF800000u;
           }
 #pragma unroll
-          for (int i = 0; i < N; i += 2) top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          for (int i = 0; i < N; i += 4) {
+            top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            top2 = max3(top2, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+          }
+          top = fmaxf(top, top2);
         }
         if (again || !group_any(group, 128, !ok || unmet || top > kRise)) break;
         // Rare (every unit's first tile does this): the references rise to the tile's largest, and the scores are taken again.
@@ -513,7 +530,7 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
         int high = 0x80000000;
 #pragma unroll 1
         for (int i = 0; i < N; ++i) {
-          float y = fmaf(tmem_ld1(tS + i), k.a * rm[(i >> 1) * 4 + (i & 1)], k.lv);
+          float y = fmaf(tmem_ld1(tS + i), k.x * rm[(i >> 1) * 4 + (i & 1)], k.y);
           if (y != y || !((seen >> i) & 1u)) y = -INFINITY;  // (a NaN goes into the weights, not into the reference)
           const int most = __reduce_max_sync(0xffffffffu, ordered(y));
           if (lane == i) high = most;
@@ -542,16 +559,8 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
         }
       }
       if (left) break;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(c.bar.s_empty + 8 * s);
-        mbar_arrive(c.bar.sc_empty + 8 * slot);
-      }
-      if (++slot == kScaleSlots) slot = 0, slot_phase ^= 1;
-      if (ok) ok = c.wait(c.bar.p_empty + 8 * s, ((it >> 1) & 1) ^ 1);
       if (!ok) continue;  // (leaves at the next vote)
-      const uint64_t iv2 = pack_f32x2(k.iv, k.iv);
+      const uint64_t iv2 = pack_f32x2(k.z, k.z);
       uint32_t h[N / 2];
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
@@ -655,14 +664,14 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
     bool left = false;
     for (int t = sg.t0; t < sg.t1; ++t, ++it) {
       const int s = it & 1;
-      if (ok) ok = c.wait(c.bar.sc_full + 8 * s, (it >> 1) & 1) && c.wait(c.bar.s_full + 8 * s, (it >> 1) & 1);
-      const float* sc = reinterpret_cast<const float*>(c.sptr + C::OFF_SC) + s * 3 * BK + 64 * half;  // a, lv, iv of this half's keys
+      if (ok) ok = c.scores_in(s, (it >> 1) & 1);
+      const float* sc = reinterpret_cast<const float*>(c.sptr + C::OFF_SC) + s * 4 * BK + 64 * half;  // a, lv, iv of this half's keys
       uint32_t x[N];
       const bool tail = (t + 1) * BK > sg.L;
       if (ok) tc_fence_after();
 #pragma unroll 1
       for (bool again = false;; again = true) {
-        float top = -INFINITY;
+        float top = -INFINITY, top2 = -INFINITY;
         if (ok) {
           tmem_ld64(c.tmem + lanes + C::COL_S + BK * s + 64 * half, x);
           const float ref = M == kFloor ? 0.f : -M;
@@ -687,7 +696,11 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
               if (!((vis >> i) & 1ull) || sc[2 * BK + i] == 0.f) x[i] = 0xFF800000u;
           }
 #pragma unroll
-          for (int i = 0; i < N; i += 2) top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          for (int i = 0; i < N; i += 4) {
+            top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            top2 = max3(top2, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+          }
+          top = fmaxf(top, top2);
         }
         if (again || !group_any(quad, 64, !ok || top > kRise || (M == kFloor && top > -INFINITY))) break;
         // Rare (every unit's first tile does this): the reference rises to the tile's largest, and the scores are taken again.
@@ -720,12 +733,7 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
         }
       }
       if (left) break;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(c.bar.s_empty + 8 * s);
-      if (ok) ok = c.wait(c.bar.p_empty + 8 * s, ((it >> 1) & 1) ^ 1);
       if (!ok) continue;  // (leaves at the next vote)
-      tc_fence_after();
 #pragma unroll
       for (int i = 0; i < N; i += 32) {
         uint32_t h[16];
@@ -744,10 +752,7 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(c.bar.sc_empty + 8 * s);
-        mbar_arrive(c.bar.p_full + 8 * s);
-      }
+      if (lane == 0) mbar_arrive(c.bar.p_full + 8 * s);
     }
     if (left) ok = false;
     if (ok) ok = c.o_holds(it - 1);
@@ -847,8 +852,8 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
     return first;
   };
   const uint32_t full_k = take(SK), empty_k = take(SK), full_v = take(SV), empty_v = take(SV), v16_full = take(NV),
-                 v16_empty = take(NV), s_full = take(2), s_empty = take(2), p_full = take(NP), p_empty = take(NP),
-                 raw_full = take(kScaleSlots), raw_empty = take(kScaleSlots), sc_full = take(2), sc_empty = take(2),
+                 v16_empty = take(NV), s_full = take(2), p_full = take(NP), p_empty = take(NP),
+                 raw_full = take(kScaleSlots), raw_empty = take(kScaleSlots), sc_full = take(2),
                  q_full = take(1), q_empty = take(1), o_free = take(1), last = take(2);
   unsigned char* misc = sptr + C::OFF_MISC;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc);
@@ -860,10 +865,9 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
     for (int i = 0; i < SK; ++i) mbar_init(full_k + 8 * i, 1), mbar_init(empty_k + 8 * i, 1);
     for (int i = 0; i < SV; ++i) mbar_init(full_v + 8 * i, 1), mbar_init(empty_v + 8 * i, 4);
     for (int i = 0; i < NV; ++i) mbar_init(v16_full + 8 * i, 4), mbar_init(v16_empty + 8 * i, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(s_empty + 8 * i, soft);
+    for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(sc_full + 8 * i, 4);
     for (int i = 0; i < NP; ++i) mbar_init(p_full + 8 * i, soft), mbar_init(p_empty + 8 * i, 1);
-    for (int i = 0; i < kScaleSlots; ++i) mbar_init(raw_full + 8 * i, 32), mbar_init(raw_empty + 8 * i, C::WIDE ? 4 : soft);
-    for (int i = 0; i < 2; ++i) mbar_init(sc_full + 8 * i, 4), mbar_init(sc_empty + 8 * i, soft);
+    for (int i = 0; i < kScaleSlots; ++i) mbar_init(raw_full + 8 * i, 32), mbar_init(raw_empty + 8 * i, 4);
     mbar_init(q_full, 4);
     mbar_init(q_empty, 1 + soft);
     mbar_init(o_free, soft);
@@ -953,8 +957,10 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       if (!ok) break;
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
         const int s = it & 1;
+        // (P V of the tile before last is done: then its weights have been made, so its scores have been read, and the softmax need
+        // not wait for its P buffer)
         ok = wait_warp(full_k + 8 * sk, phase, abort_flag, p.status) &&
-             wait_warp(s_empty + 8 * s, ((it >> 1) & 1) ^ 1, abort_flag, p.status);
+             wait_warp(p_empty + 8 * s, ((it >> 1) & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + C::COL_S + N * s;
@@ -1061,25 +1067,28 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       if (lane == 0) mbar_arrive(q_full);
       for (int t = sg.t0; t < sg.t1; ++t, ++it) {
         const int v = it & 1;
-        if constexpr (C::WIDE) {
-          // the tile's scales as the softmax wants them: a key per thread
+        {
+          // the tile's scales as the softmax wants them: a key per thread (P V of the tile before last is done, so they have been read)
           const int slot = it % kScaleSlots, key = 32 * w + lane;
           ok = wait_warp(raw_full + 8 * slot, (it / kScaleSlots) & 1, abort_flag, p.status) &&
-               wait_warp(sc_empty + 8 * v, ((it >> 1) & 1) ^ 1, abort_flag, p.status);
+               wait_warp(v16_empty + 8 * v, ((it >> 1) & 1) ^ 1, abort_flag, p.status);
           if (!ok) break;
           const KeyScale k = key_scale(reinterpret_cast<const float2*>(sptr + C::OFF_RAW)[slot * BK + key], p.scale_log2);
-          float* to = reinterpret_cast<float*>(sptr + C::OFF_SC) + v * 3 * BK;
-          to[key] = k.a;
-          to[BK + key] = k.lv;
-          to[2 * BK + key] = k.iv;
+          float* to = reinterpret_cast<float*>(sptr + C::OFF_SC) + v * 4 * BK;
+          if constexpr (C::WIDE) {
+            to[key] = k.a;
+            to[BK + key] = k.lv;
+            to[2 * BK + key] = k.iv;
+          } else {
+            reinterpret_cast<float4*>(to)[key] = make_float4(k.a, k.lv, k.iv, 0.f);
+          }
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(raw_empty + 8 * slot);
             mbar_arrive(sc_full + 8 * v);
           }
         }
-        ok = wait_warp(full_v + 8 * sv, phase, abort_flag, p.status) &&
-             wait_warp(v16_empty + 8 * v, ((it >> 1) & 1) ^ 1, abort_flag, p.status);
+        ok = wait_warp(full_v + 8 * sv, phase, abort_flag, p.status);
         if (!ok) break;
         const unsigned char* from = sptr + C::OFF_V + sv * TILE8;
         unsigned char* to = sptr + C::OFF_V16 + v * TILE16;
@@ -1130,7 +1139,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       ++seg;
     }
   } else if (warp >= C::FIRST_SOFT) {
-    const Bars bars{s_full, s_empty, p_full, p_empty, C::WIDE ? sc_full : raw_full, C::WIDE ? sc_empty : raw_empty, q_full, q_empty, o_free};
+    const Bars bars{s_full, p_full, p_empty, sc_full, q_full, q_empty, o_free};
     const Cta<R> c{p, bars, sptr, tmem, abort_flag, nan_seg, rg, cta, R0, rows_here};
     if constexpr (C::WIDE) softmax_wide(c, walk, warp, lane);
     else softmax_narrow(c, walk, warp, lane);
