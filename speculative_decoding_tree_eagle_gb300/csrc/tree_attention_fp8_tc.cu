@@ -28,9 +28,8 @@
 // to the workspace and join_kernel merges them.  With several row groups CTAs of neighbouring index walk the same tiles
 // for different rows, so all but one read them from L2.
 //
-// Warps: 0 TMA copies of K and copies of the scales, 1 K Q^T and owner of the tensor memory, 2 V^T P^T, 3 TMA copies of V, 4..7 Q and V
-// converters, from 8 on the softmax.  The roles share one instruction cache: code that every tile runs is kept short, and
-// code that runs once per unit is rolled up (unrolled, half of the fetches missed and every warp waited for them).
+// The roles of the warps (struct Cfg) share one instruction cache: code that every tile runs is kept short, and code that runs once per
+// unit is rolled up (unrolled, half of the fetches missed and every warp waited for them).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -47,7 +46,7 @@ constexpr int HD = 128;
 constexpr int BK = 128;                      // keys per tile
 constexpr uint32_t TILE8 = BK * HD;          // codes of one tile of K or V
 constexpr uint32_t TILE16 = 2 * TILE8;       // V in fp16
-constexpr int kScaleSlots = 8;
+constexpr int kScaleSlots = 4;
 constexpr uint32_t kNoPage = 0x7FDEAD01u;    // in the place of a scale: its key's page has no id
 constexpr float kFloor = -1e30f;             // reference of a row that has met no key
 constexpr float kBelow = 7.f, kRise = 15.f;  // the reference lies kBelow under the largest y; raised when exceeded by kRise
@@ -62,10 +61,14 @@ struct Cfg {
   static constexpr int CPT = WIDE ? 64 : 8;                      // scores per softmax thread and tile
   static constexpr int GROUPS = WIDE ? 4 : R / CPT;              // what shares references: a quadrant's two warps, or four warps
   static constexpr int SOFT = WIDE ? 8 : 4 * GROUPS;
-  static constexpr int FIRST_SOFT = 8;
+  // Warps: K and scale copies, V copies, K Q^T (and owner of the tensor memory), V^T P^T, converters, softmax.  Up to 32 rows, where a
+  // tile should take no longer than its bytes (1400 cycles), two copying warps and two groups of converters take alternate tiles.
+  static constexpr int PAIR = WIDE ? 1 : 2;
+  static constexpr int W_V = PAIR, W_QK = 2 * PAIR, W_PV = W_QK + 1, W_CONV = W_PV + 1, CONV = 4 * PAIR;
+  static constexpr int FIRST_SOFT = W_CONV + CONV;
   static constexpr int THREADS = 32 * (FIRST_SOFT + SOFT);
-  static constexpr int SK = R == 16 ? 5 : 4;
-  static constexpr int SV = 3;
+  static constexpr int SK = 4;
+  static constexpr int SV = WIDE ? 3 : 4;
   static constexpr int NP = 2;                                   // P buffers (wide: in tensor memory)
   static constexpr int NV = 2;                                   // fp16 V buffers
   static constexpr uint32_t PROW = 2 * R;                        // bytes of a P^T row, the width of its swizzle
@@ -77,9 +80,9 @@ struct Cfg {
   static constexpr uint32_t OFF_V16 = OFF_V + SV * TILE8;
   static constexpr uint32_t OFF_P = OFF_V16 + NV * TILE16;
   static constexpr uint32_t OFF_RAW = OFF_P + NP * PBUF;         // {ks, vs} per key, kScaleSlots tiles
-  // {ks * scale * log2 e, log2 vs, 1 / vs} of two tiles: wide as three arrays, else four floats a key
+  // {ks * scale * log2 e}, {log2 vs}, {1 / vs} of two tiles
   static constexpr uint32_t OFF_SC = OFF_RAW + kScaleSlots * BK * 8;
-  static constexpr uint32_t OFF_RM = OFF_SC + 2 * BK * 16;       // per pair of rows {r0, r1, M0, M1}
+  static constexpr uint32_t OFF_RM = OFF_SC + 2 * 3 * BK * 4;      // per pair of rows {r0, r1, M0, M1}
   static constexpr uint32_t OFF_R2 = OFF_RM + (WIDE ? 0 : R * 8);  // row scales of the next segment
   static constexpr uint32_t OFF_RED = OFF_R2 + R * 4;            // exchanged maxima and sums
   static constexpr uint32_t OFF_FAC = OFF_RED + 4 * R * 4;
@@ -92,6 +95,9 @@ struct Cfg {
   static constexpr uint32_t COL_S = R;                           // O, then S_0, S_1, wide: P_0, P_1
   static constexpr uint32_t COL_P = 3 * R;
   static_assert(SMEM <= 232448, "shared memory budget");
+  // Two copying warps and two groups of converters do not keep each other's order, so each has stages of its own: were they shared, a warp
+  // could take the phase before the last for the last and fill a stage that is still to be read.
+  static_assert(SK % PAIR == 0 && SV % PAIR == 0 && NV % PAIR == 0 && kScaleSlots % PAIR == 0, "stages of one parity of tiles");
 };
 
 struct Params {
@@ -477,15 +483,16 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
       const bool tail = (t + 1) * BK > sg.L;
       const uint32_t tS = c.tmem + lanes + C::COL_S + R * s + col0;
       if (ok) ok = c.scores_in(s, (it >> 1) & 1);
-      float4 k = make_float4(0.f, 0.f, 0.f, 0.f);  // a, lv, 1 / vs
+      KeyScale k = {0.f, 0.f, 0.f};
       uint32_t x[N];
       uint32_t seen = ~0u;  // rows that attend to this thread's key
       if (ok) {
         tc_fence_after();
-        k = reinterpret_cast<const float4*>(c.sptr + C::OFF_SC)[s * BK + key];
+        const float* sc = reinterpret_cast<const float*>(c.sptr + C::OFF_SC) + s * 3 * BK + key;
+        k = KeyScale{sc[0], sc[BK], sc[2 * BK]};
         if (tail) {
           const int n = t * BK + key - sg.L;
-          if (k.z == 0.f || n >= p.m) {
+          if (k.iv == 0.f || n >= p.m) {
             seen = 0u;
           } else if (n >= 0) {
             seen = 0u;
@@ -494,7 +501,7 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
           }
         }
       }
-      const uint64_t a2 = pack_f32x2(k.x, k.x), v2 = pack_f32x2(k.y, k.y);
+      const uint64_t a2 = pack_f32x2(k.a, k.a), v2 = pack_f32x2(k.lv, k.lv);
 #pragma unroll 1
       for (bool again = false;; again = true) {
         float top = -INFINITY, top2 = -INFINITY;
@@ -530,7 +537,7 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
         int high = 0x80000000;
 #pragma unroll 1
         for (int i = 0; i < N; ++i) {
-          float y = fmaf(tmem_ld1(tS + i), k.x * rm[(i >> 1) * 4 + (i & 1)], k.y);
+          float y = fmaf(tmem_ld1(tS + i), k.a * rm[(i >> 1) * 4 + (i & 1)], k.lv);
           if (y != y || !((seen >> i) & 1u)) y = -INFINITY;  // (a NaN goes into the weights, not into the reference)
           const int most = __reduce_max_sync(0xffffffffu, ordered(y));
           if (lane == i) high = most;
@@ -560,7 +567,7 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
       }
       if (left) break;
       if (!ok) continue;  // (leaves at the next vote)
-      const uint64_t iv2 = pack_f32x2(k.z, k.z);
+      const uint64_t iv2 = pack_f32x2(k.iv, k.iv);
       uint32_t h[N / 2];
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
@@ -665,7 +672,7 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
     for (int t = sg.t0; t < sg.t1; ++t, ++it) {
       const int s = it & 1;
       if (ok) ok = c.scores_in(s, (it >> 1) & 1);
-      const float* sc = reinterpret_cast<const float*>(c.sptr + C::OFF_SC) + s * 4 * BK + 64 * half;  // a, lv, iv of this half's keys
+      const float* sc = reinterpret_cast<const float*>(c.sptr + C::OFF_SC) + s * 3 * BK + 64 * half;  // a, lv, iv of this half's keys
       uint32_t x[N];
       const bool tail = (t + 1) * BK > sg.L;
       if (ok) tc_fence_after();
@@ -868,7 +875,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
     for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(sc_full + 8 * i, 4);
     for (int i = 0; i < NP; ++i) mbar_init(p_full + 8 * i, soft), mbar_init(p_empty + 8 * i, 1);
     for (int i = 0; i < kScaleSlots; ++i) mbar_init(raw_full + 8 * i, 32), mbar_init(raw_empty + 8 * i, 4);
-    mbar_init(q_full, 4);
+    mbar_init(q_full, C::CONV);
     mbar_init(q_empty, 1 + soft);
     mbar_init(o_free, soft);
     mbar_init(last, 1);
@@ -877,7 +884,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
     nan_seg[0] = nan_seg[1] = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == C::W_QK) {
     tmem_alloc(smem_u32(s_tmem), C::TMEM_COLS);
     tmem_relinquish();
   }
@@ -898,23 +905,27 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   const int ppt = BK >> p.bs_log2;  // pages per tile
   bool ok = true;
 
-  if (warp == 0 || warp == 3) {
-    // ------------------------------ codes by TMA: warp 0 K, warp 3 V; warp 0 also copies the scales, as they are ------------------------------
-    const bool is_k = warp == 0;
+  if (warp < C::W_QK) {
+    // ------------------------------ codes by TMA (K, V); K's warps also copy the scales, as they are ------------------------------
+    const bool is_k = warp < C::W_V;
+    const int part = warp % C::PAIR;
     const int stages = is_k ? SK : SV;
     const uint32_t full = is_k ? full_k : full_v, empty = is_k ? empty_k : empty_v;
     const uint32_t ring = sbase + (is_k ? C::OFF_K : C::OFF_V), box = p.bs * HD;
     const CUtensorMap* map = is_k ? &tmk : &tmv;
-    int it = 0, stage = 0, phase = 1, slot = 0, slot_phase = 1;
+    int before = 0, issued = 0;  // tiles of earlier segments; tiles whose copies were issued, by this warp's count
     Pages pg;
     while (ok && walk.next(p, sg)) {
       pg.begin(p, sg, ppt, lane);
+      const int n = sg.t1 - sg.t0;
 #pragma unroll 1
-      for (int i = 0; i < (sg.t1 - sg.t0) * ppt; i += ppt, ++it) {
+      for (int t = (before + part) % C::PAIR; t < n; t += C::PAIR) {
+        const int i = t * ppt, it = before + t;
         pg.seek(p, sg, i, lane);
         if (is_k) {
+          const int slot = it % kScaleSlots;
           if (pg.now == -1) report(p.status, TS_ERR_DEVICE_CHECK);
-          ok = wait_warp(raw_empty + 8 * slot, slot_phase, abort_flag, p.status);
+          ok = wait_warp(raw_empty + 8 * slot, ((it / kScaleSlots) & 1) ^ 1, abort_flag, p.status);
           if (!ok) break;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -927,9 +938,9 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
             copy4(to + 4, id >= 0 ? p.vs + o : none);
           }
           arrive_copied(raw_full + 8 * slot);
-          if (++slot == kScaleSlots) slot = 0, slot_phase ^= 1;
         }
-        ok = wait_warp(empty + 8 * stage, phase, abort_flag, p.status);
+        const int round = is_k ? it / SK : it / SV, stage = it - round * stages;
+        ok = wait_warp(empty + 8 * stage, (round & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
         if (lane == 0) mbar_expect_tx(full + 8 * stage, TILE8);
         __syncwarp();
@@ -939,14 +950,16 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
           const int id = __shfl_sync(0xffffffffu, pg.now, i - pg.base + j);
           tma_elected(to + j * box, map, full + 8 * stage, sg.h, id < 0 ? p.num_blocks : id);  // (out of range: zeros)
         }
-        if (++stage == stages) stage = 0, phase ^= 1;
+        issued = it + 1;
       }
+      before += n;
     }
-    // after an abort nobody waits for what is still on its way: the newest copy of every stage
+    // after an abort nobody waits for what is still on its way: this warp's newest copy of every stage
     if (!ok)
-      for (int i = max(0, it - stages); i < it; ++i) drain(full + 8 * (i % stages), (i / stages) & 1);
+      for (int i = max(0, issued - stages * C::PAIR); i < issued; ++i)
+        if (i % C::PAIR == part) drain(full + 8 * (i % stages), (i / stages) & 1);
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 1) {
+  } else if (warp == C::W_QK) {
     // ------------------------------ scores: K Q^T, wide Q K^T (the warp issues as one) ------------------------------
     constexpr int N = C::WIDE ? BK : R;
     constexpr uint32_t iq1 = idesc_of(N, 0, 0, 0, 0), iq2 = C::WIDE ? idesc_of(N, 1, 0, 0, 0) : idesc_of(N, 0, 1, 0, 0);
@@ -985,7 +998,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       commit_elected(last);
       drain(last, 0);
     }
-  } else if (warp == 2) {
+  } else if (warp == C::W_PV) {
     // ------------------------------ outputs: V^T P^T, wide P V ------------------------------
     constexpr uint32_t ip = C::WIDE ? idesc_of(HD, 0, 0, 0, 1) : idesc_of(R, 0, 0, 1, 1);
     const uint64_t vdesc = sdesc(sbase + C::OFF_V16, BK * 128, 1024, 128);
@@ -1016,16 +1029,16 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       commit_elected(last + 8);
       drain(last + 8, 0);
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp < C::FIRST_SOFT) {
     // ------------------------------ Q and V into the tensor cores' types ------------------------------
-    const int w = warp - 4;
-    int it = 0, seg = 0, sv = 0, phase = 0;
+    const int cw = warp - C::W_CONV, w = cw & 3, part = cw >> 2;  // (w: keys 32 w .. of every tile of this group)
+    int before = 0, seg = 0;
     while (ok && walk.next(p, sg)) {
       ok = wait_warp(q_empty, (seg & 1) ^ 1, abort_flag, p.status);
       if (!ok) break;
       // eight lanes per row, 16 values each
 #pragma unroll 1
-      for (int r0 = w * 4; r0 < R; r0 += 16) {
+      for (int r0 = cw * 4; r0 < R; r0 += 4 * C::CONV) {
         const int r = r0 + (lane >> 3), c = lane & 7;
         uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
         if (r < rows_here) {
@@ -1065,8 +1078,10 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
-      for (int t = sg.t0; t < sg.t1; ++t, ++it) {
-        const int v = it & 1;
+      const int n = sg.t1 - sg.t0;
+#pragma unroll 1
+      for (int i = (before + part) % C::PAIR; i < n; i += C::PAIR) {
+        const int t = sg.t0 + i, it = before + i, v = it & 1, sv = it % SV, phase = (it / SV) & 1;
         {
           // the tile's scales as the softmax wants them: a key per thread (P V of the tile before last is done, so they have been read)
           const int slot = it % kScaleSlots, key = 32 * w + lane;
@@ -1074,14 +1089,10 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
                wait_warp(v16_empty + 8 * v, ((it >> 1) & 1) ^ 1, abort_flag, p.status);
           if (!ok) break;
           const KeyScale k = key_scale(reinterpret_cast<const float2*>(sptr + C::OFF_RAW)[slot * BK + key], p.scale_log2);
-          float* to = reinterpret_cast<float*>(sptr + C::OFF_SC) + v * 4 * BK;
-          if constexpr (C::WIDE) {
-            to[key] = k.a;
-            to[BK + key] = k.lv;
-            to[2 * BK + key] = k.iv;
-          } else {
-            reinterpret_cast<float4*>(to)[key] = make_float4(k.a, k.lv, k.iv, 0.f);
-          }
+          float* to = reinterpret_cast<float*>(sptr + C::OFF_SC) + v * 3 * BK;
+          to[key] = k.a;
+          to[BK + key] = k.lv;
+          to[2 * BK + key] = k.iv;
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(raw_empty + 8 * slot);
@@ -1134,18 +1145,18 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
           mbar_arrive(empty_v + 8 * sv);
           mbar_arrive(v16_full + 8 * v);
         }
-        if (++sv == SV) sv = 0, phase ^= 1;
       }
+      before += n;
       ++seg;
     }
-  } else if (warp >= C::FIRST_SOFT) {
+  } else {
     const Bars bars{s_full, p_full, p_empty, sc_full, q_full, q_empty, o_free};
     const Cta<R> c{p, bars, sptr, tmem, abort_flag, nan_seg, rg, cta, R0, rows_here};
     if constexpr (C::WIDE) softmax_wide(c, walk, warp, lane);
     else softmax_narrow(c, walk, warp, lane);
   }
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+  if (warp == C::W_QK) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
 // A warp per output row: joins the parts of a unit that several CTAs walked, in the order of the CTAs.
