@@ -60,7 +60,7 @@ struct Cfg {
   static constexpr bool WIDE = R == 128;
   static constexpr int CPT = WIDE ? 64 : 8;                      // scores per softmax thread and tile
   static constexpr int GROUPS = WIDE ? 4 : R / CPT;              // what shares references: a quadrant's two warps, or four warps
-  static constexpr int SOFT = WIDE ? 8 : 4 * GROUPS;
+  static constexpr int SOFT = WIDE ? 4 * BK / CPT : 4 * GROUPS;
   // Warps: K and scale copies, V copies, K Q^T (and owner of the tensor memory), V^T P^T, converters, softmax.  Up to 32 rows, where a
   // tile should take no longer than its bytes (1400 cycles), two copying warps and two groups of converters take alternate tiles.
   static constexpr int PAIR = WIDE ? 1 : 2;
@@ -644,24 +644,27 @@ __device__ __forceinline__ uint64_t visible64(int kb, int L, int m, const uint64
   return pre > 0 ? ((1ull << pre) - 1ull) | (bits << pre) : bits;
 }
 
-// Rows are rows: a thread has one row (its TMEM lane) and 64 of the tile's keys, the thread of the warp four further on the others;
-// both keep the row's reference.  P goes to tensor memory.
-template <int R>
+// Rows are rows: a thread has one row (its TMEM lane) and N of the tile's keys, the threads of the warps four, eight, .. further on the
+// others; all of them keep the row's reference.  P goes to tensor memory.
+// COARSE (scale blocks of 16 tokens or more): the scales are those of 16 keys, so they are folded into the row's constants once for
+// 16 scores.  Otherwise each key has its own, and reading them (a broadcast of 16 bytes to a warp takes the shared memory four
+// cycles) is what paces the softmax: 177 against MEASURED us for 4 x 64 nodes of 32 heads over 32768 tokens.
+template <int R, bool COARSE>
 __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int warp, int lane) {
   using C = Cfg<R>;
-  constexpr int N = C::CPT;
+  constexpr int N = C::CPT, PARTS = BK / N;
   const Params& p = c.p;
-  const int quad = warp & 3, half = (warp - C::FIRST_SOFT) >> 2, row = 32 * quad + lane;
+  const int quad = warp & 3, part = (warp - C::FIRST_SOFT) >> 2, row = 32 * quad + lane;
   if (32 * quad >= c.rows_here) return;
-  const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16, tO = c.tmem + lanes + 64 * half;
-  float* red = reinterpret_cast<float*>(c.sptr + C::OFF_RED);  // [half][row]
+  const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16, tO = c.tmem + lanes + N * part;
+  float* red = reinterpret_cast<float*>(c.sptr + C::OFF_RED);  // [part][row]
   const bool valid = row < c.rows_here;
   Segment sg;
   bool ok = true;
   int it = 0, seg = 0;
   while (walk.next(p, sg)) {
     if (ok) ok = c.wait(c.bar.q_full, seg & 1);
-    if (group_any(quad, 64, !ok)) break;
+    if (group_any(quad, 32 * PARTS, !ok)) break;
     const float r = reinterpret_cast<const float*>(c.sptr + C::OFF_R2)[row];
     __syncwarp();
     if (lane == 0) mbar_arrive(c.bar.q_empty);  // (the row scale is taken; the MMA warp says when Q is)
@@ -672,7 +675,7 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
     for (int t = sg.t0; t < sg.t1; ++t, ++it) {
       const int s = it & 1;
       if (ok) ok = c.scores_in(s, (it >> 1) & 1);
-      const float* sc = reinterpret_cast<const float*>(c.sptr + C::OFF_SC) + s * 3 * BK + 64 * half;  // a, lv, iv of this half's keys
+      const float* sc = reinterpret_cast<const float*>(c.sptr + C::OFF_SC) + s * 3 * BK + N * part;  // a, lv, iv of this part's keys
       uint32_t x[N];
       const bool tail = (t + 1) * BK > sg.L;
       if (ok) tc_fence_after();
@@ -680,24 +683,39 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
       for (bool again = false;; again = true) {
         float top = -INFINITY, top2 = -INFINITY;
         if (ok) {
-          tmem_ld64(c.tmem + lanes + C::COL_S + BK * s + 64 * half, x);
+          tmem_ld64(c.tmem + lanes + C::COL_S + BK * s + N * part, x);
           const float ref = M == kFloor ? 0.f : -M;
-          const uint64_t r2 = pack_f32x2(r, r), m2 = pack_f32x2(ref, ref);
+          if constexpr (COARSE) {
 #pragma unroll
-          for (int i = 0; i < N; i += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(sc + i), v = *reinterpret_cast<const float4*>(sc + BK + i);
-            const uint64_t z01 = fma_f32x2(pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                                           mul_f32x2(pack_f32x2(a.x, a.y), r2), add_f32x2(pack_f32x2(v.x, v.y), m2));
-            const uint64_t z23 = fma_f32x2(pack_f32x2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
-                                           mul_f32x2(pack_f32x2(a.z, a.w), r2), add_f32x2(pack_f32x2(v.z, v.w), m2));
-            float z[4];
-            unpack_f32x2(z01, z[0], z[1]);
-            unpack_f32x2(z23, z[2], z[3]);
+            for (int g = 0; g < N; g += 16) {
+              const float a = sc[g] * r, b = sc[BK + g] + ref;
+              const uint64_t a2 = pack_f32x2(a, a), b2 = pack_f32x2(b, b);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[i + j] = __float_as_uint(z[j]);
+              for (int i = g; i < g + 16; i += 2) {
+                float z0, z1;
+                unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), a2, b2), z0, z1);
+                x[i] = __float_as_uint(z0);
+                x[i + 1] = __float_as_uint(z1);
+              }
+            }
+          } else {
+            const uint64_t r2 = pack_f32x2(r, r), m2 = pack_f32x2(ref, ref);
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+              const float4 a = *reinterpret_cast<const float4*>(sc + i), v = *reinterpret_cast<const float4*>(sc + BK + i);
+              const uint64_t z01 = fma_f32x2(pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                             mul_f32x2(pack_f32x2(a.x, a.y), r2), add_f32x2(pack_f32x2(v.x, v.y), m2));
+              const uint64_t z23 = fma_f32x2(pack_f32x2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
+                                             mul_f32x2(pack_f32x2(a.z, a.w), r2), add_f32x2(pack_f32x2(v.z, v.w), m2));
+              float z[4];
+              unpack_f32x2(z01, z[0], z[1]);
+              unpack_f32x2(z23, z[2], z[3]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[i + j] = __float_as_uint(z[j]);
+            }
           }
           if (tail) {
-            const uint64_t vis = visible64(t * BK + 64 * half, sg.L, p.m, words, p.W);
+            const uint64_t vis = (visible64(t * BK + N * part, sg.L, p.m, words, p.W));
 #pragma unroll
             for (int i = 0; i < N; ++i)
               if (!((vis >> i) & 1ull) || sc[2 * BK + i] == 0.f) x[i] = 0xFF800000u;
@@ -709,16 +727,19 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
           }
           top = fmaxf(top, top2);
         }
-        if (again || !group_any(quad, 64, !ok || top > kRise || (M == kFloor && top > -INFINITY))) break;
+        if (again || !group_any(quad, 32 * PARTS, !ok || top > kRise || (M == kFloor && top > -INFINITY))) break;
         // Rare (every unit's first tile does this): the reference rises to the tile's largest, and the scores are taken again.
-        if (group_any(quad, 64, !ok)) {
+        if (group_any(quad, 32 * PARTS, !ok)) {
           left = true;
           break;
         }
-        red[half * R + row] = top;
-        group_sync(quad, 64);
-        const float high = (M == kFloor ? 0.f : M) + fmaxf(top, red[(half ^ 1) * R + row]) - kBelow;
-        group_sync(quad, 64);  // (red is written again)
+        red[part * R + row] = top;
+        group_sync(quad, 32 * PARTS);
+        float most = red[row];
+#pragma unroll
+        for (int i = 1; i < PARTS; ++i) most = fmaxf(most, red[i * R + row]);
+        const float high = (M == kFloor ? 0.f : M) + most - kBelow;
+        group_sync(quad, 32 * PARTS);  // (red is written again)
         const bool rises = high > M;
         const float f = rises && M != kFloor ? ex2_approx(M - high) : 1.f;
         if (rises) M = high;
@@ -744,17 +765,27 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
 #pragma unroll
       for (int i = 0; i < N; i += 32) {
         uint32_t h[16];
+        uint64_t sum = 0ull;
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(sc + 2 * BK + i + j);
           const float p0 = ex2_approx(__uint_as_float(x[i + j])), p1 = ex2_approx(__uint_as_float(x[i + j + 1]));
           const float p2 = ex2_approx(__uint_as_float(x[i + j + 2])), p3 = ex2_approx(__uint_as_float(x[i + j + 3]));
-          l2 = fma_f32x2(pack_f32x2(p0, p1), pack_f32x2(v.x, v.y), l2);
-          l2 = fma_f32x2(pack_f32x2(p2, p3), pack_f32x2(v.z, v.w), l2);
+          if constexpr (COARSE) {
+            sum = add_f32x2(sum, add_f32x2(pack_f32x2(p0, p1), pack_f32x2(p2, p3)));
+            if (j % 16 == 12) {
+              const float iv = sc[2 * BK + i + j - 12];
+              l2 = fma_f32x2(sum, pack_f32x2(iv, iv), l2);
+              sum = 0ull;
+            }
+          } else {
+            const float4 v = *reinterpret_cast<const float4*>(sc + 2 * BK + i + j);
+            l2 = fma_f32x2(pack_f32x2(p0, p1), pack_f32x2(v.x, v.y), l2);
+            l2 = fma_f32x2(pack_f32x2(p2, p3), pack_f32x2(v.z, v.w), l2);
+          }
           h[j / 2] = pack_f16x2(p0, p1);
           h[j / 2 + 1] = pack_f16x2(p2, p3);
         }
-        tmem_st(c.tmem + lanes + C::COL_P + 64 * s + 32 * half + i / 2, h);
+        tmem_st(c.tmem + lanes + C::COL_P + 64 * s + N / 2 * part + i / 2, h);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -763,18 +794,20 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
     }
     if (left) ok = false;
     if (ok) ok = c.o_holds(it - 1);
-    if (group_any(quad, 64, !ok)) break;
+    if (group_any(quad, 32 * PARTS, !ok)) break;
     // ------------------------------ the segment's result ------------------------------
     tc_fence_after();
     float l, other;
     unpack_f32x2(l2, l, other);
     l += other;
-    red[half * R + row] = l;
-    group_sync(quad, 64);
-    l = red[row] + red[R + row];  // (both threads in the same order)
+    red[part * R + row] = l;
+    group_sync(quad, 32 * PARTS);
+    l = red[row];  // (all threads in the same order)
+#pragma unroll
+    for (int i = 1; i < PARTS; ++i) l += red[i * R + row];
     const bool whole = sg.t0 == 0 && sg.t1 == sg.T, poison = c.nan_seg[seg & 1] == seg + 1;
     const long long to = whole ? c.row_at(sg, row) : c.slot(sg) * R + row;
-    if (valid && half == 0) {
+    if (valid && part == 0) {
       if (!whole) p.part_ml[to] = make_float2(M, l);
       else if (p.lse != nullptr) p.lse[to] = lse_of(M, l);
     }
@@ -783,7 +816,7 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
     for (int i = 0; i < N; i += 16) {
       uint32_t o[16];
       tmem_ld(tO + i, o);
-      const int ch = 64 * half + i;
+      const int ch = N * part + i;
       if (poison) {
         // a NaN in a tree row's V: the rows that attend to it get it
         for (int n = max(0, sg.t0 * BK - sg.L); n < min(p.m, sg.t1 * BK - sg.L); ++n) {
@@ -811,7 +844,7 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(c.bar.o_free);
-    group_sync(quad, 64);  // (red is written again)
+    group_sync(quad, 32 * PARTS);  // (red is written again)
     ++seg;
   }
 }
@@ -837,7 +870,7 @@ struct Pages {
   }
 };
 
-template <int R>
+template <int R, bool COARSE>
 __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const __grid_constant__ Params p) {
   using C = Cfg<R>;
@@ -850,7 +883,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   const int rg = blockIdx.x % p.RG, cta = blockIdx.x / p.RG;
   const int R0 = rg * R, rows_here = min(R, p.rows - R0);
   // wide: quadrants of 32 rows that hold any; the softmax warps of the others have nothing to do
-  const int soft = C::WIDE ? 2 * ((rows_here + 31) / 32) : C::SOFT;
+  const int soft = C::WIDE ? BK / C::CPT * ((rows_here + 31) / 32) : C::SOFT;
 
   uint32_t at = sbase + C::OFF_BAR;
   auto take = [&](int n) {
@@ -945,11 +978,9 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
         if (lane == 0) mbar_expect_tx(full + 8 * stage, TILE8);
         __syncwarp();
         const uint32_t to = ring + stage * TILE8;
-#pragma unroll 1
-        for (int j = 0; j < ppt; ++j) {
-          const int id = __shfl_sync(0xffffffffu, pg.now, i - pg.base + j);
-          tma_elected(to + j * box, map, full + 8 * stage, sg.h, id < 0 ? p.num_blocks : id);  // (out of range: zeros)
-        }
+        const int id = __shfl_sync(0xffffffffu, pg.now, i - pg.base + lane);
+        if (lane < ppt) tma_load_4d(to + lane * box, map, full + 8 * stage, 0, 0, sg.h, id < 0 ? p.num_blocks : id);
+        __syncwarp();
         issued = it + 1;
       }
       before += n;
@@ -1152,7 +1183,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   } else {
     const Bars bars{s_full, p_full, p_empty, sc_full, q_full, q_empty, o_free};
     const Cta<R> c{p, bars, sptr, tmem, abort_flag, nan_seg, rg, cta, R0, rows_here};
-    if constexpr (C::WIDE) softmax_wide(c, walk, warp, lane);
+    if constexpr (C::WIDE) softmax_wide<R, COARSE>(c, walk, warp, lane);
     else softmax_narrow(c, walk, warp, lane);
   }
   __syncthreads();
@@ -1251,14 +1282,14 @@ bool encode_map(CUtensorMap* map, const void* base, int num_blocks, int Hkv, int
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int R>
+template <int R, bool COARSE>
 int launch(const Params& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(attn_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<R>::SMEM);
+    return cudaFuncSetAttribute(attn_kernel<R, COARSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<R>::SMEM);
   });
   if (e != cudaSuccess) return TS_ERR_CUDA;
-  e = launch_pdl(attn_kernel<R>, dim3(p.RG * p.Gr), dim3(Cfg<R>::THREADS), Cfg<R>::SMEM, stream, mk, mv, p);
+  e = launch_pdl(attn_kernel<R, COARSE>, dim3(p.RG * p.Gr), dim3(Cfg<R>::THREADS), Cfg<R>::SMEM, stream, mk, mv, p);
   if (e != cudaSuccess) return TS_ERR_CUDA;
   int launches = 1;
   if (p.Gr > 1) {
@@ -1305,9 +1336,9 @@ int attention_fp8_tc_launch(const Fp8AttnCall& a, cudaStream_t stream, int num_s
   if (!encode_map(&mk, a.k_cache, a.num_blocks, a.Hkv, a.block_size) || !encode_map(&mv, a.v_cache, a.num_blocks, a.Hkv, a.block_size))
     return TS_ERR_CUDA;
   switch (pl.R) {
-    case 16: return launch<16>(p, mk, mv, stream);
-    case 32: return launch<32>(p, mk, mv, stream);
-    default: return launch<128>(p, mk, mv, stream);
+    case 16: return launch<16, false>(p, mk, mv, stream);  // (up to 32 rows a thread has one key)
+    case 32: return launch<32, false>(p, mk, mv, stream);
+    default: return a.scale_block >= 16 ? launch<128, true>(p, mk, mv, stream) : launch<128, false>(p, mk, mv, stream);
   }
 }
 
