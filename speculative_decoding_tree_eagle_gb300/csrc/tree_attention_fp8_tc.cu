@@ -61,7 +61,7 @@ struct Cfg {
   static constexpr int CPT = WIDE ? 64 : 8;                      // scores per softmax thread and tile
   static constexpr int GROUPS = WIDE ? 4 : R / CPT;              // what shares references: a quadrant's two warps, or four warps
   static constexpr int SOFT = WIDE ? 4 * BK / CPT : 4 * GROUPS;
-  // Warps: K and scale copies, V copies, K Q^T (and owner of the tensor memory), V^T P^T, converters, softmax.  Up to 32 rows, where a
+  // Warps: K copies, V and scale copies, K Q^T (and owner of the tensor memory), V^T P^T, converters, softmax.  Up to 32 rows, where a
   // tile should take no longer than its bytes (1400 cycles), two copying warps and two groups of converters take alternate tiles.
   static constexpr int PAIR = WIDE ? 1 : 2;
   static constexpr int W_V = PAIR, W_QK = 2 * PAIR, W_PV = W_QK + 1, W_CONV = W_PV + 1, CONV = 4 * PAIR;
@@ -648,7 +648,7 @@ __device__ __forceinline__ uint64_t visible64(int kb, int L, int m, const uint64
 // others; all of them keep the row's reference.  P goes to tensor memory.
 // COARSE (scale blocks of 16 tokens or more): the scales are those of 16 keys, so they are folded into the row's constants once for
 // 16 scores.  Otherwise each key has its own, and reading them (a broadcast of 16 bytes to a warp takes the shared memory four
-// cycles) is what paces the softmax: 177 against MEASURED us for 4 x 64 nodes of 32 heads over 32768 tokens.
+// cycles) is what paces the softmax: 177 against 150 us for 4 x 64 nodes of 32 heads over 32768 tokens.
 template <int R, bool COARSE>
 __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int warp, int lane) {
   using C = Cfg<R>;
@@ -939,7 +939,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   bool ok = true;
 
   if (warp < C::W_QK) {
-    // ------------------------------ codes by TMA (K, V); K's warps also copy the scales, as they are ------------------------------
+    // ------------------------------ codes by TMA (K, V); V's warps also copy the scales, as they are ------------------------------
     const bool is_k = warp < C::W_V;
     const int part = warp % C::PAIR;
     const int stages = is_k ? SK : SV;
@@ -955,7 +955,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
       for (int t = (before + part) % C::PAIR; t < n; t += C::PAIR) {
         const int i = t * ppt, it = before + t;
         pg.seek(p, sg, i, lane);
-        if (is_k) {
+        if (!is_k) {
           const int slot = it % kScaleSlots;
           if (pg.now == -1) report(p.status, TS_ERR_DEVICE_CHECK);
           ok = wait_warp(raw_empty + 8 * slot, ((it / kScaleSlots) & 1) ^ 1, abort_flag, p.status);
@@ -1065,16 +1065,21 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
     const int cw = warp - C::W_CONV, w = cw & 3, part = cw >> 2;  // (w: keys 32 w .. of every tile of this group)
     int before = 0, seg = 0;
     while (ok && walk.next(p, sg)) {
+      // eight lanes per row, 16 values each; all rows are asked for before the wait and the first of them
+      auto q_at = [&](int r) {
+        const int row = R0 + r, node = row / p.g;
+        return p.q + ((static_cast<long long>(sg.b) * p.m + node) * p.Hq + sg.h * p.g + row - node * p.g) * HD;
+      };
+      for (int r = 4 * cw + (lane >> 3); r < rows_here; r += 4 * C::CONV)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(q_at(r) + 16 * (lane & 7)));
       ok = wait_warp(q_empty, (seg & 1) ^ 1, abort_flag, p.status);
       if (!ok) break;
-      // eight lanes per row, 16 values each
 #pragma unroll 1
       for (int r0 = cw * 4; r0 < R; r0 += 4 * C::CONV) {
         const int r = r0 + (lane >> 3), c = lane & 7;
         uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
         if (r < rows_here) {
-          const int row = R0 + r, node = row / p.g, head = sg.h * p.g + row % p.g;
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + ((static_cast<long long>(sg.b) * p.m + node) * p.Hq + head) * HD) + 2 * c;
+          const uint4* src = reinterpret_cast<const uint4*>(q_at(r)) + 2 * c;
           x[0] = __ldg(src);
           x[1] = __ldg(src + 1);
         }
