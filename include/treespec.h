@@ -594,7 +594,7 @@ int ts_kv_read_fp8(const void* k_cache, const void* v_cache, const float* k_scal
  * block_table_out and prefix_len_out may be block_table and prefix_len themselves, for an update in place, or others, for the
  * next layer's cache to be committed from the same old state.
  *
- * freed_blocks [B, max_blocks], freed_count [B].  m <= TS_MAX_NODES, any d <= 256.  Two launches, no workspace.
+ * freed_blocks [B, max_blocks], freed_count [B].  m <= TS_MAX_NODES, any d <= 256.  One launch, two in place; no workspace.
  * Device errors: as ts_kv_commit (the sequence's cache is left untouched, its table row and length are copied).
  */
 int ts_kv_commit_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size,

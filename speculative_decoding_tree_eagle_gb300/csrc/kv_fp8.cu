@@ -35,53 +35,47 @@ struct WriteParams {
   const int32_t* length;
   int32_t* status;
   int B, n, Hkv, d, bs, sb, max_blocks, num_blocks, blocks;  // blocks: that n rows can touch
-  long long items;                                           // 2 * B * blocks * Hkv
 };
 
 // One (K or V, sequence, block, head) of a write.
 struct Item {
   bool live;
   int first, rows_kept, rows_end;  // block's first position; rows [0, kept) are kept, [kept, end) new
-  const Side* side;
-  int b, h;
-  uint8_t* codes;                  // the block's first row
+  const char* src;                 // the block's first row (it may lie before the tensor where that row is kept)
+  uint8_t* codes;
   float* scale;
 };
 
-__device__ __forceinline__ Item item_of(const WriteParams& p, long long idx) {
+// Block i, head h of sequence b.
+template <typename T>
+__device__ __forceinline__ Item item_of(const WriteParams& p, const Side& side, int b, int i, int h) {
   Item it;
   it.live = false;
-  if (idx >= p.items) return it;
-  const int h = static_cast<int>(idx % p.Hkv);
-  idx /= p.Hkv;
-  const int i = static_cast<int>(idx % p.blocks);
-  idx /= p.blocks;
-  const int b = static_cast<int>(idx % p.B);
-  it.side = &p.side[idx / p.B];
-  it.b = b;
-  it.h = h;
+  if (i >= p.blocks) return it;
   const int start = p.start_len[b], len = p.length != nullptr ? p.length[b] : p.n;
   const long long end = static_cast<long long>(start) + len;
   if (start < 0 || len < 0 || len > p.n || end > min(static_cast<long long>(p.max_blocks) * p.bs, static_cast<long long>(INT32_MAX))) {
     if (i == 0) report(p.status, TS_ERR_DEVICE_CHECK);
     return it;
   }
-  const long long first = (static_cast<long long>(start / p.sb) + i) * p.sb;
-  if (len == 0 || first >= end) return it;
-  const int lp = static_cast<int>(first / p.bs);
+  const long long first_at = static_cast<long long>(start / p.sb + i) * p.sb;
+  if (len == 0 || first_at >= end) return it;
+  const int first = static_cast<int>(first_at), lp = first / p.bs;
   const int page = p.table[static_cast<long long>(b) * p.max_blocks + lp];
   if (page < 0 || page >= p.num_blocks) {
     report(p.status, TS_ERR_DEVICE_CHECK);
     return it;
   }
   it.live = true;
-  it.first = static_cast<int>(first);
-  it.rows_kept = max(0, start - it.first);
+  it.first = first;
+  it.rows_kept = max(0, start - first);
   it.rows_end = static_cast<int>(min(static_cast<long long>(p.sb), end - first));
-  const int row = it.first - lp * p.bs;
+  const int row = first - lp * p.bs;
   const long long head = static_cast<long long>(page) * p.Hkv + h;
-  it.codes = it.side->cache + (head * p.bs + row) * p.d;
-  it.scale = it.side->scale + head * (p.bs / p.sb) + row / p.sb;
+  it.codes = side.cache + (head * p.bs + row) * p.d;
+  it.scale = side.scale + head * (p.bs / p.sb) + row / p.sb;
+  it.src = static_cast<const char*>(side.src) + (static_cast<long long>(b) * side.sb_ + static_cast<long long>(first - start) * side.sn +
+                                                 static_cast<long long>(h) * side.sh) * static_cast<long long>(sizeof(T));
   return it;
 }
 
@@ -91,6 +85,13 @@ template <>
 struct Held<__nv_bfloat16> {
   uint4 w;
   __device__ void load(const void* p) { w = __ldg(static_cast<const uint4*>(p)); }
+  __device__ void keep(uint2 c) { w.x = c.x, w.y = c.y; }
+  __device__ uint2 kept() const { return make_uint2(w.x, w.y); }
+  __device__ float largest() const {  // (max passes over a NaN)
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+    const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+    return fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.f);
+  }
   __device__ void values(float (&v)[8]) const {
     v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
     v[4] = bf16_lo(w.z), v[5] = bf16_hi(w.z), v[6] = bf16_lo(w.w), v[7] = bf16_hi(w.w);
@@ -99,6 +100,12 @@ struct Held<__nv_bfloat16> {
 template <>
 struct Held<float> {
   float4 a, b;
+  __device__ void keep(uint2 c) { a.x = __uint_as_float(c.x), a.y = __uint_as_float(c.y); }
+  __device__ uint2 kept() const { return make_uint2(__float_as_uint(a.x), __float_as_uint(a.y)); }
+  __device__ float largest() const {
+    return fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
+                 fmaxf(fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))), 0.f));
+  }
   __device__ void load(const void* p) {
     a = __ldg(static_cast<const float4*>(p));
     b = __ldg(static_cast<const float4*>(p) + 1);
@@ -118,73 +125,56 @@ __device__ __forceinline__ uint2 encode8(const float (&v)[8], float by) {
   c.y = encode_e4m3x2(v[4] * by, v[5] * by) | (encode_e4m3x2(v[6] * by, v[7] * by) << 16);
   return c;
 }
-__device__ __forceinline__ float absmax8(const float (&v)[8]) {  // (NaN passed over)
-  float m = 0.f;
+__device__ __forceinline__ float largest_code(uint2 c) {  // (NaN passed over)
+  float v[8], m = 0.f;
+  decode8(c, v);
 #pragma unroll
   for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
   return m;
 }
 
-// W warps per item, kChunk elements a load (d, strides and addresses are multiples of it).  Where the block fits in
-// kHeld chunks per thread the rows stay in registers between the maximum and the codes, otherwise they are read twice.
+// W warps per item, kChunk elements a load (d, strides and addresses are multiples of it).  The W * 32 threads cover whole rows (d / kChunk
+// divides their number), so a thread stays in its columns and no load costs a division.  Where the block fits in kHeld chunks per
+// thread the rows stay in registers between the maximum and the codes, otherwise they are read twice.
 template <typename T, int W, bool HOLD>
 __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_constant__ WriteParams p) {
   __shared__ float s_max[kWriteThreads / 32];
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp / W, part = (warp % W) * 32 + lane;  // item of this CTA, thread of the item
-  const Item it = item_of(p, static_cast<long long>(blockIdx.x) * (kWriteThreads / (32 * W)) + sub);
+  const Side& side = p.side[blockIdx.z];
+  const int x = blockIdx.x * (kWriteThreads / (32 * W)) + sub, block = x / p.Hkv;
+  const Item it = item_of<T>(p, side, blockIdx.y, block, x - block * p.Hkv);
   if (W == 1 && !it.live) return;
-  const int cpr = p.d / kChunk, chunks = it.live ? it.rows_end * cpr : 0;
-  const float old = it.live && it.rows_kept > 0 ? scale_in_range(*it.scale) : 1.f;
-  const char* src = nullptr;
-  if (it.live)
-    src = static_cast<const char*>(it.side->src) +
-          (static_cast<long long>(it.b) * it.side->sb_ + static_cast<long long>(it.first - p.start_len[it.b]) * it.side->sn +
-           static_cast<long long>(it.h) * it.side->sh) * static_cast<long long>(sizeof(T));
-  auto row_of = [&](int c) { return c / cpr; };
-  auto from = [&](int c, int r) {
-    return src + (static_cast<long long>(r) * it.side->sn + static_cast<long long>(c - r * cpr) * kChunk) * static_cast<long long>(sizeof(T));
-  };
+  const int per_row = p.d / kChunk, step = 32 * W / per_row, r0 = part / per_row, col = (part - r0 * per_row) * kChunk;
+  const int kept = it.live ? it.rows_kept : 0, end = it.live ? it.rows_end : 0;
+  const float old = kept > 0 ? scale_in_range(*it.scale) : 1.f;
+  const char* src = it.src + (static_cast<long long>(r0) * side.sn + col) * static_cast<long long>(sizeof(T));
+  const long long src_step = static_cast<long long>(step) * side.sn * static_cast<long long>(sizeof(T));
+  uint8_t* codes = it.codes + r0 * p.d + col;
+  const int codes_step = step * p.d;
   float amax = 0.f, v[8];
   Held<T> held[HOLD ? kHeld : 1];
   if constexpr (HOLD) {
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
-      const int c = part + u * 32 * W;
-      if (c < chunks) {
-        const int r = row_of(c);
-        if (r >= it.rows_kept) {
-          held[u].load(from(c, r));
-        } else {
-          const uint2 k = *reinterpret_cast<const uint2*>(it.codes + static_cast<long long>(c) * kChunk);
-          *reinterpret_cast<uint2*>(&held[u]) = k;
-        }
-      }
+      const int r = r0 + u * step;
+      if (r >= kept && r < end) held[u].load(src + u * src_step);
+      else if (r < end) held[u].keep(*reinterpret_cast<const uint2*>(codes + u * codes_step));
     }
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
-      const int c = part + u * 32 * W;
-      if (c < chunks) {
-        if (row_of(c) >= it.rows_kept) {
-          held[u].values(v);
-          amax = fmaxf(amax, absmax8(v));
-        } else {
-          decode8(*reinterpret_cast<const uint2*>(&held[u]), v);
-          amax = fmaxf(amax, absmax8(v) * old);
-        }
-      }
+      const int r = r0 + u * step;
+      if (r >= kept && r < end) amax = fmaxf(amax, held[u].largest());
+      else if (r < end) amax = fmaxf(amax, largest_code(held[u].kept()) * old);
     }
   } else {
-    for (int c = part; c < chunks; c += 32 * W) {
-      const int r = row_of(c);
-      if (r >= it.rows_kept) {
-        held[0].load(from(c, r));
-        held[0].values(v);
-        amax = fmaxf(amax, absmax8(v));
+    for (int r = r0; r < end; r += step) {
+      if (r >= kept) {
+        held[0].load(src + (r - r0) / step * src_step);
+        amax = fmaxf(amax, held[0].largest());
       } else {
-        decode8(*reinterpret_cast<const uint2*>(it.codes + static_cast<long long>(c) * kChunk), v);
-        amax = fmaxf(amax, absmax8(v) * old);
+        amax = fmaxf(amax, largest_code(*reinterpret_cast<const uint2*>(codes + (r - r0) / step * codes_step)) * old);
       }
     }
   }
@@ -203,28 +193,23 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
   if constexpr (HOLD) {
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
-      const int c = part + u * 32 * W;
-      if (c < chunks) {
-        const bool kept = row_of(c) < it.rows_kept;
-        if (kept && again == 1.f) continue;
-        if (kept) decode8(*reinterpret_cast<const uint2*>(&held[u]), v);
-        else held[u].values(v);
-        *reinterpret_cast<uint2*>(it.codes + static_cast<long long>(c) * kChunk) = encode8(v, kept ? again : inv);
-      }
+      const int r = r0 + u * step;
+      if (r >= end || (r < kept && again == 1.f)) continue;
+      if (r < kept) decode8(held[u].kept(), v);
+      else held[u].values(v);
+      *reinterpret_cast<uint2*>(codes + u * codes_step) = encode8(v, r < kept ? again : inv);
     }
   } else {
-    for (int c = part; c < chunks; c += 32 * W) {
-      const int r = row_of(c);
-      const bool kept = r < it.rows_kept;
-      if (kept && again == 1.f) continue;
-      uint8_t* to = it.codes + static_cast<long long>(c) * kChunk;
-      if (kept) {
-        decode8(*reinterpret_cast<const uint2*>(to), v);
+    for (int r = r0; r < end; r += step) {
+      if (r < kept && again == 1.f) continue;
+      uint2* to = reinterpret_cast<uint2*>(codes + (r - r0) / step * codes_step);
+      if (r < kept) {
+        decode8(*to, v);
       } else {
-        held[0].load(from(c, r));
+        held[0].load(src + (r - r0) / step * src_step);
         held[0].values(v);
       }
-      *reinterpret_cast<uint2*>(to) = encode8(v, kept ? again : inv);
+      *to = encode8(v, r < kept ? again : inv);
     }
   }
   if (part == 0) *it.scale = pow2(e);
@@ -238,16 +223,17 @@ template <typename T>
 __global__ void __launch_bounds__(kWriteThreads) write_any_kernel(const __grid_constant__ WriteParams p) {
   __shared__ float s_max[kWriteThreads / 32];
   pdl_wait();
-  const Item it = item_of(p, blockIdx.x);
+  const Side& side = p.side[blockIdx.z];
+  const int block = blockIdx.x / p.Hkv;
+  const Item it = item_of<T>(p, side, blockIdx.y, block, blockIdx.x - block * p.Hkv);
   if (!it.live) return;
   const int total = it.rows_end * p.d;
   const float old = it.rows_kept > 0 ? scale_in_range(*it.scale) : 1.f;
-  const T* src = static_cast<const T*>(it.side->src) + static_cast<long long>(it.b) * it.side->sb_ +
-                 static_cast<long long>(it.first - p.start_len[it.b]) * it.side->sn + static_cast<long long>(it.h) * it.side->sh;
+  const T* src = reinterpret_cast<const T*>(it.src);
   auto value = [&](int x, bool& kept) {
     const int r = x / p.d;
     kept = r < it.rows_kept;
-    return kept ? decode_e4m3(it.codes[x]) : element(src + static_cast<long long>(r) * it.side->sn + (x - r * p.d));
+    return kept ? decode_e4m3(it.codes[x]) : element(src + static_cast<long long>(r) * side.sn + (x - r * p.d));
   };
   float amax = 0.f;
   bool kept;
@@ -272,6 +258,21 @@ __global__ void __launch_bounds__(kWriteThreads) write_any_kernel(const __grid_c
 // ---------------------------------------------------------------------------------------------- read
 constexpr int kReadThreads = 256;
 
+// x / d for 0 <= x < 2^31 as a multiplication: with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1 the quotient is
+// (x m / 2^32 + x) / 2^s.  (Six divisions a thread took a third of a read's instructions.)
+struct Divide {
+  uint32_t m, s, d;
+  Divide() = default;
+  explicit Divide(int by) : d(static_cast<uint32_t>(by)) {
+    s = 0;
+    while ((1ull << s) < d) ++s;
+    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int quotient(int x) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(x), m) + static_cast<uint32_t>(x)) >> s);
+  }
+};
+
 struct ReadParams {
   const uint8_t* cache[2];
   const float* scale[2];
@@ -281,6 +282,7 @@ struct ReadParams {
   const int32_t* start_len;
   int32_t* status;
   int B, n, Hkv, d, bs, sb, max_blocks, num_blocks;
+  Divide by_heads, by_row, by_page, by_block;  // chunks of a token, of a head's row; tokens of a page, of a scale
 };
 
 // Whether sequence b can be read; its positions start .. end - 1 exist.
@@ -293,56 +295,74 @@ __device__ __forceinline__ bool read_range(const ReadParams& p, int b, int& star
   return true;
 }
 
-// A thread per N codes of a row: N values of type T out (N = 16: one 16-byte load; N = 1: any head dim and alignment).
+// A thread per N codes of a row: N values of type T out (N = 16: one 16-byte load; N = 1: any head dim and alignment), kAtOnce rows
+// apart in flight, as each is three dependent loads (table, codes and scale).
+constexpr int kAtOnce = 2;
 template <typename T, int N>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
   pdl_wait();
   const int b = blockIdx.y, kv = blockIdx.z;
   int start, rows;
   if (!read_range(p, b, start, rows) && blockIdx.x == 0 && threadIdx.x == 0) report(p.status, TS_ERR_DEVICE_CHECK);
-  const int per = p.d / N, heads = p.Hkv * per;
-  const long long total = static_cast<long long>(p.n) * heads;
-  const long long step = static_cast<long long>(gridDim.x) * kReadThreads;
+  const int per = p.d / N, heads = p.Hkv * per, nsb = p.bs / p.sb;
+  const int total = p.n * heads, step = gridDim.x * kReadThreads;  // (checked on the host to stay below 2^31 with all steps)
   T* out = static_cast<T*>(p.out[kv]) + static_cast<long long>(b) * total * N;
-  for (long long x = static_cast<long long>(blockIdx.x) * kReadThreads + threadIdx.x; x < total; x += step) {
-    const int t = static_cast<int>(x / heads);
-    const int rest = static_cast<int>(x - static_cast<long long>(t) * heads), h = rest / per, c = rest - h * per;
-    float s = 0.f;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (t < rows) {
-      const int pos = start + t, lp = pos / p.bs, row = pos - lp * p.bs;
-      const int page = p.table[static_cast<long long>(b) * p.max_blocks + lp];
-      if (page < 0 || page >= p.num_blocks) {
+  const int32_t* table = p.table + static_cast<long long>(b) * p.max_blocks;
+  for (int x0 = blockIdx.x * kReadThreads + threadIdx.x; x0 < total; x0 += kAtOnce * step) {
+    uint4 w[kAtOnce];
+    float s[kAtOnce];
+    int page[kAtOnce], pos[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int x = x0 + u * step, t = p.by_heads.quotient(x);
+      pos[u] = start + t;
+      page[u] = x < total && t < rows ? table[p.by_page.quotient(pos[u])] : -1;
+      if (x < total && t < rows && (page[u] < 0 || page[u] >= p.num_blocks)) {
         report(p.status, TS_ERR_DEVICE_CHECK);
-      } else {
-        const long long head = static_cast<long long>(page) * p.Hkv + h;
-        const uint8_t* from = p.cache[kv] + (head * p.bs + row) * p.d + c * N;
-        s = scale_in_range(p.scale[kv][head * (p.bs / p.sb) + row / p.sb]);
-        if constexpr (N == 16) w = *reinterpret_cast<const uint4*>(from);
-        else w.x = *from;
+        page[u] = -1;
       }
     }
-    if constexpr (N == 1) {
-      const float v = decode_e4m3(w.x) * s;
-      if constexpr (sizeof(T) == 2) out[x] = __float2bfloat16_rn(v);
-      else out[x] = v;
-    } else {
-      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-      float v[16];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 lo = decode_e4m3x2(in[j]), hi = decode_e4m3x2(in[j] >> 16);
-        v[4 * j] = lo.x * s, v[4 * j + 1] = lo.y * s, v[4 * j + 2] = hi.x * s, v[4 * j + 3] = hi.y * s;
+    for (int u = 0; u < kAtOnce; ++u) {
+      w[u] = make_uint4(0, 0, 0, 0);
+      s[u] = 0.f;
+      if (page[u] >= 0) {
+        const int rest = x0 + u * step - (pos[u] - start) * heads, h = p.by_row.quotient(rest), c = rest - h * per;
+        const int row = pos[u] - p.by_page.quotient(pos[u]) * p.bs;
+        const long long head = static_cast<long long>(page[u]) * p.Hkv + h;
+        const uint8_t* from = p.cache[kv] + (head * p.bs + row) * p.d + c * N;
+        s[u] = p.scale[kv][head * nsb + p.by_block.quotient(row)];
+        if constexpr (N == 16) w[u] = *reinterpret_cast<const uint4*>(from);
+        else w[u].x = *from;
       }
-      if constexpr (sizeof(T) == 2) {
-        uint4* to = reinterpret_cast<uint4*>(out + x * 16);
-        to[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-        to[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
-                           pack_bf16x2(v[14], v[15]));
-      } else {
-        float4* to = reinterpret_cast<float4*>(out + x * 16);
+    }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int x = x0 + u * step;
+      if (x >= total) break;
+      const float f = scale_in_range(s[u]);  // (codes of 0 where there is nothing to read)
+      if constexpr (N == 1) {
+        const float v = decode_e4m3(w[u].x) * f;
+        if constexpr (sizeof(T) == 2) out[x] = __float2bfloat16_rn(v);
+        else out[x] = v;
+      } else {
+        const uint32_t in[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 lo = decode_e4m3x2(in[j]), hi = decode_e4m3x2(in[j] >> 16);
+          v[4 * j] = lo.x * f, v[4 * j + 1] = lo.y * f, v[4 * j + 2] = hi.x * f, v[4 * j + 3] = hi.y * f;
+        }
+        if constexpr (sizeof(T) == 2) {
+          uint4* to = reinterpret_cast<uint4*>(out + static_cast<long long>(x) * 16);
+          to[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+          to[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
+                             pack_bf16x2(v[14], v[15]));
+        } else {
+          float4* to = reinterpret_cast<float4*>(out + static_cast<long long>(x) * 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
       }
     }
   }
@@ -365,6 +385,7 @@ struct CommitParams {
   int32_t* freed_count;
   int32_t* status;
   int B, m, Hkv, d, bs, sb, max_blocks, num_blocks;
+  bool in_place;  // a table or length is written over its input: in a launch of its own, after the rows have read it
 };
 
 // The contract of ts_kv_commit, checked by the whole CTA for sequence b; the path and the ids of the pages that tree
@@ -400,76 +421,8 @@ __device__ __forceinline__ Commit commit_of(const CommitParams& p, int b, int* s
   return c;
 }
 
-// A CTA per (sequence, KV head, K or V).  The accepted rows' codes and scales are staged in shared memory, so every row is
-// read before any is written; then a warp per block quantises its kept and its new rows.
-template <int N>  // codes a load: 16, 4 or 1
-__global__ void __launch_bounds__(kCommitThreads) commit_rows_kernel(const __grid_constant__ CommitParams p) {
-  extern __shared__ __align__(16) unsigned char s_rows[];
-  __shared__ int s_path[TS_MAX_NODES];
-  __shared__ int s_page[kMaxPages];
-  __shared__ float s_scale[TS_MAX_NODES];
-  using Word = typename std::conditional<N == 16, uint4, typename std::conditional<N == 4, uint32_t, uint8_t>::type>::type;
-  pdl_wait();
-  const int b = blockIdx.y, h = blockIdx.x >> 1, kv = blockIdx.x & 1;
-  const Commit c = commit_of(p, b, s_path, s_page);
-  if (!c.ok) return;
-  uint8_t* cache = p.cache[kv];
-  float* scale = p.scale[kv];
-  const int nsb = p.bs / p.sb, per = p.d / N;
-  auto head_of = [&](int pos) { return static_cast<long long>(s_page[pos / p.bs - c.p0]) * p.Hkv + h; };
-  for (int x = threadIdx.x; x < c.a * per; x += kCommitThreads) {
-    const int j = x / per, q = x - j * per, pos = c.L + s_path[j];
-    reinterpret_cast<Word*>(s_rows)[x] =
-        *reinterpret_cast<const Word*>(cache + (head_of(pos) * p.bs + pos % p.bs) * p.d + q * N);
-    if (q == 0) s_scale[j] = scale_in_range(scale[head_of(pos) * nsb + pos % p.bs / p.sb]);
-  }
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int blk = c.L / p.sb + warp; blk <= (c.L + c.a - 1) / p.sb; blk += kCommitThreads / 32) {
-    const int first = blk * p.sb, kept = max(0, c.L - first), end = min(p.sb, c.L + c.a - first);
-    uint8_t* codes = cache + (head_of(max(first, c.L)) * p.bs + first % p.bs) * p.d;
-    float* sc = scale + head_of(max(first, c.L)) * nsb + first % p.bs / p.sb;
-    const float old = kept > 0 ? scale_in_range(*sc) : 1.f;
-    auto word = [&](int x) {
-      const int r = x / per;
-      return r < kept ? reinterpret_cast<const Word*>(codes)[x]
-                      : reinterpret_cast<const Word*>(s_rows)[(first + r - c.L) * per + (x - r * per)];
-    };
-    auto by = [&](int x) {
-      const int r = x / per;
-      return r < kept ? old : s_scale[first + r - c.L];
-    };
-    float amax = 0.f;
-    for (int x = lane; x < end * per; x += 32) {
-      const Word w = word(x);
-      const uint8_t* one = reinterpret_cast<const uint8_t*>(&w);
-      float big = 0.f;
-#pragma unroll
-      for (int j = 0; j < N; ++j) big = fmaxf(big, fabsf(decode_e4m3(one[j])));
-      amax = fmaxf(amax, big * by(x));
-    }
-    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-    const int e = scale_exponent(amax);
-    for (int x = lane; x < end * per; x += 32) {
-      Word w = word(x);
-      const float f = by(x) * pow2(-e);
-      uint8_t* one = reinterpret_cast<uint8_t*>(&w);
-#pragma unroll
-      for (int j = 0; j < N; ++j) one[j] = static_cast<uint8_t>(encode_e4m3x2(decode_e4m3(one[j]) * f, 0.f) & 0xFFu);
-      reinterpret_cast<Word*>(codes)[x] = w;
-    }
-    __syncwarp();
-    if (lane == 0) *sc = pow2(e);
-  }
-}
-
-// Tables, lengths and the released pages, after the rows have moved: a CTA per sequence.
-__global__ void __launch_bounds__(kCommitThreads) commit_table_kernel(const __grid_constant__ CommitParams p) {
-  __shared__ int s_path[TS_MAX_NODES];
-  __shared__ int s_page[kMaxPages];
-  pdl_wait();
-  const int b = blockIdx.x;
-  const Commit c = commit_of(p, b, s_path, s_page);
+// Tables, lengths and the released pages of sequence b, by the whole CTA.
+__device__ void commit_tables(const CommitParams& p, int b, const Commit& c, const int* s_page) {
   const long long o = static_cast<long long>(b) * p.max_blocks;
   for (int i = threadIdx.x; i < p.max_blocks; i += kCommitThreads) {
     const int k = i + c.n_keep;
@@ -485,12 +438,122 @@ __global__ void __launch_bounds__(kCommitThreads) commit_table_kernel(const __gr
   }
 }
 
+// N codes as they are loaded, and what is done to them.
+template <int N>
+struct Codes;
+template <>
+struct Codes<16> {
+  uint4 w;
+  __device__ float largest() const {
+    return fmaxf(largest_code(make_uint2(w.x, w.y)), largest_code(make_uint2(w.z, w.w)));
+  }
+  __device__ void times(float f) {
+    float v[8];
+    decode8(make_uint2(w.x, w.y), v);
+    const uint2 a = encode8(v, f);
+    decode8(make_uint2(w.z, w.w), v);
+    const uint2 b = encode8(v, f);
+    w = make_uint4(a.x, a.y, b.x, b.y);
+  }
+};
+template <>
+struct Codes<4> {
+  uint32_t w;
+  __device__ float largest() const {
+    const float2 a = decode_e4m3x2(w), b = decode_e4m3x2(w >> 16);
+    return fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))), 0.f);
+  }
+  __device__ void times(float f) {
+    const float2 a = decode_e4m3x2(w), b = decode_e4m3x2(w >> 16);
+    w = encode_e4m3x2(a.x * f, a.y * f) | (encode_e4m3x2(b.x * f, b.y * f) << 16);
+  }
+};
+template <>
+struct Codes<1> {
+  uint8_t w;
+  __device__ float largest() const { return fmaxf(fabsf(decode_e4m3(w)), 0.f); }
+  __device__ void times(float f) { w = static_cast<uint8_t>(encode_e4m3x2(decode_e4m3(w) * f, 0.f)); }
+};
+
+// A CTA per (sequence, KV head, K or V).  The accepted rows' codes and scales are staged in shared memory, so every row is
+// read before any is written; then a team of threads per block quantises its kept and its new rows: a warp, or the whole CTA (WHOLE) for
+// blocks of more than 2048 codes, of which a path touches one or two (64 x 128 codes by a warp: 11 of 19 us).
+template <int N, bool WHOLE>  // N codes a load: 16, 4 or 1
+__global__ void __launch_bounds__(kCommitThreads) commit_rows_kernel(const __grid_constant__ CommitParams p) {
+  extern __shared__ __align__(16) unsigned char s_rows[];
+  __shared__ int s_path[TS_MAX_NODES];
+  __shared__ int s_page[kMaxPages];
+  __shared__ float s_scale[TS_MAX_NODES];
+  __shared__ float s_max[kCommitThreads / 32];
+  using Word = Codes<N>;
+  pdl_wait();
+  const int b = blockIdx.y, h = blockIdx.x >> 1, kv = blockIdx.x & 1;
+  const Commit c = commit_of(p, b, s_path, s_page);
+  if (!p.in_place && blockIdx.x == 0) commit_tables(p, b, c, s_page);
+  if (!c.ok) return;
+  uint8_t* cache = p.cache[kv];
+  float* scale = p.scale[kv];
+  const int nsb = p.bs / p.sb, per = p.d / N;
+  auto head_of = [&](int pos) { return static_cast<long long>(s_page[pos / p.bs - c.p0]) * p.Hkv + h; };
+  for (int x = threadIdx.x; x < c.a * per; x += kCommitThreads) {
+    const int j = x / per, q = x - j * per, pos = c.L + s_path[j];
+    reinterpret_cast<Word*>(s_rows)[x] =
+        *reinterpret_cast<const Word*>(cache + (head_of(pos) * p.bs + pos % p.bs) * p.d + q * N);
+    if (q == 0) s_scale[j] = scale_in_range(scale[head_of(pos) * nsb + pos % p.bs / p.sb]);
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int team = WHOLE ? 0 : warp, teams = WHOLE ? 1 : kCommitThreads / 32;
+  const int me = WHOLE ? threadIdx.x : lane, size = WHOLE ? kCommitThreads : 32;
+  for (int blk = c.L / p.sb + team; blk <= (c.L + c.a - 1) / p.sb; blk += teams) {
+    const int first = blk * p.sb, kept = max(0, c.L - first), end = min(p.sb, c.L + c.a - first);
+    const long long head = head_of(max(first, c.L));
+    Word* codes = reinterpret_cast<Word*>(cache + (head * p.bs + first % p.bs) * p.d);
+    float* sc = scale + head * nsb + first % p.bs / p.sb;
+    const float old = kept > 0 ? scale_in_range(*sc) : 1.f;
+    const Word* rows = reinterpret_cast<const Word*>(s_rows) + (first - c.L) * per;
+    float amax = 0.f;
+    for (int x = me; x < end * per; x += size) {
+      const int r = x / per;
+      amax = fmaxf(amax, r < kept ? codes[x].largest() * old : rows[x].largest() * s_scale[first + r - c.L]);
+    }
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+    if constexpr (WHOLE) {
+      __syncthreads();  // (the last block's maxima have been read; everyone has the old scale)
+      if (lane == 0) s_max[warp] = amax;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kCommitThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
+    }
+    const int e = scale_exponent(amax);
+    const float inv = pow2(-e);
+    for (int x = me; x < end * per; x += size) {
+      const int r = x / per;
+      if (r < kept && old * inv == 1.f) continue;
+      Word w = r < kept ? codes[x] : rows[x];
+      w.times((r < kept ? old : s_scale[first + r - c.L]) * inv);
+      codes[x] = w;
+    }
+    __syncwarp();
+    if (me == 0) *sc = pow2(e);
+  }
+}
+
+// The tables of an update in place, after the rows have moved: a CTA per sequence.
+__global__ void __launch_bounds__(kCommitThreads) commit_table_kernel(const __grid_constant__ CommitParams p) {
+  __shared__ int s_path[TS_MAX_NODES];
+  __shared__ int s_page[kMaxPages];
+  pdl_wait();
+  const Commit c = commit_of(p, blockIdx.x, s_path, s_page);
+  commit_tables(p, blockIdx.x, c, s_page);
+}
+
 template <typename T>
 cudaError_t launch_write(const WriteParams& p, bool wide, cudaStream_t stream) {
-  const int chunks = (p.sb * p.d + kChunk - 1) / kChunk, held = 32 * kHeld;
-  auto grid = [&](int w) { return dim3(static_cast<unsigned>((p.items + kWriteThreads / (32 * w) - 1) / (kWriteThreads / (32 * w)))); };
+  const int chunks = (p.sb * p.d + kChunk - 1) / kChunk, held = 32 * kHeld, items = p.blocks * p.Hkv;
+  auto grid = [&](int w) { return dim3((items + kWriteThreads / (32 * w) - 1) / (kWriteThreads / (32 * w)), p.B, 2); };
   const dim3 block(kWriteThreads);
-  if (!wide) return launch_pdl(write_any_kernel<T>, dim3(static_cast<unsigned>(p.items)), block, 0, stream, p);
+  if (!wide) return launch_pdl(write_any_kernel<T>, dim3(items, p.B, 2), block, 0, stream, p);
   if (chunks <= held) return launch_pdl(write_kernel<T, 1, true>, grid(1), block, 0, stream, p);
   if (chunks <= 2 * held) return launch_pdl(write_kernel<T, 2, true>, grid(2), block, 0, stream, p);
   if (chunks <= 4 * held) return launch_pdl(write_kernel<T, 4, true>, grid(4), block, 0, stream, p);
@@ -511,10 +574,9 @@ int kv_write_fp8_launch(const Fp8WriteCall& c, cudaStream_t stream) {
   p.B = c.B, p.n = c.n, p.Hkv = c.Hkv, p.d = c.d, p.bs = c.block_size, p.sb = c.scale_block;
   p.max_blocks = c.max_blocks, p.num_blocks = c.num_blocks;
   p.blocks = static_cast<int>((static_cast<long long>(c.n) + 2LL * c.scale_block - 2) / c.scale_block);
-  p.items = 2LL * c.B * p.blocks * c.Hkv;
-  if (p.items > INT32_MAX) return TS_ERR_UNSUPPORTED;
+  if (static_cast<long long>(p.blocks) * c.Hkv > INT32_MAX) return TS_ERR_UNSUPPORTED;
   const size_t size = c.dt == TS_BF16 ? 2 : 4;
-  bool wide = c.d % kChunk == 0;
+  bool wide = c.d % kChunk == 0 && 32 % (c.d / kChunk) == 0;  // (a head dim of 8, 16, 32, 64, 128 or 256)
   for (const Side& s : p.side) {
     wide = wide && reinterpret_cast<uintptr_t>(s.src) % 16 == 0 && reinterpret_cast<uintptr_t>(s.cache) % 8 == 0;
     for (long long st : {s.sb_, s.sn, s.sh}) wide = wide && st * static_cast<long long>(size) % 16 == 0;
@@ -536,8 +598,13 @@ int kv_read_fp8_launch(const Fp8ReadCall& c, cudaStream_t stream, int num_sms) {
   for (const void* x : {c.k_cache, c.v_cache, static_cast<const void*>(c.k), static_cast<const void*>(c.v)})
     wide = wide && reinterpret_cast<uintptr_t>(x) % 16 == 0;
   const long long total = static_cast<long long>(c.n) * c.Hkv * (c.d / (wide ? 16 : 1));
-  const long long most = (16LL * num_sms + 2LL * c.B - 1) / (2LL * c.B);
-  const unsigned gx = static_cast<unsigned>(std::max(1LL, std::min((total + kReadThreads - 1) / kReadThreads, std::max(1LL, most))));
+  p.by_heads = Divide(c.Hkv * (c.d / (wide ? 16 : 1))), p.by_row = Divide(c.d / (wide ? 16 : 1));
+  p.by_page = Divide(c.block_size), p.by_block = Divide(c.scale_block);
+  // sixteen CTAs per SM at most, each thread with kAtOnce chunks where there are as many
+  const long long most = std::max(1LL, (16LL * num_sms + 2LL * c.B - 1) / (2LL * c.B));
+  const long long want = (total + kReadThreads * kAtOnce - 1) / (kReadThreads * kAtOnce);
+  const unsigned gx = static_cast<unsigned>(std::max(1LL, std::min(want, most)));
+  if (total + 2LL * kAtOnce * gx * kReadThreads > INT32_MAX) return TS_ERR_UNSUPPORTED;
   const dim3 grid(gx, c.B, 2), block(kReadThreads);
   cudaError_t e;
   if (c.dt == TS_BF16)
@@ -559,6 +626,7 @@ int kv_commit_fp8_launch(const Fp8CommitCall& c, cudaStream_t stream) {
   p.status = c.dev_status;
   p.B = c.B, p.m = c.m, p.Hkv = c.Hkv, p.d = c.d, p.bs = c.block_size, p.sb = c.scale_block;
   p.max_blocks = c.max_blocks, p.num_blocks = c.num_blocks;
+  p.in_place = c.block_table_out == c.block_table || c.prefix_len_out == c.prefix_len;
   const uintptr_t at = reinterpret_cast<uintptr_t>(c.k_cache) | reinterpret_cast<uintptr_t>(c.v_cache) | static_cast<uintptr_t>(c.d);
   const size_t smem = static_cast<size_t>(c.m) * c.d;  // at most 64 KB
   auto run = [&](auto kernel, std::atomic<uint64_t>& done) {
@@ -568,12 +636,15 @@ int kv_commit_fp8_launch(const Fp8CommitCall& c, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3(2 * c.Hkv, c.B), dim3(kCommitThreads), smem, stream, p);
   };
-  static std::atomic<uint64_t> done16{0}, done4{0}, done1{0};
-  cudaError_t e = at % 16 == 0 ? run(commit_rows_kernel<16>, done16)
-                               : at % 4 == 0 ? run(commit_rows_kernel<4>, done4) : run(commit_rows_kernel<1>, done1);
+  static std::atomic<uint64_t> done[6]{};
+  const bool whole = c.scale_block * c.d > 2048;
+  cudaError_t e;
+  if (at % 16 == 0) e = whole ? run(commit_rows_kernel<16, true>, done[0]) : run(commit_rows_kernel<16, false>, done[1]);
+  else if (at % 4 == 0) e = whole ? run(commit_rows_kernel<4, true>, done[2]) : run(commit_rows_kernel<4, false>, done[3]);
+  else e = whole ? run(commit_rows_kernel<1, true>, done[4]) : run(commit_rows_kernel<1, false>, done[5]);
   if (e != cudaSuccess) return TS_ERR_CUDA;
-  e = launch_pdl(commit_table_kernel, dim3(c.B), dim3(kCommitThreads), 0, stream, p);
-  count_launches(2);
+  if (p.in_place) e = launch_pdl(commit_table_kernel, dim3(c.B), dim3(kCommitThreads), 0, stream, p);
+  count_launches(p.in_place ? 2 : 1);
   return e == cudaSuccess ? TS_OK : TS_ERR_CUDA;
 }
 

@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kKeys = 64;
-constexpr int kMinTiles = 2;     // tiles that a chunk is worth
+constexpr int kMinTiles = 1;     // tiles that a chunk is worth
 constexpr float kLn2f = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634074f;
 constexpr uint32_t kMasked = 0x80000000u;  // weight -0: a key that the row does not attend to (its V may be NaN)
