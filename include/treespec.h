@@ -607,7 +607,7 @@ int ts_kv_commit_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scal
  *
  * Arguments, layouts and results as ts_tree_attention with k = code * scale, v = code * scale; a node without any key (a mask row
  * without its own bit and an empty prefix) gets out 0 and lse -inf.  scale finite, > 0.  What lies in places that a node does not
- * attend to (NaN codes among them) does not reach its output; a NaN or an infinity in a query makes that row NaN.
+ * attend to (NaN codes among them) does not reach its output; a NaN or an infinity in a query reaches that row alone.
  * Supported: fp32 and bf16, any d <= 256 and any block_size on the CUDA cores (fp32 arithmetic throughout); bf16 with d == 128
  * and block_size in {16, 32, 64, 128} on the tensor cores (queries split exactly into two 8-bit parts, weights rounded to fp16 for
  * the product with V, sums in fp32).  max_prefix <= 2^30.
@@ -667,6 +667,18 @@ int ts_kv_reserve(void* k_cache, void* v_cache, ts_dtype dt, int num_blocks, int
                   void* stream);
 
 /*
+ * ts_kv_reserve_fp8 — the same for a cache in 8 bits: with the rows of a half-filled shared page go the scales of the
+ * blocks that they reach.  k_scale, v_scale [num_blocks, Hkv, block_size / scale_block] fp32, in/out.
+ * Limits and errors as for ts_kv_write_fp8 (scale_block divides block_size, d <= 256) and as above (d a multiple of 4).
+ * Workspace: ts_kv_reserve_workspace.
+ */
+int ts_kv_reserve_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size,
+                      int scale_block, int Hkv, int d, const int32_t* block_table, int max_blocks,
+                      const int32_t* prefix_len, const int32_t* refs, int B, int n, const int32_t* freed,
+                      int num_freed, int32_t* block_table_out, int32_t* refs_out, int32_t* granted, void* workspace,
+                      size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
  * ts_kv_fork — new sequences from old ones: fork, reorder and drop.
  *
  * Row r of the new state continues row src[r] of the old one (src[r] = -1: an empty row).  The new
@@ -707,6 +719,16 @@ int ts_kv_compact(void* k_cache, void* v_cache, ts_dtype dt, void* bounds, int n
                   int Hkv, int d, const int32_t* block_table, int max_blocks, const int32_t* refs, int B,
                   int32_t* block_table_out, int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace,
                   size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * ts_kv_compact_fp8 — the same for a cache in 8 bits: a page's scales move with its rows.  k_scale, v_scale
+ * [num_blocks, Hkv, block_size / scale_block] fp32, in/out.  Limits and errors as for ts_kv_reserve_fp8.
+ * Workspace: ts_kv_compact_workspace.
+ */
+int ts_kv_compact_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size,
+                      int scale_block, int Hkv, int d, const int32_t* block_table, int max_blocks, const int32_t* refs,
+                      int B, int32_t* block_table_out, int32_t* refs_out, int32_t* remap, int32_t* live,
+                      void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------------------
  * ts_selftest_bounded_wait — failure-detection check of the bounded pipeline waits.

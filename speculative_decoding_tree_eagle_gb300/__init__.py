@@ -135,6 +135,10 @@ def library():
         L.ts_kv_reserve.argtypes = [P, P, I, I, I, I, I, P, I, P, P, I, I, P, I, P, P, P, P, S, P, P]
         L.ts_kv_fork.restype = I
         L.ts_kv_fork.argtypes = [P, I, P, P, I, I, I, P, I, P, P, P, P, P]
+        L.ts_kv_reserve_fp8.restype = I
+        L.ts_kv_reserve_fp8.argtypes = [P, P, P, P, I, I, I, I, I, P, I, P, P, I, I, P, I, P, P, P, P, S, P, P]
+        L.ts_kv_compact_fp8.restype = I
+        L.ts_kv_compact_fp8.argtypes = [P, P, P, P, I, I, I, I, I, P, I, P, I, P, P, P, P, P, S, P, P]
         L.ts_kv_compact_workspace.restype = S
         L.ts_kv_compact_workspace.argtypes = [I]
         L.ts_kv_compact.restype = I
@@ -746,30 +750,44 @@ def tree_attention_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     return out, lse
 
 
+def _pool_cache(name: str, k_cache, v_cache, k_scale, v_scale, ix):
+    """The entry point of the pool for this cache, in bf16 or fp32 or with its scales in 8 bits, and its cache arguments."""
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("a cache in 8 bits has k_scale and v_scale")
+    if k_scale is not None:
+        at, sizes = _fp8_cache(k_cache, v_cache, k_scale, v_scale, ix)
+        return getattr(library(), name + "_fp8"), [*at, *sizes]
+    dtype, dt = k_cache.dtype, _dt(k_cache)
+    NB, Hkv, bs, d = cache = k_cache.shape
+    return getattr(library(), name), [_arg("k_cache", k_cache, ix, dtype, cache), _arg("v_cache", v_cache, ix, dtype, cache), dt,
+                                      NB, bs, Hkv, d]
+
+
 def kv_reserve(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, prefix_len: torch.Tensor,
                refs: torch.Tensor, n: int, *, freed: Optional[torch.Tensor] = None,
+               k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
                out: Optional[Dict[str, torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
                status: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
     """Pages for the next n tokens of every sequence: the pages in ``freed`` (any shape, -1 skipped; such as
     kv_commit's freed_blocks) lose a reference each, missing pages are handed out, and a half-filled last page
     that others hold too is replaced by a copy (its rows move in k_cache / v_cache).  Returns the new
     block_table and refs and granted [B] (fresh pages per sequence, -1 where the pool ran short and the sequence
-    stays as it was).  In ``out``, block_table and refs may be the input tensors themselves, for an update in place;
+    stays as it was).  A cache in 8 bits is given with its k_scale and v_scale; the copied rows' scales go with them.
+    In ``out``, block_table and refs may be the input tensors themselves, for an update in place;
     otherwise the outputs lie apart from the inputs and from one another."""
     L = library()
     ix = _index_of("k_cache", k_cache, 4)
     if ix != torch.cuda.current_device():
         with torch.cuda.device(ix):
-            return kv_reserve(k_cache, v_cache, block_table, prefix_len, refs, n, freed=freed, out=out, workspace=workspace,
-                              status=status)
-    dtype, dt = k_cache.dtype, _dt(k_cache)
-    NB, Hkv, bs, d = cache = k_cache.shape
+            return kv_reserve(k_cache, v_cache, block_table, prefix_len, refs, n, freed=freed, k_scale=k_scale,
+                              v_scale=v_scale, out=out, workspace=workspace, status=status)
+    call, cache_args = _pool_cache("ts_kv_reserve", k_cache, v_cache, k_scale, v_scale, ix)
+    NB, Hkv, bs, d = k_cache.shape
     B, width = table = block_table.shape
     need = L.ts_kv_reserve_workspace(NB, bs, B, n)
     if need == 0:
         raise TreeSpecError("invalid kv_reserve sizes")
-    args = [_arg("k_cache", k_cache, ix, dtype, cache), _arg("v_cache", v_cache, ix, dtype, cache), dt, NB, bs, Hkv, d,
-            _arg("block_table", block_table, ix, _I32, table), width, _arg("prefix_len", prefix_len, ix, _I32, (B,)),
+    args = [*cache_args, _arg("block_table", block_table, ix, _I32, table), width, _arg("prefix_len", prefix_len, ix, _I32, (B,)),
             _arg("refs", refs, ix, _I32, (NB,)), B, n]
     nfreed = 0 if freed is None else freed.numel()
     freed_at = _arg("freed", freed, ix, _I32, freed.shape) if nfreed else None
@@ -778,12 +796,12 @@ def kv_reserve(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.
         out = dict(block_table=torch.empty_like(block_table), refs=torch.empty_like(refs),
                    granted=torch.empty_like(prefix_len))
     ws, ws_bytes, keep = _scratch(need, refs, workspace)
-    rc = L.ts_kv_reserve(*args, freed_at, nfreed,
-                         *_out_args(out, ix, made, block_table=(_I32, table), refs=(_I32, (NB,)), granted=(_I32, (B,))), ws,
-                         ws_bytes, _status_arg(status, ix), _raw_stream(ix))
+    rc = call(*args, freed_at, nfreed,
+              *_out_args(out, ix, made, block_table=(_I32, table), refs=(_I32, (NB,)), granted=(_I32, (B,))), ws, ws_bytes,
+              _status_arg(status, ix), _raw_stream(ix))
     if rc == _INVALID and not made:
         _apart(out, ("block_table", "refs"), block_table=block_table, refs=refs, prefix_len=prefix_len, freed=freed,
-               k_cache=k_cache, v_cache=v_cache)
+               k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
     _check(rc)
     return out
 
@@ -816,32 +834,38 @@ def kv_fork(block_table: torch.Tensor, prefix_len: torch.Tensor, refs: torch.Ten
 
 
 def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, refs: torch.Tensor, *,
-               bounds: Optional[torch.Tensor] = None, out: Optional[Dict[str, torch.Tensor]] = None,
+               bounds: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+               v_scale: Optional[torch.Tensor] = None, out: Optional[Dict[str, torch.Tensor]] = None,
                workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
-    """Move the pages in use (refs > 0) to the lowest ids, in place on k_cache / v_cache (and bounds).  Returns the
-    new block_table and refs, remap [num_blocks] (a page's new id, -1 for a free one) and live [1] (pages in
-    use).  In ``out``, block_table and refs may be the input tensors themselves, for an update in place;
-    otherwise the outputs lie apart from the inputs and from one another."""
+    """Move the pages in use (refs > 0) to the lowest ids, in place on k_cache / v_cache (and bounds; a cache in 8 bits is
+    given with its k_scale and v_scale, which move too, and has no bounds).  Returns the new block_table and refs, remap
+    [num_blocks] (a page's new id, -1 for a free one) and live [1] (pages in use).  In ``out``, block_table and refs may be
+    the input tensors themselves, for an update in place; otherwise the outputs lie apart from the inputs and from one
+    another."""
     L = library()
     ix = _index_of("k_cache", k_cache, 4)
     if ix != torch.cuda.current_device():
         with torch.cuda.device(ix):
-            return kv_compact(k_cache, v_cache, block_table, refs, bounds=bounds, out=out, workspace=workspace, status=status)
-    dtype, dt = k_cache.dtype, _dt(k_cache)
-    NB, Hkv, bs, d = cache = k_cache.shape
+            return kv_compact(k_cache, v_cache, block_table, refs, bounds=bounds, k_scale=k_scale, v_scale=v_scale, out=out,
+                              workspace=workspace, status=status)
+    call, cache_args = _pool_cache("ts_kv_compact", k_cache, v_cache, k_scale, v_scale, ix)
+    NB, Hkv, bs, d = k_cache.shape
+    if k_scale is None:
+        cache_args.insert(3, None if bounds is None else _arg("bounds", bounds, ix, _BF16, (NB, Hkv, 2, d)))
+    elif bounds is not None:
+        raise ValueError("bounds belong to a cache in bf16 or fp32")
     B, width = table = block_table.shape
-    args = [_arg("k_cache", k_cache, ix, dtype, cache), _arg("v_cache", v_cache, ix, dtype, cache), dt,
-            None if bounds is None else _arg("bounds", bounds, ix, _BF16, (NB, Hkv, 2, d)), NB, bs, Hkv, d,
-            _arg("block_table", block_table, ix, _I32, table), width, _arg("refs", refs, ix, _I32, (NB,)), B]
+    args = [*cache_args, _arg("block_table", block_table, ix, _I32, table), width, _arg("refs", refs, ix, _I32, (NB,)), B]
     made = out is None
     if made:
         out = dict(block_table=torch.empty_like(block_table), refs=torch.empty_like(refs), remap=torch.empty_like(refs),
                    live=torch.empty((1,), dtype=_I32, device=refs.device))
     ws, ws_bytes, keep = _scratch(L.ts_kv_compact_workspace(NB), refs, workspace)
-    rc = L.ts_kv_compact(*args, *_out_args(out, ix, made, block_table=(_I32, table), refs=(_I32, (NB,)),
-                                           remap=(_I32, (NB,)), live=(_I32, (1,))), ws, ws_bytes, _status_arg(status, ix), _raw_stream(ix))
+    rc = call(*args, *_out_args(out, ix, made, block_table=(_I32, table), refs=(_I32, (NB,)), remap=(_I32, (NB,)),
+                                live=(_I32, (1,))), ws, ws_bytes, _status_arg(status, ix), _raw_stream(ix))
     if rc == _INVALID and not made:
-        _apart(out, ("block_table", "refs"), block_table=block_table, refs=refs, k_cache=k_cache, v_cache=v_cache, bounds=bounds)
+        _apart(out, ("block_table", "refs"), block_table=block_table, refs=refs, k_cache=k_cache, v_cache=v_cache, bounds=bounds,
+               k_scale=k_scale, v_scale=v_scale)
     _check(rc)
     return out
 

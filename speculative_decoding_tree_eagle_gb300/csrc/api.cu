@@ -532,6 +532,13 @@ static int check_fp8(int num_blocks, int block_size, int scale_block, int Hkv, i
   if (d > 256 || Hkv > 65535 / 2) return TS_ERR_UNSUPPORTED;
   return TS_OK;
 }
+// The pool's 8-bit forms write pages of all four: they lie apart.
+static bool fp8_scales(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size,
+                       int scale_block, int Hkv, int d) {
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !aligned4_ptr(k_scale) || !aligned4_ptr(v_scale)) return false;
+  const size_t cache = times(num_blocks, Hkv, block_size, d), scales = times(num_blocks, Hkv, block_size / scale_block);
+  return outputs_apart({{k_cache, cache, 1}, {v_cache, cache, 1}, {k_scale, scales, 4}, {v_scale, scales, 4}}, {});
+}
 // Elements from a strided tensor's first to its last, and one.
 static size_t extent(const int64_t* strides, int B, int n, int Hkv, int d) {
   return static_cast<size_t>((B - 1) * strides[0] + (n - 1) * strides[1] + (Hkv - 1) * strides[2] + d);
@@ -691,16 +698,14 @@ size_t ts_kv_reserve_workspace(int num_blocks, int block_size, int B, int n) {
   return ts::kv_reserve_workspace_bytes(num_blocks, block_size, B, n);
 }
 
-int ts_kv_reserve(void* k_cache, void* v_cache, ts_dtype dt, int num_blocks, int block_size, int Hkv, int d,
-                  const int32_t* block_table, int max_blocks, const int32_t* prefix_len, const int32_t* refs,
-                  int B, int n, const int32_t* freed, int num_freed, int32_t* block_table_out,
-                  int32_t* refs_out, int32_t* granted, void* workspace, size_t ws_bytes, int32_t* dev_status,
-                  void* stream) {
-  const int rc = check_cache(dt, num_blocks, block_size, Hkv, d, max_blocks, B);
-  if (rc != TS_OK) return rc;
+// Both forms of ts_kv_reserve; the caller has checked the cache's sizes.
+static int reserve(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int scale_block, int elem_bytes, int num_blocks,
+                   int block_size, int Hkv, int d, const int32_t* block_table, int max_blocks, const int32_t* prefix_len,
+                   const int32_t* refs, int B, int n, const int32_t* freed, int num_freed, int32_t* block_table_out,
+                   int32_t* refs_out, int32_t* granted, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream) {
   if (num_blocks > (1 << 28)) return TS_ERR_UNSUPPORTED;
   if (n <= 0 || num_freed < 0 || (num_freed > 0 && !freed)) return TS_ERR_INVALID;
-  if ((d * (dt == TS_BF16 ? 2LL : 4LL)) % 4 != 0) return TS_ERR_INVALID;
+  if (static_cast<long long>(d) * elem_bytes % 4 != 0) return TS_ERR_INVALID;
   if (B > TS_MAX_POOL_ROWS) return TS_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * max_blocks > INT32_MAX) return TS_ERR_UNSUPPORTED;  // requests are counted in 32 bits
   if (!k_cache || !v_cache || !block_table || !prefix_len || !refs || !block_table_out || !refs_out || !granted || !workspace)
@@ -708,18 +713,46 @@ int ts_kv_reserve(void* k_cache, void* v_cache, ts_dtype dt, int num_blocks, int
   if (!aligned4_ptr(k_cache) || !aligned4_ptr(v_cache) || !aligned16_ptr(workspace)) return TS_ERR_INVALID;
   const size_t need = ts::kv_reserve_workspace_bytes(num_blocks, block_size, B, n);
   if (ws_bytes < need) return TS_ERR_WORKSPACE;
-  const size_t cache = times(num_blocks, Hkv, block_size, d), size = dt == TS_BF16 ? 2 : 4, cells = times(B, max_blocks);
+  const size_t cache = times(num_blocks, Hkv, block_size, d), size = elem_bytes, cells = times(B, max_blocks);
+  const size_t scales = k_scale ? times(num_blocks, Hkv, block_size / scale_block) : 0;
   if (!outputs_apart({{block_table_out, cells, 4}, {refs_out, times(num_blocks, 1), 4}, {granted, times(B, 1), 4}, {workspace, need, 1}},
                      {{block_table_out == block_table ? nullptr : block_table, cells, 4},
                       {refs_out == refs ? nullptr : refs, times(num_blocks, 1), 4},
                       {prefix_len, times(B, 1), 4},
                       {freed, times(num_freed, 1), 4},
                       {k_cache, cache, size},
-                      {v_cache, cache, size}}))
+                      {v_cache, cache, size},
+                      {k_scale, scales, 4},
+                      {v_scale, scales, 4}}))
     return TS_ERR_INVALID;
-  ts::ReserveCall c{k_cache, v_cache, dt, num_blocks, block_size, Hkv, d, block_table, max_blocks, prefix_len, refs, B, n,
-                    freed, num_freed, block_table_out, refs_out, granted, workspace, dev_status};
+  ts::ReserveCall c{k_cache, v_cache, k_scale, v_scale, scale_block, elem_bytes, num_blocks, block_size, Hkv, d, block_table,
+                    max_blocks, prefix_len, refs, B, n, freed, num_freed, block_table_out, refs_out, granted, workspace,
+                    dev_status};
   return ts::kv_reserve_launch(c, static_cast<cudaStream_t>(stream));
+}
+
+int ts_kv_reserve(void* k_cache, void* v_cache, ts_dtype dt, int num_blocks, int block_size, int Hkv, int d,
+                  const int32_t* block_table, int max_blocks, const int32_t* prefix_len, const int32_t* refs,
+                  int B, int n, const int32_t* freed, int num_freed, int32_t* block_table_out,
+                  int32_t* refs_out, int32_t* granted, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                  void* stream) {
+  const int rc = check_cache(dt, num_blocks, block_size, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  return reserve(k_cache, v_cache, nullptr, nullptr, 0, dt == TS_BF16 ? 2 : 4, num_blocks, block_size, Hkv, d, block_table,
+                 max_blocks, prefix_len, refs, B, n, freed, num_freed, block_table_out, refs_out, granted, workspace, ws_bytes,
+                 dev_status, stream);
+}
+
+int ts_kv_reserve_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size,
+                      int scale_block, int Hkv, int d, const int32_t* block_table, int max_blocks, const int32_t* prefix_len,
+                      const int32_t* refs, int B, int n, const int32_t* freed, int num_freed, int32_t* block_table_out,
+                      int32_t* refs_out, int32_t* granted, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  const int rc = check_fp8(num_blocks, block_size, scale_block, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  if (!fp8_scales(k_cache, v_cache, k_scale, v_scale, num_blocks, block_size, scale_block, Hkv, d)) return TS_ERR_INVALID;
+  return reserve(k_cache, v_cache, k_scale, v_scale, scale_block, 1, num_blocks, block_size, Hkv, d, block_table, max_blocks,
+                 prefix_len, refs, B, n, freed, num_freed, block_table_out, refs_out, granted, workspace, ws_bytes, dev_status,
+                 stream);
 }
 
 int ts_kv_fork(const int32_t* block_table, int max_blocks, const int32_t* prefix_len, const int32_t* refs,
@@ -743,34 +776,58 @@ int ts_kv_fork(const int32_t* block_table, int max_blocks, const int32_t* prefix
 
 size_t ts_kv_compact_workspace(int num_blocks) { return num_blocks > 0 ? ts::kv_compact_workspace_bytes(num_blocks) : 0; }
 
+// Both forms of ts_kv_compact; the caller has checked the cache's sizes.  side: smaller buffers of 4-byte words that move
+// too, side_words in a page.
+static int compact(void* k_cache, void* v_cache, int elem_bytes, void* side0, void* side1, long long side_words, int num_blocks,
+                   int block_size, int Hkv, int d, const int32_t* block_table, int max_blocks, const int32_t* refs, int B,
+                   int32_t* block_table_out, int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace,
+                   size_t ws_bytes, int32_t* dev_status, void* stream) {
+  if (static_cast<long long>(d) * elem_bytes % 4 != 0) return TS_ERR_INVALID;
+  if (!k_cache || !v_cache || !block_table || !refs || !block_table_out || !refs_out || !remap || !live || !workspace)
+    return TS_ERR_INVALID;
+  if (!aligned4_ptr(k_cache) || !aligned4_ptr(v_cache) || !aligned16_ptr(workspace)) return TS_ERR_INVALID;
+  if (num_blocks > (1 << 28)) return TS_ERR_UNSUPPORTED;
+  const size_t need = ts::kv_compact_workspace_bytes(num_blocks);
+  if (ws_bytes < need) return TS_ERR_WORKSPACE;
+  const size_t cache = times(num_blocks, Hkv, block_size, d), size = elem_bytes, cells = times(B, max_blocks);
+  const size_t pages = num_blocks, words = pages * static_cast<size_t>(side_words);
+  if (!outputs_apart({{block_table_out, cells, 4}, {refs_out, pages, 4}, {remap, pages, 4}, {live, 1, 4}, {workspace, need, 1}},
+                     {{block_table_out == block_table ? nullptr : block_table, cells, 4},
+                      {refs_out == refs ? nullptr : refs, pages, 4},
+                      {k_cache, cache, size},
+                      {v_cache, cache, size},
+                      {side0, words, 4},
+                      {side1, words, 4}}))
+    return TS_ERR_INVALID;
+  const int sms = ts::device_sm_count();
+  if (sms <= 0) return TS_ERR_CUDA;
+  ts::CompactCall c{k_cache, v_cache, {side0, side1}, side_words * 4, num_blocks, block_size, Hkv, d * elem_bytes, block_table,
+                    max_blocks, refs, B, block_table_out, refs_out, remap, live, workspace, dev_status};
+  return ts::kv_compact_launch(c, static_cast<cudaStream_t>(stream), sms);
+}
+
 int ts_kv_compact(void* k_cache, void* v_cache, ts_dtype dt, void* bounds, int num_blocks, int block_size,
                   int Hkv, int d, const int32_t* block_table, int max_blocks, const int32_t* refs, int B,
                   int32_t* block_table_out, int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace,
                   size_t ws_bytes, int32_t* dev_status, void* stream) {
   const int rc = check_cache(dt, num_blocks, block_size, Hkv, d, max_blocks, B);
   if (rc != TS_OK) return rc;
-  if ((d * (dt == TS_BF16 ? 2LL : 4LL)) % 4 != 0) return TS_ERR_INVALID;
-  if (!k_cache || !v_cache || !block_table || !refs || !block_table_out || !refs_out || !remap || !live || !workspace)
-    return TS_ERR_INVALID;
-  if (!aligned4_ptr(k_cache) || !aligned4_ptr(v_cache) || !aligned16_ptr(workspace)) return TS_ERR_INVALID;
-  if (num_blocks > (1 << 28)) return TS_ERR_UNSUPPORTED;
   if (bounds && !aligned16_ptr(bounds)) return TS_ERR_INVALID;
-  const size_t need = ts::kv_compact_workspace_bytes(num_blocks);
-  if (ws_bytes < need) return TS_ERR_WORKSPACE;
-  const size_t cache = times(num_blocks, Hkv, block_size, d), size = dt == TS_BF16 ? 2 : 4, cells = times(B, max_blocks);
-  const size_t pages = num_blocks;
-  if (!outputs_apart({{block_table_out, cells, 4}, {refs_out, pages, 4}, {remap, pages, 4}, {live, 1, 4}, {workspace, need, 1}},
-                     {{block_table_out == block_table ? nullptr : block_table, cells, 4},
-                      {refs_out == refs ? nullptr : refs, pages, 4},
-                      {k_cache, cache, size},
-                      {v_cache, cache, size},
-                      {bounds, times(num_blocks, Hkv, 2, d), 2}}))
-    return TS_ERR_INVALID;
-  const int sms = ts::device_sm_count();
-  if (sms <= 0) return TS_ERR_CUDA;
-  return ts::kv_compact_launch(k_cache, v_cache, dt, bounds, num_blocks, block_size, Hkv, d, block_table, max_blocks, refs, B,
-                               block_table_out, refs_out, remap, live, workspace, dev_status,
-                               static_cast<cudaStream_t>(stream), sms);
+  return compact(k_cache, v_cache, dt == TS_BF16 ? 2 : 4, bounds, nullptr, static_cast<long long>(Hkv) * d, num_blocks, block_size,
+                 Hkv, d, block_table, max_blocks, refs, B, block_table_out, refs_out, remap, live, workspace, ws_bytes, dev_status,
+                 stream);
+}
+
+int ts_kv_compact_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size,
+                      int scale_block, int Hkv, int d, const int32_t* block_table, int max_blocks, const int32_t* refs, int B,
+                      int32_t* block_table_out, int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace,
+                      size_t ws_bytes, int32_t* dev_status, void* stream) {
+  const int rc = check_fp8(num_blocks, block_size, scale_block, Hkv, d, max_blocks, B);
+  if (rc != TS_OK) return rc;
+  if (!fp8_scales(k_cache, v_cache, k_scale, v_scale, num_blocks, block_size, scale_block, Hkv, d)) return TS_ERR_INVALID;
+  return compact(k_cache, v_cache, 1, k_scale, v_scale, static_cast<long long>(Hkv) * (block_size / scale_block), num_blocks,
+                 block_size, Hkv, d, block_table, max_blocks, refs, B, block_table_out, refs_out, remap, live, workspace, ws_bytes,
+                 dev_status, stream);
 }
 
 int ts_selftest_bounded_wait(int mode, int32_t* result, int32_t* dev_status, void* stream) {

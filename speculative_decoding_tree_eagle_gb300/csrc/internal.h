@@ -256,7 +256,9 @@ int attention_fp8_tc_launch(const Fp8AttnCall& a, cudaStream_t stream, int num_s
 struct ReserveCall {
   void* k_cache;
   void* v_cache;
-  ts_dtype dt;
+  float* k_scale;  // an 8-bit cache's scales, or null
+  float* v_scale;
+  int scale_block, elem_bytes;
   int num_blocks, block_size, Hkv, d;
   const int32_t* block_table;
   int max_blocks;
@@ -277,9 +279,23 @@ int kv_fork_launch(const int32_t* block_table, int max_blocks, const int32_t* pr
                    int block_size, int B, const int32_t* src, int B_out, int32_t* block_table_out, int32_t* prefix_len_out,
                    int32_t* refs_out, int32_t* dev_status, cudaStream_t stream, int num_sms);
 size_t kv_compact_workspace_bytes(int num_blocks);
-int kv_compact_launch(void* k_cache, void* v_cache, ts_dtype dt, void* bounds, int num_blocks, int block_size, int Hkv, int d,
-                      const int32_t* block_table, int max_blocks, const int32_t* refs, int B, int32_t* block_table_out,
-                      int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace, int32_t* dev_status,
-                      cudaStream_t stream, int num_sms);
+struct CompactCall {
+  void* k_cache;
+  void* v_cache;
+  void* side[2];         // smaller buffers that move too, or null: the page bounds, an 8-bit cache's scales
+  long long side_bytes;  // of a page, in each
+  int num_blocks, block_size, Hkv, row_bytes;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* refs;
+  int B;
+  int32_t* block_table_out;
+  int32_t* refs_out;
+  int32_t* remap;
+  int32_t* live;
+  void* workspace;
+  int32_t* dev_status;
+};
+int kv_compact_launch(const CompactCall& c, cudaStream_t stream, int num_sms);
 
 }  // namespace ts

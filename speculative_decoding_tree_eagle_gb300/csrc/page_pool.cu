@@ -284,16 +284,32 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   }
 }
 
-// The first L % bs rows of the shared last pages, for every KV head: CTA (head, row b).
+// The scales of an 8-bit cache, nsb for every page and head; none: k is null.
+struct Scales {
+  float* k;
+  float* v;
+  int nsb;
+};
+
+// The first L % bs rows of the shared last pages, for every KV head: CTA (head, row b); with them the scales of the blocks
+// that those rows reach.
 template <typename Chunk>
 __global__ void __launch_bounds__(256) copy_tails_kernel(unsigned char* kc, unsigned char* vc, int Hkv, int bs, int row_bytes,
-                                                         const int32_t* __restrict__ copy,
+                                                         Scales scales, const int32_t* __restrict__ copy,
                                                          const int32_t* __restrict__ prefix_len) {
   pdl_wait();
   const int b = blockIdx.y, h = blockIdx.x;
   const int from = copy[2 * b], to = copy[2 * b + 1];
   if (from < 0 || to < 0) return;
-  const int chunks = prefix_len[b] % bs * (row_bytes / static_cast<int>(sizeof(Chunk)));
+  const int rows = prefix_len[b] % bs, chunks = rows * (row_bytes / static_cast<int>(sizeof(Chunk)));
+  if (scales.k != nullptr) {
+    const int sb = bs / scales.nsb;
+    const long long sf = (static_cast<long long>(from) * Hkv + h) * scales.nsb, st = (static_cast<long long>(to) * Hkv + h) * scales.nsb;
+    for (int i = threadIdx.x; i * sb < rows; i += 256) {
+      scales.k[st + i] = scales.k[sf + i];
+      scales.v[st + i] = scales.v[sf + i];
+    }
+  }
   const long long page = static_cast<long long>(bs) * row_bytes;
   const long long src = (static_cast<long long>(from) * Hkv + h) * page, dst = (static_cast<long long>(to) * Hkv + h) * page;
   const Chunk* ks = reinterpret_cast<const Chunk*>(kc + src);
@@ -513,10 +529,11 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   }
 }
 
-// The moves' bytes and the tables: CTAs stride over (move, buffer) and over the table's cells.
+// The moves' bytes and the tables: CTAs stride over (move, buffer) and over the table's cells.  Beside K and V up to two
+// smaller buffers of whole words move (page bounds; an 8-bit cache's scales).
 template <typename Chunk>
-__global__ void __launch_bounds__(256) move_pages_kernel(unsigned char* kc, unsigned char* vc, unsigned char* bounds,
-                                                         long long page_bytes, long long bounds_bytes,
+__global__ void __launch_bounds__(256) move_pages_kernel(unsigned char* kc, unsigned char* vc, unsigned char* side0,
+                                                         unsigned char* side1, long long page_bytes, long long side_bytes,
                                                          const int32_t* __restrict__ moves,
                                                          const int32_t* __restrict__ remap, int num_blocks,
                                                          const int32_t* table, int32_t* table_out, long long cells,
@@ -532,14 +549,15 @@ __global__ void __launch_bounds__(256) move_pages_kernel(unsigned char* kc, unsi
     }
     table_out[i] = q;
   }
-  const int n = moves[0], bufs = bounds != nullptr ? 3 : 2;
+  const int n = moves[0], bufs = 2 + (side0 != nullptr) + (side1 != nullptr);
   for (long long it = blockIdx.x; it < static_cast<long long>(n) * bufs; it += gridDim.x) {
     const int k = static_cast<int>(it / bufs), which = static_cast<int>(it - static_cast<long long>(k) * bufs);
     const long long from = moves[1 + 2 * k], to = moves[2 + 2 * k];
-    if (which == 2) {
-      const uint32_t* s = reinterpret_cast<const uint32_t*>(bounds + from * bounds_bytes);
-      uint32_t* d = reinterpret_cast<uint32_t*>(bounds + to * bounds_bytes);
-      for (long long i = tid; i < bounds_bytes / 4; i += 256) d[i] = s[i];
+    if (which >= 2) {
+      unsigned char* side = which == 2 ? side0 : side1;
+      const uint32_t* s = reinterpret_cast<const uint32_t*>(side + from * side_bytes);
+      uint32_t* d = reinterpret_cast<uint32_t*>(side + to * side_bytes);
+      for (long long i = tid; i < side_bytes / 4; i += 256) d[i] = s[i];
       continue;
     }
     unsigned char* base = which == 0 ? kc : vc;
@@ -594,14 +612,15 @@ int kv_reserve_launch(const ReserveCall& c, cudaStream_t stream) {
   cudaError_t e = launch_pdl(reserve_kernel, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
   if (e != cudaSuccess) return TS_ERR_CUDA;
   count_launches(1);
-  const int row_bytes = c.d * (c.dt == TS_BF16 ? 2 : 4);
+  const int row_bytes = c.d * c.elem_bytes;
+  const Scales scales{c.k_scale, c.v_scale, c.k_scale != nullptr ? c.block_size / c.scale_block : 0};
   unsigned char *k = static_cast<unsigned char*>(c.k_cache), *v = static_cast<unsigned char*>(c.v_cache);
   const dim3 grid(c.Hkv, c.B);
   e = wide_rows(k, v, row_bytes)
-          ? launch_pdl(copy_tails_kernel<uint4>, grid, dim3(256), 0, stream, k, v, c.Hkv, c.block_size, row_bytes, a.copy,
-                       c.prefix_len)
-          : launch_pdl(copy_tails_kernel<uint32_t>, grid, dim3(256), 0, stream, k, v, c.Hkv, c.block_size, row_bytes, a.copy,
-                       c.prefix_len);
+          ? launch_pdl(copy_tails_kernel<uint4>, grid, dim3(256), 0, stream, k, v, c.Hkv, c.block_size, row_bytes, scales,
+                       a.copy, c.prefix_len)
+          : launch_pdl(copy_tails_kernel<uint32_t>, grid, dim3(256), 0, stream, k, v, c.Hkv, c.block_size, row_bytes, scales,
+                       a.copy, c.prefix_len);
   if (e != cudaSuccess) return TS_ERR_CUDA;
   count_launches(1);
   return TS_OK;
@@ -634,31 +653,25 @@ int kv_fork_launch(const int32_t* block_table, int max_blocks, const int32_t* pr
 
 size_t kv_compact_workspace_bytes(int num_blocks) { return 4 * (static_cast<size_t>(num_blocks) + 2); }
 
-int kv_compact_launch(void* k_cache, void* v_cache, ts_dtype dt, void* bounds, int num_blocks, int block_size, int Hkv, int d,
-                      const int32_t* block_table, int max_blocks, const int32_t* refs, int B, int32_t* block_table_out,
-                      int32_t* refs_out, int32_t* remap, int32_t* live, void* workspace, int32_t* dev_status,
-                      cudaStream_t stream, int num_sms) {
-  CompactArgs a{refs, refs_out, remap, live, static_cast<int32_t*>(workspace), num_blocks};
+int kv_compact_launch(const CompactCall& c, cudaStream_t stream, int num_sms) {
+  CompactArgs a{c.refs, c.refs_out, c.remap, c.live, static_cast<int32_t*>(c.workspace), c.num_blocks};
   cudaError_t e = launch_pdl(compact_kernel, dim3(kPoolCtas), dim3(kPoolThreads), 0, stream, a);
   if (e != cudaSuccess) return TS_ERR_CUDA;
   count_launches(1);
-  const int row_bytes = d * (dt == TS_BF16 ? 2 : 4);
-  const long long page_bytes = static_cast<long long>(Hkv) * block_size * row_bytes;
-  const long long bounds_bytes = static_cast<long long>(Hkv) * 4 * d;
-  const long long cells = static_cast<long long>(B) * max_blocks;
-  unsigned char *k = static_cast<unsigned char*>(k_cache), *v = static_cast<unsigned char*>(v_cache);
-  unsigned char* bd = static_cast<unsigned char*>(bounds);
+  unsigned char *k = static_cast<unsigned char*>(c.k_cache), *v = static_cast<unsigned char*>(c.v_cache);
+  unsigned char *side0 = static_cast<unsigned char*>(c.side[0]), *side1 = static_cast<unsigned char*>(c.side[1]);
+  const long long page_bytes = static_cast<long long>(c.Hkv) * c.block_size * c.row_bytes;
+  const long long cells = static_cast<long long>(c.B) * c.max_blocks;
+  const int bufs = 2 + (side0 != nullptr) + (side1 != nullptr);
   // A CTA per buffer of a move up to 64 per SM (6100 pages of 64 KB: 148 us against 160 with eight per SM), at most
   // what this pool can have.
-  const long long most = std::max((cells + 255) / 256, (static_cast<long long>(num_blocks) / 2 + 1) * (bounds ? 3 : 2));
+  const long long most = std::max((cells + 255) / 256, (static_cast<long long>(c.num_blocks) / 2 + 1) * bufs);
   const dim3 grid(static_cast<unsigned>(std::min<long long>(64LL * num_sms, most)));
-  e = wide_rows(k, v, row_bytes)
-          ? launch_pdl(move_pages_kernel<uint4>, grid, dim3(256), 0, stream, k, v, bd, page_bytes, bounds_bytes,
-                       a.moves, remap, num_blocks, block_table,
-                       block_table_out, cells, dev_status)
-          : launch_pdl(move_pages_kernel<uint32_t>, grid, dim3(256), 0, stream, k, v, bd, page_bytes, bounds_bytes,
-                       a.moves, remap, num_blocks, block_table,
-                       block_table_out, cells, dev_status);
+  e = wide_rows(k, v, c.row_bytes)
+          ? launch_pdl(move_pages_kernel<uint4>, grid, dim3(256), 0, stream, k, v, side0, side1, page_bytes, c.side_bytes,
+                       a.moves, c.remap, c.num_blocks, c.block_table, c.block_table_out, cells, c.dev_status)
+          : launch_pdl(move_pages_kernel<uint32_t>, grid, dim3(256), 0, stream, k, v, side0, side1, page_bytes, c.side_bytes,
+                       a.moves, c.remap, c.num_blocks, c.block_table, c.block_table_out, cells, c.dev_status);
   if (e != cudaSuccess) return TS_ERR_CUDA;
   count_launches(1);
   return TS_OK;
