@@ -50,6 +50,9 @@ constexpr int kScaleSlots = 4;
 constexpr uint32_t kNoPage = 0x7FDEAD01u;    // in the place of a scale: its key's page has no id
 constexpr float kFloor = -1e30f;             // reference of a row that has met no key
 constexpr float kBelow = 7.f, kRise = 15.f;  // the reference lies kBelow under the largest y; raised when exceeded by kRise
+// References beyond this make their rows NaN: fp32 holds them to half a unit of the exponent and more, and where rounding passes the
+// margins a row would overflow or vanish.
+constexpr float kMostM = 4194304.f;
 constexpr float kLn2f = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634074f;
 
@@ -549,7 +552,7 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
           const float M = fmaxf(fmaxf(red[lane], red[R + lane]), fmaxf(red[2 * R + lane], red[3 * R + lane])) - kBelow;
           const bool rises = M > old;  // (kFloor before the first key, and nothing where there is none yet)
           factor[lane] = rises && old != kFloor ? ex2_approx(old - M) : 1.f;
-          if (rises) m_at(lane) = M;
+          if (rises) m_at(lane) = fabsf(M) > kMostM ? __int_as_float(0x7FC00000) : M;
         }
         group_sync(group, 128);
         hold();
@@ -742,7 +745,7 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
         group_sync(quad, 32 * PARTS);  // (red is written again)
         const bool rises = high > M;
         const float f = rises && M != kFloor ? ex2_approx(M - high) : 1.f;
-        if (rises) M = high;
+        if (rises) M = fabsf(high) > kMostM && valid ? __int_as_float(0x7FC00000) : high;
         l2 = mul_f32x2(l2, pack_f32x2(f, f));
         if (t > sg.t0) {
           ok = c.o_holds(it - 1);
@@ -1195,14 +1198,31 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   if (warp == C::W_QK) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-// A warp per output row: joins the parts of a unit that several CTAs walked, in the order of the CTAs.
-template <int R>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params p) {
+// Joins the parts of the units that several CTAs walked, in the order of the CTAs, a warp per row.  Either the warps are those of all
+// rows of the output, and a row whose unit one CTA had is passed over, or (BOUNDARIES) those of the rows at every boundary between
+// two of attn_kernel's CTAs, of which the first inside a unit has the unit.  The form with fewer warps is taken: with 61440 rows
+// (16 x 60 nodes of 64 heads) the call takes 173 us by boundaries against 186 by rows, with 1024 (4 x 8 nodes of 32) 68 by
+// rows against 71.
+constexpr int kJoinWarps = 8, kJoinRows = 16;  // rows of a CTA at a boundary
+template <int R, bool BOUNDARIES>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Params p) {
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (item >= static_cast<long long>(p.B) * p.Hkv * p.rows) return;
-  const int row = static_cast<int>(item % p.rows), bh = static_cast<int>(item / p.rows), b = bh / p.Hkv, h = bh % p.Hkv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int b, h, rg, r, r1, first;  // unit, row group, rows r, r + kJoinWarps, .. below r1 of it; the unit's first tile
+  if constexpr (BOUNDARIES) {
+    rg = blockIdx.x % p.RG;
+    // (every warp finds the place by itself: no barrier)
+    const Walk w = walk_of(p, blockIdx.x / p.RG + 1, lane);
+    if (w.x >= w.x1 || w.off == 0) return;  // no tiles from here on, or a unit begins here
+    b = w.b, h = w.h, first = w.x - w.off;
+    r = blockIdx.y * kJoinRows + warp;
+    r1 = min(min(R, p.rows - rg * R), static_cast<int>(blockIdx.y + 1) * kJoinRows);
+  } else {
+    const long long item = static_cast<long long>(blockIdx.x) * kJoinWarps + warp;
+    if (item >= static_cast<long long>(p.B) * p.Hkv * p.rows) return;
+    const int bh = static_cast<int>(item / p.rows), row = static_cast<int>(item - static_cast<long long>(bh) * p.rows);
+    b = bh / p.Hkv, h = bh - b * p.Hkv, rg = row / R, r = row - rg * R, r1 = r + 1, first = 0;
+  }
   const int T = tiles_of(p, b);
   if (T == 0) return;
   int before = 0, N = 0;  // tiles of the sequences before b, of all
@@ -1212,33 +1232,34 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
     if (i < b) before += x;
   }
   N = static_cast<int>(__reduce_add_sync(0xffffffffu, N)) * p.Hkv;
-  before = static_cast<int>(__reduce_add_sync(0xffffffffu, before));
+  if constexpr (!BOUNDARIES) first = static_cast<int>(__reduce_add_sync(0xffffffffu, before)) * p.Hkv + h * T;
   const Share share(N, p.Gr);
-  const int first = before * p.Hkv + h * T;
-  const int c0 = share.cta_of(first), c1 = share.cta_of(first + T - 1);
-  if (c0 == c1) return;  // (one CTA had the whole unit)
-  const int rg = row / R, r = row - rg * R;
-  auto slot = [&](int c) { return (((static_cast<long long>(rg) * p.Gr + c) * 2 + (c == c0 ? 1 : 0)) * R + r); };
-  float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[slot(c)].x);
+  const int c0 = share.cta_of(first), last = share.cta_of(first + T - 1);
+  // one CTA had the whole unit, or an earlier boundary has it
+  if (BOUNDARIES ? c0 + 1 != static_cast<int>(blockIdx.x) / p.RG + 1 : c0 == last) return;
+  auto slot = [&](int c) { return (static_cast<long long>(rg) * p.Gr + c) * 2 + (c == c0 ? 1 : 0); };
+  for (; r < r1; r += kJoinWarps) {
+    float M = -INFINITY;
+    for (int c = c0 + lane; c <= last; c += 32) M = fmaxf(M, p.part_ml[slot(c) * R + r].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float2 ml = p.part_ml[slot(c)];
-    const float4 o = *reinterpret_cast<const float4*>(p.part_o + slot(c) * HD + 4 * lane);
-    const float f = ml.x == M ? 1.f : ex2_approx(ml.x - M);
-    l = fmaf(ml.y, f, l);
-    acc.x = fmaf(o.x, f, acc.x), acc.y = fmaf(o.y, f, acc.y), acc.z = fmaf(o.z, f, acc.z), acc.w = fmaf(o.w, f, acc.w);
+    for (int c = c0; c <= last; ++c) {
+      const float2 ml = p.part_ml[slot(c) * R + r];
+      const float4 o = *reinterpret_cast<const float4*>(p.part_o + (slot(c) * R + r) * HD + 4 * lane);
+      const float f = ml.x == M ? 1.f : ex2_approx(ml.x - M);
+      l = fmaf(ml.y, f, l);
+      acc.x = fmaf(o.x, f, acc.x), acc.y = fmaf(o.y, f, acc.y), acc.z = fmaf(o.z, f, acc.z), acc.w = fmaf(o.w, f, acc.w);
+    }
+    const int row = rg * R + r, node = row / p.g, head = h * p.g + row % p.g;
+    const long long o = (static_cast<long long>(b) * p.m + node) * p.Hq + head;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2*>(p.out + o * HD + 4 * lane) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0 && p.lse != nullptr) p.lse[o] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2f;
   }
-  const int node = row / p.g, head = h * p.g + row % p.g;
-  const long long o = (static_cast<long long>(b) * p.m + node) * p.Hq + head;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(p.out + o * HD + 4 * lane) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (lane == 0 && p.lse != nullptr) p.lse[o] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2f;
 }
 
 // ------------------------------------------------------------------------------------------ host
@@ -1298,8 +1319,11 @@ int launch(const Params& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaSt
   if (e != cudaSuccess) return TS_ERR_CUDA;
   int launches = 1;
   if (p.Gr > 1) {
-    const long long rows = static_cast<long long>(p.B) * p.Hkv * p.rows;
-    e = launch_pdl(join_kernel<R>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, p);
+    const long long rows = static_cast<long long>(p.B) * p.Hkv * p.rows, blocks = (rows + kJoinWarps - 1) / kJoinWarps;
+    const dim3 by(p.RG * (p.Gr - 1), (std::min(R, p.rows) + kJoinRows - 1) / kJoinRows);
+    e = blocks <= static_cast<long long>(by.x) * by.y * (kJoinRows / kJoinWarps)
+            ? launch_pdl(join_kernel<R, false>, dim3(static_cast<unsigned>(blocks)), dim3(32 * kJoinWarps), 0, stream, p)
+            : launch_pdl(join_kernel<R, true>, by, dim3(32 * kJoinWarps), 0, stream, p);
     ++launches;
   }
   count_launches(launches);

@@ -308,3 +308,27 @@ def test_pages_beyond_32_bits(dtype, m):
         results.append((out, lse, kr, vr, *(t[shift:].view(torch.uint8) for t in dev)))
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+@forms
+def test_scores_that_fp32_cannot_tell_apart(form):
+    """Beyond 2^22 (base 2) the tensor cores' rows become NaN; below, and in fp32, they are as exact as their scores."""
+    dtype, m, Hq, Hkv, d, bs, sb = form
+    rng = np.random.default_rng(m + 6)
+    c = Cache(rng, (300, 40), m, Hkv, d, bs, sb)
+    mask = tree_mask(rng, 2, m)
+    seen = set()
+    for e in (17, 20, 22, 30, 60):
+        q = _query(rng, (2, m, Hq, d), dtype) * 2.0 ** e
+        out, lse = _attend(c.device(), c, q, mask)
+        ref, ref_lse, bo, bl = _reference(c, q, mask)
+        high = np.abs(ref_lse) * math.log2(math.e)
+        far = (high > 1.01 * 2 ** 22) & (dtype == torch.bfloat16)
+        near = (high < 0.99 * 2 ** 22) | (dtype == torch.float32)
+        seen |= {bool(x) for x in far.flatten()}
+        assert torch.isnan(lse.cpu()[torch.from_numpy(far)]).all() and torch.isnan(out.cpu()[torch.from_numpy(far)]).all()
+        nan = np.where(near, 0.0, np.nan)                      # (rows in between are not looked at)
+        keep = torch.from_numpy(nan).to(out.device)
+        assert_within(lse + keep, ref_lse + nan, bl, "lse")
+        assert_within(out + keep[..., None], ref + nan[..., None], bo, "out")
+    assert seen == ({True, False} if dtype == torch.bfloat16 else {False})
