@@ -9,6 +9,11 @@
 //
 // What bounds them: a prompt's write reads 2 or 4 bytes and writes one per element, a read the other way round: HBM.
 // The writes of single tokens and trees, and the commit, are latency: table entry -> rows -> maximum -> codes.
+//
+// Measured on the device (GB300, replayed from a graph, 8 heads of 128): a prompt of 4 x 32768 bf16 rows 144 us (5.3 TB/s, 79% of the
+// copy rate; the writes of four short streams, codes and scales of K and V, beside two reads), 60-node trees of 16 sequences 4.4,
+// one token of each of 64 sequences in 64-token blocks 6.6 (it reads its block's kept rows); a read of 2 x 8192 rows into bf16 18
+// (83%), of 16 x 64 into fp32 5.1; a commit of at most 7 rows of 16 sequences 6.1, of 16 rows of 64 sequences in 64-token blocks 10.6.
 #include <algorithm>
 #include <type_traits>
 

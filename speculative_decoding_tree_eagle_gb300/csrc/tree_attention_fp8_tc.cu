@@ -7,13 +7,14 @@
 // V's scale goes into the exponent, so the reference is that of the contributions p * v, not of the weights p alone: what
 // is small against it is small in the output, whatever the scales are.
 //
-// Layout.  The products are transposed, keys (then channels) in the 128 rows of the tensor-core tile and the queries'
-// R rows (16, 32, 64 or 128) in its columns:
+// Layout.  Up to 32 rows ("narrow", R = 16 or 32) the products are transposed, keys (then channels) in the 128 rows of the
+// tensor-core tile and the queries' R rows in its columns:
 //   S^T [128 keys x R]     = K (8 bits, as it lies in the cache) x Q^T
-//   O^T [128 channels x R] += V^T (fp16) x P^T (fp16)
+//   O^T [128 channels x R] += V^T (fp16) x P^T (fp16, from shared memory)
 // A thread of the softmax then has one key (its TMEM lane): its scales are two registers, and a call with few rows computes
 // few columns instead of 128 rows of padding, which is what single tokens and chains need (a 128-key tile's bytes
-// take some 1400 cycles of an SM's share of the HBM, less than the softmax of 128 x 128 scores).
+// take some 1400 cycles of an SM's share of the HBM, less than the softmax of 128 x 128 scores).  Above 32 rows ("wide", R = 128)
+// S [R x 128 keys] = Q x K and O [R x 128 channels] += P x V with P from tensor memory, two threads to a row.
 //   Q   each row is scaled by a power of two of its own to at most 256 and split into e4m3 + e5m2: a bf16 value has eight
 //       significant bits, the nearest e4m3 takes four and leaves a remainder of at most three, which e5m2 holds; what falls
 //       below 2^-25 of the row's largest value is lost.  Two MMAs of kind f8f6f4 (twice fp16's rate) on the
@@ -27,6 +28,12 @@
 // run may begin and end inside a unit.  Units that one CTA has whole are written at once, the parts of the others go
 // to the workspace and join_kernel merges them.  With several row groups CTAs of neighbouring index walk the same tiles
 // for different rows, so all but one read them from L2.
+//
+// Measured (GB300, 32 heads on 8 but for the last, pages of 16 tokens, a scale for 16): 8 single tokens over 1024 to 8192 tokens 27.9 us;
+// 4 x 8 nodes over 32768 66 us (4.1 TB/s, 61% of the copy rate: a tile takes some 2000 cycles, of which its shared-memory traffic
+// is 1350); 4 x 64 nodes over 32768 140 us and 16 x 60 nodes of 64 heads over 4096 169 us (48% and 40% of the bf16 rate: what
+// bounds both is the softmax, 1700 cycles a tile of 128 x 128 scores with its issue slots a third used, then 15000 cycles for a
+// unit's beginning and end).
 //
 // The roles of the warps (struct Cfg) share one instruction cache: code that every tile runs is kept short, and code that runs once per
 // unit is rolled up (unrolled, half of the fetches missed and every warp waited for them).
@@ -442,7 +449,7 @@ struct Cta {
 __device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2f; }
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
-// Columns are rows: a thread has one key (its TMEM lane) and 16 of the R rows; four warps share the rows' references.
+// Columns are rows: a thread has one key (its TMEM lane) and CPT of the R rows; four warps share the rows' references.
 template <int R>
 __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int warp, int lane) {
   using C = Cfg<R>;
@@ -658,11 +665,11 @@ __device__ __forceinline__ uint64_t visible64(int kb, int L, int m, const uint64
   return pre > 0 ? ((1ull << pre) - 1ull) | (bits << pre) : bits;
 }
 
-// Rows are rows: a thread has one row (its TMEM lane) and N of the tile's keys, the threads of the warps four, eight, .. further on the
-// others; all of them keep the row's reference.  P goes to tensor memory.
+// Rows are rows: a thread has one row (its TMEM lane) and N of the tile's keys, the thread of the warp four further on the
+// others; both keep the row's reference.  P goes to tensor memory.
 // COARSE (scale blocks of 16 tokens or more): the scales are those of 16 keys, so they are folded into the row's constants once for
 // 16 scores.  Otherwise each key has its own, and reading them (a broadcast of 16 bytes to a warp takes the shared memory four
-// cycles) is what paces the softmax: 177 against 150 us for 4 x 64 nodes of 32 heads over 32768 tokens.
+// cycles) is what paces the softmax: 177 against 150 us for 4 x 64 nodes of 32 heads over 32768 tokens when it was made.
 template <int R, bool COARSE>
 __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int warp, int lane) {
   using C = Cfg<R>;
@@ -1283,6 +1290,8 @@ int log2_of(int x) {
   return l;
 }
 // R: the smallest tile width that holds all rows, 128 at most.  CTAs: one per SM, of kMinTiles tiles at least.
+// kBegin: what a unit's beginning and end take, in tiles (of 0, 3, 5, 6, 8 and 11: six is best or within 1% of it in all cases; with none
+// chains take 69.2 us for 66.5, 16 x 60 nodes 174 for 170).
 constexpr int kMinTiles = 2, kBegin = 6;
 Plan plan_of(int B, int m, int Hq, int Hkv, int max_prefix, int num_sms) {
   const int rows = m * (Hq / Hkv);
