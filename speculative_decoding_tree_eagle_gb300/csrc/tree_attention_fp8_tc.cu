@@ -125,7 +125,6 @@ struct Params {
   int32_t* status;
   int B, m, Hq, Hkv, g, rows, W, bs, nsb, bs_log2, sb_log2, max_blocks, num_blocks, max_prefix;
   int RG, Gr;       // row groups, CTAs per row group
-  int begin;        // tiles' worth of time that a CTA takes to begin a unit
   float scale_log2;
 };
 
@@ -139,16 +138,33 @@ __device__ __forceinline__ int tiles_of(const Params& p, int b) {
 struct Segment {
   int b, h, t0, t1, T, L;
 };
-// Work is dealt out in tiles' worth of time: a unit takes its tiles and, before them, p.begin for its queries, the pipeline's filling
+// Work is dealt out in tiles' worth of time: a unit takes its tiles and, before them, `begin` for its queries, the pipeline's filling
 // and its result.  (By tiles alone the CTAs that begin a unit on their way end last: 58 against 53 us with 4 x 8 nodes over
-// 32768 tokens, 132 against 124 with 64 nodes.)
-__device__ __forceinline__ int time_of(const Params& p, int b) {
-  const int T = tiles_of(p, b);
-  return T > 0 ? T + p.begin : 0;
+// 32768 tokens, 132 against 124 with 64 nodes.)  kBegin of 0, 3, 5, 6, 8 and 11: six is best or within 1% of it where CTAs have 50 tiles
+// and more (with none chains take 69.2 us for 66.5, 16 x 60 nodes 174 for 170), three with 15 tiles, and where CTAs have few a unit's
+// beginning, which each of them has, need not be counted: a quarter of a CTA's tiles at most.
+constexpr int kBegin = 6;
+struct Time {
+  int begin, total;
+  __device__ __forceinline__ int of(int T) const { return T > 0 ? T + begin : 0; }
+};
+__device__ __forceinline__ Time time_of(const Params& p, int lane) {  // (by one warp)
+  int N = 0, units = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const int T = tiles_of(p, b);
+    N += T;
+    units += T > 0;
+  }
+  N = static_cast<int>(__reduce_add_sync(0xffffffffu, N)) * p.Hkv;
+  units = static_cast<int>(__reduce_add_sync(0xffffffffu, units)) * p.Hkv;
+  Time t;
+  t.begin = min(kBegin, N / (4 * p.Gr));
+  t.total = N + units * t.begin;
+  return t;
 }
 // The segments of the range [x, x1) of that time, from sequence b on; `off` into its unit h.
 struct Walk {
-  int x, x1, b, h, off;
+  int x, x1, b, h, off, begin;
   __device__ __forceinline__ bool next(const Params& p, Segment& s) {
     while (x < x1) {
       int T = tiles_of(p, b);
@@ -156,13 +172,13 @@ struct Walk {
         ++b;
         T = tiles_of(p, b);
       }
-      const int end = min(T + p.begin, off + (x1 - x));
+      const int end = min(T + begin, off + (x1 - x));
       s.b = b, s.h = h, s.T = T, s.L = p.prefix_len[b];
-      s.t0 = max(0, off - p.begin);
-      s.t1 = max(0, end - p.begin);
+      s.t0 = max(0, off - begin);
+      s.t1 = max(0, end - begin);
       x += end - off;
       off = end;
-      if (off == T + p.begin) {
+      if (off == T + begin) {
         off = 0;
         if (++h == p.Hkv) h = 0, ++b;
       }
@@ -185,15 +201,12 @@ struct Share {
 };
 
 // The run of CTA `cta`: all units of a row group in the order of sequences and heads, dealt out (by one warp).
-__device__ __forceinline__ Walk walk_of(const Params& p, int cta, int lane) {
-  int N = 0;
-  for (int b = lane; b < p.B; b += 32) N += time_of(p, b);
-  N = static_cast<int>(__reduce_add_sync(0xffffffffu, N)) * p.Hkv;
-  const Share share(N, p.Gr);
-  Walk w{share.start(cta), share.start(cta + 1), 0, 0, 0};
+__device__ __forceinline__ Walk walk_of(const Params& p, const Time& time, int cta, int lane) {
+  const Share share(time.total, p.Gr);
+  Walk w{share.start(cta), share.start(cta + 1), 0, 0, 0, time.begin};
   int before = 0;
   for (int b0 = 0; b0 < p.B && w.x < w.x1; b0 += 32) {
-    const int T = b0 + lane < p.B ? time_of(p, b0 + lane) : 0;
+    const int T = b0 + lane < p.B ? time.of(tiles_of(p, b0 + lane)) : 0;
     int sum = T * p.Hkv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -944,7 +957,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   }
   pdl_wait();
   if (warp == 0) {
-    const Walk w = walk_of(p, cta, lane);
+    const Walk w = walk_of(p, time_of(p, lane), cta, lane);
     if (lane == 0) *s_walk = w;
     if (blockIdx.x == 0)
       for (int b = lane; b < p.B; b += 32)
@@ -1226,13 +1239,14 @@ template <int R, bool BOUNDARIES>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Params p) {
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Time time = time_of(p, lane);
   int b, h, rg, r, r1, first;  // unit, row group, rows r, r + kJoinWarps, .. below r1 of it; the place of its first tile
   if constexpr (BOUNDARIES) {
     rg = blockIdx.x % p.RG;
     // (every warp finds the place by itself: no barrier)
-    const Walk w = walk_of(p, blockIdx.x / p.RG + 1, lane);
-    if (w.x >= w.x1 || w.off <= p.begin) return;  // nothing from here on, or a unit begins here
-    b = w.b, h = w.h, first = w.x - w.off + p.begin;
+    const Walk w = walk_of(p, time, blockIdx.x / p.RG + 1, lane);
+    if (w.x >= w.x1 || w.off <= time.begin) return;  // nothing from here on, or a unit begins here
+    b = w.b, h = w.h, first = w.x - w.off + time.begin;
     r = blockIdx.y * kJoinRows + warp;
     r1 = min(min(R, p.rows - rg * R), static_cast<int>(blockIdx.y + 1) * kJoinRows);
   } else {
@@ -1243,15 +1257,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   }
   const int T = tiles_of(p, b);
   if (T == 0) return;
-  int before = 0, N = 0;  // time of the sequences before b, of all
-  for (int i = lane; i < p.B; i += 32) {
-    const int x = time_of(p, i);
-    N += x;
-    if (i < b) before += x;
+  if constexpr (!BOUNDARIES) {
+    int before = 0;  // time of the sequences before b
+    for (int i = lane; i < b; i += 32) before += time.of(tiles_of(p, i));
+    first = static_cast<int>(__reduce_add_sync(0xffffffffu, before)) * p.Hkv + h * (T + time.begin) + time.begin;
   }
-  N = static_cast<int>(__reduce_add_sync(0xffffffffu, N)) * p.Hkv;
-  if constexpr (!BOUNDARIES) first = static_cast<int>(__reduce_add_sync(0xffffffffu, before)) * p.Hkv + h * (T + p.begin) + p.begin;
-  const Share share(N, p.Gr);
+  const Share share(time.total, p.Gr);
   const int c0 = share.cta_of(first), last = share.cta_of(first + T - 1);
   // one CTA had the whole unit, or an earlier boundary has it
   if (BOUNDARIES ? c0 + 1 != static_cast<int>(blockIdx.x) / p.RG + 1 : c0 == last) return;
@@ -1290,9 +1301,7 @@ int log2_of(int x) {
   return l;
 }
 // R: the smallest tile width that holds all rows, 128 at most.  CTAs: one per SM, of kMinTiles tiles at least.
-// kBegin: what a unit's beginning and end take, in tiles (of 0, 3, 5, 6, 8 and 11: six is best or within 1% of it in all cases; with none
-// chains take 69.2 us for 66.5, 16 x 60 nodes 174 for 170).
-constexpr int kMinTiles = 2, kBegin = 6;
+constexpr int kMinTiles = 2;
 Plan plan_of(int B, int m, int Hq, int Hkv, int max_prefix, int num_sms) {
   const int rows = m * (Hq / Hkv);
   Plan pl;
@@ -1379,7 +1388,7 @@ int attention_fp8_tc_launch(const Fp8AttnCall& a, cudaStream_t stream, int num_s
   // (a page of a power of two tokens is cut into powers of two: shifts, as a division takes one warp hundreds of cycles)
   p.bs_log2 = log2_of(a.block_size), p.sb_log2 = log2_of(a.scale_block);
   p.max_blocks = a.max_blocks, p.num_blocks = a.num_blocks, p.max_prefix = a.max_prefix;
-  p.RG = pl.RG, p.Gr = pl.Gr, p.begin = kBegin;
+  p.RG = pl.RG, p.Gr = pl.Gr;
   p.scale_log2 = a.scale * kLog2e;
   CUtensorMap mk, mv;
   if (!encode_map(&mk, a.k_cache, a.num_blocks, a.Hkv, a.block_size) || !encode_map(&mv, a.v_cache, a.num_blocks, a.Hkv, a.block_size))

@@ -332,3 +332,29 @@ def test_scores_that_fp32_cannot_tell_apart(form):
         assert_within(lse + keep, ref_lse + nan, bl, "lse")
         assert_within(out + keep[..., None], ref + nan[..., None], bo, "out")
     assert seen == ({True, False} if dtype == torch.bfloat16 else {False})
+
+
+@forms
+def test_no_sequence_can_be_read(form):
+    dtype, m, Hq, Hkv, d, bs, sb = form
+    rng = np.random.default_rng(m + 7)
+    c = Cache(rng, (90, 5), m, Hkv, d, bs, sb)
+    mask, q, dev = tree_mask(rng, 2, m), _query(rng, (2, m, Hq, d), dtype), c.device()
+    c.lens[:] = -1, 2 ** 31 - 1
+    out = torch.full(q.shape, 7.0, dtype=dtype, device="cuda")
+    _attend(dev, c, q, mask, top=4000, ok=False, out=out)
+    assert (out == 7).all()
+
+
+@forms
+def test_few_and_many_tiles_of_every_length(form):
+    """Shares of a fraction of a tile to several units for a CTA, sequences of one tile between longer ones."""
+    dtype, m, Hq, Hkv, d, bs, sb = form
+    for lens in ((0,), (700,), (3000,), (0, 0, 900), (1, 130, 0, 2000, 5), tuple(range(0, 40)), (0, 500) * 20):
+        rng = np.random.default_rng(len(lens))
+        c = Cache(rng, lens, m, Hkv, d, bs, sb)
+        mask, q = tree_mask(rng, len(lens), m), _query(rng, (len(lens), m, Hq, d), dtype)
+        out, lse = _attend(c.device(), c, q, mask)
+        ref, ref_lse, bo, bl = _reference(c, q, mask)
+        assert_within(lse, ref_lse, bl, "lse")
+        assert_within(out, ref, bo, "out")
