@@ -10,9 +10,9 @@
 // What bounds them: a prompt's write reads 2 or 4 bytes and writes one per element, a read the other way round: HBM.
 // The writes of single tokens and trees, and the commit, are latency: table entry -> rows -> maximum -> codes.
 //
-// Measured on the device (GB300, replayed from a graph, 8 heads of 128): a prompt of 4 x 32768 bf16 rows 144 us (5.3 TB/s, 79% of the
-// copy rate; the writes of four short streams, codes and scales of K and V, beside two reads), 60-node trees of 16 sequences 4.4,
-// one token of each of 64 sequences in 64-token blocks 6.6 (it reads its block's kept rows); a read of 2 x 8192 rows into bf16 18
+// Measured on the device (GB300, replayed from a graph, 8 heads of 128): a prompt of 4 x 32768 bf16 rows 122 us (6.3 TB/s, 94% of the
+// copy rate), of 2 x 32768 fp32 rows 101 (96%), 60-node trees of 16 sequences 4.1,
+// one token of each of 64 sequences in 64-token blocks 5.1 (it reads its block's kept rows); a read of 2 x 8192 rows into bf16 18
 // (83%), of 16 x 64 into fp32 5.1; a commit of at most 7 rows of 16 sequences 6.1, of 16 rows of 64 sequences in 64-token blocks 10.6.
 #include <algorithm>
 #include <type_traits>
@@ -23,9 +23,32 @@
 namespace ts {
 namespace {
 
-constexpr int kWriteThreads = 256;
+// Threads of a CTA whose items have W warps each, and CTAs per SM that its registers are to leave room for.  More CTAs of fewer
+// threads keep more reads in flight while others wait for their maximum: a prompt of 4 x 32768 bf16 rows took 144 us with 256
+// threads and what registers the compiler liked (75), 140 with 128, 127 with eight such CTAs (64 registers), 130 with seven or nine
+// (and 122 with multiplications in place of the item's five divisions).
+__host__ __device__ constexpr int write_threads(int W) { return W > 4 ? 32 * W : 128; }
+template <typename T>
+__host__ __device__ constexpr int write_ctas(int W) { return (sizeof(T) == 2 ? 1024 : 640) / write_threads(W); }
+constexpr int kAnyThreads = 256;
 constexpr int kChunk = 8;     // elements that a thread loads at once (16 bytes of bf16, 8 codes)
 constexpr int kHeld = 8;      // chunks that a thread holds between the maximum and the codes
+
+// x / d for 0 <= x < 2^31 as a multiplication: with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1 the quotient is
+// (x m / 2^32 + x) / 2^s.  (Six divisions a thread took a third of a read's instructions, five a warp
+// more than the rest of a write with four tokens to a scale.)
+struct Divide {
+  uint32_t m, s, d;
+  Divide() = default;
+  explicit Divide(int by) : d(static_cast<uint32_t>(by)) {
+    s = 0;
+    while ((1ull << s) < d) ++s;
+    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int quotient(int x) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(x), m) + static_cast<uint32_t>(x)) >> s);
+  }
+};
 
 struct Side {                 // K or V
   const void* src;            // [B, n, Hkv, d], element strides below
@@ -39,7 +62,8 @@ struct WriteParams {
   const int32_t* start_len;
   const int32_t* length;
   int32_t* status;
-  int B, n, Hkv, d, bs, sb, max_blocks, num_blocks, blocks;  // blocks: that n rows can touch
+  int B, n, Hkv, d, bs, sb, nsb, max_blocks, num_blocks, blocks;  // blocks: that n rows can touch
+  Divide by_head, by_page, by_block;
 };
 
 // One (K or V, sequence, block, head) of a write.
@@ -63,9 +87,9 @@ __device__ __forceinline__ Item item_of(const WriteParams& p, const Side& side, 
     if (i == 0) report(p.status, TS_ERR_DEVICE_CHECK);
     return it;
   }
-  const long long first_at = static_cast<long long>(start / p.sb + i) * p.sb;
+  const long long first_at = static_cast<long long>(p.by_block.quotient(start) + i) * p.sb;
   if (len == 0 || first_at >= end) return it;
-  const int first = static_cast<int>(first_at), lp = first / p.bs;
+  const int first = static_cast<int>(first_at), lp = p.by_page.quotient(first);
   const int page = p.table[static_cast<long long>(b) * p.max_blocks + lp];
   if (page < 0 || page >= p.num_blocks) {
     report(p.status, TS_ERR_DEVICE_CHECK);
@@ -78,7 +102,7 @@ __device__ __forceinline__ Item item_of(const WriteParams& p, const Side& side, 
   const int row = first - lp * p.bs;
   const long long head = static_cast<long long>(page) * p.Hkv + h;
   it.codes = side.cache + (head * p.bs + row) * p.d;
-  it.scale = side.scale + head * (p.bs / p.sb) + row / p.sb;
+  it.scale = side.scale + head * p.nsb + p.by_block.quotient(row);
   it.src = static_cast<const char*>(side.src) + (static_cast<long long>(b) * side.sb_ + static_cast<long long>(first - start) * side.sn +
                                                  static_cast<long long>(h) * side.sh) * static_cast<long long>(sizeof(T));
   return it;
@@ -142,13 +166,14 @@ __device__ __forceinline__ float largest_code(uint2 c) {  // (NaN passed over)
 // divides their number), so a thread stays in its columns and no load costs a division.  Where the block fits in kHeld chunks per
 // thread the rows stay in registers between the maximum and the codes, otherwise they are read twice.
 template <typename T, int W, bool HOLD>
-__global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_constant__ WriteParams p) {
-  __shared__ float s_max[kWriteThreads / 32];
+__global__ void __launch_bounds__(write_threads(W), write_ctas<T>(W)) write_kernel(const __grid_constant__ WriteParams p) {
+  constexpr int kItems = write_threads(W) / (32 * W);  // of a CTA
+  __shared__ float s_max[kItems * W];
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp / W, part = (warp % W) * 32 + lane;  // item of this CTA, thread of the item
   const Side& side = p.side[blockIdx.z];
-  const int x = blockIdx.x * (kWriteThreads / (32 * W)) + sub, block = x / p.Hkv;
+  const int x = blockIdx.x * kItems + sub, block = p.by_head.quotient(x);
   const Item it = item_of<T>(p, side, blockIdx.y, block, x - block * p.Hkv);
   if (W == 1 && !it.live) return;
   const int per_row = p.d / kChunk, step = 32 * W / per_row, r0 = part / per_row, col = (part - r0 * per_row) * kChunk;
@@ -223,10 +248,96 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const __grid_const
 __device__ __forceinline__ float element(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float element(const float* p) { return *p; }
 
+// Blocks smaller than what a warp holds (kHeld chunks per thread: `run` rows): a warp takes a run of positions with all their blocks, so
+// its loads are as many as for larger blocks.  Thread and rows as in write_kernel; a block is either some of a thread's chunks and all
+// threads, or one chunk of some neighbouring threads.  (A warp per block: 4 x 32768 bf16 rows with four tokens
+// to a scale 276 us, 164 by runs; 2 x 32768 with a scale for each 497 and 101.  Seven CTAs to an SM, 72 registers: with eight it spills,
+// 185 us.)
+template <typename T>
+__global__ void __launch_bounds__(write_threads(1), sizeof(T) == 2 ? 7 : 4) write_runs_kernel(const __grid_constant__ WriteParams p) {
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
+  const Side& side = p.side[blockIdx.z];
+  const int x = blockIdx.x * (write_threads(1) / 32) + warp, i = p.by_head.quotient(x), h = x - i * p.Hkv;
+  const int per_row = p.d / kChunk, step = 32 / per_row, run = kHeld * step, r0 = lane / per_row, col = (lane - r0 * per_row) * kChunk;
+  if (i >= p.blocks) return;
+  const int start = p.start_len[b], len = p.length != nullptr ? p.length[b] : p.n;
+  const long long end = static_cast<long long>(start) + len;
+  if (start < 0 || len < 0 || len > p.n || end > min(static_cast<long long>(p.max_blocks) * p.bs, static_cast<long long>(INT32_MAX))) {
+    if (i == 0) report(p.status, TS_ERR_DEVICE_CHECK);
+    return;
+  }
+  const long long first_at = static_cast<long long>(start / run + i) * run;
+  if (len == 0 || first_at >= end) return;
+  const int first = static_cast<int>(first_at), lp = p.by_page.quotient(first);
+  const int page = p.table[static_cast<long long>(b) * p.max_blocks + lp];
+  if (page < 0 || page >= p.num_blocks) {
+    report(p.status, TS_ERR_DEVICE_CHECK);
+    return;
+  }
+  // rows [low, kept) are kept ones of the block that `start` lies in, [kept, top) are new
+  const int low = max(0, p.by_block.quotient(start) * p.sb - first), kept = max(0, start - first);
+  const int top = static_cast<int>(min(static_cast<long long>(run), end - first));
+  const int at = first - lp * p.bs;
+  const long long head = static_cast<long long>(page) * p.Hkv + h;
+  uint8_t* codes = side.cache + (head * p.bs + at + r0) * p.d + col;
+  float* scale = side.scale + head * p.nsb + p.by_block.quotient(at);
+  const char* src = static_cast<const char*>(side.src) +
+                    (static_cast<long long>(b) * side.sb_ + static_cast<long long>(first - start + r0) * side.sn +
+                     static_cast<long long>(h) * side.sh + col) * static_cast<long long>(sizeof(T));
+  const long long src_step = static_cast<long long>(step) * side.sn * static_cast<long long>(sizeof(T));
+  const int codes_step = step * p.d;
+  const float old = kept > low ? scale_in_range(scale[p.by_block.quotient(low)]) : 1.f;
+  Held<T> held[kHeld];
+  float m[kHeld];
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) {
+    const int r = r0 + u * step;
+    if (r >= kept && r < top) held[u].load(src + u * src_step);
+    else if (r >= low && r < top) held[u].keep(*reinterpret_cast<const uint2*>(codes + u * codes_step));
+  }
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) {
+    const int r = r0 + u * step;
+    m[u] = r >= kept && r < top ? held[u].largest() : r >= low && r < top ? largest_code(held[u].kept()) * old : 0.f;
+  }
+  // the largest of each block: among a thread's chunks, then among threads (magnitudes order as their bits do)
+#pragma unroll
+  for (int o = 1; o < kHeld; o <<= 1) {
+    if (o * step < p.sb) {
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        if ((u & o) == 0) m[u] = m[u + o] = fmaxf(m[u], m[u + o]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) {
+    if (p.sb >= step) {
+      m[u] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m[u])));
+    } else {
+      for (int o = per_row * p.sb / 2; o > 0; o >>= 1) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) {
+    const int r = r0 + u * step;
+    if (r < low || r >= top) continue;
+    const int e = scale_exponent(m[u]);
+    const float inv = pow2(-e), again = old * inv;  // from kept codes to codes
+    if (r >= kept || again != 1.f) {
+      float v[8];
+      if (r < kept) decode8(held[u].kept(), v);
+      else held[u].values(v);
+      *reinterpret_cast<uint2*>(codes + u * codes_step) = encode8(v, r < kept ? again : inv);
+    }
+    if (col == 0 && (r & (p.sb - 1)) == 0) scale[p.by_block.quotient(r)] = pow2(e);
+  }
+}
+
 // Any head dim, strides and alignment: a CTA per item, element by element, the rows read twice.
 template <typename T>
-__global__ void __launch_bounds__(kWriteThreads) write_any_kernel(const __grid_constant__ WriteParams p) {
-  __shared__ float s_max[kWriteThreads / 32];
+__global__ void __launch_bounds__(kAnyThreads) write_any_kernel(const __grid_constant__ WriteParams p) {
+  __shared__ float s_max[kAnyThreads / 32];
   pdl_wait();
   const Side& side = p.side[blockIdx.z];
   const int block = blockIdx.x / p.Hkv;
@@ -242,7 +353,7 @@ __global__ void __launch_bounds__(kWriteThreads) write_any_kernel(const __grid_c
   };
   float amax = 0.f;
   bool kept;
-  for (int x = threadIdx.x; x < total; x += kWriteThreads) {
+  for (int x = threadIdx.x; x < total; x += kAnyThreads) {
     const float v = fabsf(value(x, kept));
     amax = fmaxf(amax, kept ? v * old : v);
   }
@@ -250,10 +361,10 @@ __global__ void __launch_bounds__(kWriteThreads) write_any_kernel(const __grid_c
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWriteThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
+  for (int w = 0; w < kAnyThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
   const int e = scale_exponent(amax);
   const float inv = pow2(-e);
-  for (int x = threadIdx.x; x < total; x += kWriteThreads) {
+  for (int x = threadIdx.x; x < total; x += kAnyThreads) {
     const float v = value(x, kept);
     it.codes[x] = static_cast<uint8_t>(encode_e4m3x2(kept ? v * (old * inv) : v * inv, 0.f) & 0xFFu);
   }
@@ -262,21 +373,6 @@ __global__ void __launch_bounds__(kWriteThreads) write_any_kernel(const __grid_c
 
 // ---------------------------------------------------------------------------------------------- read
 constexpr int kReadThreads = 256;
-
-// x / d for 0 <= x < 2^31 as a multiplication: with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1 the quotient is
-// (x m / 2^32 + x) / 2^s.  (Six divisions a thread took a third of a read's instructions.)
-struct Divide {
-  uint32_t m, s, d;
-  Divide() = default;
-  explicit Divide(int by) : d(static_cast<uint32_t>(by)) {
-    s = 0;
-    while ((1ull << s) < d) ++s;
-    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
-  }
-  __device__ __forceinline__ int quotient(int x) const {
-    return static_cast<int>((__umulhi(static_cast<uint32_t>(x), m) + static_cast<uint32_t>(x)) >> s);
-  }
-};
 
 struct ReadParams {
   const uint8_t* cache[2];
@@ -553,17 +649,32 @@ __global__ void __launch_bounds__(kCommitThreads) commit_table_kernel(const __gr
   commit_tables(p, blockIdx.x, c, s_page);
 }
 
+// Blocks (of K and V) from which a warp takes a run of them: below, a call is latency, which a warp per block spreads (with four
+// tokens to a scale one token of 64 sequences 3.6 us for 4.4, trees of 60 nodes of 16 4.6 for 5.5).  Half a run to a block is
+// faster by blocks too (165 for 185 us).
+constexpr long long kManyBlocks = 32768;
+
 template <typename T>
 cudaError_t launch_write(const WriteParams& p, bool wide, cudaStream_t stream) {
   const int chunks = (p.sb * p.d + kChunk - 1) / kChunk, held = 32 * kHeld, items = p.blocks * p.Hkv;
-  auto grid = [&](int w) { return dim3((items + kWriteThreads / (32 * w) - 1) / (kWriteThreads / (32 * w)), p.B, 2); };
-  const dim3 block(kWriteThreads);
-  if (!wide) return launch_pdl(write_any_kernel<T>, dim3(items, p.B, 2), block, 0, stream, p);
-  if (chunks <= held) return launch_pdl(write_kernel<T, 1, true>, grid(1), block, 0, stream, p);
-  if (chunks <= 2 * held) return launch_pdl(write_kernel<T, 2, true>, grid(2), block, 0, stream, p);
-  if (chunks <= 4 * held) return launch_pdl(write_kernel<T, 4, true>, grid(4), block, 0, stream, p);
-  if (chunks <= 8 * held) return launch_pdl(write_kernel<T, 8, true>, grid(8), block, 0, stream, p);
-  return launch_pdl(write_kernel<T, 8, false>, grid(8), block, 0, stream, p);
+  if (!wide) return launch_pdl(write_any_kernel<T>, dim3(items, p.B, 2), dim3(kAnyThreads), 0, stream, p);
+  auto launch = [&](auto kernel, int w) {
+    const int each = write_threads(w) / (32 * w);
+    return launch_pdl(kernel, dim3((items + each - 1) / each, p.B, 2), dim3(write_threads(w)), 0, stream, p);
+  };
+  // (d is a power of two here, a run one too, and what divides it)
+  const int run = held * kChunk / p.d;
+  if (2 * p.sb < run && run % p.sb == 0 && p.bs % run == 0 && 2LL * items * p.B >= kManyBlocks) {
+    WriteParams q = p;
+    q.blocks = static_cast<int>((static_cast<long long>(p.n) + 2LL * run - 2) / run);  // (runs, here)
+    const int each = write_threads(1) / 32;
+    return launch_pdl(write_runs_kernel<T>, dim3((q.blocks * q.Hkv + each - 1) / each, q.B, 2), dim3(write_threads(1)), 0, stream, q);
+  }
+  if (chunks <= held) return launch(write_kernel<T, 1, true>, 1);
+  if (chunks <= 2 * held) return launch(write_kernel<T, 2, true>, 2);
+  if (chunks <= 4 * held) return launch(write_kernel<T, 4, true>, 4);
+  if (chunks <= 8 * held) return launch(write_kernel<T, 8, true>, 8);
+  return launch(write_kernel<T, 8, false>, 8);
 }
 
 }  // namespace
@@ -577,9 +688,10 @@ int kv_write_fp8_launch(const Fp8WriteCall& c, cudaStream_t stream) {
   p.length = c.length;
   p.status = c.dev_status;
   p.B = c.B, p.n = c.n, p.Hkv = c.Hkv, p.d = c.d, p.bs = c.block_size, p.sb = c.scale_block;
-  p.max_blocks = c.max_blocks, p.num_blocks = c.num_blocks;
+  p.nsb = c.block_size / c.scale_block, p.max_blocks = c.max_blocks, p.num_blocks = c.num_blocks;
+  p.by_head = Divide(c.Hkv), p.by_page = Divide(c.block_size), p.by_block = Divide(c.scale_block);
   p.blocks = static_cast<int>((static_cast<long long>(c.n) + 2LL * c.scale_block - 2) / c.scale_block);
-  if (static_cast<long long>(p.blocks) * c.Hkv > INT32_MAX) return TS_ERR_UNSUPPORTED;
+  if (static_cast<long long>(p.blocks) * c.Hkv > INT32_MAX - 8) return TS_ERR_UNSUPPORTED;
   const size_t size = c.dt == TS_BF16 ? 2 : 4;
   bool wide = c.d % kChunk == 0 && 32 % (c.d / kChunk) == 0;  // (a head dim of 8, 16, 32, 64, 128 or 256)
   for (const Side& s : p.side) {

@@ -270,3 +270,50 @@ def test_refusals():
     with pytest.raises(ts.TreeSpecError, match="INVALID"):
         ts.kv_read_fp8(*dev, table, start, 4, out=(k, k))
     c.assert_equal(dev)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,bs,sb,Hkv", [(128, 16, 1, 2), (128, 16, 2, 1), (128, 32, 4, 3), (128, 64, 8, 2), (64, 32, 1, 2), (64, 64, 16, 1), (64, 16, 4, 2),
+                                         (256, 16, 2, 2), (256, 8, 1, 1), (32, 128, 2, 2), (32, 64, 8, 1), (16, 128, 32, 1), (8, 256, 4, 1)])
+def test_write_of_small_blocks(dtype, d, bs, sb, Hkv):
+    """Blocks of which a warp takes several, at every place of a page."""
+    rng = np.random.default_rng(d * bs + sb)
+    start = [0, 1, bs - 1, bs, bs // 2 + 3, 2 * bs + sb, 5, 2 * bs - sb]
+    length = [2 * bs, 1, 2, bs + 1, 0, 3, sb, 2 * sb]
+    n = max(length)
+    c = Cache(rng, start, n, Hkv, d, bs, sb)
+    status = ts.new_status()
+    k, v = _rows(rng, (8, n, Hkv, d), dtype), _rows(rng, (8, n, Hkv, d), dtype)
+    k[0, ::3], v[0, 1::5] = 0.0, float("nan")
+    k[3, :, 0] *= 2.0 ** 20
+    _write_both(c, k, v, start, length, status)
+    ts.check_status(status)
+
+
+@pytest.mark.parametrize("dtype,d,bs,sb,Hkv", [(torch.bfloat16, 128, 16, 1, 4), (torch.bfloat16, 64, 64, 2, 4), (torch.bfloat16, 256, 16, 2, 4),
+                                               (torch.float32, 128, 32, 4, 2), (torch.float32, 32, 64, 1, 4)])
+def test_write_of_many_small_blocks(dtype, d, bs, sb, Hkv):
+    """As many blocks as a warp takes a run of: prompts behind prefixes that end anywhere."""
+    rng = np.random.default_rng(d + bs + sb)
+    start = [0, 1, 3 * bs - 1, bs + bs // 2 + 1]
+    n = -(-32768 * sb // (8 * Hkv)) + 3
+    length = [n, n - 1, n - bs - 2, n]
+    c = Cache(rng, start, n, Hkv, d, bs, sb)
+    status = ts.new_status()
+    k, v = _rows(rng, (4, n, Hkv, d), dtype), _rows(rng, (4, n, Hkv, d), dtype)
+    k[0, ::3], v[0, 1::5] = 0.0, float("nan")
+    _write_both(c, k, v, start, length, status)
+    ts.check_status(status)
+    # one sequence too long, and one page out of range: the others are written
+    c2 = Cache(rng, start, n, Hkv, d, bs, sb)
+    c2.table[1, 2] = -1
+    dev, before = c2.device(), [t.view(torch.uint8).clone() for t in c2.device()]
+    starts = list(start)
+    starts[2] = c2.table.shape[1] * bs - n + 1
+    ts.kv_write_fp8(k.cuda(), v.cuda(), *dev, ints(c2.table), ints(starts), status=status)
+    with pytest.raises(ts.TreeSpecError, match="DEVICE_CHECK"):
+        ts.check_status(status)
+    for t, old in zip(dev, before):
+        pages = c2.table[2][c2.table[2] >= 0]
+        assert torch.equal(t.view(torch.uint8)[pages], old[pages])              # as they were
+        assert not torch.equal(t.view(torch.uint8)[c2.table[0, :2]], old[c2.table[0, :2]])
