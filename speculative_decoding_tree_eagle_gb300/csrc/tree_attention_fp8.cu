@@ -4,13 +4,14 @@
 // Mathematics: rows are (node, head of the KV head's group); per row the running maximum M and sum l of the softmax in
 // the log2 domain over tiles of 64 keys, in fp32 throughout:
 //   x_j = q . (code_j * ks_j) * scale * log2 e,   l = sum 2^(x_j - M),   O = sum 2^(x_j - M) * code_j * vs_j
-// A tile's codes are decoded once into fp32 in shared memory and serve up to 32 rows, which is what the split is for:
+// A tile's codes are decoded once into fp32 in shared memory and serve up to 32 rows (64 where d <= 64), which is what the split is for:
 // decoding costs more than the products of one row.  A thread of the 16 x 16 holds RPT rows x 4 keys of scores and RPT
 // rows x 4 columns (per 64 of the head dim) of the output.  Long prefixes are cut into chunks, one CTA each, whose
 // partial results a second kernel joins.
 // Bound by the CUDA cores' issue slots and by shared memory (every product reads its operands there).
-// Measured (GB300): fp32, 2 sequences of up to 700 tokens, 8 nodes, 8 heads on 2, d = 64: 19.6 us, the latency of one tile a chunk and of
-// the join.
+// Measured (GB300): fp32, 2 sequences of up to 700 tokens, 8 nodes, 8 heads on 2, d = 64: 16.4 us, the latency of one tile a chunk and of
+// the join.  8 sequences of 4096 tokens, 8 heads on 2: 32 nodes at d = 64 119 us, one at d = 128 58 (its tiles take the shared memory
+// 9000 cycles each, two thirds of the time, for four rows as for sixteen).
 #include <algorithm>
 
 #include "fp8_cache.cuh"
@@ -58,41 +59,27 @@ __device__ __forceinline__ bool usable(const Params& p, int L) {
   return L >= 0 && L <= p.max_prefix && static_cast<long long>(L) + p.m <= static_cast<long long>(p.max_blocks) * p.bs;
 }
 
-// Values of positions key0 .. key0 + 63 of one tensor -> s[64][pitch] (zeros behind `nkeys`, in pages without an id and in the
-// columns from d to dp).
-__device__ void stage(const Params& p, const uint8_t* cache, const float* scale, float* s, int pitch, int key0, int nkeys,
-                      int h, const int* s_page) {
-  const int nsb = p.bs / p.sb;
-  if (p.wide) {
-    const int per = p.d / 16;
-    for (int x = threadIdx.x; x < kKeys * per; x += kThreads) {
-      const int j = x / per, c = (x - j * per) * 16, pos = key0 + j, page = s_page[j];
-      uint4 w = make_uint4(0, 0, 0, 0);
-      float f = 0.f;
-      if (pos < nkeys && page >= 0) {
-        const int row = pos % p.bs;
-        const long long head = static_cast<long long>(page) * p.Hkv + h;
-        w = *reinterpret_cast<const uint4*>(cache + (head * p.bs + row) * p.d + c);
-        f = scale_in_range(scale[head * nsb + row / p.sb]);
-      }
-      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+// What a tile's keys are: whether there is one, its place in the cache (in rows) and its scales.
+struct Keys {
+  int page[kKeys];  // -1: behind the end, or in a page without an id
+  long long at[kKeys];
+  float ks[kKeys], vs[kKeys];
+};
+
+// Sixteen codes times f -> s (16-byte aligned).
+__device__ __forceinline__ void put16(float* s, const uint4& w, float f) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float2 lo = decode_e4m3x2(in[u]), hi = decode_e4m3x2(in[u] >> 16);
-        *reinterpret_cast<float4*>(s + j * pitch + c + 4 * u) = make_float4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
-      }
-    }
-  } else {
-    for (int x = threadIdx.x; x < kKeys * p.dp; x += kThreads) {
-      const int j = x / p.dp, c = x - j * p.dp, pos = key0 + j, page = s_page[j];
-      float v = 0.f;
-      if (pos < nkeys && page >= 0 && c < p.d) {
-        const int row = pos % p.bs;
-        const long long head = static_cast<long long>(page) * p.Hkv + h;
-        v = decode_e4m3(cache[(head * p.bs + row) * p.d + c]) * scale_in_range(scale[head * nsb + row / p.sb]);
-      }
-      s[j * pitch + c] = v;
-    }
+  for (int u = 0; u < 4; ++u) {
+    const float2 lo = decode_e4m3x2(in[u]), hi = decode_e4m3x2(in[u] >> 16);
+    *reinterpret_cast<float4*>(s + 4 * u) = make_float4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
+  }
+}
+// The tile's values of one tensor -> s[64][pitch], code by code (zeros where there is no key and in the columns from d to dp).
+__device__ void stage(const Params& p, const uint8_t* cache, const Keys& k, const float* scale, float* s, int pitch) {
+  for (int x = threadIdx.x; x < kKeys * p.dp; x += kThreads) {
+    const int j = x / p.dp, c = x - j * p.dp;
+    s[j * pitch + c] = k.page[j] >= 0 && c < p.d ? decode_e4m3(cache[k.at[j] * p.d + c]) * scale[j] : 0.f;
   }
 }
 
@@ -106,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
   float* sk = sq + ROWS * p.dp;            // [64][dp + 4]
   float* sv = sk + kKeys * kp;             // [64][dp]
   float* sp = sv + kKeys * p.dp;           // [ROWS][64]
-  __shared__ int s_page[kKeys];
+  __shared__ Keys s_keys[2];
   pdl_wait();
   const int b = blockIdx.z, h = blockIdx.y / p.row_tiles, R0 = (blockIdx.y % p.row_tiles) * ROWS, chunk = blockIdx.x;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -139,25 +126,81 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
 #pragma unroll
     for (int c = 0; c < CG; ++c) acc[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  // The first 64 threads look the keys up, a page's id three tiles ahead, its scales two; all of them ask for the codes of the next
+  // tile while they compute this one.
+  const int nsb = p.bs / p.sb;
+  auto id_of = [&](int t) {
+    const int pos = t * kKeys + static_cast<int>(threadIdx.x);
+    return t < t1 && pos < nkeys ? max(-1, p.table[static_cast<long long>(b) * p.max_blocks + pos / p.bs]) : -2;
+  };
+  int id = -2, page = -1;  // of the tile after next; of the next
+  long long at = 0;
+  float ks = 0.f, vs = 0.f;
+  auto look = [&](int t) {  // (id: that of tile t)
+    page = -1, at = 0, ks = vs = 0.f;
+    if (id == -2) return;
+    if (id < 0 || id >= p.num_blocks) {
+      report(p.status, TS_ERR_DEVICE_CHECK);
+      return;
+    }
+    const int row = (t * kKeys + static_cast<int>(threadIdx.x)) % p.bs;
+    const long long head = static_cast<long long>(id) * p.Hkv + h, block = head * nsb + row / p.sb;
+    page = id, at = head * p.bs + row, ks = scale_in_range(p.ks[block]), vs = scale_in_range(p.vs[block]);
+  };
+  auto keep = [&](int t) {
+    Keys& k = s_keys[t & 1];
+    k.page[threadIdx.x] = page, k.at[threadIdx.x] = at, k.ks[threadIdx.x] = ks, k.vs[threadIdx.x] = vs;
+  };
+  const bool finder = threadIdx.x < kKeys;
+  const int per = p.d / 16;
+  uint4 kc[CG], vc[CG];
+  auto ask = [&](int t) {
+    const Keys& k = s_keys[t & 1];
+#pragma unroll
+    for (int i = 0; i < CG; ++i) {
+      const int x = threadIdx.x + kThreads * i, j = x / per;
+      kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
+      if (j < kKeys && k.page[j] >= 0) {
+        const long long o = k.at[j] * p.d + (x - j * per) * 16;
+        kc[i] = *reinterpret_cast<const uint4*>(p.kc + o);
+        vc[i] = *reinterpret_cast<const uint4*>(p.vc + o);
+      }
+    }
+  };
+  if (finder) {
+    id = id_of(t0);
+    look(t0);
+    keep(t0);
+    id = id_of(t0 + 1);
+    look(t0 + 1);
+    id = id_of(t0 + 2);
+  }
+  __syncthreads();
+  if (p.wide) ask(t0);
   for (int t = t0; t < t1; ++t) {
     const int key0 = t * kKeys;
-    __syncthreads();
-    if (threadIdx.x < kKeys) {
-      const int pos = key0 + threadIdx.x;
-      int page = -1;
-      if (pos < nkeys) {
-        page = p.table[static_cast<long long>(b) * p.max_blocks + pos / p.bs];
-        if (page < 0 || page >= p.num_blocks) {
-          page = -1;
-          report(p.status, TS_ERR_DEVICE_CHECK);
+    const Keys& keys = s_keys[t & 1];
+    const int* s_page = keys.page;
+    if (p.wide) {
+#pragma unroll
+      for (int i = 0; i < CG; ++i) {
+        const int x = threadIdx.x + kThreads * i, j = x / per, c = (x - j * per) * 16;
+        if (j < kKeys) {
+          put16(sk + j * kp + c, kc[i], keys.ks[j]);
+          put16(sv + j * p.dp + c, vc[i], keys.vs[j]);
         }
       }
-      s_page[threadIdx.x] = page;
+    } else {
+      stage(p, p.kc, keys, keys.ks, sk, kp);
+      stage(p, p.vc, keys, keys.vs, sv, p.dp);
+    }
+    if (finder) {
+      keep(t + 1);
+      look(t + 2);
+      id = id_of(t + 3);
     }
     __syncthreads();
-    stage(p, p.kc, p.ks, sk, kp, key0, nkeys, h, s_page);
-    stage(p, p.vc, p.vs, sv, p.dp, key0, nkeys, h, s_page);
-    __syncthreads();
+    if (p.wide) ask(t + 1);
     float x[RPT][4];
 #pragma unroll
     for (int r = 0; r < RPT; ++r)
@@ -183,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int pos = key0 + tx + 16 * j, n = pos - L;
-        seen[j] = pos < nkeys && s_page[tx + 16 * j] >= 0 && (n < 0 || ((words[r][n >> 6] >> (n & 63)) & 1ull));
+        seen[j] = s_page[tx + 16 * j] >= 0 && (n < 0 || ((words[r][n >> 6] >> (n & 63)) & 1ull));
         x[r][j] *= p.scale_log2;
         if (seen[j]) top = fmaxf(top, x[r][j]);
       }
@@ -233,6 +276,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
         }
       }
     }
+    __syncthreads();
   }
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
@@ -259,50 +303,63 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
   }
 }
 
-// A warp per row: the chunks' maxima, sums and outputs joined in the order of the chunks.
+// A CTA per row: its warps take the chunks in turn, four of them in flight each, and their sums are joined in the warps' order.  (A warp
+// per row, a chunk after the other, waited for each: 20 of 74 us for 8 single tokens of 8 heads over 4096 tokens.)
+constexpr int kJoinWarps = 4;
 template <typename T>
-__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Params p) {
+  __shared__ float s_acc[kJoinWarps][256], s_l[kJoinWarps];
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  if (unit >= static_cast<long long>(p.B) * p.Hkv * p.rows) return;
-  const int row = static_cast<int>(unit % p.rows);
-  const int bh = static_cast<int>(unit / p.rows), b = bh / p.Hkv, h = bh % p.Hkv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long unit = blockIdx.x;
+  const int bh = static_cast<int>(blockIdx.x) / p.rows, row = static_cast<int>(blockIdx.x) - bh * p.rows, b = bh / p.Hkv, h = bh - b * p.Hkv;
   if (!usable(p, p.prefix_len[b])) return;
   const float2* ml = p.part_ml + unit * p.chunks;
+  const float* part = p.part_o + unit * p.chunks * p.d;
   float M = -INFINITY;
-  for (int c = 0; c < p.chunks; ++c) M = fmaxf(M, ml[c].x);
+  for (int c = lane; c < p.chunks; c += 32) M = fmaxf(M, ml[c].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float l = 0.f, acc[8] = {};
-  for (int c = 0; c < p.chunks; ++c) {
+#pragma unroll 4
+  for (int c = warp; c < p.chunks; c += kJoinWarps) {
     const float2 x = ml[c];
-    if (x.y == 0.f) continue;  // (no key in that chunk; a NaN sum goes on)
-    const float f = x.x == M ? 1.f : exp2f(x.x - M);
-    l += x.y * f;
+    const float f = x.y == 0.f ? 0.f : x.x == M ? 1.f : exp2f(x.x - M);  // (0: no key in that chunk; a NaN sum goes on)
+    l = fmaf(x.y, f, l);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int col = lane + 32 * u;
-      if (col < p.d) acc[u] = fmaf(p.part_o[(unit * p.chunks + c) * p.d + col], f, acc[u]);
+      if (col < p.d) acc[u] = fmaf(part[static_cast<long long>(c) * p.d + col], f, acc[u]);
     }
   }
-  const int node = row / p.g, head = h * p.g + row % p.g;
-  const long long o = (static_cast<long long>(b) * p.m + node) * p.Hq + head;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const int col = lane + 32 * u;
-    if (col < p.d) store1(static_cast<T*>(p.out) + o * p.d + col, acc[u] * inv);
+  for (int u = 0; u < 8; ++u) s_acc[warp][lane + 32 * u] = acc[u];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  l = s_l[0];
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) l += s_l[w];
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int node = row / p.g, head = h * p.g + row - node * p.g;
+  const long long o = (static_cast<long long>(b) * p.m + node) * p.Hq + head;
+  for (int col = threadIdx.x; col < p.d; col += 32 * kJoinWarps) {
+    float v = s_acc[0][col];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) v += s_acc[w][col];
+    store1(static_cast<T*>(p.out) + o * p.d + col, v * inv);
   }
-  if (lane == 0 && p.lse != nullptr) p.lse[o] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2f;
+  if (threadIdx.x == 0 && p.lse != nullptr) p.lse[o] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2f;
 }
 
-// Rows per CTA: 16 where there are no more, 32 otherwise (the decoded tile serves them all).
-int rows_per_cta(int rows) { return rows <= 16 ? 16 : 32; }
+// Rows per CTA: 16 where there are no more, 32 otherwise (the decoded tile serves them all).  64 halve what a row reads of the shared
+// memory: 128 rows of 4096 tokens, d = 64, 166 -> 121 us; at d = 128 they leave one CTA an SM (224 rows 130 -> 174, not taken).
+int rows_per_cta(int rows, int d) { return rows <= 16 ? 16 : rows <= 32 || d > 64 ? 32 : 64; }
 
 // Chunks per (sequence, KV head, row tile): two CTAs per SM's worth, of kMinTiles tiles at least.
-int chunks_of(int B, int m, int Hq, int Hkv, int max_prefix, int num_sms) {
+int chunks_of(int B, int m, int Hq, int Hkv, int d, int max_prefix, int num_sms) {
   const long long rows = static_cast<long long>(m) * (Hq / Hkv);
   const long long tiles = (static_cast<long long>(max_prefix) + m + kKeys - 1) / kKeys;
-  const long long units = static_cast<long long>(B) * Hkv * ((rows + rows_per_cta(static_cast<int>(rows)) - 1) / rows_per_cta(static_cast<int>(rows)));
+  const long long units = static_cast<long long>(B) * Hkv * ((rows + rows_per_cta(static_cast<int>(rows), d) - 1) / rows_per_cta(static_cast<int>(rows), d));
   const long long want = std::max(1LL, 2LL * num_sms / units);
   return static_cast<int>(std::max(1LL, std::min(want, tiles / kMinTiles)));
 }
@@ -330,17 +387,20 @@ cudaError_t launch_attn_cg(const Params& p, dim3 grid, cudaStream_t stream) {
 template <typename T>
 cudaError_t launch_all(const Params& p, cudaStream_t stream) {
   const dim3 grid(p.chunks, p.Hkv * p.row_tiles, p.B);
-  cudaError_t e = rows_per_cta(p.rows) == 16 ? launch_attn_cg<T, 1>(p, grid, stream) : launch_attn_cg<T, 2>(p, grid, stream);
+  cudaError_t e;
+  switch (rows_per_cta(p.rows, p.d)) {
+    case 16: e = launch_attn_cg<T, 1>(p, grid, stream); break;
+    case 32: e = launch_attn_cg<T, 2>(p, grid, stream); break;
+    default: e = launch_attn<T, 4, 1>(p, grid, stream); break;
+  }
   if (e != cudaSuccess || p.chunks == 1) return e;
-  const long long units = static_cast<long long>(p.B) * p.Hkv * p.rows;
-  return launch_pdl(join_kernel<T>, dim3(static_cast<unsigned>((units + kThreads / 32 - 1) / (kThreads / 32))), dim3(kThreads), 0,
-                    stream, p);
+  return launch_pdl(join_kernel<T>, dim3(static_cast<unsigned>(p.B * p.Hkv * p.rows)), dim3(32 * kJoinWarps), 0, stream, p);
 }
 
 }  // namespace
 
 size_t attention_fp8_simt_workspace_bytes(int B, int m, int Hq, int Hkv, int d, int max_prefix, int num_sms) {
-  const int chunks = chunks_of(B, m, Hq, Hkv, max_prefix, std::max(1, num_sms));
+  const int chunks = chunks_of(B, m, Hq, Hkv, d, max_prefix, std::max(1, num_sms));
   if (chunks == 1) return 256;
   return static_cast<size_t>(B) * m * Hq * chunks * (static_cast<size_t>(d) * 4 + 8) + 256;
 }
@@ -354,8 +414,8 @@ int attention_fp8_simt_launch(const Fp8AttnCall& a, cudaStream_t stream, int num
   p.B = a.B, p.m = a.m, p.Hq = a.Hq, p.Hkv = a.Hkv, p.g = a.Hq / a.Hkv, p.rows = a.m * p.g, p.d = a.d, p.dp = (a.d + 3) / 4 * 4;
   p.W = (a.m + 63) / 64, p.bs = a.block_size, p.sb = a.scale_block, p.max_blocks = a.max_blocks, p.num_blocks = a.num_blocks;
   p.max_prefix = a.max_prefix;
-  p.chunks = chunks_of(a.B, a.m, a.Hq, a.Hkv, a.max_prefix, num_sms);
-  p.row_tiles = (p.rows + rows_per_cta(p.rows) - 1) / rows_per_cta(p.rows);
+  p.chunks = chunks_of(a.B, a.m, a.Hq, a.Hkv, a.d, a.max_prefix, num_sms);
+  p.row_tiles = (p.rows + rows_per_cta(p.rows, p.d) - 1) / rows_per_cta(p.rows, p.d);
   if (static_cast<long long>(p.Hkv) * p.row_tiles > 65535) return TS_ERR_UNSUPPORTED;
   p.scale_log2 = a.scale * kLog2e;
   p.wide = a.d % 16 == 0 && (reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache)) % 16 == 0;
