@@ -680,10 +680,11 @@ __device__ __forceinline__ uint64_t visible64(int kb, int L, int m, const uint64
 
 // Rows are rows: a thread has one row (its TMEM lane) and N of the tile's keys, the thread of the warp four further on the
 // others; both keep the row's reference.  P goes to tensor memory.
-// COARSE (scale blocks of 16 tokens or more): the scales are those of 16 keys, so they are folded into the row's constants once for
-// 16 scores.  Otherwise each key has its own, and reading them (a broadcast of 16 bytes to a warp takes the shared memory four
-// cycles) is what paces the softmax: 177 against 150 us for 4 x 64 nodes of 32 heads over 32768 tokens when it was made.
-template <int R, bool COARSE>
+// GROUP keys have one scale (16, 4 or 1, as the scale blocks allow): it is folded into the row's constants once for as many scores.
+// With a scale for each key, reading them (a broadcast of 16 bytes to a warp takes the shared memory four cycles) is what paces the
+// softmax: 4 x 64 nodes of 32 heads over 32768 tokens take 141 us with a scale for 16, 152 with one for 4 or 8 (172 by keys), 170 with
+// one for each.
+template <int R, int GROUP>
 __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int warp, int lane) {
   using C = Cfg<R>;
   constexpr int N = C::CPT, PARTS = BK / N;
@@ -719,13 +720,13 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
         if (ok) {
           tmem_ld64(c.tmem + lanes + C::COL_S + BK * s + N * part, x);
           const float ref = M == kFloor ? 0.f : -M;
-          if constexpr (COARSE) {
+          if constexpr (GROUP > 1) {
 #pragma unroll
-            for (int g = 0; g < N; g += 16) {
+            for (int g = 0; g < N; g += GROUP) {
               const float a = sc[g] * r, b = sc[BK + g] + ref;
               const uint64_t a2 = pack_f32x2(a, a), b2 = pack_f32x2(b, b);
 #pragma unroll
-              for (int i = g; i < g + 16; i += 2) {
+              for (int i = g; i < g + GROUP; i += 2) {
                 float z0, z1;
                 unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), a2, b2), z0, z1);
                 x[i] = __float_as_uint(z0);
@@ -804,10 +805,10 @@ __device__ __forceinline__ void softmax_wide(const Cta<R>& c, Walk walk, int war
         for (int j = 0; j < 32; j += 4) {
           const float p0 = ex2_approx(__uint_as_float(x[i + j])), p1 = ex2_approx(__uint_as_float(x[i + j + 1]));
           const float p2 = ex2_approx(__uint_as_float(x[i + j + 2])), p3 = ex2_approx(__uint_as_float(x[i + j + 3]));
-          if constexpr (COARSE) {
+          if constexpr (GROUP > 1) {
             sum = add_f32x2(sum, add_f32x2(pack_f32x2(p0, p1), pack_f32x2(p2, p3)));
-            if (j % 16 == 12) {
-              const float iv = sc[2 * BK + i + j - 12];
+            if (j % GROUP == GROUP - 4) {
+              const float iv = sc[2 * BK + i + j + 4 - GROUP];
               l2 = fma_f32x2(sum, pack_f32x2(iv, iv), l2);
               sum = 0ull;
             }
@@ -904,7 +905,7 @@ struct Pages {
   }
 };
 
-template <int R, bool COARSE>
+template <int R, int GROUP>
 __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const __grid_constant__ Params p) {
   using C = Cfg<R>;
@@ -1222,7 +1223,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   } else {
     const Bars bars{s_full, p_full, p_empty, sc_full, q_full, q_empty, o_free};
     const Cta<R> c{p, bars, sptr, tmem, abort_flag, nan_seg, rg, cta, R0, rows_here};
-    if constexpr (C::WIDE) softmax_wide<R, COARSE>(c, walk, warp, lane);
+    if constexpr (C::WIDE) softmax_wide<R, GROUP>(c, walk, warp, lane);
     else softmax_narrow(c, walk, warp, lane);
   }
   __syncthreads();
@@ -1337,14 +1338,14 @@ bool encode_map(CUtensorMap* map, const void* base, int num_blocks, int Hkv, int
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int R, bool COARSE>
+template <int R, int GROUP>
 int launch(const Params& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(attn_kernel<R, COARSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<R>::SMEM);
+    return cudaFuncSetAttribute(attn_kernel<R, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<R>::SMEM);
   });
   if (e != cudaSuccess) return TS_ERR_CUDA;
-  e = launch_pdl(attn_kernel<R, COARSE>, dim3(p.RG * p.Gr), dim3(Cfg<R>::THREADS), Cfg<R>::SMEM, stream, mk, mv, p);
+  e = launch_pdl(attn_kernel<R, GROUP>, dim3(p.RG * p.Gr), dim3(Cfg<R>::THREADS), Cfg<R>::SMEM, stream, mk, mv, p);
   if (e != cudaSuccess) return TS_ERR_CUDA;
   int launches = 1;
   if (p.Gr > 1) {
@@ -1394,9 +1395,12 @@ int attention_fp8_tc_launch(const Fp8AttnCall& a, cudaStream_t stream, int num_s
   if (!encode_map(&mk, a.k_cache, a.num_blocks, a.Hkv, a.block_size) || !encode_map(&mv, a.v_cache, a.num_blocks, a.Hkv, a.block_size))
     return TS_ERR_CUDA;
   switch (pl.R) {
-    case 16: return launch<16, false>(p, mk, mv, stream);  // (up to 32 rows a thread has one key)
-    case 32: return launch<32, false>(p, mk, mv, stream);
-    default: return a.scale_block >= 16 ? launch<128, true>(p, mk, mv, stream) : launch<128, false>(p, mk, mv, stream);
+    case 16: return launch<16, 1>(p, mk, mv, stream);  // (up to 32 rows a thread has one key)
+    case 32: return launch<32, 1>(p, mk, mv, stream);
+    default:
+      return a.scale_block >= 16  ? launch<128, 16>(p, mk, mv, stream)
+             : a.scale_block >= 4 ? launch<128, 4>(p, mk, mv, stream)
+                                  : launch<128, 1>(p, mk, mv, stream);
   }
 }
 

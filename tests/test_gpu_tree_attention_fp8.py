@@ -65,3 +65,11 @@ def test_cuda_core_path(dtype, lens, m, Hq, Hkv, d, bs, sb):
     rng = np.random.default_rng(sum(lens) + m + d)
     c = Cache(rng, lens, m, Hkv, d, bs, sb)
     _check(c, _query(rng, (len(lens), m, Hq, d), dtype), tree_mask(rng, len(lens), m))
+
+
+@pytest.mark.parametrize("sb", [1, 2, 4, 8, 16, 32, 64])
+@pytest.mark.parametrize("m,Hq", [(2, 4), (6, 8), (40, 4)])
+def test_every_scale_block(m, Hq, sb):
+    rng = np.random.default_rng(sb + m)
+    c = Cache(rng, (400, 63, 5), m, 2, 128, 64, sb, spread=6)
+    _check(c, _query(rng, (3, m, Hq, 128), torch.bfloat16), tree_mask(rng, 3, m))
