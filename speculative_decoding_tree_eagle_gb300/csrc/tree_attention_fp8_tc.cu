@@ -1235,7 +1235,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
 // two of attn_kernel's CTAs, of which the first inside a unit has the unit.  The form with fewer warps is taken: with 61440 rows
 // (16 x 60 nodes of 64 heads) the call takes 173 us by boundaries against 186 by rows, with 1024 (4 x 8 nodes of 32) 68 by
 // rows against 71.
-constexpr int kJoinWarps = 8, kJoinRows = 16;  // rows of a CTA at a boundary
+constexpr int kJoinWarps = 8, kJoinRows = 32;  // rows of a CTA at a boundary
 template <int R, bool BOUNDARIES>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Params p) {
   pdl_wait();
@@ -1269,26 +1269,35 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   if (BOUNDARIES ? c0 + 1 != static_cast<int>(blockIdx.x) / p.RG + 1 : c0 == last) return;
   auto slot = [&](int c) { return (static_cast<long long>(rg) * p.Gr + c) * 2 + (c == c0 ? 1 : 0); };
   for (; r < r1; r += kJoinWarps) {
+    // (the first parts are asked for together with the references)
+    auto part = [&](int c) { return *reinterpret_cast<const float4*>(p.part_o + (slot(c) * R + r) * HD + 4 * lane); };
+    constexpr int AHEAD = 4;
+    float4 o[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) o[i] = part(min(c0 + i, last));
     float M = -INFINITY;
     for (int c = c0 + lane; c <= last; c += 32) M = fmaxf(M, p.part_ml[slot(c) * R + r].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = c0; c <= last; ++c) {
+    auto add = [&](int c, const float4& x) {
       const float2 ml = p.part_ml[slot(c) * R + r];
-      const float4 o = *reinterpret_cast<const float4*>(p.part_o + (slot(c) * R + r) * HD + 4 * lane);
       const float f = ml.x == M ? 1.f : ex2_approx(ml.x - M);
       l = fmaf(ml.y, f, l);
-      acc.x = fmaf(o.x, f, acc.x), acc.y = fmaf(o.y, f, acc.y), acc.z = fmaf(o.z, f, acc.z), acc.w = fmaf(o.w, f, acc.w);
-    }
+      acc.x = fmaf(x.x, f, acc.x), acc.y = fmaf(x.y, f, acc.y), acc.z = fmaf(x.z, f, acc.z), acc.w = fmaf(x.w, f, acc.w);
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (c0 + i <= last) add(c0 + i, o[i]);
+#pragma unroll 4
+    for (int c = c0 + AHEAD; c <= last; ++c) add(c, part(c));
     const int row = rg * R + r, node = row / p.g, head = h * p.g + row % p.g;
-    const long long o = (static_cast<long long>(b) * p.m + node) * p.Hq + head;
+    const long long at = (static_cast<long long>(b) * p.m + node) * p.Hq + head;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(p.out + o * HD + 4 * lane) =
+    *reinterpret_cast<uint2*>(p.out + at * HD + 4 * lane) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (lane == 0 && p.lse != nullptr) p.lse[o] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2f;
+    if (lane == 0 && p.lse != nullptr) p.lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2f;
   }
 }
 
