@@ -29,9 +29,9 @@
 // to the workspace and join_kernel merges them.  With several row groups CTAs of neighbouring index walk the same tiles
 // for different rows, so all but one read them from L2.
 //
-// Measured (GB300, 32 heads on 8 but for the last, pages of 16 tokens, a scale for 16): 8 single tokens over 1024 to 8192 tokens 27.9 us;
+// Measured (GB300, 32 heads on 8 but for the last, pages of 16 tokens, a scale for 16): 8 single tokens over 1024 to 8192 tokens 27.0 us;
 // 4 x 8 nodes over 32768 66 us (4.1 TB/s, 61% of the copy rate: a tile takes some 2000 cycles, of which its shared-memory traffic
-// is 1350); 4 x 64 nodes over 32768 140 us and 16 x 60 nodes of 64 heads over 4096 169 us (48% and 40% of the bf16 rate: what
+// is 1350); 4 x 64 nodes over 32768 140 us and 16 x 60 nodes of 64 heads over 4096 167 us (51% and 40% of the bf16 rate: what
 // bounds both is the softmax, 1700 cycles a tile of 128 x 128 scores with its issue slots a third used, then 15000 cycles for a
 // unit's beginning and end).
 //
@@ -469,6 +469,7 @@ __device__ __forceinline__ void softmax_narrow(const Cta<R>& c, Walk walk, int w
   constexpr int N = C::CPT;
   const Params& p = c.p;
   const int quarter = warp & 3, group = (warp - C::FIRST_SOFT) >> 2, col0 = group * N, key = 32 * quarter + lane;
+  if (col0 >= c.rows_here) return;  // (what P^T holds in those columns reaches theirs of O^T alone)
   const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16, tO = c.tmem + lanes + col0;
   float* rm = reinterpret_cast<float*>(c.sptr + C::OFF_RM) + 2 * col0;  // {r0, r1, M0, M1} per pair of rows
   float* red = reinterpret_cast<float*>(c.sptr + C::OFF_RED) + col0;    // [quarter * R + row]
@@ -917,8 +918,8 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rg = blockIdx.x % p.RG, cta = blockIdx.x / p.RG;
   const int R0 = rg * R, rows_here = min(R, p.rows - R0);
-  // wide: quadrants of 32 rows that hold any; the softmax warps of the others have nothing to do
-  const int soft = C::WIDE ? BK / C::CPT * ((rows_here + 31) / 32) : C::SOFT;
+  // softmax warps whose rows (wide: quadrants of 32, otherwise columns of CPT) hold any; the others have nothing to do
+  const int soft = C::WIDE ? BK / C::CPT * ((rows_here + 31) / 32) : 4 * ((rows_here + C::CPT - 1) / C::CPT);
 
   uint32_t at = sbase + C::OFF_BAR;
   auto take = [&](int n) {
