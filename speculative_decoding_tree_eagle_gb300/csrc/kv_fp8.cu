@@ -502,7 +502,7 @@ __device__ __forceinline__ Commit commit_of(const CommitParams& p, int b, int* s
   const long long used = c.L >= 0 ? (static_cast<long long>(c.L) + p.m + p.bs - 1) / p.bs : 0;
   bool bad = c.L < 0 || c.L > INT32_MAX - TS_MAX_NODES || c.a < 1 || c.a > p.m || used > p.max_blocks;
   c.n_used = bad ? 0 : static_cast<int>(used);
-  c.n_keep = bad ? 0 : (c.L + c.a + p.bs - 1) / p.bs;
+  c.n_keep = bad ? 0 : static_cast<int>((static_cast<long long>(c.L) + c.a + p.bs - 1) / p.bs);
   c.p0 = bad ? 0 : c.L / p.bs;
   bad = bad || c.n_used - c.p0 > kMaxPages;
   if (!bad) {
@@ -512,9 +512,10 @@ __device__ __forceinline__ Commit commit_of(const CommitParams& p, int b, int* s
       s_path[j] = pj;
       if (j == 0 ? pj != 0 : (pj >= p.m || pj <= path[j - 1])) bad = true;
     }
-    for (int i = c.p0 + threadIdx.x; i < c.n_used; i += blockDim.x) {
-      const int pg = p.table[static_cast<long long>(b) * p.max_blocks + i];
-      s_page[i - c.p0] = pg;
+    // (by distances from p0: positions and cells may lie just below 2^31)
+    for (int i = threadIdx.x; i < c.n_used - c.p0; i += blockDim.x) {
+      const int pg = p.table[static_cast<long long>(b) * p.max_blocks + c.p0 + i];
+      s_page[i] = pg;
       if (pg < 0 || pg >= p.num_blocks) bad = true;
     }
   }
@@ -525,8 +526,8 @@ __device__ __forceinline__ Commit commit_of(const CommitParams& p, int b, int* s
 // Tables, lengths and the released pages of sequence b, by the whole CTA.
 __device__ void commit_tables(const CommitParams& p, int b, const Commit& c, const int* s_page) {
   const long long o = static_cast<long long>(b) * p.max_blocks;
-  for (int i = threadIdx.x; i < p.max_blocks; i += kCommitThreads) {
-    const int k = i + c.n_keep;
+  for (long long i = threadIdx.x; i < p.max_blocks; i += kCommitThreads) {
+    const long long k = i + c.n_keep;
     p.freed[o + i] = c.ok && k < c.n_used ? s_page[k - c.p0] : -1;
     const bool gone = c.ok && i >= c.n_keep && i < c.n_used;
     if (gone) p.table_out[o + i] = -1;
@@ -606,8 +607,9 @@ __global__ void __launch_bounds__(kCommitThreads) commit_rows_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int team = WHOLE ? 0 : warp, teams = WHOLE ? 1 : kCommitThreads / 32;
   const int me = WHOLE ? threadIdx.x : lane, size = WHOLE ? kCommitThreads : 32;
-  for (int blk = c.L / p.sb + team; blk <= (c.L + c.a - 1) / p.sb; blk += teams) {
-    const int first = blk * p.sb, kept = max(0, c.L - first), end = min(p.sb, c.L + c.a - first);
+  const int blk0 = c.L / p.sb, blocks = (c.L + c.a - 1) / p.sb - blk0 + 1;
+  for (int i = team; i < blocks; i += teams) {
+    const int first = (blk0 + i) * p.sb, kept = max(0, c.L - first), end = min(p.sb, c.L + c.a - first);
     const long long head = head_of(max(first, c.L));
     Word* codes = reinterpret_cast<Word*>(cache + (head * p.bs + first % p.bs) * p.d);
     float* sc = scale + head * nsb + first % p.bs / p.sb;

@@ -1,0 +1,89 @@
+"""The 8-bit cache's calls at the ends of their ranges: scores and queries of every size, bounds and positions near 2^31."""
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_tree_eagle_gb300 as ts
+from fp8_helpers import F8, ints
+from gpu_helpers import lib
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _built():
+    lib()
+
+
+class Far:
+    """Four pages in one cache, named by the first table cells of a row and by those from ``at`` on of a far longer one."""
+
+    def __init__(self, bs, sb, Hkv, d, at, cells):
+        g = torch.Generator(device="cuda").manual_seed(bs + sb)
+        shape = (4, Hkv, bs, d)
+        self.start = [(torch.randn(shape, generator=g, device="cuda") * 50).to(F8) for _ in "kv"]
+        self.start += [torch.exp2(torch.randint(-6, 7, (4, Hkv, bs // sb), generator=g, device="cuda").float()) for _ in "kv"]
+        self.near = ints([[2, 0, 3]])
+        self.table = torch.full((1, cells), -1, dtype=torch.int32, device="cuda")
+        self.table[0, at:at + 3] = self.near[0, :cells - at]
+
+    def cache(self):
+        return [t.clone() for t in self.start]
+
+
+def _same(a, b):
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("bs,sb,m,a", [(1024, 1024, 20, 7), (1024, 1, 256, 256), (1024, 64, 256, 3), (128, 128, 256, 3), (128, 16, 256, 256)])
+def test_commit_near_2_to_31(bs, sb, m, a, in_place):
+    """As at the beginning of a cache: the same rows, blocks and pages."""
+    cells = (1 << 31) // bs
+    L = (1 << 31) - 257                                        # (the longest prefix that a tree may follow)
+    near = L % bs
+    p0 = (L - near) // bs
+    c = Far(bs, sb, 2, 8, p0, cells)
+    c.near = c.near[:, :cells - p0].contiguous()
+    path = torch.full((1, m), -1, dtype=torch.int32, device="cuda")
+    path[0, :a] = ints([0] + sorted(np.random.default_rng(m).choice(np.arange(1, m), a - 1, replace=False)))
+    results = []
+    for table, prefix in ((c.near, near), (c.table, L)):
+        dev, status, lens = c.cache(), ts.new_status(), ints([prefix])
+        out = None
+        if in_place:
+            table = table.clone()
+            out = dict(block_table=table, prefix_len=lens, freed_blocks=torch.empty_like(table), freed_count=torch.empty_like(lens))
+        r = ts.kv_commit_fp8(*dev, table, lens, path, ints([a]), out=out, status=status)
+        ts.check_status(status)
+        results.append((dev, r))
+    (dev, r), (far, f) = results
+    _same(dev, far)
+    assert f["prefix_len"].item() == L + a and torch.equal(f["freed_count"], r["freed_count"])
+    assert torch.equal(f["block_table"][0, p0:], r["block_table"][0]) and (f["block_table"][0, :p0] == -1).all()
+    n = r["freed_count"].item()
+    assert torch.equal(f["freed_blocks"][0, :n], r["freed_blocks"][0, :n]) and (f["freed_blocks"][0, n:] == -1).all()
+
+
+def test_commit_of_a_row_of_2_to_31_pages():
+    """Pages of one token: cells of the table are counted beyond 2^31 too."""
+    m, a, L = 40, 5, (1 << 31) - 257
+    cells = L + m
+    c = [torch.zeros(64, 1, 1, 4, dtype=F8, device="cuda") for _ in "kv"] + [torch.ones(64, 1, 1, device="cuda") for _ in "kv"]
+    table = torch.full((1, cells), -1, dtype=torch.int32, device="cuda")
+    table[0, L:L + m] = torch.arange(m, dtype=torch.int32, device="cuda")
+    out = dict(block_table=table, prefix_len=ints([L]), freed_blocks=torch.empty_like(table), freed_count=ints([-1]))
+    path = torch.full((1, m), -1, dtype=torch.int32, device="cuda")
+    path[0, :a] = ints([0, 3, 7, 20, 39])
+    for i in (0, 1):
+        c[i].copy_(torch.arange(64.0, device="cuda").view(64, 1, 1, 1).expand(64, 1, 1, 4).to(F8))
+    old, status = c[0].float().flatten(1)[:, 0], ts.new_status()
+    ts.kv_commit_fp8(*c, table, out["prefix_len"], path, ints([a]), out=out, status=status)
+    ts.check_status(status)
+    assert out["prefix_len"].item() == L + a and out["freed_count"].item() == m - a
+    assert torch.equal(table[0, L:L + a], torch.arange(a, dtype=torch.int32, device="cuda")) and (table[0, L + a:] == -1).all()
+    assert torch.equal(out["freed_blocks"][0, :m - a], torch.arange(a, m, dtype=torch.int32, device="cuda"))
+    assert (out["freed_blocks"][0, m - a:1 << 20] == -1).all() and (out["freed_blocks"][0, -(1 << 20):] == -1).all()
+    for i in (0, 1):
+        value = c[i].float().flatten(1)[:, 0] * c[2 + i].flatten()
+        assert torch.equal(value[:a], old[[0, 3, 7, 20, 39]]) and torch.equal(value[a:], old[a:])
