@@ -87,7 +87,7 @@ __device__ __forceinline__ Item item_of(const WriteParams& p, const Side& side, 
     if (i == 0) report(p.status, TS_ERR_DEVICE_CHECK);
     return it;
   }
-  const long long first_at = static_cast<long long>(p.by_block.quotient(start) + i) * p.sb;
+  const long long first_at = (static_cast<long long>(p.by_block.quotient(start)) + i) * p.sb;
   if (len == 0 || first_at >= end) return it;
   const int first = static_cast<int>(first_at), lp = p.by_page.quotient(first);
   const int page = p.table[static_cast<long long>(b) * p.max_blocks + lp];
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(write_threads(1), sizeof(T) == 2 ? 7 : 4) writ
     if (i == 0) report(p.status, TS_ERR_DEVICE_CHECK);
     return;
   }
-  const long long first_at = static_cast<long long>(start / run + i) * run;
+  const long long first_at = (static_cast<long long>(start / run) + i) * run;
   if (len == 0 || first_at >= end) return;
   const int first = static_cast<int>(first_at), lp = p.by_page.quotient(first);
   const int page = p.table[static_cast<long long>(b) * p.max_blocks + lp];

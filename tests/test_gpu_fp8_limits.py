@@ -65,6 +65,32 @@ def test_commit_near_2_to_31(bs, sb, m, a, in_place):
     assert torch.equal(f["freed_blocks"][0, :n], r["freed_blocks"][0, :n]) and (f["freed_blocks"][0, n:] == -1).all()
 
 
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.float32, 64), (torch.bfloat16, 20)])
+@pytest.mark.parametrize("bs,sb,n,length", [(1024, 1, 300, 5), (1024, 1, 300, 100), (1024, 1024, 300, 255), (256, 8, 500, 400), (16, 16, 600, 30),
+                                            (1024, 1, 20000, 100)])
+def test_write_and_read_near_2_to_31(dtype, d, bs, sb, n, length):
+    """As at the beginning of a cache, and nothing behind the last row, however many there might have been."""
+    cells = (1 << 31) // bs
+    L = (1 << 31) - 1 - length - (3 if bs > 16 else 0)
+    p0 = L // bs
+    p0 -= max(0, 3 - (cells - p0))                             # (three pages of the row are there)
+    near = L - p0 * bs
+    c = Far(bs, sb, 2, d, p0, cells)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k, v = [torch.randn(1, n, 2, d, generator=g, device="cuda").to(dtype) for _ in "kv"]
+    results = []
+    for table, start in ((c.near, near), (c.table, L)):
+        dev, status = c.cache(), ts.new_status()
+        ts.kv_write_fp8(k, v, *dev, table, ints([start]), length=ints([length]), status=status)
+        kv = ts.kv_read_fp8(*dev, table, ints([start + length]), n, start_len=ints([start]), dtype=torch.float32, status=status)
+        ts.check_status(status)
+        results.append((dev, kv))
+    _same(*(dev for dev, _ in results))
+    _same(*(kv for _, kv in results))
+    for old, new in zip(c.start[:2], results[0][0]):           # (a block's kept rows may keep its scale)
+        assert not torch.equal(old.view(torch.uint8), new.view(torch.uint8))
+
+
 def test_commit_of_a_row_of_2_to_31_pages():
     """Pages of one token: cells of the table are counted beyond 2^31 too."""
     m, a, L = 40, 5, (1 << 31) - 257
