@@ -303,9 +303,9 @@ __global__ void __launch_bounds__(256) copy_tails_kernel(unsigned char* kc, unsi
   if (from < 0 || to < 0) return;
   const int rows = prefix_len[b] % bs, chunks = rows * (row_bytes / static_cast<int>(sizeof(Chunk)));
   if (scales.k != nullptr) {
-    const int sb = bs / scales.nsb;
+    const int sb = bs / scales.nsb, blocks = rows > 0 ? (rows - 1) / sb + 1 : 0;
     const long long sf = (static_cast<long long>(from) * Hkv + h) * scales.nsb, st = (static_cast<long long>(to) * Hkv + h) * scales.nsb;
-    for (int i = threadIdx.x; i * sb < rows; i += 256) {
+    for (int i = threadIdx.x; i < blocks; i += 256) {
       scales.k[st + i] = scales.k[sf + i];
       scales.v[st + i] = scales.v[sf + i];
     }

@@ -113,3 +113,24 @@ def test_commit_of_a_row_of_2_to_31_pages():
     for i in (0, 1):
         value = c[i].float().flatten(1)[:, 0] * c[2 + i].flatten()
         assert torch.equal(value[:a], old[[0, 3, 7, 20, 39]]) and torch.equal(value[a:], old[a:])
+
+
+@pytest.mark.parametrize("nsb", [1, 2])
+def test_reserve_with_scales_of_millions_of_tokens(nsb):
+    """Scale blocks of 2^23 tokens and more: the copied page gets the scales that its rows reach, and nothing else changes."""
+    bs, rows = nsb << 23, 10
+    c = [torch.zeros(5, 1, bs, 4, dtype=F8, device="cuda") for _ in "kv"] + [torch.zeros(5, 1, nsb, device="cuda") for _ in "kv"]
+    for i in range(2):
+        c[i][1, 0, :rows] = torch.randn(rows, 4, device="cuda").to(F8)
+        c[2 + i][:] = torch.arange(1, 5 * nsb + 1, device="cuda").view(5, 1, nsb) * (i + 2)
+    before, status = [t.clone() for t in c[2:]], ts.new_status()
+    r = ts.kv_reserve(*c[:2], ints([[0, 1, -1], [0, 1, -1]]), ints([bs + rows] * 2), ints([2, 2, 0, 0, 0]), 1, k_scale=c[2], v_scale=c[3],
+                      status=status)
+    ts.check_status(status)
+    pages = set(r["block_table"][:, 1].tolist())
+    assert r["granted"].sum().item() == 1 and 1 in pages and len(pages) == 2
+    new = (pages - {1}).pop()
+    for codes, scale, old in zip(c[:2], c[2:], before):
+        assert torch.equal(codes[new, 0, :rows].float(), codes[1, 0, :rows].float()) and not codes[new, 0, rows:].view(torch.uint8).any()
+        old[new, 0, 0] = old[1, 0, 0]
+        assert torch.equal(scale, old)
