@@ -532,6 +532,8 @@ static int check_fp8(int num_blocks, int block_size, int scale_block, int Hkv, i
   if (d > 256 || Hkv > 65535 / 2) return TS_ERR_UNSUPPORTED;
   return TS_OK;
 }
+// The calls that quantise count a scale block's elements in 32 bits.
+static bool block_counts(int scale_block, int d) { return static_cast<long long>(scale_block) * d <= (1 << 30); }
 // The pool's 8-bit forms write pages of all four: they lie apart.
 static bool fp8_scales(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size,
                        int scale_block, int Hkv, int d) {
@@ -551,6 +553,7 @@ int ts_kv_write_fp8(const void* k, const void* v, ts_dtype dt, const int64_t* k_
   const int rc = check_fp8(num_blocks, block_size, scale_block, Hkv, d, max_blocks, B);
   if (rc != TS_OK) return rc;
   if ((dt != TS_F32 && dt != TS_BF16) || n <= 0) return TS_ERR_INVALID;
+  if (!block_counts(scale_block, d)) return TS_ERR_UNSUPPORTED;
   if (!k || !v || !k_strides || !v_strides || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !start_len)
     return TS_ERR_INVALID;
   const size_t size = dt == TS_BF16 ? 2 : 4;
@@ -612,7 +615,7 @@ int ts_kv_commit_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scal
   const int rc = check_fp8(num_blocks, block_size, scale_block, Hkv, d, max_blocks, B);
   if (rc != TS_OK) return rc;
   if (m <= 0) return TS_ERR_INVALID;
-  if (m > TS_MAX_NODES) return TS_ERR_UNSUPPORTED;
+  if (m > TS_MAX_NODES || !block_counts(scale_block, d)) return TS_ERR_UNSUPPORTED;
   if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !prefix_len || !accept_path || !accept_len ||
       !block_table_out || !prefix_len_out || !freed_blocks || !freed_count)
     return TS_ERR_INVALID;
