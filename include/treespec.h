@@ -563,7 +563,7 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
  * k, v        [B, n, Hkv, d] (dt), any layout with contiguous head rows: k_strides, v_strides [3] (host) are the elements between
  *             sequences, rows and heads (>= 0), so k and v may be slices of a fused projection's output.
  * block_table [B, max_blocks], start_len [B], length [B] int32 (NULL: n each), 0 <= length <= n.
- * A page that is written must belong to one sequence alone (ts_kv_reserve sees to that).  Any d <= 256, scale_block * d <= 2^30.
+ * A page that is written must belong to one sequence alone (ts_kv_reserve sees to that).  Any d <= 256, scale_block * d < 2^31 - 256.
  * One launch.
  * Device errors, TS_ERR_DEVICE_CHECK: a negative start, a length outside [0, n] or positions beyond max_blocks * block_size (the
  * sequence is skipped); a page id out of range (its rows are skipped).
@@ -595,7 +595,7 @@ int ts_kv_read_fp8(const void* k_cache, const void* v_cache, const float* k_scal
  * block_table_out and prefix_len_out may be block_table and prefix_len themselves, for an update in place, or others, for the
  * next layer's cache to be committed from the same old state.
  *
- * freed_blocks [B, max_blocks], freed_count [B].  m <= TS_MAX_NODES, any d <= 256, scale_block * d <= 2^30.  One launch, two in
+ * freed_blocks [B, max_blocks], freed_count [B].  m <= TS_MAX_NODES, any d <= 256, scale_block * d < 2^31 - 256.  One launch, two in
  * place; no workspace.
  * Device errors: as ts_kv_commit (the sequence's cache is left untouched, its table row and length are copied).
  */

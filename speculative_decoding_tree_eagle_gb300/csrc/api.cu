@@ -532,8 +532,8 @@ static int check_fp8(int num_blocks, int block_size, int scale_block, int Hkv, i
   if (d > 256 || Hkv > 65535 / 2) return TS_ERR_UNSUPPORTED;
   return TS_OK;
 }
-// The calls that quantise count a scale block's elements in 32 bits.
-static bool block_counts(int scale_block, int d) { return static_cast<long long>(scale_block) * d <= (1 << 30); }
+// The calls that quantise count a scale block's elements in 32 bits, by up to 256 at a time.
+static bool block_counts(int scale_block, int d) { return static_cast<long long>(scale_block) * d <= INT32_MAX - 256; }
 // The pool's 8-bit forms write pages of all four: they lie apart.
 static bool fp8_scales(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size,
                        int scale_block, int Hkv, int d) {

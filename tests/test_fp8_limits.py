@@ -16,10 +16,11 @@ def lib():
     return ts.library()
 
 
-@pytest.mark.parametrize("bs,sb,d", [(1 << 24, 1 << 24, 128), (1 << 23, 1 << 23, 256), (1 << 24, 1 << 23, 192), (1 << 30, 1 << 30, 2),
-                                     ((1 << 31) - 1, (1 << 31) - 1, 3), ((1 << 31) - 1, (1 << 31) - 1, 1)])
+@pytest.mark.parametrize("bs,sb,d", [(1 << 24, 1 << 24, 128), (1 << 23, 1 << 23, 256), (1 << 24, 1 << 24, 255), (1 << 30, 1 << 30, 2),
+                                     ((1 << 31) - 1, (1 << 31) - 1, 3), ((1 << 31) - 1, (1 << 31) - 1, 1),
+                                     ((1 << 31) - 256, (1 << 31) - 256, 1)])
 def test_scale_blocks_of_more_elements_than_are_counted(lib, bs, sb, d):
-    """A scale block of more than 2^30 elements of a head is neither written nor committed."""
+    """A scale block of 2^31 - 256 elements of a head and more is neither written nor committed."""
     at = [(i + 1) * TB * 16 for i in range(12)]
     strides = (ctypes.c_int64 * 3)(4 * d, d, d)
     assert lib.ts_kv_write_fp8(at[0], at[1], 1, strides, strides, *at[2:6], 1, bs, sb, 1, d, at[6], 4, at[7], None, 1, 4, None,
