@@ -90,7 +90,7 @@ struct Cfg {
   static constexpr uint32_t OFF_V16 = OFF_V + SV * TILE8;
   static constexpr uint32_t OFF_P = OFF_V16 + NV * TILE16;
   static constexpr uint32_t OFF_RAW = OFF_P + NP * PBUF;         // {ks, vs} per key, kScaleSlots tiles
-  // {ks * scale * log2 e}, {log2 vs}, {1 / vs} of two tiles
+  // {ks}, {log2 vs}, {1 / vs} of two tiles
   static constexpr uint32_t OFF_SC = OFF_RAW + kScaleSlots * BK * 8;
   static constexpr uint32_t OFF_RM = OFF_SC + 2 * 3 * BK * 4;      // per pair of rows {r0, r1, M0, M1}
   static constexpr uint32_t OFF_R2 = OFF_RM + (WIDE ? 0 : R * 8);  // row scales of the next segment
@@ -125,7 +125,7 @@ struct Params {
   int32_t* status;
   int B, m, Hq, Hkv, g, rows, W, bs, nsb, bs_log2, sb_log2, max_blocks, num_blocks, max_prefix;
   int RG, Gr;       // row groups, CTAs per row group
-  float scale_log2;
+  float scale_log2;  // scale * log2 e / 4 (the quarter keeps it finite for every finite scale; the rows' factors take it back)
 };
 
 __device__ __forceinline__ int tiles_of(const Params& p, int b) {
@@ -284,13 +284,13 @@ __device__ __forceinline__ void copy4(uint32_t dst, const float* src) {
 __device__ __forceinline__ void arrive_copied(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-// A key's scales in the exponent's units: y = s a + lv, and 1 / vs.
+// A key's scales in the exponent's units: y = s a r + lv with the row's factor r, and 1 / vs.
 struct KeyScale {
   float a, lv, iv;
 };
-__device__ __forceinline__ KeyScale key_scale(float2 raw, float scale_log2) {
+__device__ __forceinline__ KeyScale key_scale(float2 raw) {
   KeyScale k;
-  k.a = scale_in_range(raw.x) * scale_log2;
+  k.a = scale_in_range(raw.x);
   k.lv = __log2f(scale_in_range(raw.y));
   k.iv = ex2_approx(-k.lv);
   if (__float_as_uint(raw.x) == kNoPage) k = KeyScale{0.f, -INFINITY, 0.f};
@@ -1145,7 +1145,10 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
         const uint32_t off = r * 128 + ((c ^ (r & 7)) << 4);
         *reinterpret_cast<uint4*>(sptr + C::OFF_Q + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(sptr + C::OFF_Q + C::QPART + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        if (c == 0) reinterpret_cast<float*>(sptr + C::OFF_R2)[r] = big >= 0x7F800000u ? __int_as_float(0x7FC00000) : pow2(max(-126, e));
+        // The row's factor, 2^e * scale * log2 e.  (Not 2^e alone, with the rest in the keys': below 2^-126 there is no such float, and a
+        // large scale makes ordinary scores of such rows.)
+        const float factor = pow2(e / 2) * p.scale_log2 * pow2(e - e / 2 + 2);
+        if (c == 0) reinterpret_cast<float*>(sptr + C::OFF_R2)[r] = big >= 0x7F800000u ? __int_as_float(0x7FC00000) : factor;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -1160,7 +1163,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
           ok = wait_warp(raw_full + 8 * slot, (it / kScaleSlots) & 1, abort_flag, p.status) &&
                wait_warp(v16_empty + 8 * v, ((it >> 1) & 1) ^ 1, abort_flag, p.status);
           if (!ok) break;
-          const KeyScale k = key_scale(reinterpret_cast<const float2*>(sptr + C::OFF_RAW)[slot * BK + key], p.scale_log2);
+          const KeyScale k = key_scale(reinterpret_cast<const float2*>(sptr + C::OFF_RAW)[slot * BK + key]);
           float* to = reinterpret_cast<float*>(sptr + C::OFF_SC) + v * 3 * BK;
           to[key] = k.a;
           to[BK + key] = k.lv;
@@ -1400,7 +1403,7 @@ int attention_fp8_tc_launch(const Fp8AttnCall& a, cudaStream_t stream, int num_s
   p.bs_log2 = log2_of(a.block_size), p.sb_log2 = log2_of(a.scale_block);
   p.max_blocks = a.max_blocks, p.num_blocks = a.num_blocks, p.max_prefix = a.max_prefix;
   p.RG = pl.RG, p.Gr = pl.Gr;
-  p.scale_log2 = a.scale * kLog2e;
+  p.scale_log2 = 0.25f * a.scale * kLog2e;
   CUtensorMap mk, mv;
   if (!encode_map(&mk, a.k_cache, a.num_blocks, a.Hkv, a.block_size) || !encode_map(&mv, a.v_cache, a.num_blocks, a.Hkv, a.block_size))
     return TS_ERR_CUDA;

@@ -1,10 +1,12 @@
 """The 8-bit cache's calls at the ends of their ranges: scores and queries of every size, bounds and positions near 2^31."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 import speculative_decoding_tree_eagle_gb300 as ts
-from fp8_helpers import F8, ints
+from fp8_helpers import Cache, F8, assert_within, attention_bounds, ints, tree_mask, words
 from gpu_helpers import lib
 
 pytestmark = pytest.mark.gpu
@@ -134,3 +136,42 @@ def test_reserve_with_scales_of_millions_of_tokens(nsb):
         assert torch.equal(codes[new, 0, :rows].float(), codes[1, 0, :rows].float()) and not codes[new, 0, rows:].view(torch.uint8).any()
         old[new, 0, 0] = old[1, 0, 0]
         assert torch.equal(scale, old)
+
+
+# the tensor cores' forms: (m, Hq, Hkv, bs, sb); up to 16, 32 and any number of rows per KV head, scales for 16, 4 and 1 keys
+TC = dict(rows16=(4, 4, 2, 16, 16), rows32=(8, 8, 2, 32, 8), wide=(33, 8, 2, 16, 16), wide4=(40, 4, 1, 64, 4), wide1=(33, 8, 2, 16, 1))
+tc_forms = pytest.mark.parametrize("form", TC.values(), ids=TC.keys())
+
+
+def _query(rng, shape, dtype=torch.bfloat16):
+    return torch.from_numpy(rng.standard_normal(shape) * np.exp2(rng.integers(-2, 2, shape[:-1] + (1,)))).to(dtype)
+
+
+def _attend(c, q, mask, dev=None, **kw):
+    status = ts.new_status()
+    kw.setdefault("max_prefix", int(c.lens.max()))
+    r = ts.tree_attention_fp8(q.cuda(), *(dev or c.device()), ints(c.table), ints(c.lens), words(mask), status=status, **kw)
+    ts.check_status(status)
+    return r
+
+
+def _reference(c, q, mask, scale=None):
+    scale = 1 / math.sqrt(q.shape[-1]) if scale is None else scale
+    return attention_bounds(q.double().numpy(), *c.values(), c.table, c.lens, mask, scale, q.dtype == torch.bfloat16)
+
+
+@tc_forms
+def test_small_queries_under_a_large_scale(form):
+    """Rows near and below the least normal number; the call's scale makes ordinary scores of them."""
+    m, Hq, Hkv, bs, sb = form
+    rng = np.random.default_rng(m + 1)
+    lens = (0, 140, 500)
+    c = Cache(rng, lens, m, Hkv, 128, bs, sb)
+    mask = tree_mask(rng, len(lens), m)
+    size = np.exp2(-rng.integers(112, 131, (len(lens), m, Hq, 1)).astype(np.float64))
+    q = torch.from_numpy(rng.standard_normal((len(lens), m, Hq, 128)) * size).to(torch.bfloat16)
+    scale = 2.0 ** 112
+    out, lse = _attend(c, q, mask, scale=scale)
+    ref, ref_lse, bo, bl = _reference(c, q, mask, scale)
+    assert_within(lse, ref_lse, bl, "lse")
+    assert_within(out, ref, bo, "out")
