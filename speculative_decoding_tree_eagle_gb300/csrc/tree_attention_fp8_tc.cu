@@ -41,6 +41,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cstring>
 #include <mutex>
 
 #include "fp8_cache.cuh"
@@ -55,11 +56,14 @@ constexpr uint32_t TILE8 = BK * HD;          // codes of one tile of K or V
 constexpr uint32_t TILE16 = 2 * TILE8;       // V in fp16
 constexpr int kScaleSlots = 4;
 constexpr uint32_t kNoPage = 0x7FDEAD01u;    // in the place of a scale: its key's page has no id
-constexpr float kFloor = -1e30f;             // reference of a row that has met no key
+constexpr float kFloor = -INFINITY;          // reference of a row that has met no key
 constexpr float kBelow = 7.f, kRise = 15.f;  // the reference lies kBelow under the largest y; raised when exceeded by kRise
 // References beyond this make their rows NaN: fp32 holds them to half a unit of the exponent and more, and where rounding passes the
 // margins a row would overflow or vanish.
 constexpr float kMostM = 4194304.f;
+// Rows whose largest |q| * scale reaches this are NaN from the beginning: below it every score lies in fp32's range (at most 2^24
+// in Q K, 2^40 of a key's scale and 2^64 of the row's factor), so -inf means that there is no key.
+constexpr float kMostQ = 1180591620717411303424.f;  // 2^70
 constexpr float kLn2f = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634074f;
 
@@ -125,6 +129,7 @@ struct Params {
   int32_t* status;
   int B, m, Hq, Hkv, g, rows, W, bs, nsb, bs_log2, sb_log2, max_blocks, num_blocks, max_prefix;
   int RG, Gr;       // row groups, CTAs per row group
+  uint32_t q_end;    // (as bits) rows with larger queries are NaN: kMostQ / scale
   float scale_log2;  // scale * log2 e / 4 (the quarter keeps it finite for every finite scale; the rows' factors take it back)
 };
 
@@ -1120,7 +1125,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
           x[1] = __ldg(src + 1);
         }
         const uint32_t in[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-        uint32_t big = 0;  // largest magnitude, as bits (an infinity or a NaN makes the row NaN)
+        uint32_t big = 0;  // largest magnitude, as bits (from q_end on, infinities and NaN among it, the row becomes NaN)
 #pragma unroll
         for (int j = 0; j < 8; ++j) big = max(big, max((in[j] << 16) & 0x7FFF0000u, in[j] & 0x7FFF0000u));
 #pragma unroll
@@ -1148,7 +1153,7 @@ __global__ void __launch_bounds__(Cfg<R>::THREADS, 1)
         // The row's factor, 2^e * scale * log2 e.  (Not 2^e alone, with the rest in the keys': below 2^-126 there is no such float, and a
         // large scale makes ordinary scores of such rows.)
         const float factor = pow2(e / 2) * p.scale_log2 * pow2(e - e / 2 + 2);
-        if (c == 0) reinterpret_cast<float*>(sptr + C::OFF_R2)[r] = big >= 0x7F800000u ? __int_as_float(0x7FC00000) : factor;
+        if (c == 0) reinterpret_cast<float*>(sptr + C::OFF_R2)[r] = big >= p.q_end ? __int_as_float(0x7FC00000) : factor;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -1404,6 +1409,8 @@ int attention_fp8_tc_launch(const Fp8AttnCall& a, cudaStream_t stream, int num_s
   p.max_blocks = a.max_blocks, p.num_blocks = a.num_blocks, p.max_prefix = a.max_prefix;
   p.RG = pl.RG, p.Gr = pl.Gr;
   p.scale_log2 = 0.25f * a.scale * kLog2e;
+  const float q_end = kMostQ / a.scale;  // (an infinity for the least scales)
+  std::memcpy(&p.q_end, &q_end, sizeof p.q_end);
   CUtensorMap mk, mv;
   if (!encode_map(&mk, a.k_cache, a.num_blocks, a.Hkv, a.block_size) || !encode_map(&mv, a.v_cache, a.num_blocks, a.Hkv, a.block_size))
     return TS_ERR_CUDA;

@@ -175,3 +175,31 @@ def test_small_queries_under_a_large_scale(form):
     ref, ref_lse, bo, bl = _reference(c, q, mask, scale)
     assert_within(lse, ref_lse, bl, "lse")
     assert_within(out, ref, bo, "out")
+
+
+@tc_forms
+@pytest.mark.parametrize("e,ks", [(40, 1.0), (95, 1.0), (110, 1.0), (120, 2.0 ** 40)])
+def test_low_scores_do_not_pass_for_none(form, e, ks):
+    """Rows all of whose scores are far below zero, down to where fp32 ends: NaN, as any beyond 2^22, and not the zeros of a
+    row without keys.  The other rows stay as they are."""
+    m, Hq, Hkv, bs, sb = form
+    rng = np.random.default_rng(e + m)
+    lens, g = (0, 140, 500, 128), Hq // Hkv
+    c = Cache(rng, lens, m, Hkv, 128, bs, sb)
+    mask = tree_mask(rng, len(lens), m)
+    mask[0, m - 1] = False                                     # (no key at all)
+    c.codes[0][:, 0] = (c.codes[0][:, 0] & 0x1F) | 0x20        # the first KV head's keys lie between 1/8 and 2
+    c.scales[0][:, 0] *= ks
+    q = _query(rng, (len(lens), m, Hq, 128))
+    low = np.zeros(q.shape[:3], dtype=bool)
+    low[:, ::2, :g] = True
+    if ks != 1.0:
+        q[:, :, :g] /= ks                                      # (the first head's other rows: ordinary scores)
+    q[torch.from_numpy(low)] = -(2.0 ** e) * (1 + torch.rand(int(low.sum()), 128, generator=torch.Generator().manual_seed(m)).bfloat16())
+    low &= ~((~mask.any(2)) & (c.lens == 0)[:, None])[:, :, None]
+    out, lse = _attend(c, q, mask)
+    with np.errstate(all="ignore"):
+        ref, ref_lse, bo, bl = _reference(c, q, mask)
+    ref[low] = ref_lse[low] = np.nan
+    assert_within(lse, ref_lse, bl, "lse")
+    assert_within(out, ref, bo, "out")
