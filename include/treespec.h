@@ -611,7 +611,7 @@ int ts_kv_commit_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scal
  * without its own bit and an empty prefix) gets out 0 and lse -inf.  scale finite, > 0.  What lies in places that a node does not
  * attend to (NaN codes among them) does not reach its output; a NaN or an infinity in a query reaches that row alone.
  * On the tensor cores a row with scores, scale * log2 e * (q . k), beyond 2^22 in magnitude may become NaN, and one whose largest
- * |q| * scale reaches 2^70 does.
+ * |q| * scale reaches 2^70 does.  On the CUDA cores a row all of whose scores lie below fp32's range does.
  * Supported: fp32 and bf16, any d <= 256 and any block_size on the CUDA cores (fp32 arithmetic throughout); bf16 with d == 128
  * and block_size in {16, 32, 64, 128} on the tensor cores (queries split exactly into two 8-bit parts, weights rounded to fp16 for
  * the product with V, sums in fp32).  max_prefix <= 2^30.

@@ -25,6 +25,9 @@ constexpr int kKeys = 64;
 constexpr int kMinTiles = 1;     // tiles that a chunk is worth
 constexpr float kLn2f = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634074f;
+// The least maximum of a row that has met a key.  A score below fp32's range, -inf, weighs nothing beside others; where there are no
+// others the sum stays 0 under this maximum, and under -inf in a row without keys.
+constexpr float kLeast = -3.402823466e38f;
 constexpr uint32_t kMasked = 0x80000000u;  // weight -0: a key that the row does not attend to (its V may be NaN)
 
 struct Params {
@@ -54,6 +57,9 @@ template <>
 __device__ __forceinline__ float load1<__nv_bfloat16>(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// A row's sum: NaN where it is 0 although the row has met a key (M: its maximum).
+__device__ __forceinline__ float sum_of(float M, float l) { return l == 0.f && M != -INFINITY ? __int_as_float(0x7FC00000) : l; }
 
 __device__ __forceinline__ bool usable(const Params& p, int L) {
   return L >= 0 && L <= p.max_prefix && static_cast<long long>(L) + p.m <= static_cast<long long>(p.max_blocks) * p.bs;
@@ -221,15 +227,17 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     bool hidden = false;  // whether any key of the tile is left out for some row
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
-      bool seen[4];
+      bool seen[4], any = false;
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int pos = key0 + tx + 16 * j, n = pos - L;
         seen[j] = s_page[tx + 16 * j] >= 0 && (n < 0 || ((words[r][n >> 6] >> (n & 63)) & 1ull));
+        any = any || seen[j];
         x[r][j] *= p.scale_log2;
         if (seen[j]) top = fmaxf(top, x[r][j]);
       }
+      if (any) top = fmaxf(top, kLeast);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const float M2 = fmaxf(M[r], top);
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     const int row = R0 + ty * RPT + r;
     if (row >= p.rows) continue;
     const bool whole = p.chunks == 1;
-    const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+    const float sum = whole ? sum_of(M[r], l[r]) : l[r], inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long unit = (static_cast<long long>(b) * p.Hkv + h) * p.rows + row;
 #pragma unroll
     for (int c = 0; c < CG; ++c) {
@@ -298,7 +306,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     }
     if (tx == 0) {
       if (!whole) p.part_ml[unit * p.chunks + chunk] = make_float2(M[r], l[r]);
-      else if (p.lse != nullptr) p.lse[q_at(row)] = l[r] == 0.f ? -INFINITY : (M[r] + log2f(l[r])) * kLn2f;
+      else if (p.lse != nullptr) p.lse[q_at(row)] = sum == 0.f ? -INFINITY : (M[r] + log2f(sum)) * kLn2f;
     }
   }
 }
@@ -339,6 +347,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   l = s_l[0];
 #pragma unroll
   for (int w = 1; w < kJoinWarps; ++w) l += s_l[w];
+  l = sum_of(M, l);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int node = row / p.g, head = h * p.g + row - node * p.g;
   const long long o = (static_cast<long long>(b) * p.m + node) * p.Hq + head;

@@ -203,3 +203,30 @@ def test_low_scores_do_not_pass_for_none(form, e, ks):
     ref[low] = ref_lse[low] = np.nan
     assert_within(lse, ref_lse, bl, "lse")
     assert_within(out, ref, bo, "out")
+
+
+@pytest.mark.parametrize("m,Hq,Hkv,d,lens", [(5, 4, 2, 64, (0, 70, 300)), (1, 2, 1, 128, (4000, 65, 0)), (40, 8, 2, 128, (500, 20, 0))])
+def test_low_scores_in_fp32(m, Hq, Hkv, d, lens):
+    """Scores below fp32's range, -inf there: keys without weight beside others, NaN where a row has no others."""
+    rng = np.random.default_rng(m + d)
+    g = Hq // Hkv
+    c = Cache(rng, lens, m, Hkv, d, 16, 16)
+    mask = tree_mask(rng, len(lens), m)
+    c.codes[0][:, 0] = 0x7E                                    # the first KV head's keys are 448 * 8
+    c.scales[0][:, 0] = 8.0
+    for b, L in enumerate(lens):
+        if L > 0:                                              # but for one of the prefix, of zeros
+            c.codes[0][c.table[b, (L - 1) // 16], 0, (L - 1) % 16] = 0
+    q = _query(rng, (len(lens), m, Hq, d), torch.float32)
+    q[:, :, :g] = -1e37 * (1 + torch.rand(len(lens), m, g, d, generator=torch.Generator().manual_seed(d)))
+    out, lse = _attend(c, q, mask)
+    ref, ref_lse, bo, bl = _reference(c, q, mask)
+    for b, L in enumerate(lens):
+        if L > 0:
+            v = c.values()[1][c.table[b, (L - 1) // 16], 0, (L - 1) % 16]
+            ref[b, :, :g], bo[b, :, :g] = v, 0.0
+            ref_lse[b, :, :g], bl[b, :, :g] = 0.0, 0.0
+        else:
+            ref[b, :, :g] = ref_lse[b, :, :g] = np.nan
+    assert_within(lse, ref_lse, bl, "lse")
+    assert_within(out, ref, bo, "out")
