@@ -563,8 +563,8 @@ int ts_tree_attention_sparse(const void* q, const void* k_cache, const void* v_c
  * k, v        [B, n, Hkv, d] (dt), any layout with contiguous head rows: k_strides, v_strides [3] (host) are the elements between
  *             sequences, rows and heads (>= 0), so k and v may be slices of a fused projection's output.
  * block_table [B, max_blocks], start_len [B], length [B] int32 (NULL: n each), 0 <= length <= n.
- * A page that is written must belong to one sequence alone (ts_kv_reserve sees to that).  Any d <= 256, scale_block * d < 2^31 - 256.
- * One launch.
+ * A page that is written must belong to one sequence alone (ts_kv_reserve sees to that).  Any d <= 256, scale_block * d < 2^31 - 256,
+ * Hkv * (n / scale_block + 2) < 2^31 - 8.  One launch.
  * Device errors, TS_ERR_DEVICE_CHECK: a negative start, a length outside [0, n] or positions beyond max_blocks * block_size (the
  * sequence is skipped); a page id out of range (its rows are skipped).
  */
@@ -577,7 +577,8 @@ int ts_kv_write_fp8(const void* k, const void* v, ts_dtype dt, const int64_t* k_
  * ts_kv_read_fp8 — values of the cache.
  *
  * k, v [B, n, Hkv, d] (dt): row t holds the value (code * scale, rounded to dt) of position start_len[b] + t where that is below
- * prefix_len[b], 0 otherwise.  start_len NULL: 0.  Any d <= 256.  One launch.
+ * prefix_len[b], 0 otherwise.  start_len NULL: 0.  Any d <= 256, n * Hkv * d < 2^31 less 2^22 (16 times that where d is a multiple of
+ * 16 and the caches and outputs lie on 16-byte boundaries; TS_ERR_UNSUPPORTED beyond).  One launch.
  * Device errors, TS_ERR_DEVICE_CHECK: a negative length or start, or a prefix beyond max_blocks * block_size (the rows are 0); a
  * page id out of range (its rows are 0).
  */
@@ -614,7 +615,9 @@ int ts_kv_commit_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scal
  * |q| * scale reaches 2^70 does.  On the CUDA cores a row all of whose scores lie below fp32's range does.
  * Supported: fp32 and bf16, any d <= 256 and any block_size on the CUDA cores (fp32 arithmetic throughout); bf16 with d == 128
  * and block_size in {16, 32, 64, 128} on the tensor cores (queries split exactly into two 8-bit parts, weights rounded to fp16 for
- * the product with V, sums in fp32).  max_prefix <= 2^30.
+ * the product with V, sums in fp32).  max_prefix <= 2^30.  TS_ERR_UNSUPPORTED on the tensor cores also from 2^31 of
+ * B * Hkv * (n / 128 + 7) on, n being the smaller of max_prefix + m and max_blocks * block_size, and on the CUDA cores above 65535 of
+ * Hkv * ceil(m * Hq / Hkv / 32) (64 for 32 with d <= 64).
  * workspace: ts_tree_attention_fp8_workspace(...) bytes, 16-byte aligned (not read where that is 256 or less).
  * Device errors, TS_ERR_DEVICE_CHECK: a prefix_len outside [0, max_prefix] or beyond max_blocks * block_size - m (the rows of that
  * sequence are not written), a page id out of range (its keys are left out); a wait over its time bound -> TS_ERR_TIMEOUT.

@@ -1392,8 +1392,9 @@ size_t attention_fp8_tc_workspace_bytes(int B, int m, int Hq, int Hkv, int max_p
 
 int attention_fp8_tc_launch(const Fp8AttnCall& a, cudaStream_t stream, int num_sms) {
   using namespace fp8tc;
-  // (time is counted in 32 bits)
-  if (((static_cast<long long>(a.max_prefix) + a.m + BK - 1) / BK + kBegin) * a.B * a.Hkv > INT32_MAX) return TS_ERR_UNSUPPORTED;
+  // Time is counted in 32 bits, by the most tiles that sequences can have: of a longer prefix than the table has room for there are none.
+  const long long most = std::min<long long>(static_cast<long long>(a.max_prefix) + a.m, static_cast<long long>(a.max_blocks) * a.block_size);
+  if (((most + BK - 1) / BK + kBegin) * a.B * a.Hkv > INT32_MAX) return TS_ERR_UNSUPPORTED;
   const Plan pl = plan_of(a.B, a.m, a.Hq, a.Hkv, a.max_prefix, num_sms);
   Params p;
   p.q = static_cast<const __nv_bfloat16*>(a.q);

@@ -230,3 +230,17 @@ def test_low_scores_in_fp32(m, Hq, Hkv, d, lens):
             ref[b, :, :g] = ref_lse[b, :, :g] = np.nan
     assert_within(lse, ref_lse, bl, "lse")
     assert_within(out, ref, bo, "out")
+
+
+@tc_forms
+def test_any_bound_of_the_lengths(form):
+    """max_prefix 2^30, the most there is, over 256 KV heads: what a sequence can hold is bounded by its table."""
+    m, Hq, Hkv, bs, sb = form
+    rng = np.random.default_rng(m + 2)
+    lens = tuple(int(x) for x in rng.integers(0, 200, 256 // Hkv))
+    c = Cache(rng, lens, m, Hkv, 128, bs, sb)
+    mask, q = tree_mask(rng, len(lens), m), _query(rng, (len(lens), m, Hq, 128))
+    out, lse = _attend(c, q, mask, max_prefix=1 << 30)
+    ref, ref_lse, bo, bl = _reference(c, q, mask)
+    assert_within(lse, ref_lse, bl, "lse")
+    assert_within(out, ref, bo, "out")
