@@ -614,8 +614,9 @@ int ts_kv_commit_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scal
  * On the tensor cores a row with scores, scale * log2 e * (q . k), beyond 2^22 in magnitude may become NaN, and one whose largest
  * |q| * scale reaches 2^70 does.  On the CUDA cores a row all of whose scores lie below fp32's range does.
  * Supported: fp32 and bf16, any d <= 256 and any block_size on the CUDA cores (fp32 arithmetic throughout); bf16 with d == 128
- * and block_size in {16, 32, 64, 128} on the tensor cores (queries split exactly into two 8-bit parts, weights rounded to fp16 for
- * the product with V, sums in fp32).  max_prefix <= 2^30.  TS_ERR_UNSUPPORTED on the tensor cores also from 2^31 of
+ * and block_size in {16, 32, 64, 128} on the tensor cores (queries split into two 8-bit parts: exact but for
+ * elements below 2^-13 of their row's largest, which may be off by 2^-21 of it; weights rounded to fp16 for the product with V, sums
+ * in fp32).  max_prefix <= 2^30.  TS_ERR_UNSUPPORTED on the tensor cores also from 2^31 of
  * B * Hkv * (n / 128 + 7) on, n being the smaller of max_prefix + m and max_blocks * block_size, and on the CUDA cores above 65535 of
  * Hkv * ceil(m * Hq / Hkv / 32) (64 for 32 with d <= 64).
  * workspace: ts_tree_attention_fp8_workspace(...) bytes, 16-byte aligned (not read where that is 256 or less).

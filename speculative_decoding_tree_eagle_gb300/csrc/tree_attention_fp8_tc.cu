@@ -15,10 +15,11 @@
 // few columns instead of 128 rows of padding, which is what single tokens and chains need (a 128-key tile's bytes
 // take some 1400 cycles of an SM's share of the HBM, less than the softmax of 128 x 128 scores).  Above 32 rows ("wide", R = 128)
 // S [R x 128 keys] = Q x K and O [R x 128 channels] += P x V with P from tensor memory, two threads to a row.
-//   Q   each row is scaled by a power of two of its own to at most 256 and split into e4m3 + e5m2: a bf16 value has eight
-//       significant bits, the nearest e4m3 takes four and leaves a remainder of at most three, which e5m2 holds; what falls
-//       below 2^-25 of the row's largest value is lost.  Two MMAs of kind f8f6f4 (twice fp16's rate) on the
-//       codes replace a conversion of K.
+//   Q   each row is scaled by a power of two of its own to a largest magnitude in [128, 256) and split into e4m3 + e5m2: a bf16
+//       value has eight significant bits, the nearest e4m3 takes four and leaves a remainder of at most three, which e5m2 holds.
+//       That is exact down to e4m3's least normal value, 2^-6; below, e4m3's steps are 2^-9 and the remainder may need up to five
+//       bits: it is off by at most 2^-14, 2^-21 of the row's largest, in elements of less than 2^-13 of it.  Two MMAs of kind f8f6f4
+//       (twice fp16's rate) on the codes replace a conversion of K.
 //   V   is converted to fp16 in shared memory (exact) by warps of their own: weights of eight bits would need the product
 //       three times over.
 //   P'  is rounded to fp16 (half a step of 2^-11, nothing lost above 2^-25 / 2^7 of the reference): M is kept 7 below the

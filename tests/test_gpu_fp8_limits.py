@@ -244,3 +244,38 @@ def test_any_bound_of_the_lengths(form):
     ref, ref_lse, bo, bl = _reference(c, q, mask)
     assert_within(lse, ref_lse, bl, "lse")
     assert_within(out, ref, bo, "out")
+
+
+@tc_forms
+@pytest.mark.parametrize("above", [12, 14, 16, 18])
+def test_one_large_channel_that_meets_zeros(form, above):
+    """Queries with one channel 2^above times the others, whose keys are zero there: the scores are made of what the split of
+    the queries into two 8-bit parts leaves of the others.  It is off by at most 2^-21 of a row's largest in each channel, so a score by
+    dE = scale 2^-21 max|q| sum|k| beside what attention_bounds counts; the weights by twice that, relatively."""
+    m, Hq, Hkv, bs, sb = form
+    rng = np.random.default_rng(m + above)
+    lens, scale = (3, 140, 500), 1 / math.sqrt(128)
+    c = Cache(rng, lens, m, Hkv, 128, bs, sb, spread=1)
+    c.codes[0] &= 0x7F                                         # (of one sign, so that errors add up)
+    c.codes[0][..., 77] = 0
+    mask = tree_mask(rng, len(lens), m)
+    q = rng.uniform(0.5, 2.0, (len(lens), m, Hq, 128)) / 4
+    y = torch.arange(0x3E00, 0x3F00, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).float()   # 1/8 .. 1/2
+    x = y * 2.0 ** (9 - above)                                 # (the large channel at 128)
+    lost = x - x.to(torch.float8_e4m3fn).float()
+    lost -= lost.to(torch.float8_e5m2).float()
+    q[:, 1::2] = y[lost.argmax()].item()                       # every other node: the value that loses most, in all channels
+    q[..., 77] = 2.0 ** above / 4
+    q = torch.from_numpy(q).to(torch.bfloat16)
+    out, lse = _attend(c, q, mask)
+    ref, ref_lse, bo, bl = _reference(c, q, mask)
+    k, v = c.values()
+    size = attention_bounds(q.double().numpy(), k, np.abs(v), c.table, c.lens, mask, scale, True)[0]
+    dE = np.zeros(ref_lse.shape)
+    for b, L in enumerate(lens):
+        pos = np.arange(L + m)
+        most = np.abs(k[c.table[b, pos // bs], :, pos % bs]).sum(2).max(0)                       # [Hkv]
+        dE[b] = scale * 2.0 ** -21 * np.abs(q[b].double().numpy()).max(2) * np.repeat(most, Hq // Hkv)
+    assert dE.max() < 1 / 4                                    # (first order in dE)
+    assert_within(lse, ref_lse, bl + 1.5 * dE, "lse")
+    assert_within(out, ref, bo + 3 * dE[..., None] * size, "out")
