@@ -68,8 +68,8 @@ def values(cache, scale) -> np.ndarray:
     return E4M3[cache] * np.repeat(clamp_scale(scale), sb, axis=2)[..., None]
 
 
-def _quantise(cache, scale, page, h, row, rows, kept):
-    """Rows (values, the first ``kept`` of them kept ones) become rows ``row`` .. of one page's block."""
+def _quantise(cache, scale, page, h, row, rows):
+    """Rows (values, kept ones and new) become rows ``row`` .. of one page's block."""
     sb = cache.shape[2] // scale.shape[2]
     e = exponent(rows)
     with np.errstate(invalid="ignore"):
@@ -90,7 +90,7 @@ def write_one(cache, scale, rows, table_row, start: int) -> None:
         stop = min(sb, end - first)
         for h in range(cache.shape[1]):
             new = rows[max(first, start) - start: first + stop - start, h]
-            _quantise(cache, scale, page, h, row, np.concatenate([old[page, h, row:row + kept], new]), kept)
+            _quantise(cache, scale, page, h, row, np.concatenate([old[page, h, row:row + kept], new]))
 
 
 def write(cache, scale, x, table, start, length) -> None:

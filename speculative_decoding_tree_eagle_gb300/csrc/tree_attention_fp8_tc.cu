@@ -269,14 +269,6 @@ __device__ __forceinline__ void commit_elected(uint32_t bar) {
       "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
-// One box of a tensor map by the elected lane.
-__device__ __forceinline__ void tma_elected(uint32_t dst, const void* tmap, uint32_t bar, int c2, int c3) {
-  asm volatile(
-      "{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\t"
-      "@one cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(c2), "r"(c3), "r"(bar)
-      : "memory");
-}
 // Instruction descriptors (fields as in idesc_bf16_f32; format 0 is e4m3 in kind f8f6f4 and fp16 in kind f16, 1 is e5m2).
 __host__ __device__ constexpr uint32_t idesc_of(int N, int a_format, int b_format, int a_mn, int b_mn) {
   return (1u << 4) | (static_cast<uint32_t>(a_format) << 7) | (static_cast<uint32_t>(b_format) << 10) |
