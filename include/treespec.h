@@ -359,7 +359,7 @@ int ts_tree_build_from_topk(const int32_t* row_tok, const float* row_logp, const
  * All pointers are caller-owned device memory; nothing is allocated; one launch on `stream`.
  * Errors: TS_ERR_INVALID (null pointer, non-positive size, d * element size not a multiple
  * of 4) and TS_ERR_UNSUPPORTED (m > TS_MAX_NODES) before any launch.  A sequence whose
- * prefix length is negative, whose accept length is outside 1..m, whose path does not start
+ * prefix length is negative or above 2^31 - 1 - m, whose accept length is outside 1..m, whose path does not start
  * at the root or does not increase, whose pages do not fit max_blocks or whose touched page
  * ids are out of range is left untouched and *dev_status is set to TS_ERR_DEVICE_CHECK.
  */
@@ -598,7 +598,8 @@ int ts_kv_read_fp8(const void* k_cache, const void* v_cache, const float* k_scal
  *
  * freed_blocks [B, max_blocks], freed_count [B].  m <= TS_MAX_NODES, any d <= 256, scale_block * d < 2^31 - 256.  One launch, two in
  * place; no workspace.
- * Device errors: as ts_kv_commit (the sequence's cache is left untouched, its table row and length are copied).
+ * Device errors: as ts_kv_commit, a prefix length above 2^31 - 257 among them (the sequence's cache is left untouched, its table row and
+ * length are copied).
  */
 int ts_kv_commit_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks, int block_size,
                      int scale_block, int Hkv, int d, const int32_t* block_table, int max_blocks, const int32_t* prefix_len,

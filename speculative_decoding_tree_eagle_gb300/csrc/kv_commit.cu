@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(
   const int a = accept_len[b];
   // page counts in 64 bits: a prefix length near INT_MAX must fail the max_blocks check
   const long long used64 = L >= 0 ? (static_cast<long long>(L) + m + bs - 1) / bs : 0;
-  bool bad = L < 0 || a < 1 || a > m || used64 > max_blocks;
+  bool bad = L < 0 || L > INT32_MAX - m || a < 1 || a > m || used64 > max_blocks;
   const int n_used = bad ? 0 : static_cast<int>(used64);
   const int n_keep = bad ? 0 : static_cast<int>((static_cast<long long>(L) + a + bs - 1) / bs);
   const int p0 = bad ? 0 : L / bs;                 // first page a tree position touches
@@ -49,15 +49,16 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(
       s_path[j] = pj;
       if (j == 0 ? pj != 0 : (pj >= m || pj <= accept_path[static_cast<long long>(b) * m + j - 1])) bad = true;
     }
-    for (int i = p0 + tid; i < n_used; i += blockDim.x) {
-      const int pg = table[static_cast<long long>(b) * max_blocks + i];
-      s_page[i - p0] = pg;
+    // (by distances from p0: cells may lie just below 2^31)
+    for (int i = tid; i < n_used - p0; i += blockDim.x) {
+      const int pg = table[static_cast<long long>(b) * max_blocks + p0 + i];
+      s_page[i] = pg;
       if (pg < 0 || pg >= num_blocks) bad = true;
     }
   }
   if (__syncthreads_or(bad)) {
     // inputs untouched; the outputs still say "nothing released"
-    for (int i = tid; i < max_blocks; i += blockDim.x) freed[static_cast<long long>(b) * max_blocks + i] = -1;
+    for (long long i = tid; i < max_blocks; i += blockDim.x) freed[static_cast<long long>(b) * max_blocks + i] = -1;
     if (tid == 0) {
       freed_count[b] = 0;
       report(status, TS_ERR_DEVICE_CHECK);
@@ -97,9 +98,9 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(
     }
   }
   __syncthreads();  // every move has read the old table before any entry changes
-  for (int i = tid; i < max_blocks; i += blockDim.x) {
+  for (long long i = tid; i < max_blocks; i += blockDim.x) {
     const long long o = static_cast<long long>(b) * max_blocks;
-    const int k = i + n_keep;  // logical page whose id goes to freed[i]
+    const long long k = i + n_keep;  // logical page whose id goes to freed[i]
     if (k < n_used) {
       freed[o + i] = s_page[k - p0];
       table[o + k] = -1;
