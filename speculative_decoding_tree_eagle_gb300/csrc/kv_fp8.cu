@@ -10,10 +10,12 @@
 // What bounds them: a prompt's write reads 2 or 4 bytes and writes one per element, a read the other way round: HBM.
 // The writes of single tokens and trees, and the commit, are latency: table entry -> rows -> maximum -> codes.
 //
-// Measured on the device (GB300, replayed from a graph, 8 heads of 128): a prompt of 4 x 32768 bf16 rows 122 us (6.3 TB/s, 94% of the
-// copy rate), of 2 x 32768 fp32 rows 101 (96%), 60-node trees of 16 sequences 4.1,
-// one token of each of 64 sequences in 64-token blocks 5.1 (it reads its block's kept rows); a read of 2 x 8192 rows into bf16 18
-// (83%), of 16 x 64 into fp32 5.1; a commit of at most 7 rows of 16 sequences 6.1, of 16 rows of 64 sequences in 64-token blocks 10.6.
+// Measured on the device (GB300, replayed from a graph, 8 heads of 128): a prompt of 4 x 32768 bf16 rows 123 us (93% of the
+// copy rate), of 2 x 32768 fp32 rows 102 (95%), 60-node trees of 16 sequences 4.0,
+// one token of each of 64 sequences in 64-token blocks 4.8 (it reads its block's kept rows); a read of 2 x 8192 rows into bf16 18
+// (82%), of 16 x 64 into fp32 5.1; a commit of at most 7 rows of 16 sequences 6.0, of 16 rows of 64 sequences in 64-token blocks 10.8.
+// Head dims that are not a power of two go element by element: the same prompt with d = 96 747 us, with d = 192 1197 (11% and 14% of the
+// copy rate).
 #include <algorithm>
 #include <type_traits>
 
@@ -34,8 +36,8 @@ constexpr int kAnyThreads = 256;
 constexpr int kChunk = 8;     // elements that a thread loads at once (16 bytes of bf16, 8 codes)
 constexpr int kHeld = 8;      // chunks that a thread holds between the maximum and the codes
 
-// x / d for 0 <= x < 2^31 as a multiplication: with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1 the quotient is
-// (x m / 2^32 + x) / 2^s.  (Six divisions a thread took a third of a read's instructions, five a warp
+// x / d for 0 <= x < 2^31 as a multiplication (Granlund and Montgomery, "Division by invariant integers using multiplication", 1994): with
+// s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1 the quotient is (x m / 2^32 + x) / 2^s.  (Six divisions a thread took a third of a read's instructions, five a warp
 // more than the rest of a write with four tokens to a scale.)
 struct Divide {
   uint32_t m, s, d;

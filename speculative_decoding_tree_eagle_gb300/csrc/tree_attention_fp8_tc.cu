@@ -20,8 +20,8 @@
 //       That is exact down to e4m3's least normal value, 2^-6; below, e4m3's steps are 2^-9 and the remainder may need up to five
 //       bits: it is off by at most 2^-14, 2^-21 of the row's largest, in elements of less than 2^-13 of it.  Two MMAs of kind f8f6f4
 //       (twice fp16's rate) on the codes replace a conversion of K.
-//   V   is converted to fp16 in shared memory (exact) by warps of their own: weights of eight bits would need the product
-//       three times over.
+//   V   is converted to fp16 in shared memory (exact) by warps of their own: with V's codes as they are, a weight would have to be
+//       taken apart into terms of eight bits for products of their own (three e4m3 terms for fp16's eleven bits, measured: slower).
 //   P'  is rounded to fp16 (half a step of 2^-11, nothing lost above 2^-25 / 2^7 of the reference): M is kept 7 below the
 //       largest y and is raised only when a y exceeds it by 15, so p' <= 2^15.  The sum is of the unrounded p', in fp32.
 //
@@ -33,7 +33,7 @@
 // Measured (GB300, 32 heads on 8 but for the last, pages of 16 tokens, a scale for 16): 8 single tokens over 1024 to 8192 tokens 27.0 us;
 // 4 x 8 nodes over 32768 66 us (4.1 TB/s, 61% of the copy rate: a tile takes some 2000 cycles, of which its shared-memory traffic
 // is 1350); 4 x 64 nodes over 32768 140 us and 16 x 60 nodes of 64 heads over 4096 167 us (51% and 40% of the bf16 rate: what
-// bounds both is the softmax, 1700 cycles a tile of 128 x 128 scores with its issue slots a third used, then 15000 cycles for a
+// bounds both is the softmax, 1700 cycles a tile of 128 x 128 scores with the schedulers issuing in 46% of them, then 15000 cycles for a
 // unit's beginning and end).
 //
 // The roles of the warps (struct Cfg) share one instruction cache: code that every tile runs is kept short, and code that runs once per
