@@ -178,7 +178,7 @@ def test_small_queries_under_a_large_scale(form):
 
 
 @tc_forms
-@pytest.mark.parametrize("e,ks", [(40, 1.0), (95, 1.0), (110, 1.0), (120, 2.0 ** 40)])
+@pytest.mark.parametrize("e,ks", [(40, 1.0), (70, 2.0 ** 40), (95, 1.0), (110, 1.0), (120, 2.0 ** 40)])
 def test_low_scores_do_not_pass_for_none(form, e, ks):
     """Rows all of whose scores are far below zero, down to where fp32 ends: NaN, as any beyond 2^22, and not the zeros of a
     row without keys.  The other rows stay as they are."""
