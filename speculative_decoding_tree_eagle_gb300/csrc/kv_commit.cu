@@ -56,9 +56,10 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(
       if (pg < 0 || pg >= num_blocks) bad = true;
     }
   }
+  const uint32_t cells = max_blocks;  // (unsigned: a step behind the last one does not wrap, nor does a cell and a page's number)
   if (__syncthreads_or(bad)) {
     // inputs untouched; the outputs still say "nothing released"
-    for (long long i = tid; i < max_blocks; i += blockDim.x) freed[static_cast<long long>(b) * max_blocks + i] = -1;
+    for (uint32_t i = tid; i < cells; i += blockDim.x) freed[static_cast<long long>(b) * max_blocks + i] = -1;
     if (tid == 0) {
       freed_count[b] = 0;
       report(status, TS_ERR_DEVICE_CHECK);
@@ -98,10 +99,10 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(
     }
   }
   __syncthreads();  // every move has read the old table before any entry changes
-  for (long long i = tid; i < max_blocks; i += blockDim.x) {
+  for (uint32_t i = tid; i < cells; i += blockDim.x) {
     const long long o = static_cast<long long>(b) * max_blocks;
-    const long long k = i + n_keep;  // logical page whose id goes to freed[i]
-    if (k < n_used) {
+    const uint32_t k = i + n_keep;  // logical page whose id goes to freed[i]
+    if (k < static_cast<uint32_t>(n_used)) {
       freed[o + i] = s_page[k - p0];
       table[o + k] = -1;
     } else {

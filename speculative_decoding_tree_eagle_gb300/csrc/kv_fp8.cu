@@ -528,10 +528,12 @@ __device__ __forceinline__ Commit commit_of(const CommitParams& p, int b, int* s
 // Tables, lengths and the released pages of sequence b, by the whole CTA.
 __device__ void commit_tables(const CommitParams& p, int b, const Commit& c, const int* s_page) {
   const long long o = static_cast<long long>(b) * p.max_blocks;
-  for (long long i = threadIdx.x; i < p.max_blocks; i += kCommitThreads) {
-    const long long k = i + c.n_keep;
-    p.freed[o + i] = c.ok && k < c.n_used ? s_page[k - c.p0] : -1;
-    const bool gone = c.ok && i >= c.n_keep && i < c.n_used;
+  // (unsigned: a step behind the last cell does not wrap, nor does a cell and a page's number)
+  const uint32_t cells = p.max_blocks, keep = c.n_keep, used = c.n_used;
+  for (uint32_t i = threadIdx.x; i < cells; i += kCommitThreads) {
+    const uint32_t k = i + keep;
+    p.freed[o + i] = c.ok && k < used ? s_page[k - c.p0] : -1;
+    const bool gone = c.ok && i >= keep && i < used;
     if (gone) p.table_out[o + i] = -1;
     else if (p.table_out != p.table) p.table_out[o + i] = p.table[o + i];
   }
