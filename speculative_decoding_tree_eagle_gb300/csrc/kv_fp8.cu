@@ -36,9 +36,9 @@ constexpr int kAnyThreads = 256;
 constexpr int kChunk = 8;     // elements that a thread loads at once (16 bytes of bf16, 8 codes)
 constexpr int kHeld = 8;      // chunks that a thread holds between the maximum and the codes
 
-// x / d for 0 <= x < 2^31 as a multiplication (Granlund and Montgomery, "Division by invariant integers using multiplication", 1994): with
-// s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1 the quotient is (x m / 2^32 + x) / 2^s.  (Six divisions a thread took a third of a read's instructions, five a warp
-// more than the rest of a write with four tokens to a scale.)
+// x / d for 0 <= x < 2^31 as a multiplication (Granlund and Montgomery, "Division by invariant integers using multiplication",
+// 1994): with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1 the quotient is (x m / 2^32 + x) / 2^s.  (Six divisions a
+// thread took a third of a read's instructions, five a warp more than the rest of a write with four tokens to a scale.)
 struct Divide {
   uint32_t m, s, d;
   Divide() = default;
